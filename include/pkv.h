@@ -82,6 +82,7 @@ typedef struct CUevent_st* pkv_event_t;    /* same handle as cudaEvent_t    */
 #define PKV_STATUS_BAD_BLOCK  0x2u  /* block_tables entry outside [0,num_blocks)  */
 #define PKV_STATUS_BAD_QUERY  0x4u  /* query_start_loc/seq_lens inconsistent      */
 #define PKV_STATUS_TIMEOUT    0x8u  /* a bounded wait in a kernel ran out         */
+#define PKV_STATUS_BAD_POSITION 0x10u /* position outside [0, max_position): token skipped */
 
 /* Page-pool and head geometry, checked on every call.
  *   k_cache and v_cache are each [num_blocks, num_kv_heads, page_size, head_dim]
@@ -272,6 +273,112 @@ PKV_API int pkv_attend_fp8(const pkv_bf16* q, const pkv_fp8* k_cache,
                            pkv_bf16* out, void* workspace, size_t workspace_bytes,
                            const pkv_desc* desc, pkv_stream_t stream);
 
+/* ---- appends with the position rotation -------------------------------------- */
+/* Rotary embedding applied while rows are appended: the pages this library
+ * follows do not describe it; it is what a serving step does between the
+ * projections and pkv_write, and here it costs no pass of its own.
+ * cos_sin is [max_position, rotary_dim] fp32, device, 16-byte aligned: row p
+ * holds the rotary_dim/2 cosines and then the rotary_dim/2 sines of position
+ * p's angles.  Pair i of a row is its elements (i, i + rotary_dim/2), or
+ * (2i, 2i + 1) when interleaved is not 0; (a, b) becomes
+ * (a cos_i - b sin_i, b cos_i + a sin_i), in fp32 with each product and each
+ * sum rounded, then rounded once to the stored type.  Elements from
+ * rotary_dim on are copied.  rotary_dim: a multiple of 16, at most the row. */
+typedef struct {
+  const float* cos_sin;
+  int32_t max_position;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} pkv_rope;
+
+/* pkv_write_rope -- pkv_write with K rotated on the way, and the queries too.
+ *   q              NULL, or [num_tokens, num_q_heads, 128] bf16 with
+ *                  q_stride elements from token to token.
+ *   k_new, v_new   [num_tokens, num_kv_heads, 128] bf16 with k_stride and
+ *                  v_stride elements from token to token, so the three may be
+ *                  slices of one projection's output.  Strides: multiples of
+ *                  8, at least a token's elements.
+ *   positions      [num_tokens] int64.  A token whose position is outside
+ *                  [0, max_position) is skipped whole (its q_out row too) and
+ *                  flags PKV_STATUS_BAD_POSITION.
+ *   slot_mapping   as in pkv_write; a token whose slot is negative or beyond
+ *                  the pool still has its queries rotated.
+ *   q_out          [num_tokens, num_q_heads, 128] bf16, contiguous (NULL iff
+ *                  q is); may be q itself where q is contiguous. */
+PKV_API int pkv_write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                           const int64_t* positions, const int64_t* slot_mapping,
+                           int64_t num_tokens, const pkv_rope* rope, pkv_bf16* q_out,
+                           pkv_bf16* k_cache, pkv_bf16* v_cache, const pkv_desc* desc,
+                           pkv_stream_t stream);
+
+/* pkv_write_rope_fp8 -- the same into FP8 pages.  The row's power of two is
+ * taken from the rotated fp32 values, and they are rounded once, to E4M3;
+ * otherwise codes and scales are as pkv_write_fp8's. */
+PKV_API int pkv_write_rope_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new,
+                               int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               const int64_t* positions, const int64_t* slot_mapping,
+                               int64_t num_tokens, const pkv_rope* rope, pkv_bf16* q_out,
+                               pkv_fp8* k_cache, pkv_fp8* v_cache, uint8_t* k_scale,
+                               uint8_t* v_scale, const pkv_desc* desc, pkv_stream_t stream);
+
+/* ---- latent pages ------------------------------------------------------------ */
+/* Latent attention caches one vector a token in place of per-head keys and
+ * values: 512 latent values that stand for the keys and the values of every
+ * head, and 64 rotated values that are the shared part of the keys.  Both
+ * head projections can be moved to the query's and the output's side (the
+ * absorbed form), which leaves attention of all heads over one shared key of
+ * 576 values whose first 512 are the value:
+ *   out[t, h] = softmax_k(scale * q[t, h] . row[k]) row[k][0:512].
+ * The pages this library follows do not describe latent caches; the pool is
+ * this library's: latent_cache [num_blocks, 16, 576] bf16.  pkv_desc for
+ * these calls: head_dim 576, num_kv_heads 1, page_size 16, num_q_heads any
+ * number from 1 to PKV_LATENT_MAX_HEADS. */
+#define PKV_LATENT_MAX_HEADS 256
+
+/* pkv_write_latent -- append one row a token, its last 64 values rotated.
+ *   c_new          [num_tokens, 512] bf16, c_stride elements a token: the
+ *                  latent, copied as it is.
+ *   k_pe           [num_tokens, 64] bf16, k_stride elements a token: rotated.
+ *   q_pe           NULL, or [num_tokens, num_q_heads, 64] bf16 with q_stride
+ *                  and q_head_stride elements a token and a head: rotated
+ *                  into the last 64 values of q_out's rows.
+ *   q_out          [num_tokens, num_q_heads, 576] bf16, contiguous (NULL iff
+ *                  q_pe is); the first 512 values of its rows are left alone.
+ *   rope           rotary_dim 64.
+ * Strides: multiples of 8.  Positions, slots and what is skipped are as in
+ * pkv_write_rope. */
+PKV_API int pkv_write_latent(const pkv_bf16* c_new, const pkv_bf16* k_pe, const pkv_bf16* q_pe,
+                             int64_t c_stride, int64_t k_stride, int64_t q_stride,
+                             int64_t q_head_stride, const int64_t* positions,
+                             const int64_t* slot_mapping, int64_t num_tokens,
+                             const pkv_rope* rope, pkv_bf16* q_out, pkv_bf16* latent_cache,
+                             const pkv_desc* desc, pkv_stream_t stream);
+
+/* Workspace bytes pkv_attend_latent needs on the CURRENT device. */
+PKV_API int pkv_attend_latent_workspace_size(const pkv_desc* desc, int32_t num_seqs,
+                                             int32_t num_tokens, size_t* bytes);
+
+/* pkv_attend_latent -- absorbed attention of one continuous batch over latent
+ * pages, decode rows and query chunks alike, on the tensor cores.
+ *   q              [num_tokens, num_q_heads, 576] bf16: absorbed queries.
+ *   out            [num_tokens, num_q_heads, 512] bf16; rows at or beyond
+ *                  query_start_loc[num_seqs] are not written.
+ *   block_tables, seq_lens, query_start_loc, scale, workspace and stream
+ *   order as in pkv_attend (workspace: pkv_attend_latent_workspace_size).
+ *   max_query_len  host-side upper bound on the query tokens of a sequence,
+ *                  or <= 0 if unknown; it only selects tile sizes.
+ * Rows of tokens past a sequence's end are never used, whatever they hold;
+ * the rows of its cached tokens, those of this step among them, must be
+ * finite (a later row of the same chunk enters a query's sums with weight 0,
+ * and 0 times infinity is NaN). */
+PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
+                              const int32_t* block_tables, const int32_t* seq_lens,
+                              const int32_t* query_start_loc, int32_t num_seqs,
+                              int32_t num_tokens, int32_t max_query_len, float scale,
+                              pkv_bf16* out, void* workspace, size_t workspace_bytes,
+                              const pkv_desc* desc, pkv_stream_t stream);
+
 /* ---- page pool (host side) ------------------------------------------------ */
 /* The engine reserves num_gpu_blocks pages of block_size tokens (vLLM notes
  * "EngineCoreClient ...", "Flujo de datos"); the native coordinator owns the
@@ -343,7 +450,8 @@ PKV_API uint64_t pkv_launch_count(void);
 #define PKV_K_DECODE   2
 #define PKV_K_MERGE    3
 #define PKV_K_PREFILL  4
-#define PKV_K_COUNT    5
+#define PKV_K_LATENT   5
+#define PKV_K_COUNT    6
 
 typedef struct pkv_trace pkv_trace;
 /* Create a trace with room for `capacity` launches (creates 2*capacity CUDA

@@ -21,14 +21,19 @@ __all__ = [
     "PkvError", "PkvUnavailable", "lib", "open_library", "library_path", "Desc", "write", "attend",
     "workspace_size", "get_last_error", "launch_count", "Trace", "PagePool", "KERNELS",
     "export_pages", "import_pages", "write_fp8", "attend_fp8", "workspace_size_fp8",
-    "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT",
+    "write_rope", "write_rope_fp8", "write_latent", "attend_latent", "workspace_size_latent",
+    "make_desc", "make_latent_desc", "Rope",
+    "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT", "STATUS_BAD_POSITION",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.environ.get("PKV_LIBRARY", os.path.join(_HERE, "libpkv.so"))
 
 STATUS_BAD_SLOT, STATUS_BAD_BLOCK, STATUS_BAD_QUERY, STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
-KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4}
+STATUS_BAD_POSITION = 0x10
+KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5}
+LATENT_DIM, LATENT_ROPE = 512, 64
+LATENT_ROW = LATENT_DIM + LATENT_ROPE
 
 
 class PkvError(RuntimeError):
@@ -48,6 +53,11 @@ class Desc(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "pkv_write": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, ctypes.POINTER(Desc), _vp]),
@@ -60,6 +70,15 @@ _SIGS = {
     "pkv_attend_fp8_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, _i32, ctypes.POINTER(_sz)]),
     "pkv_attend_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, ctypes.c_float,
                                       _vp, _vp, _sz, ctypes.POINTER(Desc), _vp]),
+    "pkv_write_rope": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Rope), _vp,
+                                      _vp, _vp, ctypes.POINTER(Desc), _vp]),
+    "pkv_write_rope_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Rope), _vp,
+                                          _vp, _vp, _vp, _vp, ctypes.POINTER(Desc), _vp]),
+    "pkv_write_latent": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Rope),
+                                        _vp, _vp, ctypes.POINTER(Desc), _vp]),
+    "pkv_attend_latent_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, ctypes.POINTER(_sz)]),
+    "pkv_attend_latent": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz,
+                                         ctypes.POINTER(Desc), _vp]),
     "pkv_get_last_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "pkv_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "pkv_launch_count": (ctypes.c_uint64, []),
@@ -290,6 +309,214 @@ def attend_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, qu
                                     _ptr(workspace), workspace.numel(), ctypes.byref(desc),
                                     _stream(q.device, stream)),
                "pkv_attend_fp8")
+    return out
+
+
+def _need_rows(t, name, dim, heads=None):
+    """A bf16 CUDA tensor [T, heads, dim] whose heads are contiguous, or [T, dim] where heads is None,
+    with any token stride that keeps 16-byte alignment; returns that stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = (dim,) if heads is None else (heads, dim)
+    if tuple(t.shape[1:]) != shape:
+        raise ValueError(f"{name} must be [tokens, {', '.join(map(str, shape))}], got shape {tuple(t.shape)}")
+    stride = t.stride()
+    if stride[-1] != 1 or (heads is not None and heads > 1 and stride[1] != dim):
+        raise ValueError(f"a token's elements of {name} must be contiguous")
+    row = dim * (heads or 1)
+    if t.shape[0] < 2:
+        return row
+    if stride[0] < row or stride[0] % 8:
+        raise ValueError(f"{name}'s token stride must be a multiple of 8 elements and no less than a token")
+    return stride[0]
+
+
+def _need_same_device(device, *named):
+    for t, name in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+
+
+def _new(shape, like, stream, dtype=None):
+    """An uninitialised tensor that belongs to the stream it is used on."""
+    dtype = like.dtype if dtype is None else dtype
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _rope(cos_sin, interleaved):
+    _need(cos_sin, "cos_sin", torch.float32, 2)
+    return Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0)
+
+
+def _write_rope(fp8, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q, q_out,
+                interleaved, stream):
+    _, hkv, _, D = k_cache.shape
+    T = k_new.shape[0]
+    ks, vs = _need_rows(k_new, "k_new", D, hkv), _need_rows(v_new, "v_new", D, hkv)
+    _need(positions, "positions", torch.int64, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    rope = _rope(cos_sin, interleaved)
+    if v_new.shape[0] != T or positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("k_new, v_new, positions and slot_mapping disagree on the number of tokens")
+    dev = k_cache.device
+    hq, qs = hkv, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must be [tokens, Hq, D] with k_new's tokens")
+        hq = q.shape[1]
+        qs = _need_rows(q, "q", D, hq)
+        if q_out is None:
+            q_out = _new(q.shape, q, stream)
+        else:
+            _need(q_out, "q_out", torch.bfloat16, 3)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need_same_device(dev, (k_new, "k_new"), (v_new, "v_new"), (positions, "positions"), (cos_sin, "cos_sin"),
+                      (slot_mapping, "slot_mapping"), (v_cache, "v_cache"), (k_scale, "k_scale"),
+                      (v_scale, "v_scale"), (q, "q"), (q_out, "q_out"))
+    desc = make_desc(k_cache, hq, 1)
+    what = "pkv_write_rope_fp8" if fp8 else "pkv_write_rope"
+    pools = (_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))[:4 if fp8 else 2]
+    with torch.cuda.device(dev):
+        _check(getattr(lib(), what)(_ptr(q), _ptr(k_new), _ptr(v_new), qs, ks, vs, _ptr(positions),
+                                    _ptr(slot_mapping), T, ctypes.byref(rope), _ptr(q_out), *pools,
+                                    ctypes.byref(desc), _stream(dev, stream)), what)
+    return q_out
+
+
+def write_rope(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, q=None, q_out=None,
+               interleaved=False, stream=None):
+    """write() with the position rotation on the way: K rows (and the queries
+    ``q`` [T, Hq, D], if given) are rotated by their ``positions`` (int64 [T])
+    through ``cos_sin`` (fp32 [max_position, rotary_dim]: cosines, then sines;
+    rotary_dim a multiple of 16, elements behind it are copied).  Pairs are
+    (i, i + rotary_dim/2), or (2i, 2i + 1) with ``interleaved``.  k_new, v_new
+    and q may be slices of one projection's output.  Returns the rotated
+    queries (``q_out``, which may be a contiguous ``q`` itself), or None."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, n, torch.bfloat16, 4)
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache shapes disagree")
+    return _write_rope(False, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, None, None, q, q_out,
+                       interleaved, stream)
+
+
+def write_rope_fp8(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q=None,
+                   q_out=None, interleaved=False, stream=None):
+    """write_rope into FP8 pages (codes and scale bytes as in write_fp8): the
+    rotated fp32 values are rounded once, to E4M3."""
+    _need_fp8_pool(k_cache, v_cache, k_scale, v_scale)
+    return _write_rope(True, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q,
+                       q_out, interleaved, stream)
+
+
+def make_latent_desc(latent_cache, num_heads, max_blocks_per_seq):
+    nb, page, row = latent_cache.shape
+    return Desc(nb, page, 1, num_heads, row, max_blocks_per_seq)
+
+
+def write_latent(c_new, k_pe, positions, cos_sin, slot_mapping, latent_cache, q_pe=None, q_out=None,
+                 interleaved=False, stream=None):
+    """Append one row a token to latent pages [NB, 16, 576]: the latent
+    ``c_new`` [T, 512] as it is, and the shared key part ``k_pe`` [T, 64]
+    rotated by its position (see write_rope; cos_sin [max_position, 64]).
+    With ``q_pe`` [T, H, 64] the queries' rotated part goes into the last 64
+    values of ``q_out`` [T, H, 576], whose first 512 are left alone.  c_new,
+    k_pe and q_pe may be slices.  Returns q_out, or None."""
+    _need(latent_cache, "latent_cache", torch.bfloat16, 3)
+    T = c_new.shape[0]
+    cs, ks = _need_rows(c_new, "c_new", LATENT_DIM), _need_rows(k_pe, "k_pe", LATENT_ROPE)
+    _need(positions, "positions", torch.int64, 1)
+    _need(slot_mapping, "slot_mapping", torch.int64, 1)
+    rope = _rope(cos_sin, interleaved)
+    if k_pe.shape[0] != T or positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("c_new, k_pe, positions and slot_mapping disagree on the number of tokens")
+    dev = latent_cache.device
+    heads, qs, hs = 1, LATENT_ROPE, LATENT_ROPE
+    if q_pe is not None:
+        if not isinstance(q_pe, torch.Tensor) or q_pe.dtype != torch.bfloat16:
+            raise TypeError(f"q_pe must be a {torch.bfloat16} tensor")
+        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != LATENT_ROPE or q_pe.stride(2) != 1:
+            raise ValueError(f"q_pe must be [tokens, H, {LATENT_ROPE}] with contiguous rows, got shape "
+                             f"{tuple(q_pe.shape)}")
+        heads = q_pe.shape[1]
+        hs = q_pe.stride(1) if heads > 1 else LATENT_ROPE
+        qs = q_pe.stride(0) if T > 1 else heads * hs
+        if hs < LATENT_ROPE or hs % 8 or qs < (heads - 1) * hs + LATENT_ROPE or qs % 8:
+            raise ValueError("q_pe's strides must be multiples of 8 elements and its rows must not overlap")
+        if q_out is None:
+            q_out = _new((T, heads, LATENT_ROW), q_pe, stream)
+        else:
+            _need(q_out, "q_out", torch.bfloat16, 3)
+            if tuple(q_out.shape) != (T, heads, LATENT_ROW):
+                raise ValueError(f"q_out must be [tokens, H, {LATENT_ROW}]")
+    elif q_out is not None:
+        raise ValueError("q_out without q_pe")
+    _need_same_device(dev, (c_new, "c_new"), (k_pe, "k_pe"), (positions, "positions"), (cos_sin, "cos_sin"),
+                      (slot_mapping, "slot_mapping"), (q_pe, "q_pe"), (q_out, "q_out"))
+    desc = make_latent_desc(latent_cache, heads, 1)
+    with torch.cuda.device(dev):
+        _check(lib().pkv_write_latent(_ptr(c_new), _ptr(k_pe), _ptr(q_pe), cs, ks, qs, hs, _ptr(positions),
+                                      _ptr(slot_mapping), T, ctypes.byref(rope), _ptr(q_out), _ptr(latent_cache),
+                                      ctypes.byref(desc), _stream(dev, stream)), "pkv_write_latent")
+    return q_out
+
+
+def workspace_size_latent(desc, num_seqs, num_tokens, device=None):
+    """Workspace bytes attend_latent needs (make_latent_desc describes the pool)."""
+    n = _sz(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(lib().pkv_attend_latent_workspace_size(ctypes.byref(desc), int(num_seqs), int(num_tokens),
+                                                      ctypes.byref(n)), "pkv_attend_latent_workspace_size")
+    return n.value
+
+
+def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scale, out=None, workspace=None,
+                  stream=None, max_query_len=0):
+    """Absorbed attention over latent pages [NB, 16, 576]: every head of
+    ``q`` [T, H, 576] against the one shared row a token, whose first 512
+    values are the value.  Returns ``out`` [T, H, 512].  The other arguments
+    are as in attend(); max_query_len (0 = unknown) selects tile sizes, never
+    results."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(latent_cache, "latent_cache", torch.bfloat16, 3)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(query_start_loc, "query_start_loc", torch.int32, 1)
+    T, H, row = q.shape
+    B = seq_lens.shape[0]
+    if query_start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("seq_lens [B], query_start_loc [B+1] and block_tables [B, M] disagree")
+    if latent_cache.shape[2] != row:
+        raise ValueError("latent_cache and q rows disagree")
+    dev = latent_cache.device
+    desc = make_latent_desc(latent_cache, H, block_tables.shape[1])
+    if out is None:
+        out = _new((T, H, LATENT_DIM), q, stream)
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        if tuple(out.shape) != (T, H, LATENT_DIM):
+            raise ValueError(f"out must be [tokens, H, {LATENT_DIM}]")
+    if workspace is None:
+        workspace = _new((workspace_size_latent(desc, B, T, dev),), q, stream, torch.uint8)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    _need_same_device(dev, (q, "q"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
+                      (query_start_loc, "query_start_loc"), (out, "out"), (workspace, "workspace"))
+    with torch.cuda.device(dev):
+        _check(lib().pkv_attend_latent(_ptr(q), _ptr(latent_cache), _ptr(block_tables), _ptr(seq_lens),
+                                       _ptr(query_start_loc), B, T, int(max_query_len), float(scale), _ptr(out),
+                                       _ptr(workspace), workspace.numel(), ctypes.byref(desc), _stream(dev, stream)),
+               "pkv_attend_latent")
     return out
 
 

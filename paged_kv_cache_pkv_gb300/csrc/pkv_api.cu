@@ -45,6 +45,26 @@ int check_desc(const pkv_desc* d) {
   return PKV_OK;
 }
 
+// Latent pages: one shared row a token, any number of query heads.
+int check_latent_desc(const pkv_desc* d) {
+  if (!d) return PKV_ERR_NULL;
+  if (d->head_dim != kLatentRow || d->page_size != kPage || d->num_kv_heads != 1) return PKV_ERR_SHAPE;
+  if (d->num_q_heads <= 0 || d->num_q_heads > PKV_LATENT_MAX_HEADS) return PKV_ERR_SHAPE;
+  if (d->num_blocks <= 0 || d->max_blocks_per_seq <= 0) return PKV_ERR_RANGE;
+  return PKV_OK;
+}
+
+// A token stride in elements: rows of `row` elements, 16-byte aligned.
+bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8; }
+
+int check_rope(const pkv_rope* r, int max_dim) {
+  if (!r || !r->cos_sin) return PKV_ERR_NULL;
+  if (!aligned(r->cos_sin, 16)) return PKV_ERR_ALIGN;
+  if (r->rotary_dim <= 0 || r->rotary_dim > max_dim || r->rotary_dim % 16) return PKV_ERR_SHAPE;
+  if (r->max_position <= 0) return PKV_ERR_RANGE;
+  return PKV_OK;
+}
+
 }  // namespace
 
 const DeviceInfo* current_device(int* err) {
@@ -263,6 +283,121 @@ int pkv_attend_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const pkv_fp8* v_c
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   return launch_attend(ctx, a);
+}
+
+static int write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
+                      int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                      const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope* rope,
+                      pkv_bf16* q_out, void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                      const pkv_desc* desc, pkv_stream_t stream, bool fp8) {
+  if (int e = check_desc(desc)) return e;
+  if (num_tokens < 0) return PKV_ERR_RANGE;
+  if (num_tokens == 0) return PKV_OK;
+  if (!k_new || !v_new || !positions || !slot_mapping || !k_cache || !v_cache || !q != !q_out ||
+      (fp8 && (!k_scale || !v_scale)))
+    return PKV_ERR_NULL;
+  if (int e = check_rope(rope, kHeadDim)) return e;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+      !aligned(positions, 8) || !aligned(slot_mapping, 8))
+    return PKV_ERR_ALIGN;
+  const int64_t kv_row = int64_t(desc->num_kv_heads) * kHeadDim;
+  if (bad_stride(k_stride, kv_row) || bad_stride(v_stride, kv_row) ||
+      (q && bad_stride(q_stride, int64_t(desc->num_q_heads) * kHeadDim)))
+    return PKV_ERR_SHAPE;
+  LaunchCtx ctx{};
+  if (int e = make_ctx(stream, &ctx)) return e;
+  RopeWriteArgs a{};
+  a.q = q, a.k = k_new, a.v = v_new;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.positions = positions, a.slots = slot_mapping, a.num_tokens = num_tokens;
+  a.cos_sin = rope->cos_sin;
+  a.max_position = rope->max_position, a.rotary_dim = rope->rotary_dim, a.interleaved = rope->interleaved;
+  a.q_out = q_out, a.k_cache = k_cache, a.v_cache = v_cache, a.k_scale = k_scale, a.v_scale = v_scale;
+  a.num_blocks = desc->num_blocks, a.num_q_heads = desc->num_q_heads, a.num_kv_heads = desc->num_kv_heads;
+  a.status = ctx.status;
+  return launch_write_rope(ctx, a, fp8);
+}
+
+int pkv_write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                   const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope* rope,
+                   pkv_bf16* q_out, pkv_bf16* k_cache, pkv_bf16* v_cache, const pkv_desc* desc,
+                   pkv_stream_t stream) {
+  return write_rope(q, k_new, v_new, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, rope,
+                    q_out, k_cache, v_cache, nullptr, nullptr, desc, stream, false);
+}
+
+int pkv_write_rope_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                       const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope* rope,
+                       pkv_bf16* q_out, pkv_fp8* k_cache, pkv_fp8* v_cache, uint8_t* k_scale,
+                       uint8_t* v_scale, const pkv_desc* desc, pkv_stream_t stream) {
+  return write_rope(q, k_new, v_new, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, rope,
+                    q_out, k_cache, v_cache, k_scale, v_scale, desc, stream, true);
+}
+
+int pkv_write_latent(const pkv_bf16* c_new, const pkv_bf16* k_pe, const pkv_bf16* q_pe, int64_t c_stride,
+                     int64_t k_stride, int64_t q_stride, int64_t q_head_stride, const int64_t* positions,
+                     const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope* rope,
+                     pkv_bf16* q_out, pkv_bf16* latent_cache, const pkv_desc* desc, pkv_stream_t stream) {
+  if (int e = check_latent_desc(desc)) return e;
+  if (num_tokens < 0) return PKV_ERR_RANGE;
+  if (num_tokens == 0) return PKV_OK;
+  if (!c_new || !k_pe || !positions || !slot_mapping || !latent_cache || !q_pe != !q_out) return PKV_ERR_NULL;
+  if (int e = check_rope(rope, kLatentRope)) return e;
+  if (rope->rotary_dim != kLatentRope) return PKV_ERR_SHAPE;
+  if (!aligned(c_new, 16) || !aligned(k_pe, 16) || !aligned(q_pe, 16) || !aligned(q_out, 16) ||
+      !aligned(latent_cache, 16) || !aligned(positions, 8) || !aligned(slot_mapping, 8))
+    return PKV_ERR_ALIGN;
+  if (bad_stride(c_stride, kLatentDim) || bad_stride(k_stride, kLatentRope) ||
+      (q_pe && (bad_stride(q_head_stride, kLatentRope) ||
+                bad_stride(q_stride, (desc->num_q_heads - 1) * q_head_stride + kLatentRope))))
+    return PKV_ERR_SHAPE;
+  LaunchCtx ctx{};
+  if (int e = make_ctx(stream, &ctx)) return e;
+  LatentWriteArgs a{};
+  a.c_new = c_new, a.k_pe = k_pe, a.q_pe = q_pe;
+  a.c_stride = c_stride, a.k_stride = k_stride, a.q_stride = q_stride, a.q_head_stride = q_head_stride;
+  a.positions = positions, a.slots = slot_mapping, a.num_tokens = num_tokens;
+  a.cos_sin = rope->cos_sin;
+  a.max_position = rope->max_position, a.interleaved = rope->interleaved;
+  a.q_out = q_out, a.cache = latent_cache;
+  a.num_blocks = desc->num_blocks, a.num_heads = desc->num_q_heads;
+  a.status = ctx.status;
+  return launch_write_latent(ctx, a);
+}
+
+int pkv_attend_latent_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                     size_t* bytes) {
+  if (int e = check_latent_desc(desc)) return e;
+  if (!bytes) return PKV_ERR_NULL;
+  if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS || num_tokens < 0) return PKV_ERR_RANGE;
+  int err = PKV_OK;
+  const DeviceInfo* dev = current_device(&err);
+  if (!dev) return err;
+  *bytes = latent_workspace_bytes(*dev);
+  return PKV_OK;
+}
+
+int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                      int32_t num_tokens, int32_t max_query_len, float scale, pkv_bf16* out,
+                      void* workspace, size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream) {
+  if (int e = check_latent_desc(desc)) return e;
+  if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS || num_tokens < 0) return PKV_ERR_RANGE;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!q || !latent_cache || !block_tables || !seq_lens || !query_start_loc || !out || !workspace)
+    return PKV_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(workspace, 256))
+    return PKV_ERR_ALIGN;
+  LaunchCtx ctx{};
+  if (int e = make_ctx(stream, &ctx)) return e;
+  const LatentAttendArgs a{q,          latent_cache, block_tables, seq_lens,  query_start_loc, num_seqs,
+                           num_tokens, max_query_len, scale,       out,       workspace,       workspace_bytes,
+                           *desc};
+  return launch_attend_latent(ctx, a);
 }
 
 int pkv_get_last_error(pkv_stream_t stream, uint32_t* flags) {

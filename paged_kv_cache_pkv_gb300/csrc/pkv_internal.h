@@ -56,6 +56,51 @@ int launch_write_fp8(const LaunchCtx& ctx, const uint16_t* k_new, const uint16_t
                      uint8_t* v_cache, uint8_t* k_scale, uint8_t* v_scale, int32_t num_blocks,
                      int32_t num_kv_heads);
 
+// pkv_write_rope / pkv_write_rope_fp8 (strides in elements, per token).
+struct RopeWriteArgs {
+  const uint16_t *q, *k, *v;  // q null: queries are not rotated
+  int64_t q_stride, k_stride, v_stride;
+  const int64_t *positions, *slots;
+  int64_t num_tokens;
+  const float* cos_sin;  // [max_position][rotary_dim]: cosines, then sines
+  int32_t max_position, rotary_dim, interleaved;
+  uint16_t* q_out;  // [T][Hq][128]
+  void *k_cache, *v_cache;
+  uint8_t *k_scale, *v_scale;  // FP8 pages only
+  int32_t num_blocks, num_q_heads, num_kv_heads;
+  unsigned* status;
+};
+int launch_write_rope(const LaunchCtx& ctx, const RopeWriteArgs& a, bool fp8);
+
+// pkv_write_latent.
+struct LatentWriteArgs {
+  const uint16_t *c_new, *k_pe, *q_pe;  // q_pe null: queries are not rotated
+  int64_t c_stride, k_stride, q_stride, q_head_stride;
+  const int64_t *positions, *slots;
+  int64_t num_tokens;
+  const float* cos_sin;  // [max_position][64]
+  int32_t max_position, interleaved;
+  uint16_t* q_out;  // [T][H][576], the last 64 of each row written
+  uint16_t* cache;  // [NB][16][576]
+  int32_t num_blocks, num_heads;
+  unsigned* status;
+};
+int launch_write_latent(const LaunchCtx& ctx, const LatentWriteArgs& a);
+
+// pkv_attend_latent (pkv_latent.cu).
+struct LatentAttendArgs {
+  const uint16_t *q, *cache;
+  const int32_t *block_tables, *seq_lens, *query_start_loc;
+  int32_t num_seqs, num_tokens, max_query_len;
+  float scale;
+  uint16_t* out;
+  void* workspace;
+  size_t workspace_bytes;
+  pkv_desc desc;
+};
+size_t latent_workspace_bytes(const DeviceInfo& dev);
+int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a);
+
 struct AttendArgs {
   const uint16_t* q;
   const void* k_cache;  // bf16 pages, or E4M3 codes when fp8
@@ -93,7 +138,7 @@ int prefill_groups(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int 
 int launch_prefill(const LaunchCtx& ctx, const AttendArgs& a, int split_max_q, int max_tiles,
                    unsigned long long* join, unsigned long long epoch);
 // Shared-prefix pass: key chunks of the prefix and tiles per chunk.
-// A tiled TMA descriptor with 128-byte swizzle (rank <= 3; strides in bytes
+// A tiled TMA descriptor with 128-byte swizzle (rank <= 5; strides in bytes
 // for dims 1..rank-1).  Returns false when the driver entry point is missing
 // or the driver rejects the description.
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int rank,

@@ -1,0 +1,854 @@
+// pkv_latent.cu -- attention over latent pages in the absorbed form: one
+// vector of 576 values a cached token is the key of every query head, and its
+// first 512 values are the value of every head.
+//
+//   s[r][k] = scale * q[r] . row[k]            r a (query token, head) pair
+//   o[r]    = sum_k softmax_k(s[r][k]) row[k][0:512],  keys k visible to r
+//
+// What bounds it: a key's 1152 bytes serve H rows of 2 * (576 + 512) FLOPs
+// each, so one query token a sequence at 128 heads is just below the ridge
+// of this GPU (242 FLOP a byte) and fewer heads are bound by HBM; several
+// query tokens a sequence are bound by the tensor cores.
+//
+// Design:
+//  * Rows of a sequence (token-major, then head: contiguous in q and out) are
+//    cut into tiles of N = 16, 32, 48 or 64 rows, so any head count fits.  A
+//    tile needs 512 x N fp32 of accumulators and one SM's TMEM holds
+//    512 x 128, all of it: N = 64 leaves room for two score tiles.
+//  * The products are computed transposed, with the cache tile as the A
+//    operand of both, straight from shared memory as TMA landed it:
+//      S^T [64 keys x N] = K Q^T      9 x 4 tcgen05.mma, M = 64, K-major A
+//      O^T [512 x N]    += V^T P^T    4 blocks of M = 128 dims, MN-major A
+//    Few rows then cost little (N is the short side), where rows as M would
+//    pad them to 64 or 128, and one copy of the tile serves both products.
+//  * A cache tile is 64 keys = 4 pages.  One TMA box a page, from the pool
+//    viewed as [groups of 8 rows][9 chunks of 64 dims][8 rows][64 dims], so
+//    that each (group, chunk) lands as one 128-byte-swizzled 1 KiB atom and
+//    atoms follow each other at one stride along keys (9 KiB) and along dims
+//    (1 KiB), as both products' descriptors need.  Two tiles are in flight.
+//  * Softmax without a row maximum a tile.  In S^T a row's scores lie across
+//    lanes and warps, where a maximum costs shuffles; but P needs only some
+//    reference m near the row's maximum: p = 2^(s - m) has the same relative
+//    precision in bf16 whatever its size.  m is the maximum of the tile's
+//    first 64 keys, and is raised (and O^T rescaled) only when a later score
+//    exceeds it by more than kTau; otherwise a tile needs one vote.
+//    Row sums add the rounded p in fp32, a partial sum a thread, joined once
+//    at the end of a tile of rows.
+//  * P is one bf16 term: rounding it (2^-9 a value, independent from key to
+//    key) adds as much error as rounding the output to bf16 does, and a
+//    second term would double the larger product's cost.
+//  * Two warpgroups run the softmax, each for half of the rows; a thread has
+//    one key and N/4 rows (16x32bx2 loads: lanes 0-15 and 16-31 read the
+//    same keys' two column halves).  One warp loads, one issues the MMAs.
+//  * Work split (stream-K): tiles of rows laid end to end, each weighing its
+//    keys plus a constant, are cut into equal shares, one a CTA; a share may
+//    start or end inside a tile.  Pieces of a cut tile leave fp32 partials
+//    (m, l, O) in the workspace that a merge kernel joins; whole tiles are
+//    written at once.  A CTA cuts at most two tiles, so the partials do not
+//    grow with the batch, and the joining order is fixed.
+//  * Every mbarrier wait is bounded; on expiry the role flags
+//    PKV_STATUS_TIMEOUT, what is in flight lands, TMEM is freed.
+#include <mutex>
+
+#include "pkv_internal.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kLtKeys = 64;                        // keys a cache tile
+constexpr int kLtPages = kLtKeys / kPage;          // 4
+constexpr int kLtChunks = kLatentRow / 64;         // 9 chunks of 64 dims (the last is rotated, keys only)
+constexpr int kLtSoftmaxThreads = 256;
+constexpr int kLtThreads = kLtSoftmaxThreads + 64;  // + loader and MMA warps
+constexpr uint32_t kLtGroupBytes = kLtChunks * 1024;         // 8 rows
+constexpr uint32_t kLtPageBytes = 2 * kLtGroupBytes;         // 18 KiB
+constexpr uint32_t kLtTileBytes = kLtPages * kLtPageBytes;   // 72 KiB
+constexpr int kLtStages = 2;
+constexpr float kLtTau = 20.0f;  // log2 of how far a score may exceed the reference
+
+// Shared memory (offsets from a 1024-byte aligned base).
+template <int N>
+struct LtSmem {
+  static constexpr uint32_t kv = 0;
+  static constexpr uint32_t q = kv + kLtStages * kLtTileBytes;  // [9][N rows][128 B]
+  static constexpr uint32_t p = q + kLtChunks * N * 128;        // [64 keys][128 B]
+  static constexpr uint32_t misc = p + kLtKeys * 128;
+  // misc: barriers, TMEM address, share bounds, per-row reductions
+  static constexpr uint32_t bars = misc;           // 16 x 8
+  static constexpr uint32_t tmem = misc + 128;
+  static constexpr uint32_t share = misc + 144;    // 2 bounds x 4 ints, then G_eff and the join's last CTA
+  static constexpr uint32_t wsum = misc + 192;     // [10] x 8, plan scan
+  static constexpr uint32_t red = misc + 272;      // [4 quadrants][N] floats
+  static constexpr uint32_t alpha = red + 16 * N;  // [N] floats
+  static constexpr uint32_t end = alpha + 4 * N;
+  static constexpr uint32_t bytes = end + 1024;    // + alignment slack
+};
+static_assert(LtSmem<64>::bytes <= 232448, "latent attention shared memory above the 227 KiB limit");
+static_assert((PKV_MAX_SEQS + 1) * 8 <= kLtTileBytes, "the plan's scan borrows the first cache tile");
+
+struct LatentParams {
+  const int32_t *block_tables, *seq_lens, *qsl;
+  uint16_t* out;
+  float* partials;     // [CTAs][2][partial_stride]
+  int4* joins;         // [CTAs] (first row, rows, last CTA, -): the tile that CTA's share ends inside
+  unsigned* status;
+  int32_t B, T, H, max_blocks, num_blocks;
+  float qscale;        // scale * log2(e)
+};
+
+// A partial: O [N][512], then m [N], l [N].
+constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
+
+// Weights of the work split, in units of (keys x heads): tile j of a sequence
+// of n query tokens and ctx = L - n earlier ones weighs H * (ctx + kLtTileCost)
+// + (j + 1) * N, which is H times its last row's keys plus a constant for
+// loading its queries and writing its result; the sum over tiles is closed.
+constexpr int kLtTileCost = 128;
+// A share is at least this many keys: below it a second CTA's start and the
+// merge cost more than the keys.
+constexpr int kLtMinShare = 256 + kLtTileCost;
+
+struct LtSeq {
+  int q0, n, L, rows, tiles;  // tiles == 0: no rows, or inconsistent
+  bool bad;
+};
+
+template <int N>
+__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b) {
+  LtSeq s;
+  s.q0 = __ldg(p.qsl + b);
+  const int q1 = __ldg(p.qsl + b + 1);
+  s.L = __ldg(p.seq_lens + b);
+  s.n = q1 - s.q0;
+  s.bad = s.q0 < 0 || s.n < 0 || q1 > p.T || s.n > s.L || s.L < 0 ||
+          (s.L + kPage - 1) / kPage > p.max_blocks || (b == 0 && s.q0 != 0);
+  if (s.bad) s.n = 0;
+  s.rows = s.n * p.H;
+  s.tiles = (s.rows + N - 1) / N;
+  return s;
+}
+
+// Weight of the first j tiles of a sequence.
+template <int N>
+__device__ __forceinline__ int64_t lt_weight(const LatentParams& p, const LtSeq& s, int64_t j) {
+  return j * (int64_t(p.H) * (s.L - s.n + kLtTileCost)) + N * (j * (j + 1) / 2);
+}
+
+// Key blocks that tile j of a sequence sees.
+template <int N>
+__device__ __forceinline__ int lt_blocks(const LatentParams& p, const LtSeq& s, int j) {
+  const int last_row = min(s.rows, (j + 1) * N) - 1;
+  const int keys = s.L - s.n + last_row / p.H + 1;
+  return (keys + kLtKeys - 1) / kLtKeys;
+}
+
+// A place in the work: key block k of tile j of sequence b (b == B: the end).
+struct LtPos {
+  int b, j, k;
+};
+
+// A piece of one tile: key blocks [k0, k1) of its `blocks`.
+struct LtPiece {
+  int b, j, k0, k1, blocks;
+  int row0, rows;   // of the tile: first row in q and out, rows
+  int local_row;    // the first row's index within the sequence's rows
+  int q0, n, L;
+};
+
+// The next piece (never empty) at `at`, and `at` moved behind it; false at
+// the share's end.
+template <int N>
+__device__ __forceinline__ bool lt_next(const LatentParams& p, LtPos& at, const LtPos& end, LtPiece& x) {
+  for (;;) {
+    if (at.b >= p.B || at.b > end.b ||
+        (at.b == end.b && (at.j > end.j || (at.j == end.j && at.k >= end.k))))
+      return false;
+    const LtSeq s = lt_seq<N>(p, at.b);
+    if (at.j >= s.tiles) {
+      at.b += 1;
+      at.j = at.k = 0;
+      continue;
+    }
+    x.b = at.b;
+    x.j = at.j;
+    x.k0 = at.k;
+    x.blocks = lt_blocks<N>(p, s, at.j);
+    x.k1 = (at.b == end.b && at.j == end.j) ? end.k : x.blocks;
+    x.local_row = at.j * N;
+    x.rows = min(N, s.rows - at.j * N);
+    x.row0 = s.q0 * p.H + at.j * N;
+    x.q0 = s.q0;
+    x.n = s.n;
+    x.L = s.L;
+    at.j += 1;
+    at.k = 0;
+    return true;
+  }
+}
+
+// tcgen05.ld of X columns: lanes 0-15 read theirs from taddr on, lanes 16-31
+// the same TMEM lanes' columns SPLIT further on.
+#define PKV_LD_SPLIT(SPLIT)                                                                       \
+  if constexpr (X == 4)                                                                           \
+    asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x4.b32 {%0, %1, %2, %3}, [%4], " #SPLIT ";"    \
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])                                 \
+                 : "r"(taddr));                                                                   \
+  else if constexpr (X == 8)                                                                      \
+    asm volatile(                                                                                 \
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], " #SPLIT \
+        ";"                                                                                       \
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),     \
+          "=f"(r[7])                                                                              \
+        : "r"(taddr));                                                                            \
+  else                                                                                            \
+    asm volatile(                                                                                 \
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, " \
+        "%11, %12, %13, %14, %15}, [%16], " #SPLIT ";"                                            \
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),     \
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),              \
+          "=f"(r[13]), "=f"(r[14]), "=f"(r[15])                                                   \
+        : "r"(taddr));
+
+// N/4 score columns a thread: columns c0.. for lanes 0-15, c0 + N/4.. for 16-31.
+template <int N>
+__device__ __forceinline__ void lt_load_scores(uint32_t taddr, float (&s)[N / 4]) {
+  float* r = s;
+  if constexpr (N == 16) {
+    constexpr int X = 4;
+    PKV_LD_SPLIT(4)
+  } else if constexpr (N == 32) {
+    constexpr int X = 8;
+    PKV_LD_SPLIT(8)
+  } else if constexpr (N == 48) {
+    {
+      constexpr int X = 8;
+      PKV_LD_SPLIT(12)
+    }
+    r += 8;
+    taddr += 8;
+    {
+      constexpr int X = 4;
+      PKV_LD_SPLIT(12)
+    }
+  } else {
+    constexpr int X = 16;
+    PKV_LD_SPLIT(16)
+  }
+}
+#undef PKV_LD_SPLIT
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+                 "=f"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]));
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// kind::f16 instruction descriptor: bf16 A and B, fp32 D.
+constexpr uint32_t lt_idesc(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kLtThreads, 1)
+    pkv_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                      const LatentParams p) {
+  using S = LtSmem<N>;
+  constexpr int NC = N / 4;  // score columns a thread
+  constexpr int NW = N / 2;  // rows a softmax warpgroup
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
+  uint64_t* bar_q = bars;            // a tile's queries landed
+  uint64_t* bar_qfree = bars + 1;    // its score MMAs are done
+  uint64_t* bar_kv = bars + 2;       // [2] cache tile landed
+  uint64_t* bar_kvfree = bars + 4;   // [2] the MMAs that read it are done
+  uint64_t* bar_s = bars + 6;        // [2] scores written
+  uint64_t* bar_p = bars + 8;        // P written (256 arrivals)
+  uint64_t* bar_o = bars + 9;        // P V done: P's buffer is free, O^T up to date
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
+  int* s_share = reinterpret_cast<int*>(sm + S::share);
+  int64_t* s_wsum = reinterpret_cast<int64_t*>(sm + S::wsum);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) mbar_init(bars + i, bars + i == bar_p ? kLtSoftmaxThreads : 1);
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (warp == 8 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+  }
+  griddep_wait();  // what the stream did before: the queries, this step's rows, the metadata
+
+  // ---- plan: this CTA's share of the work -------------------------------------
+  {
+    int64_t* s_scan = reinterpret_cast<int64_t*>(sm + S::kv);  // weight before sequence b
+    const int per = (p.B + kLtThreads - 1) / kLtThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    int64_t local = 0;
+    for (int b = b0; b < b1; ++b) {
+      const LtSeq s = lt_seq<N>(p, b);
+      if (s.bad && blockIdx.x == 0) flag_status(p.status, PKV_STATUS_BAD_QUERY);
+      const int64_t w = lt_weight<N>(p, s, s.tiles);
+      s_scan[b] = w;
+      local += w;
+    }
+    int64_t incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
+    __syncthreads();
+    int64_t run = incl - local, total = 0;
+#pragma unroll
+    for (int x = 0; x < kLtThreads / 32; ++x) {
+      if (x < warp) run += s_wsum[x];
+      total += s_wsum[x];
+    }
+    for (int b = b0; b < b1; ++b) {
+      const int64_t w = s_scan[b];
+      s_scan[b] = run;
+      run += w;
+    }
+    if (tid == 0) s_scan[p.B] = total;
+    __syncthreads();
+    if (tid < 2) {  // thread 0: the share's start, thread 1: its end
+      int64_t g = total / (int64_t(p.H) * kLtMinShare);
+      g = g < 1 ? 1 : g > gridDim.x ? gridDim.x : g;
+      const int64_t c = int64_t(blockIdx.x) + tid;
+      LtPos at{p.B, 0, 0};
+      int last = -1;
+      if (total > 0 && c < g) {
+        const int64_t x = c * total / g;
+        int lo = 0, hi = p.B;  // last b with s_scan[b] <= x
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_scan[mid] <= x) lo = mid; else hi = mid;
+        }
+        const LtSeq s = lt_seq<N>(p, lo);
+        const int64_t y = x - s_scan[lo];
+        int jl = 0, jh = s.tiles;  // last j with weight(j) <= y
+        while (jh - jl > 1) {
+          const int mid = (jl + jh) >> 1;
+          if (lt_weight<N>(p, s, mid) <= y) jl = mid; else jh = mid;
+        }
+        const int64_t w0 = lt_weight<N>(p, s, jl), w1 = lt_weight<N>(p, s, jl + 1);
+        at.b = lo;
+        at.j = jl;
+        at.k = int((y - w0) * lt_blocks<N>(p, s, jl) / (w1 - w0));
+        // the last CTA whose share starts before this tile's end
+        const int64_t e = s_scan[lo] + w1;
+        last = int((e * g + total - 1) / total) - 1;
+      }
+      s_share[tid * 4] = at.b;
+      s_share[tid * 4 + 1] = at.j;
+      s_share[tid * 4 + 2] = at.k;
+      s_share[tid * 4 + 3] = last;
+    }
+    // the scan's words are rewritten by the copy engine
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const LtPos begin{s_share[0], s_share[1], s_share[2]};
+  const LtPos end{s_share[4], s_share[5], s_share[6]};
+  auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
+
+  if (warp == 8) {
+    // ===== loader: queries and cache tiles, in the order they are used =====
+    LtPos at = begin;
+    LtPiece x;
+    int g = 0, pieces = 0;  // cache tiles and tiles of rows so far
+    bool ok = true;
+    while (ok && lt_next<N>(p, at, end, x)) {
+      if (lane == 0) {
+        if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
+        if (ok) {
+          mbar_arrive_expect_tx(bar_q, kLtChunks * N * 128);
+          if (!(kDropFirstCopy && pieces == 0)) tma_load_3d(sm + S::q, &tm_q, 0, x.row0, 0, bar_q);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      ++pieces;
+      const int32_t* table = p.block_tables + int64_t(x.b) * p.max_blocks;
+      const int pages = (x.L + kPage - 1) / kPage;
+      // lane l: page l of a group of eight cache tiles, read a group ahead.
+      // -1 past the sequence (no copy); an id that is no page of the pool is
+      // flagged and page 0 is read in its place.
+      auto group_id = [&](int k) {
+        const int i = k * kLtPages + lane;
+        if (i >= x.k1 * kLtPages || i >= pages) return -1;
+        int id = __ldg(table + i);
+        if (id < 0 || id >= p.num_blocks) {
+          flag_status(p.status, PKV_STATUS_BAD_BLOCK);
+          id = 0;
+        }
+        return id;
+      };
+      int ids = group_id(x.k0), next = group_id(x.k0 + 8);
+      for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+        const int in_group = (k - x.k0) & 7;
+        if (k > x.k0 && in_group == 0) {
+          ids = next;
+          next = group_id(k + 8);
+        }
+        int id[kLtPages];
+        int valid = 0;
+#pragma unroll
+        for (int i = 0; i < kLtPages; ++i) {
+          id[i] = __shfl_sync(0xffffffffu, ids, in_group * kLtPages + i);
+          valid += id[i] >= 0;
+        }
+        const int st = g % kLtStages;
+        if (lane == 0) {
+          if (g >= kLtStages) ok = mbar_wait(bar_kvfree + st, (g / kLtStages - 1) & 1);
+          if (ok) {
+            mbar_arrive_expect_tx(bar_kv + st, uint32_t(valid) * kLtPageBytes);
+#pragma unroll
+            for (int i = 0; i < kLtPages; ++i)
+              if (id[i] >= 0)
+                tma_load_4d(sm + S::kv + st * kLtTileBytes + i * kLtPageBytes, &tm_kv, 0, 0, 0, 2 * id[i],
+                            bar_kv + st);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        if (!ok) break;
+      }
+    }
+    if (lane == 0) {
+      // copies land before the CTA's shared memory is released
+      const uint64_t limit = ok ? kLandLimitNs : kDrainLimitNs;
+      for (int i = g > kLtStages ? g - kLtStages : 0; i < g; ++i)
+        mbar_wait(bar_kv + i % kLtStages, (i / kLtStages) & 1, limit);
+      if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);
+      if (!ok) flag_status(p.status, PKV_STATUS_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ===== MMA issuer: scores of tile g + 1 before P V of tile g =====
+    constexpr uint32_t idesc_s = lt_idesc(64, N, false, false);
+    constexpr uint32_t idesc_o = lt_idesc(128, N, true, true);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    const uint32_t aq = smem_u32(sm + S::q), ap = smem_u32(sm + S::p);
+    LtPos at = begin;
+    LtPiece x;
+    int g = 0, pieces = 0, ns = 0, npv = 0;
+    bool ok = true;
+    auto issue_scores = [&](int t) {
+      const uint32_t kv = smem_u32(sm + S::kv + (t % kLtStages) * kLtTileBytes);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kLtChunks; ++c)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma(tmem_s(t), smem_desc(kv + c * 1024 + kk * 32, 16, kLtGroupBytes),
+               smem_desc(aq + c * (N * 128) + kk * 32, 16, 1024), idesc_s, c + kk > 0);
+      umma_commit(bar_s + (t & 1));
+      ++ns;
+    };
+    while (ok && lt_next<N>(p, at, end, x)) {
+      const int tiles = x.k1 - x.k0;
+      if (!(ok = wait_all(bar_q, pieces & 1) && wait_all(bar_kv + g % kLtStages, (g / kLtStages) & 1))) break;
+      issue_scores(g);
+      if (tiles == 1) umma_commit(bar_qfree);
+      for (int i = 0; i < tiles; ++i, ++g) {
+        if (i + 1 < tiles) {
+          if (!(ok = wait_all(bar_kv + (g + 1) % kLtStages, ((g + 1) / kLtStages) & 1))) break;
+          issue_scores(g + 1);
+          if (i + 2 == tiles) umma_commit(bar_qfree);
+        }
+        if (!(ok = wait_all(bar_p, g & 1))) break;
+        tc_fence_after();
+        const uint32_t kv = smem_u32(sm + S::kv + (g % kLtStages) * kLtTileBytes);
+#pragma unroll
+        for (int ks = 0; ks < kLtPages; ++ks)
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
+                 smem_desc(ap + ks * 2048, 1024, 1024), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
+        umma_commit(bar_kvfree + g % kLtStages);
+        umma_commit(bar_o);
+        ++npv;
+      }
+      ++pieces;
+    }
+    if (!ok && lane == 0) flag_status(p.status, PKV_STATUS_TIMEOUT);
+    // what was issued lands before TMEM is released
+    if (ns > 0) mbar_wait(bar_s + ((ns - 1) & 1), ((ns - 1) >> 1) & 1, kLandLimitNs);
+    if (npv > 0) mbar_wait(bar_o, (npv - 1) & 1, kLandLimitNs);
+    __syncwarp();
+  } else {
+    // ===== softmax and results: warpgroup w has rows [w * NW, (w + 1) * NW) =====
+    const int wg = warp >> 2, quad = warp & 3, half = lane >> 4;
+    const int key = quad * 16 + (lane & 15);      // this thread's key of a tile
+    const int col0 = wg * NW + half * NC;         // its first row
+    const uint32_t lane_off = uint32_t(quad * 32) << 16;
+    float* s_red = reinterpret_cast<float*>(sm + S::red);      // [4][N]
+    float* s_alpha = reinterpret_cast<float*>(sm + S::alpha);  // [N]
+    const int bar_id = 1 + wg;
+    LtPos at = begin;
+    LtPiece x;
+    int g = 0;
+    // A warp whose wait ran out waits no more, but goes through the rest of
+    // its share all the same (writing no result), so that the warpgroup's
+    // barriers keep all their threads.
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    while (lt_next<N>(p, at, end, x)) {
+      float m[NC], l[NC];
+      int lim[NC];  // last key that the row sees
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        m[c] = 0.f;
+        l[c] = 0.f;
+        lim[c] = x.L - x.n + min(x.n - 1, (x.local_row + col0 + c) / p.H);
+      }
+      const int first_lim = x.L - x.n + x.local_row / p.H;  // the tile's first row's
+      for (int k = x.k0; k < x.k1; ++k, ++g) {
+        wait(bar_s + (g & 1), (g >> 1) & 1);
+        tc_fence_after();
+        float s[NC];
+        lt_load_scores<N>(tmem_s(g) + uint32_t(wg * NW) + lane_off, s);
+        tmem_wait_ld();
+        const int pos = k * kLtKeys + key;
+        const bool masked = k * kLtKeys + kLtKeys - 1 > first_lim;
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          s[c] *= p.qscale;
+          if (masked && pos > lim[c]) s[c] = -INFINITY;
+          top = fmaxf(top, s[c] - m[c]);
+        }
+        const bool first = k == x.k0;
+        if (named_sync_or(bar_id, 128, first || top > kLtTau)) {
+          // New references: the maximum over the tile's 64 keys, if above the
+          // old one.  Rows that see nothing yet keep reference 0: they see
+          // nothing of this piece (what a row sees is a prefix).
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float v = s[c];
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if ((lane & 15) == 0) s_red[quad * N + col0 + c] = v;
+          }
+          named_sync(bar_id, 128);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            float v = s_red[col0 + c];
+#pragma unroll
+            for (int q = 1; q < 4; ++q) v = fmaxf(v, s_red[q * N + col0 + c]);
+            float a = 1.f;
+            if (first) {
+              m[c] = v == -INFINITY ? 0.f : v;
+            } else if (v > m[c]) {
+              a = ex2(m[c] - v);
+              m[c] = v;
+              l[c] *= a;
+            }
+            if (quad == 0 && (lane & 15) == 0) s_alpha[col0 + c] = a;
+          }
+          if (!first) {
+            // O^T of the earlier tiles under the new references
+            named_sync(bar_id, 128);
+            wait(bar_o, (g - 1) & 1);
+            tc_fence_after();
+#pragma unroll 1
+            for (int d = 0; d < 4; ++d)
+#pragma unroll 1
+              for (int c = 0; c < NW; c += 8) {
+                const uint32_t ta = tmem + uint32_t(d * N + wg * NW + c) + lane_off;
+                float o[8];
+                tmem_ld8(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= s_alpha[wg * NW + c + e];
+                tmem_st8(ta, o);
+              }
+            tmem_wait_st();
+          }
+        }
+        uint32_t pk[NC / 2];
+#pragma unroll
+        for (int c = 0; c < NC; c += 2) {
+          pk[c / 2] = pack_bf16x2(ex2(s[c] - m[c]), ex2(s[c + 1] - m[c + 1]));
+          l[c] += bf_lo(pk[c / 2]);
+          l[c + 1] += bf_hi(pk[c / 2]);
+        }
+        // P's buffer is free once the product before is done
+        if (g > 0) wait(bar_o, (g - 1) & 1);
+        if (!ok) continue;
+        uint8_t* prow = sm + S::p + key * 128;
+#pragma unroll
+        for (int c = 0; c < NC; c += 4) {
+          const uint32_t byte = uint32_t(col0 + c) * 2;
+          *reinterpret_cast<uint2*>(prow + (((byte >> 4) ^ (key & 7)) << 4) + (byte & 8)) =
+              make_uint2(pk[c / 2], pk[c / 2 + 1]);
+        }
+        const int valid = x.L - k * kLtKeys;
+        if (valid < kLtKeys) {
+          // rows past the sequence hold whatever the pages or the buffer
+          // held: zero their values, since 0 x NaN is NaN (their scores are
+          // masked).  The scores' MMAs are done, this tile's P V not issued.
+          uint8_t* kv = sm + S::kv + (g % kLtStages) * kLtTileBytes;
+          for (int i = tid; i < (kLtKeys - valid) * 64; i += kLtSoftmaxThreads) {
+            const int r = valid + (i >> 6), ch = (i >> 3) & 7, v = i & 7;
+            *reinterpret_cast<uint4*>(kv + (r >> 3) * kLtGroupBytes + ch * 1024 + (r & 7) * 128 + v * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar_p);
+      }
+
+      // ---- the piece's result ----
+      const bool whole = x.k0 == 0 && x.k1 == x.blocks;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
+      }
+      named_sync(bar_id, 128);  // s_red's last readers are done
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        if ((lane & 15) == 0) s_red[quad * N + col0 + c] = l[c];
+      float* part = p.partials + (size_t(blockIdx.x) * 2 + (x.k0 == 0 ? 1 : 0)) * kLtPartialFloats;
+      if (!whole && quad == 0 && (lane & 15) == 0) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) part[N * kLatentDim + col0 + c] = m[c];
+      }
+      named_sync(bar_id, 128);
+      auto row_sum = [&](int r) { return (s_red[r] + s_red[N + r]) + (s_red[2 * N + r] + s_red[3 * N + r]); };
+      if (!whole && quad == 0 && lane < NW) part[N * kLatentDim + N + wg * NW + lane] = row_sum(wg * NW + lane);
+      wait(bar_o, (g - 1) & 1);
+      if (ok) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < NW; c += 8) {
+          const int r0 = wg * NW + c;  // first row of the eight
+          if (r0 >= x.rows) break;
+          float inv[8];
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              inv[e] = 1.f / row_sum(r0 + e);
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            float o[8];
+            tmem_ld8(tmem + uint32_t(d * N + r0) + lane_off, o);
+            tmem_wait_ld();
+            const int dim = d * 128 + quad * 32 + lane;
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (r0 + e < x.rows) {
+                  const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv[e]);
+                  p.out[size_t(x.row0 + r0 + e) * kLatentDim + dim] = *reinterpret_cast<const uint16_t*>(&v);
+                }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) part[(r0 + e) * kLatentDim + dim] = o[e];
+            }
+          }
+        }
+        tc_fence_before();  // read before the next piece's first P V overwrites it
+      }
+    }
+    if (!ok) flag_status(p.status, PKV_STATUS_TIMEOUT);
+    // A share that begins and ends at the same block inside a tile is a piece
+    // without keys, which the merge skips by its l of 0.
+    if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < N)
+      p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + N * kLatentDim + N + tid] = 0.f;
+    // what the merge joins for this CTA: the tile its share ends inside, if
+    // its first block is in this share
+    if (tid == 0) {
+      int4 join = make_int4(0, 0, 0, 0);
+      if (end.b < p.B && end.k > 0 &&
+          (begin.b < end.b || (begin.b == end.b && (begin.j < end.j || (begin.j == end.j && begin.k == 0))))) {
+        const LtSeq s = lt_seq<N>(p, end.b);
+        join = make_int4(s.q0 * p.H + end.j * N, min(N, s.rows - end.j * N), s_share[7], 0);
+      }
+      p.joins[blockIdx.x] = join;
+    }
+  }
+  // Let the merge kernel be scheduled; it waits for this grid.
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+// Joins the pieces of one cut tile: block (c, y) row y of the tile that CTA
+// c's share ended inside; its pieces are c's second partial and the first
+// partials of c + 1 .. last.  With weights w_i = 2^(m_i - M), M the largest
+// reference of a piece that saw a key: out = sum w_i O_i / sum w_i l_i.
+template <int N>
+__global__ void __launch_bounds__(128) pkv_latent_merge_kernel(const LatentParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = blockIdx.x, r = blockIdx.y;
+  const int4 join = __ldcg(p.joins + c);
+  if (r >= join.y) return;
+  const int pieces = join.z - c + 1;
+  auto part = [&](int i) {
+    return p.partials + (i == 0 ? size_t(c) * 2 + 1 : size_t(c + i) * 2) * kLtPartialFloats;
+  };
+  float M = -INFINITY;
+  for (int i = 0; i < pieces; ++i) {
+    const float* head = part(i) + N * kLatentDim;
+    if (__ldcg(head + N + r) != 0.f) M = fmaxf(M, __ldcg(head + r));
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const float* head = part(i) + N * kLatentDim;
+    const float l = __ldcg(head + N + r);
+    if (l == 0.f) continue;  // saw no key: its O is not read
+    const float w = ex2(__ldcg(head + r) - M);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(part(i) + size_t(r) * kLatentDim) + threadIdx.x);
+    sum += w * l;
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+  }
+  const float inv = 1.f / sum;
+  const uint2 v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *(reinterpret_cast<uint2*>(p.out + size_t(join.x + r) * kLatentDim) + threadIdx.x) = v;
+}
+
+template <int N>
+int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams lp) {
+  static std::mutex mu;
+  static bool ready[64] = {};
+  const int device = ctx.dev->device;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!ready[device]) {
+      if (cudaFuncSetAttribute(pkv_latent_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(LtSmem<N>::bytes)) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_LAUNCH;
+      }
+      ready[device] = true;
+    }
+  }
+  const pkv_desc& d = a.desc;
+  CUtensorMap tq, tkv;
+  {
+    const cuuint64_t dims[3] = {64, cuuint64_t(a.num_tokens) * d.num_q_heads, kLtChunks};
+    const cuuint64_t strides[2] = {kLatentRow * 2, 128};
+    const cuuint32_t box[3] = {64, N, kLtChunks};
+    if (!encode_tensor_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box)) return PKV_ERR_LAUNCH;
+  }
+  {
+    const cuuint64_t dims[4] = {64, 8, kLtChunks, cuuint64_t(d.num_blocks) * 2};
+    const cuuint64_t strides[3] = {kLatentRow * 2, 128, kLatentRow * 16};
+    const cuuint32_t box[4] = {64, 8, kLtChunks, 2};
+    if (!encode_tensor_map(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.cache, 4, dims, strides, box))
+      return PKV_ERR_LAUNCH;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctx.dev->sm_count);
+  cfg.blockDim = dim3(kLtThreads);
+  cfg.dynamicSmemBytes = LtSmem<N>::bytes;
+  cfg.stream = ctx.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  {
+    TraceScope ts(ctx.stream, PKV_K_LATENT);
+    cudaLaunchKernelEx(&cfg, pkv_latent_kernel<N>, tq, tkv, lp);
+    if (int e = ts.done()) return e;
+  }
+  cfg.gridDim = dim3(ctx.dev->sm_count, N);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  TraceScope ts(ctx.stream, PKV_K_MERGE);
+  cudaLaunchKernelEx(&cfg, pkv_latent_merge_kernel<N>, lp);
+  return ts.done();
+}
+
+}  // namespace
+
+// Two partials and one join record a CTA, whatever the batch.
+size_t latent_workspace_bytes(const DeviceInfo& dev) {
+  return align_up(size_t(dev.sm_count) * 2 * kLtPartialFloats * sizeof(float), 256) +
+         align_up(size_t(dev.sm_count) * sizeof(int4), 256);
+}
+
+int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
+  const pkv_desc& d = a.desc;
+  // rows are int32 on the device, and so are the tensor map's coordinates
+  if (int64_t(a.num_tokens) * d.num_q_heads >= (int64_t(1) << 31) - 64) return PKV_ERR_RANGE;
+  if (int64_t(d.num_blocks) * 2 >= (int64_t(1) << 31)) return PKV_ERR_RANGE;
+  // the plan multiplies the batch's weight by the CTAs in 64 bits
+  const double heaviest = 2.0 * d.num_q_heads * (16.0 * d.max_blocks_per_seq + kLtTileCost) + 64.0;
+  const double tiles_bound = double(a.num_tokens) * d.num_q_heads / 16.0 + a.num_seqs;
+  if (heaviest * tiles_bound * ctx.dev->sm_count >= 9.0e18) return PKV_ERR_RANGE;
+  if (a.workspace_bytes < latent_workspace_bytes(*ctx.dev)) return PKV_ERR_WORKSPACE;
+  LatentParams lp{};
+  lp.block_tables = a.block_tables;
+  lp.seq_lens = a.seq_lens;
+  lp.qsl = a.query_start_loc;
+  lp.out = a.out;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  lp.partials = reinterpret_cast<float*>(ws);
+  lp.joins = reinterpret_cast<int4*>(
+      ws + align_up(size_t(ctx.dev->sm_count) * 2 * kLtPartialFloats * sizeof(float), 256));
+  lp.status = ctx.status;
+  lp.B = a.num_seqs;
+  lp.T = a.num_tokens;
+  lp.H = d.num_q_heads;
+  lp.max_blocks = d.max_blocks_per_seq;
+  lp.num_blocks = d.num_blocks;
+  lp.qscale = a.scale * 1.4426950408889634f;
+  // Rows a tile: the least multiple of 16 that cuts the longest sequence's
+  // rows into as few tiles as 64 would.
+  const int64_t most = a.max_query_len > 0 && a.max_query_len < a.num_tokens ? a.max_query_len : a.num_tokens;
+  const int64_t rows = most * d.num_q_heads;
+  const int64_t tiles = (rows + 63) / 64;
+  const int64_t per = (rows + tiles - 1) / tiles;
+  if (per <= 16) return launch_latent<16>(ctx, a, lp);
+  if (per <= 32) return launch_latent<32>(ctx, a, lp);
+  if (per <= 48) return launch_latent<48>(ctx, a, lp);
+  return launch_latent<64>(ctx, a, lp);
+}
+
+}  // namespace pkv
