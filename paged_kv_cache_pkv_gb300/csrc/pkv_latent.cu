@@ -248,6 +248,25 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
                "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]));
 }
+// X columns (a multiple of 8) of this warp's 32 lanes.
+template <int X>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[X]) {
+#pragma unroll
+  for (int i = 0; i < X; i += 8) tmem_ld8(taddr + i, r + i);
+}
+
+// One non-blocking test of a barrier's phase.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                             uint64_t* bar) {
@@ -450,52 +469,58 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ===== MMA issuer: scores of tile g + 1 before P V of tile g =====
+    // ===== MMA issuer =====
+    // Within a piece, whichever product can go next goes: the scores of the
+    // next tile once it has landed and the softmax is done with their buffer,
+    // or P V of the oldest tile whose P is written; scores first where both
+    // can, so that the softmax of one tile runs under P V of the other.  (In
+    // a fixed order, P V waited for the next tile's copies, and those for the
+    // buffer that P V frees: 5000 cycles a tile against 2200.)
     constexpr uint32_t idesc_s = lt_idesc(64, N, false, false);
     constexpr uint32_t idesc_o = lt_idesc(128, N, true, true);
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-    };
     const uint32_t aq = smem_u32(sm + S::q), ap = smem_u32(sm + S::p);
+    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
     LtPos at = begin;
     LtPiece x;
-    int g = 0, pieces = 0, ns = 0, npv = 0;
+    int ns = 0, npv = 0, pieces = 0;  // scores and P V of tiles issued so far
     bool ok = true;
-    auto issue_scores = [&](int t) {
-      const uint32_t kv = smem_u32(sm + S::kv + (t % kLtStages) * kLtTileBytes);
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < kLtChunks; ++c)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma(tmem_s(t), smem_desc(kv + c * 1024 + kk * 32, 16, kLtGroupBytes),
-               smem_desc(aq + c * (N * 128) + kk * 32, 16, 1024), idesc_s, c + kk > 0);
-      umma_commit(bar_s + (t & 1));
-      ++ns;
-    };
     while (ok && lt_next<N>(p, at, end, x)) {
-      const int tiles = x.k1 - x.k0;
-      if (!(ok = wait_all(bar_q, pieces & 1) && wait_all(bar_kv + g % kLtStages, (g / kLtStages) & 1))) break;
-      issue_scores(g);
-      if (tiles == 1) umma_commit(bar_qfree);
-      for (int i = 0; i < tiles; ++i, ++g) {
-        if (i + 1 < tiles) {
-          if (!(ok = wait_all(bar_kv + (g + 1) % kLtStages, ((g + 1) / kLtStages) & 1))) break;
-          issue_scores(g + 1);
-          if (i + 2 == tiles) umma_commit(bar_qfree);
+      const int last = npv + x.k1 - x.k0;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_q, pieces & 1));
+      uint64_t since = 0;  // of the first test in a row that found nothing to do
+      int idle = 0;
+      while (ok && npv < last) {
+        if (ns < last && ns <= npv + 1 && ready(bar_kv + ns % kLtStages, (ns / kLtStages) & 1)) {
+          const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(ns % kLtStages) * kLtTileBytes;
+          tc_fence_after();
+#pragma unroll 3
+          for (int c = 0; c < kLtChunks; ++c)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma(tmem_s(ns), smem_desc(kv + c * 1024 + kk * 32, 16, kLtGroupBytes),
+                   smem_desc(aq + c * (N * 128) + kk * 32, 16, 1024), idesc_s, c + kk > 0);
+          umma_commit(bar_s + (ns & 1));
+          if (++ns == last) umma_commit(bar_qfree);
+          idle = 0;
+        } else if (npv < ns && ready(bar_p, npv & 1)) {
+          const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(npv % kLtStages) * kLtTileBytes;
+          const uint32_t more = npv > last - (x.k1 - x.k0) ? 1u : 0u;  // not the piece's first tile
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < kLtPages; ++ks)
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+              umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
+                   smem_desc(ap + ks * 2048, 1024, 1024), idesc_o, ks > 0 ? 1u : more);
+          umma_commit(bar_kvfree + npv % kLtStages);
+          umma_commit(bar_o);
+          ++npv;
+          idle = 0;
+        } else if (idle++ == 0) {
+          since = global_ns();
+        } else if ((idle & 63) == 0) {
+          ok = __all_sync(0xffffffffu, global_ns() - since <= kWaitLimitNs);
         }
-        if (!(ok = wait_all(bar_p, g & 1))) break;
-        tc_fence_after();
-        const uint32_t kv = smem_u32(sm + S::kv + (g % kLtStages) * kLtTileBytes);
-#pragma unroll
-        for (int ks = 0; ks < kLtPages; ++ks)
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
-                 smem_desc(ap + ks * 2048, 1024, 1024), idesc_o, (i > 0 || ks > 0) ? 1u : 0u);
-        umma_commit(bar_kvfree + g % kLtStages);
-        umma_commit(bar_o);
-        ++npv;
       }
       ++pieces;
     }
@@ -541,18 +566,29 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         tmem_wait_ld();
         const int pos = k * kLtKeys + key;
         const bool masked = k * kLtKeys + kLtKeys - 1 > first_lim;
-        float top = -INFINITY;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           s[c] *= p.qscale;
           if (masked && pos > lim[c]) s[c] = -INFINITY;
-          top = fmaxf(top, s[c] - m[c]);
         }
-        const bool first = k == x.k0;
-        if (named_sync_or(bar_id, 128, first || top > kLtTau)) {
-          // New references: the maximum over the tile's 64 keys, if above the
-          // old one.  Rows that see nothing yet keep reference 0: they see
-          // nothing of this piece (what a row sees is a prefix).
+        if (k == x.k0) {
+          // A piece's first reference is its first key's score.  Rows that do
+          // not see that key see nothing of this piece (what a row sees is a
+          // prefix) and keep 0.
+          if (key == 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) s_alpha[col0 + c] = s[c] == -INFINITY ? 0.f : s[c];
+          }
+          named_sync(bar_id, 128);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) m[c] = s_alpha[col0 + c];
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) top = fmaxf(top, s[c] - m[c]);
+        if (named_sync_or(bar_id, 128, top > kLtTau)) {
+          // New references: the maximum over the tile's 64 keys where that is
+          // above the old one.
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             float v = s[c];
@@ -567,16 +603,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 #pragma unroll
             for (int q = 1; q < 4; ++q) v = fmaxf(v, s_red[q * N + col0 + c]);
             float a = 1.f;
-            if (first) {
-              m[c] = v == -INFINITY ? 0.f : v;
-            } else if (v > m[c]) {
+            if (v > m[c]) {
               a = ex2(m[c] - v);
               m[c] = v;
               l[c] *= a;
             }
             if (quad == 0 && (lane & 15) == 0) s_alpha[col0 + c] = a;
           }
-          if (!first) {
+          if (k > x.k0) {
             // O^T of the earlier tiles under the new references
             named_sync(bar_id, 128);
             wait(bar_o, (g - 1) & 1);
@@ -647,39 +681,42 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         for (int c = 0; c < NC; ++c) part[N * kLatentDim + col0 + c] = m[c];
       }
       named_sync(bar_id, 128);
-      auto row_sum = [&](int r) { return (s_red[r] + s_red[N + r]) + (s_red[2 * N + r] + s_red[3 * N + r]); };
-      if (!whole && quad == 0 && lane < NW) part[N * kLatentDim + N + wg * NW + lane] = row_sum(wg * NW + lane);
+      if (quad == 0 && lane < NW) {
+        const int r = wg * NW + lane;
+        const float sum = (s_red[r] + s_red[N + r]) + (s_red[2 * N + r] + s_red[3 * N + r]);
+        if (whole)
+          s_alpha[r] = 1.f / sum;
+        else
+          part[N * kLatentDim + N + r] = sum;
+      }
+      named_sync(bar_id, 128);
       wait(bar_o, (g - 1) & 1);
       if (ok) {
         tc_fence_after();
+        const int r0 = wg * NW;  // this warpgroup's rows of the tile
 #pragma unroll 1
-        for (int c = 0; c < NW; c += 8) {
-          const int r0 = wg * NW + c;  // first row of the eight
-          if (r0 >= x.rows) break;
-          float inv[8];
+        for (int d = 0; d < 4; ++d) {
+          float o[NW];  // lane: dim d * 128 + quad * 32 + lane; column: row
+          tmem_ld_cols<NW>(tmem + uint32_t(d * N + r0) + lane_off, o);
+          tmem_wait_ld();
+          const int dim = d * 128 + quad * 32;
           if (whole) {
+            // two rows at a time: even lanes take the first row's pair of
+            // dims, odd lanes the second's, so a lane stores two values
+            uint32_t* to = reinterpret_cast<uint32_t*>(p.out + size_t(x.row0 + r0 + (lane & 1)) * kLatentDim + dim) +
+                           (lane >> 1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              inv[e] = 1.f / row_sum(r0 + e);
+            for (int c = 0; c < NW; c += 2) {
+              const float a = o[c] * s_alpha[r0 + c], b = o[c + 1] * s_alpha[r0 + c + 1];
+              const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+              if (r0 + c + (lane & 1) < x.rows)
+                to[c * (kLatentDim / 2)] = (lane & 1) ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
             }
-          }
+          } else {
+            float* to = part + size_t(r0) * kLatentDim + dim + lane;
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            float o[8];
-            tmem_ld8(tmem + uint32_t(d * N + r0) + lane_off, o);
-            tmem_wait_ld();
-            const int dim = d * 128 + quad * 32 + lane;
-            if (whole) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (r0 + e < x.rows) {
-                  const __nv_bfloat16 v = __float2bfloat16_rn(o[e] * inv[e]);
-                  p.out[size_t(x.row0 + r0 + e) * kLatentDim + dim] = *reinterpret_cast<const uint16_t*>(&v);
-                }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) part[(r0 + e) * kLatentDim + dim] = o[e];
-            }
+            for (int c = 0; c < NW; ++c)
+              if (r0 + c < x.rows) to[c * kLatentDim] = o[c];
           }
         }
         tc_fence_before();  // read before the next piece's first P V overwrites it
@@ -711,44 +748,126 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-// Joins the pieces of one cut tile: block (c, y) row y of the tile that CTA
-// c's share ended inside; its pieces are c's second partial and the first
-// partials of c + 1 .. last.  With weights w_i = 2^(m_i - M), M the largest
-// reference of a piece that saw a key: out = sum w_i O_i / sum w_i l_i.
+// Joins the pieces of the cut tiles.  With weights w_i = 2^(m_i - M), M the
+// largest reference of a piece that saw a key:
+//   out = sum w_i O_i / sum w_i l_i.
+// CTA c's share ends inside at most one tile, whose pieces are c's second
+// partial and the first partials of c + 1 .. last.  Most tiles have two or
+// three pieces: block (c, y) joins rows 8y .. 8y + 7 of that tile, a warp a
+// row.  A long sequence alone is one tile of a piece a CTA: there the blocks
+// of all its CTAs take (row, 128 dims) units and a block's warps share the
+// pieces (64 rows of 152 pieces: 84 us a warp a row, see below for the rest).
+constexpr int kLtMergeThreads = 256;
+constexpr int kLtFewPieces = 6;
+
 template <int N>
-__global__ void __launch_bounds__(128) pkv_latent_merge_kernel(const LatentParams p) {
+__global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const LatentParams p) {
+  constexpr int kWarps = kLtMergeThreads / 32;
+  __shared__ int s_head;
+  __shared__ float s_sum[kWarps];
+  __shared__ float4 s_acc[kWarps][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int c = blockIdx.x, r = blockIdx.y;
-  const int4 join = __ldcg(p.joins + c);
-  if (r >= join.y) return;
-  const int pieces = join.z - c + 1;
-  auto part = [&](int i) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto part = [&](int c, int i) {
     return p.partials + (i == 0 ? size_t(c) * 2 + 1 : size_t(c + i) * 2) * kLtPartialFloats;
   };
-  float M = -INFINITY;
-  for (int i = 0; i < pieces; ++i) {
-    const float* head = part(i) + N * kLatentDim;
-    if (__ldcg(head + N + r) != 0.f) M = fmaxf(M, __ldcg(head + r));
+  auto add = [](float4& a, float w, const float4& o) {
+    a.x += w * o.x;
+    a.y += w * o.y;
+    a.z += w * o.z;
+    a.w += w * o.w;
+  };
+  // out row of a tile: four dims a lane at float4 index i
+  auto put = [&](int row, int i, const float4& a, float inv) {
+    *(reinterpret_cast<uint2*>(p.out + size_t(row) * kLatentDim) + i) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  };
+  if (tid == 0) s_head = -1;
+  __syncthreads();
+  // the tile of many pieces that this CTA holds one of from an earlier CTA's
+  // share, if any (at most one: its share begins in it)
+  for (int c = tid; c < int(blockIdx.x); c += kLtMergeThreads) {
+    const int4 j = __ldcg(p.joins + c);
+    if (j.y > 0 && j.z >= int(blockIdx.x) && j.z - c + 1 > kLtFewPieces) s_head = c;
   }
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
+  __syncthreads();
+  const int4 own = __ldcg(p.joins + blockIdx.x);  // the tile that its share ends inside
+  const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
+  if (!own_many) {
+    const int c = blockIdx.x;
+    const int4 join = own;
+    const int r = blockIdx.y * kWarps + warp;
+    const int pieces = join.z - c + 1;
+    if (r < join.y) {
+      float m[kLtFewPieces], l[kLtFewPieces];
+      float M = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kLtFewPieces; ++i) {
+        const float* head = part(c, min(i, pieces - 1)) + N * kLatentDim;
+        m[i] = __ldcg(head + r);
+        l[i] = i < pieces ? __ldcg(head + N + r) : 0.f;
+        if (l[i] != 0.f) M = fmaxf(M, m[i]);
+      }
+      float4 acc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kLtFewPieces; ++i) {
+        if (l[i] == 0.f) continue;  // no piece, or one that saw no key: its O is not read
+        const float w = ex2(m[i] - M);
+        const float4* o = reinterpret_cast<const float4*>(part(c, i) + size_t(r) * kLatentDim);
+        sum += w * l[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) add(acc[e], w, __ldcg(o + e * 32 + lane));
+      }
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) put(join.x + r, e * 32 + lane, acc[e], inv);
+    }
+  }
+  for (int which = 0; which < 2; ++which) {
+    const int c0 = which == 0 ? s_head : own_many ? int(blockIdx.x) : -1;
+    if (c0 < 0) continue;
+    const int4 join = __ldcg(p.joins + c0);
+    const int pieces = join.z - c0 + 1;
+    const int team = pieces * gridDim.y;
+    for (int u = (blockIdx.x - c0) * gridDim.y + blockIdx.y; u < join.y * 4; u += team) {
+      const int r = u >> 2, i4 = (u & 3) * 32 + lane;
+      float M = -INFINITY;
+      for (int i = lane; i < pieces; i += 32) {
+        const float* head = part(c0, i) + N * kLatentDim;
+        if (__ldcg(head + N + r) != 0.f) M = fmaxf(M, __ldcg(head + r));
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
 #pragma unroll 4
-  for (int i = 0; i < pieces; ++i) {
-    const float* head = part(i) + N * kLatentDim;
-    const float l = __ldcg(head + N + r);
-    if (l == 0.f) continue;  // saw no key: its O is not read
-    const float w = ex2(__ldcg(head + r) - M);
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(part(i) + size_t(r) * kLatentDim) + threadIdx.x);
-    sum += w * l;
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
+      for (int i = warp; i < pieces; i += kWarps) {
+        const float* head = part(c0, i) + N * kLatentDim;
+        const float l = __ldcg(head + N + r), m = __ldcg(head + r);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(part(c0, i) + size_t(r) * kLatentDim) + i4);
+        if (l == 0.f) continue;  // saw no key: its O was not written
+        const float w = ex2(m - M);
+        sum += w * l;
+        add(acc, w, o);
+      }
+      s_acc[warp][lane] = acc;
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = s_sum[0];
+        for (int w = 1; w < kWarps; ++w) {
+          sum += s_sum[w];
+          add(acc, 1.f, s_acc[w][lane]);
+        }
+        put(join.x + r, i4, acc, 1.f / sum);
+      }
+      __syncthreads();
+    }
   }
-  const float inv = 1.f / sum;
-  const uint2 v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  *(reinterpret_cast<uint2*>(p.out + size_t(join.x + r) * kLatentDim) + threadIdx.x) = v;
 }
 
 template <int N>
@@ -797,8 +916,8 @@ int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams 
     cudaLaunchKernelEx(&cfg, pkv_latent_kernel<N>, tq, tkv, lp);
     if (int e = ts.done()) return e;
   }
-  cfg.gridDim = dim3(ctx.dev->sm_count, N);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(ctx.dev->sm_count, N / (kLtMergeThreads / 32));
+  cfg.blockDim = dim3(kLtMergeThreads);
   cfg.dynamicSmemBytes = 0;
   TraceScope ts(ctx.stream, PKV_K_MERGE);
   cudaLaunchKernelEx(&cfg, pkv_latent_merge_kernel<N>, lp);
