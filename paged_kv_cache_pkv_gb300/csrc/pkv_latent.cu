@@ -65,6 +65,10 @@ constexpr uint32_t kLtGroupBytes = kLtChunks * 1024;         // 8 rows
 constexpr uint32_t kLtPageBytes = 2 * kLtGroupBytes;         // 18 KiB
 constexpr uint32_t kLtTileBytes = kLtPages * kLtPageBytes;   // 72 KiB
 constexpr int kLtStages = 2;
+// P of a tile overwrites the tile's rotated chunk, which only the scores read:
+// 64 keys of 128 bytes, at the same strides, so P needs no memory of its own
+// and never waits for the P V before it.
+constexpr uint32_t kLtChunkP = (kLtChunks - 1) * 1024;
 constexpr float kLtTau = 20.0f;  // log2 of how far a score may exceed the reference
 
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -72,12 +76,11 @@ template <int N>
 struct LtSmem {
   static constexpr uint32_t kv = 0;
   static constexpr uint32_t q = kv + kLtStages * kLtTileBytes;  // [9][N rows][128 B]
-  static constexpr uint32_t p = q + kLtChunks * N * 128;        // [64 keys][128 B]
-  static constexpr uint32_t misc = p + kLtKeys * 128;
+  static constexpr uint32_t misc = q + kLtChunks * N * 128;
   // misc: barriers, TMEM address, share bounds, per-row reductions
-  static constexpr uint32_t bars = misc;           // 16 x 8
-  static constexpr uint32_t tmem = misc + 128;
-  static constexpr uint32_t share = misc + 144;    // 2 bounds x 4 ints, then G_eff and the join's last CTA
+  static constexpr uint32_t bars = misc;           // 17 x 8
+  static constexpr uint32_t tmem = misc + 144;
+  static constexpr uint32_t share = misc + 160;    // 2 bounds x 4 ints, then G_eff and the join's last CTA
   static constexpr uint32_t wsum = misc + 192;     // [10] x 8, plan scan
   static constexpr uint32_t red = misc + 272;      // [4 quadrants][N] floats
   static constexpr uint32_t alpha = red + 16 * N;  // [N] floats
@@ -97,7 +100,8 @@ struct LatentParams {
   float qscale;        // scale * log2(e)
 };
 
-// A partial: O [N][512], then m [N], l [N].
+// A partial: O in the order in which the softmax warps hold it, [4 blocks of
+// 128 dims][4 warps][N/4 groups of rows][32 dims][4 rows], then m [N], l [N].
 constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
 
 // Weights of the work split, in units of (keys x heads): tile j of a sequence
@@ -296,17 +300,17 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   uint64_t* bar_q = bars;            // a tile's queries landed
   uint64_t* bar_qfree = bars + 1;    // its score MMAs are done
   uint64_t* bar_kv = bars + 2;       // [2] cache tile landed
-  uint64_t* bar_kvfree = bars + 4;   // [2] the MMAs that read it are done
-  uint64_t* bar_s = bars + 6;        // [2] scores written
-  uint64_t* bar_p = bars + 8;        // P written (256 arrivals)
-  uint64_t* bar_o = bars + 9;        // P V done: P's buffer is free, O^T up to date
+  uint64_t* bar_kvfree = bars + 4;   // [2][4] the MMAs that read a page of it are done
+  uint64_t* bar_s = bars + 12;       // [2] scores written
+  uint64_t* bar_p = bars + 14;       // P written (256 arrivals)
+  uint64_t* bar_o = bars + 15;       // [2] P V done: O^T up to date
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
   int64_t* s_wsum = reinterpret_cast<int64_t*>(sm + S::wsum);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(bars + i, bars + i == bar_p ? kLtSoftmaxThreads : 1);
+    for (int i = 0; i < 17; ++i) mbar_init(bars + i, bars + i == bar_p ? kLtSoftmaxThreads : 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -403,6 +407,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     LtPos at = begin;
     LtPiece x;
     int g = 0, pieces = 0;  // cache tiles and tiles of rows so far
+    int landing = 0;        // cache tiles whose copies were issued
     bool ok = true;
     while (ok && lt_next<N>(p, at, end, x)) {
       if (lane == 0) {
@@ -445,15 +450,24 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         const int st = g % kLtStages;
         if (lane == 0) {
-          if (g >= kLtStages) ok = mbar_wait(bar_kvfree + st, (g / kLtStages - 1) & 1);
-          if (ok) {
-            mbar_arrive_expect_tx(bar_kv + st, uint32_t(valid) * kLtPageBytes);
+          // page by page, as P V of the tile two before lets go of them
+          int sent = 0;
 #pragma unroll
-            for (int i = 0; i < kLtPages; ++i)
-              if (id[i] >= 0)
-                tma_load_4d(sm + S::kv + st * kLtTileBytes + i * kLtPageBytes, &tm_kv, 0, 0, 0, 2 * id[i],
-                            bar_kv + st);
+          for (int i = 0; i < kLtPages; ++i) {
+            if (g >= kLtStages && ok) ok = mbar_wait(bar_kvfree + st * kLtPages + i, (g / kLtStages - 1) & 1);
+            if (!ok) break;
+            if (i == 0) mbar_arrive_expect_tx(bar_kv + st, uint32_t(valid) * kLtPageBytes);
+            if (id[i] >= 0) {
+              tma_load_4d(sm + S::kv + st * kLtTileBytes + i * kLtPageBytes, &tm_kv, 0, 0, 0, 2 * id[i], bar_kv + st);
+              ++sent;
+            }
           }
+          // a tile given up half way: let its phase end with what was sent
+          if (!ok && sent > 0)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar_kv + st)),
+                         "r"(uint32_t(valid - sent) * kLtPageBytes)
+                         : "memory");
+          if (sent > 0) landing = g + 1;
         }
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         if (!ok) break;
@@ -462,7 +476,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (lane == 0) {
       // copies land before the CTA's shared memory is released
       const uint64_t limit = ok ? kLandLimitNs : kDrainLimitNs;
-      for (int i = g > kLtStages ? g - kLtStages : 0; i < g; ++i)
+      for (int i = landing > kLtStages ? landing - kLtStages : 0; i < landing; ++i)
         mbar_wait(bar_kv + i % kLtStages, (i / kLtStages) & 1, limit);
       if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);
       if (!ok) flag_status(p.status, PKV_STATUS_TIMEOUT);
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // buffer that P V frees: 5000 cycles a tile against 2200.)
     constexpr uint32_t idesc_s = lt_idesc(64, N, false, false);
     constexpr uint32_t idesc_o = lt_idesc(128, N, true, true);
-    const uint32_t aq = smem_u32(sm + S::q), ap = smem_u32(sm + S::p);
+    const uint32_t aq = smem_u32(sm + S::q);
     auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
     LtPos at = begin;
     LtPiece x;
@@ -507,13 +521,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           const uint32_t more = npv > last - (x.k1 - x.k0) ? 1u : 0u;  // not the piece's first tile
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < kLtPages; ++ks)
+          for (int ks = 0; ks < kLtPages; ++ks) {
 #pragma unroll
             for (int d = 0; d < 4; ++d)
               umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
-                   smem_desc(ap + ks * 2048, 1024, 1024), idesc_o, ks > 0 ? 1u : more);
-          umma_commit(bar_kvfree + npv % kLtStages);
-          umma_commit(bar_o);
+                   smem_desc(kv + ks * kLtPageBytes + kLtChunkP, 1024, kLtGroupBytes), idesc_o, ks > 0 ? 1u : more);
+            umma_commit(bar_kvfree + (npv % kLtStages) * kLtPages + ks);
+          }
+          umma_commit(bar_o + (npv & 1));
           ++npv;
           idle = 0;
         } else if (idle++ == 0) {
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (!ok && lane == 0) flag_status(p.status, PKV_STATUS_TIMEOUT);
     // what was issued lands before TMEM is released
     if (ns > 0) mbar_wait(bar_s + ((ns - 1) & 1), ((ns - 1) >> 1) & 1, kLandLimitNs);
-    if (npv > 0) mbar_wait(bar_o, (npv - 1) & 1, kLandLimitNs);
+    if (npv > 0) mbar_wait(bar_o + ((npv - 1) & 1), ((npv - 1) >> 1) & 1, kLandLimitNs);
     __syncwarp();
   } else {
     // ===== softmax and results: warpgroup w has rows [w * NW, (w + 1) * NW) =====
@@ -547,6 +562,14 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+    };
+    // P V of the first `tiles` tiles.  A wait names a phase by its parity, so
+    // it has to come before the barrier can be a whole phase further: even and
+    // odd tiles have a barrier each, and every tile waits, before its P is
+    // given away, for the P V two tiles before.
+    int o_seen = 0;
+    auto wait_o = [&](int tiles) {
+      for (; o_seen < tiles; ++o_seen) wait(bar_o + (o_seen & 1), (o_seen >> 1) & 1);
     };
     while (lt_next<N>(p, at, end, x)) {
       float m[NC], l[NC];
@@ -613,7 +636,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           if (k > x.k0) {
             // O^T of the earlier tiles under the new references
             named_sync(bar_id, 128);
-            wait(bar_o, (g - 1) & 1);
+            wait_o(g);
             tc_fence_after();
 #pragma unroll 1
             for (int d = 0; d < 4; ++d)
@@ -637,10 +660,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           l[c] += bf_lo(pk[c / 2]);
           l[c + 1] += bf_hi(pk[c / 2]);
         }
-        // P's buffer is free once the product before is done
-        if (g > 0) wait(bar_o, (g - 1) & 1);
+        wait_o(g - 1);  // done long since: the tile two before shares this one's buffer
         if (!ok) continue;
-        uint8_t* prow = sm + S::p + key * 128;
+        uint8_t* kv = sm + S::kv + (g % kLtStages) * kLtTileBytes;
+        uint8_t* prow = kv + (key >> 3) * kLtGroupBytes + kLtChunkP + (key & 7) * 128;
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
           const uint32_t byte = uint32_t(col0 + c) * 2;
@@ -652,7 +675,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           // rows past the sequence hold whatever the pages or the buffer
           // held: zero their values, since 0 x NaN is NaN (their scores are
           // masked).  The scores' MMAs are done, this tile's P V not issued.
-          uint8_t* kv = sm + S::kv + (g % kLtStages) * kLtTileBytes;
           for (int i = tid; i < (kLtKeys - valid) * 64; i += kLtSoftmaxThreads) {
             const int r = valid + (i >> 6), ch = (i >> 3) & 7, v = i & 7;
             *reinterpret_cast<uint4*>(kv + (r >> 3) * kLtGroupBytes + ch * 1024 + (r & 7) * 128 + v * 16) =
@@ -690,7 +712,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           part[N * kLatentDim + N + r] = sum;
       }
       named_sync(bar_id, 128);
-      wait(bar_o, (g - 1) & 1);
+      wait_o(g);
       if (ok) {
         tc_fence_after();
         const int r0 = wg * NW;  // this warpgroup's rows of the tile
@@ -713,10 +735,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                 to[c * (kLatentDim / 2)] = (lane & 1) ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
             }
           } else {
-            float* to = part + size_t(r0) * kLatentDim + dim + lane;
+            float4* to = reinterpret_cast<float4*>(part) + ((d * 4 + quad) * (N / 4) + r0 / 4) * 32 + lane;
 #pragma unroll
-            for (int c = 0; c < NW; ++c)
-              if (r0 + c < x.rows) to[c * kLatentDim] = o[c];
+            for (int c = 0; c < NW; c += 4)
+              if (r0 + c < x.rows) to[c * 8] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
           }
         }
         tc_fence_before();  // read before the next piece's first P V overwrites it
@@ -752,19 +774,40 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 // largest reference of a piece that saw a key:
 //   out = sum w_i O_i / sum w_i l_i.
 // CTA c's share ends inside at most one tile, whose pieces are c's second
-// partial and the first partials of c + 1 .. last.  Most tiles have two or
-// three pieces: block (c, y) joins rows 8y .. 8y + 7 of that tile, a warp a
-// row.  A long sequence alone is one tile of a piece a CTA: there the blocks
-// of all its CTAs take (row, 128 dims) units and a block's warps share the
-// pieces (64 rows of 152 pieces: 84 us a warp a row, see below for the rest).
+// partial and the first partials of c + 1 .. last.  A warp joins four rows
+// (a float4 a lane of the partials' layout).  Most tiles have two or three
+// pieces: there warp i of the N warps of blocks (c, *) takes rows 4 (i / 4) ..
+// + 3 of the 128 dims i % 4.  A long sequence alone is one tile with a piece
+// a CTA: there the blocks of all its CTAs take units of four rows and 32 dims,
+// and a block's warps share the pieces.  (64 rows of 152 pieces, 20 MB: 84 us
+// with a block a row in the first way, 15 us in the second.)
 constexpr int kLtMergeThreads = 256;
 constexpr int kLtFewPieces = 6;
+
+__device__ __forceinline__ float4 f4_weights(const float4& m, const float4& M, const float4& l) {
+  // a piece that saw no key of a row has weight 0 there
+  return make_float4(l.x == 0.f ? 0.f : ex2(m.x - M.x), l.y == 0.f ? 0.f : ex2(m.y - M.y),
+                     l.z == 0.f ? 0.f : ex2(m.z - M.z), l.w == 0.f ? 0.f : ex2(m.w - M.w));
+}
+__device__ __forceinline__ void f4_max_seen(float4& M, const float4& m, const float4& l) {
+  if (l.x != 0.f) M.x = fmaxf(M.x, m.x);
+  if (l.y != 0.f) M.y = fmaxf(M.y, m.y);
+  if (l.z != 0.f) M.z = fmaxf(M.z, m.z);
+  if (l.w != 0.f) M.w = fmaxf(M.w, m.w);
+}
+// a += w * o where w is not 0 (an O that saw no key may not have been written)
+__device__ __forceinline__ void f4_add(float4& a, const float4& w, const float4& o) {
+  if (w.x != 0.f) a.x += w.x * o.x;
+  if (w.y != 0.f) a.y += w.y * o.y;
+  if (w.z != 0.f) a.z += w.z * o.z;
+  if (w.w != 0.f) a.w += w.w * o.w;
+}
 
 template <int N>
 __global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const LatentParams p) {
   constexpr int kWarps = kLtMergeThreads / 32;
   __shared__ int s_head;
-  __shared__ float s_sum[kWarps];
+  __shared__ float4 s_sum[kWarps];
   __shared__ float4 s_acc[kWarps][32];
   griddep_wait();
   griddep_launch_dependents();
@@ -772,17 +815,29 @@ __global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const
   auto part = [&](int c, int i) {
     return p.partials + (i == 0 ? size_t(c) * 2 + 1 : size_t(c + i) * 2) * kLtPartialFloats;
   };
-  auto add = [](float4& a, float w, const float4& o) {
-    a.x += w * o.x;
-    a.y += w * o.y;
-    a.z += w * o.z;
-    a.w += w * o.w;
+  auto m_of = [&](int c, int i, int rq) {
+    return __ldcg(reinterpret_cast<const float4*>(part(c, i) + N * kLatentDim) + rq);
   };
-  // out row of a tile: four dims a lane at float4 index i
-  auto put = [&](int row, int i, const float4& a, float inv) {
-    *(reinterpret_cast<uint2*>(p.out + size_t(row) * kLatentDim) + i) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  auto l_of = [&](int c, int i, int rq) {
+    return __ldcg(reinterpret_cast<const float4*>(part(c, i) + N * kLatentDim + N) + rq);
   };
+  auto o_of = [&](int c, int i, int rq, int dq) {  // 32 dims dq, rows 4 rq .. + 3
+    return __ldcg(reinterpret_cast<const float4*>(part(c, i)) + (dq * (N / 4) + rq) * 32 + lane);
+  };
+  // rows 4 rq .. + 3 of a tile, dim 32 dq + lane of each; even lanes store a
+  // pair of dims of the first of two rows, odd lanes of the second
+  auto put = [&](const int4& join, int rq, int dq, const float4& a, const float4& sum) {
+    const float v[4] = {a.x / sum.x, a.y / sum.y, a.z / sum.z, a.w / sum.w};
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[e] : v[e + 1], 1);
+      const int r = rq * 4 + e + (lane & 1);
+      if (r < join.y)
+        *(reinterpret_cast<uint32_t*>(p.out + size_t(join.x + r) * kLatentDim + dq * 32) + (lane >> 1)) =
+            (lane & 1) ? pack_bf16x2(other, v[e + 1]) : pack_bf16x2(v[e], other);
+    }
+  };
+  constexpr float kNone = -INFINITY;
   if (tid == 0) s_head = -1;
   __syncthreads();
   // the tile of many pieces that this CTA holds one of from an earlier CTA's
@@ -795,75 +850,61 @@ __global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const
   const int4 own = __ldcg(p.joins + blockIdx.x);  // the tile that its share ends inside
   const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
   if (!own_many) {
-    const int c = blockIdx.x;
-    const int4 join = own;
-    const int r = blockIdx.y * kWarps + warp;
-    const int pieces = join.z - c + 1;
-    if (r < join.y) {
-      float m[kLtFewPieces], l[kLtFewPieces];
-      float M = -INFINITY;
+    const int c = blockIdx.x, i = blockIdx.y * kWarps + warp;
+    const int rq = i / 4, pieces = own.z - c + 1;
+    if (rq * 4 < own.y) {
+      float4 M = make_float4(kNone, kNone, kNone, kNone);
+      for (int k = 0; k < pieces; ++k) f4_max_seen(M, m_of(c, k, rq), l_of(c, k, rq));
+      float4 acc[4], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kLtFewPieces; ++i) {
-        const float* head = part(c, min(i, pieces - 1)) + N * kLatentDim;
-        m[i] = __ldcg(head + r);
-        l[i] = i < pieces ? __ldcg(head + N + r) : 0.f;
-        if (l[i] != 0.f) M = fmaxf(M, m[i]);
+      for (int e = 0; e < 4; ++e) acc[e] = sum;
+#pragma unroll 2
+      for (int k = 0; k < pieces; ++k) {
+        const float4 l = l_of(c, k, rq);
+        const float4 w = f4_weights(m_of(c, k, rq), M, l);
+        f4_add(sum, w, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f4_add(acc[e], w, o_of(c, k, rq, (i & 3) * 4 + e));
       }
-      float4 acc[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < kLtFewPieces; ++i) {
-        if (l[i] == 0.f) continue;  // no piece, or one that saw no key: its O is not read
-        const float w = ex2(m[i] - M);
-        const float4* o = reinterpret_cast<const float4*>(part(c, i) + size_t(r) * kLatentDim);
-        sum += w * l[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) add(acc[e], w, __ldcg(o + e * 32 + lane));
-      }
-      const float inv = 1.f / sum;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) put(join.x + r, e * 32 + lane, acc[e], inv);
+      for (int e = 0; e < 4; ++e) put(own, rq, (i & 3) * 4 + e, acc[e], sum);
     }
   }
   for (int which = 0; which < 2; ++which) {
-    const int c0 = which == 0 ? s_head : own_many ? int(blockIdx.x) : -1;
-    if (c0 < 0) continue;
-    const int4 join = __ldcg(p.joins + c0);
-    const int pieces = join.z - c0 + 1;
+    const int c = which == 0 ? s_head : own_many ? int(blockIdx.x) : -1;
+    if (c < 0) continue;
+    const int4 join = __ldcg(p.joins + c);
+    const int pieces = join.z - c + 1;
     const int team = pieces * gridDim.y;
-    for (int u = (blockIdx.x - c0) * gridDim.y + blockIdx.y; u < join.y * 4; u += team) {
-      const int r = u >> 2, i4 = (u & 3) * 32 + lane;
-      float M = -INFINITY;
-      for (int i = lane; i < pieces; i += 32) {
-        const float* head = part(c0, i) + N * kLatentDim;
-        if (__ldcg(head + N + r) != 0.f) M = fmaxf(M, __ldcg(head + r));
-      }
+    for (int u = (blockIdx.x - c) * gridDim.y + blockIdx.y; u < (join.y + 3) / 4 * 16; u += team) {
+      const int rq = u >> 4, dq = u & 15;
+      float4 M = make_float4(kNone, kNone, kNone, kNone);
+      for (int k = lane; k < pieces; k += 32) f4_max_seen(M, m_of(c, k, rq), l_of(c, k, rq));
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
+      for (int o = 16; o >= 1; o >>= 1) {
+        M.x = fmaxf(M.x, __shfl_xor_sync(0xffffffffu, M.x, o));
+        M.y = fmaxf(M.y, __shfl_xor_sync(0xffffffffu, M.y, o));
+        M.z = fmaxf(M.z, __shfl_xor_sync(0xffffffffu, M.z, o));
+        M.w = fmaxf(M.w, __shfl_xor_sync(0xffffffffu, M.w, o));
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = acc;
 #pragma unroll 4
-      for (int i = warp; i < pieces; i += kWarps) {
-        const float* head = part(c0, i) + N * kLatentDim;
-        const float l = __ldcg(head + N + r), m = __ldcg(head + r);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(part(c0, i) + size_t(r) * kLatentDim) + i4);
-        if (l == 0.f) continue;  // saw no key: its O was not written
-        const float w = ex2(m - M);
-        sum += w * l;
-        add(acc, w, o);
+      for (int k = warp; k < pieces; k += kWarps) {
+        const float4 l = l_of(c, k, rq), m = m_of(c, k, rq), o = o_of(c, k, rq, dq);
+        const float4 w = f4_weights(m, M, l);
+        f4_add(sum, w, l);
+        f4_add(acc, w, o);
       }
       s_acc[warp][lane] = acc;
       if (lane == 0) s_sum[warp] = sum;
       __syncthreads();
       if (warp == 0) {
-        sum = s_sum[0];
+        const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
         for (int w = 1; w < kWarps; ++w) {
-          sum += s_sum[w];
-          add(acc, 1.f, s_acc[w][lane]);
+          f4_add(acc, one, s_acc[w][lane]);
+          f4_add(sum, one, s_sum[w]);
         }
-        put(join.x + r, i4, acc, 1.f / sum);
+        put(join, rq, dq, acc, sum);
       }
       __syncthreads();
     }
