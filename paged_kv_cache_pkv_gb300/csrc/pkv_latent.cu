@@ -78,7 +78,7 @@ struct LtSmem {
   static constexpr uint32_t q = kv + kLtStages * kLtTileBytes;  // [9][N rows][128 B]
   static constexpr uint32_t misc = q + kLtChunks * N * 128;
   // misc: barriers, TMEM address, share bounds, per-row reductions
-  static constexpr uint32_t bars = misc;           // 17 x 8
+  static constexpr uint32_t bars = misc;           // 18 x 8
   static constexpr uint32_t tmem = misc + 144;
   static constexpr uint32_t share = misc + 160;    // 2 bounds x 4 ints, then G_eff and the join's last CTA
   static constexpr uint32_t wsum = misc + 192;     // [10] x 8, plan scan
@@ -302,15 +302,15 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   uint64_t* bar_kv = bars + 2;       // [2] cache tile landed
   uint64_t* bar_kvfree = bars + 4;   // [2][4] the MMAs that read a page of it are done
   uint64_t* bar_s = bars + 12;       // [2] scores written
-  uint64_t* bar_p = bars + 14;       // P written (256 arrivals)
-  uint64_t* bar_o = bars + 15;       // [2] P V done: O^T up to date
+  uint64_t* bar_p = bars + 14;       // [2] P written (256 arrivals)
+  uint64_t* bar_o = bars + 16;       // [2] P V done: O^T up to date
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
   int64_t* s_wsum = reinterpret_cast<int64_t*>(sm + S::wsum);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    for (int i = 0; i < 17; ++i) mbar_init(bars + i, bars + i == bar_p ? kLtSoftmaxThreads : 1);
+    for (int i = 0; i < 18; ++i) mbar_init(bars + i, bars + i == bar_p || bars + i == bar_p + 1 ? kLtSoftmaxThreads : 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           umma_commit(bar_s + (ns & 1));
           if (++ns == last) umma_commit(bar_qfree);
           idle = 0;
-        } else if (npv < ns && ready(bar_p, npv & 1)) {
+        } else if (npv < ns && ready(bar_p + (npv & 1), (npv >> 1) & 1)) {
           const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(npv % kLtStages) * kLtTileBytes;
           const uint32_t more = npv > last - (x.k1 - x.k0) ? 1u : 0u;  // not the piece's first tile
           tc_fence_after();
@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     };
     // P V of the first `tiles` tiles.  A wait names a phase by its parity, so
     // it has to come before the barrier can be a whole phase further: even and
-    // odd tiles have a barrier each, and every tile waits, before its P is
-    // given away, for the P V two tiles before.
+    // odd tiles have a barrier each (here, for P and for the scores), and every
+    // tile waits, before its P is given away, for the P V two tiles before.
     int o_seen = 0;
     auto wait_o = [&](int tiles) {
       for (; o_seen < tiles; ++o_seen) wait(bar_o + (o_seen & 1), (o_seen >> 1) & 1);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar_p);
+        mbar_arrive(bar_p + (g & 1));
       }
 
       // ---- the piece's result ----
