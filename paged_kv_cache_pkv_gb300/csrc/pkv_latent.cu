@@ -60,11 +60,12 @@ constexpr int kLtKeys = 64;                        // keys a cache tile
 constexpr int kLtPages = kLtKeys / kPage;          // 4
 constexpr int kLtChunks = kLatentRow / 64;         // 9 chunks of 64 dims (the last is rotated, keys only)
 constexpr int kLtSoftmaxThreads = 256;
-constexpr int kLtThreads = kLtSoftmaxThreads + 64;  // + loader and MMA warps
+constexpr int kLtThreads = kLtSoftmaxThreads + 96;  // + loader, score and value warps
 constexpr uint32_t kLtGroupBytes = kLtChunks * 1024;         // 8 rows
 constexpr uint32_t kLtPageBytes = 2 * kLtGroupBytes;         // 18 KiB
 constexpr uint32_t kLtTileBytes = kLtPages * kLtPageBytes;   // 72 KiB
 constexpr int kLtStages = 2;
+constexpr int kAhead = 1;
 // P of a tile overwrites the tile's rotated chunk, which only the scores read:
 // 64 keys of 128 bytes, at the same strides, so P needs no memory of its own
 // and never waits for the P V before it.
@@ -93,6 +94,7 @@ static_assert((PKV_MAX_SEQS + 1) * 8 <= kLtTileBytes, "the plan's scan borrows t
 struct LatentParams {
   const int32_t *block_tables, *seq_lens, *qsl;
   uint16_t* out;
+  const uint16_t* cache;
   float* partials;     // [CTAs][2][partial_stride]
   int4* joins;         // [CTAs] (first row, rows, last CTA, -): the tile that CTA's share ends inside
   unsigned* status;
@@ -259,19 +261,6 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[X]) {
   for (int i = 0; i < X; i += 8) tmem_ld8(taddr + i, r + i);
 }
 
-// One non-blocking test of a barrier's phase.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                             uint64_t* bar) {
   asm volatile(
@@ -402,6 +391,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const LtPos end{s_share[4], s_share[5], s_share[6]};
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
+  // every lane waits; the warp goes on only if all of them saw the phase
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  };
+
   if (warp == 8) {
     // ===== loader: queries and cache tiles, in the order they are used =====
     LtPos at = begin;
@@ -449,6 +443,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           valid += id[i] >= 0;
         }
         const int st = g % kLtStages;
+        {
+          const int src = in_group + kAhead < 8 ? ids : next;
+          const int pid = __shfl_sync(0xffffffffu, src, ((in_group + kAhead) & 7) * kLtPages + (lane & 3));
+          if (lane < 4 && pid >= 0) prefetch_l2(p.cache + size_t(pid) * (kPage * kLatentRow), kLtPageBytes);
+        }
         if (lane == 0) {
           // page by page, as P V of the tile two before lets go of them
           int sent = 0;
@@ -483,66 +482,66 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ===== MMA issuer =====
-    // Within a piece, whichever product can go next goes: the scores of the
-    // next tile once it has landed and the softmax is done with their buffer,
-    // or P V of the oldest tile whose P is written; scores first where both
-    // can, so that the softmax of one tile runs under P V of the other.  (In
-    // a fixed order, P V waited for the next tile's copies, and those for the
-    // buffer that P V frees: 5000 cycles a tile against 2200.)
-    constexpr uint32_t idesc_s = lt_idesc(64, N, false, false);
-    constexpr uint32_t idesc_o = lt_idesc(128, N, true, true);
+    // ===== scores: S^T of tile after tile, each once it has landed and the
+    // softmax has taken the scores two tiles before from its buffer =====
+    constexpr uint32_t idesc = lt_idesc(64, N, false, false);
     const uint32_t aq = smem_u32(sm + S::q);
-    auto ready = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
     LtPos at = begin;
     LtPiece x;
-    int ns = 0, npv = 0, pieces = 0;  // scores and P V of tiles issued so far
+    int g = 0, pieces = 0;
     bool ok = true;
     while (ok && lt_next<N>(p, at, end, x)) {
-      const int last = npv + x.k1 - x.k0;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_q, pieces & 1));
-      uint64_t since = 0;  // of the first test in a row that found nothing to do
-      int idle = 0;
-      while (ok && npv < last) {
-        if (ns < last && ns <= npv + 1 && ready(bar_kv + ns % kLtStages, (ns / kLtStages) & 1)) {
-          const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(ns % kLtStages) * kLtTileBytes;
-          tc_fence_after();
+      ok = wait_all(bar_q, pieces & 1);
+      for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+        if (g >= 2) ok = wait_all(bar_p + (g & 1), ((g >> 1) - 1) & 1);
+        if (ok) ok = wait_all(bar_kv + g % kLtStages, (g / kLtStages) & 1);
+        if (!ok) break;
+        const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(g % kLtStages) * kLtTileBytes;
+        tc_fence_after();
 #pragma unroll 3
-          for (int c = 0; c < kLtChunks; ++c)
+        for (int c = 0; c < kLtChunks; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma(tmem_s(ns), smem_desc(kv + c * 1024 + kk * 32, 16, kLtGroupBytes),
-                   smem_desc(aq + c * (N * 128) + kk * 32, 16, 1024), idesc_s, c + kk > 0);
-          umma_commit(bar_s + (ns & 1));
-          if (++ns == last) umma_commit(bar_qfree);
-          idle = 0;
-        } else if (npv < ns && ready(bar_p + (npv & 1), (npv >> 1) & 1)) {
-          const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(npv % kLtStages) * kLtTileBytes;
-          const uint32_t more = npv > last - (x.k1 - x.k0) ? 1u : 0u;  // not the piece's first tile
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < kLtPages; ++ks) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-              umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
-                   smem_desc(kv + ks * kLtPageBytes + kLtChunkP, 1024, kLtGroupBytes), idesc_o, ks > 0 ? 1u : more);
-            umma_commit(bar_kvfree + (npv % kLtStages) * kLtPages + ks);
-          }
-          umma_commit(bar_o + (npv & 1));
-          ++npv;
-          idle = 0;
-        } else if (idle++ == 0) {
-          since = global_ns();
-        } else if ((idle & 63) == 0) {
-          ok = __all_sync(0xffffffffu, global_ns() - since <= kWaitLimitNs);
-        }
+          for (int kk = 0; kk < 4; ++kk)
+            umma(tmem_s(g), smem_desc(kv + c * 1024 + kk * 32, 16, kLtGroupBytes),
+                 smem_desc(aq + c * (N * 128) + kk * 32, 16, 1024), idesc, c + kk > 0);
+        umma_commit(bar_s + (g & 1));
+        if (k + 1 == x.k1) umma_commit(bar_qfree);
       }
       ++pieces;
     }
     if (!ok && lane == 0) flag_status(p.status, PKV_STATUS_TIMEOUT);
     // what was issued lands before TMEM is released
-    if (ns > 0) mbar_wait(bar_s + ((ns - 1) & 1), ((ns - 1) >> 1) & 1, kLandLimitNs);
-    if (npv > 0) mbar_wait(bar_o + ((npv - 1) & 1), ((npv - 1) >> 1) & 1, kLandLimitNs);
+    if (g > 0) mbar_wait(bar_s + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
+    __syncwarp();
+  } else if (warp == 10) {
+    // ===== values: O^T += V^T P^T of tile after tile, once its P is written.
+    // A warp of its own: behind the scores of the next tile, in one warp, P V
+    // waited for that tile's copies, and they for the buffer that P V frees
+    // (5000 cycles a tile against 3100). =====
+    constexpr uint32_t idesc = lt_idesc(128, N, true, true);
+    LtPos at = begin;
+    LtPiece x;
+    int g = 0;
+    bool ok = true;
+    while (ok && lt_next<N>(p, at, end, x)) {
+      for (int k = x.k0; k < x.k1; ++k, ++g) {
+        if (!(ok = wait_all(bar_p + (g & 1), (g >> 1) & 1))) break;
+        const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(g % kLtStages) * kLtTileBytes;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kLtPages; ++ks) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            umma(tmem + uint32_t(d) * N, smem_desc(kv + ks * kLtPageBytes + d * 2048, 1024, kLtGroupBytes),
+                 smem_desc(kv + ks * kLtPageBytes + kLtChunkP, 1024, kLtGroupBytes), idesc,
+                 (k > x.k0 || ks > 0) ? 1u : 0u);
+          umma_commit(bar_kvfree + (g % kLtStages) * kLtPages + ks);
+        }
+        umma_commit(bar_o + (g & 1));
+      }
+    }
+    if (!ok && lane == 0) flag_status(p.status, PKV_STATUS_TIMEOUT);
+    if (g > 0) mbar_wait(bar_o + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
     __syncwarp();
   } else {
     // ===== softmax and results: warpgroup w has rows [w * NW, (w + 1) * NW) =====
@@ -988,6 +987,7 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   lp.seq_lens = a.seq_lens;
   lp.qsl = a.query_start_loc;
   lp.out = a.out;
+  lp.cache = a.cache;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   lp.partials = reinterpret_cast<float*>(ws);
   lp.joins = reinterpret_cast<int4*>(
