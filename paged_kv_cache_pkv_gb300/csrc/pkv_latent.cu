@@ -79,9 +79,9 @@ struct LtSmem {
   static constexpr uint32_t q = kv + kLtStages * kLtTileBytes;  // [9][N rows][128 B]
   static constexpr uint32_t misc = q + kLtChunks * N * 128;
   // misc: barriers, TMEM address, share bounds, per-row reductions
-  static constexpr uint32_t bars = misc;           // 18 x 8
-  static constexpr uint32_t tmem = misc + 144;
-  static constexpr uint32_t share = misc + 160;    // 2 bounds x 4 ints, then G_eff and the join's last CTA
+  static constexpr uint32_t bars = misc;           // 16 x 8
+  static constexpr uint32_t tmem = misc + 128;
+  static constexpr uint32_t share = misc + 144;    // 2 bounds x 4 ints, the first sequence's 4 ints
   static constexpr uint32_t wsum = misc + 192;     // [10] x 8, plan scan
   static constexpr uint32_t red = misc + 272;      // [4 quadrants][N] floats
   static constexpr uint32_t alpha = red + 16 * N;  // [N] floats
@@ -89,7 +89,7 @@ struct LtSmem {
   static constexpr uint32_t bytes = end + 1024;    // + alignment slack
 };
 static_assert(LtSmem<64>::bytes <= 232448, "latent attention shared memory above the 227 KiB limit");
-static_assert((PKV_MAX_SEQS + 1) * 8 <= kLtTileBytes, "the plan's scan borrows the first cache tile");
+static_assert((PKV_MAX_SEQS + 2) * 8 + PKV_MAX_SEQS * 16 <= kLtTileBytes, "the plan borrows the first cache tile");
 
 struct LatentParams {
   const int32_t *block_tables, *seq_lens, *qsl;
@@ -121,18 +121,21 @@ struct LtSeq {
 };
 
 template <int N>
-__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b) {
+__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b, int q0, int q1, int L) {
   LtSeq s;
-  s.q0 = __ldg(p.qsl + b);
-  const int q1 = __ldg(p.qsl + b + 1);
-  s.L = __ldg(p.seq_lens + b);
-  s.n = q1 - s.q0;
-  s.bad = s.q0 < 0 || s.n < 0 || q1 > p.T || s.n > s.L || s.L < 0 ||
-          (s.L + kPage - 1) / kPage > p.max_blocks || (b == 0 && s.q0 != 0);
+  s.q0 = q0;
+  s.L = L;
+  s.n = q1 - q0;
+  s.bad = q0 < 0 || s.n < 0 || q1 > p.T || s.n > L || L < 0 || (L + kPage - 1) / kPage > p.max_blocks ||
+          (b == 0 && q0 != 0);
   if (s.bad) s.n = 0;
   s.rows = s.n * p.H;
   s.tiles = (s.rows + N - 1) / N;
   return s;
+}
+template <int N>
+__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b) {
+  return lt_seq<N>(p, b, __ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b));
 }
 
 // Weight of the first j tiles of a sequence.
@@ -159,36 +162,41 @@ struct LtPiece {
   int b, j, k0, k1, blocks;
   int row0, rows;   // of the tile: first row in q and out, rows
   int local_row;    // the first row's index within the sequence's rows
-  int q0, n, L;
+  int n, L;
 };
 
-// The next piece (never empty) at `at`, and `at` moved behind it; false at
-// the share's end.
+// A walk over a share's pieces.  The sequence it is in is kept: its numbers
+// are read once.
+struct LtWalk {
+  LtPos at, end;
+  LtSeq s;  // of sequence at.b
+};
+
+// The next piece (never empty); false at the share's end.
 template <int N>
-__device__ __forceinline__ bool lt_next(const LatentParams& p, LtPos& at, const LtPos& end, LtPiece& x) {
+__device__ __forceinline__ bool lt_next(const LatentParams& p, LtWalk& w, LtPiece& x) {
   for (;;) {
-    if (at.b >= p.B || at.b > end.b ||
-        (at.b == end.b && (at.j > end.j || (at.j == end.j && at.k >= end.k))))
+    const LtPos& e = w.end;
+    if (w.at.b >= p.B || w.at.b > e.b || (w.at.b == e.b && (w.at.j > e.j || (w.at.j == e.j && w.at.k >= e.k))))
       return false;
-    const LtSeq s = lt_seq<N>(p, at.b);
-    if (at.j >= s.tiles) {
-      at.b += 1;
-      at.j = at.k = 0;
+    if (w.at.j >= w.s.tiles) {
+      w.at.b += 1;
+      w.at.j = w.at.k = 0;
+      if (w.at.b < p.B) w.s = lt_seq<N>(p, w.at.b);
       continue;
     }
-    x.b = at.b;
-    x.j = at.j;
-    x.k0 = at.k;
-    x.blocks = lt_blocks<N>(p, s, at.j);
-    x.k1 = (at.b == end.b && at.j == end.j) ? end.k : x.blocks;
-    x.local_row = at.j * N;
-    x.rows = min(N, s.rows - at.j * N);
-    x.row0 = s.q0 * p.H + at.j * N;
-    x.q0 = s.q0;
-    x.n = s.n;
-    x.L = s.L;
-    at.j += 1;
-    at.k = 0;
+    x.b = w.at.b;
+    x.j = w.at.j;
+    x.k0 = w.at.k;
+    x.blocks = lt_blocks<N>(p, w.s, w.at.j);
+    x.k1 = (w.at.b == e.b && w.at.j == e.j) ? e.k : x.blocks;
+    x.local_row = w.at.j * N;
+    x.rows = min(N, w.s.rows - w.at.j * N);
+    x.row0 = w.s.q0 * p.H + w.at.j * N;
+    x.n = w.s.n;
+    x.L = w.s.L;
+    w.at.j += 1;
+    w.at.k = 0;
     return true;
   }
 }
@@ -292,14 +300,13 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   uint64_t* bar_kvfree = bars + 4;   // [2][4] the MMAs that read a page of it are done
   uint64_t* bar_s = bars + 12;       // [2] scores written
   uint64_t* bar_p = bars + 14;       // [2] P written (256 arrivals)
-  uint64_t* bar_o = bars + 16;       // [2] P V done: O^T up to date
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
   int64_t* s_wsum = reinterpret_cast<int64_t*>(sm + S::wsum);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
-    for (int i = 0; i < 18; ++i) mbar_init(bars + i, bars + i == bar_p || bars + i == bar_p + 1 ? kLtSoftmaxThreads : 1);
+    for (int i = 0; i < 16; ++i) mbar_init(bars + i, bars + i == bar_p || bars + i == bar_p + 1 ? kLtSoftmaxThreads : 1);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -315,12 +322,16 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 
   // ---- plan: this CTA's share of the work -------------------------------------
   {
-    int64_t* s_scan = reinterpret_cast<int64_t*>(sm + S::kv);  // weight before sequence b
+    // the plan's arrays borrow the first cache tile
+    int64_t* s_scan = reinterpret_cast<int64_t*>(sm + S::kv);      // weight before sequence b
+    int4* s_seq = reinterpret_cast<int4*>(s_scan + PKV_MAX_SEQS + 2);  // its q0, q1, L
     const int per = (p.B + kLtThreads - 1) / kLtThreads;
     const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     int64_t local = 0;
     for (int b = b0; b < b1; ++b) {
-      const LtSeq s = lt_seq<N>(p, b);
+      const int4 raw = make_int4(__ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b), 0);
+      s_seq[b] = raw;
+      const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
       if (s.bad && blockIdx.x == 0) flag_status(p.status, PKV_STATUS_BAD_QUERY);
       const int64_t w = lt_weight<N>(p, s, s.tiles);
       s_scan[b] = w;
@@ -360,7 +371,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           const int mid = (lo + hi) >> 1;
           if (s_scan[mid] <= x) lo = mid; else hi = mid;
         }
-        const LtSeq s = lt_seq<N>(p, lo);
+        const int4 raw = s_seq[lo];
+        const LtSeq s = lt_seq<N>(p, lo, raw.x, raw.y, raw.z);
         const int64_t y = x - s_scan[lo];
         int jl = 0, jh = s.tiles;  // last j with weight(j) <= y
         while (jh - jl > 1) {
@@ -374,6 +386,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         // the last CTA whose share starts before this tile's end
         const int64_t e = s_scan[lo] + w1;
         last = int((e * g + total - 1) / total) - 1;
+        if (tid == 0) *reinterpret_cast<int4*>(s_share + 8) = raw;
       }
       s_share[tid * 4] = at.b;
       s_share[tid * 4 + 1] = at.j;
@@ -389,6 +402,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const uint32_t tmem = *s_tmem;
   const LtPos begin{s_share[0], s_share[1], s_share[2]};
   const LtPos end{s_share[4], s_share[5], s_share[6]};
+  const LtWalk first{begin, end, lt_seq<N>(p, begin.b, s_share[8], s_share[9], s_share[10])};
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
   // every lane waits; the warp goes on only if all of them saw the phase
@@ -398,12 +412,12 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 
   if (warp == 8) {
     // ===== loader: queries and cache tiles, in the order they are used =====
-    LtPos at = begin;
+    LtWalk walk = first;
     LtPiece x;
     int g = 0, pieces = 0;  // cache tiles and tiles of rows so far
     int landing = 0;        // cache tiles whose copies were issued
     bool ok = true;
-    while (ok && lt_next<N>(p, at, end, x)) {
+    while (ok && lt_next<N>(p, walk, x)) {
       if (lane == 0) {
         if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
         if (ok) {
@@ -486,11 +500,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // softmax has taken the scores two tiles before from its buffer =====
     constexpr uint32_t idesc = lt_idesc(64, N, false, false);
     const uint32_t aq = smem_u32(sm + S::q);
-    LtPos at = begin;
+    LtWalk walk = first;
     LtPiece x;
     int g = 0, pieces = 0;
     bool ok = true;
-    while (ok && lt_next<N>(p, at, end, x)) {
+    while (ok && lt_next<N>(p, walk, x)) {
       ok = wait_all(bar_q, pieces & 1);
       for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
         if (g >= 2) ok = wait_all(bar_p + (g & 1), ((g >> 1) - 1) & 1);
@@ -519,11 +533,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // waited for that tile's copies, and they for the buffer that P V frees
     // (5000 cycles a tile against 3100). =====
     constexpr uint32_t idesc = lt_idesc(128, N, true, true);
-    LtPos at = begin;
+    LtWalk walk = first;
     LtPiece x;
     int g = 0;
     bool ok = true;
-    while (ok && lt_next<N>(p, at, end, x)) {
+    while (ok && lt_next<N>(p, walk, x)) {
       for (int k = x.k0; k < x.k1; ++k, ++g) {
         if (!(ok = wait_all(bar_p + (g & 1), (g >> 1) & 1))) break;
         const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(g % kLtStages) * kLtTileBytes;
@@ -537,11 +551,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                  (k > x.k0 || ks > 0) ? 1u : 0u);
           umma_commit(bar_kvfree + (g % kLtStages) * kLtPages + ks);
         }
-        umma_commit(bar_o + (g & 1));
       }
     }
     if (!ok && lane == 0) flag_status(p.status, PKV_STATUS_TIMEOUT);
-    if (g > 0) mbar_wait(bar_o + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
+    if (g > 0)
+      mbar_wait(bar_kvfree + ((g - 1) % kLtStages) * kLtPages + kLtPages - 1, ((g - 1) / kLtStages) & 1, kLandLimitNs);
     __syncwarp();
   } else {
     // ===== softmax and results: warpgroup w has rows [w * NW, (w + 1) * NW) =====
@@ -552,7 +566,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     float* s_red = reinterpret_cast<float*>(sm + S::red);      // [4][N]
     float* s_alpha = reinterpret_cast<float*>(sm + S::alpha);  // [N]
     const int bar_id = 1 + wg;
-    LtPos at = begin;
+    LtWalk walk = first;
     LtPiece x;
     int g = 0;
     // A warp whose wait ran out waits no more, but goes through the rest of
@@ -562,21 +576,22 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
     };
-    // P V of the first `tiles` tiles.  A wait names a phase by its parity, so
-    // it has to come before the barrier can be a whole phase further: even and
-    // odd tiles have a barrier each (here, for P and for the scores), and every
-    // tile waits, before its P is given away, for the P V two tiles before.
-    int o_seen = 0;
-    auto wait_o = [&](int tiles) {
-      for (; o_seen < tiles; ++o_seen) wait(bar_o + (o_seen & 1), (o_seen >> 1) & 1);
+    // O^T up to date with tile t, the last one whose P this warp gave away:
+    // P V's last page is let go of.  (A wait names a phase by its parity, so it
+    // must not be able to be a whole phase late: the next phase of that barrier
+    // is tile t + 2's, whose P this warp has yet to write.  For the same reason
+    // even and odd tiles have a barrier each for P and for the scores.)
+    auto wait_o = [&](int t) {
+      wait(bar_kvfree + (t % kLtStages) * kLtPages + kLtPages - 1, (t / kLtStages) & 1);
     };
-    while (lt_next<N>(p, at, end, x)) {
-      float m[NC], l[NC];
+    while (lt_next<N>(p, walk, x)) {
+      float m[NC];       // reference of each row
+      uint64_t l2[NC / 2];  // row sums of this thread's keys, two rows a word
       int lim[NC];  // last key that the row sees
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         m[c] = 0.f;
-        l[c] = 0.f;
+        l2[c / 2] = 0;
         lim[c] = x.L - x.n + min(x.n - 1, (x.local_row + col0 + c) / p.H);
       }
       const int first_lim = x.L - x.n + x.local_row / p.H;  // the tile's first row's
@@ -588,54 +603,70 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         tmem_wait_ld();
         const int pos = k * kLtKeys + key;
         const bool masked = k * kLtKeys + kLtKeys - 1 > first_lim;
+        // x = scaled score - reference, two rows an instruction
+        float xs[NC];
+        auto relative = [&]() {
+          const uint64_t q2 = f2(p.qscale, p.qscale);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          s[c] *= p.qscale;
-          if (masked && pos > lim[c]) s[c] = -INFINITY;
-        }
+          for (int c = 0; c < NC; c += 2)
+            f2_split(f2_fma(f2(s[c], s[c + 1]), q2, f2(-m[c], -m[c + 1])), xs[c], xs[c + 1]);
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (pos > lim[c]) xs[c] = -INFINITY;
+          }
+        };
+        relative();
         if (k == x.k0) {
           // A piece's first reference is its first key's score.  Rows that do
           // not see that key see nothing of this piece (what a row sees is a
           // prefix) and keep 0.
           if (key == 0) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) s_alpha[col0 + c] = s[c] == -INFINITY ? 0.f : s[c];
+            for (int c = 0; c < NC; ++c) s_alpha[col0 + c] = xs[c] == -INFINITY ? 0.f : xs[c];
           }
           named_sync(bar_id, 128);
 #pragma unroll
           for (int c = 0; c < NC; ++c) m[c] = s_alpha[col0 + c];
+          relative();
         }
-        float top = -INFINITY;
+        float top = xs[0];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) top = fmaxf(top, s[c] - m[c]);
+        for (int c = 0; c < NC; c += 2) top = max3(top, xs[c], xs[c + 1]);
         if (named_sync_or(bar_id, 128, top > kLtTau)) {
           // New references: the maximum over the tile's 64 keys where that is
           // above the old one.
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            float v = s[c];
+            float v = xs[c];
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
             if ((lane & 15) == 0) s_red[quad * N + col0 + c] = v;
           }
           named_sync(bar_id, 128);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            float v = s_red[col0 + c];
+          for (int c = 0; c < NC; c += 2) {
+            float a[2];
 #pragma unroll
-            for (int q = 1; q < 4; ++q) v = fmaxf(v, s_red[q * N + col0 + c]);
-            float a = 1.f;
-            if (v > m[c]) {
-              a = ex2(m[c] - v);
-              m[c] = v;
-              l[c] *= a;
+            for (int e = 0; e < 2; ++e) {
+              float v = s_red[col0 + c + e];
+#pragma unroll
+              for (int q = 1; q < 4; ++q) v = fmaxf(v, s_red[q * N + col0 + c + e]);
+              a[e] = 1.f;
+              if (v > 0.f) {
+                const float up = m[c + e] + v;
+                a[e] = ex2(m[c + e] - up);
+                m[c + e] = up;
+              }
+              if (quad == 0 && (lane & 15) == 0) s_alpha[col0 + c + e] = a[e];
             }
-            if (quad == 0 && (lane & 15) == 0) s_alpha[col0 + c] = a;
+            l2[c / 2] = f2_fma(l2[c / 2], f2(a[0], a[1]), 0);
           }
+          relative();
           if (k > x.k0) {
             // O^T of the earlier tiles under the new references
             named_sync(bar_id, 128);
-            wait_o(g);
+            wait_o(g - 1);
             tc_fence_after();
 #pragma unroll 1
             for (int d = 0; d < 4; ++d)
@@ -655,11 +686,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         uint32_t pk[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          pk[c / 2] = pack_bf16x2(ex2(s[c] - m[c]), ex2(s[c + 1] - m[c + 1]));
-          l[c] += bf_lo(pk[c / 2]);
-          l[c + 1] += bf_hi(pk[c / 2]);
+          pk[c / 2] = pack_bf16x2(ex2(xs[c]), ex2(xs[c + 1]));
+          l2[c / 2] = f2_add(l2[c / 2], f2(bf_lo(pk[c / 2]), bf_hi(pk[c / 2])));
         }
-        wait_o(g - 1);  // done long since: the tile two before shares this one's buffer
         if (!ok) continue;
         uint8_t* kv = sm + S::kv + (g % kLtStages) * kLtTileBytes;
         uint8_t* prow = kv + (key >> 3) * kLtGroupBytes + kLtChunkP + (key & 7) * 128;
@@ -687,8 +716,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 
       // ---- the piece's result ----
       const bool whole = x.k0 == 0 && x.k1 == x.blocks;
+      float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        if (c % 2 == 0) f2_split(l2[c / 2], l[c], l[c + 1]);
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
       }
@@ -711,7 +742,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           part[N * kLatentDim + N + r] = sum;
       }
       named_sync(bar_id, 128);
-      wait_o(g);
+      wait_o(g - 1);
       if (ok) {
         tc_fence_after();
         const int r0 = wg * NW;  // this warpgroup's rows of the tile
