@@ -312,84 +312,105 @@ def attend_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, qu
     return out
 
 
-def _need_rows(t, name, dim, heads=None):
-    """A bf16 CUDA tensor [T, heads, dim] whose heads are contiguous, or [T, dim] where heads is None,
-    with any token stride that keeps 16-byte alignment; returns that stride in elements."""
+# The calls below are a few microseconds of GPU work for small batches, so
+# their checks are made for speed: one short test a tensor, and the words for
+# what is wrong with it only where it fails.
+
+
+def _index(t, name):
+    """The CUDA device that ``t`` is on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    shape = (dim,) if heads is None else (heads, dim)
-    if tuple(t.shape[1:]) != shape:
-        raise ValueError(f"{name} must be [tokens, {', '.join(map(str, shape))}], got shape {tuple(t.shape)}")
+    return index
+
+
+def _take(t, name, dtype, ndim, index):
+    """The address of ``t``, a contiguous tensor of this type on device ``index``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == ndim
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, name, dtype, ndim)
+    raise ValueError(f"{name} is on {t.device}, not on device {index} like the cache")
+
+
+def _take_rows(t, name, tokens, heads, dim, index):
+    """(address, token stride) of a bf16 tensor [tokens, heads, dim], or
+    [tokens, dim] where heads is 0: a token's elements contiguous, any token
+    stride that keeps 16-byte alignment."""
+    shape = (tokens, heads, dim) if heads else (tokens, dim)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on the cache's device, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
     stride = t.stride()
-    if stride[-1] != 1 or (heads is not None and heads > 1 and stride[1] != dim):
+    if stride[-1] != 1 or (heads > 1 and stride[1] != dim):
         raise ValueError(f"a token's elements of {name} must be contiguous")
     row = dim * (heads or 1)
-    if t.shape[0] < 2:
-        return row
+    if tokens < 2:
+        return t.data_ptr(), row
     if stride[0] < row or stride[0] % 8:
         raise ValueError(f"{name}'s token stride must be a multiple of 8 elements and no less than a token")
-    return stride[0]
+    return t.data_ptr(), stride[0]
 
 
-def _need_same_device(device, *named):
-    for t, name in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-
-
-def _new(shape, like, stream, dtype=None):
+def _new(shape, dtype, device, stream):
     """An uninitialised tensor that belongs to the stream it is used on."""
-    dtype = like.dtype if dtype is None else dtype
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rope(cos_sin, interleaved):
-    _need(cos_sin, "cos_sin", torch.float32, 2)
-    return Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0)
+def _run(what, fn, index, stream, *args):
+    """fn(*args, stream) with device ``index`` current."""
+    # the current stream's handle, without the Stream object around it
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, handle)
+    if code:
+        raise PkvError(code, what)
 
 
-def _write_rope(fp8, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q, q_out,
-                interleaved, stream):
-    _, hkv, _, D = k_cache.shape
-    T = k_new.shape[0]
-    ks, vs = _need_rows(k_new, "k_new", D, hkv), _need_rows(v_new, "v_new", D, hkv)
-    _need(positions, "positions", torch.int64, 1)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    rope = _rope(cos_sin, interleaved)
-    if v_new.shape[0] != T or positions.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("k_new, v_new, positions and slot_mapping disagree on the number of tokens")
-    dev = k_cache.device
-    hq, qs = hkv, 0
+def _rope(cos_sin, interleaved, index):
+    at = _take(cos_sin, "cos_sin", torch.float32, 2, index)
+    max_position, dim = cos_sin.shape
+    return Rope(at, max_position, dim, 1 if interleaved else 0)
+
+
+def _write_rope(what, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q, q_out, interleaved,
+                stream):
+    blocks, hkv, page, D = k_cache.shape
+    T = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() else -1
+    k, ks = _take_rows(k_new, "k_new", T, hkv, D, index)
+    v, vs = _take_rows(v_new, "v_new", T, hkv, D, index)
+    pos = _take(positions, "positions", torch.int64, 1, index)
+    slots = _take(slot_mapping, "slot_mapping", torch.int64, 1, index)
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("k_new, positions and slot_mapping disagree on the number of tokens")
+    hq, qs, qp, qo = hkv, 0, None, None
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
-            raise ValueError("q must be [tokens, Hq, D] with k_new's tokens")
-        hq = q.shape[1]
-        qs = _need_rows(q, "q", D, hq)
+        hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+        qp, qs = _take_rows(q, "q", T, hq, D, index)
         if q_out is None:
-            q_out = _new(q.shape, q, stream)
-        else:
-            _need(q_out, "q_out", torch.bfloat16, 3)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
+            q_out = _new(q.shape, q.dtype, q.device, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qo = _take(q_out, "q_out", torch.bfloat16, 3, index)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _need_same_device(dev, (k_new, "k_new"), (v_new, "v_new"), (positions, "positions"), (cos_sin, "cos_sin"),
-                      (slot_mapping, "slot_mapping"), (v_cache, "v_cache"), (k_scale, "k_scale"),
-                      (v_scale, "v_scale"), (q, "q"), (q_out, "q_out"))
-    desc = make_desc(k_cache, hq, 1)
-    what = "pkv_write_rope_fp8" if fp8 else "pkv_write_rope"
-    pools = (_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale))[:4 if fp8 else 2]
-    with torch.cuda.device(dev):
-        _check(getattr(lib(), what)(_ptr(q), _ptr(k_new), _ptr(v_new), qs, ks, vs, _ptr(positions),
-                                    _ptr(slot_mapping), T, ctypes.byref(rope), _ptr(q_out), *pools,
-                                    ctypes.byref(desc), _stream(dev, stream)), what)
+    rope, desc = _rope(cos_sin, interleaved, index), Desc(blocks, page, hkv, hq, D, 1)
+    _run(what, getattr(lib(), what), index, stream, qp, k, v, qs, ks, vs, pos, slots, T, ctypes.byref(rope), qo, *pools,
+         ctypes.byref(desc))
     return q_out
 
 
@@ -402,20 +423,25 @@ def write_rope(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache,
     (i, i + rotary_dim/2), or (2i, 2i + 1) with ``interleaved``.  k_new, v_new
     and q may be slices of one projection's output.  Returns the rotated
     queries (``q_out``, which may be a contiguous ``q`` itself), or None."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _need(t, n, torch.bfloat16, 4)
+    index = _index(k_cache, "k_cache")
+    pools = (_take(k_cache, "k_cache", torch.bfloat16, 4, index), _take(v_cache, "v_cache", torch.bfloat16, 4, index))
     if k_cache.shape != v_cache.shape:
         raise ValueError("k_cache and v_cache shapes disagree")
-    return _write_rope(False, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, None, None, q, q_out,
-                       interleaved, stream)
+    return _write_rope("pkv_write_rope", k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q,
+                       q_out, interleaved, stream)
 
 
 def write_rope_fp8(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q=None,
                    q_out=None, interleaved=False, stream=None):
     """write_rope into FP8 pages (codes and scale bytes as in write_fp8): the
     rotated fp32 values are rounded once, to E4M3."""
-    _need_fp8_pool(k_cache, v_cache, k_scale, v_scale)
-    return _write_rope(True, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q,
+    index = _index(k_cache, "k_cache")
+    pools = (_take(k_cache, "k_cache", torch.uint8, 4, index), _take(v_cache, "v_cache", torch.uint8, 4, index),
+             _take(k_scale, "k_scale", torch.uint8, 3, index), _take(v_scale, "v_scale", torch.uint8, 3, index))
+    shape = k_cache.shape
+    if v_cache.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+        raise ValueError("FP8 pools must be codes [NB, Hkv, P, D] and scales [NB, Hkv, P]")
+    return _write_rope("pkv_write_rope_fp8", k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q,
                        q_out, interleaved, stream)
 
 
@@ -432,19 +458,21 @@ def write_latent(c_new, k_pe, positions, cos_sin, slot_mapping, latent_cache, q_
     With ``q_pe`` [T, H, 64] the queries' rotated part goes into the last 64
     values of ``q_out`` [T, H, 576], whose first 512 are left alone.  c_new,
     k_pe and q_pe may be slices.  Returns q_out, or None."""
-    _need(latent_cache, "latent_cache", torch.bfloat16, 3)
-    T = c_new.shape[0]
-    cs, ks = _need_rows(c_new, "c_new", LATENT_DIM), _need_rows(k_pe, "k_pe", LATENT_ROPE)
-    _need(positions, "positions", torch.int64, 1)
-    _need(slot_mapping, "slot_mapping", torch.int64, 1)
-    rope = _rope(cos_sin, interleaved)
-    if k_pe.shape[0] != T or positions.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("c_new, k_pe, positions and slot_mapping disagree on the number of tokens")
-    dev = latent_cache.device
-    heads, qs, hs = 1, LATENT_ROPE, LATENT_ROPE
+    index = _index(latent_cache, "latent_cache")
+    pool = _take(latent_cache, "latent_cache", torch.bfloat16, 3, index)
+    T = c_new.shape[0] if isinstance(c_new, torch.Tensor) and c_new.dim() else -1
+    c, cs = _take_rows(c_new, "c_new", T, 0, LATENT_DIM, index)
+    k, ks = _take_rows(k_pe, "k_pe", T, 0, LATENT_ROPE, index)
+    pos = _take(positions, "positions", torch.int64, 1, index)
+    slots = _take(slot_mapping, "slot_mapping", torch.int64, 1, index)
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("c_new, positions and slot_mapping disagree on the number of tokens")
+    heads, qs, hs, qp, qo = 1, 0, 0, None, None
     if q_pe is not None:
-        if not isinstance(q_pe, torch.Tensor) or q_pe.dtype != torch.bfloat16:
+        if not isinstance(q_pe, torch.Tensor) or q_pe.dtype is not torch.bfloat16:
             raise TypeError(f"q_pe must be a {torch.bfloat16} tensor")
+        if q_pe.get_device() != index:
+            raise ValueError(f"q_pe must be a CUDA tensor on the cache's device, got {q_pe.device}")
         if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != LATENT_ROPE or q_pe.stride(2) != 1:
             raise ValueError(f"q_pe must be [tokens, H, {LATENT_ROPE}] with contiguous rows, got shape "
                              f"{tuple(q_pe.shape)}")
@@ -454,20 +482,15 @@ def write_latent(c_new, k_pe, positions, cos_sin, slot_mapping, latent_cache, q_
         if hs < LATENT_ROPE or hs % 8 or qs < (heads - 1) * hs + LATENT_ROPE or qs % 8:
             raise ValueError("q_pe's strides must be multiples of 8 elements and its rows must not overlap")
         if q_out is None:
-            q_out = _new((T, heads, LATENT_ROW), q_pe, stream)
-        else:
-            _need(q_out, "q_out", torch.bfloat16, 3)
-            if tuple(q_out.shape) != (T, heads, LATENT_ROW):
-                raise ValueError(f"q_out must be [tokens, H, {LATENT_ROW}]")
+            q_out = _new((T, heads, LATENT_ROW), torch.bfloat16, q_pe.device, stream)
+        elif q_out.shape != (T, heads, LATENT_ROW):
+            raise ValueError(f"q_out must be [tokens, H, {LATENT_ROW}]")
+        qp, qo = q_pe.data_ptr(), _take(q_out, "q_out", torch.bfloat16, 3, index)
     elif q_out is not None:
         raise ValueError("q_out without q_pe")
-    _need_same_device(dev, (c_new, "c_new"), (k_pe, "k_pe"), (positions, "positions"), (cos_sin, "cos_sin"),
-                      (slot_mapping, "slot_mapping"), (q_pe, "q_pe"), (q_out, "q_out"))
-    desc = make_latent_desc(latent_cache, heads, 1)
-    with torch.cuda.device(dev):
-        _check(lib().pkv_write_latent(_ptr(c_new), _ptr(k_pe), _ptr(q_pe), cs, ks, qs, hs, _ptr(positions),
-                                      _ptr(slot_mapping), T, ctypes.byref(rope), _ptr(q_out), _ptr(latent_cache),
-                                      ctypes.byref(desc), _stream(dev, stream)), "pkv_write_latent")
+    rope, desc = _rope(cos_sin, interleaved, index), make_latent_desc(latent_cache, heads, 1)
+    _run("pkv_write_latent", lib().pkv_write_latent, index, stream, c, k, qp, cs, ks, qs, hs, pos, slots, T,
+         ctypes.byref(rope), qo, pool, ctypes.byref(desc))
     return q_out
 
 
@@ -487,36 +510,28 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
     values are the value.  Returns ``out`` [T, H, 512].  The other arguments
     are as in attend(); max_query_len (0 = unknown) selects tile sizes, never
     results."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(latent_cache, "latent_cache", torch.bfloat16, 3)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(query_start_loc, "query_start_loc", torch.int32, 1)
+    index = _index(latent_cache, "latent_cache")
+    pool = _take(latent_cache, "latent_cache", torch.bfloat16, 3, index)
+    qp = _take(q, "q", torch.bfloat16, 3, index)
+    tables = _take(block_tables, "block_tables", torch.int32, 2, index)
+    lens = _take(seq_lens, "seq_lens", torch.int32, 1, index)
+    qsl = _take(query_start_loc, "query_start_loc", torch.int32, 1, index)
     T, H, row = q.shape
     B = seq_lens.shape[0]
     if query_start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
         raise ValueError("seq_lens [B], query_start_loc [B+1] and block_tables [B, M] disagree")
     if latent_cache.shape[2] != row:
         raise ValueError("latent_cache and q rows disagree")
-    dev = latent_cache.device
     desc = make_latent_desc(latent_cache, H, block_tables.shape[1])
     if out is None:
-        out = _new((T, H, LATENT_DIM), q, stream)
-    else:
-        _need(out, "out", torch.bfloat16, 3)
-        if tuple(out.shape) != (T, H, LATENT_DIM):
-            raise ValueError(f"out must be [tokens, H, {LATENT_DIM}]")
+        out = _new((T, H, LATENT_DIM), torch.bfloat16, q.device, stream)
+    elif out.shape != (T, H, LATENT_DIM):
+        raise ValueError(f"out must be [tokens, H, {LATENT_DIM}]")
     if workspace is None:
-        workspace = _new((workspace_size_latent(desc, B, T, dev),), q, stream, torch.uint8)
-    else:
-        _need(workspace, "workspace", torch.uint8)
-    _need_same_device(dev, (q, "q"), (block_tables, "block_tables"), (seq_lens, "seq_lens"),
-                      (query_start_loc, "query_start_loc"), (out, "out"), (workspace, "workspace"))
-    with torch.cuda.device(dev):
-        _check(lib().pkv_attend_latent(_ptr(q), _ptr(latent_cache), _ptr(block_tables), _ptr(seq_lens),
-                                       _ptr(query_start_loc), B, T, int(max_query_len), float(scale), _ptr(out),
-                                       _ptr(workspace), workspace.numel(), ctypes.byref(desc), _stream(dev, stream)),
-               "pkv_attend_latent")
+        workspace = _new((workspace_size_latent(desc, B, T, index),), torch.uint8, q.device, stream)
+    _run("pkv_attend_latent", lib().pkv_attend_latent, index, stream, qp, pool, tables, lens, qsl, B, T,
+         int(max_query_len), scale, _take(out, "out", torch.bfloat16, 3, index),
+         _take(workspace, "workspace", torch.uint8, 1, index), workspace.numel(), ctypes.byref(desc))
     return out
 
 

@@ -65,7 +65,6 @@ constexpr uint32_t kLtGroupBytes = kLtChunks * 1024;         // 8 rows
 constexpr uint32_t kLtPageBytes = 2 * kLtGroupBytes;         // 18 KiB
 constexpr uint32_t kLtTileBytes = kLtPages * kLtPageBytes;   // 72 KiB
 constexpr int kLtStages = 2;
-constexpr int kAhead = 1;
 // P of a tile overwrites the tile's rotated chunk, which only the scores read:
 // 64 keys of 128 bytes, at the same strides, so P needs no memory of its own
 // and never waits for the P V before it.
@@ -82,8 +81,8 @@ struct LtSmem {
   static constexpr uint32_t bars = misc;           // 16 x 8
   static constexpr uint32_t tmem = misc + 128;
   static constexpr uint32_t share = misc + 144;    // 2 bounds x 4 ints, the first sequence's 4 ints
-  static constexpr uint32_t wsum = misc + 192;     // [10] x 8, plan scan
-  static constexpr uint32_t red = misc + 272;      // [4 quadrants][N] floats
+  static constexpr uint32_t wsum = misc + 192;     // [11] x 8, plan scan
+  static constexpr uint32_t red = misc + 288;      // [4 quadrants][N] floats
   static constexpr uint32_t alpha = red + 16 * N;  // [N] floats
   static constexpr uint32_t end = alpha + 4 * N;
   static constexpr uint32_t bytes = end + 1024;    // + alignment slack
@@ -96,7 +95,10 @@ struct LatentParams {
   uint16_t* out;
   const uint16_t* cache;
   float* partials;     // [CTAs][2][partial_stride]
-  int4* joins;         // [CTAs] (first row, rows, last CTA, -): the tile that CTA's share ends inside
+  // [CTAs] the tile that the CTA's share ends inside (first row, rows, last
+  // CTA with a piece of it; 0 rows: none), and the first CTA of the tile that
+  // its share begins inside (-1: none)
+  int4* joins;
   unsigned* status;
   int32_t B, T, H, max_blocks, num_blocks;
   float qscale;        // scale * log2(e)
@@ -359,13 +361,17 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (tid == 0) s_scan[p.B] = total;
     __syncthreads();
     if (tid < 2) {  // thread 0: the share's start, thread 1: its end
-      int64_t g = total / (int64_t(p.H) * kLtMinShare);
-      g = g < 1 ? 1 : g > gridDim.x ? gridDim.x : g;
-      const int64_t c = int64_t(blockIdx.x) + tid;
+      // Where a share begins is a product of floats: it only has to be the
+      // same for the CTAs on both sides and to rise with c, and a 64-bit
+      // integer division costs as much as a key block.
+      const float w = float(total);
+      const int g = max(1, min(int(gridDim.x), int(w / (float(p.H) * kLtMinShare))));
+      auto start = [&](int c) { return min(total - 1, int64_t(w * (float(c) / float(g)))); };
+      const int c = int(blockIdx.x) + tid;
       LtPos at{p.B, 0, 0};
       int last = -1;
       if (total > 0 && c < g) {
-        const int64_t x = c * total / g;
+        const int64_t x = start(c);
         int lo = 0, hi = p.B;  // last b with s_scan[b] <= x
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -380,13 +386,34 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           if (lt_weight<N>(p, s, mid) <= y) jl = mid; else jh = mid;
         }
         const int64_t w0 = lt_weight<N>(p, s, jl), w1 = lt_weight<N>(p, s, jl + 1);
+        const int blocks = lt_blocks<N>(p, s, jl);
         at.b = lo;
         at.j = jl;
-        at.k = int((y - w0) * lt_blocks<N>(p, s, jl) / (w1 - w0));
+        at.k = min(blocks - 1, int(float(y - w0) / float(w1 - w0) * float(blocks)));
         // the last CTA whose share starts before this tile's end
         const int64_t e = s_scan[lo] + w1;
-        last = int((e * g + total - 1) / total) - 1;
-        if (tid == 0) *reinterpret_cast<int4*>(s_share + 8) = raw;
+        last = max(c, min(g - 1, int(float(e) / w * float(g))));
+        while (last + 1 < g && start(last + 1) < e) ++last;
+        while (last > c && start(last) >= e) --last;
+        if (tid == 0) {
+          *reinterpret_cast<int4*>(s_share + 8) = raw;
+          // the CTA that has this tile's first block: the last one whose
+          // share does not begin behind it
+          int head = -1;
+          if (at.k > 0) {
+            const int64_t t0 = s_scan[lo] + w0;
+            auto behind = [&](int h) {
+              const int64_t v = start(h) - t0;
+              return v > 0 && min(blocks - 1, int(float(v) / float(w1 - w0) * float(blocks))) > 0;
+            };
+            head = max(0, min(c - 1, int(float(t0) / w * float(g))));
+            while (head + 1 < c && !behind(head + 1)) ++head;
+            while (head > 0 && behind(head)) --head;
+          }
+          s_share[11] = head;
+        }
+      } else if (tid == 0) {
+        s_share[11] = -1;
       }
       s_share[tid * 4] = at.b;
       s_share[tid * 4 + 1] = at.j;
@@ -457,11 +484,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           valid += id[i] >= 0;
         }
         const int st = g % kLtStages;
-        {
-          const int src = in_group + kAhead < 8 ? ids : next;
-          const int pid = __shfl_sync(0xffffffffu, src, ((in_group + kAhead) & 7) * kLtPages + (lane & 3));
-          if (lane < 4 && pid >= 0) prefetch_l2(p.cache + size_t(pid) * (kPage * kLatentRow), kLtPageBytes);
-        }
         if (lane == 0) {
           // page by page, as P V of the tile two before lets go of them
           int sent = 0;
@@ -484,6 +506,12 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         if (!ok) break;
+        // the next tile's pages into L2, a lane a page (the second tile's own
+        // copies follow at once)
+        const int id_next = __shfl_sync(0xffffffffu, in_group < 7 ? ids : next,
+                                        ((in_group + 1) & 7) * kLtPages + (lane & (kLtPages - 1)));
+        if (g > 0 && lane < kLtPages && id_next >= 0)
+          prefetch_l2(p.cache + size_t(id_next) * (kPage * kLatentRow), kLtPageBytes);
       }
     }
     if (lane == 0) {
@@ -746,6 +774,12 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       if (ok) {
         tc_fence_after();
         const int r0 = wg * NW;  // this warpgroup's rows of the tile
+        float inv[NW];
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < NW; c += 4)
+            *reinterpret_cast<float4*>(inv + c) = *reinterpret_cast<const float4*>(s_alpha + r0 + c);
+        }
 #pragma unroll 1
         for (int d = 0; d < 4; ++d) {
           float o[NW];  // lane: dim d * 128 + quad * 32 + lane; column: row
@@ -759,7 +793,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
                            (lane >> 1);
 #pragma unroll
             for (int c = 0; c < NW; c += 2) {
-              const float a = o[c] * s_alpha[r0 + c], b = o[c + 1] * s_alpha[r0 + c + 1];
+              const float a = o[c] * inv[c], b = o[c + 1] * inv[c + 1];
               const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
               if (r0 + c + (lane & 1) < x.rows)
                 to[c * (kLatentDim / 2)] = (lane & 1) ? pack_bf16x2(other, b) : pack_bf16x2(a, other);
@@ -782,11 +816,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // what the merge joins for this CTA: the tile its share ends inside, if
     // its first block is in this share
     if (tid == 0) {
-      int4 join = make_int4(0, 0, 0, 0);
+      int4 join = make_int4(0, 0, 0, s_share[11]);
       if (end.b < p.B && end.k > 0 &&
           (begin.b < end.b || (begin.b == end.b && (begin.j < end.j || (begin.j == end.j && begin.k == 0))))) {
         const LtSeq s = lt_seq<N>(p, end.b);
-        join = make_int4(s.q0 * p.H + end.j * N, min(N, s.rows - end.j * N), s_share[7], 0);
+        join = make_int4(s.q0 * p.H + end.j * N, min(N, s.rows - end.j * N), s_share[7], join.w);
       }
       p.joins[blockIdx.x] = join;
     }
@@ -809,36 +843,44 @@ __global__ void __launch_bounds__(kLtThreads, 1)
 // pieces: there warp i of the N warps of blocks (c, *) takes rows 4 (i / 4) ..
 // + 3 of the 128 dims i % 4.  A long sequence alone is one tile with a piece
 // a CTA: there the blocks of all its CTAs take units of four rows and 32 dims,
-// and a block's warps share the pieces.  (64 rows of 152 pieces, 20 MB: 84 us
-// with a block a row in the first way, 15 us in the second.)
+// and a block's warps share the pieces.  Both read O without waiting for the
+// weights: what bounds this kernel is the number of reads that wait for one
+// another.
 constexpr int kLtMergeThreads = 256;
+constexpr int kLtMergeWarps = kLtMergeThreads / 32;
 constexpr int kLtFewPieces = 6;
+constexpr int kLtBatch = 8;  // pieces that a warp has under way (64 registers: four blocks an SM)
 
-__device__ __forceinline__ float4 f4_weights(const float4& m, const float4& M, const float4& l) {
-  // a piece that saw no key of a row has weight 0 there
-  return make_float4(l.x == 0.f ? 0.f : ex2(m.x - M.x), l.y == 0.f ? 0.f : ex2(m.y - M.y),
-                     l.z == 0.f ? 0.f : ex2(m.z - M.z), l.w == 0.f ? 0.f : ex2(m.w - M.w));
+__device__ __forceinline__ float4 f4(float v) { return make_float4(v, v, v, v); }
+// a * x + y where a is not 0, else y: an O that saw no key was not written
+__device__ __forceinline__ float fma_seen(float a, float x, float y) { return a != 0.f ? fmaf(a, x, y) : y; }
+__device__ __forceinline__ float4 fma_seen(const float4& a, const float4& x, const float4& y) {
+  return make_float4(fma_seen(a.x, x.x, y.x), fma_seen(a.y, x.y, y.y), fma_seen(a.z, x.z, y.z),
+                     fma_seen(a.w, x.w, y.w));
 }
-__device__ __forceinline__ void f4_max_seen(float4& M, const float4& m, const float4& l) {
-  if (l.x != 0.f) M.x = fmaxf(M.x, m.x);
-  if (l.y != 0.f) M.y = fmaxf(M.y, m.y);
-  if (l.z != 0.f) M.z = fmaxf(M.z, m.z);
-  if (l.w != 0.f) M.w = fmaxf(M.w, m.w);
+__device__ __forceinline__ float4 f4_max(const float4& a, const float4& b) {
+  return make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
 }
-// a += w * o where w is not 0 (an O that saw no key may not have been written)
-__device__ __forceinline__ void f4_add(float4& a, const float4& w, const float4& o) {
-  if (w.x != 0.f) a.x += w.x * o.x;
-  if (w.y != 0.f) a.y += w.y * o.y;
-  if (w.z != 0.f) a.z += w.z * o.z;
-  if (w.w != 0.f) a.w += w.w * o.w;
+// references, those of pieces that saw no key put below all others
+__device__ __forceinline__ float4 f4_seen(const float4& m, const float4& l) {
+  constexpr float none = -INFINITY;
+  return make_float4(l.x != 0.f ? m.x : none, l.y != 0.f ? m.y : none, l.z != 0.f ? m.z : none,
+                     l.w != 0.f ? m.w : none);
+}
+__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
+__device__ __forceinline__ float4 f4_weight(const float4& m, const float4& M) {
+  return make_float4(weight(m.x, M.x), weight(m.y, M.y), weight(m.z, M.z), weight(m.w, M.w));
+}
+__device__ __forceinline__ float4 f4_shfl_xor(const float4& v, int o) {
+  return make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                     __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
 }
 
 template <int N>
-__global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const LatentParams p) {
-  constexpr int kWarps = kLtMergeThreads / 32;
-  __shared__ int s_head;
-  __shared__ float4 s_sum[kWarps];
-  __shared__ float4 s_acc[kWarps][32];
+__global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(const LatentParams p) {
+  __shared__ float4 s_max[kLtMergeWarps], s_sum[kLtMergeWarps];
+  __shared__ float4 s_w[kLtMergeThreads];  // of a piece; the grid has fewer CTAs
+  __shared__ float4 s_acc[kLtMergeWarps][32];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -867,72 +909,84 @@ __global__ void __launch_bounds__(kLtMergeThreads) pkv_latent_merge_kernel(const
             (lane & 1) ? pack_bf16x2(other, v[e + 1]) : pack_bf16x2(v[e], other);
     }
   };
-  constexpr float kNone = -INFINITY;
-  if (tid == 0) s_head = -1;
-  __syncthreads();
-  // the tile of many pieces that this CTA holds one of from an earlier CTA's
-  // share, if any (at most one: its share begins in it)
-  for (int c = tid; c < int(blockIdx.x); c += kLtMergeThreads) {
-    const int4 j = __ldcg(p.joins + c);
-    if (j.y > 0 && j.z >= int(blockIdx.x) && j.z - c + 1 > kLtFewPieces) s_head = c;
-  }
-  __syncthreads();
-  const int4 own = __ldcg(p.joins + blockIdx.x);  // the tile that its share ends inside
+  const int4 own = __ldcg(p.joins + blockIdx.x);
   const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
   if (!own_many) {
-    const int c = blockIdx.x, i = blockIdx.y * kWarps + warp;
+    const int c = blockIdx.x, i = blockIdx.y * kLtMergeWarps + warp;
     const int rq = i / 4, pieces = own.z - c + 1;
     if (rq * 4 < own.y) {
-      float4 M = make_float4(kNone, kNone, kNone, kNone);
-      for (int k = 0; k < pieces; ++k) f4_max_seen(M, m_of(c, k, rq), l_of(c, k, rq));
-      float4 acc[4], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 M = f4(-INFINITY), sum = f4(0.f), acc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = sum;
 #pragma unroll 2
       for (int k = 0; k < pieces; ++k) {
-        const float4 l = l_of(c, k, rq);
-        const float4 w = f4_weights(m_of(c, k, rq), M, l);
-        f4_add(sum, w, l);
+        const float4 l = l_of(c, k, rq), m = f4_seen(m_of(c, k, rq), l);
+        float4 o[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f4_add(acc[e], w, o_of(c, k, rq, (i & 3) * 4 + e));
+        for (int e = 0; e < 4; ++e) o[e] = o_of(c, k, rq, (i & 3) * 4 + e);
+        const float4 up = f4_max(M, m);
+        const float4 old = f4_weight(M, up), w = f4_weight(m, up);
+        M = up;
+        sum = fma_seen(w, l, fma_seen(old, sum, f4(0.f)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fma_seen(w, o[e], fma_seen(old, acc[e], f4(0.f)));
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) put(own, rq, (i & 3) * 4 + e, acc[e], sum);
     }
   }
   for (int which = 0; which < 2; ++which) {
-    const int c = which == 0 ? s_head : own_many ? int(blockIdx.x) : -1;
+    const int c = which == 0 ? own.w : own_many ? int(blockIdx.x) : -1;
     if (c < 0) continue;
     const int4 join = __ldcg(p.joins + c);
     const int pieces = join.z - c + 1;
+    if (pieces <= kLtFewPieces) continue;
     const int team = pieces * gridDim.y;
     for (int u = (blockIdx.x - c) * gridDim.y + blockIdx.y; u < (join.y + 3) / 4 * 16; u += team) {
       const int rq = u >> 4, dq = u & 15;
-      float4 M = make_float4(kNone, kNone, kNone, kNone);
-      for (int k = lane; k < pieces; k += 32) f4_max_seen(M, m_of(c, k, rq), l_of(c, k, rq));
+      float4 o[kLtBatch];
+      auto read = [&](int first) {
 #pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) {
-        M.x = fmaxf(M.x, __shfl_xor_sync(0xffffffffu, M.x, o));
-        M.y = fmaxf(M.y, __shfl_xor_sync(0xffffffffu, M.y, o));
-        M.z = fmaxf(M.z, __shfl_xor_sync(0xffffffffu, M.z, o));
-        M.w = fmaxf(M.w, __shfl_xor_sync(0xffffffffu, M.w, o));
+        for (int i = 0; i < kLtBatch; ++i) {
+          const int k = first + i * kLtMergeWarps;
+          if (k < pieces) o[i] = o_of(c, k, rq, dq);
+        }
+      };
+      read(warp);
+      float4 l = f4(0.f), m = f4(-INFINITY);
+      if (tid < pieces) {
+        l = l_of(c, tid, rq);
+        m = f4_seen(m_of(c, tid, rq), l);
       }
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), sum = acc;
-#pragma unroll 4
-      for (int k = warp; k < pieces; k += kWarps) {
-        const float4 l = l_of(c, k, rq), m = m_of(c, k, rq), o = o_of(c, k, rq, dq);
-        const float4 w = f4_weights(m, M, l);
-        f4_add(sum, w, l);
-        f4_add(acc, w, o);
-      }
-      s_acc[warp][lane] = acc;
+      float4 M = m;
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) M = f4_max(M, f4_shfl_xor(M, d));
+      if (lane == 0) s_max[warp] = M;
+      __syncthreads();
+      for (int w = 0; w < kLtMergeWarps; ++w) M = f4_max(M, s_max[w]);
+      const float4 w = f4_weight(m, M);
+      s_w[tid] = w;
+      float4 sum = make_float4(w.x * l.x, w.y * l.y, w.z * l.z, w.w * l.w);
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) sum = fma_seen(f4(1.f), f4_shfl_xor(sum, d), sum);
       if (lane == 0) s_sum[warp] = sum;
       __syncthreads();
+      float4 acc = f4(0.f);
+      for (int first = warp; first < pieces; first += kLtBatch * kLtMergeWarps) {
+        if (first > warp) read(first);
+#pragma unroll
+        for (int i = 0; i < kLtBatch; ++i) {
+          const int k = first + i * kLtMergeWarps;
+          if (k < pieces) acc = fma_seen(s_w[k], o[i], acc);
+        }
+      }
+      s_acc[warp][lane] = acc;
+      __syncthreads();
       if (warp == 0) {
-        const float4 one = make_float4(1.f, 1.f, 1.f, 1.f);
-        for (int w = 1; w < kWarps; ++w) {
-          f4_add(acc, one, s_acc[w][lane]);
-          f4_add(sum, one, s_sum[w]);
+        sum = s_sum[0];
+        for (int i = 1; i < kLtMergeWarps; ++i) {
+          acc = fma_seen(f4(1.f), s_acc[i][lane], acc);
+          sum = fma_seen(f4(1.f), s_sum[i], sum);
         }
         put(join, rq, dq, acc, sum);
       }
@@ -1007,6 +1061,7 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   const pkv_desc& d = a.desc;
   // rows are int32 on the device, and so are the tensor map's coordinates
   if (int64_t(a.num_tokens) * d.num_q_heads >= (int64_t(1) << 31) - 64) return PKV_ERR_RANGE;
+  if (ctx.dev->sm_count > kLtMergeThreads) return PKV_ERR_LAUNCH;  // the merge holds a piece a thread
   if (int64_t(d.num_blocks) * 2 >= (int64_t(1) << 31)) return PKV_ERR_RANGE;
   // the plan multiplies the batch's weight by the CTAs in 64 bits
   const double heaviest = 2.0 * d.num_q_heads * (16.0 * d.max_blocks_per_seq + kLtTileCost) + 64.0;

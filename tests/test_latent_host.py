@@ -102,13 +102,13 @@ def test_binding_refuses_types_and_host_tensors():
     ids = torch.zeros(4, dtype=torch.int64)
     tab = torch.zeros(8, 128)
     with pytest.raises(TypeError, match="k_cache"):
-        pkv.write_rope(bf(4, 2, 128), bf(4, 2, 128), ids, tab, ids, torch.zeros(8, 2, 16, 128), bf(8, 2, 16, 128))
+        pkv.write_rope(bf(4, 2, 128), bf(4, 2, 128), ids, tab, ids, [0.0], bf(8, 2, 16, 128))
     with pytest.raises(ValueError, match="CUDA"):
         pkv.write_rope(bf(4, 2, 128), bf(4, 2, 128), ids, tab, ids, bf(8, 2, 16, 128), bf(8, 2, 16, 128))
     with pytest.raises(ValueError, match="CUDA"):
         pkv.write_latent(bf(4, 512), bf(4, 64), ids, tab[:, :64], ids, bf(8, 16, 576))
-    with pytest.raises(TypeError, match="q must be"):
-        pkv.attend_latent(torch.zeros(4, 8, 576), bf(8, 16, 576), ids, ids, ids, 0.1)
+    with pytest.raises(TypeError, match="latent_cache must be"):
+        pkv.attend_latent(bf(4, 8, 576), None, ids, ids, ids, 0.1)
     with pytest.raises(ValueError, match="CUDA"):
         pkv.attend_latent(bf(4, 8, 576), bf(8, 16, 576), ids, ids, ids, 0.1)
 
