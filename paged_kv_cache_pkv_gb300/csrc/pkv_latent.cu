@@ -48,6 +48,7 @@
 //    grow with the batch, and the joining order is fixed.
 //  * Every mbarrier wait is bounded; on expiry the role flags
 //    PKV_STATUS_TIMEOUT, what is in flight lands, TMEM is freed.
+#include <algorithm>
 #include <mutex>
 
 #include "pkv_internal.h"
@@ -101,6 +102,7 @@ struct LatentParams {
   int4* joins;
   unsigned* status;
   int32_t B, T, H, max_blocks, num_blocks;
+  uint32_t inv_heads;  // floor(2^32 / H), at most 2^32 - 1
   float qscale;        // scale * log2(e)
 };
 
@@ -120,6 +122,12 @@ constexpr int kLtMinShare = 256 + kLtTileCost;
 // cost more to join than they save; above the most, equal shares of the
 // weight are the better balance.
 constexpr int kLtLeastOwn = 4, kLtMostOwn = 16;
+
+// row / H (row >= 0): the product is one short of it at most.
+__device__ __forceinline__ int lt_token(const LatentParams& p, int row) {
+  const int t = int(__umulhi(uint32_t(row), p.inv_heads));
+  return row - t * p.H >= p.H ? t + 1 : t;
+}
 
 struct LtSeq {
   int q0, n, L, rows, tiles;  // tiles == 0: no rows, or inconsistent
@@ -154,7 +162,7 @@ __device__ __forceinline__ int64_t lt_weight(const LatentParams& p, const LtSeq&
 template <int N>
 __device__ __forceinline__ int lt_blocks(const LatentParams& p, const LtSeq& s, int j) {
   const int last_row = min(s.rows, (j + 1) * N) - 1;
-  const int keys = s.L - s.n + last_row / p.H + 1;
+  const int keys = s.L - s.n + lt_token(p, last_row) + 1;
   return (keys + kLtKeys - 1) / kLtKeys;
 }
 
@@ -349,6 +357,15 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
   }
+  if (warp == 10) {
+    // The block tables into L2, shared among the CTAs: the first page ids
+    // then come 2500 cycles sooner.  (A hint: what the stream does before may
+    // still write them.)
+    const char* tables = reinterpret_cast<const char*>(p.block_tables);
+    const int64_t bytes = int64_t(p.B) * p.max_blocks * 4;
+    for (int64_t i = (int64_t(blockIdx.x) * 32 + lane) * 128; i < bytes; i += int64_t(gridDim.x) * 32 * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(tables + i));
+  }
   griddep_wait();  // what the stream did before: the queries, this step's rows, the metadata
 
   // ---- plan: this CTA's share of the work -------------------------------------
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         first_cta += s.tiles * n;
         if (r < 0 || r >= s.tiles * n) continue;
         const int j = r / n, i = r - j * n, blocks = lt_blocks<N>(p, s, j);
-        const int k0 = int(int64_t(i) * blocks / n), k1 = int(int64_t(i + 1) * blocks / n);
+        const int k0 = i * blocks / n, k1 = (i + 1) * blocks / n;  // blocks <= the cap's few thousand
         // a tile of fewer blocks than pieces begins at the first piece that has one
         const int head = k0 > 0 ? int(blockIdx.x) - i + (n + blocks - 1) / blocks - 1 : -1;
         *reinterpret_cast<int4*>(s_share) = make_int4(b, j, k0, 0);
@@ -427,11 +444,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       }
     } else if (tid < 2) {  // thread 0: the share's start, thread 1: its end
       // Where a share begins is a product of floats: it only has to be the
-      // same for the CTAs on both sides and to rise with c, and a 64-bit
-      // integer division costs as much as a key block.
-      const float w = float(total);
-      const int g = max(1, min(int(gridDim.x), int(w / (float(p.H) * kLtMinShare))));
-      auto start = [&](int c) { return min(total - 1, int64_t(w * (float(c) / float(g)))); };
+      // same for the CTAs on both sides and to rise with c, and exact
+      // divisions, of 64-bit integers above all, cost as much as a key block.
+      const int g = max(1, min(int(gridDim.x), int(__fdividef(float(total), float(p.H) * kLtMinShare))));
+      const float each = __fdividef(float(total), float(g));  // a share's weight
+      auto start = [&](int c) { return min(total - 1, int64_t(float(c) * each)); };
       const int c = int(blockIdx.x) + tid;
       LtPos at{p.B, 0, 0};
       int last = -1;
@@ -454,10 +471,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         const int blocks = lt_blocks<N>(p, s, jl);
         at.b = lo;
         at.j = jl;
-        at.k = min(blocks - 1, int(float(y - w0) / float(w1 - w0) * float(blocks)));
+        at.k = min(blocks - 1, int(__fdividef(float(y - w0), float(w1 - w0)) * float(blocks)));
         // the last CTA whose share starts before this tile's end
         const int64_t e = s_scan[lo] + w1;
-        last = max(c, min(g - 1, int(float(e) / w * float(g))));
+        last = max(c, min(g - 1, int(__fdividef(float(e), each))));
         while (last + 1 < g && start(last + 1) < e) ++last;
         while (last > c && start(last) >= e) --last;
         if (tid == 0) {
@@ -469,9 +486,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
             const int64_t t0 = s_scan[lo] + w0;
             auto behind = [&](int h) {
               const int64_t v = start(h) - t0;
-              return v > 0 && min(blocks - 1, int(float(v) / float(w1 - w0) * float(blocks))) > 0;
+              return v > 0 && min(blocks - 1, int(__fdividef(float(v), float(w1 - w0)) * float(blocks))) > 0;
             };
-            head = max(0, min(c - 1, int(float(t0) / w * float(g))));
+            head = max(0, min(c - 1, int(__fdividef(float(t0), each))));
             while (head + 1 < c && !behind(head + 1)) ++head;
             while (head > 0 && behind(head)) --head;
           }
@@ -685,9 +702,9 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       for (int c = 0; c < NC; ++c) {
         m[c] = 0.f;
         l2[c / 2] = 0;
-        lim[c] = x.L - x.n + min(x.n - 1, (x.local_row + col0 + c) / p.H);
+        lim[c] = x.L - x.n + min(x.n - 1, lt_token(p, x.local_row + col0 + c));
       }
-      const int first_lim = x.L - x.n + x.local_row / p.H;  // the tile's first row's
+      const int first_lim = x.L - x.n + lt_token(p, x.local_row);  // the tile's first row's
       for (int k = x.k0; k < x.k1; ++k, ++g) {
         wait(bar_s + (g & 1), (g >> 1) & 1);
         tc_fence_after();
@@ -1147,6 +1164,7 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   lp.B = a.num_seqs;
   lp.T = a.num_tokens;
   lp.H = d.num_q_heads;
+  lp.inv_heads = uint32_t(std::min<uint64_t>((uint64_t(1) << 32) / d.num_q_heads, 0xFFFFFFFFu));
   lp.max_blocks = d.max_blocks_per_seq;
   lp.num_blocks = d.num_blocks;
   lp.qscale = a.scale * 1.4426950408889634f;
