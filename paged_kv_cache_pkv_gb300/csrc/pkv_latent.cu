@@ -50,16 +50,17 @@
 //    PKV_STATUS_TIMEOUT, what is in flight lands, TMEM is freed.
 #include <algorithm>
 #include <mutex>
+#include <cstdlib>
 
 #include "pkv_internal.h"
-#include "pkv_tcgen05.cuh"
+#include "pkv_latent.cuh"
+#include "pkv_latent_merge.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kLtKeys = 64;                        // keys a cache tile
 constexpr int kLtPages = kLtKeys / kPage;          // 4
-constexpr int kLtChunks = kLatentRow / 64;         // 9 chunks of 64 dims (the last is rotated, keys only)
 constexpr int kLtSoftmaxThreads = 256;
 constexpr int kLtThreads = kLtSoftmaxThreads + 96;  // + loader, score and value warps
 constexpr uint32_t kLtGroupBytes = kLtChunks * 1024;         // 8 rows
@@ -89,131 +90,8 @@ struct LtSmem {
   static constexpr uint32_t bytes = end + 1024;    // + alignment slack
 };
 static_assert(LtSmem<64>::bytes <= 232448, "latent attention shared memory above the 227 KiB limit");
-static_assert((PKV_MAX_SEQS + 2) * 8 + PKV_MAX_SEQS * 16 <= kLtTileBytes, "the plan borrows the first cache tile");
+static_assert(kLtPlanBytes <= kLtTileBytes, "the plan borrows the first cache tile");
 
-struct LatentParams {
-  const int32_t *block_tables, *seq_lens, *qsl;
-  uint16_t* out;
-  const uint16_t* cache;
-  float* partials;     // [CTAs][2][partial_stride]
-  // [CTAs] the tile that the CTA's share ends inside (first row, rows, last
-  // CTA with a piece of it; 0 rows: none), and the first CTA of the tile that
-  // its share begins inside (-1: none)
-  int4* joins;
-  unsigned* status;
-  int32_t B, T, H, max_blocks, num_blocks;
-  uint32_t inv_heads;  // floor(2^32 / H), at most 2^32 - 1
-  float qscale;        // scale * log2(e)
-};
-
-// A partial: O in the order in which the softmax warps hold it, [4 blocks of
-// 128 dims][4 warps][N/4 groups of rows][32 dims][4 rows], then m [N], l [N].
-constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
-
-// Weights of the work split, in units of (keys x heads): tile j of a sequence
-// of n query tokens and ctx = L - n earlier ones weighs H * (ctx + kLtTileCost)
-// + (j + 1) * N, which is H times its last row's keys plus a constant for
-// loading its queries and writing its result; the sum over tiles is closed.
-constexpr int kLtTileCost = 128;
-// A share is at least this many keys: below it a second CTA's start and the
-// merge cost more than the keys.
-constexpr int kLtMinShare = 256 + kLtTileCost;
-// Key blocks a piece where tiles have CTAs of their own: fewer than the least
-// cost more to join than they save; above the most, equal shares of the
-// weight are the better balance.
-constexpr int kLtLeastOwn = 4, kLtMostOwn = 16;
-
-// row / H (row >= 0): the product is one short of it at most.
-__device__ __forceinline__ int lt_token(const LatentParams& p, int row) {
-  const int t = int(__umulhi(uint32_t(row), p.inv_heads));
-  return row - t * p.H >= p.H ? t + 1 : t;
-}
-
-struct LtSeq {
-  int q0, n, L, rows, tiles;  // tiles == 0: no rows, or inconsistent
-  bool bad;
-};
-
-template <int N>
-__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b, int q0, int q1, int L) {
-  LtSeq s;
-  s.q0 = q0;
-  s.L = L;
-  s.n = q1 - q0;
-  s.bad = q0 < 0 || s.n < 0 || q1 > p.T || s.n > L || L < 0 || (L + kPage - 1) / kPage > p.max_blocks ||
-          (b == 0 && q0 != 0);
-  if (s.bad) s.n = 0;
-  s.rows = s.n * p.H;
-  s.tiles = (s.rows + N - 1) / N;
-  return s;
-}
-template <int N>
-__device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b) {
-  return lt_seq<N>(p, b, __ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b));
-}
-
-// Weight of the first j tiles of a sequence.
-template <int N>
-__device__ __forceinline__ int64_t lt_weight(const LatentParams& p, const LtSeq& s, int64_t j) {
-  return j * (int64_t(p.H) * (s.L - s.n + kLtTileCost)) + N * (j * (j + 1) / 2);
-}
-
-// Key blocks that tile j of a sequence sees.
-template <int N>
-__device__ __forceinline__ int lt_blocks(const LatentParams& p, const LtSeq& s, int j) {
-  const int last_row = min(s.rows, (j + 1) * N) - 1;
-  const int keys = s.L - s.n + lt_token(p, last_row) + 1;
-  return (keys + kLtKeys - 1) / kLtKeys;
-}
-
-// A place in the work: key block k of tile j of sequence b (b == B: the end).
-struct LtPos {
-  int b, j, k;
-};
-
-// A piece of one tile: key blocks [k0, k1) of its `blocks`.
-struct LtPiece {
-  int b, j, k0, k1, blocks;
-  int row0, rows;   // of the tile: first row in q and out, rows
-  int local_row;    // the first row's index within the sequence's rows
-  int n, L;
-};
-
-// A walk over a share's pieces.  The sequence it is in is kept: its numbers
-// are read once.
-struct LtWalk {
-  LtPos at, end;
-  LtSeq s;  // of sequence at.b
-};
-
-// The next piece (never empty); false at the share's end.
-template <int N>
-__device__ __forceinline__ bool lt_next(const LatentParams& p, LtWalk& w, LtPiece& x) {
-  for (;;) {
-    const LtPos& e = w.end;
-    if (w.at.b >= p.B || w.at.b > e.b || (w.at.b == e.b && (w.at.j > e.j || (w.at.j == e.j && w.at.k >= e.k))))
-      return false;
-    if (w.at.j >= w.s.tiles) {
-      w.at.b += 1;
-      w.at.j = w.at.k = 0;
-      if (w.at.b < p.B) w.s = lt_seq<N>(p, w.at.b);
-      continue;
-    }
-    x.b = w.at.b;
-    x.j = w.at.j;
-    x.k0 = w.at.k;
-    x.blocks = lt_blocks<N>(p, w.s, w.at.j);
-    x.k1 = (w.at.b == e.b && w.at.j == e.j) ? e.k : x.blocks;
-    x.local_row = w.at.j * N;
-    x.rows = min(N, w.s.rows - w.at.j * N);
-    x.row0 = w.s.q0 * p.H + w.at.j * N;
-    x.n = w.s.n;
-    x.L = w.s.L;
-    w.at.j += 1;
-    w.at.k = 0;
-    return true;
-  }
-}
 
 // tcgen05.ld of X columns: lanes 0-15 read theirs from taddr on, lanes 16-31
 // the same TMEM lanes' columns SPLIT further on.
@@ -237,31 +115,6 @@ __device__ __forceinline__ bool lt_next(const LatentParams& p, LtWalk& w, LtPiec
           "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]),              \
           "=f"(r[13]), "=f"(r[14]), "=f"(r[15])                                                   \
         : "r"(taddr));
-
-// Sum over the threads before this one of their `v`, and over all of `v` and
-// of `u`.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t u, longlong2* s_wsum, longlong2& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    u += __shfl_xor_sync(0xffffffffu, u, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) s_wsum[warp] = make_longlong2(incl, u);
-  __syncthreads();
-  int64_t run = incl - v;
-  total = make_longlong2(0, 0);
-#pragma unroll
-  for (int x = 0; x < kLtThreads / 32; ++x) {
-    const longlong2 s = s_wsum[x];
-    if (x < warp) run += s.x;
-    total.x += s.x;
-    total.y += s.y;
-  }
-  return run;
-}
 
 // N/4 score columns a thread: columns c0.. for lanes 0-15, c0 + N/4.. for 16-31.
 template <int N>
@@ -368,143 +221,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   }
   griddep_wait();  // what the stream did before: the queries, this step's rows, the metadata
 
-  // ---- plan: this CTA's share of the work -------------------------------------
-  {
-    // the plan's arrays borrow the first cache tile
-    int64_t* s_scan = reinterpret_cast<int64_t*>(sm + S::kv);      // weight before sequence b
-    int4* s_seq = reinterpret_cast<int4*>(s_scan + PKV_MAX_SEQS + 2);  // its q0, q1, L
-    const int per = (p.B + kLtThreads - 1) / kLtThreads;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-    // Tiles and key blocks of the batch ride along in one word, each capped
-    // far above what the choice below looks at.
-    int64_t local = 0, tiles_of = 0, blocks_of = 0;
-    for (int b = b0; b < b1; ++b) {
-      const int4 raw = make_int4(__ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b), 0);
-      s_seq[b] = raw;
-      const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
-      if (s.bad && blockIdx.x == 0) flag_status(p.status, PKV_STATUS_BAD_QUERY);
-      const int64_t w = lt_weight<N>(p, s, s.tiles);
-      s_scan[b] = w;
-      local += w;
-      tiles_of += s.tiles;
-      blocks_of += int64_t(s.tiles) * ((s.L + kLtKeys - 1) / kLtKeys);
-    }
-    longlong2 sums;
-    int64_t run = block_scan(local, (min(tiles_of, int64_t(1) << 20) << 32) | min(blocks_of, int64_t(1) << 20), s_wsum, sums);
-    const int64_t total = sums.x;
-    const int tiles = int(sums.y >> 32), blocks_all = int(sums.y & 0xFFFFFFFF);
-    for (int b = b0; b < b1; ++b) {
-      const int64_t w = s_scan[b];
-      s_scan[b] = run;
-      run += w;
-    }
-    if (tid == 0) s_scan[p.B] = total;
-    __syncthreads();
-    // Few tiles: each has CTAs of its own, pieces of `own` key blocks, so that
-    // a CTA has one piece and no tile is cut that need not be (four sequences
-    // of up to 255 tokens: 16.3 -> 13.4 us).  The pieces fit the grid because
-    // ceil(n / own) sums to no more than tiles + blocks / own.
-    int own = 0;
-    if (tiles > 0 && tiles < int(gridDim.x)) {
-      const float t = float(blocks_all) / float(int(gridDim.x) - tiles);
-      if (t <= float(kLtMostOwn)) own = max(kLtLeastOwn, int(ceilf(t)));
-    }
-    if (own > 0) {
-      auto cuts = [&](const LtSeq& s) {  // pieces of a tile
-        const int n = (s.L + kLtKeys - 1) / kLtKeys;
-        return n <= 2 * own ? 1 : (n + own - 1) / own;
-      };
-      int64_t count = 0;
-      for (int b = b0; b < b1; ++b) {
-        const int4 raw = s_seq[b];
-        const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
-        count += int64_t(s.tiles) * cuts(s);
-      }
-      int first_cta = int(block_scan(count, 0, s_wsum + kLtThreads / 32, sums));
-      if (tid == 0) {
-        *reinterpret_cast<int4*>(s_share) = make_int4(p.B, 0, 0, -1);
-        *reinterpret_cast<int4*>(s_share + 4) = make_int4(p.B, 0, 0, -1);
-        *reinterpret_cast<int4*>(s_share + 8) = make_int4(0, 0, 0, -1);
-      }
-      __syncthreads();
-      for (int b = b0; b < b1; ++b) {
-        const int4 raw = s_seq[b];
-        const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
-        const int n = cuts(s), r = int(blockIdx.x) - first_cta;
-        first_cta += s.tiles * n;
-        if (r < 0 || r >= s.tiles * n) continue;
-        const int j = r / n, i = r - j * n, blocks = lt_blocks<N>(p, s, j);
-        const int k0 = i * blocks / n, k1 = (i + 1) * blocks / n;  // blocks <= the cap's few thousand
-        // a tile of fewer blocks than pieces begins at the first piece that has one
-        const int head = k0 > 0 ? int(blockIdx.x) - i + (n + blocks - 1) / blocks - 1 : -1;
-        *reinterpret_cast<int4*>(s_share) = make_int4(b, j, k0, 0);
-        *reinterpret_cast<int4*>(s_share + 4) =
-            k1 == blocks ? make_int4(b, j + 1, 0, 0) : make_int4(b, j, k1, int(blockIdx.x) - i + n - 1);
-        *reinterpret_cast<int4*>(s_share + 8) = make_int4(raw.x, raw.y, raw.z, head);
-      }
-    } else if (tid < 2) {  // thread 0: the share's start, thread 1: its end
-      // Where a share begins is a product of floats: it only has to be the
-      // same for the CTAs on both sides and to rise with c, and exact
-      // divisions, of 64-bit integers above all, cost as much as a key block.
-      const int g = max(1, min(int(gridDim.x), int(__fdividef(float(total), float(p.H) * kLtMinShare))));
-      const float each = __fdividef(float(total), float(g));  // a share's weight
-      auto start = [&](int c) { return min(total - 1, int64_t(float(c) * each)); };
-      const int c = int(blockIdx.x) + tid;
-      LtPos at{p.B, 0, 0};
-      int last = -1;
-      if (total > 0 && c < g) {
-        const int64_t x = start(c);
-        int lo = 0, hi = p.B;  // last b with s_scan[b] <= x
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (s_scan[mid] <= x) lo = mid; else hi = mid;
-        }
-        const int4 raw = s_seq[lo];
-        const LtSeq s = lt_seq<N>(p, lo, raw.x, raw.y, raw.z);
-        const int64_t y = x - s_scan[lo];
-        int jl = 0, jh = s.tiles;  // last j with weight(j) <= y
-        while (jh - jl > 1) {
-          const int mid = (jl + jh) >> 1;
-          if (lt_weight<N>(p, s, mid) <= y) jl = mid; else jh = mid;
-        }
-        const int64_t w0 = lt_weight<N>(p, s, jl), w1 = lt_weight<N>(p, s, jl + 1);
-        const int blocks = lt_blocks<N>(p, s, jl);
-        at.b = lo;
-        at.j = jl;
-        at.k = min(blocks - 1, int(__fdividef(float(y - w0), float(w1 - w0)) * float(blocks)));
-        // the last CTA whose share starts before this tile's end
-        const int64_t e = s_scan[lo] + w1;
-        last = max(c, min(g - 1, int(__fdividef(float(e), each))));
-        while (last + 1 < g && start(last + 1) < e) ++last;
-        while (last > c && start(last) >= e) --last;
-        if (tid == 0) {
-          *reinterpret_cast<int4*>(s_share + 8) = raw;
-          // the CTA that has this tile's first block: the last one whose
-          // share does not begin behind it
-          int head = -1;
-          if (at.k > 0) {
-            const int64_t t0 = s_scan[lo] + w0;
-            auto behind = [&](int h) {
-              const int64_t v = start(h) - t0;
-              return v > 0 && min(blocks - 1, int(__fdividef(float(v), float(w1 - w0)) * float(blocks))) > 0;
-            };
-            head = max(0, min(c - 1, int(__fdividef(float(t0), each))));
-            while (head + 1 < c && !behind(head + 1)) ++head;
-            while (head > 0 && behind(head)) --head;
-          }
-          s_share[11] = head;
-        }
-      } else if (tid == 0) {
-        s_share[11] = -1;
-      }
-      s_share[tid * 4] = at.b;
-      s_share[tid * 4 + 1] = at.j;
-      s_share[tid * 4 + 2] = at.k;
-      s_share[tid * 4 + 3] = last;
-    }
-    // the scan's words are rewritten by the copy engine
-    fence_proxy_async_smem();
-  }
+  // the plan borrows the first cache tile
+  lt_plan<N, kLtKeys, kLtThreads>(p, int(blockIdx.x), int(gridDim.x), sm + S::kv, s_wsum, s_share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -526,7 +244,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     int g = 0, pieces = 0;  // cache tiles and tiles of rows so far
     int landing = 0;        // cache tiles whose copies were issued
     bool ok = true;
-    while (ok && lt_next<N>(p, walk, x)) {
+    while (ok && lt_next<N, kLtKeys>(p, walk, x)) {
       if (lane == 0) {
         if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
         if (ok) {
@@ -614,7 +332,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     LtPiece x;
     int g = 0, pieces = 0;
     bool ok = true;
-    while (ok && lt_next<N>(p, walk, x)) {
+    while (ok && lt_next<N, kLtKeys>(p, walk, x)) {
       ok = wait_all(bar_q, pieces & 1);
       for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
         if (g >= 2) ok = wait_all(bar_p + (g & 1), ((g >> 1) - 1) & 1);
@@ -647,7 +365,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     LtPiece x;
     int g = 0;
     bool ok = true;
-    while (ok && lt_next<N>(p, walk, x)) {
+    while (ok && lt_next<N, kLtKeys>(p, walk, x)) {
       for (int k = x.k0; k < x.k1; ++k, ++g) {
         if (!(ok = wait_all(bar_p + (g & 1), (g >> 1) & 1))) break;
         const uint32_t kv = smem_u32(sm + S::kv) + uint32_t(g % kLtStages) * kLtTileBytes;
@@ -694,7 +412,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     auto wait_o = [&](int t) {
       wait(bar_kvfree + (t % kLtStages) * kLtPages + kLtPages - 1, (t / kLtStages) & 1);
     };
-    while (lt_next<N>(p, walk, x)) {
+    while (lt_next<N, kLtKeys>(p, walk, x)) {
       float m[NC];       // reference of each row
       uint64_t l2[NC / 2];  // row sums of this thread's keys, two rows a word
       int lim[NC];  // last key that the row sees
@@ -916,167 +634,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }
 
-// Joins the pieces of the cut tiles.  With weights w_i = 2^(m_i - M), M the
-// largest reference of a piece that saw a key:
-//   out = sum w_i O_i / sum w_i l_i.
-// CTA c's share ends inside at most one tile, whose pieces are c's second
-// partial and the first partials of c + 1 .. last.  A warp joins four rows
-// (a float4 a lane of the partials' layout).  Most tiles have two or three
-// pieces: there warp i of the N warps of blocks (c, *) takes rows 4 (i / 4) ..
-// + 3 of the 128 dims i % 4.  A long sequence alone is one tile with a piece
-// a CTA: there the blocks of all its CTAs take units of four rows and 32 dims,
-// and a block's warps share the pieces.  Both read O without waiting for the
-// weights: what bounds this kernel is the number of reads that wait for one
-// another.
-constexpr int kLtMergeThreads = 256;
-constexpr int kLtMergeWarps = kLtMergeThreads / 32;
-constexpr int kLtFewPieces = 6;
-constexpr int kLtBatch = 8;  // pieces that a warp has under way (64 registers: four blocks an SM)
-
-__device__ __forceinline__ float4 f4(float v) { return make_float4(v, v, v, v); }
-// a * x + y where a is not 0, else y: an O that saw no key was not written
-__device__ __forceinline__ float fma_seen(float a, float x, float y) { return a != 0.f ? fmaf(a, x, y) : y; }
-__device__ __forceinline__ float4 fma_seen(const float4& a, const float4& x, const float4& y) {
-  return make_float4(fma_seen(a.x, x.x, y.x), fma_seen(a.y, x.y, y.y), fma_seen(a.z, x.z, y.z),
-                     fma_seen(a.w, x.w, y.w));
-}
-__device__ __forceinline__ float4 f4_max(const float4& a, const float4& b) {
-  return make_float4(fmaxf(a.x, b.x), fmaxf(a.y, b.y), fmaxf(a.z, b.z), fmaxf(a.w, b.w));
-}
-// references, those of pieces that saw no key put below all others
-__device__ __forceinline__ float4 f4_seen(const float4& m, const float4& l) {
-  constexpr float none = -INFINITY;
-  return make_float4(l.x != 0.f ? m.x : none, l.y != 0.f ? m.y : none, l.z != 0.f ? m.z : none,
-                     l.w != 0.f ? m.w : none);
-}
-__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : ex2(m - M); }
-__device__ __forceinline__ float4 f4_weight(const float4& m, const float4& M) {
-  return make_float4(weight(m.x, M.x), weight(m.y, M.y), weight(m.z, M.z), weight(m.w, M.w));
-}
-__device__ __forceinline__ float4 f4_shfl_xor(const float4& v, int o) {
-  return make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
-                     __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
-}
-
-template <int N>
-__global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(const LatentParams p) {
-  __shared__ float4 s_max[kLtMergeWarps], s_sum[kLtMergeWarps];
-  __shared__ float4 s_w[kLtMergeThreads];  // of a piece; the grid has fewer CTAs
-  __shared__ float4 s_acc[kLtMergeWarps][32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto part = [&](int c, int i) {
-    return p.partials + (i == 0 ? size_t(c) * 2 + 1 : size_t(c + i) * 2) * kLtPartialFloats;
-  };
-  auto m_of = [&](int c, int i, int rq) {
-    return __ldcg(reinterpret_cast<const float4*>(part(c, i) + N * kLatentDim) + rq);
-  };
-  auto l_of = [&](int c, int i, int rq) {
-    return __ldcg(reinterpret_cast<const float4*>(part(c, i) + N * kLatentDim + N) + rq);
-  };
-  auto o_of = [&](int c, int i, int rq, int dq) {  // 32 dims dq, rows 4 rq .. + 3
-    return __ldcg(reinterpret_cast<const float4*>(part(c, i)) + (dq * (N / 4) + rq) * 32 + lane);
-  };
-  // rows 4 rq .. + 3 of a tile, dim 32 dq + lane of each; even lanes store a
-  // pair of dims of the first of two rows, odd lanes of the second
-  auto put = [&](const int4& join, int rq, int dq, const float4& a, const float4& sum) {
-    const float v[4] = {a.x / sum.x, a.y / sum.y, a.z / sum.z, a.w / sum.w};
-#pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[e] : v[e + 1], 1);
-      const int r = rq * 4 + e + (lane & 1);
-      if (r < join.y)
-        *(reinterpret_cast<uint32_t*>(p.out + size_t(join.x + r) * kLatentDim + dq * 32) + (lane >> 1)) =
-            (lane & 1) ? pack_bf16x2(other, v[e + 1]) : pack_bf16x2(v[e], other);
-    }
-  };
-  const int4 own = __ldcg(p.joins + blockIdx.x);
-  const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
-  if (!own_many) {
-    const int c = blockIdx.x, i = blockIdx.y * kLtMergeWarps + warp;
-    const int rq = i / 4, pieces = own.z - c + 1;
-    if (rq * 4 < own.y) {
-      float4 M = f4(-INFINITY), sum = f4(0.f), acc[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = sum;
-#pragma unroll 2
-      for (int k = 0; k < pieces; ++k) {
-        const float4 l = l_of(c, k, rq), m = f4_seen(m_of(c, k, rq), l);
-        float4 o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o_of(c, k, rq, (i & 3) * 4 + e);
-        const float4 up = f4_max(M, m);
-        const float4 old = f4_weight(M, up), w = f4_weight(m, up);
-        M = up;
-        sum = fma_seen(w, l, fma_seen(old, sum, f4(0.f)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fma_seen(w, o[e], fma_seen(old, acc[e], f4(0.f)));
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) put(own, rq, (i & 3) * 4 + e, acc[e], sum);
-    }
-  }
-  for (int which = 0; which < 2; ++which) {
-    const int c = which == 0 ? own.w : own_many ? int(blockIdx.x) : -1;
-    if (c < 0) continue;
-    const int4 join = __ldcg(p.joins + c);
-    const int pieces = join.z - c + 1;
-    if (pieces <= kLtFewPieces) continue;
-    const int team = pieces * gridDim.y;
-    for (int u = (blockIdx.x - c) * gridDim.y + blockIdx.y; u < (join.y + 3) / 4 * 16; u += team) {
-      const int rq = u >> 4, dq = u & 15;
-      float4 o[kLtBatch];
-      auto read = [&](int first) {
-#pragma unroll
-        for (int i = 0; i < kLtBatch; ++i) {
-          const int k = first + i * kLtMergeWarps;
-          if (k < pieces) o[i] = o_of(c, k, rq, dq);
-        }
-      };
-      read(warp);
-      float4 l = f4(0.f), m = f4(-INFINITY);
-      if (tid < pieces) {
-        l = l_of(c, tid, rq);
-        m = f4_seen(m_of(c, tid, rq), l);
-      }
-      float4 M = m;
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) M = f4_max(M, f4_shfl_xor(M, d));
-      if (lane == 0) s_max[warp] = M;
-      __syncthreads();
-      for (int w = 0; w < kLtMergeWarps; ++w) M = f4_max(M, s_max[w]);
-      const float4 w = f4_weight(m, M);
-      s_w[tid] = w;
-      float4 sum = make_float4(w.x * l.x, w.y * l.y, w.z * l.z, w.w * l.w);
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) sum = fma_seen(f4(1.f), f4_shfl_xor(sum, d), sum);
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();
-      float4 acc = f4(0.f);
-      for (int first = warp; first < pieces; first += kLtBatch * kLtMergeWarps) {
-        if (first > warp) read(first);
-#pragma unroll
-        for (int i = 0; i < kLtBatch; ++i) {
-          const int k = first + i * kLtMergeWarps;
-          if (k < pieces) acc = fma_seen(s_w[k], o[i], acc);
-        }
-      }
-      s_acc[warp][lane] = acc;
-      __syncthreads();
-      if (warp == 0) {
-        sum = s_sum[0];
-        for (int i = 1; i < kLtMergeWarps; ++i) {
-          acc = fma_seen(f4(1.f), s_acc[i][lane], acc);
-          sum = fma_seen(f4(1.f), s_sum[i], sum);
-        }
-        put(join, rq, dq, acc, sum);
-      }
-      __syncthreads();
-    }
-  }
-}
-
 template <int N>
 int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams lp) {
   static std::mutex mu;
@@ -1127,7 +684,7 @@ int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams 
   cfg.blockDim = dim3(kLtMergeThreads);
   cfg.dynamicSmemBytes = 0;
   TraceScope ts(ctx.stream, PKV_K_MERGE);
-  cudaLaunchKernelEx(&cfg, pkv_latent_merge_kernel<N>, lp);
+  cudaLaunchKernelEx(&cfg, pkv_latent_merge_kernel<N, false>, lp);
   return ts.done();
 }
 
@@ -1174,6 +731,7 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   const int64_t rows = most * d.num_q_heads;
   const int64_t tiles = (rows + 63) / 64;
   const int64_t per = (rows + tiles - 1) / tiles;
+  if (rows > 64 && !getenv("LT_NOPAIR")) return launch_latent_pair(ctx, a, lp);
   if (per <= 16) return launch_latent<16>(ctx, a, lp);
   if (per <= 32) return launch_latent<32>(ctx, a, lp);
   if (per <= 48) return launch_latent<48>(ctx, a, lp);
