@@ -22,9 +22,11 @@
 //    64 KiB, with 72 KiB of queries and 16 KiB of P all that an SM has, so
 //    each has one buffer, loaded and let go of in slices (K by three chunks of
 //    64 dims, V by 32 keys).
-//  * The leader (rank 0) issues all MMAs.  Each CTA's copies report to its own
-//    barriers; in the other CTA two warps forward them to the leader.  Commits
-//    go to both CTAs.
+//  * The leader (rank 0) issues all MMAs.  Copies of K report to its barriers
+//    from both CTAs; queries and V, whose rows past a sequence's end the CTA
+//    itself has to zero, are forwarded by two warps of the other CTA (400
+//    cycles, which K, in the shortest loop, has not to spare).  Commits go to
+//    both CTAs.
 //  * In S a row is a lane, so the row's reference is one register.  A score
 //    may exceed the reference (the first key's score) by 2^64 without harm to
 //    bf16 or fp32; there is no test a tile, only a flag when one does.  Then
@@ -142,6 +144,19 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
 }
+// A copy into this CTA's shared memory that reports to a barrier of either CTA
+// of the pair (its cluster address), and the announcement of its bytes there.
+__device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                                 uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(cluster_bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_expect_at(uint32_t cluster_bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
   uint32_t u[32];
   tmem_ld32(taddr, u);
@@ -164,17 +179,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
   uint64_t* bar_q = bars;                          // own queries landed
   uint64_t* bar_qfree = bars + 1;                  // the piece's scores are done
-  uint64_t* bar_k = bars + 2;                      // [3] own slice of K landed
+  uint64_t* bar_k = bars + 2;                      // [3] leader: slice of K landed in both CTAs
   uint64_t* bar_kfree = bars + 5;                  // [3] the scores that read it are done
   uint64_t* bar_v = bars + 8;                      // [4] own slice of V landed
   uint64_t* bar_vfree = bars + 12;                 // [4] the P V that reads it is done
   uint64_t* bar_s = bars + 16;                     // [2] scores written
-  uint64_t* bar_p = bars + 18;                     // [2] leader: P written, both CTAs (16 warps)
-  uint64_t* bar_q2 = bars + 20;                    // leader: the other CTA's queries,
-  uint64_t* bar_k2 = bars + 21;                    // [3] slices of K
-  uint64_t* bar_v2 = bars + 24;                    // [4] and of V landed
-  uint64_t* bar_x = bars + 28;                     // [2] leader: scores taken, in a pass for maxima (16 warps)
-  uint64_t* bar_inv = bars + 30;                   // row sums of both CTAs here (16 warps)
+  uint64_t* bar_p = bars + 18;                     // [2 tiles][2 halves] leader: P of 64 keys written (8 warps)
+  uint64_t* bar_x = bars + 22;                     // [2][2] leader: scores taken, in a pass for maxima
+  uint64_t* bar_inv = bars + 26;                   // row sums of both CTAs here (16 warps)
+  uint64_t* bar_q2 = bars + 27;                    // leader: the other CTA's queries landed
+  uint64_t* bar_v2 = bars + 28;                    // [4] leader: the other CTA's slices of V landed
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   volatile int* s_flags = reinterpret_cast<volatile int*>(sm + S::flags);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
@@ -185,10 +199,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   enum { kOverflow = 1, kTimeout = 2 };  // of s_flags
 
   if (tid == 0) {
-    for (int i = 0; i < 31; ++i) {
-      const bool warps = i == 18 || i == 19 || i >= 28;  // bar_p, bar_x, bar_inv
-      mbar_init(bars + i, warps ? 2 * kPrSoftmaxThreads / 32 : 1);
+    for (int i = 0; i < 32; ++i) {
+      uint64_t* b = bars + i;
+      const bool k = b >= bar_k && b < bar_k + kPrSlicesK;
+      mbar_init(b, k ? 2 : b == bar_inv ? 16 : b >= bar_p && b < bar_inv ? 8 : 1);
     }
+
     fence_mbar_init();
     s_flags[0] = s_flags[1] = 0;
   }
@@ -245,6 +261,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     LtPiece x;
     if (warp == 8) {
       // ===== queries and K =====
+      const uint32_t lead_k = cluster_addr(bar_k, 0);
       while (ok && next_piece(walk, x)) {
         for (int pass = round == 0; ok && pass < 2; ++pass) {
           if (lane == 0) {
@@ -275,12 +292,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 if (g > 0) ok = mbar_wait(bar_kfree + d, (g - 1) & 1);
                 if (!ok) break;
                 ++slices;
-                mbar_arrive_expect_tx(bar_k + d, uint32_t(valid) * (kPrSliceK / 4));
+                arrive_expect_at(lead_k + d * 8, uint32_t(valid) * (kPrSliceK / 4));
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   if (id[i] >= 0)
-                    tma_load_4d(sm + S::k + d * kPrSliceK + i * (kPrSliceK / 4), &tm_k, 0, 0, d * 3, 2 * id[i],
-                                bar_k + d);
+                    tma_load_4d_pair(sm + S::k + d * kPrSliceK + i * (kPrSliceK / 4), &tm_k, 0, 0, d * 3, 2 * id[i],
+                                     lead_k + d * 8);
               }
             }
             ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
@@ -332,21 +349,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           ok = wait_all(bar_q, pieces & 1);
           if (ok && rank == 0) ok = wait_all(bar_q2, pieces & 1);
           if (ok && rank == 1 && lane == 0) arrive_at(cluster_addr(bar_q2, 0));
-          for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+          for (int k = x.k0; rank == 0 && ok && k < x.k1; ++k, ++g) {
             // the softmax has taken the scores two tiles before
-            if (rank == 0 && taken[g & 1] >= 0) {
+            if (taken[g & 1] >= 0) {
               const int t = taken[g & 1] >> 1;
-              ok = wait_all((taken[g & 1] & 1 ? bar_p : bar_x) + (t & 1), (t >> 1) & 1);
+              uint64_t* bar = (taken[g & 1] & 1 ? bar_p : bar_x) + (t & 1) * 2;
+              ok = wait_all(bar, (t >> 1) & 1) && wait_all(bar + 1, (t >> 1) & 1);
             }
             taken[g & 1] = pass == 1 ? gv++ * 2 + 1 : g0++ * 2;
             for (int d = 0; ok && d < kPrSlicesK; ++d) {
-              ok = wait_all(bar_k + d, g & 1);
-              if (!ok) break;
-              if (rank == 1) {
-                if (lane == 0) arrive_at(cluster_addr(bar_k2 + d, 0));
-                continue;
-              }
-              if (!(ok = wait_all(bar_k2 + d, g & 1))) break;
+              if (!(ok = wait_all(bar_k + d, g & 1))) break;
               tc_fence_after();
 #pragma unroll
               for (int c = 0; c < 3; ++c)
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                             (d + c + kk) > 0);
               umma_pair_commit(bar_kfree + d);
             }
-            if (!ok || rank == 1) continue;
+            if (!ok) break;
             umma_pair_commit(bar_s + (g & 1));
             if (k + 1 == x.k1) umma_pair_commit(bar_qfree);
           }
@@ -370,37 +382,38 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t av = smem_u32(sm + S::v), ap = smem_u32(sm + S::p);
       while (ok && next_piece(walk, x)) {
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
-            if (rank == 0 && !(ok = wait_all(bar_p + (gv & 1), (gv >> 1) & 1))) break;
-            const int valid = x.L - k * kPrKeys;
-            for (int d = 0; ok && d < kPrSlicesV; ++d) {
-              if (!(ok = wait_all(bar_v + d, gv & 1))) break;
-              if (valid < (d + 1) * 32) {
-                // rows past the sequence hold whatever the pages or the buffer
-                // held: zero them, since their weight of 0 times NaN is NaN
-                for (int r = max(0, valid - d * 32); r < 32; ++r)
-                  *reinterpret_cast<uint4*>(sm + S::v + d * kPrSliceV + (r >> 3) * kPrGroupV + (lane >> 3) * 1024 +
-                                            (r & 7) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-              if (rank == 1) {
-                if (lane == 0) arrive_at(cluster_addr(bar_v2 + d, 0));
-                continue;
-              }
-              if (!(ok = wait_all(bar_v2 + d, gv & 1))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int ks = 0; ks < 2; ++ks) {
-                const int i = d * 2 + ks;  // 16 keys
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  umma_pair(tmem + uint32_t(e) * kPrRows,
-                            smem_desc(av + i * kPrPageV + e * 2048, 1024, kPrGroupV),
-                            smem_desc(ap + (i >> 2) * (kPrOwn * 128) + (i & 3) * 32, 16, 1024), idesc,
-                            (k > x.k0 || i > 0) ? 1u : 0u);
-              }
-              umma_pair_commit(bar_vfree + d);
+          const int valid = x.L - k * kPrKeys;
+          for (int d = 0; ok && d < kPrSlicesV; ++d) {
+            if (rank == 0 && (d & 1) == 0) ok = wait_all(bar_p + (gv & 1) * 2 + (d >> 1), (gv >> 1) & 1);
+            if (ok) ok = wait_all(bar_v + d, gv & 1);
+            if (!ok) break;
+            if (valid < (d + 1) * 32) {
+              // rows past the sequence hold whatever the pages or the buffer
+              // held: zero them, since their weight of 0 times NaN is NaN
+              for (int r = max(0, valid - d * 32); r < 32; ++r)
+                *reinterpret_cast<uint4*>(sm + S::v + d * kPrSliceV + (r >> 3) * kPrGroupV + (lane >> 3) * 1024 +
+                                          (r & 7) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
             }
+            if (rank == 1) {
+              if (lane == 0) arrive_at(cluster_addr(bar_v2 + d, 0));
+              continue;
+            }
+            if (!(ok = wait_all(bar_v2 + d, gv & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+              const int i = d * 2 + ks;  // 16 keys
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                umma_pair(tmem + uint32_t(e) * kPrRows,
+                          smem_desc(av + i * kPrPageV + e * 2048, 1024, kPrGroupV),
+                          smem_desc(ap + (i >> 2) * (kPrOwn * 128) + (i & 3) * 32, 16, 1024), idesc,
+                          (k > x.k0 || i > 0) ? 1u : 0u);
+            }
+            umma_pair_commit(bar_vfree + d);
+          }
         }
       }
     } else {
@@ -413,7 +426,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok) ok = wait_all(bar, parity);
       };
-      const uint32_t lead_p = cluster_addr(bar_p, 0), lead_x = cluster_addr(bar_x, 0);  // + 8 for odd tiles
+      const int half = quad >> 1;                                 // its keys' half of a tile
+      const uint32_t lead_p = cluster_addr(bar_p + half, 0), lead_x = cluster_addr(bar_x + half, 0);  // + 16: odd tiles
       bool over = false;
       while (next_piece(walk, x)) {
         const int lim = x.L - x.n + min(x.n - 1, lt_token(p, x.local_row + rank * kPrOwn + row));  // last key it sees
@@ -464,8 +478,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               float lo, hi;
               f2_split(sum, lo, hi);
               l += lo + hi;
-              // P's buffer is free once the P V before is done
-              if (gv > 0) wait(bar_vfree + kPrSlicesV - 1, (gv - 1) & 1);
+              // P's half of the buffer is free once the P V before is through
+              // with its keys: P V of the next tile starts on the first half
+              // while the second is still written
+              if (gv > 0) wait(bar_vfree + half * 2 + 1, (gv - 1) & 1);
               ++gv;
               uint8_t* prow = sm + S::p + (key0 >> 6) * (kPrOwn * 128) + row * 128;
 #pragma unroll
@@ -476,7 +492,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (ok && lane == 0) arrive_at(pass == 1 ? lead_p + ((gv - 1) & 1) * 8 : lead_x + (g0 & 1) * 8);
+            if (ok && lane == 0) arrive_at(pass == 1 ? lead_p + ((gv - 1) & 1) * 16 : lead_x + (g0 & 1) * 16);
             if (pass == 0) ++g0;
           }
           if (pass == 0) {
@@ -581,7 +597,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint64_t limit = ok ? kLandLimitNs : kDrainLimitNs;
     const int n = warp == 8 ? kPrSlicesK : kPrSlicesV;
     uint64_t* bar = warp == 8 ? bar_k : bar_v;
-    for (int i = max(0, slices - n); i < slices; ++i) mbar_wait(bar + i % n, (i / n) & 1, limit);
+    if (warp == 11 || rank == 0)  // (the leader's barriers count both CTAs' copies of K)
+      for (int i = max(0, slices - n); i < slices; ++i) mbar_wait(bar + i % n, (i / n) & 1, limit);
     if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);  // (the V loader counts no pieces)
   }
   if (warp == 9 && rank == 0 && g > 0) mbar_wait(bar_s + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
