@@ -22,11 +22,11 @@
 //    64 KiB, with 72 KiB of queries and 16 KiB of P all that an SM has, so
 //    each has one buffer, loaded and let go of in slices (K by three chunks of
 //    64 dims, V by 32 keys).
-//  * The leader (rank 0) issues all MMAs.  Copies of K report to its barriers
-//    from both CTAs; queries and V, whose rows past a sequence's end the CTA
-//    itself has to zero, are forwarded by two warps of the other CTA (400
-//    cycles, which K, in the shortest loop, has not to spare).  Commits go to
-//    both CTAs.
+//  * The leader (rank 0) issues all MMAs.  Copies of K and V report to its
+//    barriers from both CTAs (a warp that forwards them costs 400 cycles, in
+//    the loops of load and use that set the pace), but for a sequence's last
+//    tile, whose rows past the end of V the CTA itself has to zero.  Commits go
+//    to both CTAs.
 //  * In S a row is a lane, so the row's reference is one register.  A score
 //    may exceed the reference (the first key's score) by 2^64 without harm to
 //    bf16 or fp32; there is no test a tile, only a flag when one does.  Then
@@ -181,14 +181,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* bar_qfree = bars + 1;                  // the piece's scores are done
   uint64_t* bar_k = bars + 2;                      // [3] leader: slice of K landed in both CTAs
   uint64_t* bar_kfree = bars + 5;                  // [3] the scores that read it are done
-  uint64_t* bar_v = bars + 8;                      // [4] own slice of V landed
+  uint64_t* bar_v = bars + 8;                      // [4] leader: slice of V landed in both CTAs
   uint64_t* bar_vfree = bars + 12;                 // [4] the P V that reads it is done
   uint64_t* bar_s = bars + 16;                     // [2] scores written
   uint64_t* bar_p = bars + 18;                     // [2 tiles][2 halves] leader: P of 64 keys written (8 warps)
   uint64_t* bar_x = bars + 22;                     // [2][2] leader: scores taken, in a pass for maxima
   uint64_t* bar_inv = bars + 26;                   // row sums of both CTAs here (16 warps)
   uint64_t* bar_q2 = bars + 27;                    // leader: the other CTA's queries landed
-  uint64_t* bar_v2 = bars + 28;                    // [4] leader: the other CTA's slices of V landed
+  uint64_t* bar_tail = bars + 28;                  // [4] own slice of V landed, of a sequence's last tile
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   volatile int* s_flags = reinterpret_cast<volatile int*>(sm + S::flags);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 32; ++i) {
       uint64_t* b = bars + i;
-      const bool k = b >= bar_k && b < bar_k + kPrSlicesK;
-      mbar_init(b, k ? 2 : b == bar_inv ? 16 : b >= bar_p && b < bar_inv ? 8 : 1);
+      const bool both = (b >= bar_k && b < bar_k + kPrSlicesK) || (b >= bar_v && b < bar_v + kPrSlicesV);
+      mbar_init(b, both ? 2 : b == bar_inv ? 16 : b >= bar_p && b < bar_inv ? 8 : 1);
     }
 
     fence_mbar_init();
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // tiles, gv those with a P V.  A second round (some score exceeded the
   // reference by too much) walks every piece twice, for maxima first.
   int g = 0, gv = 0, pieces = 0, wholes = 0;
-  int slices = 0;  // that a loader has sent
+  int slices = 0, tails = 0;  // that a loader has sent; slices of last tiles
   int g0 = 0, taken[2] = {-1, -1};  // tiles of passes for maxima; of the tile in each score buffer, count and kind
   bool ok = true;
   for (int round = 0; round < 2; ++round) {
@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 11) {
       // ===== V: the 128 keys' own dims =====
+      const uint32_t lead_v = cluster_addr(bar_v, 0);
       while (ok && next_piece(walk, x)) {
         int ids = page_id(x, x.k0 * 8 + lane), next = page_id(x, x.k0 * 8 + 32 + lane);
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
@@ -320,17 +321,25 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             ids = next;
             next = page_id(x, (k + 4) * 8 + lane);
           }
+          // the sequence's last tile, if it ends short, goes to barriers of
+          // this CTA's own: its value warp zeroes the rows behind the end first
+          const bool tail = x.L - k * kPrKeys < kPrKeys;
           for (int d = 0; ok && d < kPrSlicesV; ++d) {
             const int id0 = __shfl_sync(0xffffffffu, ids, in_group * 8 + d * 2);
             const int id1 = __shfl_sync(0xffffffffu, ids, in_group * 8 + d * 2 + 1);
             if (lane == 0) {
               if (gv > 0) ok = mbar_wait(bar_vfree + d, (gv - 1) & 1);
               if (ok) {
-                ++slices;
-                mbar_arrive_expect_tx(bar_v + d, uint32_t((id0 >= 0) + (id1 >= 0)) * kPrPageV);
+                const uint32_t bar = tail ? smem_u32(bar_tail + d) : lead_v + d * 8;
+                arrive_expect_at(tail ? cluster_addr(bar_tail + d, rank) : bar,
+                                 uint32_t((id0 >= 0) + (id1 >= 0)) * kPrPageV);
                 uint8_t* dst = sm + S::v + d * kPrSliceV;
-                if (id0 >= 0) tma_load_4d(dst, &tm_v, 0, 0, rank * 4, 2 * id0, bar_v + d);
-                if (id1 >= 0) tma_load_4d(dst + kPrPageV, &tm_v, 0, 0, rank * 4, 2 * id1, bar_v + d);
+                if (id0 >= 0) tma_load_4d_pair(dst, &tm_v, 0, 0, rank * 4, 2 * id0, bar);
+                if (id1 >= 0) tma_load_4d_pair(dst + kPrPageV, &tm_v, 0, 0, rank * 4, 2 * id1, bar);
+                if (tail)
+                  ++tails;
+                else
+                  ++slices;
               }
             }
             ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
@@ -384,23 +393,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
           const int valid = x.L - k * kPrKeys;
           for (int d = 0; ok && d < kPrSlicesV; ++d) {
-            if (rank == 0 && (d & 1) == 0) ok = wait_all(bar_p + (gv & 1) * 2 + (d >> 1), (gv >> 1) & 1);
-            if (ok) ok = wait_all(bar_v + d, gv & 1);
-            if (!ok) break;
-            if (valid < (d + 1) * 32) {
+            if (valid < kPrKeys) {
               // rows past the sequence hold whatever the pages or the buffer
               // held: zero them, since their weight of 0 times NaN is NaN
+              if (!(ok = wait_all(bar_tail + d, (tails / kPrSlicesV) & 1))) break;
+              ++tails;
               for (int r = max(0, valid - d * 32); r < 32; ++r)
                 *reinterpret_cast<uint4*>(sm + S::v + d * kPrSliceV + (r >> 3) * kPrGroupV + (lane >> 3) * 1024 +
                                           (r & 7) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
               fence_proxy_async_smem();
               __syncwarp();
+              if (lane == 0) arrive_at(cluster_addr(bar_v + d, 0));
             }
-            if (rank == 1) {
-              if (lane == 0) arrive_at(cluster_addr(bar_v2 + d, 0));
-              continue;
-            }
-            if (!(ok = wait_all(bar_v2 + d, gv & 1))) break;
+            if (rank == 1) continue;
+            if ((d & 1) == 0) ok = wait_all(bar_p + (gv & 1) * 2 + (d >> 1), (gv >> 1) & 1);
+            if (ok) ok = wait_all(bar_v + d, gv & 1);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -596,9 +604,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if ((warp == 8 || warp == 11) && lane == 0) {
     const uint64_t limit = ok ? kLandLimitNs : kDrainLimitNs;
     const int n = warp == 8 ? kPrSlicesK : kPrSlicesV;
+    const int sent = warp == 8 ? slices : slices + tails;  // phases of the leader's barriers
     uint64_t* bar = warp == 8 ? bar_k : bar_v;
-    if (warp == 11 || rank == 0)  // (the leader's barriers count both CTAs' copies of K)
-      for (int i = max(0, slices - n); i < slices; ++i) mbar_wait(bar + i % n, (i / n) & 1, limit);
+    if (rank == 0)  // they count both CTAs' copies
+      for (int i = max(0, sent - n); i < sent; ++i) mbar_wait(bar + i % n, (i / n) & 1, limit);
+    for (int i = max(0, tails - n); i < tails; ++i) mbar_wait(bar_tail + i % n, (i / n) & 1, limit);
     if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);  // (the V loader counts no pieces)
   }
   if (warp == 9 && rank == 0 && g > 0) mbar_wait(bar_s + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
