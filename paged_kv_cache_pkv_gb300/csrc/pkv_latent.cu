@@ -245,15 +245,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     int landing = 0;        // cache tiles whose copies were issued
     bool ok = true;
     while (ok && lt_next<N, kLtKeys>(p, walk, x)) {
-      if (lane == 0) {
-        if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
-        if (ok) {
-          mbar_arrive_expect_tx(bar_q, kLtChunks * N * 128);
-          if (!(kDropFirstCopy && pieces == 0)) tma_load_3d(sm + S::q, &tm_q, 0, x.row0, 0, bar_q);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-      ++pieces;
       const int32_t* table = p.block_tables + int64_t(x.b) * p.max_blocks;
       const int pages = (x.L + kPage - 1) / kPage;
       // lane l: page l of a group of eight cache tiles, read a group ahead.
@@ -269,7 +260,18 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         return id;
       };
+      // (before the wait below: the reads take longer than what is left of the
+      // piece before)
       int ids = group_id(x.k0), next = group_id(x.k0 + 8);
+      if (lane == 0) {
+        if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
+        if (ok) {
+          mbar_arrive_expect_tx(bar_q, kLtChunks * N * 128);
+          if (!(kDropFirstCopy && pieces == 0)) tma_load_3d(sm + S::q, &tm_q, 0, x.row0, 0, bar_q);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      ++pieces;
       for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
         const int in_group = (k - x.k0) & 7;
         if (k > x.k0 && in_group == 0) {

@@ -264,6 +264,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t lead_k = cluster_addr(bar_k, 0);
       while (ok && next_piece(walk, x)) {
         for (int pass = round == 0; ok && pass < 2; ++pass) {
+          // (before the wait below: the reads take longer than what is left of
+          // the piece before)
+          int ids = page_id(x, x.k0 * 8 + lane), next = page_id(x, x.k0 * 8 + 32 + lane);
           if (lane == 0) {
             if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
             if (ok) {
@@ -274,7 +277,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
           ++pieces;
-          int ids = page_id(x, x.k0 * 8 + lane), next = page_id(x, x.k0 * 8 + 32 + lane);
           for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
             const int in_group = (k - x.k0) & 3;
             if (k > x.k0 && in_group == 0) {
@@ -392,20 +394,23 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       while (ok && next_piece(walk, x)) {
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
           const int valid = x.L - k * kPrKeys;
-          for (int d = 0; ok && d < kPrSlicesV; ++d) {
-            if (valid < kPrKeys) {
-              // rows past the sequence hold whatever the pages or the buffer
-              // held: zero them, since their weight of 0 times NaN is NaN
+          if (valid < kPrKeys) {
+            // rows past the sequence hold whatever the pages or the buffer
+            // held: zero them, since their weight of 0 times NaN is NaN
+            for (int d = 0; ok && d < kPrSlicesV; ++d, ++tails) {
               if (!(ok = wait_all(bar_tail + d, (tails / kPrSlicesV) & 1))) break;
-              ++tails;
-              for (int r = max(0, valid - d * 32); r < 32; ++r)
+              const int first = max(0, valid - d * 32);
+              for (int r = first; r < 32; ++r)
                 *reinterpret_cast<uint4*>(sm + S::v + d * kPrSliceV + (r >> 3) * kPrGroupV + (lane >> 3) * 1024 +
                                           (r & 7) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-              fence_proxy_async_smem();
+              if (first < 32) fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) arrive_at(cluster_addr(bar_v + d, 0));
             }
-            if (rank == 1) continue;
+          }
+          if (rank == 1) continue;
+#pragma unroll 1
+          for (int d = 0; ok && d < kPrSlicesV; ++d) {
             if ((d & 1) == 0) ok = wait_all(bar_p + (gv & 1) * 2 + (d >> 1), (gv >> 1) & 1);
             if (ok) ok = wait_all(bar_v + d, gv & 1);
             if (!ok) break;
@@ -547,39 +552,57 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         if (ok) {
           tc_fence_after();
-          const int r0 = wg * kPrOwn;  // this warpgroup's rows of the tile
+          // lane: dim rank * 256 + e * 128 + quad * 32 + lane; column: row
+          if (!whole) {
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            const int e = i >> 1, r1 = r0 + (i & 1) * 32;
-            if (r1 >= x.rows) continue;
-            float o[32];  // lane: dim rank * 256 + e * 128 + quad * 32 + lane; column: row
-            tmem_ld32f(tmem + uint32_t(e * kPrRows + r1) + lane_off, o);
-            if (whole) {
-              uint32_t* to = reinterpret_cast<uint32_t*>(p.out + size_t(x.row0 + r1 + (lane & 1)) * kLatentDim +
-                                                         rank * 256 + e * 128 + quad * 32) +
-                             (lane >> 1);
-#pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const float4 inv = *reinterpret_cast<const float4*>(s_inv + r1 + c);
-                const float v[4] = {o[c] * inv.x, o[c + 1] * inv.y, o[c + 2] * inv.z, o[c + 3] * inv.w};
-#pragma unroll
-                for (int h = 0; h < 4; h += 2) {
-                  // even lanes take the first row's pair of dims, odd lanes the second's
-                  const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[h] : v[h + 1], 1);
-                  if (r1 + c + h + (lane & 1) < x.rows)
-                    to[(c + h) * (kLatentDim / 2)] =
-                        (lane & 1) ? pack_bf16x2(other, v[h + 1]) : pack_bf16x2(v[h], other);
-                }
-              }
-            } else {
+            for (int i = 0; i < 4; ++i) {
+              const int e = i >> 1, r1 = wg * kPrOwn + (i & 1) * 32;
+              if (r1 >= x.rows) continue;
+              float o[32];
+              tmem_ld32f(tmem + uint32_t(e * kPrRows + r1) + lane_off, o);
               float4* to = reinterpret_cast<float4*>(part) + ((e * 4 + quad) * (kPrRows / 4) + r1 / 4) * 32 + lane;
 #pragma unroll
               for (int c = 0; c < 32; c += 4)
                 if (r1 + c < x.rows) to[c * 8] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
             }
           }
-          tc_fence_before();  // read before the next piece's first P V overwrites it
         }
+        if (whole) {
+          // 32 rows at a time through P's buffer (the last P V is done with
+          // it), so that a row's 512 bytes leave in one piece: 2-byte or
+          // paired stores straight from the columns take 6000 cycles a tile.
+          uint8_t* stage = sm + S::p;
+          const int e = wg;
+#pragma unroll 1
+          for (int r1 = 0; r1 < x.rows; r1 += 32) {
+            float o[32];
+            tmem_ld32f(tmem + uint32_t(e * kPrRows + r1) + lane_off, o);
+            // even lanes take the first row's pair of dims, odd lanes the
+            // second's; odd rows swap their 64-byte halves, for the banks
+            uint8_t* to = stage + (lane & 1) * 512 + ((e * 256 + quad * 64 + (lane >> 1) * 4) ^ ((lane & 1) << 6));
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const float4 inv = *reinterpret_cast<const float4*>(s_inv + r1 + c);
+              const float v[4] = {o[c] * inv.x, o[c + 1] * inv.y, o[c + 2] * inv.z, o[c + 3] * inv.w};
+#pragma unroll
+              for (int h = 0; h < 4; h += 2) {
+                const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[h] : v[h + 1], 1);
+                *reinterpret_cast<uint32_t*>(to + (c + h) * 512) =
+                    (lane & 1) ? pack_bf16x2(other, v[h + 1]) : pack_bf16x2(v[h], other);
+              }
+            }
+            named_sync(1, kPrSoftmaxThreads);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int r = j * 8 + warp;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 512 + ((lane * 16) ^ ((r & 1) << 6)));
+              if (ok && r1 + r < x.rows)
+                *(reinterpret_cast<uint4*>(p.out + size_t(x.row0 + r1 + r) * kLatentDim + rank * 256) + lane) = v;
+            }
+            named_sync(1, kPrSoftmaxThreads);
+          }
+        }
+        tc_fence_before();  // read before the next piece's first P V overwrites it
       }
       if (over) s_flags[0] = kOverflow;  // (a plain store: every writer's value)
     }
