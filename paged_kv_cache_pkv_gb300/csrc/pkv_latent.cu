@@ -50,7 +50,6 @@
 //    PKV_STATUS_TIMEOUT, what is in flight lands, TMEM is freed.
 #include <algorithm>
 #include <mutex>
-#include <cstdlib>
 
 #include "pkv_internal.h"
 #include "pkv_latent.cuh"
@@ -71,6 +70,7 @@ constexpr int kLtStages = 2;
 // 64 keys of 128 bytes, at the same strides, so P needs no memory of its own
 // and never waits for the P V before it.
 constexpr uint32_t kLtChunkP = (kLtChunks - 1) * 1024;
+constexpr int kLtPairTokens = 2048;  // table width in tokens from which pairs of CTAs take over
 constexpr float kLtTau = 20.0f;  // log2 of how far a score may exceed the reference
 
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -701,7 +701,7 @@ size_t latent_workspace_bytes(const DeviceInfo& dev) {
 int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   const pkv_desc& d = a.desc;
   // rows are int32 on the device, and so are the tensor map's coordinates
-  if (int64_t(a.num_tokens) * d.num_q_heads >= (int64_t(1) << 31) - 64) return PKV_ERR_RANGE;
+  if (int64_t(a.num_tokens) * d.num_q_heads >= (int64_t(1) << 31) - 256) return PKV_ERR_RANGE;
   if (ctx.dev->sm_count > kLtMergeThreads) return PKV_ERR_LAUNCH;  // the merge holds a piece a thread
   if (int64_t(d.num_blocks) * 2 >= (int64_t(1) << 31)) return PKV_ERR_RANGE;
   // the plan multiplies the batch's weight by the CTAs in 64 bits
@@ -727,13 +727,19 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   lp.max_blocks = d.max_blocks_per_seq;
   lp.num_blocks = d.num_blocks;
   lp.qscale = a.scale * 1.4426950408889634f;
-  // Rows a tile: the least multiple of 16 that cuts the longest sequence's
-  // rows into as few tiles as 64 would.
   const int64_t most = a.max_query_len > 0 && a.max_query_len < a.num_tokens ? a.max_query_len : a.num_tokens;
   const int64_t rows = most * d.num_q_heads;
+  // More than 64 rows a sequence go to pairs of CTAs where sequences may be
+  // long: 128 heads, 64 sequences of 512-4096 tokens 68 us against 78, two
+  // 1023-token chunks over 1536-3584 tokens 583 against 930.  A pair takes
+  // longer to start and to end a tile (128 heads, 256 sequences of 100-400
+  // tokens: 66 us against 60; a 1023-token prompt of 16 heads: 61 against 48),
+  // and how long sequences are is known here only as the tables' width.
+  if (rows > 64 && int64_t(d.max_blocks_per_seq) * kPage >= kLtPairTokens) return launch_latent_pair(ctx, a, lp);
+  // Rows a tile: the least multiple of 16 that cuts the longest sequence's
+  // rows into as few tiles as 64 would.
   const int64_t tiles = (rows + 63) / 64;
   const int64_t per = (rows + tiles - 1) / tiles;
-  if (rows > 64 && !getenv("LT_NOPAIR")) return launch_latent_pair(ctx, a, lp);
   if (per <= 16) return launch_latent<16>(ctx, a, lp);
   if (per <= 32) return launch_latent<32>(ctx, a, lp);
   if (per <= 48) return launch_latent<48>(ctx, a, lp);

@@ -63,8 +63,8 @@ struct PrSmem {
   static constexpr uint32_t v = k + kPrSlicesK * kPrSliceK;
   static constexpr uint32_t q = v + kPrSlicesV * kPrSliceV;  // [9][64 rows][128 B]
   static constexpr uint32_t p = q + kLtChunks * kPrOwn * 128;  // [2 halves][64 rows][64 keys]
-  static constexpr uint32_t bars = p + 2 * kPrOwn * 128;       // 32 x 8
-  static constexpr uint32_t tmem = bars + 256;
+  static constexpr uint32_t bars = p + 2 * kPrOwn * 128;       // 33 x 8
+  static constexpr uint32_t tmem = bars + 272;
   static constexpr uint32_t flags = tmem + 8;                  // own, the other CTA's
   static constexpr uint32_t share = tmem + 16;                 // 12 ints
   static constexpr uint32_t inv = share + 48;                  // [128] 1 / row sums
@@ -132,8 +132,10 @@ __device__ __forceinline__ bool wait_published(uint64_t* bar, uint32_t parity) {
     if (global_ns() - t0 > kWaitLimitNs) return false;
   return true;
 }
+// Both CTAs are here.  (No fence: barriers' initial values have one of their
+// own, and nothing else is handed over this way.)
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -189,6 +191,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* bar_inv = bars + 26;                   // row sums of both CTAs here (16 warps)
   uint64_t* bar_q2 = bars + 27;                    // leader: the other CTA's queries landed
   uint64_t* bar_tail = bars + 28;                  // [4] own slice of V landed, of a sequence's last tile
+  uint64_t* bar_round = bars + 32;                 // the other CTA's flags are here
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   volatile int* s_flags = reinterpret_cast<volatile int*>(sm + S::flags);
   int* s_share = reinterpret_cast<int*>(sm + S::share);
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   enum { kOverflow = 1, kTimeout = 2 };  // of s_flags
 
   if (tid == 0) {
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 33; ++i) {
       uint64_t* b = bars + i;
       const bool both = (b >= bar_k && b < bar_k + kPrSlicesK) || (b >= bar_v && b < bar_v + kPrSlicesV);
       mbar_init(b, both ? 2 : b == bar_inv ? 16 : b >= bar_p && b < bar_inv ? 8 : 1);
@@ -606,20 +609,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       if (over) s_flags[0] = kOverflow;  // (a plain store: every writer's value)
     }
-    // Both CTAs agree on whether there is a second round.
+    // Both CTAs agree on whether there is a second round.  (One thread of a
+    // warp that stores nothing to global memory tells the other CTA: a release
+    // over every thread's stores would wait for the results to be written.)
     const bool failed = __syncthreads_or(!ok) != 0;
-    if (tid == 0) {
+    if (warp == 9 && lane == 0) {
       const int mine = failed ? kTimeout : int(s_flags[0]);
       s_flags[0] = mine;
       asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(const_cast<int*>(s_flags + 1), rank ^ 1)),
                    "r"(mine)
                    : "memory");
+      arrive_publish(cluster_addr(bar_round, rank ^ 1));
       if (failed) flag_status(p.status, PKV_STATUS_TIMEOUT);
+      if (!wait_published(bar_round, round)) s_flags[0] = kTimeout;
     }
     __syncthreads();
-    cluster_sync();
-    const int both = s_flags[0] | s_flags[1];
-    if (both != kOverflow) break;
+    if ((s_flags[0] | s_flags[1]) != kOverflow) break;
   }
 
   // What is still under way lands before shared memory and TMEM are let go of:
@@ -632,7 +637,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     if (rank == 0)  // they count both CTAs' copies
       for (int i = max(0, sent - n); i < sent; ++i) mbar_wait(bar + i % n, (i / n) & 1, limit);
     for (int i = max(0, tails - n); i < tails; ++i) mbar_wait(bar_tail + i % n, (i / n) & 1, limit);
-    if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);  // (the V loader counts no pieces)
+    if (warp == 8 && pieces > 0) {
+      mbar_wait(bar_q, (pieces - 1) & 1, limit);
+      mbar_wait(bar_qfree, (pieces - 1) & 1, limit);  // (commits that reach this CTA)
+      for (int d = 0; d < n; ++d) mbar_wait(bar_kfree + d, (g - 1) & 1, limit);
+    }
   }
   if (warp == 9 && rank == 0 && g > 0) mbar_wait(bar_s + ((g - 1) & 1), ((g - 1) >> 1) & 1, kLandLimitNs);
   if (warp == 10 && rank == 0 && gv > 0) mbar_wait(bar_vfree + kPrSlicesV - 1, (gv - 1) & 1, kLandLimitNs);

@@ -23,9 +23,9 @@ def cuda(a, dtype=None):
 class Case:
     """A batch over a shuffled pool.  Whatever no query may see is NaN: rows
     past each sequence's end and whole unused pages; unused table entries
-    name no page."""
+    name no page.  Tables ``width`` pages wide or more."""
 
-    def __init__(self, lens, q_lens, H, seed=0, extra_tokens=0, spread=1.0):
+    def __init__(self, lens, q_lens, H, seed=0, extra_tokens=0, spread=1.0, width=1):
         rng = np.random.default_rng(seed)
         gen = torch.Generator(device="cuda")
         gen.manual_seed(seed)
@@ -33,7 +33,7 @@ class Case:
         need = -(-lens // 16)
         nb = int(need.sum()) + 3
         perm = rng.permutation(nb)
-        self.tables = np.full((len(lens), max(1, int(need.max()))), nb, np.int32)
+        self.tables = np.full((len(lens), max(width, int(need.max()))), nb, np.int32)
         at = 0
         for b, n in enumerate(need):
             self.tables[b, :n] = perm[at:at + n]
@@ -85,10 +85,15 @@ CASES = {
 }
 
 
+# Wide tables put sequences of more than 64 rows on pairs of CTAs.
+WIDE = 128
+
+
+@pytest.mark.parametrize("width", [1, WIDE])
 @pytest.mark.parametrize("name", CASES)
-def test_attend_latent(pkvlib, name):
+def test_attend_latent(pkvlib, name, width):
     lens, q_lens, H = CASES[name]
-    c = Case(lens, q_lens, H, seed=len(name))
+    c = Case(lens, q_lens, H, seed=len(name), width=width)
     out = torch.full((c.q.shape[0], H, 512), float("nan"), device="cuda", dtype=torch.bfloat16)
     got = pkv.attend_latent(*c.args(), out=out, max_query_len=max(q_lens))
     assert got is out
@@ -100,10 +105,12 @@ def test_attend_latent(pkvlib, name):
     c.check(pkv.attend_latent(*c.args()), want)  # other tiles where no bound is given
 
 
-def test_rising_scores_move_the_reference(pkvlib):
+@pytest.mark.parametrize("H,width", [(20, 1), (96, WIDE), (128, WIDE)])
+def test_rising_scores_move_the_reference(pkvlib, H, width):
     """Keys that score higher and higher along the sequence: every tile raises
-    the reference and rescales what was summed before."""
-    c = Case([1000, 130], [1, 3], 20, seed=3)
+    the reference and rescales what was summed before (one CTA), or the share
+    is done again with the maxima known (pairs)."""
+    c = Case([1000, 130, 40], [1, 3, 1], H, seed=3, width=width)
     u = torch.randn(576, device="cuda")
     u /= u.norm()
     c.q[:] = (u * 30).to(torch.bfloat16)
@@ -113,9 +120,10 @@ def test_rising_scores_move_the_reference(pkvlib):
     c.check(pkv.attend_latent(*c.args()))
 
 
-def test_falling_and_far_negative_scores(pkvlib):
+@pytest.mark.parametrize("H,width", [(16, 1), (128, WIDE)])
+def test_falling_and_far_negative_scores(pkvlib, H, width):
     """The first key dominates by far; the rest underflow."""
-    c = Case([700], [1], 16, seed=4)
+    c = Case([700], [1], H, seed=4, width=width)
     u = torch.randn(576, device="cuda")
     u /= u.norm()
     c.q[:] = (u * 60).to(torch.bfloat16)
@@ -124,16 +132,18 @@ def test_falling_and_far_negative_scores(pkvlib):
     c.check(pkv.attend_latent(*c.args()))
 
 
-def test_rows_behind_the_last_sequence_are_left(pkvlib):
-    c = Case([100, 40], [1, 2], 12, seed=5, extra_tokens=5)
-    out = torch.full((8, 12, 512), 7.0, device="cuda", dtype=torch.bfloat16)
+@pytest.mark.parametrize("H,width", [(12, 1), (72, WIDE)])
+def test_rows_behind_the_last_sequence_are_left(pkvlib, H, width):
+    c = Case([100, 40], [1, 2], H, seed=5, extra_tokens=5, width=width)
+    out = torch.full((8, H, 512), 7.0, device="cuda", dtype=torch.bfloat16)
     pkv.attend_latent(*c.args(), out=out)
     assert bool((out[3:] == 7.0).all())
     c.check(out)
 
 
-def test_nan_query_stays_in_its_row(pkvlib):
-    c = Case([300], [4], 8, seed=6)
+@pytest.mark.parametrize("H,width", [(8, 1), (24, WIDE)])
+def test_nan_query_stays_in_its_row(pkvlib, H, width):
+    c = Case([300], [4], H, seed=6, width=width)
     c.q[1, 3, 5] = float("nan")
     out = pkv.attend_latent(*c.args())
     assert bool(torch.isnan(out[1, 3]).all())
@@ -150,9 +160,10 @@ def test_shared_pages_and_long_tables(pkvlib):
     c.check(pkv.attend_latent(*c.args()))
 
 
-def test_inconsistent_batches_are_flagged(pkvlib):
+@pytest.mark.parametrize("H,width", [(16, 1), (80, WIDE)])
+def test_inconsistent_batches_are_flagged(pkvlib, H, width):
     pkv.get_last_error()
-    c = Case([100, 50, 20], [1, 1, 1], 16, seed=8)
+    c = Case([100, 50, 20], [1, 1, 1], H, seed=8, width=width)
     good = c.expect()
     tables = c.tables.copy()
     tables[1, 2] = c.pool.shape[0]  # names no page
@@ -163,7 +174,7 @@ def test_inconsistent_batches_are_flagged(pkvlib):
     assert (np.abs(got - good[0])[[0, 2]] <= good[1][[0, 2]]).all()
     short = c.lens.copy()
     short[1] = 0  # fewer tokens than queries
-    out = torch.full((3, 16, 512), 7.0, device="cuda", dtype=torch.bfloat16)
+    out = torch.full((3, H, 512), 7.0, device="cuda", dtype=torch.bfloat16)
     pkv.attend_latent(q, pool, cuda(c.tables), cuda(short), qsl, scale, out=out)
     assert pkv.get_last_error() == pkv.STATUS_BAD_QUERY
     assert bool((out[1] == 7.0).all())
@@ -172,7 +183,8 @@ def test_inconsistent_batches_are_flagged(pkvlib):
 
 
 def test_two_graphs_share_a_workspace_and_a_stream_of_its_own(pkvlib):
-    cases = [Case([3000, 200], [1, 1], 16, seed=9), Case([70, 2500, 5], [3, 1, 1], 64, seed=10)]
+    cases = [Case([3000, 200], [1, 1], 16, seed=9), Case([70, 2500, 5], [3, 1, 1], 64, seed=10),
+             Case([900, 2100], [1, 1], 128, seed=11)]
     size = max(pkv.workspace_size_latent(pkv.make_latent_desc(c.pool, c.H, c.tables.shape[1]), len(c.lens), c.q.shape[0])
                for c in cases)
     ws = torch.full((size,), 255, device="cuda", dtype=torch.uint8)
@@ -256,3 +268,32 @@ def test_rotated_append_then_attend(pkvlib):
                  b.query_start_loc, b.scale, 32, 8, 16)
     err = np.abs(bf16_to_f64(bits(out)) - ref)
     assert err.max() <= MAX_ABS_TOL and err.mean() <= MEAN_ABS_TOL
+
+
+@pytest.mark.parametrize("H,width", [(5, 1), (64, 1), (128, WIDE)])
+def test_the_same_bits_many_times(pkvlib, H, width):
+    """Calls right behind each other on one workspace: nothing of a result may
+    depend on when a CTA or a copy was ready."""
+    c = Case([2300, 17, 640, 1, 64, 1025, 333], [1, 2, 1, 1, 3, 1, 1], H, seed=12, width=width)
+    args = c.args()
+    ws = torch.zeros(pkv.workspace_size_latent(pkv.make_latent_desc(c.pool, H, c.tables.shape[1]), 7, c.q.shape[0]),
+                     dtype=torch.uint8, device="cuda")
+    outs = [pkv.attend_latent(*args, workspace=ws, max_query_len=3) for _ in range(200)]
+    c.check(outs[0])
+    assert all(torch.equal(outs[0].view(torch.int16), o.view(torch.int16)) for o in outs)
+    assert pkv.get_last_error() == 0
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(pkvlib, seed):
+    rng = np.random.default_rng(100 + seed)
+    B, H = int(rng.integers(1, 12)), int(rng.integers(1, 257))
+    lens = np.round(np.exp(rng.uniform(0, np.log(3000), B))).astype(int)
+    most = int(rng.choice([1, 1, 4, 60]))
+    q_lens = np.minimum(rng.integers(0 if B > 1 else 1, most, size=B, endpoint=True), lens)
+    if q_lens.sum() == 0:
+        q_lens[0] = 1
+    c = Case(lens, q_lens, H, seed=seed, width=int(rng.choice([1, WIDE])))
+    bound = int(rng.choice([0, 1, int(q_lens.max()), 1000]))  # a wrong bound changes tiles, not results
+    c.check(pkv.attend_latent(*c.args(), max_query_len=bound))
+    assert pkv.get_last_error() == 0
