@@ -242,9 +242,10 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const La
 }
 
 // Blocks over tokens, and over the rows of a token while there are few
-// tokens: as many as fill the SMs about `resident` deep.
+// tokens: as many as are resident at once (nine of 128 threads an SM; 16 a SM
+// took 34.2 us for 8191 tokens of 32 + 8 heads, 9 take 33.1).
 dim3 token_grid(const DeviceInfo& dev, int64_t tokens, int rows, int rows_per_block) {
-  const int64_t want = int64_t(dev.sm_count) * 16;
+  const int64_t want = int64_t(dev.sm_count) * 9;
   const int64_t gx = tokens < want ? tokens : want;
   const int most = (rows + rows_per_block - 1) / rows_per_block;
   int64_t gy = want / gx;
