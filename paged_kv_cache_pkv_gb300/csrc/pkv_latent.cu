@@ -79,18 +79,17 @@ struct LtSmem {
   static constexpr uint32_t kv = 0;
   static constexpr uint32_t q = kv + kLtStages * kLtTileBytes;  // [9][N rows][128 B]
   static constexpr uint32_t misc = q + kLtChunks * N * 128;
-  // misc: barriers, TMEM address, share bounds, per-row reductions
+  // misc: barriers, TMEM address, plan, per-row reductions
   static constexpr uint32_t bars = misc;           // 16 x 8
   static constexpr uint32_t tmem = misc + 128;
-  static constexpr uint32_t share = misc + 144;    // 2 bounds x 4 ints, the first sequence's 4 ints
-  static constexpr uint32_t wsum = misc + 192;     // [2][11] x 16, plan scans
-  static constexpr uint32_t red = misc + 544;      // [4 quadrants][N] floats
+  static constexpr uint32_t plan = misc + 144;     // LtPlan
+  static constexpr uint32_t wsum = misc + 272;     // [2][11] x 16, plan scans
+  static constexpr uint32_t red = misc + 624;      // [4 quadrants][N] floats
   static constexpr uint32_t alpha = red + 16 * N;  // [N] floats
   static constexpr uint32_t end = alpha + 4 * N;
   static constexpr uint32_t bytes = end + 1024;    // + alignment slack
 };
 static_assert(LtSmem<64>::bytes <= 232448, "latent attention shared memory above the 227 KiB limit");
-static_assert(kLtPlanBytes <= kLtTileBytes, "the plan borrows the first cache tile");
 
 
 // tcgen05.ld of X columns: lanes 0-15 read theirs from taddr on, lanes 16-31
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   uint64_t* bar_s = bars + 12;       // [2] scores written
   uint64_t* bar_p = bars + 14;       // [2] P written (256 arrivals)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
-  int* s_share = reinterpret_cast<int*>(sm + S::share);
+  LtPlan* plan = reinterpret_cast<LtPlan*>(sm + S::plan);
   longlong2* s_wsum = reinterpret_cast<longlong2*>(sm + S::wsum);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -221,15 +220,13 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   }
   griddep_wait();  // what the stream did before: the queries, this step's rows, the metadata
 
-  // the plan borrows the first cache tile
-  lt_plan<N, kLtKeys, kLtThreads>(p, int(blockIdx.x), int(gridDim.x), sm + S::kv, s_wsum, s_share);
+  lt_plan<N, kLtKeys, kLtThreads>(p, int(blockIdx.x), int(gridDim.x), s_wsum, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const LtPos begin{s_share[0], s_share[1], s_share[2]};
-  const LtPos end{s_share[4], s_share[5], s_share[6]};
-  const LtWalk first{begin, end, lt_seq<N>(p, begin.b, s_share[8], s_share[9], s_share[10])};
+  const LtPos begin = plan->begin, end = plan->end;
+  const LtWalk first{begin, end, lt_seq<N>(p, begin.b, plan->q0, plan->q1, plan->L)};
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
   // every lane waits; the warp goes on only if all of them saw the phase
@@ -396,6 +393,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     float* s_red = reinterpret_cast<float*>(sm + S::red);      // [4][N]
     float* s_alpha = reinterpret_cast<float*>(sm + S::alpha);  // [N]
     const int bar_id = 1 + wg;
+    // (here, in the time that the first copies take)
+    if (tid == 0) p.joins[blockIdx.x] = lt_join<N>(p, *plan, int(blockIdx.x), int(gridDim.x));
     LtWalk walk = first;
     LtPiece x;
     int g = 0;
@@ -615,17 +614,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // without keys, which the merge skips by its l of 0.
     if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < N)
       p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + N * kLatentDim + N + tid] = 0.f;
-    // what the merge joins for this CTA: the tile its share ends inside, if
-    // its first block is in this share
-    if (tid == 0) {
-      int4 join = make_int4(0, 0, 0, s_share[11]);
-      if (end.b < p.B && end.k > 0 &&
-          (begin.b < end.b || (begin.b == end.b && (begin.j < end.j || (begin.j == end.j && begin.k == 0))))) {
-        const LtSeq s = lt_seq<N>(p, end.b);
-        join = make_int4(s.q0 * p.H + end.j * N, min(N, s.rows - end.j * N), s_share[7], join.w);
-      }
-      p.joins[blockIdx.x] = join;
-    }
   }
   // Let the merge kernel be scheduled; it waits for this grid.
   griddep_launch_dependents();

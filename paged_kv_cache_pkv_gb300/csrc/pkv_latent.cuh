@@ -129,9 +129,59 @@ __device__ __forceinline__ bool lt_next(const LatentParams& p, LtWalk& w, LtPiec
   }
 }
 
-// Shared memory that the plan borrows: weight before each sequence, and its
-// query_start_loc[b], [b + 1] and seq_lens[b].
-constexpr int kLtPlanBytes = (PKV_MAX_SEQS + 2) * 8 + PKV_MAX_SEQS * 16;
+// A tile among the batch's weights: where it starts, its weight, its blocks.
+struct LtTile {
+  int64_t start, weight;
+  int blocks;
+  // the tile's key block at weight x
+  __device__ __forceinline__ int block(int64_t x) const {
+    return min(blocks - 1, int(__fdividef(float(x - start), float(weight)) * float(blocks)));
+  }
+};
+
+// Equal shares of a batch's weight: `count` of them, share c starting at
+// start(c).  Where that is, is a product of floats: it only has to be the same
+// for the parts on both sides and to rise with c, and exact divisions, of
+// 64-bit integers above all, cost as much as a key block.
+struct LtShares {
+  int64_t total;
+  int count;
+  float each;  // weight of a share
+  __device__ __forceinline__ LtShares(int64_t total_, int H, int parts) {
+    total = total_;
+    count = max(1, min(parts, int(__fdividef(float(total_), float(H) * kLtMinShare))));
+    each = __fdividef(float(total_), float(count));
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return min(total - 1, int64_t(float(c) * each)); }
+  // the last part, from c on, whose share starts before the tile's end
+  __device__ __forceinline__ int last_before(int c, const LtTile& t) const {
+    const int64_t e = t.start + t.weight;
+    int last = max(c, min(count - 1, int(__fdividef(float(e), each))));
+    while (last + 1 < count && start(last + 1) < e) ++last;
+    while (last > c && start(last) >= e) --last;
+    return last;
+  }
+  // the part that has the tile's first block, where c's share begins behind
+  // it: the last one whose share does not
+  __device__ __forceinline__ int head_of(int c, const LtTile& t) const {
+    auto behind = [&](int h) { return start(h) > t.start && t.block(start(h)) > 0; };
+    int head = max(0, min(c - 1, int(__fdividef(float(t.start), each))));
+    while (head + 1 < c && !behind(head + 1)) ++head;
+    while (head > 0 && behind(head)) --head;
+    return head;
+  }
+};
+
+// What the plan leaves in shared memory.
+struct LtPlan {
+  LtPos begin, end;     // of the share
+  int own;              // key blocks a piece where tiles have parts of their own; 0: equal shares
+  int last, head;       // of the tile that the share ends (begins) inside, the last (first) part with a piece
+  int q0, q1, L;        // query_start_loc[b], [b + 1] and seq_lens[b] of sequence begin.b
+  LtTile tile0, tile1;  // that begin and end are in (equal shares)
+  int64_t total;
+};
+static_assert(sizeof(LtPlan) <= 128, "the plan's place in the kernels' shared memory");
 
 // Sum over the threads before this one of their `v`, and over all of `v` and
 // of `u`.
@@ -159,52 +209,64 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t u, longlong2* s
   return run;
 }
 
-// The share of part `part` of `parts` (a CTA, or a pair of them): begin in
-// share[0..2], end in [4..6], in [7] the last part with a piece of the tile that
-// the share ends inside, in [8..10] the numbers of the first sequence, in [11]
-// the first part of the tile that the share begins inside (-1: none).  All
-// threads of the block take part; the caller synchronises behind it.
+// The place at weight x, which is in sequence b, whose tiles start at `run`.
+template <int N, int KEYS>
+__device__ __forceinline__ LtPos lt_place(const LatentParams& p, int b, const LtSeq& s, int64_t run, int64_t x,
+                                          LtTile& tile) {
+  int lo = 0, hi = s.tiles;  // last tile that starts at or before x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (run + lt_weight<N>(p, s, mid) <= x) lo = mid; else hi = mid;
+  }
+  LtTile t;
+  t.start = run + lt_weight<N>(p, s, lo);
+  t.weight = run + lt_weight<N>(p, s, lo + 1) - t.start;
+  t.blocks = lt_blocks<N, KEYS>(p, s, lo);
+  tile = t;
+  return LtPos{b, lo, t.block(x)};
+}
+
+// The share of part `part` of `parts` (a CTA, or a pair of them).  Every thread
+// of the block reads its sequences once and, after one scan, whichever thread
+// owns the sequence that a bound falls into writes it down; the caller
+// synchronises behind it.  s_wsum: 2 * THREADS / 32 words.
 template <int N, int KEYS, int THREADS>
-__device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int parts, uint8_t* scratch,
-                                        longlong2* s_wsum, int* s_share) {
+__device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int parts, longlong2* s_wsum, LtPlan* plan) {
   const int tid = threadIdx.x;
-  int64_t* s_scan = reinterpret_cast<int64_t*>(scratch);      // weight before sequence b
-  int4* s_seq = reinterpret_cast<int4*>(s_scan + PKV_MAX_SEQS + 2);  // its q0, q1, L
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  // Tiles and key blocks of the batch ride along in one word, each capped
-  // far above what the choice below looks at.
-  int64_t local = 0, tiles_of = 0, blocks_of = 0;
+  // Tiles and key blocks of the batch ride along in one word, each capped far
+  // above what the choice below looks at.
+  int64_t weight = 0, tiles_of = 0, blocks_of = 0;
   for (int b = b0; b < b1; ++b) {
-    const int4 raw = make_int4(__ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b), 0);
-    s_seq[b] = raw;
-    const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
+    const LtSeq s = lt_seq<N>(p, b);
     if (s.bad && part == 0) flag_status(p.status, PKV_STATUS_BAD_QUERY);
-    const int64_t w = lt_weight<N>(p, s, s.tiles);
-    s_scan[b] = w;
-    local += w;
+    weight += lt_weight<N>(p, s, s.tiles);
     tiles_of += s.tiles;
     blocks_of += int64_t(s.tiles) * ((s.L + KEYS - 1) / KEYS);
   }
+  if (tid == 0) {
+    plan->begin = plan->end = LtPos{p.B, 0, 0};
+    plan->q0 = plan->q1 = plan->L = 0;
+    plan->last = plan->head = -1;
+  }
+  constexpr int64_t cap = int64_t(1) << 20;
   longlong2 sums;
-  int64_t run = block_scan<THREADS>(local, (min(tiles_of, int64_t(1) << 20) << 32) | min(blocks_of, int64_t(1) << 20), s_wsum, sums);
+  int64_t run = block_scan<THREADS>(weight, (min(tiles_of, cap) << 32) | min(blocks_of, cap), s_wsum, sums);
   const int64_t total = sums.x;
   const int tiles = int(sums.y >> 32), blocks_all = int(sums.y & 0xFFFFFFFF);
-  for (int b = b0; b < b1; ++b) {
-    const int64_t w = s_scan[b];
-    s_scan[b] = run;
-    run += w;
-  }
-  if (tid == 0) s_scan[p.B] = total;
-  __syncthreads();
-  // Few tiles: each has parts of its own, pieces of `own` key blocks, so that
-  // a part has one piece and no tile is cut that need not be (four sequences
-  // of up to 255 tokens: 16.3 -> 13.4 us).  The pieces fit the grid because
+  // Few tiles: each has parts of its own, pieces of `own` key blocks, so that a
+  // part has one piece and no tile is cut that need not be (four sequences of
+  // up to 255 tokens: 16.3 -> 12.1 us).  The pieces fit the grid because
   // ceil(n / own) sums to no more than tiles + blocks / own.
   int own = 0;
   if (tiles > 0 && tiles < parts) {
     const float t = float(blocks_all) / float(parts - tiles);
     if (t <= float(kLtMostOwn / KEYS)) own = max(kLtLeastOwn / KEYS, int(ceilf(t)));
+  }
+  if (tid == 0) {
+    plan->own = own;
+    plan->total = total;
   }
   if (own > 0) {
     auto cuts = [&](const LtSeq& s) {  // pieces of a tile
@@ -213,94 +275,64 @@ __device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int par
     };
     int64_t count = 0;
     for (int b = b0; b < b1; ++b) {
-      const int4 raw = s_seq[b];
-      const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
+      const LtSeq s = lt_seq<N>(p, b);
       count += int64_t(s.tiles) * cuts(s);
     }
-    int first_cta = int(block_scan<THREADS>(count, 0, s_wsum + THREADS / 32, sums));
-    if (tid == 0) {
-      *reinterpret_cast<int4*>(s_share) = make_int4(p.B, 0, 0, -1);
-      *reinterpret_cast<int4*>(s_share + 4) = make_int4(p.B, 0, 0, -1);
-      *reinterpret_cast<int4*>(s_share + 8) = make_int4(0, 0, 0, -1);
-    }
-    __syncthreads();
+    int first = int(block_scan<THREADS>(count, 0, s_wsum + THREADS / 32, sums));
     for (int b = b0; b < b1; ++b) {
-      const int4 raw = s_seq[b];
-      const LtSeq s = lt_seq<N>(p, b, raw.x, raw.y, raw.z);
-      const int n = cuts(s), r = part - first_cta;
-      first_cta += s.tiles * n;
+      const LtSeq s = lt_seq<N>(p, b);
+      const int n = cuts(s), r = part - first;
+      first += s.tiles * n;
       if (r < 0 || r >= s.tiles * n) continue;
       const int j = r / n, i = r - j * n, blocks = lt_blocks<N, KEYS>(p, s, j);
       const int k0 = i * blocks / n, k1 = (i + 1) * blocks / n;  // blocks <= the cap's few thousand
+      plan->begin = LtPos{b, j, k0};
+      plan->end = k1 == blocks ? LtPos{b, j + 1, 0} : LtPos{b, j, k1};
+      plan->last = part - i + n - 1;
       // a tile of fewer blocks than pieces begins at the first piece that has one
-      const int head = k0 > 0 ? part - i + (n + blocks - 1) / blocks - 1 : -1;
-      *reinterpret_cast<int4*>(s_share) = make_int4(b, j, k0, 0);
-      *reinterpret_cast<int4*>(s_share + 4) =
-          k1 == blocks ? make_int4(b, j + 1, 0, 0) : make_int4(b, j, k1, part - i + n - 1);
-      *reinterpret_cast<int4*>(s_share + 8) = make_int4(raw.x, raw.y, raw.z, head);
+      if (k0 > 0) plan->head = part - i + (n + blocks - 1) / blocks - 1;
+      plan->q0 = s.q0;
+      plan->q1 = s.q0 + s.n;
+      plan->L = s.L;
     }
-  } else if (tid < 2) {  // thread 0: the share's start, thread 1: its end
-    // Where a share begins is a product of floats: it only has to be the
-    // same for the CTAs on both sides and to rise with c, and exact
-    // divisions, of 64-bit integers above all, cost as much as a key block.
-    const int g = max(1, min(parts, int(__fdividef(float(total), float(p.H) * kLtMinShare))));
-    const float each = __fdividef(float(total), float(g));  // a share's weight
-    auto start = [&](int c) { return min(total - 1, int64_t(float(c) * each)); };
-    const int c = part + tid;
-    LtPos at{p.B, 0, 0};
-    int last = -1;
-    if (total > 0 && c < g) {
-      const int64_t x = start(c);
-      int lo = 0, hi = p.B;  // last b with s_scan[b] <= x
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_scan[mid] <= x) lo = mid; else hi = mid;
+  } else if (total > 0) {
+    const LtShares shares(total, p.H, parts);
+    const int64_t x0 = shares.start(part), x1 = shares.start(part + 1);
+    for (int b = b0; b < b1; ++b) {
+      const LtSeq s = lt_seq<N>(p, b);
+      const int64_t w = lt_weight<N>(p, s, s.tiles);
+      if (part < shares.count && x0 >= run && x0 < run + w) {
+        plan->begin = lt_place<N, KEYS>(p, b, s, run, x0, plan->tile0);
+        plan->q0 = s.q0;
+        plan->q1 = s.q0 + s.n;
+        plan->L = s.L;
       }
-      const int4 raw = s_seq[lo];
-      const LtSeq s = lt_seq<N>(p, lo, raw.x, raw.y, raw.z);
-      const int64_t y = x - s_scan[lo];
-      int jl = 0, jh = s.tiles;  // last j with weight(j) <= y
-      while (jh - jl > 1) {
-        const int mid = (jl + jh) >> 1;
-        if (lt_weight<N>(p, s, mid) <= y) jl = mid; else jh = mid;
-      }
-      const int64_t w0 = lt_weight<N>(p, s, jl), w1 = lt_weight<N>(p, s, jl + 1);
-      const int blocks = lt_blocks<N, KEYS>(p, s, jl);
-      at.b = lo;
-      at.j = jl;
-      at.k = min(blocks - 1, int(__fdividef(float(y - w0), float(w1 - w0)) * float(blocks)));
-      // the last CTA whose share starts before this tile's end
-      const int64_t e = s_scan[lo] + w1;
-      last = max(c, min(g - 1, int(__fdividef(float(e), each))));
-      while (last + 1 < g && start(last + 1) < e) ++last;
-      while (last > c && start(last) >= e) --last;
-      if (tid == 0) {
-        *reinterpret_cast<int4*>(s_share + 8) = raw;
-        // the CTA that has this tile's first block: the last one whose
-        // share does not begin behind it
-        int head = -1;
-        if (at.k > 0) {
-          const int64_t t0 = s_scan[lo] + w0;
-          auto behind = [&](int h) {
-            const int64_t v = start(h) - t0;
-            return v > 0 && min(blocks - 1, int(__fdividef(float(v), float(w1 - w0)) * float(blocks))) > 0;
-          };
-          head = max(0, min(c - 1, int(__fdividef(float(t0), each))));
-          while (head + 1 < c && !behind(head + 1)) ++head;
-          while (head > 0 && behind(head)) --head;
-        }
-        s_share[11] = head;
-      }
-    } else if (tid == 0) {
-      s_share[11] = -1;
+      if (part + 1 < shares.count && x1 >= run && x1 < run + w)
+        plan->end = lt_place<N, KEYS>(p, b, s, run, x1, plan->tile1);
+      run += w;
     }
-    s_share[tid * 4] = at.b;
-    s_share[tid * 4 + 1] = at.j;
-    s_share[tid * 4 + 2] = at.k;
-    s_share[tid * 4 + 3] = last;
   }
-  // the scan's words are rewritten by the copy engine
-  fence_proxy_async_smem();
+}
+
+// What the merge needs to know of a share (LatentParams::joins).  Not part of
+// the plan: nothing waits for it.
+template <int N>
+__device__ __forceinline__ int4 lt_join(const LatentParams& p, const LtPlan& plan, int part, int parts) {
+  const LtPos &begin = plan.begin, &end = plan.end;
+  if (begin.b >= p.B) return make_int4(0, 0, 0, -1);
+  int last = plan.last, head = plan.head;
+  if (plan.own == 0) {
+    const LtShares shares(plan.total, p.H, parts);
+    if (end.b < p.B) last = shares.last_before(part, plan.tile1);
+    if (begin.k > 0) head = shares.head_of(part, plan.tile0);
+  }
+  // its last tile is cut, and the tile's first block is in this share
+  if (end.b < p.B && end.k > 0 &&
+      (begin.b < end.b || (begin.b == end.b && (begin.j < end.j || (begin.j == end.j && begin.k == 0))))) {
+    const LtSeq s = lt_seq<N>(p, end.b);
+    return make_int4(s.q0 * p.H + end.j * N, min(N, s.rows - end.j * N), last, head);
+  }
+  return make_int4(0, 0, 0, head);
 }
 
 // Sequences of more than 64 rows, on pairs of CTAs (pkv_latent_pair.cu).

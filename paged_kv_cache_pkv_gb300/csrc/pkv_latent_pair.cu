@@ -66,15 +66,15 @@ struct PrSmem {
   static constexpr uint32_t bars = p + 2 * kPrOwn * 128;       // 33 x 8
   static constexpr uint32_t tmem = bars + 272;
   static constexpr uint32_t flags = tmem + 8;                  // own, the other CTA's
-  static constexpr uint32_t share = tmem + 16;                 // 12 ints
-  static constexpr uint32_t inv = share + 48;                  // [128] 1 / row sums
+  static constexpr uint32_t plan = tmem + 16;                  // LtPlan
+  static constexpr uint32_t inv = plan + 128;                  // [128] 1 / row sums
   static constexpr uint32_t red = inv + 512;                   // [4][64] partial sums, maxima
   static constexpr uint32_t wsum = red;                        // plan scans
   static constexpr uint32_t end = red + 1024;
   static constexpr uint32_t bytes = end + 1024;                // + alignment slack
 };
 static_assert(PrSmem::bytes <= 232448, "paired latent attention: shared memory above the 227 KiB limit");
-static_assert(kLtPlanBytes <= PrSmem::q && 2 * (kPrThreads / 32) * 16 <= 1024, "what the plan borrows");
+static_assert(2 * (kPrThreads / 32) * 16 <= 1024, "what the plan borrows");
 
 // ---- two-CTA forms of the tcgen05 and barrier helpers ---------------------------
 __device__ __forceinline__ void umma_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* bar_round = bars + 32;                 // the other CTA's flags are here
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::tmem);
   volatile int* s_flags = reinterpret_cast<volatile int*>(sm + S::flags);
-  int* s_share = reinterpret_cast<int*>(sm + S::share);
+  LtPlan* plan = reinterpret_cast<LtPlan*>(sm + S::plan);
   float* s_inv = reinterpret_cast<float*>(sm + S::inv);
   float* s_red = reinterpret_cast<float*>(sm + S::red);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -225,15 +225,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(tables + i));
   }
   griddep_wait();
-  lt_plan<kPrRows, kPrKeys, kPrThreads>(p, pair, pairs, sm, reinterpret_cast<longlong2*>(sm + S::wsum), s_share);
+  lt_plan<kPrRows, kPrKeys, kPrThreads>(p, pair, pairs, reinterpret_cast<longlong2*>(sm + S::wsum), plan);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised, their plans read
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const LtPos begin{s_share[0], s_share[1], s_share[2]};
-  const LtPos end{s_share[4], s_share[5], s_share[6]};
-  const LtWalk first{begin, end, lt_seq<kPrRows>(p, begin.b, s_share[8], s_share[9], s_share[10])};
+  const LtPos begin = plan->begin, end = plan->end;
+  const LtWalk first{begin, end, lt_seq<kPrRows>(p, begin.b, plan->q0, plan->q1, plan->L)};
   auto next_piece = [&](LtWalk& w, LtPiece& x) { return lt_next<kPrRows, kPrKeys>(p, w, x); };
   const uint32_t tmem_s[2] = {tmem + 256u, tmem + 320u};  // O^T: [0, 128) and [128, 256)
   auto wait_all = [&](uint64_t* bar, uint32_t parity) {
@@ -255,6 +254,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // What each role carries from the first round to a second.  g counts cache
   // tiles, gv those with a P V.  A second round (some score exceeded the
   // reference by too much) walks every piece twice, for maxima first.
+  if (tid == 0 && rank == 0) p.joins[pair] = lt_join<kPrRows>(p, *plan, pair, pairs);
   int g = 0, gv = 0, pieces = 0, wholes = 0;
   int slices = 0, tails = 0;  // that a loader has sent; slices of last tiles
   int g0 = 0, taken[2] = {-1, -1};  // tiles of passes for maxima; of the tile in each score buffer, count and kind
@@ -651,15 +651,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // without keys, which the merge skips by its l of 0.
   if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < kPrOwn)
     p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + kPrRows * kLatentDim / 2 + kPrOwn + tid] = 0.f;
-  if (tid == 0 && rank == 0) {
-    int4 join = make_int4(0, 0, 0, s_share[11]);
-    if (end.b < p.B && end.k > 0 &&
-        (begin.b < end.b || (begin.b == end.b && (begin.j < end.j || (begin.j == end.j && begin.k == 0))))) {
-      const LtSeq s = lt_seq<kPrRows>(p, end.b);
-      join = make_int4(s.q0 * p.H + end.j * kPrRows, min(kPrRows, s.rows - end.j * kPrRows), s_share[7], join.w);
-    }
-    p.joins[pair] = join;
-  }
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
