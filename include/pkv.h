@@ -302,7 +302,10 @@ typedef struct {
  *                  [0, max_position) is skipped whole (its q_out row too) and
  *                  flags PKV_STATUS_BAD_POSITION.
  *   slot_mapping   as in pkv_write; a token whose slot is negative or beyond
- *                  the pool still has its queries rotated.
+ *                  the pool still has its queries rotated.  Two tokens of one
+ *                  call with the same slot leave either's values, or a mixture
+ *                  (on FP8 pages of codes and scales too): the tokens of a call
+ *                  have slots of their own.
  *   q_out          [num_tokens, num_q_heads, 128] bf16, contiguous (NULL iff
  *                  q is); may be q itself where q is contiguous. */
 PKV_API int pkv_write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new,
@@ -367,7 +370,12 @@ PKV_API int pkv_attend_latent_workspace_size(const pkv_desc* desc, int32_t num_s
  *   block_tables, seq_lens, query_start_loc, scale, workspace and stream
  *   order as in pkv_attend (workspace: pkv_attend_latent_workspace_size).
  *   max_query_len  host-side upper bound on the query tokens of a sequence,
- *                  or <= 0 if unknown; it only selects tile sizes.
+ *                  or <= 0 if unknown.  It selects tile sizes, and with the
+ *                  tables' width whether pairs of SMs share a tile: results are
+ *                  right whatever it says, their last bits may differ.
+ * out must not overlap q, the pool or the workspace; calls that may overlap on
+ * the GPU need workspaces of their own.  PKV_ERR_RANGE where num_tokens *
+ * num_q_heads, num_blocks * 2 or max_blocks_per_seq * 16 come near 2^31.
  * Rows of tokens past a sequence's end are never used, whatever they hold;
  * the rows of its cached tokens, those of this step among them, must be
  * finite (a later row of the same chunk enters a query's sums with weight 0,

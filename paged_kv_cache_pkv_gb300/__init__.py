@@ -508,8 +508,8 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
     """Absorbed attention over latent pages [NB, 16, 576]: every head of
     ``q`` [T, H, 576] against the one shared row a token, whose first 512
     values are the value.  Returns ``out`` [T, H, 512].  The other arguments
-    are as in attend(); max_query_len (0 = unknown) selects tile sizes, never
-    results."""
+    are as in attend(); max_query_len (0 = unknown) selects tile sizes, which
+    may change results in their last bits, never which rows are right."""
     index = _index(latent_cache, "latent_cache")
     pool = _take(latent_cache, "latent_cache", torch.bfloat16, 3, index)
     qp = _take(q, "q", torch.bfloat16, 3, index)

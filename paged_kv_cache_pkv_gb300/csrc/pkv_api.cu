@@ -54,6 +54,19 @@ int check_latent_desc(const pkv_desc* d) {
   return PKV_OK;
 }
 
+// Rows, groups of eight cache rows and positions are int32 on the device (with
+// a tile of rows or keys on top), and the work split adds its weights, heads x
+// keys for each tile of 16 rows at the finest, up in 64 bits.
+int check_latent_range(const pkv_desc* d, int32_t num_seqs, int32_t num_tokens) {
+  constexpr int64_t top = int64_t(1) << 31;
+  if (int64_t(num_tokens) * d->num_q_heads >= top - 1024 || int64_t(d->num_blocks) * 2 >= top ||
+      int64_t(d->max_blocks_per_seq) * kPage >= top - 1024)
+    return PKV_ERR_RANGE;
+  const double heaviest = 2.0 * d->num_q_heads * (double(kPage) * d->max_blocks_per_seq + 1024);
+  const double tiles = double(num_tokens) * d->num_q_heads / 16.0 + num_seqs;
+  return heaviest * tiles < 9.0e18 ? PKV_OK : PKV_ERR_RANGE;
+}
+
 // A token stride in elements: rows of `row` elements, 16-byte aligned.
 bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8; }
 
@@ -392,6 +405,7 @@ int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache, const int
   if (!aligned(q, 16) || !aligned(latent_cache, 16) || !aligned(out, 16) || !aligned(block_tables, 4) ||
       !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(workspace, 256))
     return PKV_ERR_ALIGN;
+  if (int e = check_latent_range(desc, num_seqs, num_tokens)) return e;
   LaunchCtx ctx{};
   if (int e = make_ctx(stream, &ctx)) return e;
   const LatentAttendArgs a{q,          latent_cache, block_tables, seq_lens,  query_start_loc, num_seqs,

@@ -688,14 +688,7 @@ size_t latent_workspace_bytes(const DeviceInfo& dev) {
 
 int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   const pkv_desc& d = a.desc;
-  // rows are int32 on the device, and so are the tensor map's coordinates
-  if (int64_t(a.num_tokens) * d.num_q_heads >= (int64_t(1) << 31) - 256) return PKV_ERR_RANGE;
   if (ctx.dev->sm_count > kLtMergeThreads) return PKV_ERR_LAUNCH;  // the merge holds a piece a thread
-  if (int64_t(d.num_blocks) * 2 >= (int64_t(1) << 31)) return PKV_ERR_RANGE;
-  // the plan multiplies the batch's weight by the CTAs in 64 bits
-  const double heaviest = 2.0 * d.num_q_heads * (16.0 * d.max_blocks_per_seq + kLtTileCost) + 64.0;
-  const double tiles_bound = double(a.num_tokens) * d.num_q_heads / 16.0 + a.num_seqs;
-  if (heaviest * tiles_bound * ctx.dev->sm_count >= 9.0e18) return PKV_ERR_RANGE;
   if (a.workspace_bytes < latent_workspace_bytes(*ctx.dev)) return PKV_ERR_WORKSPACE;
   LatentParams lp{};
   lp.block_tables = a.block_tables;

@@ -51,12 +51,12 @@ struct LtSeq {
 template <int N>
 __device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b, int q0, int q1, int L) {
   LtSeq s;
+  // (any int32 may stand there: no sum or difference of them before its bounds
+  // are known; the host has checked that max_blocks * kPage is an int32)
+  s.bad = q0 < 0 || q1 < q0 || q1 > p.T || L < 0 || q1 - q0 > L || L > p.max_blocks * kPage || (b == 0 && q0 != 0);
   s.q0 = q0;
-  s.L = L;
-  s.n = q1 - q0;
-  s.bad = q0 < 0 || s.n < 0 || q1 > p.T || s.n > L || L < 0 || (L + kPage - 1) / kPage > p.max_blocks ||
-          (b == 0 && q0 != 0);
-  if (s.bad) s.n = 0;
+  s.L = s.bad ? 0 : L;
+  s.n = s.bad ? 0 : q1 - q0;
   s.rows = s.n * p.H;
   s.tiles = (s.rows + N - 1) / N;
   return s;

@@ -182,6 +182,36 @@ def test_inconsistent_batches_are_flagged(pkvlib, H, width):
     assert (np.abs(got - good[0])[[0, 2]] <= good[1][[0, 2]]).all()
 
 
+@pytest.mark.parametrize("H,width", [(16, 1), (96, WIDE)])
+def test_any_int32_as_length_or_query_start(pkvlib, H, width):
+    """Lengths and query starts whose sums or differences leave int32 are
+    inconsistent like any other: the sequence is skipped, its neighbours are
+    not."""
+    pkv.get_last_error()
+    c = Case([100, 50, 20], [1, 1, 1], H, seed=12, width=width)
+    good = c.expect()
+    q, pool, tables, lens, qsl, scale = c.args()
+    top = 2**31 - 1
+    for at, value in ((1, top), (1, top - 7), (1, -2**31), (1, tables.shape[1] * 16 + 1)):
+        L = c.lens.copy()
+        L[at] = value
+        out = torch.full((3, H, 512), 7.0, device="cuda", dtype=torch.bfloat16)
+        pkv.attend_latent(q, pool, tables, cuda(L), qsl, scale, out=out)
+        assert pkv.get_last_error() == pkv.STATUS_BAD_QUERY
+        assert bool((out[1] == 7.0).all())
+        got = bf16_to_f64(bits(out))
+        assert (np.abs(got - good[0])[[0, 2]] <= good[1][[0, 2]]).all()
+    for value in (top, -2**31):  # the end of the second sequence and the start of the third
+        starts = c.qsl.copy()
+        starts[2] = value
+        out = torch.full((3, H, 512), 7.0, device="cuda", dtype=torch.bfloat16)
+        pkv.attend_latent(q, pool, tables, lens, cuda(starts), scale, out=out)
+        assert pkv.get_last_error() == pkv.STATUS_BAD_QUERY
+        assert bool((out[1:] == 7.0).all())
+        got = bf16_to_f64(bits(out))
+        assert (np.abs(got - good[0])[0] <= good[1][0]).all()
+
+
 def test_two_graphs_share_a_workspace_and_a_stream_of_its_own(pkvlib):
     cases = [Case([3000, 200], [1, 1], 16, seed=9), Case([70, 2500, 5], [3, 1, 1], 64, seed=10),
              Case([900, 2100], [1, 1], 128, seed=11)]

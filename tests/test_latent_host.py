@@ -97,6 +97,15 @@ def test_attend_latent_refuses(pkvlib, bad, code):
     assert pkvlib.pkv_launch_count() == before
 
 
+@pytest.mark.parametrize("bad", [
+    dict(desc=_latent(num_q_heads=256), T=2**23), dict(desc=_latent(num_blocks=2**30)),
+    dict(desc=_latent(max_blocks_per_seq=2**27 - 64)), dict(desc=_latent(max_blocks_per_seq=2**31 - 1)),
+    dict(desc=_latent(num_q_heads=256, max_blocks_per_seq=2**27 - 65), T=2**22),
+])
+def test_attend_latent_refuses_what_leaves_its_integers(pkvlib, bad):
+    assert _attend(pkvlib, **bad) == RANGE
+
+
 def test_binding_refuses_types_and_host_tensors():
     bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
     ids = torch.zeros(4, dtype=torch.int64)
