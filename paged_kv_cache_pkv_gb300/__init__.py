@@ -32,8 +32,6 @@ library_path = os.environ.get("PKV_LIBRARY", os.path.join(_HERE, "libpkv.so"))
 STATUS_BAD_SLOT, STATUS_BAD_BLOCK, STATUS_BAD_QUERY, STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 STATUS_BAD_POSITION = 0x10
 KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5}
-LATENT_DIM, LATENT_ROPE = 512, 64
-LATENT_ROW = LATENT_DIM + LATENT_ROPE
 
 
 class PkvError(RuntimeError):
@@ -312,9 +310,28 @@ def attend_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, qu
     return out
 
 
-# The calls below are a few microseconds of GPU work for small batches, so
-# their checks are made for speed: one short test a tensor, and the words for
-# what is wrong with it only where it fails.
+# The calls below are a few microseconds of GPU work for small batches: their
+# arguments are checked and handed over by a compiled module
+# (csrc/pkv_binding.cpp) in place of Python code and ctypes.
+
+_binding = None
+
+
+def _native():
+    """The compiled argument checks, bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        handle = lib()
+        try:
+            from . import _pkv_binding
+        except ImportError as e:
+            raise PkvUnavailable(f"the binding of the rotated and latent calls is missing ({e}): build it with "
+                                 "`python -m paged_kv_cache_pkv_gb300.build`") from e
+        _pkv_binding.bind(PkvError, *(ctypes.cast(getattr(handle, n), _vp).value for n in (
+            "pkv_write_rope", "pkv_write_rope_fp8", "pkv_write_latent", "pkv_attend_latent",
+            "pkv_attend_latent_workspace_size")))
+        _binding = _pkv_binding
+    return _binding
 
 
 def _index(t, name):
@@ -327,93 +344,6 @@ def _index(t, name):
     return index
 
 
-def _take(t, name, dtype, ndim, index):
-    """The address of ``t``, a contiguous tensor of this type on device ``index``."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.dim() == ndim
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _need(t, name, dtype, ndim)
-    raise ValueError(f"{name} is on {t.device}, not on device {index} like the cache")
-
-
-def _take_rows(t, name, tokens, heads, dim, index):
-    """(address, token stride) of a bf16 tensor [tokens, heads, dim], or
-    [tokens, dim] where heads is 0: a token's elements contiguous, any token
-    stride that keeps 16-byte alignment."""
-    shape = (tokens, heads, dim) if heads else (tokens, dim)
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be a CUDA tensor on the cache's device, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
-    stride = t.stride()
-    if stride[-1] != 1 or (heads > 1 and stride[1] != dim):
-        raise ValueError(f"a token's elements of {name} must be contiguous")
-    row = dim * (heads or 1)
-    if tokens < 2:
-        return t.data_ptr(), row
-    if stride[0] < row or stride[0] % 8:
-        raise ValueError(f"{name}'s token stride must be a multiple of 8 elements and no less than a token")
-    return t.data_ptr(), stride[0]
-
-
-def _new(shape, dtype, device, stream):
-    """An uninitialised tensor that belongs to the stream it is used on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _run(what, fn, index, stream, *args):
-    """fn(*args, stream) with device ``index`` current."""
-    # the current stream's handle, without the Stream object around it
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        code = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            code = fn(*args, handle)
-    if code:
-        raise PkvError(code, what)
-
-
-def _rope(cos_sin, interleaved, index):
-    at = _take(cos_sin, "cos_sin", torch.float32, 2, index)
-    max_position, dim = cos_sin.shape
-    return Rope(at, max_position, dim, 1 if interleaved else 0)
-
-
-def _write_rope(what, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q, q_out, interleaved,
-                stream):
-    blocks, hkv, page, D = k_cache.shape
-    T = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() else -1
-    k, ks = _take_rows(k_new, "k_new", T, hkv, D, index)
-    v, vs = _take_rows(v_new, "v_new", T, hkv, D, index)
-    pos = _take(positions, "positions", torch.int64, 1, index)
-    slots = _take(slot_mapping, "slot_mapping", torch.int64, 1, index)
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("k_new, positions and slot_mapping disagree on the number of tokens")
-    hq, qs, qp, qo = hkv, 0, None, None
-    if q is not None:
-        hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        qp, qs = _take_rows(q, "q", T, hq, D, index)
-        if q_out is None:
-            q_out = _new(q.shape, q.dtype, q.device, stream)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-        qo = _take(q_out, "q_out", torch.bfloat16, 3, index)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rope, desc = _rope(cos_sin, interleaved, index), Desc(blocks, page, hkv, hq, D, 1)
-    _run(what, getattr(lib(), what), index, stream, qp, k, v, qs, ks, vs, pos, slots, T, ctypes.byref(rope), qo, *pools,
-         ctypes.byref(desc))
-    return q_out
-
-
 def write_rope(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, q=None, q_out=None,
                interleaved=False, stream=None):
     """write() with the position rotation on the way: K rows (and the queries
@@ -424,11 +354,8 @@ def write_rope(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache,
     and q may be slices of one projection's output.  Returns the rotated
     queries (``q_out``, which may be a contiguous ``q`` itself), or None."""
     index = _index(k_cache, "k_cache")
-    pools = (_take(k_cache, "k_cache", torch.bfloat16, 4, index), _take(v_cache, "v_cache", torch.bfloat16, 4, index))
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache shapes disagree")
-    return _write_rope("pkv_write_rope", k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q,
-                       q_out, interleaved, stream)
+    return (_binding or _native()).write_rope(index, stream, k_new, v_new, positions, cos_sin, slot_mapping, k_cache,
+                                              v_cache, q, q_out, interleaved)
 
 
 def write_rope_fp8(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale, q=None,
@@ -436,13 +363,8 @@ def write_rope_fp8(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_ca
     """write_rope into FP8 pages (codes and scale bytes as in write_fp8): the
     rotated fp32 values are rounded once, to E4M3."""
     index = _index(k_cache, "k_cache")
-    pools = (_take(k_cache, "k_cache", torch.uint8, 4, index), _take(v_cache, "v_cache", torch.uint8, 4, index),
-             _take(k_scale, "k_scale", torch.uint8, 3, index), _take(v_scale, "v_scale", torch.uint8, 3, index))
-    shape = k_cache.shape
-    if v_cache.shape != shape or k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
-        raise ValueError("FP8 pools must be codes [NB, Hkv, P, D] and scales [NB, Hkv, P]")
-    return _write_rope("pkv_write_rope_fp8", k_new, v_new, positions, cos_sin, slot_mapping, k_cache, pools, index, q,
-                       q_out, interleaved, stream)
+    return (_binding or _native()).write_rope_fp8(index, stream, k_new, v_new, positions, cos_sin, slot_mapping,
+                                                  k_cache, v_cache, q, q_out, interleaved, k_scale, v_scale)
 
 
 def make_latent_desc(latent_cache, num_heads, max_blocks_per_seq):
@@ -457,41 +379,11 @@ def write_latent(c_new, k_pe, positions, cos_sin, slot_mapping, latent_cache, q_
     rotated by its position (see write_rope; cos_sin [max_position, 64]).
     With ``q_pe`` [T, H, 64] the queries' rotated part goes into the last 64
     values of ``q_out`` [T, H, 576], whose first 512 are left alone.  c_new,
-    k_pe and q_pe may be slices.  Returns q_out, or None."""
+    k_pe and q_pe may be slices, q_pe q_out's own last 64 values.  Returns
+    q_out, or None."""
     index = _index(latent_cache, "latent_cache")
-    pool = _take(latent_cache, "latent_cache", torch.bfloat16, 3, index)
-    T = c_new.shape[0] if isinstance(c_new, torch.Tensor) and c_new.dim() else -1
-    c, cs = _take_rows(c_new, "c_new", T, 0, LATENT_DIM, index)
-    k, ks = _take_rows(k_pe, "k_pe", T, 0, LATENT_ROPE, index)
-    pos = _take(positions, "positions", torch.int64, 1, index)
-    slots = _take(slot_mapping, "slot_mapping", torch.int64, 1, index)
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("c_new, positions and slot_mapping disagree on the number of tokens")
-    heads, qs, hs, qp, qo = 1, 0, 0, None, None
-    if q_pe is not None:
-        if not isinstance(q_pe, torch.Tensor) or q_pe.dtype is not torch.bfloat16:
-            raise TypeError(f"q_pe must be a {torch.bfloat16} tensor")
-        if q_pe.get_device() != index:
-            raise ValueError(f"q_pe must be a CUDA tensor on the cache's device, got {q_pe.device}")
-        if q_pe.dim() != 3 or q_pe.shape[0] != T or q_pe.shape[2] != LATENT_ROPE or q_pe.stride(2) != 1:
-            raise ValueError(f"q_pe must be [tokens, H, {LATENT_ROPE}] with contiguous rows, got shape "
-                             f"{tuple(q_pe.shape)}")
-        heads = q_pe.shape[1]
-        hs = q_pe.stride(1) if heads > 1 else LATENT_ROPE
-        qs = q_pe.stride(0) if T > 1 else heads * hs
-        if hs < LATENT_ROPE or hs % 8 or qs < (heads - 1) * hs + LATENT_ROPE or qs % 8:
-            raise ValueError("q_pe's strides must be multiples of 8 elements and its rows must not overlap")
-        if q_out is None:
-            q_out = _new((T, heads, LATENT_ROW), torch.bfloat16, q_pe.device, stream)
-        elif q_out.shape != (T, heads, LATENT_ROW):
-            raise ValueError(f"q_out must be [tokens, H, {LATENT_ROW}]")
-        qp, qo = q_pe.data_ptr(), _take(q_out, "q_out", torch.bfloat16, 3, index)
-    elif q_out is not None:
-        raise ValueError("q_out without q_pe")
-    rope, desc = _rope(cos_sin, interleaved, index), make_latent_desc(latent_cache, heads, 1)
-    _run("pkv_write_latent", lib().pkv_write_latent, index, stream, c, k, qp, cs, ks, qs, hs, pos, slots, T,
-         ctypes.byref(rope), qo, pool, ctypes.byref(desc))
-    return q_out
+    return (_binding or _native()).write_latent(index, stream, c_new, k_pe, positions, cos_sin, slot_mapping,
+                                                latent_cache, q_pe, q_out, interleaved)
 
 
 def workspace_size_latent(desc, num_seqs, num_tokens, device=None):
@@ -511,28 +403,8 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
     are as in attend(); max_query_len (0 = unknown) selects tile sizes, which
     may change results in their last bits, never which rows are right."""
     index = _index(latent_cache, "latent_cache")
-    pool = _take(latent_cache, "latent_cache", torch.bfloat16, 3, index)
-    qp = _take(q, "q", torch.bfloat16, 3, index)
-    tables = _take(block_tables, "block_tables", torch.int32, 2, index)
-    lens = _take(seq_lens, "seq_lens", torch.int32, 1, index)
-    qsl = _take(query_start_loc, "query_start_loc", torch.int32, 1, index)
-    T, H, row = q.shape
-    B = seq_lens.shape[0]
-    if query_start_loc.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError("seq_lens [B], query_start_loc [B+1] and block_tables [B, M] disagree")
-    if latent_cache.shape[2] != row:
-        raise ValueError("latent_cache and q rows disagree")
-    desc = make_latent_desc(latent_cache, H, block_tables.shape[1])
-    if out is None:
-        out = _new((T, H, LATENT_DIM), torch.bfloat16, q.device, stream)
-    elif out.shape != (T, H, LATENT_DIM):
-        raise ValueError(f"out must be [tokens, H, {LATENT_DIM}]")
-    if workspace is None:
-        workspace = _new((workspace_size_latent(desc, B, T, index),), torch.uint8, q.device, stream)
-    _run("pkv_attend_latent", lib().pkv_attend_latent, index, stream, qp, pool, tables, lens, qsl, B, T,
-         int(max_query_len), scale, _take(out, "out", torch.bfloat16, 3, index),
-         _take(workspace, "workspace", torch.uint8, 1, index), workspace.numel(), ctypes.byref(desc))
-    return out
+    return (_binding or _native()).attend_latent(index, stream, q, latent_cache, block_tables, seq_lens,
+                                                 query_start_loc, scale, out, workspace, max_query_len)
 
 
 def export_pages(k_cache, v_cache, pages, out=None, stream=None):
