@@ -183,10 +183,16 @@ struct LtPlan {
 };
 static_assert(sizeof(LtPlan) <= 128, "the plan's place in the kernels' shared memory");
 
+// a / b, for a < 2^24 and b > 0: exact, and a quarter of an integer division.
+__device__ __forceinline__ int lt_div(int a, int b) {
+  const int q = int(__fdividef(float(a), float(b)));
+  return q - (q * b > a) + ((q + 1) * b <= a);
+}
+
 // Sum over the threads before this one of their `v`, and over all of `v` and
-// of `u`.
+// of `u`.  warp_only: over the first warp, which is alone here.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t u, longlong2* s_wsum, longlong2& total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t u, bool warp_only, longlong2* s_wsum, longlong2& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t incl = v;
 #pragma unroll
@@ -195,9 +201,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t u, longlong2* s
     u += __shfl_xor_sync(0xffffffffu, u, o);
     if (lane >= o) incl += x;
   }
+  int64_t run = incl - v;
+  if (warp_only) {
+    total = make_longlong2(__shfl_sync(0xffffffffu, incl, 31), u);
+    return run;
+  }
   if (lane == 31) s_wsum[warp] = make_longlong2(incl, u);
   __syncthreads();
-  int64_t run = incl - v;
   total = make_longlong2(0, 0);
 #pragma unroll
   for (int x = 0; x < THREADS / 32; ++x) {
@@ -226,12 +236,14 @@ __device__ __forceinline__ LtPos lt_place(const LatentParams& p, int b, const Lt
   return LtPos{b, lo, t.block(x)};
 }
 
-// The share of part `part` of `parts` (a CTA, or a pair of them).  Every thread
-// of the block reads its sequences once and, after one scan, whichever thread
+// The share of part `part` of `parts` (a CTA, or a pair of them).  Every one of
+// the THREADS reads its sequences once and, after one scan, whichever thread
 // owns the sequence that a bound falls into writes it down; the caller
 // synchronises behind it.  s_wsum: 2 * THREADS / 32 words.
 template <int N, int KEYS, int THREADS>
 __device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int parts, longlong2* s_wsum, LtPlan* plan) {
+  const bool warp_only = p.B <= 32;  // a warp plans alone: no barrier
+  if (warp_only && threadIdx.x >= 32) return;
   const int tid = threadIdx.x;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
@@ -252,7 +264,8 @@ __device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int par
   }
   constexpr int64_t cap = int64_t(1) << 20;
   longlong2 sums;
-  int64_t run = block_scan<THREADS>(weight, (min(tiles_of, cap) << 32) | min(blocks_of, cap), s_wsum, sums);
+  int64_t run = block_scan<THREADS>(weight, (min(tiles_of, cap) << 32) | min(blocks_of, cap), warp_only, s_wsum,
+                                    sums);
   const int64_t total = sums.x;
   const int tiles = int(sums.y >> 32), blocks_all = int(sums.y & 0xFFFFFFFF);
   // Few tiles: each has parts of its own, pieces of `own` key blocks, so that a
@@ -278,14 +291,15 @@ __device__ __forceinline__ void lt_plan(const LatentParams& p, int part, int par
       const LtSeq s = lt_seq<N>(p, b);
       count += int64_t(s.tiles) * cuts(s);
     }
-    int first = int(block_scan<THREADS>(count, 0, s_wsum + THREADS / 32, sums));
+    int first = int(block_scan<THREADS>(count, 0, warp_only, s_wsum + THREADS / 32, sums));
     for (int b = b0; b < b1; ++b) {
       const LtSeq s = lt_seq<N>(p, b);
       const int n = cuts(s), r = part - first;
       first += s.tiles * n;
       if (r < 0 || r >= s.tiles * n) continue;
-      const int j = r / n, i = r - j * n, blocks = lt_blocks<N, KEYS>(p, s, j);
-      const int k0 = i * blocks / n, k1 = (i + 1) * blocks / n;  // blocks <= the cap's few thousand
+      // (r < parts, and blocks are at most kLtMostOwn / KEYS times the parts)
+      const int j = lt_div(r, n), i = r - j * n, blocks = lt_blocks<N, KEYS>(p, s, j);
+      const int k0 = lt_div(i * blocks, n), k1 = lt_div((i + 1) * blocks, n);
       plan->begin = LtPos{b, j, k0};
       plan->end = k1 == blocks ? LtPos{b, j + 1, 0} : LtPos{b, j, k1};
       plan->last = part - i + n - 1;
