@@ -182,6 +182,21 @@ def test_inconsistent_batches_are_flagged(pkvlib, H, width):
     assert (np.abs(got - good[0])[[0, 2]] <= good[1][[0, 2]]).all()
 
 
+@pytest.mark.parametrize("B,longest,joined", [(38, 512, False), (38, 513, True), (39, 512, True), (1, 512, False)])
+def test_short_batches_are_not_joined(pkvlib, B, longest, joined):
+    """Few sequences of at most 512 tokens are cut nowhere, so no kernel joins
+    pieces; one sequence or one token more, and it runs."""
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("the bounds are those of 152 SMs")
+    c = Case([longest] + [512 - 13 * (b % 39) for b in range(1, B)], [1] * B, 16, seed=B)
+    c.check(pkv.attend_latent(*c.args(), max_query_len=1))
+    with pkv.Trace(8) as tr:
+        pkv.attend_latent(*c.args(), max_query_len=1)
+    torch.cuda.synchronize()
+    assert tr.read("latent")[1] == 1 and tr.read("merge")[1] == int(joined)
+    assert pkv.get_last_error() == 0
+
+
 @pytest.mark.parametrize("H,width", [(16, 1), (96, WIDE)])
 def test_any_int32_as_length_or_query_start(pkvlib, H, width):
     """Lengths and query starts whose sums or differences leave int32 are
@@ -242,6 +257,28 @@ def test_two_graphs_share_a_workspace_and_a_stream_of_its_own(pkvlib):
     stream.synchronize()
     for c, o, w in zip(cases, got, wants):
         c.check(o, w)
+
+
+def test_calls_at_once_on_two_streams(pkvlib):
+    """Both kernels fill an SM each; calls on two streams share the GPU and
+    nothing else."""
+    pkv.get_last_error()
+    cases = [Case([3000, 200, 77], [1, 1, 1], 16, seed=13), Case([900, 2100], [2, 1], 96, seed=14, width=WIDE)]
+    args = [c.args() for c in cases]
+    want = [pkv.attend_latent(*a) for a in args]
+    for c, w in zip(cases, want):
+        c.check(w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for i in range(12):
+        for k in (i & 1, 1 - (i & 1)):
+            got[k].append(pkv.attend_latent(*args[k], stream=streams[k]))  # a workspace of its own each call
+    torch.cuda.synchronize()
+    for k in range(2):
+        for g in got[k]:
+            assert torch.equal(g.view(torch.int16), want[k].view(torch.int16))
+    assert pkv.get_last_error() == 0
 
 
 def test_a_step_appends_and_attends(pkvlib):
