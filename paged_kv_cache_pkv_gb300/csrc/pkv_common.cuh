@@ -17,12 +17,6 @@ constexpr int kPageBytes = kPage * kHeadDim * 2;  // one (page, kv head): 4 KiB
 constexpr int kPageBytesF8 = kPage * kHeadDim;    // the same in E4M3 codes: 2 KiB
 constexpr int kScaleBytes = kPage;                // FP8 row scales of one (page, kv head)
 
-// Latent pages: a token's row is 512 latent values (keys and values of every
-// head) and 64 rotated values (keys only).
-constexpr int kLatentDim = 512;
-constexpr int kLatentRope = 64;
-constexpr int kLatentRow = kLatentDim + kLatentRope;
-
 // Split-KV decode kernel shape.
 #ifndef PKV_DEC_WARPS
 #define PKV_DEC_WARPS 12

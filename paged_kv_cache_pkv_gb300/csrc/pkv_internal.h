@@ -10,6 +10,12 @@
 
 namespace pkv {
 
+// Latent pages: a token's row is 512 latent values (keys and values of every
+// head) and 64 rotated values (keys only).
+constexpr int kLatentDim = 512;
+constexpr int kLatentRope = 64;
+constexpr int kLatentRow = kLatentDim + kLatentRope;
+
 struct DeviceInfo {
   int device = -1;
   int sm_count = 0;

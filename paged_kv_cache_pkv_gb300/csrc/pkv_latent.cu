@@ -14,24 +14,36 @@
 //  * Rows of a sequence (token-major, then head: contiguous in q and out) are
 //    cut into tiles of N = 16, 32, 48 or 64 rows, so any head count fits.  A
 //    tile needs 512 x N fp32 of accumulators and one SM's TMEM holds
-//    512 x 128, all of it: N = 64 leaves room for two score tiles.
+//    512 x 128, all of it: N = 64 leaves room for two score tiles.  Sequences
+//    of more than 64 rows over long tables go to pairs of CTAs
+//    (pkv_latent_pair.cu).
 //  * The products are computed transposed, with the cache tile as the A
 //    operand of both, straight from shared memory as TMA landed it:
 //      S^T [64 keys x N] = K Q^T      9 x 4 tcgen05.mma, M = 64, K-major A
 //      O^T [512 x N]    += V^T P^T    4 blocks of M = 128 dims, MN-major A
 //    Few rows then cost little (N is the short side), where rows as M would
 //    pad them to 64 or 128, and one copy of the tile serves both products.
+//    At N = 64 a tile takes 2500 cycles of shared-memory reads by the two
+//    products, which bounds it; 64 sequences of 512-4096 tokens take 40, 47
+//    and 55 us at 16, 32 and 64 heads, and their bytes 23, 26 and 27.
 //  * A cache tile is 64 keys = 4 pages.  One TMA box a page, from the pool
 //    viewed as [groups of 8 rows][9 chunks of 64 dims][8 rows][64 dims], so
 //    that each (group, chunk) lands as one 128-byte-swizzled 1 KiB atom and
 //    atoms follow each other at one stride along keys (9 KiB) and along dims
-//    (1 KiB), as both products' descriptors need.  Two tiles are in flight.
+//    (1 KiB), as both products' descriptors need.  (Five smaller boxes a page,
+//    which would let the scores start earlier, were slower: TMA spends 56-70
+//    cycles a box.)  Two tiles are in flight, let go of and refilled page by
+//    page as P V gets through them, and the pages of the next tile are asked
+//    into L2 meanwhile (long tail 239 us without that, 219 with it; two or
+//    three tiles ahead it was slower again).
+//  * P of a tile overwrites the tile's rotated chunk, which only the scores
+//    read: it needs no buffer of its own and never waits for the P V before.
 //  * Softmax without a row maximum a tile.  In S^T a row's scores lie across
 //    lanes and warps, where a maximum costs shuffles; but P needs only some
 //    reference m near the row's maximum: p = 2^(s - m) has the same relative
-//    precision in bf16 whatever its size.  m is the maximum of the tile's
-//    first 64 keys, and is raised (and O^T rescaled) only when a later score
-//    exceeds it by more than kTau; otherwise a tile needs one vote.
+//    precision in bf16 whatever its size.  m is the score of the piece's first
+//    key, and is raised (and O^T rescaled) only where a later score exceeds it
+//    by more than 2^kLtTau; otherwise a tile needs one vote.
 //    Row sums add the rounded p in fp32, a partial sum a thread, joined once
 //    at the end of a tile of rows.
 //  * P is one bf16 term: rounding it (2^-9 a value, independent from key to
@@ -39,13 +51,16 @@
 //    second term would double the larger product's cost.
 //  * Two warpgroups run the softmax, each for half of the rows; a thread has
 //    one key and N/4 rows (16x32bx2 loads: lanes 0-15 and 16-31 read the
-//    same keys' two column halves).  One warp loads, one issues the MMAs.
+//    same keys' two column halves).  One warp loads, one issues the scores'
+//    MMAs and one the values': in one warp P V stood behind scores that waited
+//    for copies that waited for P V.
 //  * Work split (stream-K): tiles of rows laid end to end, each weighing its
 //    keys plus a constant, are cut into equal shares, one a CTA; a share may
-//    start or end inside a tile.  Pieces of a cut tile leave fp32 partials
-//    (m, l, O) in the workspace that a merge kernel joins; whole tiles are
-//    written at once.  A CTA cuts at most two tiles, so the partials do not
-//    grow with the batch, and the joining order is fixed.
+//    start or end inside a tile.  (Few tiles are split each by itself, see
+//    lt_plan.)  Pieces of a cut tile leave fp32 partials (m, l, O) in the
+//    workspace that a merge kernel joins; whole tiles are written at once.  A
+//    CTA cuts at most two tiles, so the partials do not grow with the batch,
+//    and the joining order is fixed.
 //  * Every mbarrier wait is bounded; on expiry the role flags
 //    PKV_STATUS_TIMEOUT, what is in flight lands, TMEM is freed.
 #include <algorithm>
