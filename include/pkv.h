@@ -373,6 +373,9 @@ PKV_API int pkv_attend_latent_workspace_size(const pkv_desc* desc, int32_t num_s
  *                  or <= 0 if unknown.  It selects tile sizes, and with the
  *                  tables' width whether pairs of SMs share a tile: results are
  *                  right whatever it says, their last bits may differ.
+ * As in pkv_attend, seq_lens, query_start_loc and block_tables are read while
+ * the library call right before this one on the stream may still run, which
+ * must therefore not write them (none does).
  * out must not overlap q, the pool or the workspace; calls that may overlap on
  * the GPU need workspaces of their own.  PKV_ERR_RANGE where num_tokens *
  * num_q_heads, num_blocks * 2 or max_blocks_per_seq * 16 come near 2^31.

@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     for (int64_t i = (int64_t(blockIdx.x) * 32 + lane) * 128; i < bytes; i += int64_t(gridDim.x) * 32 * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(tables + i));
   }
-  griddep_wait();  // what the stream did before: the queries, this step's rows, the metadata
-
+  // The lengths, query starts and tables are not what the call right before
+  // this one writes, so the plan need not wait for it.
   lt_plan<N, kLtKeys, kLtThreads>(p, int(blockIdx.x), int(gridDim.x), s_wsum, plan);
   tc_fence_before();
   __syncthreads();
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const uint32_t tmem = *s_tmem;
   const LtPos begin = plan->begin, end = plan->end;
   const LtWalk first{begin, end, lt_seq<N>(p, begin.b, plan->q0, plan->q1, plan->L)};
+  griddep_launch_dependents();  // (which wait for this grid)
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
   // every lane waits; the warp goes on only if all of them saw the phase
@@ -275,6 +276,13 @@ __global__ void __launch_bounds__(kLtThreads, 1)
       // (before the wait below: the reads take longer than what is left of the
       // piece before)
       int ids = group_id(x.k0), next = group_id(x.k0 + 8);
+      if (pieces == 0) {
+        // the first tile's pages into L2 (a hint), then what the stream did
+        // before: the queries, this step's rows
+        if (lane < kLtPages && ids >= 0)
+          prefetch_l2(p.cache + size_t(ids) * (kPage * kLatentRow), kLtPageBytes);
+        griddep_wait();
+      }
       if (lane == 0) {
         if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
         if (ok) {
@@ -408,6 +416,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     float* s_red = reinterpret_cast<float*>(sm + S::red);      // [4][N]
     float* s_alpha = reinterpret_cast<float*>(sm + S::alpha);  // [N]
     const int bar_id = 1 + wg;
+    griddep_wait();  // an earlier call may still read the workspace and write to out
     // (here, in the time that the first copies take)
     if (tid == 0) p.joins[blockIdx.x] = lt_join<N>(p, *plan, int(blockIdx.x), int(gridDim.x));
     LtWalk walk = first;
@@ -630,8 +639,6 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < N)
       p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + N * kLatentDim + N + tid] = 0.f;
   }
-  // Let the merge kernel be scheduled; it waits for this grid.
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

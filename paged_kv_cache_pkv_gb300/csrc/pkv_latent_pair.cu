@@ -234,7 +234,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     for (int64_t i = (int64_t(blockIdx.x) * 32 + lane) * 128; i < bytes; i += int64_t(gridDim.x) * 32 * 128)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(tables + i));
   }
-  griddep_wait();
+  // The lengths, query starts and tables are not what the call right before
+  // this one writes, so the plan need not wait for it.
   lt_plan<kPrRows, kPrKeys, kPrThreads>(p, pair, pairs, reinterpret_cast<longlong2*>(sm + S::wsum), plan);
   tc_fence_before();
   __syncthreads();
@@ -264,6 +265,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // What each role carries from the first round to a second.  g counts cache
   // tiles, gv those with a P V.  A second round (some score exceeded the
   // reference by too much) walks every piece twice, for maxima first.
+  griddep_launch_dependents();  // (which wait for this grid)
+  if (warp < kPrSoftmaxThreads / 32) griddep_wait();  // an earlier call may still read the workspace and write to out
   if (tid == 0 && rank == 0) p.joins[pair] = lt_join<kPrRows>(p, *plan, pair, pairs);
   int g = 0, gv = 0, pieces = 0, wholes = 0;
   int slices = 0, tails = 0;  // that a loader has sent; slices of last tiles
@@ -280,6 +283,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           // (before the wait below: the reads take longer than what is left of
           // the piece before)
           int ids = page_id(x, x.k0 * 8 + lane), next = page_id(x, x.k0 * 8 + 32 + lane);
+          if (pieces == 0) {
+            // the first tile's pages into L2 (a hint), then what the stream did
+            // before: the queries, this step's rows
+            if (lane >> 2 == rank && ids >= 0)
+              prefetch_l2(p.cache + size_t(ids) * (kPage * kLatentRow), kPage * kLatentRow * 2);
+            griddep_wait();
+          }
           if (lane == 0) {
             if (pieces > 0) ok = mbar_wait(bar_qfree, (pieces - 1) & 1);
             if (ok) {
@@ -330,6 +340,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const uint32_t lead_v = cluster_addr(bar_v, 0);
       while (ok && next_piece(walk, x)) {
         int ids = page_id(x, x.k0 * 8 + lane), next = page_id(x, x.k0 * 8 + 32 + lane);
+        if (gv == 0) griddep_wait();
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
           const int in_group = (k - x.k0) & 3;
           if (k > x.k0 && in_group == 0) {
@@ -661,7 +672,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // without keys, which the merge skips by its l of 0.
   if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < kPrOwn)
     p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + kPrRows * kLatentDim / 2 + kPrOwn + tid] = 0.f;
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // neither CTA leaves while the other may still reach into it
