@@ -29,6 +29,14 @@ struct LatentParams {
 // + (j + 1) * N, which is H times its last row's keys plus a constant for
 // loading its queries and writing its result; the sum over tiles is closed.
 constexpr int kLtTileCost = 128;
+// On pairs of CTAs (N = 128) the first tile of a sequence weighs this much more:
+// its pages come from HBM (8 % more a key over long sequences; later tiles find
+// them in L2), and decode rows' tiles are cut almost always, which costs a pair
+// four cache tiles' time.  64 decode rows of 128 heads 67.3 -> 64.7 us, 32
+// drafts 54.5 -> 50.2, chunks beside decode rows 574 -> 565; 512 on every tile
+// gives 64.8, 50.1 and 590, and on one CTA 128 and no more is best.
+template <int N>
+constexpr int kLtFirstCost = N == 128 ? 384 : 0;
 // A share is at least this many keys: below it a second CTA's start and the
 // merge cost more than the keys.
 constexpr int kLtMinShare = 256 + kLtTileCost;
@@ -69,7 +77,8 @@ __device__ __forceinline__ LtSeq lt_seq(const LatentParams& p, int b) {
 // Weight of the first j tiles of a sequence.
 template <int N>
 __device__ __forceinline__ int64_t lt_weight(const LatentParams& p, const LtSeq& s, int64_t j) {
-  return j * (int64_t(p.H) * (s.L - s.n + kLtTileCost)) + N * (j * (j + 1) / 2);
+  return j * (int64_t(p.H) * (s.L - s.n + kLtTileCost)) + N * (j * (j + 1) / 2) +
+         (j > 0 ? p.H * kLtFirstCost<N> : 0);
 }
 
 // Key blocks that tile j of a sequence sees.
