@@ -697,7 +697,7 @@ int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams 
   // pieces (four sequences of up to 255 tokens: 11.6 -> 10.4 us).
   const int64_t tiles = int64_t(a.num_tokens) * d.num_q_heads / N + a.num_seqs;
   if (int64_t(d.max_blocks_per_seq) * kPage <= 2 * kLtLeastOwn && 2 * tiles <= ctx.dev->sm_count) return PKV_OK;
-  cfg.gridDim = dim3(ctx.dev->sm_count, N / (kLtMergeThreads / 32));
+  cfg.gridDim = dim3(ctx.dev->sm_count, lt_merge_blocks(N));
   cfg.blockDim = dim3(kLtMergeThreads);
   cfg.dynamicSmemBytes = 0;
   TraceScope ts(ctx.stream, PKV_K_MERGE);

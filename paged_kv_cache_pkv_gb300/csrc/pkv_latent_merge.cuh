@@ -17,16 +17,21 @@ constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
 // CTA c's share ends inside at most one tile, whose pieces are c's second
 // partial and the first partials of c + 1 .. last.  A warp joins four rows
 // (a float4 a lane of the partials' layout).  Most tiles have two or three
-// pieces: there warp i of the N warps of blocks (c, *) takes rows 4 (i / 4) ..
-// + 3 of the 128 dims i % 4.  A long sequence alone is one tile with a piece
-// a CTA: there the blocks of all its CTAs take units of four rows and 32 dims,
-// and a block's warps share the pieces.  Both read O without waiting for the
-// weights: what bounds this kernel is the number of reads that wait for one
-// another.
+// pieces: there the warps of blocks (c, *) take four rows and four or eight
+// times 32 dims each.  A long sequence alone is one tile with a piece a CTA:
+// there the blocks of all its CTAs take units of four rows and 32 dims, and a
+// block's warps share the pieces.  What bounds it: reads that wait for one
+// another (the join record, then O; O does not wait for the weights), and
+// fetching its own instructions, so its loops are rolled and it divides once.
 constexpr int kLtMergeThreads = 256;
 constexpr int kLtMergeWarps = kLtMergeThreads / 32;
 constexpr int kLtFewPieces = 6;
 constexpr int kLtBatch = 8;  // pieces that a warp has under way (64 registers: four blocks an SM)
+
+// Batches of four times 32 dims that a warp goes through for its rows, and the
+// blocks a CTA of the main kernel that makes: tiles of many rows in one wave.
+constexpr int lt_merge_batches(int N) { return N >= 64 ? 2 : 1; }
+constexpr int lt_merge_blocks(int N) { return N / kLtMergeWarps / lt_merge_batches(N); }
 
 __device__ __forceinline__ float4 f4(float v) { return make_float4(v, v, v, v); }
 // a * x + y where a is not 0, else y: an O that saw no key was not written
@@ -48,6 +53,10 @@ __device__ __forceinline__ float weight(float m, float M) { return m == -INFINIT
 __device__ __forceinline__ float4 f4_weight(const float4& m, const float4& M) {
   return make_float4(weight(m.x, M.x), weight(m.y, M.y), weight(m.z, M.z), weight(m.w, M.w));
 }
+__device__ __forceinline__ float4 f4_shfl(const float4& v, int lane) {
+  return make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                     __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+}
 __device__ __forceinline__ float4 f4_shfl_xor(const float4& v, int o) {
   return make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
                      __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
@@ -56,7 +65,7 @@ __device__ __forceinline__ float4 f4_shfl_xor(const float4& v, int o) {
 // PAIR: the parts are pairs of CTAs with tiles of N = 128 rows.  CTA i of a pair
 // holds dims 256 i .. of all rows, and the references and sums of rows 64 i ..
 template <int N, bool PAIR>
-__global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(const LatentParams p) {
+__global__ void __launch_bounds__(kLtMergeThreads, 3) pkv_latent_merge_kernel(const LatentParams p) {
   constexpr int kParts = PAIR ? 2 : 1;    // partials of a piece
   constexpr int kRows = N / kParts;       // rows whose m and l are in one
   constexpr int kDq = 16 / kParts;        // groups of 32 dims in one
@@ -64,8 +73,8 @@ __global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(co
   __shared__ float4 s_max[kLtMergeWarps], s_sum[kLtMergeWarps];
   __shared__ float4 s_w[kLtMergeThreads];  // of a piece; the grid has fewer CTAs
   __shared__ float4 s_acc[kLtMergeWarps][32];
+  griddep_launch_dependents();  // (which wait for this grid)
   griddep_wait();
-  griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // piece i of the tile that c's share ends inside, its partial of CTA `of`
   auto part = [&](int c, int i, int of) {
@@ -83,8 +92,8 @@ __global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(co
   };
   // rows 4 rq .. + 3 of a tile, dim 32 dq + lane of each; even lanes store a
   // pair of dims of the first of two rows, odd lanes of the second
-  auto put = [&](const int4& join, int rq, int dq, const float4& a, const float4& sum) {
-    const float v[4] = {a.x / sum.x, a.y / sum.y, a.z / sum.z, a.w / sum.w};
+  auto put = [&](const int4& join, int rq, int dq, const float4& a) {
+    const float v[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int e = 0; e < 4; e += 2) {
       const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[e] : v[e + 1], 1);
@@ -97,27 +106,54 @@ __global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(co
   const int4 own = __ldcg(p.joins + blockIdx.x);
   const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
   if (!own_many) {
+    constexpr int kWarps = 4 / lt_merge_batches(N);  // that share four rows
     const int c = blockIdx.x, i = blockIdx.y * kLtMergeWarps + warp;
-    const int rq = i / 4, pieces = own.z - c + 1;
+    const int rq = i / kWarps, pieces = own.z - c + 1;
     if (rq * 4 < own.y) {
-      float4 M = f4(-INFINITY), sum = f4(0.f), acc[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = sum;
-#pragma unroll 2
-      for (int k = 0; k < pieces; ++k) {
-        const float4 l = l_of(c, k, rq), m = f4_seen(m_of(c, k, rq), l);
-        float4 o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o_of(c, k, rq, (i & 3) * 4 + e);
-        const float4 up = f4_max(M, m);
-        const float4 old = f4_weight(M, up), w = f4_weight(m, up);
-        M = up;
-        sum = fma_seen(w, l, fma_seen(old, sum, f4(0.f)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = fma_seen(w, o[e], fma_seen(old, acc[e], f4(0.f)));
+      // lane k of eight: piece k's weight, divided by the rows' sums
+      const int k = lane & 7;
+      float4 l = f4(0.f), m = f4(-INFINITY), w;
+      if (k < pieces) {
+        l = l_of(c, k, rq);
+        m = m_of(c, k, rq);
       }
+#pragma unroll 1
+      for (int b = 0; b < lt_merge_batches(N); ++b) {
+        const int d0 = ((i % kWarps) * lt_merge_batches(N) + b) * 4;
+        float4 acc[4], o[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) put(own, rq, (i & 3) * 4 + e, acc[e], sum);
+        for (int e = 0; e < 4; ++e) acc[e] = o_of(c, 0, rq, d0 + e);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = o_of(c, 1, rq, d0 + e);  // (a cut tile has two pieces at least)
+        if (b == 0) {
+          m = f4_seen(m, l);
+          float4 M = m;
+#pragma unroll
+          for (int d = 4; d >= 1; d >>= 1) M = f4_max(M, f4_shfl_xor(M, d));
+          w = f4_weight(m, M);
+          float4 sum = make_float4(w.x * l.x, w.y * l.y, w.z * l.z, w.w * l.w);
+#pragma unroll
+          for (int d = 4; d >= 1; d >>= 1) {
+            const float4 x = f4_shfl_xor(sum, d);
+            sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+          }
+          w = make_float4(w.x / sum.x, w.y / sum.y, w.z / sum.z, w.w / sum.w);
+        }
+        float4 wk = f4_shfl(w, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = fma_seen(wk, acc[e], f4(0.f));
+#pragma unroll 1
+        for (int q = 1;;) {
+          wk = f4_shfl(w, q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = fma_seen(wk, o[e], acc[e]);
+          if (++q >= pieces) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = o_of(c, q, rq, d0 + e);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put(own, rq, d0 + e, acc[e]);
+      }
     }
   }
   for (int which = 0; which < 2; ++which) {
@@ -173,7 +209,7 @@ __global__ void __launch_bounds__(kLtMergeThreads, 4) pkv_latent_merge_kernel(co
           acc = fma_seen(f4(1.f), s_acc[i][lane], acc);
           sum = fma_seen(f4(1.f), s_sum[i], sum);
         }
-        put(join, rq, dq, acc, sum);
+        put(join, rq, dq, make_float4(acc.x / sum.x, acc.y / sum.y, acc.z / sum.z, acc.w / sum.w));
       }
       __syncthreads();
     }

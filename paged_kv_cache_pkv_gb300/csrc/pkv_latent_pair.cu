@@ -731,7 +731,7 @@ int launch_latent_pair(const LaunchCtx& ctx, const LatentAttendArgs& a, const La
     cudaLaunchKernelEx(&cfg, pkv_latent_pair_kernel, tq, tk, tv, lp);
     if (int e = ts.done()) return e;
   }
-  cfg.gridDim = dim3(pairs, kPrRows / kLtMergeWarps);
+  cfg.gridDim = dim3(pairs, lt_merge_blocks(kPrRows));
   cfg.blockDim = dim3(kLtMergeThreads);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
