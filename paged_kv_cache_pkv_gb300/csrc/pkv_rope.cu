@@ -104,6 +104,8 @@ __device__ __forceinline__ uint2 to_e4m3(const float* o, float inv) {
 // threads a row, one unit each.
 template <bool F8>
 __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const RopeWriteArgs p) {
+  // What the stream did before: the projections, and calls that read the pools.
+  griddep_wait();
   // Let a dependent attention kernel start its set-up; it reads the pools and
   // the queries after this grid has finished.
   griddep_launch_dependents();
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
 // handles one token at a time: rows of four units (the shared key part and
 // each query head's rotated part) and the latent's 64 vectors.
 __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const LatentWriteArgs p) {
+  griddep_wait();
   griddep_launch_dependents();
   constexpr int kUnits = kLatentRope / 16;  // 4
   constexpr int kRows = kRopeThreads / kUnits;
@@ -253,25 +256,37 @@ dim3 token_grid(const DeviceInfo& dev, int64_t tokens, int rows, int rows_per_bl
   return dim3(unsigned(gx), unsigned(gy));
 }
 
+// Launched while the stream's last kernel may still run, if that is one of this
+// library's (64 tokens 2.4 -> 2.0 us on FP8 pages and 2.6 -> 2.2 on latent ones,
+// between others in a graph).
+template <class Args>
+int launch(const LaunchCtx& ctx, void (*kernel)(Args), dim3 grid, const Args& args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = ctx.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TraceScope ts(ctx.stream, PKV_K_WRITE);
+  cudaLaunchKernelEx(&cfg, kernel, args);
+  return ts.done();
+}
+
 }  // namespace
 
 int launch_write_rope(const LaunchCtx& ctx, const RopeWriteArgs& a, bool fp8) {
   const int rows = (a.q ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
   const dim3 grid = token_grid(*ctx.dev, a.num_tokens, rows, kRopeThreads / (kHeadDim / 16));
-  TraceScope ts(ctx.stream, PKV_K_WRITE);
-  if (fp8)
-    pkv_write_rope_kernel<true><<<grid, kRopeThreads, 0, ctx.stream>>>(a);
-  else
-    pkv_write_rope_kernel<false><<<grid, kRopeThreads, 0, ctx.stream>>>(a);
-  return ts.done();
+  return launch(ctx, fp8 ? pkv_write_rope_kernel<true> : pkv_write_rope_kernel<false>, grid, a);
 }
 
 int launch_write_latent(const LaunchCtx& ctx, const LatentWriteArgs& a) {
   const dim3 grid = token_grid(*ctx.dev, a.num_tokens, a.q_pe ? a.num_heads + 1 : 1,
                                kRopeThreads / (kLatentRope / 16));
-  TraceScope ts(ctx.stream, PKV_K_WRITE);
-  pkv_write_latent_kernel<<<grid, kRopeThreads, 0, ctx.stream>>>(a);
-  return ts.done();
+  return launch(ctx, pkv_write_latent_kernel, grid, a);
 }
 
 }  // namespace pkv
