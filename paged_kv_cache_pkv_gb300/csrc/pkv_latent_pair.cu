@@ -563,14 +563,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
         named_sync(1, kPrSoftmaxThreads);
-        wait(bar_vfree + kPrSlicesV - 1, (gv - 1) & 1);
         if (whole) {
-          // both CTAs need all 128 rows' sums
+          // both CTAs need all 128 rows' sums (said before the wait for the last
+          // P V, which takes as long as the word to the other CTA)
           __syncwarp();
           if (lane == 0) {
             arrive_publish(cluster_addr(bar_inv, 0));
             arrive_publish(cluster_addr(bar_inv, 1));
           }
+        }
+        wait(bar_vfree + kPrSlicesV - 1, (gv - 1) & 1);
+        if (whole) {
           if (ok) ok = __all_sync(0xffffffffu, wait_published(bar_inv, wholes & 1));
           ++wholes;
         }
