@@ -15,8 +15,8 @@
 //    cut into tiles of N = 16, 32, 48 or 64 rows, so any head count fits.  A
 //    tile needs 512 x N fp32 of accumulators and one SM's TMEM holds
 //    512 x 128, all of it: N = 64 leaves room for two score tiles.  Sequences
-//    of more than 64 rows over long tables go to pairs of CTAs
-//    (pkv_latent_pair.cu).
+//    of more than 64 rows go to pairs of CTAs (pkv_latent_pair.cu) unless they
+//    are short.
 //  * The products are computed transposed, with the cache tile as the A
 //    operand of both, straight from shared memory as TMA landed it:
 //      S^T [64 keys x N] = K Q^T      9 x 4 tcgen05.mma, M = 64, K-major A
@@ -24,8 +24,8 @@
 //    Few rows then cost little (N is the short side), where rows as M would
 //    pad them to 64 or 128, and one copy of the tile serves both products.
 //    At N = 64 a tile takes 2500 cycles of shared-memory reads by the two
-//    products, which bounds it; 64 sequences of 512-4096 tokens take 40, 47
-//    and 55 us at 16, 32 and 64 heads, and their bytes 23, 26 and 27.
+//    products, which bounds it; 64 sequences of 512-4096 tokens take 36, 44
+//    and 53 us at 16, 32 and 64 heads, and their bytes 23, 26 and 27.
 //  * A cache tile is 64 keys = 4 pages.  One TMA box a page, from the pool
 //    viewed as [groups of 8 rows][9 chunks of 64 dims][8 rows][64 dims], so
 //    that each (group, chunk) lands as one 128-byte-swizzled 1 KiB atom and
@@ -85,7 +85,7 @@ constexpr int kLtStages = 2;
 // 64 keys of 128 bytes, at the same strides, so P needs no memory of its own
 // and never waits for the P V before it.
 constexpr uint32_t kLtChunkP = (kLtChunks - 1) * 1024;
-constexpr int kLtPairTokens = 2048;  // table width in tokens from which pairs of CTAs take over
+constexpr int kLtPairTokens = 2048;  // table width in tokens from which pairs of CTAs take over (a quarter over context)
 constexpr float kLtTau = 20.0f;  // log2 of how far a score may exceed the reference
 
 // Shared memory (offsets from a 1024-byte aligned base).
@@ -737,13 +737,19 @@ int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a) {
   lp.qscale = a.scale * 1.4426950408889634f;
   const int64_t most = a.max_query_len > 0 && a.max_query_len < a.num_tokens ? a.max_query_len : a.num_tokens;
   const int64_t rows = most * d.num_q_heads;
-  // More than 64 rows a sequence go to pairs of CTAs where sequences may be
-  // long: 128 heads, 64 sequences of 512-4096 tokens 68 us against 78, two
-  // 1023-token chunks over 1536-3584 tokens 583 against 930.  A pair takes
-  // longer to start and to end a tile (128 heads, 256 sequences of 100-400
-  // tokens: 66 us against 60; a 1023-token prompt of 16 heads: 61 against 48),
-  // and how long sequences are is known here only as the tables' width.
-  if (rows > 64 && int64_t(d.max_blocks_per_seq) * kPage >= kLtPairTokens) return launch_latent_pair(ctx, a, lp);
+  // More than 64 rows a sequence go to pairs of CTAs, which take longer to start
+  // and to end a tile but half as long a key: 64 sequences of 128 heads and
+  // 512-4096 tokens 61 us against 77, of 512-1023 tokens 38 against 43; two
+  // 1023-token chunks over 1536-3584 tokens, 64 heads, 553 against 944; a
+  // 512-token chunk over 1500 tokens, 128 heads, 195 against 309.  Not where
+  // tiles are short: four sequences of up to 255 tokens 17 against 10, prompts
+  // of 400-1500 tokens, whose tiles see half of them, 84-567 against 76-528
+  // (2200 tokens: 1021 and 994; 4096 of 16 heads: 342 and 380).  How long
+  // sequences are is known here only as the tables' width, and context only as
+  // what that leaves beside the longest query.
+  const int64_t width = int64_t(d.max_blocks_per_seq) * kPage;
+  if (rows > 64 && (width >= kLtPairTokens || (width >= kLtPairTokens / 4 && most <= width / 2)))
+    return launch_latent_pair(ctx, a, lp);
   // Rows a tile: the least multiple of 16 that cuts the longest sequence's
   // rows into as few tiles as 64 would.
   const int64_t tiles = (rows + 63) / 64;
