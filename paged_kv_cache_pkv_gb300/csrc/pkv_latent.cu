@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const uint32_t tmem = *s_tmem;
   const LtPos begin = plan->begin, end = plan->end;
   const LtWalk first{begin, end, lt_seq<N>(p, begin.b, plan->q0, plan->q1, plan->L)};
-  griddep_launch_dependents();  // (which wait for this grid)
+  // The merge kernel may be scheduled; it waits for this grid.  A kernel of
+  // another call may write before it waits, to memory that the caller takes for
+  // free once this call is behind it on the stream: that one not before the end.
+  if (p.joins) griddep_launch_dependents();
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
   // every lane waits; the warp goes on only if all of them saw the phase
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     const int bar_id = 1 + wg;
     griddep_wait();  // an earlier call may still read the workspace and write to out
     // (here, in the time that the first copies take)
-    if (tid == 0) p.joins[blockIdx.x] = lt_join<N>(p, *plan, int(blockIdx.x), int(gridDim.x));
+    if (tid == 0 && p.joins) p.joins[blockIdx.x] = lt_join<N>(p, *plan, int(blockIdx.x), int(gridDim.x));
     LtWalk walk = first;
     LtPiece x;
     int g = 0;
@@ -639,6 +642,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < N)
       p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + N * kLatentDim + N + tid] = 0.f;
   }
+  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -677,6 +681,12 @@ int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams 
     if (!encode_tensor_map(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.cache, 4, dims, strides, box))
       return PKV_ERR_LAUNCH;
   }
+  // Where the plan cuts no tile there is nothing to join: few tiles (so that
+  // each has CTAs of its own, lt_plan) of sequences no longer than two least
+  // pieces (four sequences of up to 255 tokens: 11.6 -> 10.4 us).
+  const int64_t tiles = int64_t(a.num_tokens) * d.num_q_heads / N + a.num_seqs;
+  const bool cut = int64_t(d.max_blocks_per_seq) * kPage > 2 * kLtLeastOwn || 2 * tiles > ctx.dev->sm_count;
+  if (!cut) lp.joins = nullptr;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -692,11 +702,7 @@ int launch_latent(const LaunchCtx& ctx, const LatentAttendArgs& a, LatentParams 
     cudaLaunchKernelEx(&cfg, pkv_latent_kernel<N>, tq, tkv, lp);
     if (int e = ts.done()) return e;
   }
-  // Where the plan cuts no tile there is nothing to join: few tiles (so that
-  // each has CTAs of its own, lt_plan) of sequences no longer than two least
-  // pieces (four sequences of up to 255 tokens: 11.6 -> 10.4 us).
-  const int64_t tiles = int64_t(a.num_tokens) * d.num_q_heads / N + a.num_seqs;
-  if (int64_t(d.max_blocks_per_seq) * kPage <= 2 * kLtLeastOwn && 2 * tiles <= ctx.dev->sm_count) return PKV_OK;
+  if (!cut) return PKV_OK;
   cfg.gridDim = dim3(ctx.dev->sm_count, lt_merge_blocks(N));
   cfg.blockDim = dim3(kLtMergeThreads);
   cfg.dynamicSmemBytes = 0;

@@ -17,7 +17,7 @@ struct LatentParams {
   // [CTAs] the tile that the CTA's share ends inside (first row, rows, last
   // CTA with a piece of it; 0 rows: none), and the first CTA of the tile that
   // its share begins inside (-1: none)
-  int4* joins;
+  int4* joins;         // nullptr: nothing is cut, and the workspace is not touched
   unsigned* status;
   int32_t B, T, H, max_blocks, num_blocks;
   uint32_t inv_heads;  // floor(2^32 / H), at most 2^32 - 1

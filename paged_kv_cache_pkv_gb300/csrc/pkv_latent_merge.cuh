@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(kLtMergeThreads, 3) pkv_latent_merge_kernel(co
   __shared__ float4 s_max[kLtMergeWarps], s_sum[kLtMergeWarps];
   __shared__ float4 s_w[kLtMergeThreads];  // of a piece; the grid has fewer CTAs
   __shared__ float4 s_acc[kLtMergeWarps][32];
-  griddep_launch_dependents();  // (which wait for this grid)
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // piece i of the tile that c's share ends inside, its partial of CTA `of`
@@ -220,6 +219,10 @@ __global__ void __launch_bounds__(kLtMergeThreads, 3) pkv_latent_merge_kernel(co
       __syncthreads();
     }
   }
+  // Not before the partials are read: pkv_attend's kernel writes to its
+  // workspace, which may be the same memory, before it waits for this grid
+  // (earlier, a call of this kind behind this one gains 2-4 us).
+  griddep_launch_dependents();
 }
 
 }  // namespace

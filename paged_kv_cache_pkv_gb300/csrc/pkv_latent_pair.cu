@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // What each role carries from the first round to a second.  g counts cache
   // tiles, gv those with a P V.  A second round (some score exceeded the
   // reference by too much) walks every piece twice, for maxima first.
-  griddep_launch_dependents();  // (which wait for this grid)
+  griddep_launch_dependents();  // the merge kernel, which waits for this grid
   if (warp < kPrSoftmaxThreads / 32) griddep_wait();  // an earlier call may still read the workspace and write to out
   if (tid == 0 && rank == 0) p.joins[pair] = lt_join<kPrRows>(p, *plan, pair, pairs);
   int g = 0, gv = 0, pieces = 0, wholes = 0;

@@ -106,9 +106,6 @@ template <bool F8>
 __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const RopeWriteArgs p) {
   // What the stream did before: the projections, and calls that read the pools.
   griddep_wait();
-  // Let a dependent attention kernel start its set-up; it reads the pools and
-  // the queries after this grid has finished.
-  griddep_launch_dependents();
   constexpr int kUnits = kHeadDim / 16;  // 8
   constexpr int kRows = kRopeThreads / kUnits;
   const int j = threadIdx.x % kUnits;
@@ -192,6 +189,11 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
       }
     }
   }
+  // Let a dependent attention kernel start its set-up; it reads the pools and
+  // the queries after this grid has finished.  (Not at the start: it stamps
+  // counters in its workspace before that, and the caller may have taken that
+  // memory from this call's inputs.)
+  griddep_launch_dependents();
 }
 
 // Latent pages: row = [512 latent values | 64 rotated key values].  One block
@@ -199,7 +201,6 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
 // each query head's rotated part) and the latent's 64 vectors.
 __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const LatentWriteArgs p) {
   griddep_wait();
-  griddep_launch_dependents();
   constexpr int kUnits = kLatentRope / 16;  // 4
   constexpr int kRows = kRopeThreads / kUnits;
   constexpr int kVecs = kLatentDim / 8;     // 64
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const La
       to[vb] = x.b;
     }
   }
+  griddep_launch_dependents();
 }
 
 // Blocks over tokens, and over the rows of a token while there are few

@@ -259,6 +259,70 @@ def test_two_graphs_share_a_workspace_and_a_stream_of_its_own(pkvlib):
         c.check(o, w)
 
 
+@pytest.mark.parametrize("lens,H,width", [([3000, 200, 77], 16, 1), ([3000, 900, 77], 96, WIDE), ([70, 200, 77], 16, 1)])
+def test_a_workspace_shared_with_the_other_attention(pkvlib, lens, H, width):
+    """One scratch buffer behind both attention calls of a stream: each may
+    begin before the other has ended, and neither touches it before that."""
+    pkv.get_last_error()
+    c = Case(lens, [1, 1, 1], H, seed=15, width=width)
+    args = c.args()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(15)
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)
+    q, kc, vc = normal(3, 32, 128), normal(c.pool.shape[0], 8, 16, 128), normal(c.pool.shape[0], 8, 16, 128)
+    other = (q, kc, vc, *args[2:5], 0.088)
+    want, want_other = pkv.attend_latent(*args), pkv.attend(*other, max_query_len=1)
+    c.check(want)
+    size = max(pkv.workspace_size_latent(pkv.make_latent_desc(c.pool, H, c.tables.shape[1]), 3, 3),
+               pkv.workspace_size(pkv.make_desc(kc, 32, c.tables.shape[1]), 3, 3))
+    ws = torch.full((size,), 255, device="cuda", dtype=torch.uint8)
+    got = []
+    for _ in range(20):
+        got.append((pkv.attend_latent(*args, workspace=ws), pkv.attend(*other, workspace=ws, max_query_len=1)))
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert torch.equal(a.view(torch.int16), want.view(torch.int16))
+        torch.testing.assert_close(b.float(), want_other.float(), rtol=2**-7, atol=1e-2)
+    assert pkv.get_last_error() == 0
+
+
+def test_lengths_written_right_before_each_call(pkvlib):
+    """A decode loop whose lengths, tables and queries are device results of
+    the operations right before the call, eager and captured."""
+    pkv.get_last_error()
+    for H, width in ((16, 1), (96, WIDE)):
+        c = Case([700, 400, 90], [1, 1, 1], H, seed=16, width=width)
+        q, pool, tables, _, qsl, scale = c.args()
+        lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+        steps = [cuda(np.array(x, np.int32)) for x in ([700, 1, 33], [5, 400, 90], [699, 17, 64], [1, 1, 1])]
+        moved = torch.empty_like(tables)
+        want = [pkv.attend_latent(q, pool, tables, x, qsl, scale) for x in steps]
+        torch.cuda.synchronize()
+
+        def loop(outs):
+            for x, out in zip(steps, outs):
+                lens.copy_(x * 2 - x)
+                moved.copy_(tables)
+                pkv.attend_latent(q * 1, pool, moved, lens + 0, qsl, scale, out=out)
+                moved.fill_(-1)  # behind the call: it has read them
+
+        outs = [torch.empty_like(w) for w in want]
+        for _ in range(5):
+            loop(outs)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o.view(torch.int16), w.view(torch.int16)) for o, w in zip(outs, want))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            loop(outs)
+        for _ in range(5):
+            for o in outs:
+                o.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o.view(torch.int16), w.view(torch.int16)) for o, w in zip(outs, want))
+    assert pkv.get_last_error() == 0
+
+
 def test_calls_at_once_on_two_streams(pkvlib):
     """Both kernels fill an SM each; calls on two streams share the GPU and
     nothing else."""
