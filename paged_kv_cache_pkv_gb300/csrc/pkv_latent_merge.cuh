@@ -25,7 +25,7 @@ constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
 // cycles each while all SMs read at once, and fetching its own instructions, so
 // its loops are rolled and it divides once.  Registers hold what is under way:
 // 80 of them, three blocks an SM, with 64 and four blocks it spilled (64 decode
-// rows of 128 heads: 61 us for the call, 64).  Asynchronous copies into shared
+// rows of 128 heads: 61 us for the call, and 64).  Asynchronous copies into shared
 // memory in their place took longer (64 us), as did bulk copies into a ring that
 // eight warps add up (72): fewer warps that add, and blocks that find no room
 // beside the main kernel's CTAs before these end.
