@@ -59,10 +59,6 @@ __device__ __forceinline__ float weight(float m, float M) { return m == -INFINIT
 __device__ __forceinline__ float4 f4_weight(const float4& m, const float4& M) {
   return make_float4(weight(m.x, M.x), weight(m.y, M.y), weight(m.z, M.z), weight(m.w, M.w));
 }
-__device__ __forceinline__ float4 f4_shfl(const float4& v, int lane) {
-  return make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
-                     __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
-}
 __device__ __forceinline__ float4 f4_shfl_xor(const float4& v, int o) {
   return make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
                      __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o));
@@ -110,54 +106,64 @@ __global__ void __launch_bounds__(kLtMergeThreads, 3) pkv_latent_merge_kernel(co
   };
   const int4 own = __ldcg(p.joins + blockIdx.x);
   const bool own_many = own.y > 0 && own.z - int(blockIdx.x) + 1 > kLtFewPieces;
-  if (!own_many) {
+  if (own.y > 0 && !own_many) {
     constexpr int kWarps = 4 / lt_merge_batches(N);  // that share four rows
-    const int c = blockIdx.x, i = blockIdx.y * kLtMergeWarps + warp;
-    const int rq = i / kWarps, pieces = own.z - c + 1;
-    if (rq * 4 < own.y) {
-      // lane k of eight: piece k's weight, divided by the rows' sums
-      const int k = lane & 7;
-      float4 l = f4(0.f), m = f4(-INFINITY), w;
-      if (k < pieces) {
-        l = l_of(c, k, rq);
-        m = m_of(c, k, rq);
+    constexpr int kGroups = kLtMergeWarps / kWarps;  // of four rows, a block
+    const int c = blockIdx.x, group = warp / kWarps, first = int(blockIdx.y) * kGroups;
+    const int rq = first + group, pieces = own.z - c + 1;
+    const bool work = rq * 4 < own.y;
+    float4 acc[4], o[4];
+    auto read = [&](int b) {  // (a cut tile has two pieces at least)
+      const int d0 = (warp % kWarps * lt_merge_batches(N) + b) * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = o_of(c, 0, rq, d0 + e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = o_of(c, 1, rq, d0 + e);
+    };
+    if (work) read(0);
+    if (warp == 0) {
+      // lane (g, k): piece k's weight for the block's rows 4 g .. + 3, divided
+      // by the rows' sums; a warp for all, since every warp for its own rows
+      // takes as long as the reads
+      const int g = lane >> 3, k = lane & 7;
+      float4 l = f4(0.f), m = f4(-INFINITY);
+      if (g < kGroups && k < pieces) {
+        l = l_of(c, k, first + g);
+        m = m_of(c, k, first + g);
       }
+      m = f4_seen(m, l);
+      float4 M = m;
+#pragma unroll
+      for (int d = 4; d >= 1; d >>= 1) M = f4_max(M, f4_shfl_xor(M, d));
+      const float4 w = f4_weight(m, M);
+      float4 sum = make_float4(w.x * l.x, w.y * l.y, w.z * l.z, w.w * l.w);
+#pragma unroll
+      for (int d = 4; d >= 1; d >>= 1) {
+        const float4 x = f4_shfl_xor(sum, d);
+        sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+      }
+      s_w[lane] = make_float4(w.x / sum.x, w.y / sum.y, w.z / sum.z, w.w / sum.w);
+    }
+    __syncthreads();
+    if (work) {
 #pragma unroll 1
       for (int b = 0; b < lt_merge_batches(N); ++b) {
-        const int d0 = ((i % kWarps) * lt_merge_batches(N) + b) * 4;
-        float4 acc[4], o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = o_of(c, 0, rq, d0 + e);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = o_of(c, 1, rq, d0 + e);  // (a cut tile has two pieces at least)
-        if (b == 0) {
-          m = f4_seen(m, l);
-          float4 M = m;
-#pragma unroll
-          for (int d = 4; d >= 1; d >>= 1) M = f4_max(M, f4_shfl_xor(M, d));
-          w = f4_weight(m, M);
-          float4 sum = make_float4(w.x * l.x, w.y * l.y, w.z * l.z, w.w * l.w);
-#pragma unroll
-          for (int d = 4; d >= 1; d >>= 1) {
-            const float4 x = f4_shfl_xor(sum, d);
-            sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
-          }
-          w = make_float4(w.x / sum.x, w.y / sum.y, w.z / sum.z, w.w / sum.w);
-        }
-        float4 wk = f4_shfl(w, 0);
+        if (b > 0) read(b);
+        float4 wk = s_w[group * 8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[e] = fma_seen(wk, acc[e], f4(0.f));
 #pragma unroll 1
         for (int q = 1;;) {
-          wk = f4_shfl(w, q);
+          wk = s_w[group * 8 + q];
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] = fma_seen(wk, o[e], acc[e]);
           if (++q >= pieces) break;
+          const int d0 = (warp % kWarps * lt_merge_batches(N) + b) * 4;
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = o_of(c, q, rq, d0 + e);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) put(own, rq, d0 + e, acc[e]);
+        for (int e = 0; e < 4; ++e) put(own, rq, (warp % kWarps * lt_merge_batches(N) + b) * 4 + e, acc[e]);
       }
     }
   }
