@@ -24,18 +24,18 @@ constexpr int kLtPartialFloats = 64 * kLatentDim + 2 * 64;
 // another (the join record, then O; O does not wait for the weights), at 2000
 // cycles each while all SMs read at once, and fetching its own instructions, so
 // its loops are rolled and it divides once.  Registers hold what is under way:
-// 80 of them, three blocks an SM, with 64 and four blocks it spilled (64 decode
-// rows of 128 heads: 61 us for the call, and 64).  Asynchronous copies into shared
-// memory in their place took longer (64 us), as did bulk copies into a ring that
-// eight warps add up (72): fewer warps that add, and blocks that find no room
-// beside the main kernel's CTAs before these end.
+// 80 of them and three blocks an SM (64 decode rows of 128 heads 61.9 us for the
+// call; with 64 and four blocks 63.4, with 128 and two 64.6).  Asynchronous
+// copies into shared memory in their place took 3 us longer, and bulk copies into
+// a ring that eight warps add up 10: fewer warps that add, and blocks that find
+// no room beside the main kernel's CTAs before these end.
 constexpr int kLtMergeThreads = 256;
 constexpr int kLtMergeWarps = kLtMergeThreads / 32;
 constexpr int kLtFewPieces = 6;
 constexpr int kLtBatch = 8;  // pieces that a warp has under way
 
 // Batches of four times 32 dims that a warp goes through for its rows, and the
-// blocks a CTA of the main kernel that makes: tiles of many rows in one wave.
+// blocks a CTA of the main kernel that makes.
 constexpr int lt_merge_batches(int N) { return N >= 64 ? 2 : 1; }
 constexpr int lt_merge_blocks(int N) { return N / kLtMergeWarps / lt_merge_batches(N); }
 

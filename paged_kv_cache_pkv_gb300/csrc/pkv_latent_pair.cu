@@ -40,7 +40,7 @@
 // takes 3200 cycles there: with one buffer each, a slice's way from being let
 // go of to being here again (2300 cycles, 400 of them for the word to the other
 // CTA) and its product follow one another, and neither product has work while
-// both wait.  64 decode rows of 128 heads over 512-4096 tokens: 63 us; a share is
+// both wait.  64 decode rows of 128 heads over 512-4096 tokens: 62 us; a share is
 // 16 tiles there, and the 13000 cycles from the last P V of one piece to the
 // first of the next (result out, 72 KiB of queries and the first K and V in)
 // cost as much as four of them.  Of a whole tile's 11000 the result takes 6000,
