@@ -80,8 +80,8 @@ struct PrSmem {
   static constexpr uint32_t tmem = bars + 272;
   static constexpr uint32_t flags = tmem + 8;                  // own, the other CTA's
   static constexpr uint32_t plan = tmem + 16;                  // LtPlan
-  static constexpr uint32_t inv = plan + 128;                  // [128] 1 / row sums
-  static constexpr uint32_t red = inv + 512;                   // [4][64] partial sums, maxima
+  static constexpr uint32_t inv = plan + 128;                  // [2 whole tiles][64] 1 / row sums of the other CTA's rows
+  static constexpr uint32_t red = inv + 512;                   // [4][64] partial sums, maxima; own rows' 1 / row sums
   static constexpr uint32_t wsum = red;                        // plan scans
   static constexpr uint32_t end = red + 1024;
   static constexpr uint32_t bytes = end + 1024;                // + alignment slack
@@ -555,9 +555,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (part_of_row == 0) {
           const float sum = (s_red[row] + s_red[kPrOwn + row]) + (s_red[2 * kPrOwn + row] + s_red[3 * kPrOwn + row]);
           if (whole) {
+            // Into the other CTA by turns: it may still be at the result of
+            // the whole tile before, which takes the other buffer.  That one
+            // is free: all of its warps have said (bar_inv) that they have
+            // this CTA's rows' sums of the tile before, behind their last read
+            // of the one before that.  Own rows' go where this thread's
+            // partial sums were.
             const float inv = 1.f / sum;
-            s_inv[rank * kPrOwn + row] = inv;
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(s_inv + rank * kPrOwn + row, rank ^ 1)),
+            s_red[row] = inv;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                             cluster_addr(s_inv + (wholes & 1) * kPrOwn + row, rank ^ 1)),
                          "f"(inv)
                          : "memory");
           } else {
@@ -576,6 +583,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
         wait(bar_vfree + kPrSlicesV - 1, (gv - 1) & 1);
+        const float* s_other = s_inv + (wholes & 1) * kPrOwn;
         if (whole) {
           if (ok) ok = __all_sync(0xffffffffu, wait_published(bar_inv, wholes & 1));
           ++wholes;
@@ -605,6 +613,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const int e = wg;
 #pragma unroll 1
           for (int r1 = 0; r1 < x.rows; r1 += 32) {
+            const float* s_of = ((r1 >> 6) == rank ? s_red : s_other) + (r1 & (kPrOwn - 1));
             float o[32];
             tmem_ld32f(tmem + uint32_t(e * kPrRows + r1) + lane_off, o);
             // even lanes take the first row's pair of dims, odd lanes the
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             uint8_t* to = stage + (lane & 1) * 512 + ((e * 256 + quad * 64 + (lane >> 1) * 4) ^ ((lane & 1) << 6));
 #pragma unroll
             for (int c = 0; c < 32; c += 4) {
-              const float4 inv = *reinterpret_cast<const float4*>(s_inv + r1 + c);
+              const float4 inv = *reinterpret_cast<const float4*>(s_of + c);
               const float v[4] = {o[c] * inv.x, o[c + 1] * inv.y, o[c + 2] * inv.z, o[c + 3] * inv.w};
 #pragma unroll
               for (int h = 0; h < 4; h += 2) {
