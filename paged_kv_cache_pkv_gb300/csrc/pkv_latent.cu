@@ -184,6 +184,11 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Bytes that a phase of the barrier waits for, beside its arrivals.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // kind::f16 instruction descriptor: bf16 A and B, fp32 D.
 constexpr uint32_t lt_idesc(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
@@ -310,13 +315,16 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         }
         const int st = g % kLtStages;
         if (lane == 0) {
-          // page by page, as P V of the tile two before lets go of them
+          // page by page, as P V of the tile two before lets go of them.  The
+          // arrival comes behind the last page's wait, also where that page
+          // is not loaded: what follows it writes P over all four, and zeros
+          // behind the sequence's end.
           int sent = 0;
 #pragma unroll
           for (int i = 0; i < kLtPages; ++i) {
             if (g >= kLtStages && ok) ok = mbar_wait(bar_kvfree + st * kLtPages + i, (g / kLtStages - 1) & 1);
             if (!ok) break;
-            if (i == 0) mbar_arrive_expect_tx(bar_kv + st, uint32_t(valid) * kLtPageBytes);
+            if (i == 0) mbar_expect_tx(bar_kv + st, uint32_t(valid) * kLtPageBytes);
             if (id[i] >= 0) {
               tma_load_4d(sm + S::kv + st * kLtTileBytes + i * kLtPageBytes, &tm_kv, 0, 0, 0, 2 * id[i], bar_kv + st);
               ++sent;
@@ -327,7 +335,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
             asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar_kv + st)),
                          "r"(uint32_t(valid - sent) * kLtPageBytes)
                          : "memory");
-          if (sent > 0) landing = g + 1;
+          if (sent > 0) {  // (a tile's first page is always loaded)
+            mbar_arrive(bar_kv + st);
+            landing = g + 1;
+          }
         }
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         if (!ok) break;

@@ -31,22 +31,24 @@ def rising(c, step=0.25):
 
 def check_repeatedly(c, times=40, **kw):
     """Every call the same bits, the first within the bound; meanwhile copies on
-    another stream delay some SMs' memory more than others'."""
+    another stream take the memory, and the instructions out of the caches, so
+    that single warps fall behind by microseconds."""
     pkv.get_last_error()
     args = c.args()
     ws = torch.empty(pkv.workspace_size_latent(pkv.make_latent_desc(c.pool, c.H, c.tables.shape[1]), len(c.lens),
                                                c.q.shape[0]), dtype=torch.uint8, device="cuda")
     noise = torch.empty(2, 1 << 26, device="cuda", dtype=torch.uint8)
     side = torch.cuda.Stream()
-    torch.cuda.synchronize()
-    outs = []
-    for _ in range(times):
-        with torch.cuda.stream(side):
-            noise[0].copy_(noise[1])
-        outs.append(pkv.attend_latent(*args, workspace=ws, **kw))
-    torch.cuda.synchronize()
-    c.check(outs[0])
-    assert all(torch.equal(outs[0].view(torch.int16), o.view(torch.int16)) for o in outs)
+    first = pkv.attend_latent(*args, workspace=ws, **kw)
+    c.check(first)
+    for i in range(0, times, 20):
+        outs = []
+        for _ in range(min(20, times - i)):
+            with torch.cuda.stream(side):
+                noise[0].copy_(noise[1])
+            outs.append(pkv.attend_latent(*args, workspace=ws, **kw))
+        torch.cuda.synchronize()
+        assert all(torch.equal(first.view(torch.int16), o.view(torch.int16)) for o in outs)
     assert pkv.get_last_error() == 0
 
 
@@ -79,3 +81,34 @@ def test_a_second_round_over_several_pieces_on_pairs(pkvlib, H, most):
     c = Case(lens, 1 + np.arange(90) % most, H, seed=25, width=WIDE)
     rising(c)
     check_repeatedly(c, times=10)
+
+
+@pytest.mark.parametrize("H", [16, 20, 40, 64])
+def test_equal_shares_on_single_ctas(pkvlib, H):
+    """Most sequences' last tile has pages that are not loaded; what is written
+    over them must not come before the tile two before is done with them."""
+    lens = lengths(26 + H, 170, 1, 300)
+    check_repeatedly(Case(lens, np.ones(170, int), H, seed=26), times=500, max_query_len=1)
+
+
+@pytest.mark.parametrize("H", [12, 64])
+def test_tiles_cut_among_several_ctas(pkvlib, H):
+    lens = np.concatenate([lengths(28, 90, 1, 200), [9000, 2049], lengths(29, 70, 1, 200), [4096]])
+    check_repeatedly(Case(lens, np.ones(len(lens), int), H, seed=28), times=10, max_query_len=1)
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_references_raised_over_several_pieces_on_single_ctas(pkvlib, H):
+    lens = lengths(30, 170, 1, 300)
+    c = Case(lens, np.ones(170, int), H, seed=30)
+    rising(c)
+    check_repeatedly(c, times=10, max_query_len=1)
+
+
+def test_more_sequences_than_a_warp_of_the_plan_scans_at_once(pkvlib):
+    """As many sequences as a call takes, some without rows, some without
+    tokens."""
+    lens = lengths(31, 2048, 0, 40)
+    q_lens = np.minimum(lens, lengths(32, 2048, 0, 1))
+    check_repeatedly(Case(lens, q_lens, 8, seed=31), times=5, max_query_len=1)
+    check_repeatedly(Case(lens, q_lens, 72, seed=31, width=WIDE), times=5, max_query_len=1)
