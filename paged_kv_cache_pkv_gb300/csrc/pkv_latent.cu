@@ -487,14 +487,16 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         if (k == x.k0) {
           // A piece's first reference is its first key's score.  Rows that do
           // not see that key see nothing of this piece (what a row sees is a
-          // prefix) and keep 0.
+          // prefix) and keep 0.  (Through s_red, whose readers of the piece
+          // before are behind a barrier: of s_alpha a slower warp may still
+          // read that piece's 1 / row sums.)
           if (key == 0) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) s_alpha[col0 + c] = xs[c] == -INFINITY ? 0.f : xs[c];
+            for (int c = 0; c < NC; ++c) s_red[col0 + c] = xs[c] == -INFINITY ? 0.f : xs[c];
           }
           named_sync(bar_id, 128);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) m[c] = s_alpha[col0 + c];
+          for (int c = 0; c < NC; ++c) m[c] = s_red[col0 + c];
           relative();
         }
         float top = xs[0];

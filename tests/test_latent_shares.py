@@ -91,6 +91,14 @@ def test_equal_shares_on_single_ctas(pkvlib, H):
     check_repeatedly(Case(lens, np.ones(170, int), H, seed=26), times=500, max_query_len=1)
 
 
+def test_whole_tiles_follow_each_other_on_single_ctas(pkvlib):
+    """Prompts whose tiles of 64 rows are one to four steps long, a dozen whole
+    ones a CTA: each begins with new references where the one before ended with
+    its row sums."""
+    lens = [250, 64, 100, 130, 192, 7]
+    check_repeatedly(Case(lens, lens, 128, seed=27), max_query_len=250)
+
+
 @pytest.mark.parametrize("H", [12, 64])
 def test_tiles_cut_among_several_ctas(pkvlib, H):
     lens = np.concatenate([lengths(28, 90, 1, 200), [9000, 2049], lengths(29, 70, 1, 200), [4096]])
