@@ -655,10 +655,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     if (begin.k > 0 && begin.b == end.b && begin.j == end.j && begin.k == end.k && tid < N)
       p.partials[size_t(blockIdx.x) * 2 * kLtPartialFloats + N * kLatentDim + N + tid] = 0.f;
   }
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  griddep_launch_dependents();  // behind the barrier: one thread of a CTA speaks for all
   if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
 }

@@ -192,7 +192,9 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
   // Let a dependent attention kernel start its set-up; it reads the pools and
   // the queries after this grid has finished.  (Not at the start: it stamps
   // counters in its workspace before that, and the caller may have taken that
-  // memory from this call's inputs.)
+  // memory from this call's inputs.  And behind a barrier: a block's first
+  // thread to say so speaks for all of them, also for those still reading.)
+  __syncthreads();
   griddep_launch_dependents();
 }
 
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const La
       to[vb] = x.b;
     }
   }
+  __syncthreads();  // as above
   griddep_launch_dependents();
 }
 
