@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const LtWalk first{begin, end, lt_seq<N>(p, begin.b, plan->q0, plan->q1, plan->L)};
   // The merge kernel may be scheduled; it waits for this grid.  A kernel of
   // another call may write before it waits, to memory that the caller takes for
-  // free once this call is behind it on the stream: that one not before the end.
+  // free once this call is behind it on the stream: that one not before this
+  // call has read everything.
   if (p.joins) griddep_launch_dependents();
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 
@@ -357,6 +358,11 @@ __global__ void __launch_bounds__(kLtThreads, 1)
         mbar_wait(bar_kv + i % kLtStages, (i / kLtStages) & 1, limit);
       if (pieces > 0) mbar_wait(bar_q, (pieces - 1) & 1, limit);
       if (!ok) flag_status(p.status, PKV_STATUS_TIMEOUT);
+      // Where nothing is joined a share is one whole tile at most, and with its
+      // copies landed this CTA has read all that it reads: a kernel let in now
+      // waits for what is left (four short sequences behind one another 10.7 us
+      // a call without this, 8.7 with it).
+      if (ok && pieces > 0 && !p.joins) griddep_launch_dependents();
     }
     __syncwarp();
   } else if (warp == 9) {
