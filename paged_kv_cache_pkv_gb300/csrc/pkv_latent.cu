@@ -495,10 +495,13 @@ __global__ void __launch_bounds__(kLtThreads, 1)
           // not see that key see nothing of this piece (what a row sees is a
           // prefix) and keep 0.  (Through s_red, whose readers of the piece
           // before are behind a barrier: of s_alpha a slower warp may still
-          // read that piece's 1 / row sums.)
+          // read that piece's 1 / row sums.)  Rows behind the tile's last, the
+          // next sequence's or what a padded batch holds, take infinity, so
+          // that no score of theirs ever moves the tile's references.
           if (key == 0) {
 #pragma unroll
-            for (int c = 0; c < NC; ++c) s_red[col0 + c] = xs[c] == -INFINITY ? 0.f : xs[c];
+            for (int c = 0; c < NC; ++c)
+              s_red[col0 + c] = col0 + c >= x.rows ? INFINITY : xs[c] == -INFINITY ? 0.f : xs[c];
           }
           named_sync(bar_id, 128);
 #pragma unroll

@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             m = fmaxf(fmaxf(s_red[row], s_red[kPrOwn + row]), fmaxf(s_red[2 * kPrOwn + row], s_red[3 * kPrOwn + row]));
             if (m == -INFINITY) m = 0.f;
             named_sync(1, kPrSoftmaxThreads);
-          } else if (top > kPrTau) {
-            over = true;
+          } else if (top > kPrTau && rank * kPrOwn + row < x.rows) {
+            over = true;  // (rows behind the tile's last are another sequence's, or padding)
           }
         }
 

@@ -120,3 +120,23 @@ def test_more_sequences_than_a_warp_of_the_plan_scans_at_once(pkvlib):
     q_lens = np.minimum(lens, lengths(32, 2048, 0, 1))
     check_repeatedly(Case(lens, q_lens, 8, seed=31), times=5, max_query_len=1)
     check_repeatedly(Case(lens, q_lens, 72, seed=31, width=WIDE), times=5, max_query_len=1)
+
+
+@pytest.mark.parametrize("H,width", [(20, 1), (40, 1), (70, 1), (70, WIDE), (96, WIDE)])
+def test_a_row_goes_by_its_own_tile_alone(pkvlib, H, width):
+    """A tile's copy of queries runs on into the next sequence's, or into tokens
+    behind the last one: whatever these hold, a sequence's bits stay the same."""
+    pkv.get_last_error()
+    c = Case([300, 900, 77], [1, 1, 1], H, seed=33, extra_tokens=4, width=width)
+    want = pkv.attend_latent(*c.args(), max_query_len=1)
+    c.check(want)
+    q0 = c.q.clone()
+    for value in (3e4, -3e4, 3e38, float("inf"), float("nan")):
+        for tokens in ([1], [2], [3, 4, 5, 6]):
+            c.q.copy_(q0)
+            c.q[tokens] *= value
+            got = pkv.attend_latent(*c.args(), max_query_len=1)
+            others = [b for b in range(3) if b not in tokens]
+            same = torch.equal(got[others].view(torch.int16), want[others].view(torch.int16))
+            assert same, (value, tokens)
+    assert pkv.get_last_error() == 0
