@@ -146,15 +146,20 @@ struct Stream {
   }
 };
 
+// Without the interpreter's lock for as long as it lives, however that ends.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // call(): the entry point's code, with device `index` current.
 template <class F>
 void run(const char* what, int index, F call) {
   int code;
   {
     c10::cuda::CUDAGuard guard{c10::DeviceIndex(index)};
-    Py_BEGIN_ALLOW_THREADS;
+    Unlocked unlocked;
     code = call();
-    Py_END_ALLOW_THREADS;
   }
   if (code != PKV_OK) {
     PyObject* args = Py_BuildValue("(is)", code, what);
@@ -364,10 +369,12 @@ PyObject* attend_latent(PyObject* const* a, Py_ssize_t n) {
   }
   void* ws = inout<void>(scratch);
   const size_t ws_bytes = size_t(scratch.size(0));
+  // (here, with the interpreter's lock: a tensor without memory of its own raises)
+  const auto *qp = in<pkv_bf16>(q), *cache = in<pkv_bf16>(pool);
+  const int32_t *bt = in<int32_t>(tables), *sl = in<int32_t>(lens), *starts = in<int32_t>(qsl);
   run("pkv_attend_latent", index, [&] {
-    return g_attend_latent(in<pkv_bf16>(q), in<pkv_bf16>(pool), in<int32_t>(tables), in<int32_t>(lens),
-                           in<int32_t>(qsl), seqs, tokens, max_query_len, float(scale), out, ws, ws_bytes, &desc,
-                           stream.handle);
+    return g_attend_latent(qp, cache, bt, sl, starts, seqs, tokens, max_query_len, float(scale), out, ws, ws_bytes,
+                           &desc, stream.handle);
   });
   return result(a[8], made);
 }
