@@ -508,8 +508,9 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
       s_q0[b] = q0;
       s_len[b] = L;
       if (b == p.B - 1) s_q0[p.B] = q1;
-      const bool bad = q0 < 0 || n < 0 || q1 > p.T || n > L || L < 0 ||
-                       (L + kPage - 1) / kPage > p.max_blocks || (b == 0 && q0 != 0);
+      // (any int32 may stand there: no sum of them, and L - 1 only where L > 0)
+      const bool bad = q0 < 0 || q1 < q0 || q1 > p.T || L < 0 || n > L ||
+                       (L > 0 && (L - 1) / kPage >= p.max_blocks) || (b == 0 && q0 != 0);
       if (bad && blockIdx.x == 0) flag_status(p.status, PKV_STATUS_BAD_QUERY);
       int units = 0;
       if (!bad && n >= 1 && n <= p.simt_max_q) {

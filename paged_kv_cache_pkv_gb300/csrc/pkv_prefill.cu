@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(kPfThreadsOf<F8>, 1)
     for (int bb = b0; bb < b1; ++bb) {
       const int qq0 = __ldg(p.qsl + bb), q1 = __ldg(p.qsl + bb + 1), LL = __ldg(p.seq_lens + bb);
       const int nn = q1 - qq0;
-      const bool bad = qq0 < 0 || nn < 0 || q1 > p.T || nn > LL || LL < 0 ||
-                       (LL + kPage - 1) / kPage > p.max_blocks || (bb == 0 && qq0 != 0);
+      const bool bad = qq0 < 0 || q1 < qq0 || q1 > p.T || LL < 0 || nn > LL ||
+                       (LL > 0 && (LL - 1) / kPage >= p.max_blocks) || (bb == 0 && qq0 != 0);
       const int groups = (!bad && nn > p.split_max_q) ? (nn + TG - 1) / TG : 0;
       s_scan[bb] = groups;
       local += groups;
