@@ -167,9 +167,9 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu(const unsigned long
 }
 
 // Arrival on a counter word that holds a 48-bit launch epoch over a 16-bit
-// count.  The launch stamps (epoch, 0) into the word before any arrival can
-// happen, but the stamp may not be visible yet, and an add that reaches the
-// word before it is overwritten by it.  So: one add (the usual case, the
+// count.  The launch stamps (epoch, 0) into the word at its start, but the
+// stamp may not be there yet, and an add that reaches the word before it is
+// overwritten by it.  So: one add (the usual case, the
 // stamp is there); if the word still held an older epoch, plain loads wait
 // for the stamp (bounded) and the add is made again.  No arrival adds twice
 // into an older epoch's word, so with fewer than 32768 arrivals per launch

@@ -479,22 +479,11 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
   // (plan, cursor, first block ids, L2 prefetch hints) overlaps the previous
   // kernel (pkv_write, the shared-prefix pass, or a chunked-prefill pass that
   // runs first).  It reads only seq_lens, query_start_loc and block_tables,
-  // which none of them writes; the pools and the workspace records are read
-  // only after the wait.
+  // which none of them writes, and writes nothing but status bits; the pools
+  // and the workspace records are read only after the wait.
 
   // ---- plan: per-sequence unit counts and their exclusive prefix ----------
   const int per_row = p.Hkv * p.nsub;
-  // Stamp this launch's epoch (count 0) into every arrival counter, a share
-  // per thread, so that arrivals are single atomic adds.  A counter is first
-  // hit when a warp finishes a split item, long after these stamps; an
-  // arrival that still sees an old epoch adds again once it is stamped.
-#ifndef PKV_TEST_NO_EPOCH_STAMP  // a test build leaves the counters unstamped: arrivals time out
-  for (int i = blockIdx.x * NT + threadIdx.x; i < p.T * per_row; i += gridDim.x * NT)
-    atomicExch(p.counters + i, p.epoch << 16);
-#endif
-  // the prefill pass launched after this kernel counts its exits here (it
-  // launches only once this CTA has passed its trigger below, or exited)
-  if (p.lead && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.join, p.epoch << 16);
   __shared__ long long s_pfw[NW];
   long long lead_steps = 0;  // lead: K/V tile steps of the prefill pass, all its CTAs
   {
@@ -593,11 +582,29 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
   // shatter into one-page partials
   const int chunk = max(kMinChunk, (U + nw - 1) / nw);
   const int w = blockIdx.x * NW + wib;
+  // Stamp this launch's epoch (count 0) into every arrival counter, a share
+  // per thread, so that arrivals are single atomic adds.  Behind the wait: the
+  // workspace may be memory that the kernel before still reads, such as
+  // pkv_write's inputs, which are the caller's again once that call is behind
+  // on the stream.  A counter is first hit when a warp finishes a split item,
+  // long after these stamps; an arrival that still sees an old epoch adds
+  // again once it is stamped.  The prefill pass launched after this kernel
+  // counts its exits in p.join in the same way.
+  auto stamp = [&] {
+#ifndef PKV_TEST_NO_EPOCH_STAMP  // a test build leaves the counters unstamped: arrivals time out
+    for (int i = blockIdx.x * NT + threadIdx.x; i < p.T * per_row; i += gridDim.x * NT)
+      atomicExch(p.counters + i, p.epoch << 16);
+#endif
+    if (p.lead && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.join, p.epoch << 16);
+  };
   if (w >= nw || int64_t(w) * chunk >= U) {
     // lead: this CTA's exit may let the prefill pass launch, which must not
-    // happen before the pool writes are complete; beside the pass: the call
+    // happen before the pool writes are complete; beside the pass (which began
+    // behind everything before it and leaves the counters alone): the call
     // ends with this grid, so it must not end before the pass
-    if (p.lead || !p.wait_prev) griddep_wait();
+    if (p.wait_prev) griddep_wait();
+    stamp();
+    if (!p.wait_prev) griddep_wait();
     return;
   }
   const int u_begin = w * chunk;
@@ -679,6 +686,7 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
       if (s + 1 < n_units) cursor_advance(pc, p, sq, per_row);
     }
   }
+  stamp();  // in the time that the first copies take
 
   // ---- consumer state ----------------------------------------------------------
   // MMA fragments: lane = (gq = lane/4, tq = lane%4).  qb: Q^T operand of head

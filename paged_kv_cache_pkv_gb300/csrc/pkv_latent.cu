@@ -247,10 +247,10 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   const uint32_t tmem = *s_tmem;
   const LtPos begin = plan->begin, end = plan->end;
   const LtWalk first{begin, end, lt_seq<N>(p, begin.b, plan->q0, plan->q1, plan->L)};
-  // The merge kernel may be scheduled; it waits for this grid.  A kernel of
-  // another call may write before it waits, to memory that the caller takes for
-  // free once this call is behind it on the stream: that one not before this
-  // call has read everything.
+  // The merge kernel may be scheduled; it waits for this grid.  A kernel that
+  // is not this library's may write before it waits, to memory that the caller
+  // has back once this call is behind it on the stream: what follows the call
+  // is let in no sooner than the call has read everything.
   if (p.joins) griddep_launch_dependents();
   auto tmem_s = [&](int g) { return tmem + 256u + uint32_t(g & 1) * 64u; };
 

@@ -225,10 +225,11 @@ __global__ void __launch_bounds__(kLtMergeThreads, 3) pkv_latent_merge_kernel(co
       __syncthreads();
     }
   }
-  // Not before the partials are read: pkv_attend's kernel writes to its
-  // workspace, which may be the same memory, before it waits for this grid
-  // (earlier, a call of this kind behind this one gains 2-4 us).  A block's
-  // first thread to say so speaks for all of them, hence the barrier.
+  // Not before the partials are read: the workspace is the caller's again
+  // behind this call on the stream, and a kernel let in, if it is not one of
+  // this library's, may write to it before it waits (earlier, a call of this
+  // kind behind this one gains 2-4 us).  A block's first thread to say so
+  // speaks for all of them, hence the barrier.
   __syncthreads();
   griddep_launch_dependents();
 }

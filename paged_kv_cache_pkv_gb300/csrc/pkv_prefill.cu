@@ -246,10 +246,9 @@ __global__ void __launch_bounds__(kPfThreadsOf<F8>, 1)
   // the SMs this grid leaves free, beside this compute-bound pass (it reads
   // nothing this writes, and waits for this grid before it exits).  Mixed
   // step 329 -> 306 us.  Not for the shared-prefix pass: there it made the
-  // step 6 % slower.  Run behind split-KV: no early start for what follows
-  // (the next call's split-KV kernel would stamp its counters while this
-  // call's still merges); it launches once every CTA here has exited, the
-  // last of them after the split-KV kernel completed.
+  // step 6 % slower.  Run behind split-KV: no early start for what follows;
+  // it launches once every CTA here has exited, the last of them after the
+  // split-KV kernel completed.
   if constexpr (!PREFIX) {
     if (!p.join) griddep_launch_dependents();
   }

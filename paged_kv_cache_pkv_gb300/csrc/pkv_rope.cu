@@ -190,10 +190,11 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
     }
   }
   // Let a dependent attention kernel start its set-up; it reads the pools and
-  // the queries after this grid has finished.  (Not at the start: it stamps
-  // counters in its workspace before that, and the caller may have taken that
-  // memory from this call's inputs.  And behind a barrier: a block's first
-  // thread to say so speaks for all of them, also for those still reading.)
+  // the queries after this grid has finished.  (Not at the start: a kernel that
+  // is not one of this library's may write before it waits, to memory that the
+  // caller has back from this call's inputs.  And behind a barrier: a block's
+  // first thread to say so speaks for all of them, also for those still
+  // reading.)
   __syncthreads();
   griddep_launch_dependents();
 }

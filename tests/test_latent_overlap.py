@@ -1,8 +1,7 @@
 """Calls behind one another on a stream, where the next one's kernel is let in
-before the last one's has ended: pkv_attend stamps counters in its workspace
-before it waits.  That memory may be what the call before has just been given
-as inputs or scratch and no longer needs: a stream's order is all a caller
-owes it."""
+before the last one's has ended: pkv_attend stamps counters in its workspace.
+That memory may be what the call before has just been given as inputs or
+scratch and no longer needs: a stream's order is all a caller owes it."""
 
 import numpy as np
 import pytest
@@ -127,5 +126,37 @@ def test_counters_over_the_inputs_of_a_latent_append(pkvlib, T, H):
         pkv.write_latent(kv[:, :512], kv[:, 512:], *meta, cache, q_pe=qp, q_out=q, interleaved=True)
         stamp(buf)
         assert np.array_equal(bits(cache), want) and np.array_equal(bits(q), want_q)
+    stamp.check()
+    assert pkv.get_last_error() == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,hkv", [(64, 8), (4001, 8), (9001, 2)])
+def test_counters_over_the_inputs_of_a_plain_append(pkvlib, T, hkv, fp8):
+    """pkv_write and pkv_write_fp8 let the next kernel in as they start."""
+    pkv.get_last_error()
+    stamp = Stamper(2 * T * hkv * 256)
+    rng = np.random.default_rng(T)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(T)
+    pages = -(-T // 16) + 1
+    src = torch.randn(2, T, hkv, 128, generator=gen, device="cuda").to(torch.bfloat16)
+    slots = cuda(rng.permutation(pages * 16)[:T])
+    buf = torch.zeros(max(stamp.need, src.numel() * 2), dtype=torch.uint8, device="cuda")
+    k, v = buf[:src.numel() * 2].view(torch.bfloat16).view(src.shape)
+    kind = torch.uint8 if fp8 else torch.bfloat16
+    shapes = [(pages, hkv, 16, 128)] * 2 + [(pages, hkv, 16)] * (2 * fp8)
+    append = pkv.write_fp8 if fp8 else pkv.write
+    want = [torch.zeros(s, dtype=kind, device="cuda") for s in shapes]
+    append(src[0], src[1], slots, *want)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        k.copy_(src[0])
+        v.copy_(src[1])
+        pools = [torch.zeros(s, dtype=kind, device="cuda") for s in shapes]
+        append(k, v, slots, *pools)
+        stamp(buf)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(pools, want))
     stamp.check()
     assert pkv.get_last_error() == 0
