@@ -169,14 +169,16 @@ PKV_API int pkv_attend_workspace_size(const pkv_desc* desc, int32_t num_seqs,
  * set-up (reading seq_lens, query_start_loc and block_tables, and L2
  * prefetch hints for the first pages) overlaps the write kernel through
  * programmatic dependent launch; the pools are read only after the write has
- * finished.  Those three arrays must therefore not be
- * written by the pkv_write call right before it (pkv_write never does).
+ * finished.  Those three arrays must therefore not be written by a kernel
+ * right before the call that lets its dependents start early: no call of this
+ * library writes them, and a kernel of the caller's that does must leave out
+ * that early start (griddepcontrol.launch_dependents).
  * A call with query chunks longer than PKV_SPLITKV_MAX_QLEN runs its split-KV
  * kernel and its tensor-core prefill kernel at the same time on disjoint
  * SMs; work enqueued on the stream after the call still starts only once
  * both have finished.  The SM share follows the two kernels' work; it is
  * scaled by the environment variables PKV_PREFILL_STEP_UNITS (bf16 pages,
- * default 1900) and PKV_PREFILL_STEP_UNITS_FP8 (default 10000), read once
+ * default 2400) and PKV_PREFILL_STEP_UNITS_FP8 (default 5000), read once
  * per process; 0 runs the prefill kernel first instead, with split-KV beside
  * it on the SMs it leaves free.  With shared_prefix_pages > 0 the prefill kernel always runs
  * first. */
@@ -374,8 +376,9 @@ PKV_API int pkv_attend_latent_workspace_size(const pkv_desc* desc, int32_t num_s
  *                  tables' width whether pairs of SMs share a tile: results are
  *                  right whatever it says, their last bits may differ.
  * As in pkv_attend, seq_lens, query_start_loc and block_tables are read while
- * the library call right before this one on the stream may still run, which
- * must therefore not write them (none does).
+ * the kernel right before the call on the stream may still run, if it lets its
+ * dependents start early: such a kernel, of the caller's too, must not write
+ * them (none of this library's does).
  * out must not overlap q, the pool or the workspace; calls that may overlap on
  * the GPU need workspaces of their own.  PKV_ERR_RANGE where num_tokens *
  * num_q_heads, num_blocks * 2 or max_blocks_per_seq * 16 come near 2^31.

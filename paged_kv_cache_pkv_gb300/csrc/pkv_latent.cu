@@ -189,12 +189,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// kind::f16 instruction descriptor: bf16 A and B, fp32 D.
-constexpr uint32_t lt_idesc(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
-}
-
 template <int N>
 __global__ void __launch_bounds__(kLtThreads, 1)
     pkv_latent_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -368,7 +362,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
   } else if (warp == 9) {
     // ===== scores: S^T of tile after tile, each once it has landed and the
     // softmax has taken the scores two tiles before from its buffer =====
-    constexpr uint32_t idesc = lt_idesc(64, N, false, false);
+    constexpr uint32_t idesc = idesc_bf16(64, N, false);
     const uint32_t aq = smem_u32(sm + S::q);
     LtWalk walk = first;
     LtPiece x;
@@ -402,7 +396,7 @@ __global__ void __launch_bounds__(kLtThreads, 1)
     // A warp of its own: behind the scores of the next tile, in one warp, P V
     // waited for that tile's copies, and they for the buffer that P V frees
     // (5000 cycles a tile against 3100). =====
-    constexpr uint32_t idesc = lt_idesc(128, N, true, true);
+    constexpr uint32_t idesc = idesc_bf16(128, N, true, true);
     LtWalk walk = first;
     LtPiece x;
     int g = 0;

@@ -36,7 +36,7 @@
 //    place of a CTA.
 //
 // Measured: two 1023-token chunks over 1536-3584 tokens and 33 decode rows, 64
-// heads: 564 us, 0.75 of the bf16 burst peak (one CTA a tile: 944).  A tile
+// heads: 555-565 us, 0.75 of the bf16 burst peak (one CTA a tile: 944).  A tile
 // takes 3200 cycles there: with one buffer each, a slice's way from being let
 // go of to being here again (2300 cycles, 400 of them for the word to the other
 // CTA) and its product follow one another, and neither product has work while
@@ -151,14 +151,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
 // A copy into this CTA's shared memory that reports to a barrier of either CTA
 // of the pair (its cluster address), and the announcement of its bytes there.
 __device__ __forceinline__ void tma_load_4d_pair(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -178,11 +170,6 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
-}
-
-constexpr uint32_t pr_idesc(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 __global__ void __launch_bounds__(kPrThreads, 1)
@@ -377,7 +364,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 9) {
       // ===== scores (leader); the other CTA's warp says when its queries are here =====
-      constexpr uint32_t idesc = pr_idesc(128, kPrKeys, false, false);
+      constexpr uint32_t idesc = idesc_bf16(128, kPrKeys, false);
       const uint32_t aq = smem_u32(sm + S::q), ak = smem_u32(sm + S::k);
       // g0: tiles of passes for maxima.  Each kind of pass reports to barriers
       // of its own, so that the value warp, which waits in one kind only,
@@ -416,7 +403,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
     } else if (warp == 10) {
       // ===== values (leader); both CTAs' warps zero what lies behind a sequence's end =====
-      constexpr uint32_t idesc = pr_idesc(256, kPrRows, true, false);
+      constexpr uint32_t idesc = idesc_bf16(256, kPrRows, false, true);
       const uint32_t av = smem_u32(sm + S::v), ap = smem_u32(sm + S::p);
       while (ok && next_piece(walk, x)) {
         for (int k = x.k0; ok && k < x.k1; ++k, ++gv) {
