@@ -99,6 +99,7 @@ struct DecodeParams {
   // lead_sat: SMs at which this kernel's page stream saturates HBM (0: it
   // never does, i.e. it is bound by the SMs it runs on)
   int32_t lead, pf_cost, lead_sat;
+  uint32_t zero;  // 0, which the compiler does not know: see `issue`
   unsigned long long* join;
   // shared prefix: the first np pages of every row were attended by the
   // prefix pass, whose partial records (chunks per row and head) are merged
@@ -634,8 +635,18 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
     cursor_bid(pc, p);
   }
   // warp-collective (every lane holds the same cursor): one elected lane
-  // arms the stage and issues its copies
-  auto issue = [&](int stage) {
+  // arms the stage and issues its copies.  `after_reads` is 0, made of what was
+  // read of the page that the stage held (& p.zero): the copies' coordinate
+  // waits for it, and so the copies for the reads.  Nothing else makes them
+  // wait.  A read that is under way may take microseconds where another
+  // kernel's blocks share the SM (beside a CTA whose last warps have no work,
+  // their registers are free), longer than the copy into its place: rows of
+  // the last warps' items came out wrong in one of a hundred calls beside
+  // copies on another stream.  (The barrier's arrival, made to return before
+  // the copy, does not wait for the reads either.)  No time lost: 688-690 us
+  // on the long tail, 109 on 64 sequences, both as without it; on FP8 pages
+  // 469.5 and 74.6 for 468 and 74.5.
+  auto issue = [&](int stage, uint32_t after_reads) {
     constexpr int PB = kPageBytesOf<F8>;
     const int g = pc.item / p.nsub;
     const size_t ph = size_t(pc.bid) * p.Hkv + g;  // (page, kv head)
@@ -647,8 +658,8 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
     // one box per page: the pool viewed as [units][128 bytes]; the host
     // checks that unit indices fit int32
     const int unit0 = int(ph) * (PB / 128);
-    tma_load_2d_hint_w(&R.kv[stage][0][0], &tmk, 0, unit0, &M.bar[stage], policy);
-    tma_load_2d_hint_w(&R.kv[stage][1][0], &tmv, 0, unit0, &M.bar[stage], policy);
+    tma_load_2d_hint_w(&R.kv[stage][0][0], &tmk, int(after_reads), unit0, &M.bar[stage], policy);
+    tma_load_2d_hint_w(&R.kv[stage][1][0], &tmv, int(after_reads), unit0, &M.bar[stage], policy);
     if constexpr (F8) {
       bulk_g2s_w(&M.sc[stage][0], p.k_scale + ph * kScaleBytes, kScaleBytes, &M.bar[stage], policy);
       bulk_g2s_w(&M.sc[stage][1], p.v_scale + ph * kScaleBytes, kScaleBytes, &M.bar[stage], policy);
@@ -682,7 +693,7 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
   {
     const int prologue = min(NS, n_units);
     for (int s = 0; s < prologue; ++s) {
-      issue(s);
+      issue(s, 0);
       if (s + 1 < n_units) cursor_advance(pc, p, sq, per_row);
     }
   }
@@ -979,9 +990,11 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
       uint4 vc = swz(Vp, 2 * tq + 8, gq), vd = swz(Vp, 2 * tq + 9, gq);
       const uint4 ksc = M.sc[stage][0], vsc = M.sc[stage][1];
       // The page now lives in registers: hand the stage back to the copy engine.
+      const uint32_t read =
+          (ka0.x ^ ka1.x ^ kb0.x ^ kb1.x ^ va.x ^ vb.x ^ vc.x ^ vd.x ^ ksc.x ^ vsc.x) & p.zero;
       __syncwarp();
       if (it + NS < n_units) {
-        issue(stage);
+        issue(stage, read);
         if (it + NS + 1 < n_units) cursor_advance(pc, p, sq, per_row);
       }
 
@@ -1148,11 +1161,6 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
 #pragma unroll
         for (int x = 0; x < 4; ++x) vr[x][c] = swz(Vp, 2 * (tq + 4 * x) + c, gq);
       }
-      __syncwarp();
-      if (it + NS < n_units) {
-        issue(stage);
-        if (it + NS + 1 < n_units) cursor_advance(pc, p, sq, per_row);
-      }
       const bool t0 = gq < nvalid, t1 = gq + 8 < nvalid;
       const bool h0 = 2 * tq < 2 * GH, h1r = 2 * tq + 1 < 2 * GH;
       float sv[4];
@@ -1162,7 +1170,16 @@ __global__ void __launch_bounds__(F8 ? kDecWarpsF8 * 32 : kDecThreads, PKV_DEC_M
       sv[3] = t1 && h1r ? sacc[3] * qmul : -INFINITY;
       const bool exceed = sv[0] > m2[0] + kTau || sv[2] > m2[0] + kTau || sv[1] > m2[1] + kTau ||
                           sv[3] > m2[1] + kTau;
-      if (__any_sync(kFull, exceed)) {
+      const bool move = __any_sync(kFull, exceed);
+      // (S too: its products have read K)
+      const uint32_t read = (vr[0][0].x ^ vr[0][1].x ^ vr[1][0].x ^ vr[1][1].x ^ vr[2][0].x ^ vr[2][1].x ^
+                             vr[3][0].x ^ vr[3][1].x ^ __float_as_uint(sacc[0])) & p.zero;
+      __syncwarp();
+      if (it + NS < n_units) {
+        issue(stage, read);
+        if (it + NS + 1 < n_units) cursor_advance(pc, p, sq, per_row);
+      }
+      if (move) {
         float full0 = fmaxf(sv[0], sv[2]), full1 = fmaxf(sv[1], sv[3]);
 #pragma unroll
         for (int o2 = 4; o2 < 32; o2 <<= 1) {
@@ -1423,6 +1440,7 @@ int launch_attend(const LaunchCtx& ctx, const AttendArgs& a) {
   dp.epoch = epoch;
   dp.wait_prev = (prefill && !lead && a.shared_prefix_pages == 0) ? 0 : 1;
   dp.lead = lead ? 1 : 0;
+  dp.zero = 0;
   dp.pf_cost = pf_cost;
   dp.lead_sat = split_kv_saturating_sms(a.fp8);
   dp.join = lead ? join : nullptr;
