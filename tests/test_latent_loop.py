@@ -89,3 +89,38 @@ def test_a_captured_decode_loop_in_place(pkvlib, H, pages):
         assert torch.equal(outs[i].view(torch.int16), want.view(torch.int16)), i
     assert torch.equal(pool.view(torch.int16), cache.view(torch.int16))
     assert grow > 30 and pkv.get_last_error() == 0
+
+
+def test_calls_from_several_threads(pkvlib):
+    """A thread a stream, each with its own step of append and attention; the
+    calls run without the interpreter's lock."""
+    import threading
+
+    from test_latent import WIDE, Case
+    pkv.get_last_error()
+    cases = [Case([300, 77, 1500], [1, 1, 1], 16, seed=81), Case([300, 900], [2, 1], 96, seed=82, width=WIDE),
+             Case([64, 65, 9], [1, 3, 1], 20, seed=83), Case([2100], [1], 64, seed=84)]
+    args = [c.args() for c in cases]
+    want = [pkv.attend_latent(*a) for a in args]
+    for c, w in zip(cases, want):
+        c.check(w)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                got = [pkv.attend_latent(*args[k]) for _ in range(100)]
+                stream.synchronize()
+            if not all(torch.equal(g.view(torch.int16), want[k].view(torch.int16)) for g in got):
+                failed.append(k)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and pkv.get_last_error() == 0
