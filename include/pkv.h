@@ -173,6 +173,10 @@ PKV_API int pkv_attend_workspace_size(const pkv_desc* desc, int32_t num_seqs,
  * right before the call that lets its dependents start early: no call of this
  * library writes them, and a kernel of the caller's that does must leave out
  * that early start (griddepcontrol.launch_dependents).
+ * A call may be captured into a graph and replayed with other values in its
+ * arrays, lengths among them; num_seqs, num_tokens and max_query_len stay those
+ * of the capture.  It then ends with one or two small memory sets of its
+ * workspace's counters.
  * A call with query chunks longer than PKV_SPLITKV_MAX_QLEN runs its split-KV
  * kernel and its tensor-core prefill kernel at the same time on disjoint
  * SMs; work enqueued on the stream after the call still starts only once

@@ -52,7 +52,8 @@
 //    A split one writes (m, l, o) to one of its two partial slots and bumps
 //    an epoch-tagged arrival counter; the last warp to arrive merges the
 //    partials (log-sum-exp) and writes the output.  The epoch is new on every
-//    call, so the workspace never needs clearing.
+//    call, so the workspace never needs clearing; a captured call, whose
+//    replays repeat its epoch, clears the counters behind itself.
 //  * Beside the tensor-core prefill pass of the same call: this kernel is
 //    launched first and its plan leaves the pass part of the SMs (sized from
 //    the pass's tile steps against this kernel's units); the pass, launched
@@ -1477,8 +1478,21 @@ int launch_attend(const LaunchCtx& ctx, const AttendArgs& a) {
       default: e = launch_decode<4, false>(ctx, dp, tk, tv); break;
     }
   }
-  if (e || !lead) return e;
-  return launch_prefill(ctx, a, split_max_q, max_tiles, join, epoch);
+  if (!e && lead) e = launch_prefill(ctx, a, split_max_q, max_tiles, join, epoch);
+  if (e) return e;
+  // A replayed graph repeats its epoch: an arrival of one replay must not find
+  // that of the last one still there, ahead of its own stamp.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(ctx.stream, &capture) != cudaSuccess) cudaGetLastError();
+  if (capture == cudaStreamCaptureStatusActive) {
+    const size_t words = size_t(a.num_tokens) * d.num_kv_heads * nsub;
+    if (cudaMemsetAsync(dp.counters, 0, words * sizeof(unsigned long long), ctx.stream) != cudaSuccess ||
+        (lead && cudaMemsetAsync(join, 0, sizeof(unsigned long long), ctx.stream) != cudaSuccess)) {
+      cudaGetLastError();
+      return PKV_ERR_LAUNCH;
+    }
+  }
+  return PKV_OK;
 }
 
 }  // namespace pkv
