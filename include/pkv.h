@@ -331,6 +331,49 @@ PKV_API int pkv_write_rope_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const p
                                pkv_fp8* k_cache, pkv_fp8* v_cache, uint8_t* k_scale,
                                uint8_t* v_scale, const pkv_desc* desc, pkv_stream_t stream);
 
+/* ---- appends of tokens with several positions ----------------------------------- */
+/* A patch of an image or of a video has a position on each of several axes
+ * (time, height, width); every pair of its rows' elements is rotated by the
+ * position of one of them.  The pages this library follows do not describe
+ * it.  cos_sin, max_position, rotary_dim and interleaved are pkv_rope's;
+ * pair i turns by entry i of the table's row of its own axis, so a layout
+ * that gives each axis frequencies of its own is a matter of the table.
+ *   axis_of_pair   HOST pointer, rotary_dim/2 bytes: the axis of each pair,
+ *                  below num_axes; blocks of pairs, axes in turn, or any other
+ *                  order.  Read before the call returns.
+ *   num_axes       1 to PKV_MAX_AXES. */
+#define PKV_MAX_AXES 4
+typedef struct {
+  const float* cos_sin;
+  int32_t max_position;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t num_axes;
+  const uint8_t* axis_of_pair;
+} pkv_rope_axes;
+
+/* pkv_write_rope_axes, pkv_write_rope_axes_fp8 -- pkv_write_rope and
+ * pkv_write_rope_fp8 with num_axes positions a token.
+ *   positions      [num_axes, num_tokens] int64, position_stride elements from
+ *                  axis to axis (0: all axes read the same positions).  A
+ *                  token with any of its positions outside [0, max_position)
+ *                  is skipped whole and flags PKV_STATUS_BAD_POSITION.
+ * Everything else is as in pkv_write_rope; with one axis the results are
+ * pkv_write_rope's, bit for bit. */
+PKV_API int pkv_write_rope_axes(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new,
+                                int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                const int64_t* positions, int64_t position_stride,
+                                const int64_t* slot_mapping, int64_t num_tokens,
+                                const pkv_rope_axes* rope, pkv_bf16* q_out, pkv_bf16* k_cache,
+                                pkv_bf16* v_cache, const pkv_desc* desc, pkv_stream_t stream);
+PKV_API int pkv_write_rope_axes_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new,
+                                    int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                    const int64_t* positions, int64_t position_stride,
+                                    const int64_t* slot_mapping, int64_t num_tokens,
+                                    const pkv_rope_axes* rope, pkv_bf16* q_out, pkv_fp8* k_cache,
+                                    pkv_fp8* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                    const pkv_desc* desc, pkv_stream_t stream);
+
 /* ---- latent pages ------------------------------------------------------------ */
 /* Latent attention caches one vector a token in place of per-head keys and
  * values: 512 latent values that stand for the keys and the values of every

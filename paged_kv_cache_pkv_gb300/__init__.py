@@ -21,8 +21,8 @@ __all__ = [
     "PkvError", "PkvUnavailable", "lib", "open_library", "library_path", "Desc", "write", "attend",
     "workspace_size", "get_last_error", "launch_count", "Trace", "PagePool", "KERNELS",
     "export_pages", "import_pages", "write_fp8", "attend_fp8", "workspace_size_fp8",
-    "write_rope", "write_rope_fp8", "write_latent", "attend_latent", "workspace_size_latent",
-    "make_desc", "make_latent_desc", "Rope",
+    "write_rope", "write_rope_fp8", "write_rope_axes", "write_rope_axes_fp8", "rope_axes", "write_latent", "attend_latent", "workspace_size_latent",
+    "make_desc", "make_latent_desc", "Rope", "RopeAxes",
     "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT", "STATUS_BAD_POSITION",
 ]
 
@@ -56,6 +56,10 @@ class Rope(ctypes.Structure):
                 ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = Rope._fields_ + [("num_axes", ctypes.c_int32), ("axis_of_pair", ctypes.c_void_p)]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "pkv_write": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _vp, ctypes.POINTER(Desc), _vp]),
@@ -72,6 +76,11 @@ _SIGS = {
                                       _vp, _vp, ctypes.POINTER(Desc), _vp]),
     "pkv_write_rope_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Rope), _vp,
                                           _vp, _vp, _vp, _vp, ctypes.POINTER(Desc), _vp]),
+    "pkv_write_rope_axes": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                           ctypes.POINTER(RopeAxes), _vp, _vp, _vp, ctypes.POINTER(Desc), _vp]),
+    "pkv_write_rope_axes_fp8": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
+                                               ctypes.POINTER(RopeAxes), _vp, _vp, _vp, _vp, _vp,
+                                               ctypes.POINTER(Desc), _vp]),
     "pkv_write_latent": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.POINTER(Rope),
                                         _vp, _vp, ctypes.POINTER(Desc), _vp]),
     "pkv_attend_latent_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, ctypes.POINTER(_sz)]),
@@ -328,8 +337,8 @@ def _native():
             raise PkvUnavailable(f"the binding of the rotated and latent calls is missing ({e}): build it with "
                                  "`python -m paged_kv_cache_pkv_gb300.build`") from e
         _pkv_binding.bind(PkvError, *(ctypes.cast(getattr(handle, n), _vp).value for n in (
-            "pkv_write_rope", "pkv_write_rope_fp8", "pkv_write_latent", "pkv_attend_latent",
-            "pkv_attend_latent_workspace_size")))
+            "pkv_write_rope", "pkv_write_rope_fp8", "pkv_write_rope_axes", "pkv_write_rope_axes_fp8",
+            "pkv_write_latent", "pkv_attend_latent", "pkv_attend_latent_workspace_size")))
         _binding = _pkv_binding
     return _binding
 
@@ -365,6 +374,45 @@ def write_rope_fp8(k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_ca
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).write_rope_fp8(index, stream, k_new, v_new, positions, cos_sin, slot_mapping,
                                                   k_cache, v_cache, q, q_out, interleaved, k_scale, v_scale)
+
+
+def rope_axes(sections, in_turn=False):
+    """The axis of each pair, as write_rope_axes takes it: ``sections`` says
+    how many pairs turn by each axis, e.g. (16, 24, 24) for time, height and
+    width of 64 pairs.  In blocks, or axes in turn (0, 1, 2, 0, 1, 2, ...) for
+    as long as each has pairs left."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0:
+        raise ValueError("sections must be numbers of pairs")
+    if not in_turn:
+        return bytes(axis for axis, n in enumerate(left) for _ in range(n))
+    axes = []
+    while any(left):
+        for axis, n in enumerate(left):
+            if n:
+                axes.append(axis)
+                left[axis] -= 1
+    return bytes(axes)
+
+
+def write_rope_axes(k_new, v_new, positions, axes, cos_sin, slot_mapping, k_cache, v_cache, q=None, q_out=None,
+                    interleaved=False, stream=None):
+    """write_rope for tokens with several positions (time, height and width of
+    an image's or a video's patch): ``positions`` is int64 [A, T], A from 1 to
+    4, and ``axes`` (bytes, a list or a tuple; see rope_axes) names for each of
+    the rotary_dim/2 pairs the axis whose position it turns by.  ``positions``
+    may be a slice of a longer buffer, or one row expanded to all axes."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).write_rope_axes(index, stream, k_new, v_new, positions, cos_sin, slot_mapping,
+                                                   k_cache, v_cache, q, q_out, interleaved, axes)
+
+
+def write_rope_axes_fp8(k_new, v_new, positions, axes, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                        q=None, q_out=None, interleaved=False, stream=None):
+    """write_rope_axes into FP8 pages (as write_rope_fp8)."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).write_rope_axes_fp8(index, stream, k_new, v_new, positions, cos_sin, slot_mapping,
+                                                       k_cache, v_cache, q, q_out, interleaved, k_scale, v_scale, axes)
 
 
 def make_latent_desc(latent_cache, num_heads, max_blocks_per_seq):

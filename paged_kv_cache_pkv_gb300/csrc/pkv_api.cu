@@ -298,11 +298,16 @@ int pkv_attend_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const pkv_fp8* v_c
   return launch_attend(ctx, a);
 }
 
+static pkv_rope one_axis(const pkv_rope_axes* r) {
+  return r ? pkv_rope{r->cos_sin, r->max_position, r->rotary_dim, r->interleaved} : pkv_rope{};
+}
+
 static int write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
                       int64_t k_stride, int64_t v_stride, const int64_t* positions,
                       const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope* rope,
                       pkv_bf16* q_out, void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
-                      const pkv_desc* desc, pkv_stream_t stream, bool fp8) {
+                      const pkv_desc* desc, pkv_stream_t stream, bool fp8, const pkv_rope_axes* axes = nullptr,
+                      int64_t position_stride = 0) {
   if (int e = check_desc(desc)) return e;
   if (num_tokens < 0) return PKV_ERR_RANGE;
   if (num_tokens == 0) return PKV_OK;
@@ -310,6 +315,12 @@ static int write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* 
       (fp8 && (!k_scale || !v_scale)))
     return PKV_ERR_NULL;
   if (int e = check_rope(rope, kHeadDim)) return e;
+  if (axes) {
+    if (!axes->axis_of_pair) return PKV_ERR_NULL;
+    if (axes->num_axes < 1 || axes->num_axes > PKV_MAX_AXES || position_stride < 0) return PKV_ERR_RANGE;
+    for (int i = 0; i < rope->rotary_dim / 2; ++i)
+      if (axes->axis_of_pair[i] >= axes->num_axes) return PKV_ERR_RANGE;
+  }
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(q, 16) || !aligned(q_out, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
       !aligned(positions, 8) || !aligned(slot_mapping, 8))
@@ -329,6 +340,11 @@ static int write_rope(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* 
   a.q_out = q_out, a.k_cache = k_cache, a.v_cache = v_cache, a.k_scale = k_scale, a.v_scale = v_scale;
   a.num_blocks = desc->num_blocks, a.num_q_heads = desc->num_q_heads, a.num_kv_heads = desc->num_kv_heads;
   a.status = ctx.status;
+  if (axes) {
+    a.num_axes = axes->num_axes;
+    a.position_stride = position_stride;
+    for (int i = 0; i < rope->rotary_dim / 2; ++i) a.axis_pairs[axes->axis_of_pair[i]] |= uint64_t(1) << i;
+  }
   return launch_write_rope(ctx, a, fp8);
 }
 
@@ -348,6 +364,28 @@ int pkv_write_rope_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16*
                        uint8_t* v_scale, const pkv_desc* desc, pkv_stream_t stream) {
   return write_rope(q, k_new, v_new, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, rope,
                     q_out, k_cache, v_cache, k_scale, v_scale, desc, stream, true);
+}
+
+int pkv_write_rope_axes(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, const int64_t* positions, int64_t position_stride,
+                        const int64_t* slot_mapping, int64_t num_tokens, const pkv_rope_axes* rope,
+                        pkv_bf16* q_out, pkv_bf16* k_cache, pkv_bf16* v_cache, const pkv_desc* desc,
+                        pkv_stream_t stream) {
+  if (!rope && num_tokens != 0) return PKV_ERR_NULL;
+  const pkv_rope one = one_axis(rope);
+  return write_rope(q, k_new, v_new, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, &one,
+                    q_out, k_cache, v_cache, nullptr, nullptr, desc, stream, false, rope, position_stride);
+}
+
+int pkv_write_rope_axes_fp8(const pkv_bf16* q, const pkv_bf16* k_new, const pkv_bf16* v_new, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                            int64_t position_stride, const int64_t* slot_mapping, int64_t num_tokens,
+                            const pkv_rope_axes* rope, pkv_bf16* q_out, pkv_fp8* k_cache, pkv_fp8* v_cache,
+                            uint8_t* k_scale, uint8_t* v_scale, const pkv_desc* desc, pkv_stream_t stream) {
+  if (!rope && num_tokens != 0) return PKV_ERR_NULL;
+  const pkv_rope one = one_axis(rope);
+  return write_rope(q, k_new, v_new, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, &one,
+                    q_out, k_cache, v_cache, k_scale, v_scale, desc, stream, true, rope, position_stride);
 }
 
 int pkv_write_latent(const pkv_bf16* c_new, const pkv_bf16* k_pe, const pkv_bf16* q_pe, int64_t c_stride,

@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <exception>
 #include <optional>
+#include <type_traits>
 
 #include "pkv.h"
 
@@ -34,6 +35,8 @@ struct Raised {};  // a Python error is set
 
 decltype(&pkv_write_rope) g_write_rope;
 decltype(&pkv_write_rope_fp8) g_write_rope_fp8;
+decltype(&pkv_write_rope_axes) g_write_rope_axes;
+decltype(&pkv_write_rope_axes_fp8) g_write_rope_axes_fp8;
 decltype(&pkv_write_latent) g_write_latent;
 decltype(&pkv_attend_latent) g_attend_latent;
 decltype(&pkv_attend_latent_workspace_size) g_workspace_size;
@@ -195,11 +198,32 @@ void need_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) RAISE(TypeError, "%zd arguments, not %zd", want, n);
 }
 
+// The axis of each of `pairs` pairs: bytes, or a list or tuple of numbers.
+void axes_of(PyObject* o, int64_t pairs, uint8_t* axis) {
+  if (PyBytes_Check(o)) {
+    if (PyBytes_GET_SIZE(o) != pairs) RAISE(ValueError, "axes must name the axis of each of rotary_dim / 2 pairs");
+    const char* at = PyBytes_AS_STRING(o);
+    for (int64_t i = 0; i < pairs; ++i) axis[i] = uint8_t(at[i]);
+    return;
+  }
+  if (!PyList_Check(o) && !PyTuple_Check(o))
+    RAISE(TypeError, "axes must be bytes, a list or a tuple, got %s", Py_TYPE(o)->tp_name);
+  if (PySequence_Fast_GET_SIZE(o) != pairs)
+    RAISE(ValueError, "axes must name the axis of each of rotary_dim / 2 pairs");
+  for (int64_t i = 0; i < pairs; ++i) {
+    PyObject* item = PySequence_Fast_GET_ITEM(o, i);
+    const long v = PyLong_AsLong(item);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    if (v < 0 || v > UINT8_MAX) RAISE(ValueError, "axes must be axes of positions");
+    axis[i] = uint8_t(v);
+  }
+}
+
 // (index, stream, k_new, v_new, positions, cos_sin, slot_mapping, k_cache,
-//  v_cache, q, q_out, interleaved[, k_scale, v_scale])
-template <bool F8>
+//  v_cache, q, q_out, interleaved[, k_scale, v_scale][, axes])
+template <bool F8, bool AXES>
 PyObject* write_rope(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, F8 ? 14 : 12);
+  need_args(n, (F8 ? 14 : 12) + AXES);
   const int index = device_of(a[0]);
   constexpr at::ScalarType kind = F8 ? at::kByte : at::kBFloat16;
   const at::Tensor& kc = take(a[7], "k_cache", kind, 4, index);
@@ -217,11 +241,27 @@ PyObject* write_rope(PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& k_new = tensor(a[2], "k_new");
   const int64_t T = k_new.dim() ? k_new.size(0) : -1, hkv = kc.size(1), D = kc.size(3);
   const Rows k = take_rows(a[2], "k_new", T, hkv, D, index), v = take_rows(a[3], "v_new", T, hkv, D, index);
-  const at::Tensor& pos = take(a[4], "positions", at::kLong, 1, index);
+  const at::Tensor& pos = AXES ? tensor(a[4], "positions") : take(a[4], "positions", at::kLong, 1, index);
+  if constexpr (AXES) {  // [num_axes, T], a slice of a longer buffer or one row for all axes too
+    need_dtype(a[4], pos, "positions", at::kLong);
+    need_device(pos, "positions", index);
+    if (pos.dim() != 2) bad_shape(a[4], "positions", "[axes, tokens]");
+    if (T > 1 && pos.stride(1) != 1) RAISE(ValueError, "an axis's positions must be contiguous");
+  }
   const at::Tensor& slots = take(a[6], "slot_mapping", at::kLong, 1, index);
-  if (pos.size(0) != T || slots.size(0) != T)
+  if (pos.size(AXES ? 1 : 0) != T || slots.size(0) != T)
     RAISE(ValueError, "k_new, positions and slot_mapping disagree on the number of tokens");
   const pkv_rope rope = rope_of(a[5], a[11], index);
+  uint8_t axis[128];
+  pkv_rope_axes several{};
+  if constexpr (AXES) {
+    if (pos.size(0) < 1 || pos.size(0) > PKV_MAX_AXES) RAISE(ValueError, "positions must have 1 to %d axes", PKV_MAX_AXES);
+    if (rope.rotary_dim > int32_t(2 * sizeof axis)) bad_shape(a[5], "cos_sin", "[max_position, rotary_dim]");
+    axes_of(a[F8 ? 14 : 12], rope.rotary_dim / 2, axis);
+    for (int32_t i = 0; i < rope.rotary_dim / 2; ++i)
+      if (axis[i] >= pos.size(0)) RAISE(ValueError, "axes must be axes of positions");
+    several = {rope.cos_sin, rope.max_position, rope.rotary_dim, rope.interleaved, int32_t(pos.size(0)), axis};
+  }
   const Stream stream(a[1], index);
   Rows q{nullptr, 0};
   pkv_bf16* q_out = nullptr;
@@ -246,15 +286,22 @@ PyObject* write_rope(PyObject* const* a, Py_ssize_t n) {
   const pkv_desc desc{i32(kc.size(0), "k_cache"), i32(kc.size(2), "k_cache"), i32(hkv, "k_cache"),
                       i32(hq, "q"),               i32(D, "k_cache"),          1};
   const int64_t *p = in<int64_t>(pos), *s = in<int64_t>(slots);
+  [[maybe_unused]] const int64_t ps = AXES ? pos.stride(0) : 0;
   if constexpr (F8) {
     auto *kp = inout<pkv_fp8>(kc), *vp = inout<pkv_fp8>(vc);
-    run("pkv_write_rope_fp8", index, [&] {
+    run(AXES ? "pkv_write_rope_axes_fp8" : "pkv_write_rope_fp8", index, [&] {
+      if constexpr (AXES)
+        return g_write_rope_axes_fp8(q.at, k.at, v.at, q.stride, k.stride, v.stride, p, ps, s, T, &several,
+                                     q_out, kp, vp, ks, vs, &desc, stream.handle);
       return g_write_rope_fp8(q.at, k.at, v.at, q.stride, k.stride, v.stride, p, s, T, &rope, q_out, kp, vp, ks, vs,
                               &desc, stream.handle);
     });
   } else {
     auto *kp = inout<pkv_bf16>(kc), *vp = inout<pkv_bf16>(vc);
-    run("pkv_write_rope", index, [&] {
+    run(AXES ? "pkv_write_rope_axes" : "pkv_write_rope", index, [&] {
+      if constexpr (AXES)
+        return g_write_rope_axes(q.at, k.at, v.at, q.stride, k.stride, v.stride, p, ps, s, T, &several,
+                                 q_out, kp, vp, &desc, stream.handle);
       return g_write_rope(q.at, k.at, v.at, q.stride, k.stride, v.stride, p, s, T, &rope, q_out, kp, vp, &desc,
                           stream.handle);
     });
@@ -381,17 +428,20 @@ PyObject* attend_latent(PyObject* const* a, Py_ssize_t n) {
 
 // (PkvError, addresses of the entry points in the order below)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 6);
-  void* at[5];
-  for (int i = 0; i < 5; ++i) {
-    at[i] = PyLong_AsVoidPtr(a[i + 1]);
+  need_args(n, 8);
+  Py_ssize_t next = 1;
+  auto take_address = [&](auto& entry) {
+    void* at = PyLong_AsVoidPtr(a[next++]);
     if (PyErr_Occurred()) throw Raised{};
-  }
-  g_write_rope = reinterpret_cast<decltype(g_write_rope)>(at[0]);
-  g_write_rope_fp8 = reinterpret_cast<decltype(g_write_rope_fp8)>(at[1]);
-  g_write_latent = reinterpret_cast<decltype(g_write_latent)>(at[2]);
-  g_attend_latent = reinterpret_cast<decltype(g_attend_latent)>(at[3]);
-  g_workspace_size = reinterpret_cast<decltype(g_workspace_size)>(at[4]);
+    entry = reinterpret_cast<std::remove_reference_t<decltype(entry)>>(at);
+  };
+  take_address(g_write_rope);
+  take_address(g_write_rope_fp8);
+  take_address(g_write_rope_axes);
+  take_address(g_write_rope_axes_fp8);
+  take_address(g_write_latent);
+  take_address(g_attend_latent);
+  take_address(g_workspace_size);
   Py_XSETREF(g_error, Py_NewRef(a[0]));
   return Py_NewRef(Py_None);
 }
@@ -416,8 +466,10 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<bind>("bind"),
-                           method<write_rope<false>>("write_rope"),
-                           method<write_rope<true>>("write_rope_fp8"),
+                           method<write_rope<false, false>>("write_rope"),
+                           method<write_rope<true, false>>("write_rope_fp8"),
+                           method<write_rope<false, true>>("write_rope_axes"),
+                           method<write_rope<true, true>>("write_rope_axes_fp8"),
                            method<write_latent>("write_latent"),
                            method<attend_latent>("attend_latent"),
                            {nullptr, nullptr, 0, nullptr}};

@@ -75,6 +75,11 @@ struct RopeWriteArgs {
   uint8_t *k_scale, *v_scale;  // FP8 pages only
   int32_t num_blocks, num_q_heads, num_kv_heads;
   unsigned* status;
+  // pkv_write_rope_axes: positions [num_axes][position_stride]; bit i of
+  // axis_pairs[a] says that pair i turns by axis a.  num_axes 0: pkv_write_rope.
+  int32_t num_axes = 0;
+  int64_t position_stride = 0;
+  uint64_t axis_pairs[PKV_MAX_AXES] = {};
 };
 int launch_write_rope(const LaunchCtx& ctx, const RopeWriteArgs& a, bool fp8);
 

