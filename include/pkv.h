@@ -440,6 +440,57 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
                               pkv_bf16* out, void* workspace, size_t workspace_bytes,
                               const pkv_desc* desc, pkv_stream_t stream);
 
+/* ---- eviction by accumulated attention weight ------------------------------------- */
+/* A cache is cut down by keeping, beside the first and the most recent tokens,
+ * those that attention has looked at most.  The pages this library follows do
+ * not describe it; formulas and layout are this library's.
+ *   scores         [num_blocks, num_kv_heads, 16] fp32, device: one value a
+ *                  cached token and kv head, in the place of the token's row
+ *                  in its page.  Each kv head keeps tokens of its own.
+ *   first          NULL, or [num_seqs] int32, device: so many leading tokens
+ *                  of each sequence are always kept and none of them is moved, so
+ *                  their pages may be shared by several sequences; other pages
+ *                  belong to one sequence, as for pkv_write.
+ * Rows keep the rotation that they were appended with: the positions of
+ * later tokens go on counting the tokens of the text, while seq_lens and
+ * slots count the cached ones. */
+
+/* pkv_evict -- cut sequences down to keep[b] cached tokens, in place.
+ * A sequence of at most keep[b] tokens is left as it is.  Of a longer one each
+ * kv head keeps f = min(first[b], keep[b]) leading tokens, the last
+ * r = min(recent, keep[b] - f), and of those between as many of the largest
+ * scores as make keep[b] (equal scores: the lowest token first; a score that
+ * is not a number counts as -infinity).  Kept tokens move, in their order, to
+ * rows 0..keep[b]-1 of the sequence: K and V rows, scale bytes and scores.
+ * Rows from keep[b] on are left as they were, and the caller may let go of
+ * pages that have become empty.
+ *   keep           [num_seqs] int32, device, not negative.
+ *   new_lens       [num_seqs] int32, device, must not overlap seq_lens, keep
+ *                  or first: min(L, keep[b]), the sequence's length from now on.
+ *   recent         >= 0.
+ *   workspace      at least pkv_evict_workspace_size bytes, 256-byte aligned,
+ *                  no initialisation needed; calls that may overlap on the
+ *                  GPU need workspaces of their own.
+ * desc: num_q_heads is not used (any valid value).  Pages of a sequence from
+ * its first[b]-th token on must belong to it alone.  A sequence whose numbers
+ * do not fit (length negative or beyond its table, negative keep or first) is
+ * left alone and flags PKV_STATUS_BAD_QUERY; new_lens[b] is then its length.
+ * A token whose page id is outside the pool counts as -infinity and is not
+ * moved, nor is anything moved onto it (PKV_STATUS_BAD_BLOCK).
+ * Deterministic. */
+PKV_API int pkv_evict_workspace_size(const pkv_desc* desc, int32_t num_seqs, size_t* bytes);
+PKV_API int pkv_evict(pkv_bf16* k_cache, pkv_bf16* v_cache, float* scores,
+                      const int32_t* block_tables, const int32_t* seq_lens, const int32_t* keep,
+                      const int32_t* first, int32_t recent, int32_t num_seqs, int32_t* new_lens,
+                      void* workspace, size_t workspace_bytes, const pkv_desc* desc,
+                      pkv_stream_t stream);
+/* pkv_evict_fp8 -- the same on FP8 pages. */
+PKV_API int pkv_evict_fp8(pkv_fp8* k_cache, pkv_fp8* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                          float* scores, const int32_t* block_tables, const int32_t* seq_lens,
+                          const int32_t* keep, const int32_t* first, int32_t recent,
+                          int32_t num_seqs, int32_t* new_lens, void* workspace,
+                          size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream);
+
 /* ---- page pool (host side) ------------------------------------------------ */
 /* The engine reserves num_gpu_blocks pages of block_size tokens (vLLM notes
  * "EngineCoreClient ...", "Flujo de datos"); the native coordinator owns the
@@ -512,7 +563,8 @@ PKV_API uint64_t pkv_launch_count(void);
 #define PKV_K_MERGE    3
 #define PKV_K_PREFILL  4
 #define PKV_K_LATENT   5
-#define PKV_K_COUNT    6
+#define PKV_K_EVICT    6
+#define PKV_K_COUNT    7
 
 typedef struct pkv_trace pkv_trace;
 /* Create a trace with room for `capacity` launches (creates 2*capacity CUDA

@@ -22,6 +22,7 @@ __all__ = [
     "workspace_size", "get_last_error", "launch_count", "Trace", "PagePool", "KERNELS",
     "export_pages", "import_pages", "write_fp8", "attend_fp8", "workspace_size_fp8",
     "write_rope", "write_rope_fp8", "write_rope_axes", "write_rope_axes_fp8", "rope_axes", "write_latent", "attend_latent", "workspace_size_latent",
+    "evict", "evict_fp8", "workspace_size_evict",
     "make_desc", "make_latent_desc", "Rope", "RopeAxes",
     "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT", "STATUS_BAD_POSITION",
 ]
@@ -31,7 +32,7 @@ library_path = os.environ.get("PKV_LIBRARY", os.path.join(_HERE, "libpkv.so"))
 
 STATUS_BAD_SLOT, STATUS_BAD_BLOCK, STATUS_BAD_QUERY, STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 STATUS_BAD_POSITION = 0x10
-KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5}
+KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5, "evict": 6}
 
 
 class PkvError(RuntimeError):
@@ -86,6 +87,11 @@ _SIGS = {
     "pkv_attend_latent_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, ctypes.POINTER(_sz)]),
     "pkv_attend_latent": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz,
                                          ctypes.POINTER(Desc), _vp]),
+    "pkv_evict_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, ctypes.POINTER(_sz)]),
+    "pkv_evict": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(Desc),
+                                 _vp]),
+    "pkv_evict_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _sz,
+                                     ctypes.POINTER(Desc), _vp]),
     "pkv_get_last_error": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "pkv_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "pkv_launch_count": (ctypes.c_uint64, []),
@@ -338,7 +344,8 @@ def _native():
                                  "`python -m paged_kv_cache_pkv_gb300.build`") from e
         _pkv_binding.bind(PkvError, *(ctypes.cast(getattr(handle, n), _vp).value for n in (
             "pkv_write_rope", "pkv_write_rope_fp8", "pkv_write_rope_axes", "pkv_write_rope_axes_fp8",
-            "pkv_write_latent", "pkv_attend_latent", "pkv_attend_latent_workspace_size")))
+            "pkv_write_latent", "pkv_attend_latent", "pkv_attend_latent_workspace_size", "pkv_evict", "pkv_evict_fp8",
+            "pkv_evict_workspace_size")))
         _binding = _pkv_binding
     return _binding
 
@@ -453,6 +460,37 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
     index = _index(latent_cache, "latent_cache")
     return (_binding or _native()).attend_latent(index, stream, q, latent_cache, block_tables, seq_lens,
                                                  query_start_loc, scale, out, workspace, max_query_len)
+
+
+def workspace_size_evict(desc, num_seqs, device=None):
+    """Workspace bytes evict and evict_fp8 need."""
+    n = _sz(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(lib().pkv_evict_workspace_size(ctypes.byref(desc), int(num_seqs), ctypes.byref(n)),
+               "pkv_evict_workspace_size")
+    return n.value
+
+
+def evict(k_cache, v_cache, scores, block_tables, seq_lens, keep, first=None, recent=0, new_lens=None, workspace=None,
+          stream=None):
+    """Cut every sequence above its budget ``keep`` (int32 [B]) down to it, in
+    place.  Each kv head keeps the ``first`` leading tokens (int32 [B], None:
+    none; their pages may be shared), the last ``recent`` ones and those of
+    the largest ``scores`` (fp32 [NB, Hkv, 16]) between; they move, in their
+    order, to the front of the sequence's pages, their scores too.  Returns
+    the new lengths (``new_lens``, int32 [B], not seq_lens itself): pages
+    behind them may be let go of."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).evict(index, stream, k_cache, v_cache, scores, block_tables, seq_lens, keep, first,
+                                         recent, new_lens, workspace)
+
+
+def evict_fp8(k_cache, v_cache, k_scale, v_scale, scores, block_tables, seq_lens, keep, first=None, recent=0,
+              new_lens=None, workspace=None, stream=None):
+    """evict on FP8 pages (codes and scale bytes as in write_fp8)."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).evict_fp8(index, stream, k_cache, v_cache, scores, block_tables, seq_lens, keep,
+                                             first, recent, new_lens, workspace, k_scale, v_scale)
 
 
 def export_pages(k_cache, v_cache, pages, out=None, stream=None):

@@ -67,6 +67,16 @@ int check_latent_range(const pkv_desc* d, int32_t num_seqs, int32_t num_tokens) 
   return heaviest * tiles < 9.0e18 ? PKV_OK : PKV_ERR_RANGE;
 }
 
+// Positions in a sequence are int32 on the device, with a tile of them on top.
+int check_positions(const pkv_desc* d) {
+  return int64_t(d->max_blocks_per_seq) * kPage >= (int64_t(1) << 31) - 1024 ? PKV_ERR_RANGE : PKV_OK;
+}
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
 // A token stride in elements: rows of `row` elements, 16-byte aligned.
 bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8; }
 
@@ -450,6 +460,58 @@ int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache, const int
                            num_tokens, max_query_len, scale,       out,       workspace,       workspace_bytes,
                            *desc};
   return launch_attend_latent(ctx, a);
+}
+
+int pkv_evict_workspace_size(const pkv_desc* desc, int32_t num_seqs, size_t* bytes) {
+  if (int e = check_desc(desc)) return e;
+  if (!bytes) return PKV_ERR_NULL;
+  if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS) return PKV_ERR_RANGE;
+  if (int e = check_positions(desc)) return e;
+  *bytes = evict_workspace_bytes(*desc, num_seqs);
+  return PKV_OK;
+}
+
+static int evict(void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale, float* scores,
+                 const int32_t* block_tables, const int32_t* seq_lens, const int32_t* keep, const int32_t* first,
+                 int32_t recent, int32_t num_seqs, int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                 const pkv_desc* desc, pkv_stream_t stream, bool fp8) {
+  if (int e = check_desc(desc)) return e;
+  if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS || recent < 0) return PKV_ERR_RANGE;
+  if (int e = check_positions(desc)) return e;
+  if (num_seqs == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !scores || !block_tables || !seq_lens || !keep || !new_lens || !workspace ||
+      (fp8 && (!k_scale || !v_scale)))
+    return PKV_ERR_NULL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) ||
+      !aligned(scores, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) ||
+      !aligned(first, 4) || !aligned(new_lens, 4) || !aligned(workspace, 256))
+    return PKV_ERR_ALIGN;
+  // a CTA of one head writes a new length while others read the old one
+  const size_t bytes = sizeof(int32_t) * size_t(num_seqs);
+  if (overlap(new_lens, bytes, seq_lens, bytes) || overlap(new_lens, bytes, keep, bytes) ||
+      (first && overlap(new_lens, bytes, first, bytes)))
+    return PKV_ERR_RANGE;
+  LaunchCtx ctx{};
+  if (int e = make_ctx(stream, &ctx)) return e;
+  const EvictArgs a{k_cache, v_cache, k_scale,  v_scale,  scores,    block_tables,    seq_lens, keep,
+                    first,   recent,  num_seqs, new_lens, workspace, workspace_bytes, *desc,    ctx.status};
+  return launch_evict(ctx, a, fp8);
+}
+
+int pkv_evict(pkv_bf16* k_cache, pkv_bf16* v_cache, float* scores, const int32_t* block_tables,
+              const int32_t* seq_lens, const int32_t* keep, const int32_t* first, int32_t recent, int32_t num_seqs,
+              int32_t* new_lens, void* workspace, size_t workspace_bytes, const pkv_desc* desc,
+              pkv_stream_t stream) {
+  return evict(k_cache, v_cache, nullptr, nullptr, scores, block_tables, seq_lens, keep, first, recent, num_seqs,
+               new_lens, workspace, workspace_bytes, desc, stream, false);
+}
+
+int pkv_evict_fp8(pkv_fp8* k_cache, pkv_fp8* v_cache, uint8_t* k_scale, uint8_t* v_scale, float* scores,
+                  const int32_t* block_tables, const int32_t* seq_lens, const int32_t* keep, const int32_t* first,
+                  int32_t recent, int32_t num_seqs, int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                  const pkv_desc* desc, pkv_stream_t stream) {
+  return evict(k_cache, v_cache, k_scale, v_scale, scores, block_tables, seq_lens, keep, first, recent, num_seqs,
+               new_lens, workspace, workspace_bytes, desc, stream, true);
 }
 
 int pkv_get_last_error(pkv_stream_t stream, uint32_t* flags) {

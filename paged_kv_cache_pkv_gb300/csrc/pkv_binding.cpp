@@ -1,5 +1,5 @@
-// pkv_binding.cpp -- Python arguments of the rotated appends and of latent
-// attention, checked and handed to libpkv's entry points.
+// pkv_binding.cpp -- Python arguments of the rotated appends, of latent
+// attention and of eviction, checked and handed to libpkv's entry points.
 //
 // A decode step's append is 2 us of GPU work.  Its checks of a dozen tensors
 // and the marshalling of 18 arguments took 13 us through Python and ctypes (20
@@ -40,6 +40,9 @@ decltype(&pkv_write_rope_axes_fp8) g_write_rope_axes_fp8;
 decltype(&pkv_write_latent) g_write_latent;
 decltype(&pkv_attend_latent) g_attend_latent;
 decltype(&pkv_attend_latent_workspace_size) g_workspace_size;
+decltype(&pkv_evict) g_evict;
+decltype(&pkv_evict_fp8) g_evict_fp8;
+decltype(&pkv_evict_workspace_size) g_evict_size;
 PyObject* g_error;  // PkvError
 
 const char* name_of(at::ScalarType t) {
@@ -183,6 +186,28 @@ int device_of(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Raised{};
   return int(v);
 }
+
+double number_of(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    if (PyErr_ExceptionMatches(PyExc_TypeError))
+      RAISE(TypeError, "%s must be a float, got %s", name, Py_TYPE(o)->tp_name);
+    throw Raised{};
+  }
+  return v;
+}
+
+int64_t whole_of(PyObject* whole) {  // takes over the reference
+  if (!whole) throw Raised{};
+  int overflow = 0;
+  const int64_t v = PyLong_AsLongLongAndOverflow(whole, &overflow);
+  Py_DECREF(whole);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return overflow > 0 ? INT64_MAX : overflow < 0 ? INT64_MIN : v;
+}
+
+// A host-side bound: what is negative counts as 0, what is above `top` as top.
+int64_t bound_of(PyObject* o, int64_t top) { return std::clamp<int64_t>(whole_of(PyNumber_Long(o)), 0, top); }
 
 pkv_rope rope_of(PyObject* o, PyObject* interleaved, int index) {
   const at::Tensor& t = take(o, "cos_sin", at::kFloat, 2, index);
@@ -378,19 +403,8 @@ PyObject* attend_latent(PyObject* const* a, Py_ssize_t n) {
   if (qsl.size(0) != B + 1 || tables.size(0) != B)
     RAISE(ValueError, "seq_lens [B], query_start_loc [B+1] and block_tables [B, M] disagree");
   if (pool.size(2) != q.size(2)) RAISE(ValueError, "latent_cache and q rows disagree");
-  const double scale = PyFloat_AsDouble(a[7]);
-  if (scale == -1.0 && PyErr_Occurred()) {
-    if (PyErr_ExceptionMatches(PyExc_TypeError))
-      RAISE(TypeError, "scale must be a float, got %s", Py_TYPE(a[7])->tp_name);
-    throw Raised{};
-  }
-  PyObject* whole = PyNumber_Long(a[10]);
-  if (!whole) throw Raised{};
-  int overflow = 0;
-  const int64_t bound = PyLong_AsLongLongAndOverflow(whole, &overflow);
-  Py_DECREF(whole);
-  const int32_t max_query_len =
-      overflow > 0 ? INT32_MAX : overflow < 0 ? 0 : int32_t(std::clamp<int64_t>(bound, 0, INT32_MAX));
+  const double scale = number_of(a[7], "scale");
+  const int32_t max_query_len = int32_t(bound_of(a[10], INT32_MAX));
   const pkv_desc desc{i32(pool.size(0), "latent_cache"), i32(pool.size(1), "latent_cache"), 1, i32(q.size(1), "q"),
                       i32(q.size(2), "q"),               i32(tables.size(1), "block_tables")};
   const int32_t seqs = i32(B, "seq_lens"), tokens = i32(q.size(0), "q");
@@ -426,9 +440,88 @@ PyObject* attend_latent(PyObject* const* a, Py_ssize_t n) {
   return result(a[8], made);
 }
 
+// An int32 number a sequence, or nothing.
+const int32_t* per_sequence(PyObject* o, const char* name, int64_t seqs, int index) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = take(o, name, at::kInt, 1, index);
+  if (t.size(0) != seqs) RAISE(ValueError, "%s must have a number for each sequence", name);
+  return in<int32_t>(t);
+}
+
+// (index, stream, k_cache, v_cache, scores, block_tables, seq_lens, keep,
+//  first, recent, new_lens, workspace[, k_scale, v_scale])
+template <bool F8>
+PyObject* evict(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, F8 ? 14 : 12);
+  const int index = device_of(a[0]);
+  constexpr at::ScalarType kind = F8 ? at::kByte : at::kBFloat16;
+  const at::Tensor& kc = take(a[2], "k_cache", kind, 4, index);
+  const at::Tensor& vc = take(a[3], "v_cache", kind, 4, index);
+  if (kc.sizes() != vc.sizes()) RAISE(ValueError, "k_cache and v_cache shapes disagree");
+  const at::Tensor& scores = take(a[4], "scores", at::kFloat, 3, index);
+  if (scores.sizes() != kc.sizes().slice(0, 3)) RAISE(ValueError, "scores must be [NB, Hkv, P] like k_cache");
+  uint8_t *ks = nullptr, *vs = nullptr;
+  if constexpr (F8) {
+    const at::Tensor& s = take(a[12], "k_scale", at::kByte, 3, index);
+    const at::Tensor& u = take(a[13], "v_scale", at::kByte, 3, index);
+    if (s.sizes() != kc.sizes().slice(0, 3) || u.sizes() != s.sizes())
+      RAISE(ValueError, "FP8 pools must be codes [NB, Hkv, P, D] and scales [NB, Hkv, P]");
+    ks = inout<uint8_t>(s);
+    vs = inout<uint8_t>(u);
+  }
+  const at::Tensor& tables = take(a[5], "block_tables", at::kInt, 2, index);
+  const at::Tensor& lens = take(a[6], "seq_lens", at::kInt, 1, index);
+  const int64_t B = lens.size(0);
+  if (tables.size(0) != B) RAISE(ValueError, "seq_lens [B] and block_tables [B, M] disagree");
+  if (a[7] == Py_None) RAISE(TypeError, "keep must be a torch.Tensor");
+  const int32_t* keep = per_sequence(a[7], "keep", B, index);
+  const int32_t* first = per_sequence(a[8], "first", B, index);
+  if (!PyIndex_Check(a[9])) RAISE(TypeError, "recent must be an int, got %s", Py_TYPE(a[9])->tp_name);
+  const int64_t recent = whole_of(PyNumber_Index(a[9]));
+  if (recent < 0) RAISE(ValueError, "recent must not be negative");
+  const int32_t last = int32_t(std::min<int64_t>(recent, INT32_MAX));
+  const pkv_desc desc{i32(kc.size(0), "k_cache"), i32(kc.size(2), "k_cache"), i32(kc.size(1), "k_cache"),
+                      i32(kc.size(1), "k_cache"), i32(kc.size(3), "k_cache"), i32(tables.size(1), "block_tables")};
+  const int32_t seqs = i32(B, "seq_lens");
+  const Stream stream(a[1], index);
+  at::Tensor made, scratch;
+  int32_t* out;
+  if (a[10] == Py_None) {
+    made = stream.fresh({B}, at::kInt, index);
+    out = inout<int32_t>(made);
+  } else {
+    const at::Tensor& o = take(a[10], "new_lens", at::kInt, 1, index);
+    if (o.size(0) != B) RAISE(ValueError, "new_lens must have a number for each sequence");
+    out = inout<int32_t>(o);
+  }
+  if (a[11] == Py_None) {
+    size_t bytes = 0;
+    run("pkv_evict_workspace_size", index, [&] { return g_evict_size(&desc, seqs, &bytes); });
+    scratch = stream.fresh({int64_t(bytes)}, at::kByte, index);
+  } else {
+    scratch = take(a[11], "workspace", at::kByte, 1, index);
+  }
+  void* ws = inout<void>(scratch);
+  const size_t ws_bytes = size_t(scratch.size(0));
+  auto* sp = inout<float>(scores);
+  const int32_t *bt = in<int32_t>(tables), *sl = in<int32_t>(lens);
+  if constexpr (F8) {
+    auto *kp = inout<pkv_fp8>(kc), *vp = inout<pkv_fp8>(vc);
+    run("pkv_evict_fp8", index, [&] {
+      return g_evict_fp8(kp, vp, ks, vs, sp, bt, sl, keep, first, last, seqs, out, ws, ws_bytes, &desc, stream.handle);
+    });
+  } else {
+    auto *kp = inout<pkv_bf16>(kc), *vp = inout<pkv_bf16>(vc);
+    run("pkv_evict", index, [&] {
+      return g_evict(kp, vp, sp, bt, sl, keep, first, last, seqs, out, ws, ws_bytes, &desc, stream.handle);
+    });
+  }
+  return result(a[10], made);
+}
+
 // (PkvError, addresses of the entry points in the order below)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 8);
+  need_args(n, 11);
   Py_ssize_t next = 1;
   auto take_address = [&](auto& entry) {
     void* at = PyLong_AsVoidPtr(a[next++]);
@@ -442,6 +535,9 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   take_address(g_write_latent);
   take_address(g_attend_latent);
   take_address(g_workspace_size);
+  take_address(g_evict);
+  take_address(g_evict_fp8);
+  take_address(g_evict_size);
   Py_XSETREF(g_error, Py_NewRef(a[0]));
   return Py_NewRef(Py_None);
 }
@@ -470,6 +566,8 @@ PyMethodDef g_methods[] = {method<bind>("bind"),
                            method<write_rope<true, false>>("write_rope_fp8"),
                            method<write_rope<false, true>>("write_rope_axes"),
                            method<write_rope<true, true>>("write_rope_axes_fp8"),
+                           method<evict<false>>("evict"),
+                           method<evict<true>>("evict_fp8"),
                            method<write_latent>("write_latent"),
                            method<attend_latent>("attend_latent"),
                            {nullptr, nullptr, 0, nullptr}};

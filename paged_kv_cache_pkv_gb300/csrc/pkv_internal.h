@@ -112,6 +112,22 @@ struct LatentAttendArgs {
 size_t latent_workspace_bytes(const DeviceInfo& dev);
 int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a);
 
+// pkv_evict / pkv_evict_fp8 (pkv_evict.cu).
+struct EvictArgs {
+  void *k_cache, *v_cache;
+  uint8_t *k_scale, *v_scale;  // FP8 pages only
+  float* scores;
+  const int32_t *block_tables, *seq_lens, *keep, *first;
+  int32_t recent, num_seqs;
+  int32_t* new_lens;
+  void* workspace;
+  size_t workspace_bytes;
+  pkv_desc desc;
+  unsigned* status;
+};
+size_t evict_workspace_bytes(const pkv_desc& d, int32_t num_seqs);
+int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8);
+
 struct AttendArgs {
   const uint16_t* q;
   const void* k_cache;  // bf16 pages, or E4M3 codes when fp8
