@@ -442,18 +442,69 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
 
 /* ---- eviction by accumulated attention weight ------------------------------------- */
 /* A cache is cut down by keeping, beside the first and the most recent tokens,
- * those that attention has looked at most.  The pages this library follows do
- * not describe it; formulas and layout are this library's.
+ * those that attention has looked at most.  pkv_weigh adds up the weights,
+ * pkv_evict keeps and moves.  The pages this library follows do not describe
+ * it; formulas and layout are this library's.
  *   scores         [num_blocks, num_kv_heads, 16] fp32, device: one value a
  *                  cached token and kv head, in the place of the token's row
  *                  in its page.  Each kv head keeps tokens of its own.
  *   first          NULL, or [num_seqs] int32, device: so many leading tokens
- *                  of each sequence are always kept and none of them is moved, so
- *                  their pages may be shared by several sequences; other pages
+ *                  of each sequence are always kept.  pkv_weigh writes no
+ *                  scores for them and pkv_evict moves none of them, so their
+ *                  pages may be shared by several sequences; other pages
  *                  belong to one sequence, as for pkv_write.
  * Rows keep the rotation that they were appended with: the positions of
  * later tokens go on counting the tokens of the text, while seq_lens and
  * slots count the cached ones. */
+
+/* pkv_weigh -- add to the scores the attention weights of this step's rows.
+ * For sequence b with L = seq_lens[b] cached tokens and n query rows (row j at
+ * position L-n+j sees keys 0..L-n+j), kv head g and key k:
+ *   w[k] = sum over rows j and query heads h of g, of the softmax weight of
+ *          key k (softmax of scale * q[j, h] . K over the keys that row j sees)
+ *   score[k] = (k < scored[b] ? decay * score[k] : 0) + w[k]  for first[b] <= k < L
+ *   q, k_cache, block_tables, seq_lens, query_start_loc and scale are as in
+ *   pkv_attend (scale finite and not negative).  Sequences without query rows
+ *   are left alone, scores of rows past a sequence's end too.
+ *   scored         NULL, or [num_seqs] int32: tokens from scored[b] on have no
+ *                  score yet and what their pages hold is not read.  NULL:
+ *                  L - n, i.e. this step's own tokens are new, the others have
+ *                  been weighed since they were appended.
+ *   decay          finite, not negative.  1 adds up, less lets older weights
+ *                  fade, 0 starts anew (the scores are written, never read).
+ *   max_query_len  host-side upper bound on n over the batch, or <= 0 if
+ *                  unknown: it selects kernels and sizes the workspace.  A
+ *                  sequence with more rows is skipped and flags
+ *                  PKV_STATUS_BAD_QUERY.
+ *   num_keys       host-side upper bound on the sum of the seq_lens, each
+ *                  rounded up to 16, or <= 0 if unknown (then the block tables'
+ *                  width bounds them): it sizes the workspace.  Sequences
+ *                  behind that many keys are skipped and flag
+ *                  PKV_STATUS_BAD_QUERY.
+ *   workspace      at least pkv_weigh_workspace_size bytes for the same
+ *                  num_seqs, num_tokens, max_query_len and num_keys, 256-byte
+ *                  aligned, no initialisation needed; calls that may overlap
+ *                  on the GPU need workspaces of their own.
+ * Sums and scores are fp32, in an order that goes by the call's shapes and
+ * lengths alone: the same inputs give the same bits.  K rows and scores of
+ * rows past a sequence's end are never used, whatever they hold; the rows of
+ * its cached tokens and its queries must be finite. */
+PKV_API int pkv_weigh_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t max_query_len, int64_t num_keys, size_t* bytes);
+PKV_API int pkv_weigh(const pkv_bf16* q, const pkv_bf16* k_cache, float* scores,
+                      const int32_t* block_tables, const int32_t* seq_lens,
+                      const int32_t* query_start_loc, const int32_t* first, const int32_t* scored,
+                      int32_t num_seqs, int32_t num_tokens, int32_t max_query_len, int64_t num_keys,
+                      float scale, float decay, void* workspace, size_t workspace_bytes,
+                      const pkv_desc* desc, pkv_stream_t stream);
+/* pkv_weigh_fp8 -- the same over FP8 pages (k_scale as in pkv_attend_fp8). */
+PKV_API int pkv_weigh_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const uint8_t* k_scale,
+                          float* scores, const int32_t* block_tables, const int32_t* seq_lens,
+                          const int32_t* query_start_loc, const int32_t* first,
+                          const int32_t* scored, int32_t num_seqs, int32_t num_tokens,
+                          int32_t max_query_len, int64_t num_keys, float scale, float decay,
+                          void* workspace, size_t workspace_bytes, const pkv_desc* desc,
+                          pkv_stream_t stream);
 
 /* pkv_evict -- cut sequences down to keep[b] cached tokens, in place.
  * A sequence of at most keep[b] tokens is left as it is.  Of a longer one each
@@ -564,7 +615,8 @@ PKV_API uint64_t pkv_launch_count(void);
 #define PKV_K_PREFILL  4
 #define PKV_K_LATENT   5
 #define PKV_K_EVICT    6
-#define PKV_K_COUNT    7
+#define PKV_K_WEIGH    7
+#define PKV_K_COUNT    8
 
 typedef struct pkv_trace pkv_trace;
 /* Create a trace with room for `capacity` launches (creates 2*capacity CUDA

@@ -22,7 +22,7 @@ __all__ = [
     "workspace_size", "get_last_error", "launch_count", "Trace", "PagePool", "KERNELS",
     "export_pages", "import_pages", "write_fp8", "attend_fp8", "workspace_size_fp8",
     "write_rope", "write_rope_fp8", "write_rope_axes", "write_rope_axes_fp8", "rope_axes", "write_latent", "attend_latent", "workspace_size_latent",
-    "evict", "evict_fp8", "workspace_size_evict",
+    "weigh", "weigh_fp8", "workspace_size_weigh", "evict", "evict_fp8", "workspace_size_evict",
     "make_desc", "make_latent_desc", "Rope", "RopeAxes",
     "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT", "STATUS_BAD_POSITION",
 ]
@@ -32,7 +32,7 @@ library_path = os.environ.get("PKV_LIBRARY", os.path.join(_HERE, "libpkv.so"))
 
 STATUS_BAD_SLOT, STATUS_BAD_BLOCK, STATUS_BAD_QUERY, STATUS_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 STATUS_BAD_POSITION = 0x10
-KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5, "evict": 6}
+KERNELS = {"write": 0, "plan": 1, "decode": 2, "merge": 3, "prefill": 4, "latent": 5, "evict": 6, "weigh": 7}
 
 
 class PkvError(RuntimeError):
@@ -87,6 +87,11 @@ _SIGS = {
     "pkv_attend_latent_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, ctypes.POINTER(_sz)]),
     "pkv_attend_latent": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _sz,
                                          ctypes.POINTER(Desc), _vp]),
+    "pkv_weigh_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, _i32, _i32, _i64, ctypes.POINTER(_sz)]),
+    "pkv_weigh": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, ctypes.c_float,
+                                 ctypes.c_float, _vp, _sz, ctypes.POINTER(Desc), _vp]),
+    "pkv_weigh_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64,
+                                     ctypes.c_float, ctypes.c_float, _vp, _sz, ctypes.POINTER(Desc), _vp]),
     "pkv_evict_workspace_size": (ctypes.c_int, [ctypes.POINTER(Desc), _i32, ctypes.POINTER(_sz)]),
     "pkv_evict": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _sz, ctypes.POINTER(Desc),
                                  _vp]),
@@ -344,8 +349,8 @@ def _native():
                                  "`python -m paged_kv_cache_pkv_gb300.build`") from e
         _pkv_binding.bind(PkvError, *(ctypes.cast(getattr(handle, n), _vp).value for n in (
             "pkv_write_rope", "pkv_write_rope_fp8", "pkv_write_rope_axes", "pkv_write_rope_axes_fp8",
-            "pkv_write_latent", "pkv_attend_latent", "pkv_attend_latent_workspace_size", "pkv_evict", "pkv_evict_fp8",
-            "pkv_evict_workspace_size")))
+            "pkv_write_latent", "pkv_attend_latent", "pkv_attend_latent_workspace_size", "pkv_weigh", "pkv_weigh_fp8",
+            "pkv_weigh_workspace_size", "pkv_evict", "pkv_evict_fp8", "pkv_evict_workspace_size")))
         _binding = _pkv_binding
     return _binding
 
@@ -460,6 +465,41 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
     index = _index(latent_cache, "latent_cache")
     return (_binding or _native()).attend_latent(index, stream, q, latent_cache, block_tables, seq_lens,
                                                  query_start_loc, scale, out, workspace, max_query_len)
+
+
+def workspace_size_weigh(desc, num_seqs, num_tokens, device=None, max_query_len=0, num_keys=0):
+    """Workspace bytes weigh and weigh_fp8 need for the same max_query_len and
+    num_keys (0 = unknown: what num_tokens and the tables' width allow)."""
+    n = _sz(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        _check(lib().pkv_weigh_workspace_size(ctypes.byref(desc), int(num_seqs), int(num_tokens), int(max_query_len),
+                                              int(num_keys), ctypes.byref(n)), "pkv_weigh_workspace_size")
+    return n.value
+
+
+def weigh(q, k_cache, scores, block_tables, seq_lens, query_start_loc, scale, decay=1.0, first=None, scored=None,
+          workspace=None, stream=None, max_query_len=0, num_keys=0):
+    """Add to ``scores`` (fp32 [NB, Hkv, 16], a value in the place of each
+    cached row) the attention weights that the rows of ``q`` [T, Hq, D] give
+    each cached token, summed over rows and over the query heads of a kv head;
+    rows and keys are as in attend().  Older scores are multiplied by
+    ``decay`` (0: not read); tokens from ``scored`` on (int32 [B]; None: this
+    step's own) have none yet.  The ``first`` tokens of a sequence (int32 [B])
+    get none.  ``max_query_len`` and ``num_keys`` (the sum of the lengths, each
+    rounded up to 16) are host-side bounds, 0 = unknown: sequences beyond them
+    are skipped and flagged, so they must hold; they keep the workspace small."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).weigh(index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
+                                         scale, decay, first, scored, workspace, max_query_len, num_keys)
+
+
+def weigh_fp8(q, k_cache, k_scale, scores, block_tables, seq_lens, query_start_loc, scale, decay=1.0, first=None,
+              scored=None, workspace=None, stream=None, max_query_len=0, num_keys=0):
+    """weigh over FP8 pages (codes and scale bytes as in write_fp8)."""
+    index = _index(k_cache, "k_cache")
+    return (_binding or _native()).weigh_fp8(index, stream, q, k_cache, scores, block_tables, seq_lens,
+                                             query_start_loc, scale, decay, first, scored, workspace, max_query_len,
+                                             num_keys, k_scale)
 
 
 def workspace_size_evict(desc, num_seqs, device=None):

@@ -9,6 +9,7 @@
 // stay alive until the asynchronous consumer is done with them).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
@@ -460,6 +461,85 @@ int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache, const int
                            num_tokens, max_query_len, scale,       out,       workspace,       workspace_bytes,
                            *desc};
   return launch_attend_latent(ctx, a);
+}
+
+// Rows, units of work and keys are counted in 64 bits on the device, tokens and
+// positions in 32.
+static int check_weigh(const pkv_desc* d, int32_t num_seqs, int32_t num_tokens) {
+  if (int e = check_desc(d)) return e;
+  if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS || num_tokens < 0 || num_tokens > INT32_MAX - 1024)
+    return PKV_ERR_RANGE;
+  return check_positions(d);
+}
+
+// The host's bounds as they are used: where unknown, what the call's sizes allow.
+static int32_t most_rows(int32_t max_query_len, int32_t num_tokens) {
+  return max_query_len > 0 ? std::min(max_query_len, num_tokens) : num_tokens;
+}
+static int64_t most_keys(const pkv_desc* d, int32_t num_seqs, int64_t num_keys) {
+  const int64_t top = int64_t(num_seqs) * d->max_blocks_per_seq * kPage;
+  return num_keys > 0 ? std::min(num_keys, top) : top;
+}
+
+int pkv_weigh_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+                             int64_t num_keys, size_t* bytes) {
+  if (int e = check_weigh(desc, num_seqs, num_tokens)) return e;
+  if (!bytes) return PKV_ERR_NULL;
+  int err = PKV_OK;
+  const DeviceInfo* dev = current_device(&err);
+  if (!dev) return err;
+  *bytes = weigh_workspace_bytes(*dev, *desc, num_seqs, num_tokens, most_rows(max_query_len, num_tokens),
+                                 most_keys(desc, num_seqs, num_keys));
+  return PKV_OK;
+}
+
+static int weigh(const pkv_bf16* q, const void* k_cache, const uint8_t* k_scale, float* scores,
+                 const int32_t* block_tables, const int32_t* seq_lens, const int32_t* query_start_loc,
+                 const int32_t* first, const int32_t* scored, int32_t num_seqs, int32_t num_tokens,
+                 int32_t max_query_len, int64_t num_keys, float scale, float decay, void* workspace,
+                 size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream, bool fp8) {
+  if (int e = check_weigh(desc, num_seqs, num_tokens)) return e;
+  // (not >=: a NaN is refused too)
+  if (!(scale >= 0.f) || !std::isfinite(scale) || !(decay >= 0.f) || !std::isfinite(decay)) return PKV_ERR_RANGE;
+  if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+  if (!q || !k_cache || (fp8 && !k_scale) || !scores || !block_tables || !seq_lens || !query_start_loc || !workspace)
+    return PKV_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(k_scale, 16) || !aligned(scores, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(query_start_loc, 4) || !aligned(first, 4) ||
+      !aligned(scored, 4) || !aligned(workspace, 256))
+    return PKV_ERR_ALIGN;
+  LaunchCtx ctx{};
+  if (int e = make_ctx(stream, &ctx)) return e;
+  WeighArgs a{};
+  a.q = q, a.k_cache = k_cache, a.k_scale = k_scale, a.scores = scores;
+  a.block_tables = block_tables, a.seq_lens = seq_lens, a.query_start_loc = query_start_loc;
+  a.first = first, a.scored = scored;
+  a.num_seqs = num_seqs, a.num_tokens = num_tokens;
+  a.max_rows = most_rows(max_query_len, num_tokens);
+  a.num_keys = most_keys(desc, num_seqs, num_keys);
+  a.qscale = scale * 1.4426950408889634f;
+  a.decay = decay;
+  a.workspace = workspace, a.workspace_bytes = workspace_bytes;
+  a.desc = *desc;
+  a.status = ctx.status;
+  return launch_weigh(ctx, a, fp8);
+}
+
+int pkv_weigh(const pkv_bf16* q, const pkv_bf16* k_cache, float* scores, const int32_t* block_tables,
+              const int32_t* seq_lens, const int32_t* query_start_loc, const int32_t* first, const int32_t* scored,
+              int32_t num_seqs, int32_t num_tokens, int32_t max_query_len, int64_t num_keys, float scale,
+              float decay, void* workspace, size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream) {
+  return weigh(q, k_cache, nullptr, scores, block_tables, seq_lens, query_start_loc, first, scored, num_seqs,
+               num_tokens, max_query_len, num_keys, scale, decay, workspace, workspace_bytes, desc, stream, false);
+}
+
+int pkv_weigh_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const uint8_t* k_scale, float* scores,
+                  const int32_t* block_tables, const int32_t* seq_lens, const int32_t* query_start_loc,
+                  const int32_t* first, const int32_t* scored, int32_t num_seqs, int32_t num_tokens,
+                  int32_t max_query_len, int64_t num_keys, float scale, float decay, void* workspace,
+                  size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream) {
+  return weigh(q, k_cache, k_scale, scores, block_tables, seq_lens, query_start_loc, first, scored, num_seqs,
+               num_tokens, max_query_len, num_keys, scale, decay, workspace, workspace_bytes, desc, stream, true);
 }
 
 int pkv_evict_workspace_size(const pkv_desc* desc, int32_t num_seqs, size_t* bytes) {

@@ -1,5 +1,6 @@
 // pkv_binding.cpp -- Python arguments of the rotated appends, of latent
-// attention and of eviction, checked and handed to libpkv's entry points.
+// attention, of attention weights and of eviction, checked and handed to libpkv's
+// entry points.
 //
 // A decode step's append is 2 us of GPU work.  Its checks of a dozen tensors
 // and the marshalling of 18 arguments took 13 us through Python and ctypes (20
@@ -40,6 +41,9 @@ decltype(&pkv_write_rope_axes_fp8) g_write_rope_axes_fp8;
 decltype(&pkv_write_latent) g_write_latent;
 decltype(&pkv_attend_latent) g_attend_latent;
 decltype(&pkv_attend_latent_workspace_size) g_workspace_size;
+decltype(&pkv_weigh) g_weigh;
+decltype(&pkv_weigh_fp8) g_weigh_fp8;
+decltype(&pkv_weigh_workspace_size) g_weigh_size;
 decltype(&pkv_evict) g_evict;
 decltype(&pkv_evict_fp8) g_evict_fp8;
 decltype(&pkv_evict_workspace_size) g_evict_size;
@@ -208,6 +212,11 @@ int64_t whole_of(PyObject* whole) {  // takes over the reference
 
 // A host-side bound: what is negative counts as 0, what is above `top` as top.
 int64_t bound_of(PyObject* o, int64_t top) { return std::clamp<int64_t>(whole_of(PyNumber_Long(o)), 0, top); }
+
+int64_t int_of(PyObject* o, const char* name) {
+  if (!PyIndex_Check(o)) RAISE(TypeError, "%s must be an int, got %s", name, Py_TYPE(o)->tp_name);
+  return whole_of(PyNumber_Index(o));
+}
 
 pkv_rope rope_of(PyObject* o, PyObject* interleaved, int index) {
   const at::Tensor& t = take(o, "cos_sin", at::kFloat, 2, index);
@@ -448,6 +457,68 @@ const int32_t* per_sequence(PyObject* o, const char* name, int64_t seqs, int ind
   return in<int32_t>(t);
 }
 
+// (index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
+//  scale, decay, first, scored, workspace, max_query_len, num_keys[, k_scale])
+template <bool F8>
+PyObject* weigh(PyObject* const* a, Py_ssize_t n) {
+  need_args(n, F8 ? 16 : 15);
+  const int index = device_of(a[0]);
+  const at::Tensor& kc = take(a[3], "k_cache", F8 ? at::kByte : at::kBFloat16, 4, index);
+  const at::Tensor& q = take(a[2], "q", at::kBFloat16, 3, index);
+  const at::Tensor& scores = take(a[4], "scores", at::kFloat, 3, index);
+  const at::Tensor& tables = take(a[5], "block_tables", at::kInt, 2, index);
+  const at::Tensor& lens = take(a[6], "seq_lens", at::kInt, 1, index);
+  const at::Tensor& qsl = take(a[7], "query_start_loc", at::kInt, 1, index);
+  const int64_t B = lens.size(0);
+  if (qsl.size(0) != B + 1 || tables.size(0) != B)
+    RAISE(ValueError, "seq_lens [B], query_start_loc [B+1] and block_tables [B, M] disagree");
+  if (kc.size(3) != q.size(2)) RAISE(ValueError, "k_cache and q shapes disagree");
+  if (scores.sizes() != kc.sizes().slice(0, 3)) RAISE(ValueError, "scores must be [NB, Hkv, P] like k_cache");
+  [[maybe_unused]] const uint8_t* ks = nullptr;
+  if constexpr (F8) {
+    const at::Tensor& s = take(a[15], "k_scale", at::kByte, 3, index);
+    if (s.sizes() != kc.sizes().slice(0, 3))
+      RAISE(ValueError, "FP8 pools must be codes [NB, Hkv, P, D] and scales [NB, Hkv, P]");
+    ks = in<uint8_t>(s);
+  }
+  const float scale = float(number_of(a[8], "scale")), decay = float(number_of(a[9], "decay"));
+  const int32_t* first = per_sequence(a[10], "first", B, index);
+  const int32_t* scored = per_sequence(a[11], "scored", B, index);
+  const int32_t most = int32_t(std::clamp<int64_t>(int_of(a[13], "max_query_len"), 0, INT32_MAX));
+  const int64_t keys = std::max<int64_t>(int_of(a[14], "num_keys"), 0);
+  const pkv_desc desc{i32(kc.size(0), "k_cache"), i32(kc.size(2), "k_cache"), i32(kc.size(1), "k_cache"),
+                      i32(q.size(1), "q"),        i32(kc.size(3), "k_cache"), i32(tables.size(1), "block_tables")};
+  const int32_t seqs = i32(B, "seq_lens"), tokens = i32(q.size(0), "q");
+  const Stream stream(a[1], index);
+  at::Tensor scratch;
+  if (a[12] == Py_None) {
+    size_t bytes = 0;
+    run("pkv_weigh_workspace_size", index, [&] { return g_weigh_size(&desc, seqs, tokens, most, keys, &bytes); });
+    scratch = stream.fresh({int64_t(bytes)}, at::kByte, index);
+  } else {
+    scratch = take(a[12], "workspace", at::kByte, 1, index);
+  }
+  void* ws = inout<void>(scratch);
+  const size_t ws_bytes = size_t(scratch.size(0));
+  const auto* qp = in<pkv_bf16>(q);
+  auto* sp = inout<float>(scores);
+  const int32_t *bt = in<int32_t>(tables), *sl = in<int32_t>(lens), *starts = in<int32_t>(qsl);
+  if constexpr (F8) {
+    const auto* kp = in<pkv_fp8>(kc);
+    run("pkv_weigh_fp8", index, [&] {
+      return g_weigh_fp8(qp, kp, ks, sp, bt, sl, starts, first, scored, seqs, tokens, most, keys, scale, decay, ws,
+                         ws_bytes, &desc, stream.handle);
+    });
+  } else {
+    const auto* kp = in<pkv_bf16>(kc);
+    run("pkv_weigh", index, [&] {
+      return g_weigh(qp, kp, sp, bt, sl, starts, first, scored, seqs, tokens, most, keys, scale, decay, ws, ws_bytes,
+                     &desc, stream.handle);
+    });
+  }
+  return Py_NewRef(Py_None);
+}
+
 // (index, stream, k_cache, v_cache, scores, block_tables, seq_lens, keep,
 //  first, recent, new_lens, workspace[, k_scale, v_scale])
 template <bool F8>
@@ -476,8 +547,7 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   if (a[7] == Py_None) RAISE(TypeError, "keep must be a torch.Tensor");
   const int32_t* keep = per_sequence(a[7], "keep", B, index);
   const int32_t* first = per_sequence(a[8], "first", B, index);
-  if (!PyIndex_Check(a[9])) RAISE(TypeError, "recent must be an int, got %s", Py_TYPE(a[9])->tp_name);
-  const int64_t recent = whole_of(PyNumber_Index(a[9]));
+  const int64_t recent = int_of(a[9], "recent");
   if (recent < 0) RAISE(ValueError, "recent must not be negative");
   const int32_t last = int32_t(std::min<int64_t>(recent, INT32_MAX));
   const pkv_desc desc{i32(kc.size(0), "k_cache"), i32(kc.size(2), "k_cache"), i32(kc.size(1), "k_cache"),
@@ -521,7 +591,7 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
 
 // (PkvError, addresses of the entry points in the order below)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  need_args(n, 11);
+  need_args(n, 14);
   Py_ssize_t next = 1;
   auto take_address = [&](auto& entry) {
     void* at = PyLong_AsVoidPtr(a[next++]);
@@ -535,6 +605,9 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   take_address(g_write_latent);
   take_address(g_attend_latent);
   take_address(g_workspace_size);
+  take_address(g_weigh);
+  take_address(g_weigh_fp8);
+  take_address(g_weigh_size);
   take_address(g_evict);
   take_address(g_evict_fp8);
   take_address(g_evict_size);
@@ -566,6 +639,8 @@ PyMethodDef g_methods[] = {method<bind>("bind"),
                            method<write_rope<true, false>>("write_rope_fp8"),
                            method<write_rope<false, true>>("write_rope_axes"),
                            method<write_rope<true, true>>("write_rope_axes_fp8"),
+                           method<weigh<false>>("weigh"),
+                           method<weigh<true>>("weigh_fp8"),
                            method<evict<false>>("evict"),
                            method<evict<true>>("evict_fp8"),
                            method<write_latent>("write_latent"),

@@ -112,6 +112,27 @@ struct LatentAttendArgs {
 size_t latent_workspace_bytes(const DeviceInfo& dev);
 int launch_attend_latent(const LaunchCtx& ctx, const LatentAttendArgs& a);
 
+// pkv_weigh / pkv_weigh_fp8 (pkv_weigh.cu).
+struct WeighArgs {
+  const uint16_t* q;
+  const void* k_cache;     // bf16 pages, or E4M3 codes
+  const uint8_t* k_scale;  // FP8 pages only
+  float* scores;
+  const int32_t *block_tables, *seq_lens, *query_start_loc, *first, *scored;
+  int32_t num_seqs, num_tokens;
+  int32_t max_rows;  // most query rows of a sequence
+  int64_t num_keys;  // most keys of the batch, each sequence's rounded up to 16
+  float qscale;      // scale * log2(e)
+  float decay;
+  void* workspace;
+  size_t workspace_bytes;
+  pkv_desc desc;
+  unsigned* status;
+};
+size_t weigh_workspace_bytes(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens,
+                             int32_t max_rows, int64_t num_keys);
+int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8);
+
 // pkv_evict / pkv_evict_fp8 (pkv_evict.cu).
 struct EvictArgs {
   void *k_cache, *v_cache;
