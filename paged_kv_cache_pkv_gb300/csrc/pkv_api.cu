@@ -12,6 +12,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <limits>
 #include <mutex>
 #include <vector>
 
@@ -517,7 +518,8 @@ static int weigh(const pkv_bf16* q, const void* k_cache, const uint8_t* k_scale,
   a.num_seqs = num_seqs, a.num_tokens = num_tokens;
   a.max_rows = most_rows(max_query_len, num_tokens);
   a.num_keys = most_keys(desc, num_seqs, num_keys);
-  a.qscale = scale * 1.4426950408889634f;
+  // (a masked score is -infinity: scale 0, all keys alike, is a scale too small to part them)
+  a.qscale = std::max(scale * 1.4426950408889634f, std::numeric_limits<float>::min());
   a.decay = decay;
   a.workspace = workspace, a.workspace_bytes = workspace_bytes;
   a.desc = *desc;

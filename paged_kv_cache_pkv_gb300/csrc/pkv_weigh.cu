@@ -5,38 +5,477 @@
 //   lse[j, h] = log sum_{k <= pos j} exp(scale q[j, h] . K[k])
 //   w[k]      = sum_{j, h: k <= pos j} exp(scale q[j, h] . K[k] - lse[j, h])
 //
-// A weight needs its row's sum over all keys first, so there are two passes:
-// one over the keys of each row, one over the rows of each key.  Both work in
-// the log2 domain (exp2), sums in fp32.
+// A weight needs its row's sum over all keys first, so there are two passes.
+// Both work in the log2 domain (exp2), sums in fp32.
+//
+// Few rows (up to kSmallRows query rows x heads of a kv head a sequence):
+// bound by the bytes of K, which are read once.
+//  * pkv_weigh_scores_kernel: K pages against the rows on warp-level MMAs, the
+//    page's 16 keys as M, the rows as N (8, 16 or 32).  A product of two
+//    vectors does not go by the order of their elements, so a lane takes 16
+//    contiguous bytes of a key's row as its elements of two k-steps, and the
+//    queries' fragments are permuted alike: pages go from HBM to registers in
+//    16-byte loads, without shared memory or barriers, two pages (E4M3: four)
+//    of a warp in flight.  Each lane keeps running maxima and sums of its own
+//    keys, reduced over lanes once a piece.  Scores go to the workspace, 4
+//    bytes a (row, key): at one row of four heads a sixteenth of K's bytes,
+//    and mostly read back from L2.
+//  * pkv_weigh_add_kernel: joins the pieces' sums and turns scores into
+//    weights, one key a lane, with the update of the paged score.
+//  * Units of work are pages of a kv head in the order (sequence, head, page);
+//    a warp takes an equal share of them, so that lengths of any mixture load
+//    all warps alike.  Piece p of the row has the record (items before it +
+//    warps before it), unique as one of them grows from piece to piece.
+//  * E4M3 pages: codes become f16 exactly; the bf16 queries become f16 under a
+//    power of two a row that takes its largest element to [2^14, 2^15).  What
+//    that loses of an element is below 2^-24 in f16's units, 2^-38 of the
+//    largest: less than fp32 sums of 128 terms lose.  The key's scale is
+//    applied to the finished score.
 #include <cmath>
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "pkv_common.cuh"
-#include "pkv_internal.h"
+#include "pkv_weigh.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kWeighThreads = 128;
+constexpr int kSmallRows = 32;
+constexpr int kWsThreads = 256;
+constexpr int kWsWarps = kWsThreads / 32;
 
-struct Sequence {
-  int q0, n, L;
+// The workspace of a call.
+struct WeighLayout {
+  size_t records, scores, sums, total;
 };
 
-// Sequence b's rows and length; false (and flagged) where they do not fit.
-__device__ __forceinline__ bool sequence_of(const WeighArgs& p, int b, Sequence& s) {
-  const int q0 = __ldg(p.query_start_loc + b), q1 = __ldg(p.query_start_loc + b + 1), L = __ldg(p.seq_lens + b);
-  s = {q0, 0, 0};
-  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || L < 0 || q1 - q0 > L ||
-      (L > 0 && (L - 1) / kPage >= p.desc.max_blocks_per_seq) || (b == 0 && q0 != 0) || q1 - q0 > p.max_rows) {
-    flag_status(p.status, PKV_STATUS_BAD_QUERY);
-    return false;
-  }
-  s.n = q1 - q0;
-  s.L = L;
-  return true;
+// What the kernels of few rows need beside the call's arguments.
+struct SmallParams {
+  WeighArgs a;
+  float2* records;  // [items + warps][rows]: (maximum, sum) of a piece
+  float* scores;    // [units][16][stride]
+  int64_t max_units;
+  int32_t small_rows;   // rows x heads of a sequence that they take
+  int32_t stride_log2;  // of a key's scores
+  int32_t share_warps;  // warps of pkv_weigh_scores_kernel
+};
+
+__device__ __forceinline__ int64_t share_of(const SmallParams& p, int64_t units) {
+  return max(int64_t(1), (units + p.share_warps - 1) / p.share_warps);
 }
+
+// Units before each sequence, in shared memory: [num_seqs + 1].  Sequences of
+// other sizes, without rows or beyond the workspace have none.
+__device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before, int64_t (*warp_sums)[2]) {
+  const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads, G = p.a.desc.num_q_heads / Hkv;
+  const int per = (B + kWsThreads - 1) / kWsThreads;
+  const int b0 = min(B, int(threadIdx.x) * per), b1 = min(B, b0 + per);
+  int64_t sum[2] = {0, 0}, total[2];
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    WeighSequence s;
+    bad = !weigh_sequence(p.a, b, s) || bad;
+    const int64_t units =
+        s.n > 0 && int64_t(s.n) * G <= p.small_rows ? int64_t(Hkv) * ((s.L + kPage - 1) / kPage) : 0;
+    before[b] = units;
+    sum[0] += units;
+  }
+  // The first sequence that does not fit the workspace whole ends the list.
+  __shared__ unsigned long long limit;
+  if (threadIdx.x == 0) limit = ~0ull;
+  block_scan<kWsThreads>(sum, total, warp_sums);
+  int64_t run = sum[0];
+  for (int b = b0; b < b1; ++b) {
+    const int64_t units = before[b];
+    if (units > 0 && run + units > p.max_units) {
+      atomicMin(&limit, static_cast<unsigned long long>(run));
+      bad = true;
+    }
+    before[b] = run;
+    run += units;
+  }
+  __syncthreads();
+  const int64_t top = int64_t(min(limit, 0x7FFFFFFFFFFFFFFFull));
+  for (int b = b0; b < b1; ++b) before[b] = min(before[b], top);
+  if (threadIdx.x == 0) before[B] = min(total[0], top);
+  if (bad && blockIdx.x == 0) flag_status(p.a.status, PKV_STATUS_BAD_QUERY);
+  __syncthreads();
+}
+
+// Last sequence with before[b] <= unit (one that has units).
+__device__ __forceinline__ int sequence_at(const int64_t* before, int B, int64_t unit) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= unit) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// 16 bytes that are read once: past L1, and first to leave L2, where the scores
+// written meanwhile are read back.
+__device__ __forceinline__ uint4 load_once(const void* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Four E4M3 codes (lowest byte first) -> two f16x2, exactly.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// One page of K as a lane holds it: rows lane / 4 and lane / 4 + 8, of each row
+// the 16-byte pieces lane % 4, lane % 4 + 4, ...
+template <bool F8>
+struct KeyPage {
+  static constexpr int kPieces = F8 ? 2 : 4;
+  uint4 lo[kPieces], hi[kPieces];
+  uint32_t sc_lo, sc_hi;  // E4M3: the rows' scale bytes
+};
+
+template <int NT, bool F8>
+__global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_kernel(const SmallParams p) {
+  __shared__ int64_t before[kMaxSeqs + 1];
+  __shared__ int64_t warp_sums[kWsWarps][2];
+  griddep_wait();
+  griddep_launch_dependents();  // only pkv_weigh_add_kernel follows; it waits
+  plan_units(p, before, warp_sums);
+  const WeighArgs& a = p.a;
+  const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, Hq = a.desc.num_q_heads, G = Hq / Hkv;
+  const int lane = threadIdx.x & 31;
+  const int row = lane >> 2, t = lane & 3;
+  const int64_t units = before[B], share = share_of(p, units);
+  const int64_t warp = int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5);
+  int64_t u = min(units, warp * share);
+  const int64_t end = min(units, u + share);
+  if (u >= end) return;
+  constexpr int kPieces = KeyPage<F8>::kPieces;
+  constexpr int kDeep = F8 ? 4 : 2;      // pages in flight
+  constexpr int kPieceBytes = 64;        // of a row, between a lane's pieces
+  constexpr int kRowBytes = F8 ? kHeadDim : 2 * kHeadDim;
+  const int stride = 1 << p.stride_log2;
+  const uint64_t policy = l2_evict_first_policy();
+  int b = sequence_at(before, B, u);
+  while (u < end) {
+    WeighSequence s;
+    weigh_sequence(a, b, s);
+    const int pages = (s.L + kPage - 1) / kPage;
+    const int64_t rem = u - before[b];
+    const int g = int(rem / pages), first = int(rem % pages);
+    const int count = int(min(end - u, int64_t(pages - first)));
+    const int rows = s.n * G;  // the group's rows, j * G + h
+
+    // ---- the rows, as B fragments: lane's column row, its elements as in a key ----
+    uint32_t qf[NT][8][2];
+    float unscale[NT][2];  // E4M3: of the lane's two score columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int col = nt * 8 + row;
+      const bool live = col < rows;
+      const uint16_t* qr = a.q + (int64_t(s.q0 + (live ? col / G : 0)) * Hq + g * G + (live ? col % G : 0)) * kHeadDim;
+      if constexpr (!F8) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = __ldg(reinterpret_cast<const uint4*>(qr + c * 32 + t * 8));
+          qf[nt][2 * c][0] = v.x, qf[nt][2 * c][1] = v.y;
+          qf[nt][2 * c + 1][0] = v.z, qf[nt][2 * c + 1][1] = v.w;
+        }
+      } else {
+        uint4 v[2][2];
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v[c][h] = make_uint4(0, 0, 0, 0);
+            if (live) v[c][h] = __ldg(reinterpret_cast<const uint4*>(qr + c * 64 + t * 16 + h * 8));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = fmaxf(top, fmaxf(fabsf(bf_lo(word(v[c][h], i))), fabsf(bf_hi(word(v[c][h], i)))));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^x takes top to [2^14, 2^15); x is bounded so that 2^x and 2^-x are
+        // normal floats (a row below 2^-100 then has elements below 1)
+        const int x = top == 0.f ? 0 : max(-113, min(114, 14 + 127 - int(__float_as_uint(top) >> 23)));
+        const float up = __uint_as_float(uint32_t(127 + x) << 23), down = __uint_as_float(uint32_t(127 - x) << 23);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // words of two elements
+            const uint32_t w = word(v[c][i >> 2], i & 3);
+            const __half2 h = __floats2half2_rn(bf_lo(w) * up, bf_hi(w) * up);
+            qf[nt][c * 4 + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        unscale[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        unscale[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      }
+    }
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = kWeighNoScore;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    // ---- pages ----
+    // Page ids 32 at a time, one a lane; an id outside the pool is flagged and
+    // page 0 read in its place.
+    const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq + first;
+    int ids = 0;
+    auto page_id = [&](int i) {
+      if ((i & 31) == 0) {
+        ids = i + lane < count ? __ldg(table + i + lane) : 0;
+        if (ids < 0 || ids >= a.desc.num_blocks) {
+          flag_status(a.status, PKV_STATUS_BAD_BLOCK);
+          ids = 0;
+        }
+      }
+      return __shfl_sync(0xffffffffu, ids, i & 31);
+    };
+    auto fetch = [&](KeyPage<F8>& k, int i) {
+      const int64_t r = (int64_t(page_id(i)) * Hkv + g) * kPage + row;
+      const char* at = static_cast<const char*>(a.k_cache) + r * kRowBytes + t * 16;
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        k.lo[c] = load_once(at + c * kPieceBytes, policy);
+        k.hi[c] = load_once(at + 8 * kRowBytes + c * kPieceBytes, policy);
+      }
+      if constexpr (F8) {
+        k.sc_lo = __ldg(a.k_scale + r);
+        k.sc_hi = __ldg(a.k_scale + r + 8);
+      }
+    };
+    auto weigh_page = [&](const KeyPage<F8>& k, int i) {
+      float d[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (F8) {
+          codes_f16(word(k.lo[ks >> 2], ks & 3), a0, a2);
+          codes_f16(word(k.hi[ks >> 2], ks & 3), a1, a3);
+        } else {
+          const int w = (ks & 1) * 2;
+          a0 = word(k.lo[ks >> 1], w), a2 = word(k.lo[ks >> 1], w + 1);
+          a1 = word(k.hi[ks >> 1], w), a3 = word(k.hi[ks >> 1], w + 1);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (NT == 1 || nt * 8 < rows) mma16816<F8>(d[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+      }
+      const int key = (first + i) * kPage + row;
+      const bool edge = (first + i) * kPage + kPage - 1 > s.L - s.n;  // some row does not see all of the page
+      float* out = p.scores + ((u + i) * kPage + row) * stride + 2 * t;
+      float klo = 1.f, khi = 1.f;
+      if constexpr (F8) {
+        klo = __uint_as_float(k.sc_lo << 23);
+        khi = __uint_as_float(k.sc_hi << 23);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (NT > 1 && nt * 8 >= rows) break;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float x = d[nt][j], y = d[nt][2 + j];
+          if constexpr (F8) {
+            x *= klo * unscale[nt][j];
+            y *= khi * unscale[nt][j];
+          }
+          if (edge) {
+            const int last = s.L - s.n + (nt * 8 + 2 * t + j) / G;
+            if (key > last) x = -INFINITY;
+            if (key + 8 > last) y = -INFINITY;
+          }
+          const float mn = fmaxf(m[nt][j], fmaxf(x, y));
+          l[nt][j] = l[nt][j] * ex2((m[nt][j] - mn) * a.qscale) + ex2((x - mn) * a.qscale) + ex2((y - mn) * a.qscale);
+          m[nt][j] = mn;
+          d[nt][j] = x;
+          d[nt][2 + j] = y;
+        }
+        if (nt * 8 + 2 * t < stride) {
+          *reinterpret_cast<float2*>(out + nt * 8) = make_float2(d[nt][0], d[nt][1]);
+          *reinterpret_cast<float2*>(out + 8 * stride + nt * 8) = make_float2(d[nt][2], d[nt][3]);
+        }
+      }
+    };
+    KeyPage<F8> k[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (i < count) fetch(k[i], i);
+    for (int i = 0; i < count; i += kDeep) {
+#pragma unroll
+      for (int j = 0; j < kDeep; ++j) {
+        if (i + j >= count) break;
+        weigh_page(k[j], i + j);
+        if (i + j + kDeep < count) fetch(k[j], i + j + kDeep);
+      }
+    }
+
+    // ---- the piece's maxima and sums, over the lanes of a column ----
+    float2* rec = p.records + (int64_t(b) * Hkv + g + warp) * (8 * NT) + 2 * t;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          const float mo = __shfl_xor_sync(0xffffffffu, m[nt][j], o), lo = __shfl_xor_sync(0xffffffffu, l[nt][j], o);
+          const float mn = fmaxf(m[nt][j], mo);
+          l[nt][j] = l[nt][j] * ex2((m[nt][j] - mn) * a.qscale) + lo * ex2((mo - mn) * a.qscale);
+          m[nt][j] = mn;
+        }
+      }
+      if (row == 0)
+        *reinterpret_cast<float4*>(rec + nt * 8) = make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
+    }
+    u += count;
+    while (b + 1 < B && before[b + 1] <= u) ++b;  // u < end: some later sequence has it
+  }
+}
+
+// Scores -> weights -> paged scores.  STRIDE scores a key; ROWS the records' width.
+template <int STRIDE, int ROWS>
+__global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallParams p) {
+  __shared__ int64_t before[kMaxSeqs + 1];
+  __shared__ int64_t warp_sums[kWsWarps][2];
+  plan_units(p, before, warp_sums);  // of arrays that the kernel before only reads
+  griddep_wait();
+  const WeighArgs& a = p.a;
+  const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
+  const int lane = threadIdx.x & 31;
+  const int64_t units = before[B], share = share_of(p, units);
+  const int64_t warps = int64_t(gridDim.x) * kWsWarps, mine = (units + warps - 1) / warps;
+  int64_t u = min(units, (int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5)) * mine);
+  const int64_t end = min(units, u + mine);
+  int b = u < end ? sequence_at(before, B, u) : 0;
+  while (u < end) {
+    WeighSequence s;
+    weigh_sequence(a, b, s);
+    const int pages = (s.L + kPage - 1) / kPage;
+    const int64_t rem = u - before[b];
+    const int g = int(rem / pages), first = int(rem % pages);
+    const int count = int(min(end - u, int64_t(pages - first)));
+    const int rows = s.n * G;
+    const int from = a.first ? max(0, __ldg(a.first + b)) : 0;
+    const int scored = a.decay == 0.f ? 0 : a.scored ? __ldg(a.scored + b) : s.L - s.n;
+
+    // ---- log-sums of the rows: a column a lane, pieces in turn ----
+    constexpr int kCols = ROWS < 32 ? ROWS : 32;
+    const int64_t u0 = before[b] + int64_t(g) * pages;
+    const int64_t w0 = u0 / share, w1 = (u0 + pages - 1) / share;
+    const float2* rec = p.records + (int64_t(b) * Hkv + g) * ROWS + lane % kCols;
+    float m = kWeighNoScore, l = 0.f;
+    for (int64_t w = w0 + lane / kCols; w <= w1; w += 32 / kCols) {
+      const float2 x = __ldcg(rec + w * ROWS);
+      const float mn = fmaxf(m, x.x);
+      l = l * ex2((m - mn) * a.qscale) + x.y * ex2((x.x - mn) * a.qscale);
+      m = mn;
+    }
+#pragma unroll
+    for (int o = kCols; o < 32; o <<= 1) {
+      const float mo = __shfl_xor_sync(0xffffffffu, m, o), lo = __shfl_xor_sync(0xffffffffu, l, o);
+      const float mn = fmaxf(m, mo);
+      l = l * ex2((m - mn) * a.qscale) + lo * ex2((mo - mn) * a.qscale);
+      m = mn;
+    }
+    const float mine_lse = m * a.qscale + __log2f(l);
+    // Columns without a row get weight 0; whole MMA tiles of them have no scores.
+    const int columns = (rows + 7) / 8 * 8;
+    float lse[STRIDE];
+#pragma unroll
+    for (int c = 0; c < STRIDE; ++c) {
+      lse[c] = __shfl_sync(0xffffffffu, mine_lse, c % kCols);
+      if (c >= rows) lse[c] = INFINITY;
+    }
+
+    // ---- a key a lane, kDeep pairs of pages at a time ----
+    const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq;
+    constexpr int kDeep = STRIDE <= 8 ? 4 : 1;
+    for (int i = 0; i < count; i += 2 * kDeep) {
+      int64_t at[kDeep];
+      float old[kDeep], w[kDeep];
+      float2 x[kDeep][STRIDE / 2];
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        const int page = first + i + 2 * d + (lane >> 4);
+        const int key = page * kPage + (lane & 15);
+        at[d] = -1;
+        if (i + 2 * d + (lane >> 4) < count && key >= from && key < s.L) {
+          const int id = __ldg(table + page);
+          if (id >= 0 && id < a.desc.num_blocks) at[d] = (int64_t(id) * Hkv + g) * kPage + (lane & 15);
+        }
+        if (at[d] >= 0) {
+          const float2* src = reinterpret_cast<const float2*>(
+              p.scores + ((u + i + 2 * d) * kPage + lane) * STRIDE);
+#pragma unroll
+          for (int c = 0; c < STRIDE / 2; c += 2) {
+            if (STRIDE > 8 && 2 * c >= columns) break;
+            if constexpr (STRIDE == 2) {
+              x[d][0] = __ldcg(src);
+            } else {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + c));
+              x[d][c] = make_float2(v.x, v.y);
+              x[d][c + 1] = make_float2(v.z, v.w);
+            }
+          }
+          old[d] = key < scored ? __ldcg(a.scores + at[d]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kDeep; ++d) {
+        if (at[d] < 0) continue;
+        w[d] = 0.f;
+#pragma unroll
+        for (int c = 0; c < STRIDE / 2; ++c) {
+          if (STRIDE > 8 && 2 * c >= columns) break;
+          w[d] += ex2(fmaf(x[d][c].x, a.qscale, -lse[2 * c])) + ex2(fmaf(x[d][c].y, a.qscale, -lse[2 * c + 1]));
+        }
+        a.scores[at[d]] = fmaf(a.decay, old[d], w[d]);
+      }
+    }
+    u += count;
+    while (b + 1 < B && before[b + 1] <= u) ++b;
+  }
+  // (behind a barrier: a block's first thread to say so speaks for all of them)
+  __syncthreads();
+  griddep_launch_dependents();
+}
+
+constexpr int kWeighThreads = 128;
 
 template <bool F8>
 __device__ __forceinline__ float dot(const WeighArgs& p, const float* q, int64_t row) {
@@ -70,7 +509,7 @@ __device__ __forceinline__ int64_t key_row(const WeighArgs& p, int b, int g, int
 
 // One warp a (query row, head): lanes take keys in turn.
 template <bool F8>
-__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_sums_kernel(const WeighArgs p) {
+__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_sums_kernel(const WeighArgs p, float* sums) {
   griddep_wait();
   __shared__ float sq[kWeighThreads / 32][kHeadDim];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -84,8 +523,8 @@ __global__ void __launch_bounds__(kWeighThreads) pkv_weigh_sums_kernel(const Wei
     if (__ldg(p.query_start_loc + mid) <= t) lo = mid;
     else hi = mid;
   }
-  Sequence s;
-  if (!sequence_of(p, lo, s) || t >= s.q0 + s.n) return;
+  WeighSequence s;
+  if (!weigh_sequence(p, lo, s) || t >= s.q0 + s.n || s.n * G <= kSmallRows) return;
   for (int d = lane; d < kHeadDim; d += 32) {
     const uint16_t x = p.q[item * kHeadDim + d];
     sq[warp][d] = __uint_as_float(uint32_t(x) << 16);
@@ -107,19 +546,19 @@ __global__ void __launch_bounds__(kWeighThreads) pkv_weigh_sums_kernel(const Wei
     l = (m == -INFINITY ? 0.f : l * ex2(m - mn)) + (mo == -INFINITY ? 0.f : lo_ * ex2(mo - mn));
     m = mn;
   }
-  if (lane == 0) static_cast<float*>(p.workspace)[item] = m + __log2f(l);
+  if (lane == 0) sums[item] = m + __log2f(l);
 }
 
 // One warp a (sequence, kv head, key): lanes take rows in turn.
 template <bool F8>
-__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_add_kernel(const WeighArgs p) {
+__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_all_kernel(const WeighArgs p, const float* sums) {
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hq = p.desc.num_q_heads, Hkv = p.desc.num_kv_heads, G = Hq / Hkv;
   const int b = blockIdx.y / Hkv, g = blockIdx.y % Hkv;
-  Sequence s;
-  if (!sequence_of(p, b, s) || s.n == 0) return;
-  const float* lse = static_cast<const float*>(p.workspace);
+  WeighSequence s;
+  if (!weigh_sequence(p, b, s) || s.n * G <= kSmallRows) return;
+  const float* lse = sums;
   const int first = p.first ? max(0, __ldg(p.first + b)) : 0;
   const int scored = p.scored ? __ldg(p.scored + b) : s.L - s.n;
   for (int k = first + blockIdx.x * (kWeighThreads / 32) + warp; k < s.L; k += gridDim.x * (kWeighThreads / 32)) {
@@ -139,39 +578,130 @@ __global__ void __launch_bounds__(kWeighThreads) pkv_weigh_add_kernel(const Weig
   }
 }
 
-template <class Kernel>
-int launch(const LaunchCtx& ctx, Kernel kernel, dim3 grid, const WeighArgs& a) {
+// Launched while the kernel before may still run, if that lets it.
+template <class... Params, class... Args>
+int launch(const LaunchCtx& ctx, void (*kernel)(Params...), dim3 grid, int threads, const Args&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kWeighThreads);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.stream = ctx.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   TraceScope ts(ctx.stream, PKV_K_WEIGH);
-  cudaLaunchKernelEx(&cfg, kernel, a);
+  cudaLaunchKernelEx(&cfg, kernel, args...);
   return ts.done();
+}
+
+// MMA columns of the few-rows kernels: rows x heads, rounded up.
+int column_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+// Scores a key in the workspace, as a power of two.
+int stride_log2(int64_t rows) {
+  int k = 1;
+  while ((1 << k) < rows) ++k;
+  return k;
+}
+
+// Rows x heads of a kv head that the few-rows kernels are launched for.
+int64_t small_rows(const pkv_desc& d, int32_t max_rows) {
+  const int64_t rows = int64_t(max_rows) * (d.num_q_heads / d.num_kv_heads);
+  return rows < kSmallRows ? rows : kSmallRows;
+}
+
+using ScoresKernel = void (*)(SmallParams);
+
+template <bool F8>
+ScoresKernel scores_kernel(int tiles) {
+  return tiles == 1   ? pkv_weigh_scores_kernel<1, F8>
+         : tiles == 2 ? pkv_weigh_scores_kernel<2, F8>
+                      : pkv_weigh_scores_kernel<4, F8>;
+}
+
+ScoresKernel add_kernel(int tiles, int stride) {
+  return stride == 2    ? pkv_weigh_add_kernel<2, 8>
+         : stride == 4  ? pkv_weigh_add_kernel<4, 8>
+         : stride == 8  ? pkv_weigh_add_kernel<8, 8>
+         : stride == 16 ? pkv_weigh_add_kernel<16, 16>
+                        : pkv_weigh_add_kernel<32, 32>;
+}
+
+// Blocks of the scores kernel on an SM: what its launch bounds ask for.
+int scores_ctas(int tiles) { return tiles == 1 ? 2 : 1; }
+
+int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int32_t max_rows, int64_t num_keys) {
+  const int64_t units = num_keys / kPage * d.num_kv_heads;
+  const int64_t most = int64_t(dev.sm_count) * scores_ctas(column_tiles(small_rows(d, max_rows)));
+  const int64_t want = (units + kWsWarps - 1) / kWsWarps;
+  return int(want < 1 ? 1 : want < most ? want : most);
+}
+
+int add_grid(const DeviceInfo& dev, const pkv_desc& d, int64_t num_keys) {
+  const int64_t units = num_keys / kPage * d.num_kv_heads;
+  const int64_t most = int64_t(dev.sm_count) * 8, want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
+  return int(want < 1 ? 1 : want < most ? want : most);
+}
+
+WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int32_t max_rows,
+                   int64_t num_keys) {
+  WeighLayout w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  const int64_t rows = small_rows(d, max_rows);
+  const size_t slots = size_t(num_seqs) * d.num_kv_heads +
+                       size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
+  w.records = take(slots * 8 * column_tiles(rows) * sizeof(float2));
+  w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * (size_t(1) << stride_log2(rows)) * sizeof(float));
+  w.sums = take(sizeof(float) * size_t(num_tokens) * size_t(d.num_q_heads));
+  w.total = off;
+  return w;
 }
 
 }  // namespace
 
-size_t weigh_workspace_bytes(const DeviceInfo&, const pkv_desc& d, int32_t, int32_t num_tokens, int32_t, int64_t) {
-  return align_up(sizeof(float) * size_t(num_tokens) * size_t(d.num_q_heads), 256);
+size_t weigh_workspace_bytes(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens,
+                             int32_t max_rows, int64_t num_keys) {
+  return layout(dev, d, num_seqs, num_tokens, max_rows, num_keys).total;
 }
 
 int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
-  if (a.workspace_bytes < weigh_workspace_bytes(*ctx.dev, a.desc, a.num_seqs, a.num_tokens, a.max_rows, a.num_keys))
-    return PKV_ERR_WORKSPACE;
-  const int64_t warps = int64_t(a.num_tokens) * a.desc.num_q_heads;
-  const int64_t pairs = int64_t(a.num_seqs) * a.desc.num_kv_heads;
+  const pkv_desc& d = a.desc;
+  const WeighLayout w = layout(*ctx.dev, d, a.num_seqs, a.num_tokens, a.max_rows, a.num_keys);
+  if (a.workspace_bytes < w.total) return PKV_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const int64_t rows = small_rows(d, a.max_rows);
+  const int tiles = column_tiles(rows);
+  const int grid = scores_grid(*ctx.dev, d, a.max_rows, a.num_keys);
+  SmallParams p{a,
+                reinterpret_cast<float2*>(ws + w.records),
+                reinterpret_cast<float*>(ws + w.scores),
+                a.num_keys / kPage * d.num_kv_heads,
+                int32_t(rows),
+                stride_log2(rows),
+                grid * kWsWarps};
+  if (int e = launch(ctx, fp8 ? scores_kernel<true>(tiles) : scores_kernel<false>(tiles), dim3(unsigned(grid)),
+                     kWsThreads, p))
+    return e;
+  if (int e = launch(ctx, add_kernel(tiles, 1 << p.stride_log2), dim3(unsigned(add_grid(*ctx.dev, d, a.num_keys))),
+                     kWsThreads, p))
+    return e;
+  if (int64_t(a.max_rows) * (d.num_q_heads / d.num_kv_heads) <= kSmallRows) return PKV_OK;
+  const int64_t warps = int64_t(a.num_tokens) * d.num_q_heads;
+  const int64_t pairs = int64_t(a.num_seqs) * d.num_kv_heads;
   if (pairs > 65535) return PKV_ERR_RANGE;
   constexpr int per = kWeighThreads / 32;
+  float* sums = reinterpret_cast<float*>(ws + w.sums);
   if (int e = launch(ctx, fp8 ? pkv_weigh_sums_kernel<true> : pkv_weigh_sums_kernel<false>,
-                     dim3(unsigned((warps + per - 1) / per)), a))
+                     dim3(unsigned((warps + per - 1) / per)), kWeighThreads, a, sums))
     return e;
-  return launch(ctx, fp8 ? pkv_weigh_add_kernel<true> : pkv_weigh_add_kernel<false>, dim3(64, unsigned(pairs)), a);
+  return launch(ctx, fp8 ? pkv_weigh_all_kernel<true> : pkv_weigh_all_kernel<false>, dim3(64, unsigned(pairs)),
+                kWeighThreads, a, sums);
 }
 
 }  // namespace pkv

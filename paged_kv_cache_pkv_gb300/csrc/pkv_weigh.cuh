@@ -1,0 +1,62 @@
+// pkv_weigh.cuh -- what the kernels of accumulated attention weights share: a
+// sequence's place in the batch and the way its units of work are counted.
+#pragma once
+
+#include "pkv_common.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+// Running maxima start here instead of at -infinity, whose difference with
+// itself is not a number; a masked score, -infinity, adds exp2(-inf) = 0.
+constexpr float kWeighNoScore = -1e30f;
+
+struct WeighSequence {
+  int q0, n, L;
+};
+
+// Sequence b's first row, rows and length; false where they do not fit.  Any
+// int32 may stand there.
+__device__ __forceinline__ bool weigh_sequence(const WeighArgs& p, int b, WeighSequence& s) {
+  const int q0 = __ldg(p.query_start_loc + b), q1 = __ldg(p.query_start_loc + b + 1), L = __ldg(p.seq_lens + b);
+  if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || L < 0 || q1 - q0 > L ||
+      (L > 0 && (L - 1) / kPage >= p.desc.max_blocks_per_seq) || (b == 0 && q0 != 0) || q1 - q0 > p.max_rows) {
+    s = {0, 0, 0};
+    return false;
+  }
+  s = {q0, q1 - q0, L};
+  return true;
+}
+
+// Exclusive prefix sums of two counts over the block's threads, in thread
+// order; the totals come back in `total`.
+template <int kThreads>
+__device__ __forceinline__ void block_scan(int64_t (&x)[2], int64_t (&total)[2], int64_t (*warp_sums)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl[2] = {x[0], x[1]};
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += v;
+    }
+  }
+  if (lane == 31) {
+    warp_sums[warp][0] = incl[0];
+    warp_sums[warp][1] = incl[1];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int64_t before = 0;
+    total[i] = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += warp_sums[w][i];
+      total[i] += warp_sums[w][i];
+    }
+    x[i] = before + incl[i] - x[i];
+  }
+}
+
+}  // namespace pkv
