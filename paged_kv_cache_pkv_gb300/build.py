@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
 BINDING = os.path.join(HERE, "_pkv_binding.so")
 SOURCES = ["pkv_api.cu", "pkv_write.cu", "pkv_decode.cu", "pkv_prefill.cu", "pkv_static.cu", "pkv_pool.cu",
-           "pkv_rope.cu", "pkv_latent.cu", "pkv_latent_pair.cu", "pkv_evict.cu", "pkv_weigh.cu"]
+           "pkv_rope.cu", "pkv_latent.cu", "pkv_latent_pair.cu", "pkv_evict.cu", "pkv_weigh.cu", "pkv_weigh_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]

@@ -132,6 +132,11 @@ struct WeighArgs {
 size_t weigh_workspace_bytes(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens,
                              int32_t max_rows, int64_t num_keys);
 int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8);
+// Its tensor-core kernels, for sequences of more than small_rows rows x heads
+// of a kv head (pkv_weigh_tc.cu).
+size_t weigh_tc_workspace_bytes(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens,
+                                int64_t num_keys);
+int launch_weigh_tc(const LaunchCtx& ctx, const WeighArgs& a, bool fp8, int32_t small_rows, uint8_t* workspace);
 
 // pkv_evict / pkv_evict_fp8 (pkv_evict.cu).
 struct EvictArgs {

@@ -31,10 +31,9 @@
 //    that loses of an element is below 2^-24 in f16's units, 2^-38 of the
 //    largest: less than fp32 sums of 128 terms lose.  The key's scale is
 //    applied to the finished score.
-#include <cmath>
-
+//
+// Sequences of more rows go to the tensor cores (pkv_weigh_tc.cu).
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "pkv_weigh.cuh"
 
@@ -47,7 +46,7 @@ constexpr int kWsWarps = kWsThreads / 32;
 
 // The workspace of a call.
 struct WeighLayout {
-  size_t records, scores, sums, total;
+  size_t records, scores, many, total;
 };
 
 // What the kernels of few rows need beside the call's arguments.
@@ -475,109 +474,6 @@ __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallPa
   griddep_launch_dependents();
 }
 
-constexpr int kWeighThreads = 128;
-
-template <bool F8>
-__device__ __forceinline__ float dot(const WeighArgs& p, const float* q, int64_t row) {
-  float acc = 0.f;
-  if constexpr (F8) {
-    const uint8_t* k = static_cast<const uint8_t*>(p.k_cache) + row * kHeadDim;
-    for (int d = 0; d < kHeadDim; ++d) {
-      __nv_fp8_e4m3 c;
-      c.__x = k[d];
-      acc = fmaf(q[d], float(c), acc);
-    }
-    return acc * __uint_as_float(uint32_t(p.k_scale[row]) << 23);
-  } else {
-    const uint32_t* k = static_cast<const uint32_t*>(p.k_cache) + row * (kHeadDim / 2);
-    for (int d = 0; d < kHeadDim / 2; ++d) {
-      acc = fmaf(q[2 * d], bf_lo(k[d]), acc);
-      acc = fmaf(q[2 * d + 1], bf_hi(k[d]), acc);
-    }
-    return acc;
-  }
-}
-
-__device__ __forceinline__ int64_t key_row(const WeighArgs& p, int b, int g, int k) {
-  int id = __ldg(p.block_tables + int64_t(b) * p.desc.max_blocks_per_seq + k / kPage);
-  if (id < 0 || id >= p.desc.num_blocks) {
-    flag_status(p.status, PKV_STATUS_BAD_BLOCK);
-    return -1;
-  }
-  return (int64_t(id) * p.desc.num_kv_heads + g) * kPage + k % kPage;
-}
-
-// One warp a (query row, head): lanes take keys in turn.
-template <bool F8>
-__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_sums_kernel(const WeighArgs p, float* sums) {
-  griddep_wait();
-  __shared__ float sq[kWeighThreads / 32][kHeadDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Hq = p.desc.num_q_heads, G = Hq / p.desc.num_kv_heads;
-  const int64_t item = int64_t(blockIdx.x) * (kWeighThreads / 32) + warp;
-  if (item >= int64_t(p.num_tokens) * Hq) return;
-  const int t = int(item / Hq), h = int(item % Hq);
-  int lo = 0, hi = p.num_seqs;  // last b with query_start_loc[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (__ldg(p.query_start_loc + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  WeighSequence s;
-  if (!weigh_sequence(p, lo, s) || t >= s.q0 + s.n || s.n * G <= kSmallRows) return;
-  for (int d = lane; d < kHeadDim; d += 32) {
-    const uint16_t x = p.q[item * kHeadDim + d];
-    sq[warp][d] = __uint_as_float(uint32_t(x) << 16);
-  }
-  __syncwarp();
-  const int last = s.L - s.n + (t - s.q0);
-  float m = -INFINITY, l = 0.f;
-  for (int k = lane; k <= last; k += 32) {
-    const int64_t row = key_row(p, lo, h / G, k);
-    const float x = row < 0 ? 0.f : dot<F8>(p, sq[warp], row) * p.qscale;
-    const float mn = fmaxf(m, x);
-    l = l * ex2(m - mn) + ex2(x - mn);
-    m = mn;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const float mo = __shfl_xor_sync(0xffffffffu, m, o), lo_ = __shfl_xor_sync(0xffffffffu, l, o);
-    const float mn = fmaxf(m, mo);
-    l = (m == -INFINITY ? 0.f : l * ex2(m - mn)) + (mo == -INFINITY ? 0.f : lo_ * ex2(mo - mn));
-    m = mn;
-  }
-  if (lane == 0) sums[item] = m + __log2f(l);
-}
-
-// One warp a (sequence, kv head, key): lanes take rows in turn.
-template <bool F8>
-__global__ void __launch_bounds__(kWeighThreads) pkv_weigh_all_kernel(const WeighArgs p, const float* sums) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int Hq = p.desc.num_q_heads, Hkv = p.desc.num_kv_heads, G = Hq / Hkv;
-  const int b = blockIdx.y / Hkv, g = blockIdx.y % Hkv;
-  WeighSequence s;
-  if (!weigh_sequence(p, b, s) || s.n * G <= kSmallRows) return;
-  const float* lse = sums;
-  const int first = p.first ? max(0, __ldg(p.first + b)) : 0;
-  const int scored = p.scored ? __ldg(p.scored + b) : s.L - s.n;
-  for (int k = first + blockIdx.x * (kWeighThreads / 32) + warp; k < s.L; k += gridDim.x * (kWeighThreads / 32)) {
-    const int64_t row = key_row(p, b, g, k);
-    if (row < 0) continue;
-    const int j0 = max(0, k - (s.L - s.n));
-    float w = 0.f;
-    for (int i = j0 * G + lane; i < s.n * G; i += 32) {
-      const int64_t item = int64_t(s.q0 + i / G) * Hq + g * G + i % G;
-      float q[kHeadDim];
-      for (int d = 0; d < kHeadDim; ++d) q[d] = __uint_as_float(uint32_t(p.q[item * kHeadDim + d]) << 16);
-      w += ex2(dot<F8>(p, q, row) * p.qscale - lse[item]);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-    if (lane == 0) p.scores[row] = (k < scored && p.decay != 0.f ? p.decay * p.scores[row] : 0.f) + w;
-  }
-}
-
 // Launched while the kernel before may still run, if that lets it.
 template <class... Params, class... Args>
 int launch(const LaunchCtx& ctx, void (*kernel)(Params...), dim3 grid, int threads, const Args&... args) {
@@ -609,6 +505,11 @@ int stride_log2(int64_t rows) {
 int64_t small_rows(const pkv_desc& d, int32_t max_rows) {
   const int64_t rows = int64_t(max_rows) * (d.num_q_heads / d.num_kv_heads);
   return rows < kSmallRows ? rows : kSmallRows;
+}
+
+// Whether a sequence may have more.
+bool has_many(const pkv_desc& d, int32_t max_rows) {
+  return int64_t(max_rows) * (d.num_q_heads / d.num_kv_heads) > kSmallRows;
 }
 
 using ScoresKernel = void (*)(SmallParams);
@@ -658,7 +559,8 @@ WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
                        size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
   w.records = take(slots * 8 * column_tiles(rows) * sizeof(float2));
   w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * (size_t(1) << stride_log2(rows)) * sizeof(float));
-  w.sums = take(sizeof(float) * size_t(num_tokens) * size_t(d.num_q_heads));
+  w.many = off;
+  if (has_many(d, max_rows)) take(weigh_tc_workspace_bytes(dev, d, num_seqs, num_tokens, num_keys));
   w.total = off;
   return w;
 }
@@ -691,17 +593,8 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
   if (int e = launch(ctx, add_kernel(tiles, 1 << p.stride_log2), dim3(unsigned(add_grid(*ctx.dev, d, a.num_keys))),
                      kWsThreads, p))
     return e;
-  if (int64_t(a.max_rows) * (d.num_q_heads / d.num_kv_heads) <= kSmallRows) return PKV_OK;
-  const int64_t warps = int64_t(a.num_tokens) * d.num_q_heads;
-  const int64_t pairs = int64_t(a.num_seqs) * d.num_kv_heads;
-  if (pairs > 65535) return PKV_ERR_RANGE;
-  constexpr int per = kWeighThreads / 32;
-  float* sums = reinterpret_cast<float*>(ws + w.sums);
-  if (int e = launch(ctx, fp8 ? pkv_weigh_sums_kernel<true> : pkv_weigh_sums_kernel<false>,
-                     dim3(unsigned((warps + per - 1) / per)), kWeighThreads, a, sums))
-    return e;
-  return launch(ctx, fp8 ? pkv_weigh_all_kernel<true> : pkv_weigh_all_kernel<false>, dim3(64, unsigned(pairs)),
-                kWeighThreads, a, sums);
+  if (!has_many(d, a.max_rows)) return PKV_OK;
+  return launch_weigh_tc(ctx, a, fp8, int32_t(rows), ws + w.many);
 }
 
 }  // namespace pkv

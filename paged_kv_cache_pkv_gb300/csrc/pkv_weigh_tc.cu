@@ -1,0 +1,852 @@
+// pkv_weigh_tc.cu -- accumulated attention weights of many rows (query chunks,
+// windows, whole prompts) on the 5th-generation tensor cores.
+//
+// The formulas are pkv_weigh.cu's.  Scores of many rows do not fit anywhere
+// (rows x keys), so both passes compute them, from one kernel:
+//  * sums (pass 1): S = Q K^T, 128 query rows (128 / G tokens x the G heads of a
+//    kv head) as M, 128 keys as N; a thread has a row's scores and keeps its
+//    running maximum and sum.
+//  * weights (pass 2): S^T = K Q^T, 128 keys as M, 128 query rows as N; a thread
+//    has a key's scores and adds exp2(s - lse) over rows in a register: no sum
+//    crosses threads, and none goes through atomics.
+// Of either pass two tiles of the M side stay in shared memory (double-buffered:
+// the next item's pair lands while this one's rows stream past) and tiles of
+// the N side stream through a ring, each used for both: what the tensor cores
+// read from L2 is halved.  S goes to TMEM, two buffers for each M tile (all 512
+// columns), and from there to the registers of the four warps that own the
+// tile's lanes; the buffer is free again as soon as it is read.
+//
+// Work: a unit is a tile of the N side under a pair of the M side; units in the
+// order (sequence, kv head, pair) are cut into equal shares, one a CTA, one CTA
+// an SM.  A pair cut between CTAs leaves records (its item + the CTA: unique, as
+// one of them grows from piece to piece), joined in CTA order by small kernels:
+// pkv_weigh_join_kernel makes the rows' log-sums, pkv_weigh_write_kernel the new
+// scores.  A row tile is left out where causality hides the whole key pair.
+//
+// E4M3 pages: TMA lands a tile's codes and scale bytes in a staging area, four
+// warps widen them to bf16 (exact, scale included).
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "pkv_tcgen05.cuh"
+#include "pkv_weigh.cuh"
+#include "pkv_widen.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTile = 128;            // rows or keys of a tile
+constexpr int kPair = 2 * kTile;      // of the M side's pair
+constexpr int kTilePages = kTile / kPage;
+constexpr uint32_t kHalf = kTile * 128;      // 128 rows of 64 bf16, 128-byte swizzle
+constexpr uint32_t kTileBytes = 2 * kHalf;
+constexpr uint32_t kColumns = 512;
+
+constexpr int kEpilogueThreads = 256;
+constexpr int kPairWarp = 8, kStreamWarp = 9, kMmaWarp = 10;
+constexpr int kWidenWarp = 12, kWidenWarps = 4;
+template <bool F8>
+constexpr int kTcThreads = F8 ? 512 : 384;
+template <bool F8>
+constexpr int kRing = F8 ? 2 : 3;     // tiles of the N side in flight
+
+// Shared memory, from a 1024-byte boundary.
+constexpr uint32_t kStagePage = kPage * kHeadDim;
+constexpr uint32_t kStageTile = kTilePages * (kStagePage + kScaleBytes);  // codes, then scale bytes
+template <bool F8>
+struct Smem {
+  static constexpr uint32_t pair = 0;                                 // [2][2 tiles]
+  static constexpr uint32_t ring = pair + 4 * kTileBytes;
+  static constexpr uint32_t stage = ring + kRing<F8> * kTileBytes;    // [2]: codes of both, then scales of both
+  static constexpr uint32_t lse = stage + (F8 ? 2 * kStageTile : 0);  // [kRing][128] (pass 2)
+  static constexpr uint32_t bars = lse + kRing<F8> * kTile * 4;
+  static constexpr uint32_t total = bars + 256 + 1024;
+  static_assert(total <= 232448, "above the 227 KiB of shared memory a CTA can have");
+};
+
+// An item's pieces and, in pass 2, its place.
+struct Item {
+  int32_t b, g, pair, first, last;  // first and last CTA with a piece of it
+};
+
+struct TcParams {
+  WeighArgs a;
+  int32_t small_rows;          // rows x heads that are the few-rows kernels'
+  int64_t max_items1, max_items2;
+  int64_t* totals;             // [2]: items of pass 1, of pass 2
+  Item *items1, *items2;
+  float2* records1;            // [items1 + CTAs][256]: (maximum, sum) of a row, log2 domain
+  float* lse;                  // [items1][256]: -log2 of the rows' sums
+  float* records2;             // [items2 + CTAs][256]: weight of a key
+};
+
+// ---- counting units ----------------------------------------------------------
+
+// Sum over i < x of floor(i / k).
+__device__ __forceinline__ int64_t floor_sum(int64_t x, int64_t k) {
+  const int64_t q = x / k;
+  return k * (q * (q - 1) / 2) + q * (x - k * q);
+}
+
+// A sequence as a pass sees it.  tile_tokens: query tokens of a row tile.
+template <int PASS>
+struct Shape {
+  int n, L, context, tile_tokens;
+  __device__ __forceinline__ int row_tiles() const { return (n + tile_tokens - 1) / tile_tokens; }
+  __device__ __forceinline__ int row_pairs() const { return (n + 2 * tile_tokens - 1) / (2 * tile_tokens); }
+  __device__ __forceinline__ int items() const { return PASS == 1 ? row_pairs() : (L + kPair - 1) / kPair; }
+  // Pass 2: first row tile that sees a key of the pair.
+  __device__ __forceinline__ int first_row_tile(int pair) const {
+    const int64_t x = int64_t(pair) * kPair - context;
+    return x <= 0 ? 0 : int(x / tile_tokens);
+  }
+  // Tiles of the N side for one pair of the M side.
+  __device__ __forceinline__ int units(int pair) const {
+    if constexpr (PASS == 1)
+      return int((int64_t(context) + min(int64_t(n), (int64_t(pair) + 1) * 2 * tile_tokens) - 1) / kTile) + 1;
+    else
+      return row_tiles() - first_row_tile(pair);
+  }
+  // Units of the pairs before `pair` (pass 1: not the last one's, which may be short).
+  __device__ __forceinline__ int64_t before(int pair) const {
+    if constexpr (PASS == 1) {
+      const int64_t tokens = 2 * tile_tokens, a = int64_t(context) + tokens - 1;
+      int64_t sum;
+      if (tokens >= kTile) {
+        sum = pair * (a / kTile) + tokens / kTile * (int64_t(pair) * (pair - 1) / 2);
+      } else {
+        const int64_t k = kTile / tokens;
+        sum = floor_sum(a / tokens + pair, k) - floor_sum(a / tokens, k);
+      }
+      return sum + pair;
+    } else {
+      // hidden row tiles of pair i: max(0, i d - e)
+      const int64_t d = kPair / tile_tokens, e = (int64_t(context) + tile_tokens - 1) / tile_tokens;
+      const int64_t i0 = e / d + 1;
+      int64_t hidden = 0;
+      if (pair > i0) hidden = d * (int64_t(pair) * (pair - 1) / 2 - i0 * (i0 - 1) / 2) - e * (pair - i0);
+      return int64_t(pair) * row_tiles() - hidden;
+    }
+  }
+  __device__ __forceinline__ int64_t all() const {
+    const int last = items() - 1;
+    return before(last) + units(last);
+  }
+};
+
+// A place in the order of units, and the walk from piece to piece.
+template <int PASS>
+struct Walk {
+  Shape<PASS> s;
+  int b, q0, g, pair, at;  // at: first unit of the piece within the pair
+  int64_t item, item1;     // of this pass; of pass 1 at the sequence's start
+
+  __device__ __forceinline__ bool load(const TcParams& p) {
+    WeighSequence x;
+    const int G = p.a.desc.num_q_heads / p.a.desc.num_kv_heads;
+    if (!weigh_sequence(p.a, b, x) || x.n == 0 || int64_t(x.n) * G <= p.small_rows) return false;
+    s = {x.n, x.L, x.L - x.n, kTile / G};
+    q0 = x.q0;
+    return true;
+  }
+  // Units of this piece when `left` remain in the CTA's share.
+  __device__ __forceinline__ int count(int64_t left) const { return int(min(left, int64_t(s.units(pair) - at))); }
+  __device__ __forceinline__ void next(const TcParams& p, int64_t left) {
+    at = 0;
+    ++item;
+    if (++pair < s.items()) return;
+    pair = 0;
+    if (++g < p.a.desc.num_kv_heads) return;
+    g = 0;
+    item1 += int64_t(s.row_pairs()) * p.a.desc.num_kv_heads;
+    ++b;
+    if (left > 0)
+      while (b < p.a.num_seqs && !load(p)) ++b;
+  }
+};
+
+// This CTA's share [u0, u1) and its first place, the same in every thread.
+// Sequences beyond the workspace are left out and flagged.  `scratch`: 3 x
+// (kMaxSeqs + 1) int64 in shared memory.
+template <int PASS, int kThreads>
+__device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch, Walk<PASS>& w, int64_t& share,
+                                            bool& idle) {
+  const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads;
+  int64_t *units = scratch, *items1 = scratch + kMaxSeqs + 1, *items2 = items1 + kMaxSeqs + 1;
+  __shared__ int64_t warp_sums[kThreads / 32][2];
+  __shared__ unsigned long long limit[1];
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, int(threadIdx.x) * per), b1 = min(B, b0 + per);
+  int64_t items[2] = {0, 0}, total[2];
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    WeighSequence x;
+    bad = !weigh_sequence(p.a, b, x) || bad;
+    Walk<PASS> v;
+    v.b = b;
+    int64_t u = 0, i1 = 0, i2 = 0;
+    if (v.load(p)) {
+      u = v.s.all() * Hkv;
+      i1 = int64_t(v.s.row_pairs()) * Hkv;
+      i2 = int64_t((v.s.L + kPair - 1) / kPair) * Hkv;
+    }
+    units[b] = u;
+    items1[b] = i1;
+    items2[b] = i2;
+    items[0] += i1;
+    items[1] += i2;
+  }
+  if (threadIdx.x == 0) limit[0] = B;
+  block_scan<kThreads>(items, total, warp_sums);
+  int64_t r1 = items[0], r2 = items[1];
+  for (int b = b0; b < b1; ++b) {
+    const int64_t i1 = items1[b], i2 = items2[b];
+    if (i1 > 0 && (r1 + i1 > p.max_items1 || r2 + i2 > p.max_items2)) {
+      atomicMin(limit, static_cast<unsigned long long>(b));
+      bad = true;
+    }
+    items1[b] = r1;
+    items2[b] = r2;
+    r1 += i1;
+    r2 += i2;
+  }
+  if (threadIdx.x == 0) {
+    items1[B] = total[0];
+    items2[B] = total[1];
+  }
+  if (PASS == 1 && bad && blockIdx.x == 0) flag_status(p.a.status, PKV_STATUS_BAD_QUERY);
+  __syncthreads();
+  const int end = int(limit[0]);  // sequences that count
+  int64_t mine[2] = {0, 0};
+  for (int b = b0; b < min(b1, end); ++b) mine[0] += units[b];
+  block_scan<kThreads>(mine, total, warp_sums);
+  int64_t run = mine[0];
+  for (int b = b0; b < b1; ++b) {
+    const int64_t u = b < end ? units[b] : 0;
+    units[b] = run;
+    run += u;
+  }
+  if (threadIdx.x == 0) units[B] = total[0];
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.totals[PASS - 1] = PASS == 1 ? items1[end] : items2[end];
+  __syncthreads();
+  const int64_t U = units[B], ctas = min(int64_t(gridDim.x), U);
+  idle = int64_t(blockIdx.x) >= ctas;
+  if (!idle) {
+    const int64_t u0 = int64_t(blockIdx.x) * U / ctas;
+    share = (int64_t(blockIdx.x) + 1) * U / ctas - u0;
+    int lo = 0, hi = B;  // last sequence with units[b] <= u0: it has units
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (units[mid] <= u0) lo = mid;
+      else hi = mid;
+    }
+    w.b = lo;
+    w.load(p);
+    int64_t rem = u0 - units[lo];
+    const int64_t head = w.s.all();
+    w.g = int(rem / head);
+    rem -= w.g * head;
+    int first = 0, last = w.s.items();  // last pair with before(pair) <= rem
+    while (last - first > 1) {
+      const int mid = (first + last) >> 1;
+      if (w.s.before(mid) <= rem) first = mid;
+      else last = mid;
+    }
+    w.pair = first;
+    w.at = int(rem - w.s.before(first));
+    w.item1 = items1[lo];
+    w.item = (PASS == 1 ? items1[lo] : items2[lo]) + int64_t(w.g) * w.s.items() + first;
+  }
+  __syncthreads();  // scratch is free
+}
+
+// ---- the two passes ------------------------------------------------------------
+
+template <int PASS, bool F8>
+__global__ void __launch_bounds__(kTcThreads<F8>, 1)
+    pkv_weigh_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const TcParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  using S = Smem<F8>;
+  constexpr int kN = kRing<F8>;
+  griddep_wait();
+  Walk<PASS> w;
+  int64_t left = 0;
+  bool idle;
+  plan_shares<PASS, kTcThreads<F8>>(p, reinterpret_cast<int64_t*>(sm), w, left, idle);
+  if (idle) return;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
+  uint64_t* pair_full = bars;             // [2]
+  uint64_t* pair_free = bars + 2;         // [2]
+  uint64_t* ring_full = bars + 4;         // [kN]
+  uint64_t* ring_free = ring_full + kN;   // [kN]
+  uint64_t* s_full = ring_free + kN;      // [2 tiles][2 buffers]
+  uint64_t* s_free = s_full + 4;          // [2][2]
+  uint64_t* stage_full = s_free + 4;      // [2], E4M3
+  uint64_t* stage_free = stage_full + 2;  // [2]
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::bars + 240);
+  static_assert((4 + 2 * 3 + 8 + 4) * 8 <= 240, "barriers and the TMEM address share 256 bytes");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      // K tiles on E4M3 pages are complete by the widening warps' arrivals
+      mbar_init(pair_full + i, F8 && PASS == 2 ? 2 * kWidenWarps : 1);
+      mbar_init(pair_free + i, 1);
+      mbar_init(stage_full + i, 1);
+      mbar_init(stage_free + i, kWidenWarps);
+    }
+    for (int i = 0; i < kN; ++i) {
+      mbar_init(ring_full + i, F8 && PASS == 1 ? kWidenWarps : 1);
+      mbar_init(ring_free + i, PASS == 2 ? 1 + kEpilogueThreads / 32 : 1);  // pass 2: its log-sums are read by all
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                 "r"(kColumns));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_proxy_async_smem();  // the plan's shared memory is written by copies next
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  const WeighArgs& a = p.a;
+  const int Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
+  const int shift = 31 - __clz(G);
+  // Tiles of the M side that the pair has.
+  auto tiles_of = [&](const Walk<PASS>& x) {
+    return PASS == 1 ? (x.s.n - x.pair * 2 * x.s.tile_tokens > x.s.tile_tokens ? 2 : 1)
+                     : (x.s.L - x.pair * kPair > kTile ? 2 : 1);
+  };
+  // Page id of this lane's page (lane < 8) of a key tile, -1 behind the sequence.
+  auto page_id = [&](const Walk<PASS>& x, int tile) {
+    const int page = tile * kTilePages + lane;
+    if (lane >= kTilePages || page >= (x.s.L + kPage - 1) / kPage) return -1;
+    int id = __ldg(a.block_tables + int64_t(x.b) * a.desc.max_blocks_per_seq + page);
+    if (id < 0 || id >= a.desc.num_blocks) {
+      flag_status(a.status, PKV_STATUS_BAD_BLOCK);
+      id = 0;
+    }
+    return id;
+  };
+  // A lane's page of a key tile into the tile's buffer, bytes announced before.
+  auto copy_page = [&](uint8_t* tile, int id, int g, uint64_t* bar) {
+    if (id < 0) return;
+    const int row = (id * Hkv + g) * kPage;
+    tma_load_2d(tile + lane * 2048, &map_k, 0, row, bar);
+    tma_load_2d(tile + kHalf + lane * 2048, &map_k, 64, row, bar);
+  };
+  auto stage_page = [&](int slot, int id, int g) {
+    if (id < 0) return;
+    uint8_t* codes = sm + S::stage + slot * kTilePages * kStagePage;
+    uint8_t* scales = sm + S::stage + 2 * kTilePages * kStagePage + slot * kTilePages * kScaleBytes;
+    const int64_t page = int64_t(id) * Hkv + g;
+    tma_load_2d(codes + lane * kStagePage, &map_k, 0, int(page) * kPage, stage_full + slot);
+    bulk_copy(scales + lane * kScaleBytes, a.k_scale + page * kScaleBytes, kScaleBytes, stage_full + slot);
+  };
+  auto copy_rows = [&](uint8_t* tile, const Walk<PASS>& x, int token, uint64_t* bar) {
+    for (int h = 0; h < 2; ++h) tma_load_3d(tile + h * kHalf, &map_q, h * 64, x.g * G, x.q0 + token, bar);
+  };
+  // All lanes wait; a warp goes on only if all saw the phase.
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+  bool ok = true;
+
+  if (warp == kPairWarp) {
+    // ===== the M side's pairs =====
+    int staged = 0, i = 0;
+    for (; left > 0 && ok; ++i) {
+      const int count = w.count(left), tiles = tiles_of(w), slot = i & 1;
+      uint8_t* dst = sm + S::pair + slot * 2 * kTileBytes;
+      int ids[2];
+      if constexpr (PASS == 2) {
+        ids[0] = page_id(w, 2 * w.pair);
+        ids[1] = tiles > 1 ? page_id(w, 2 * w.pair + 1) : -1;
+      }
+      if constexpr (PASS == 2 && F8) {
+        for (int u = 0; u < tiles && ok; ++u, ++staged) {
+          const int st = staged & 1;
+          if (staged >= 2 && !(ok = wait_all(stage_free + st, ((staged >> 1) - 1) & 1))) break;
+          const int valid = __popc(__ballot_sync(0xffffffffu, ids[u] >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(stage_full + st, uint32_t(valid) * (kStagePage + kScaleBytes));
+          __syncwarp();
+          stage_page(st, ids[u], w.g);
+        }
+      } else {
+        if (i >= 2 && !(ok = wait_all(pair_free + slot, ((i >> 1) - 1) & 1))) break;
+        if constexpr (PASS == 1) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(pair_full + slot, uint32_t(tiles) * kTileBytes);
+            for (int u = 0; u < tiles; ++u)
+              copy_rows(dst + u * kTileBytes, w, (2 * w.pair + u) * w.s.tile_tokens, pair_full + slot);
+          }
+        } else {
+          const int valid = __popc(__ballot_sync(0xffffffffu, ids[0] >= 0)) +
+                            __popc(__ballot_sync(0xffffffffu, ids[1] >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(pair_full + slot, uint32_t(valid) * 4096);
+          __syncwarp();
+          copy_page(dst, ids[0], w.g, pair_full + slot);
+          copy_page(dst + kTileBytes, ids[1], w.g, pair_full + slot);
+        }
+      }
+      left -= count;
+      w.next(p, left);
+    }
+    // copies land before the CTA's shared memory is released
+    if constexpr (PASS == 2 && F8) {
+      for (int k = max(0, staged - 2); k < staged; ++k)
+        ok = mbar_wait(stage_full + (k & 1), (k >> 1) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
+    } else {
+      for (int k = max(0, i - 2); k < i; ++k)
+        ok = mbar_wait(pair_full + (k & 1), (k >> 1) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
+    }
+    if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+  } else if (warp == kStreamWarp) {
+    // ===== the N side's tiles =====
+    int j = 0;
+    while (left > 0 && ok) {
+      const int count = w.count(left);
+      int id = -1;
+      if constexpr (PASS == 1) id = page_id(w, w.at);
+      for (int u = 0; u < count; ++u, ++j) {
+        if constexpr (PASS == 1) {
+          const int now = id;
+          if (u + 1 < count) id = page_id(w, w.at + u + 1);  // read a tile ahead
+          const int valid = __popc(__ballot_sync(0xffffffffu, now >= 0));
+          if constexpr (F8) {
+            const int st = j & 1;
+            if (j >= 2 && !(ok = wait_all(stage_free + st, ((j >> 1) - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(stage_full + st, uint32_t(valid) * (kStagePage + kScaleBytes));
+            __syncwarp();
+            stage_page(st, now, w.g);
+          } else {
+            const int slot = j % kN;
+            if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(ring_full + slot, uint32_t(valid) * 4096);
+            __syncwarp();
+            copy_page(sm + S::ring + slot * kTileBytes, now, w.g, ring_full + slot);
+          }
+        } else {
+          const int slot = j % kN;
+          if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
+          if (lane == 0) {
+            const int tile = w.s.first_row_tile(w.pair) + w.at + u;
+            const int64_t item1 = w.item1 + int64_t(w.g) * w.s.row_pairs() + (tile >> 1);
+            mbar_arrive_expect_tx(ring_full + slot, kTileBytes + kTile * 4);
+            copy_rows(sm + S::ring + slot * kTileBytes, w, tile * w.s.tile_tokens, ring_full + slot);
+            bulk_copy(sm + S::lse + slot * kTile * 4, p.lse + item1 * kPair + (tile & 1) * kTile, kTile * 4,
+                      ring_full + slot);
+          }
+        }
+      }
+      left -= count;
+      w.next(p, left);
+    }
+    if constexpr (PASS == 1 && F8) {
+      for (int k = max(0, j - 2); k < j; ++k)
+        ok = mbar_wait(stage_full + (k & 1), (k >> 1) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
+    } else {
+      for (int k = max(0, j - kN); k < j; ++k)
+        ok = mbar_wait(ring_full + k % kN, (k / kN) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
+    }
+    if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+  } else if (warp == kMmaWarp) {
+    // ===== MMAs: the warp runs the loop, one elected lane issues =====
+    const uint32_t idesc = idesc_bf16(kTile, kTile, false);
+    int i = 0, j = 0, done[2] = {0, 0}, last_tile = 0;
+    for (; left > 0 && ok; ++i) {
+      const int count = w.count(left), tiles = tiles_of(w), slot = i & 1;
+      if (!(ok = wait_all(pair_full + slot, (i >> 1) & 1))) break;
+      for (int u = 0; u < count; ++u, ++j) {
+        const int r = j % kN;
+        if (!(ok = wait_all(ring_full + r, (j / kN) & 1))) break;
+        for (int x = 0; x < tiles; ++x) {
+          const int buf = done[x] & 1;
+          if (done[x] >= 2 && !(ok = wait_all(s_free + 2 * x + buf, ((done[x] >> 1) - 1) & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+            umma(tmem + x * 256 + buf * 128,
+                 smem_desc(smem_u32(sm + S::pair + (slot * 2 + x) * kTileBytes) + off, 16, 1024),
+                 smem_desc(smem_u32(sm + S::ring + r * kTileBytes) + off, 16, 1024), idesc, ks > 0);
+          }
+          umma_commit(s_full + 2 * x + buf);
+          ++done[x];
+          last_tile = x;
+        }
+        if (!ok) break;
+        umma_commit(ring_free + r);
+      }
+      if (!ok) break;
+      umma_commit(pair_free + slot);
+      left -= count;
+      w.next(p, left);
+    }
+    // the newest commits arrive before shared memory and TMEM are released
+    if (ok) {
+      ok = mbar_wait(pair_free + ((i - 1) & 1), ((i - 1) >> 1) & 1, kLandLimitNs) &&
+           mbar_wait(ring_free + (j - 1) % kN, ((j - 1) / kN) & 1, kLandLimitNs);
+    } else if (done[last_tile] > 0) {
+      const int k = done[last_tile] - 1;
+      mbar_wait(s_full + 2 * last_tile + (k & 1), (k >> 1) & 1, kDrainLimitNs);
+    }
+    if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+    __syncwarp();
+  } else if (F8 && warp >= kWidenWarp) {
+    // ===== E4M3 key tiles to bf16, two pages a warp =====
+    if constexpr (F8) {
+      const int mine = warp - kWidenWarp;
+      int staged = 0, i = 0, j = 0;
+      auto widen = [&](uint8_t* tile, const Walk<PASS>& x, int key_tile) {
+        const int st = staged & 1;
+        if (!wait_all(stage_full + st, (staged >> 1) & 1)) return false;
+        const uint8_t* codes = sm + S::stage + st * kTilePages * kStagePage;
+        const uint8_t* scales = sm + S::stage + 2 * kTilePages * kStagePage + st * kTilePages * kScaleBytes;
+        const int pages = (x.s.L + kPage - 1) / kPage;
+        const int r = lane >> 1, h = lane & 1;
+#pragma unroll 1
+        for (int k = mine; k < kTilePages; k += kWidenWarps)
+          if (key_tile * kTilePages + k < pages)
+            widen_row_half(codes + k * kStagePage, scales[k * kScaleBytes + r],
+                           tile + h * kHalf + (k * kPage + r) * 128, r, h);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stage_free + st);
+        ++staged;
+        return true;
+      };
+      while (left > 0 && ok) {
+        const int count = w.count(left);
+        if constexpr (PASS == 1) {
+          for (int u = 0; u < count; ++u, ++j) {
+            const int slot = j % kN;
+            if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
+            if (!(ok = widen(sm + S::ring + slot * kTileBytes, w, w.at + u))) break;
+            if (lane == 0) mbar_arrive(ring_full + slot);
+          }
+        } else {
+          const int slot = i & 1, tiles = tiles_of(w);
+          if (i >= 2 && !(ok = wait_all(pair_free + slot, ((i >> 1) - 1) & 1))) break;
+          for (int u = 0; u < 2; ++u) {
+            if (u < tiles && !(ok = widen(sm + S::pair + (slot * 2 + u) * kTileBytes, w, 2 * w.pair + u))) break;
+            if (lane == 0) mbar_arrive(pair_full + slot);
+          }
+          ++i;
+        }
+        left -= count;
+        w.next(p, left);
+      }
+      if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+    }
+  } else if (warp < kEpilogueThreads / 32) {
+    // ===== scores to sums or weights: warps 0-3 the pair's first tile, 4-7 its second =====
+    const int x = warp >> 2, r = tid & (kTile - 1);
+    const uint32_t lanes = tmem + x * 256 + (uint32_t((warp & 3) * 32) << 16);
+    const uint64_t qs2 = f2(a.qscale, a.qscale);
+    int j = 0, done = 0;
+    while (left > 0 && ok) {
+      const int count = w.count(left);
+      const bool active = x < tiles_of(w);
+      float m = kWeighNoScore, sum = 0.f;
+      // pass 1: the row's last key; pass 2: the thread's key
+      int mark;
+      if constexpr (PASS == 1) {
+        const int token = (2 * w.pair + x) * w.s.tile_tokens + (r >> shift);
+        mark = token < w.s.n ? w.s.context + token : INT32_MAX;
+      } else {
+        mark = w.pair * kPair + x * kTile + r;
+      }
+      for (int u = 0; u < count; ++u, ++j) {
+        const int slot = j % kN;
+        if constexpr (PASS == 2) {
+          if (!(ok = wait_all(ring_full + slot, (j / kN) & 1))) break;  // the tile's log-sums
+        }
+        if (active) {
+          const int buf = done & 1;
+          if (!(ok = wait_all(s_full + 2 * x + buf, (done >> 1) & 1))) break;
+          tc_fence_after();
+          // Columns [from, to) count, for this thread; `full`: all, for the whole warp.
+          int from = 0, to = kTile;
+          if constexpr (PASS == 1) {
+            to = min(int64_t(kTile), int64_t(mark) + 1 - int64_t(w.at + u) * kTile);
+          } else {
+            const int token = (w.s.first_row_tile(w.pair) + w.at + u) * w.s.tile_tokens;
+            from = int(min(int64_t(kTile), max(int64_t(0), (int64_t(mark) - w.s.context - token) * G)));
+            to = int(min(int64_t(kTile), int64_t(w.s.n - token) * G));
+          }
+          const bool full = __all_sync(0xffffffffu, from == 0 && to == kTile);
+          float part = 0.f;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t v[2][32];
+            tmem_ld32(lanes + buf * 128 + half * 64, v[0]);
+            tmem_ld32(lanes + buf * 128 + half * 64 + 32, v[1]);
+            tmem_wait_ld();
+            if (half == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(s_free + 2 * x + buf);
+            }
+            if (!full) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c) {
+                const int column = half * 64 + c;
+                if (column < from || column >= to) v[c >> 5][c & 31] = 0xFF800000u;  // -infinity
+              }
+            }
+            uint64_t acc[2] = {0ull, 0ull};
+            if constexpr (PASS == 1) {
+              float top[2] = {m, m};
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                top[0] = max3(top[0], __uint_as_float(v[0][c]), __uint_as_float(v[0][c + 1]));
+                top[1] = max3(top[1], __uint_as_float(v[1][c]), __uint_as_float(v[1][c + 1]));
+              }
+              const float mn = fmaxf(top[0], top[1]);
+              sum *= ex2((m - mn) * a.qscale);
+              m = mn;
+              const float shift_by = -mn * a.qscale;
+              const uint64_t s2 = f2(shift_by, shift_by);
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) {
+                float e0, e1;
+                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c & 31) + 1])), qs2, s2),
+                         e0, e1);
+                acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
+              }
+            } else {
+              const ulonglong2* lse =
+                  reinterpret_cast<const ulonglong2*>(sm + S::lse + slot * kTile * 4 + half * 64 * 4);
+#pragma unroll
+              for (int c = 0; c < 64; c += 4) {
+                const ulonglong2 n4 = lse[c >> 2];
+                float e0, e1, e2, e3;
+                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c & 31) + 1])), qs2,
+                                n4.x), e0, e1);
+                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][(c & 31) + 2]), __uint_as_float(v[c >> 5][(c & 31) + 3])),
+                                qs2, n4.y), e2, e3);
+                if (!full) {  // (rows behind the sequence have no log-sum)
+                  if (half * 64 + c < from || half * 64 + c >= to) e0 = -INFINITY;
+                  if (half * 64 + c + 1 < from || half * 64 + c + 1 >= to) e1 = -INFINITY;
+                  if (half * 64 + c + 2 < from || half * 64 + c + 2 >= to) e2 = -INFINITY;
+                  if (half * 64 + c + 3 < from || half * 64 + c + 3 >= to) e3 = -INFINITY;
+                }
+                acc[0] = f2_add(acc[0], f2(ex2(e0), ex2(e1)));
+                acc[1] = f2_add(acc[1], f2(ex2(e2), ex2(e3)));
+              }
+            }
+            float s0, s1, s2_, s3;
+            f2_split(acc[0], s0, s1);
+            f2_split(acc[1], s2_, s3);
+            if constexpr (PASS == 1) sum += (s0 + s1) + (s2_ + s3);
+            else part += (s0 + s1) + (s2_ + s3);
+          }
+          if constexpr (PASS == 2) sum += part;
+          ++done;
+        }
+        if constexpr (PASS == 2) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ring_free + slot);
+        }
+      }
+      if (!ok) break;
+      const int64_t at = (w.item + blockIdx.x) * kPair + x * kTile + r;
+      if (active) {
+        if constexpr (PASS == 1) p.records1[at] = make_float2(m * a.qscale, sum);
+        else p.records2[at] = sum;
+      }
+      if (tid == 0) {
+        Item& item = (PASS == 1 ? p.items1 : p.items2)[w.item];
+        if (w.at == 0) {
+          item.b = w.b;
+          item.g = w.g;
+          item.pair = w.pair;
+          item.first = int(blockIdx.x);
+        }
+        if (w.at + count == w.s.units(w.pair)) item.last = int(blockIdx.x);
+      }
+      left -= count;
+      w.next(p, left);
+    }
+    if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kColumns));
+  }
+}
+
+// ---- joining pieces ---------------------------------------------------------------
+
+// A row pair's pieces, in CTA order -> -log2 of its rows' sums.
+__global__ void __launch_bounds__(kPair) pkv_weigh_join_kernel(const TcParams p) {
+  griddep_wait();
+  const int64_t items = p.totals[0];
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const int first = p.items1[i].first, last = p.items1[i].last;
+    float m = kWeighNoScore, l = 0.f;
+    for (int c = first; c <= last; ++c) {
+      const float2 x = __ldcg(p.records1 + (i + c) * kPair + threadIdx.x);
+      const float mn = fmaxf(m, x.x);
+      l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
+      m = mn;
+    }
+    p.lse[i * kPair + threadIdx.x] = -(m + __log2f(l));
+  }
+}
+
+// A key pair's pieces, in CTA order -> its paged scores.
+__global__ void __launch_bounds__(kPair) pkv_weigh_write_kernel(const TcParams p) {
+  griddep_wait();
+  const WeighArgs& a = p.a;
+  const int64_t items = p.totals[1];
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+    const Item item = p.items2[i];
+    WeighSequence s;
+    weigh_sequence(a, item.b, s);
+    const int64_t key = int64_t(item.pair) * kPair + threadIdx.x;
+    const int from = a.first ? __ldg(a.first + item.b) : 0;
+    if (key >= s.L || key < from) continue;
+    const int scored = a.decay == 0.f ? 0 : a.scored ? __ldg(a.scored + item.b) : s.L - s.n;
+    const int id = __ldg(a.block_tables + int64_t(item.b) * a.desc.max_blocks_per_seq + key / kPage);
+    if (id < 0 || id >= a.desc.num_blocks) continue;  // flagged where its keys were read
+    const int64_t at = (int64_t(id) * a.desc.num_kv_heads + item.g) * kPage + key % kPage;
+    float sum = 0.f;
+    for (int c = item.first; c <= item.last; ++c) sum += __ldcg(p.records2 + (i + c) * kPair + threadIdx.x);
+    const float old = key < scored ? __ldcg(a.scores + at) : 0.f;
+    a.scores[at] = fmaf(a.decay, old, sum);
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+}
+
+// ---- host side ------------------------------------------------------------------
+
+int tile_tokens(const pkv_desc& d) { return kTile / (d.num_q_heads / d.num_kv_heads); }
+
+// Every sequence may end in a part of a pair.
+int64_t most_items1(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens) {
+  return (int64_t(num_tokens) / (2 * tile_tokens(d)) + std::min(num_seqs, num_tokens)) * d.num_kv_heads;
+}
+int64_t most_items2(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int64_t num_keys) {
+  return (num_keys / kPair + std::min(num_seqs, num_tokens)) * d.num_kv_heads;
+}
+
+struct TcLayout {
+  size_t totals, items1, items2, records1, lse, records2, total;
+};
+
+TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int64_t num_keys) {
+  const size_t i1 = size_t(most_items1(d, num_seqs, num_tokens));
+  const size_t i2 = size_t(most_items2(d, num_seqs, num_tokens, num_keys));
+  TcLayout w{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, 256);
+    return at;
+  };
+  w.totals = take(2 * sizeof(int64_t));
+  w.items1 = take(i1 * sizeof(Item));
+  w.items2 = take(i2 * sizeof(Item));
+  w.records1 = take((i1 + dev.sm_count) * kPair * sizeof(float2));
+  w.lse = take(i1 * kPair * sizeof(float));
+  w.records2 = take((i2 + dev.sm_count) * kPair * sizeof(float));
+  w.total = off;
+  return w;
+}
+
+template <int PASS, bool F8>
+int ensure_attr(int device) {
+  static bool done[64] = {};
+  if (device < 0 || device >= 64) return PKV_ERR_DEVICE;
+  if (!done[device]) {
+    if (cudaFuncSetAttribute(pkv_weigh_tc_kernel<PASS, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(Smem<F8>::total)) != cudaSuccess) {
+      cudaGetLastError();
+      return PKV_ERR_LAUNCH;
+    }
+    done[device] = true;
+  }
+  return PKV_OK;
+}
+
+template <class... Params, class... Args>
+int launch(const LaunchCtx& ctx, void (*kernel)(Params...), int grid, int threads, size_t smem, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = ctx.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  TraceScope ts(ctx.stream, PKV_K_WEIGH);
+  cudaLaunchKernelEx(&cfg, kernel, args...);
+  return ts.done();
+}
+
+template <bool F8>
+int run(const LaunchCtx& ctx, const CUtensorMap& q, const CUtensorMap& k, const TcParams& p) {
+  if (int e = ensure_attr<1, F8>(ctx.dev->device)) return e;
+  if (int e = ensure_attr<2, F8>(ctx.dev->device)) return e;
+  const int sms = ctx.dev->sm_count;
+  auto blocks = [&](int64_t items) { return int(std::max<int64_t>(1, std::min<int64_t>(items, int64_t(sms) * 8))); };
+  if (int e = launch(ctx, pkv_weigh_tc_kernel<1, F8>, sms, kTcThreads<F8>, Smem<F8>::total, q, k, p)) return e;
+  if (int e = launch(ctx, pkv_weigh_join_kernel, blocks(p.max_items1), kPair, 0, p)) return e;
+  if (int e = launch(ctx, pkv_weigh_tc_kernel<2, F8>, sms, kTcThreads<F8>, Smem<F8>::total, q, k, p)) return e;
+  return launch(ctx, pkv_weigh_write_kernel, blocks(p.max_items2), kPair, 0, p);
+}
+
+}  // namespace
+
+size_t weigh_tc_workspace_bytes(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens,
+                                int64_t num_keys) {
+  return tc_layout(dev, d, num_seqs, num_tokens, num_keys).total;
+}
+
+int launch_weigh_tc(const LaunchCtx& ctx, const WeighArgs& a, bool fp8, int32_t small_rows, uint8_t* workspace) {
+  const pkv_desc& d = a.desc;
+  const TcLayout w = tc_layout(*ctx.dev, d, a.num_seqs, a.num_tokens, a.num_keys);
+  CUtensorMap q, k;
+  {
+    const cuuint64_t dims[3] = {cuuint64_t(kHeadDim), cuuint64_t(d.num_q_heads), cuuint64_t(a.num_tokens)};
+    const cuuint64_t strides[2] = {cuuint64_t(kHeadDim) * 2, cuuint64_t(d.num_q_heads) * kHeadDim * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(d.num_q_heads / d.num_kv_heads), cuuint32_t(tile_tokens(d))};
+    if (!encode_tensor_map(&q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, strides, box)) return PKV_ERR_LAUNCH;
+  }
+  {
+    const cuuint64_t dims[2] = {cuuint64_t(kHeadDim), cuuint64_t(d.num_blocks) * d.num_kv_heads * kPage};
+    const cuuint64_t strides[1] = {cuuint64_t(kHeadDim) * (fp8 ? 1 : 2)};
+    const cuuint32_t box[2] = {cuuint32_t(fp8 ? kHeadDim : kHeadDim / 2), cuuint32_t(kPage)};
+    if (!encode_tensor_map(&k, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k_cache, 2,
+                           dims, strides, box))
+      return PKV_ERR_LAUNCH;
+  }
+  const TcParams p{a,
+                   small_rows,
+                   most_items1(d, a.num_seqs, a.num_tokens),
+                   most_items2(d, a.num_seqs, a.num_tokens, a.num_keys),
+                   reinterpret_cast<int64_t*>(workspace + w.totals),
+                   reinterpret_cast<Item*>(workspace + w.items1),
+                   reinterpret_cast<Item*>(workspace + w.items2),
+                   reinterpret_cast<float2*>(workspace + w.records1),
+                   reinterpret_cast<float*>(workspace + w.lse),
+                   reinterpret_cast<float*>(workspace + w.records2)};
+  return fp8 ? run<true>(ctx, q, k, p) : run<false>(ctx, q, k, p);
+}
+
+}  // namespace pkv
