@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv_tcgen05.cuh"
 #include "pkv_weigh.cuh"
@@ -43,11 +44,15 @@ constexpr uint32_t kHalf = kTile * 128;      // 128 rows of 64 bf16, 128-byte sw
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kColumns = 512;
 
-constexpr int kEpilogueThreads = 256;
-constexpr int kPairWarp = 8, kStreamWarp = 9, kMmaWarp = 10;
-constexpr int kWidenWarp = 12, kWidenWarps = 4;
+// Warps: 16 of the epilogue (four for the lanes of an M tile, twice for its
+// columns' halves), one each for the pairs, the stream and the MMAs, four that
+// widen E4M3 tiles.  (Eight epilogue warps: the passes of a 4095-token prompt
+// took EIGHT_WARPS.)
+constexpr int kEpilogueWarps = 16;
+constexpr int kPairWarp = kEpilogueWarps, kStreamWarp = kPairWarp + 1, kMmaWarp = kPairWarp + 2;
+constexpr int kWidenWarp = kPairWarp + 3, kWidenWarps = 4;
 template <bool F8>
-constexpr int kTcThreads = F8 ? 512 : 384;
+constexpr int kTcThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kWidenWarp);
 template <bool F8>
 constexpr int kRing = F8 ? 2 : 3;     // tiles of the N side in flight
 
@@ -76,9 +81,9 @@ struct TcParams {
   int64_t max_items1, max_items2;
   int64_t* totals;             // [2]: items of pass 1, of pass 2
   Item *items1, *items2;
-  float2* records1;            // [items1 + CTAs][256]: (maximum, sum) of a row, log2 domain
+  float2* records1;            // [items1 + CTAs][2][256]: (maximum, sum) of a row, log2 domain, by column half
   float* lse;                  // [items1][256]: -log2 of the rows' sums
-  float* records2;             // [items2 + CTAs][256]: weight of a key
+  float* records2;             // [items2 + CTAs][2][256]: weight of a key
 };
 
 // ---- counting units ----------------------------------------------------------
@@ -168,14 +173,14 @@ struct Walk {
 
 // This CTA's share [u0, u1) and its first place, the same in every thread.
 // Sequences beyond the workspace are left out and flagged.  `scratch`: 3 x
-// (kMaxSeqs + 1) int64 in shared memory.
+// (kMaxSeqs + 1) + 2 x warps + 1 int64 in shared memory.
 template <int PASS, int kThreads>
 __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch, Walk<PASS>& w, int64_t& share,
                                             bool& idle) {
   const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads;
   int64_t *units = scratch, *items1 = scratch + kMaxSeqs + 1, *items2 = items1 + kMaxSeqs + 1;
-  __shared__ int64_t warp_sums[kThreads / 32][2];
-  __shared__ unsigned long long limit[1];
+  auto* warp_sums = reinterpret_cast<int64_t (*)[2]>(items2 + kMaxSeqs + 1);
+  auto* limit = reinterpret_cast<unsigned long long*>(warp_sums + kThreads / 32);
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, int(threadIdx.x) * per), b1 = min(B, b0 + per);
   int64_t items[2] = {0, 0}, total[2];
@@ -300,11 +305,11 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     }
     for (int i = 0; i < kN; ++i) {
       mbar_init(ring_full + i, F8 && PASS == 1 ? kWidenWarps : 1);
-      mbar_init(ring_free + i, PASS == 2 ? 1 + kEpilogueThreads / 32 : 1);  // pass 2: its log-sums are read by all
+      mbar_init(ring_free + i, PASS == 2 ? 1 + kEpilogueWarps : 1);  // pass 2: its log-sums are read by all
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, 4);
+      mbar_init(s_free + i, kEpilogueWarps / 2);
     }
     fence_mbar_init();
   }
@@ -547,10 +552,11 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
       }
       if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
     }
-  } else if (warp < kEpilogueThreads / 32) {
-    // ===== scores to sums or weights: warps 0-3 the pair's first tile, 4-7 its second =====
-    const int x = warp >> 2, r = tid & (kTile - 1);
-    const uint32_t lanes = tmem + x * 256 + (uint32_t((warp & 3) * 32) << 16);
+  } else if (warp < kEpilogueWarps) {
+    // ===== scores to sums or weights =====
+    const int x = (warp >> 2) & 1, half = warp >> 3;      // M tile, half of its columns
+    const int r = (warp & 3) * 32 + lane;                 // TMEM lane: row or key of the tile
+    const uint32_t columns = tmem + x * 256 + half * 64 + (uint32_t((warp & 3) * 32) << 16);
     const uint64_t qs2 = f2(a.qscale, a.qscale);
     int j = 0, done = 0;
     while (left > 0 && ok) {
@@ -572,85 +578,88 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         }
         if (active) {
           const int buf = done & 1;
-          if (!(ok = wait_all(s_full + 2 * x + buf, (done >> 1) & 1))) break;
-          tc_fence_after();
-          // Columns [from, to) count, for this thread; `full`: all, for the whole warp.
-          int from = 0, to = kTile;
+          // Columns [from, to) of the half count, for this thread; `full`: all, for the whole warp.
+          int from = 0, to;
           if constexpr (PASS == 1) {
-            to = min(int64_t(kTile), int64_t(mark) + 1 - int64_t(w.at + u) * kTile);
+            to = int(min(int64_t(64), int64_t(mark) + 1 - int64_t(w.at + u) * kTile - half * 64));
           } else {
             const int token = (w.s.first_row_tile(w.pair) + w.at + u) * w.s.tile_tokens;
-            from = int(min(int64_t(kTile), max(int64_t(0), (int64_t(mark) - w.s.context - token) * G)));
-            to = int(min(int64_t(kTile), int64_t(w.s.n - token) * G));
+            from = int(min(int64_t(64), max(int64_t(0), (int64_t(mark) - w.s.context - token) * G - half * 64)));
+            to = int(min(int64_t(64), int64_t(w.s.n - token) * G - half * 64));
           }
-          const bool full = __all_sync(0xffffffffu, from == 0 && to == kTile);
-          float part = 0.f;
+          const bool full = __all_sync(0xffffffffu, from == 0 && to == 64);
+          if (!(ok = wait_all(s_full + 2 * x + buf, (done >> 1) & 1))) break;
+          tc_fence_after();
+          uint64_t acc[2] = {0ull, 0ull};
+          // 32 columns; MASKED: some do not count, their weight is 0 whatever
+          // the score or (rows behind the sequence have none) the log-sum is.
+          auto add = [&](uint32_t (&v)[32], int chunk, auto masked_t) {
+            constexpr bool MASKED = decltype(masked_t)::value;
+            auto counts = [&](int c) { return chunk * 32 + c >= from && chunk * 32 + c < to; };
+            if constexpr (PASS == 1) {
+              if constexpr (MASKED) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t v[2][32];
-            tmem_ld32(lanes + buf * 128 + half * 64, v[0]);
-            tmem_ld32(lanes + buf * 128 + half * 64 + 32, v[1]);
+                for (int c = 0; c < 32; ++c)
+                  if (!counts(c)) v[c] = 0xFF800000u;  // -infinity
+              }
+              float top[2] = {m, m};
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                top[0] = max3(top[0], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                top[1] = max3(top[1], __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+              }
+              const float mn = fmaxf(top[0], top[1]);
+              const float alpha = ex2((m - mn) * a.qscale);
+              sum *= alpha;
+              m = mn;
+              float a0, a1;  // the sums so far have the old reference
+              f2_split(acc[0], a0, a1);
+              acc[0] = f2(a0 * alpha, a1 * alpha);
+              f2_split(acc[1], a0, a1);
+              acc[1] = f2(a0 * alpha, a1 * alpha);
+              const uint64_t by = f2(-mn * a.qscale, -mn * a.qscale);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float e0, e1;
+                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, by), e0, e1);
+                acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
+              }
+            } else {
+              const ulonglong2* lse = reinterpret_cast<const ulonglong2*>(
+                  sm + S::lse + (slot * kTile + half * 64 + chunk * 32) * 4);
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const ulonglong2 n4 = lse[c >> 2];
+                float e[4];
+                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, n4.x), e[0], e[1]);
+                f2_split(f2_fma(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), qs2, n4.y), e[2], e[3]);
+                if constexpr (MASKED) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if (!counts(c + k)) e[k] = -INFINITY;
+                }
+                acc[0] = f2_add(acc[0], f2(ex2(e[0]), ex2(e[1])));
+                acc[1] = f2_add(acc[1], f2(ex2(e[2]), ex2(e[3])));
+              }
+            }
+          };
+#pragma unroll
+          for (int chunk = 0; chunk < 2; ++chunk) {
+            uint32_t v[32];
+            tmem_ld32(columns + buf * 128 + chunk * 32, v);
             tmem_wait_ld();
-            if (half == 1) {
+            if (chunk == 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(s_free + 2 * x + buf);
             }
-            if (!full) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c) {
-                const int column = half * 64 + c;
-                if (column < from || column >= to) v[c >> 5][c & 31] = 0xFF800000u;  // -infinity
-              }
-            }
-            uint64_t acc[2] = {0ull, 0ull};
-            if constexpr (PASS == 1) {
-              float top[2] = {m, m};
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                top[0] = max3(top[0], __uint_as_float(v[0][c]), __uint_as_float(v[0][c + 1]));
-                top[1] = max3(top[1], __uint_as_float(v[1][c]), __uint_as_float(v[1][c + 1]));
-              }
-              const float mn = fmaxf(top[0], top[1]);
-              sum *= ex2((m - mn) * a.qscale);
-              m = mn;
-              const float shift_by = -mn * a.qscale;
-              const uint64_t s2 = f2(shift_by, shift_by);
-#pragma unroll
-              for (int c = 0; c < 64; c += 2) {
-                float e0, e1;
-                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c & 31) + 1])), qs2, s2),
-                         e0, e1);
-                acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
-              }
-            } else {
-              const ulonglong2* lse =
-                  reinterpret_cast<const ulonglong2*>(sm + S::lse + slot * kTile * 4 + half * 64 * 4);
-#pragma unroll
-              for (int c = 0; c < 64; c += 4) {
-                const ulonglong2 n4 = lse[c >> 2];
-                float e0, e1, e2, e3;
-                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][c & 31]), __uint_as_float(v[c >> 5][(c & 31) + 1])), qs2,
-                                n4.x), e0, e1);
-                f2_split(f2_fma(f2(__uint_as_float(v[c >> 5][(c & 31) + 2]), __uint_as_float(v[c >> 5][(c & 31) + 3])),
-                                qs2, n4.y), e2, e3);
-                if (!full) {  // (rows behind the sequence have no log-sum)
-                  if (half * 64 + c < from || half * 64 + c >= to) e0 = -INFINITY;
-                  if (half * 64 + c + 1 < from || half * 64 + c + 1 >= to) e1 = -INFINITY;
-                  if (half * 64 + c + 2 < from || half * 64 + c + 2 >= to) e2 = -INFINITY;
-                  if (half * 64 + c + 3 < from || half * 64 + c + 3 >= to) e3 = -INFINITY;
-                }
-                acc[0] = f2_add(acc[0], f2(ex2(e0), ex2(e1)));
-                acc[1] = f2_add(acc[1], f2(ex2(e2), ex2(e3)));
-              }
-            }
-            float s0, s1, s2_, s3;
-            f2_split(acc[0], s0, s1);
-            f2_split(acc[1], s2_, s3);
-            if constexpr (PASS == 1) sum += (s0 + s1) + (s2_ + s3);
-            else part += (s0 + s1) + (s2_ + s3);
+            if (full) add(v, chunk, std::false_type{});
+            else add(v, chunk, std::true_type{});
           }
-          if constexpr (PASS == 2) sum += part;
+          float s0, s1, s2, s3;
+          f2_split(acc[0], s0, s1);
+          f2_split(acc[1], s2, s3);
+          sum += (s0 + s1) + (s2 + s3);
           ++done;
         }
         if constexpr (PASS == 2) {
@@ -659,7 +668,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         }
       }
       if (!ok) break;
-      const int64_t at = (w.item + blockIdx.x) * kPair + x * kTile + r;
+      const int64_t at = ((w.item + blockIdx.x) * 2 + half) * kPair + x * kTile + r;
       if (active) {
         if constexpr (PASS == 1) p.records1[at] = make_float2(m * a.qscale, sum);
         else p.records2[at] = sum;
@@ -696,8 +705,8 @@ __global__ void __launch_bounds__(kPair) pkv_weigh_join_kernel(const TcParams p)
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int first = p.items1[i].first, last = p.items1[i].last;
     float m = kWeighNoScore, l = 0.f;
-    for (int c = first; c <= last; ++c) {
-      const float2 x = __ldcg(p.records1 + (i + c) * kPair + threadIdx.x);
+    for (int c = 2 * first; c < 2 * last + 2; ++c) {
+      const float2 x = __ldcg(p.records1 + (2 * i + c) * kPair + threadIdx.x);
       const float mn = fmaxf(m, x.x);
       l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
       m = mn;
@@ -723,7 +732,8 @@ __global__ void __launch_bounds__(kPair) pkv_weigh_write_kernel(const TcParams p
     if (id < 0 || id >= a.desc.num_blocks) continue;  // flagged where its keys were read
     const int64_t at = (int64_t(id) * a.desc.num_kv_heads + item.g) * kPage + key % kPage;
     float sum = 0.f;
-    for (int c = item.first; c <= item.last; ++c) sum += __ldcg(p.records2 + (i + c) * kPair + threadIdx.x);
+    for (int c = 2 * item.first; c < 2 * item.last + 2; ++c)
+      sum += __ldcg(p.records2 + (2 * i + c) * kPair + threadIdx.x);
     const float old = key < scored ? __ldcg(a.scores + at) : 0.f;
     a.scores[at] = fmaf(a.decay, old, sum);
   }
@@ -760,9 +770,9 @@ TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   w.totals = take(2 * sizeof(int64_t));
   w.items1 = take(i1 * sizeof(Item));
   w.items2 = take(i2 * sizeof(Item));
-  w.records1 = take((i1 + dev.sm_count) * kPair * sizeof(float2));
+  w.records1 = take((i1 + dev.sm_count) * 2 * kPair * sizeof(float2));
   w.lse = take(i1 * kPair * sizeof(float));
-  w.records2 = take((i2 + dev.sm_count) * kPair * sizeof(float));
+  w.records2 = take((i2 + dev.sm_count) * 2 * kPair * sizeof(float));
   w.total = off;
   return w;
 }
