@@ -46,12 +46,13 @@ constexpr int kWsWarps = kWsThreads / 32;
 
 // The workspace of a call.
 struct WeighLayout {
-  size_t records, scores, many, total;
+  size_t units, records, scores, many, total;
 };
 
 // What the kernels of few rows need beside the call's arguments.
 struct SmallParams {
   WeighArgs a;
+  int64_t* units;   // of the batch, for pkv_weigh_add_kernel
   float2* records;  // [items + warps][rows]: (maximum, sum) of a piece
   float* scores;    // [units][16][stride]
   int64_t max_units;
@@ -61,7 +62,8 @@ struct SmallParams {
 };
 
 __device__ __forceinline__ int64_t share_of(const SmallParams& p, int64_t units) {
-  return max(int64_t(1), (units + p.share_warps - 1) / p.share_warps);
+  int64_t rest;
+  return max(int64_t(1), divide(units + p.share_warps - 1, p.share_warps, rest));
 }
 
 // Units before each sequence, in shared memory: [num_seqs + 1].  Sequences of
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
   const int row = lane >> 2, t = lane & 3;
   const int64_t units = before[B], share = share_of(p, units);
   const int64_t warp = int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.units = units;
   int64_t u = min(units, warp * share);
   const int64_t end = min(units, u + share);
   if (u >= end) return;
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     WeighSequence s;
     weigh_sequence(a, b, s);
     const int pages = (s.L + kPage - 1) / kPage;
-    const int64_t rem = u - before[b];
-    const int g = int(rem / pages), first = int(rem % pages);
+    int64_t rest;
+    const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
     const int count = int(min(end - u, int64_t(pages - first)));
     const int rows = s.n * G;  // the group's rows, j * G + h
 
@@ -371,13 +374,16 @@ template <int STRIDE, int ROWS>
 __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallParams p) {
   __shared__ int64_t before[kMaxSeqs + 1];
   __shared__ int64_t warp_sums[kWsWarps][2];
-  plan_units(p, before, warp_sums);  // of arrays that the kernel before only reads
   griddep_wait();
+  if (__ldcg(p.units) == 0) return;  // all sequences have more rows
+  plan_units(p, before, warp_sums);
   const WeighArgs& a = p.a;
   const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
   const int lane = threadIdx.x & 31;
   const int64_t units = before[B], share = share_of(p, units);
-  const int64_t warps = int64_t(gridDim.x) * kWsWarps, mine = (units + warps - 1) / warps;
+  const int64_t warps = int64_t(gridDim.x) * kWsWarps;
+  int64_t spare;
+  const int64_t mine = divide(units + warps - 1, warps, spare);
   int64_t u = min(units, (int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5)) * mine);
   const int64_t end = min(units, u + mine);
   int b = u < end ? sequence_at(before, B, u) : 0;
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallPa
     WeighSequence s;
     weigh_sequence(a, b, s);
     const int pages = (s.L + kPage - 1) / kPage;
-    const int64_t rem = u - before[b];
-    const int g = int(rem / pages), first = int(rem % pages);
+    int64_t rest;
+    const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
     const int count = int(min(end - u, int64_t(pages - first)));
     const int rows = s.n * G;
     const int from = a.first ? max(0, __ldg(a.first + b)) : 0;
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallPa
     // ---- log-sums of the rows: a column a lane, pieces in turn ----
     constexpr int kCols = ROWS < 32 ? ROWS : 32;
     const int64_t u0 = before[b] + int64_t(g) * pages;
-    const int64_t w0 = u0 / share, w1 = (u0 + pages - 1) / share;
+    const int64_t w0 = divide(u0, share, rest), w1 = divide(u0 + pages - 1, share, rest);
     const float2* rec = p.records + (int64_t(b) * Hkv + g) * ROWS + lane % kCols;
     float m = kWeighNoScore, l = 0.f;
     for (int64_t w = w0 + lane / kCols; w <= w1; w += 32 / kCols) {
@@ -557,6 +563,7 @@ WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   const int64_t rows = small_rows(d, max_rows);
   const size_t slots = size_t(num_seqs) * d.num_kv_heads +
                        size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
+  w.units = take(sizeof(int64_t));
   w.records = take(slots * 8 * column_tiles(rows) * sizeof(float2));
   w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * (size_t(1) << stride_log2(rows)) * sizeof(float));
   w.many = off;
@@ -581,6 +588,7 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
   const int tiles = column_tiles(rows);
   const int grid = scores_grid(*ctx.dev, d, a.max_rows, a.num_keys);
   SmallParams p{a,
+                reinterpret_cast<int64_t*>(ws + w.units),
                 reinterpret_cast<float2*>(ws + w.records),
                 reinterpret_cast<float*>(ws + w.scores),
                 a.num_keys / kPage * d.num_kv_heads,

@@ -47,16 +47,28 @@ __device__ __forceinline__ void block_scan(int64_t (&x)[2], int64_t (&total)[2],
     warp_sums[warp][1] = incl[1];
   }
   __syncthreads();
+  static_assert(kThreads <= 1024, "a lane a warp");
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    int64_t before = 0;
-    total[i] = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += warp_sums[w][i];
-      total[i] += warp_sums[w][i];
+    int64_t sums = lane < kThreads / 32 ? warp_sums[lane][i] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sums, o);
+      if (lane >= o) sums += v;
     }
-    x[i] = before + incl[i] - x[i];
+    total[i] = __shfl_sync(0xffffffffu, sums, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);  // of the warps before
+    x[i] = (warp ? before : 0) + incl[i] - x[i];
   }
+}
+
+// Quotient and remainder of counts, which hardly ever need 64 bits.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t& rest) {
+  int64_t q;
+  if (((a | b) >> 31) == 0) q = uint32_t(a) / uint32_t(b);
+  else q = a / b;
+  rest = a - q * b;
+  return q;
 }
 
 }  // namespace pkv

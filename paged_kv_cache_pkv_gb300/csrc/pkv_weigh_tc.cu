@@ -64,8 +64,7 @@ struct Smem {
   static constexpr uint32_t pair = 0;                                 // [2][2 tiles]
   static constexpr uint32_t ring = pair + 4 * kTileBytes;
   static constexpr uint32_t stage = ring + kRing<F8> * kTileBytes;    // [2]: codes of both, then scales of both
-  static constexpr uint32_t lse = stage + (F8 ? 2 * kStageTile : 0);  // [kRing][128] (pass 2)
-  static constexpr uint32_t bars = lse + kRing<F8> * kTile * 4;
+  static constexpr uint32_t bars = stage + (F8 ? 2 * kStageTile : 0);
   static constexpr uint32_t total = bars + 256 + 1024;
   static_assert(total <= 232448, "above the 227 KiB of shared memory a CTA can have");
 };
@@ -88,50 +87,47 @@ struct TcParams {
 
 // ---- counting units ----------------------------------------------------------
 
-// Sum over i < x of floor(i / k).
-__device__ __forceinline__ int64_t floor_sum(int64_t x, int64_t k) {
-  const int64_t q = x / k;
-  return k * (q * (q - 1) / 2) + q * (x - k * q);
+// Sum over i < x of floor(i / 2^k).
+__device__ __forceinline__ int64_t floor_sum(int x, int k) {
+  const int64_t q = x >> k;
+  return ((q * (q - 1) / 2) << k) + q * (x - (q << k));
 }
 
-// A sequence as a pass sees it.  tile_tokens: query tokens of a row tile.
+// A sequence as a pass sees it.  A row tile has 2^log_tokens query tokens (8 to
+// 128); every size here is a power of two, so that there are no divisions.
 template <int PASS>
 struct Shape {
-  int n, L, context, tile_tokens;
-  __device__ __forceinline__ int row_tiles() const { return (n + tile_tokens - 1) / tile_tokens; }
-  __device__ __forceinline__ int row_pairs() const { return (n + 2 * tile_tokens - 1) / (2 * tile_tokens); }
-  __device__ __forceinline__ int items() const { return PASS == 1 ? row_pairs() : (L + kPair - 1) / kPair; }
+  int n, L, context, log_tokens;
+  __device__ __forceinline__ int row_tiles() const { return ((n - 1) >> log_tokens) + 1; }
+  __device__ __forceinline__ int row_pairs() const { return ((n - 1) >> (log_tokens + 1)) + 1; }
+  __device__ __forceinline__ int items() const { return PASS == 1 ? row_pairs() : (L - 1) / kPair + 1; }
   // Pass 2: first row tile that sees a key of the pair.
   __device__ __forceinline__ int first_row_tile(int pair) const {
-    const int64_t x = int64_t(pair) * kPair - context;
-    return x <= 0 ? 0 : int(x / tile_tokens);
+    return max(0, pair * kPair - context) >> log_tokens;
   }
   // Tiles of the N side for one pair of the M side.
   __device__ __forceinline__ int units(int pair) const {
     if constexpr (PASS == 1)
-      return int((int64_t(context) + min(int64_t(n), (int64_t(pair) + 1) * 2 * tile_tokens) - 1) / kTile) + 1;
+      return (context + int(min(int64_t(n), (int64_t(pair) + 1) << (log_tokens + 1))) - 1) / kTile + 1;
     else
       return row_tiles() - first_row_tile(pair);
   }
   // Units of the pairs before `pair` (pass 1: not the last one's, which may be short).
   __device__ __forceinline__ int64_t before(int pair) const {
     if constexpr (PASS == 1) {
-      const int64_t tokens = 2 * tile_tokens, a = int64_t(context) + tokens - 1;
-      int64_t sum;
-      if (tokens >= kTile) {
-        sum = pair * (a / kTile) + tokens / kTile * (int64_t(pair) * (pair - 1) / 2);
-      } else {
-        const int64_t k = kTile / tokens;
-        sum = floor_sum(a / tokens + pair, k) - floor_sum(a / tokens, k);
-      }
+      // floor((a + i 2^t) / 128) + 1 of pair i, with 2^t tokens a pair
+      const int t = log_tokens + 1, a = context + (1 << t) - 1;
+      const int64_t triangle = int64_t(pair) * (pair - 1) / 2;
+      const int64_t sum = t >= 7 ? int64_t(pair) * (a >> 7) + (triangle << (t - 7))
+                                 : floor_sum((a >> t) + pair, 7 - t) - floor_sum(a >> t, 7 - t);
       return sum + pair;
     } else {
-      // hidden row tiles of pair i: max(0, i d - e)
-      const int64_t d = kPair / tile_tokens, e = (int64_t(context) + tile_tokens - 1) / tile_tokens;
-      const int64_t i0 = e / d + 1;
+      // hidden row tiles of pair i: max(0, i 2^d - e)
+      const int d = 8 - log_tokens, e = (context + (1 << log_tokens) - 1) >> log_tokens;
+      const int64_t i0 = (e >> d) + 1, x = pair;
       int64_t hidden = 0;
-      if (pair > i0) hidden = d * (int64_t(pair) * (pair - 1) / 2 - i0 * (i0 - 1) / 2) - e * (pair - i0);
-      return int64_t(pair) * row_tiles() - hidden;
+      if (x > i0) hidden = ((x * (x - 1) / 2 - i0 * (i0 - 1) / 2) << d) - e * (x - i0);
+      return x * row_tiles() - hidden;
     }
   }
   __device__ __forceinline__ int64_t all() const {
@@ -151,7 +147,7 @@ struct Walk {
     WeighSequence x;
     const int G = p.a.desc.num_q_heads / p.a.desc.num_kv_heads;
     if (!weigh_sequence(p.a, b, x) || x.n == 0 || int64_t(x.n) * G <= p.small_rows) return false;
-    s = {x.n, x.L, x.L - x.n, kTile / G};
+    s = {x.n, x.L, x.L - x.n, __ffs(kTile / G) - 1};
     q0 = x.q0;
     return true;
   }
@@ -238,8 +234,9 @@ __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch,
   const int64_t U = units[B], ctas = min(int64_t(gridDim.x), U);
   idle = int64_t(blockIdx.x) >= ctas;
   if (!idle) {
-    const int64_t u0 = int64_t(blockIdx.x) * U / ctas;
-    share = (int64_t(blockIdx.x) + 1) * U / ctas - u0;
+    int64_t rest;
+    const int64_t u0 = divide(int64_t(blockIdx.x) * U, ctas, rest);
+    share = divide((int64_t(blockIdx.x) + 1) * U, ctas, rest) - u0;
     int lo = 0, hi = B;  // last sequence with units[b] <= u0: it has units
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -248,10 +245,8 @@ __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch,
     }
     w.b = lo;
     w.load(p);
-    int64_t rem = u0 - units[lo];
-    const int64_t head = w.s.all();
-    w.g = int(rem / head);
-    rem -= w.g * head;
+    int64_t rem;
+    w.g = int(divide(u0 - units[lo], w.s.all(), rem));
     int first = 0, last = w.s.items();  // last pair with before(pair) <= rem
     while (last - first > 1) {
       const int mid = (first + last) >> 1;
@@ -273,15 +268,24 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     pkv_weigh_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                         const TcParams p) {
   extern __shared__ uint8_t smem_raw[];
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+  }
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using S = Smem<F8>;
   constexpr int kN = kRing<F8>;
-  griddep_wait();
+  // Planned while the kernel before still runs: it is one of this call's, which
+  // has itself waited for what came before the call, and writes none of the
+  // arrays read here; no kernel before reads this pass's total any more.
   Walk<PASS> w;
   int64_t left = 0;
   bool idle;
   plan_shares<PASS, kTcThreads<F8>>(p, reinterpret_cast<int64_t*>(sm), w, left, idle);
-  if (idle) return;
+  if (idle) {
+    griddep_wait();
+    return;
+  }
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::bars);
   uint64_t* pair_full = bars;             // [2]
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     }
     for (int i = 0; i < kN; ++i) {
       mbar_init(ring_full + i, F8 && PASS == 1 ? kWidenWarps : 1);
-      mbar_init(ring_free + i, PASS == 2 ? 1 + kEpilogueWarps : 1);  // pass 2: its log-sums are read by all
+      mbar_init(ring_free + i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
@@ -323,25 +327,31 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
+  griddep_wait();
 
   const WeighArgs& a = p.a;
   const int Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
   const int shift = 31 - __clz(G);
   // Tiles of the M side that the pair has.
   auto tiles_of = [&](const Walk<PASS>& x) {
-    return PASS == 1 ? (x.s.n - x.pair * 2 * x.s.tile_tokens > x.s.tile_tokens ? 2 : 1)
-                     : (x.s.L - x.pair * kPair > kTile ? 2 : 1);
+    return PASS == 1 ? ((x.s.n - 1) >> x.s.log_tokens > 2 * x.pair ? 2 : 1) : ((x.s.L - 1) / kTile > 2 * x.pair ? 2 : 1);
   };
-  // Page id of this lane's page (lane < 8) of a key tile, -1 behind the sequence.
-  auto page_id = [&](const Walk<PASS>& x, int tile) {
+  // The table entry of this lane's page (lane < 8) of a key tile, -1 behind the
+  // sequence; nothing here waits for it.
+  struct Entry {
+    int id;
+    bool live;
+  };
+  auto entry_of = [&](const Walk<PASS>& x, int tile) {
     const int page = tile * kTilePages + lane;
-    if (lane >= kTilePages || page >= (x.s.L + kPage - 1) / kPage) return -1;
-    int id = __ldg(a.block_tables + int64_t(x.b) * a.desc.max_blocks_per_seq + page);
-    if (id < 0 || id >= a.desc.num_blocks) {
-      flag_status(a.status, PKV_STATUS_BAD_BLOCK);
-      id = 0;
-    }
-    return id;
+    const bool live = lane < kTilePages && page < (x.s.L + kPage - 1) / kPage;
+    return Entry{live ? __ldg(a.block_tables + int64_t(x.b) * a.desc.max_blocks_per_seq + page) : -1, live};
+  };
+  // Its page id; one outside the pool is flagged and page 0 read in its place.
+  auto page_id = [&](const Entry& e) {
+    if (!e.live || (e.id >= 0 && e.id < a.desc.num_blocks)) return e.id;
+    flag_status(a.status, PKV_STATUS_BAD_BLOCK);
+    return 0;
   };
   // A lane's page of a key tile into the tile's buffer, bytes announced before.
   auto copy_page = [&](uint8_t* tile, int id, int g, uint64_t* bar) {
@@ -373,8 +383,9 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
       uint8_t* dst = sm + S::pair + slot * 2 * kTileBytes;
       int ids[2];
       if constexpr (PASS == 2) {
-        ids[0] = page_id(w, 2 * w.pair);
-        ids[1] = tiles > 1 ? page_id(w, 2 * w.pair + 1) : -1;
+        const Entry e0 = entry_of(w, 2 * w.pair), e1 = entry_of(w, 2 * w.pair + 1);
+        ids[0] = page_id(e0);
+        ids[1] = page_id(e1);
       }
       if constexpr (PASS == 2 && F8) {
         for (int u = 0; u < tiles && ok; ++u, ++staged) {
@@ -391,7 +402,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(pair_full + slot, uint32_t(tiles) * kTileBytes);
             for (int u = 0; u < tiles; ++u)
-              copy_rows(dst + u * kTileBytes, w, (2 * w.pair + u) * w.s.tile_tokens, pair_full + slot);
+              copy_rows(dst + u * kTileBytes, w, (2 * w.pair + u) << w.s.log_tokens, pair_full + slot);
           }
         } else {
           const int valid = __popc(__ballot_sync(0xffffffffu, ids[0] >= 0)) +
@@ -419,12 +430,12 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     int j = 0;
     while (left > 0 && ok) {
       const int count = w.count(left);
-      int id = -1;
-      if constexpr (PASS == 1) id = page_id(w, w.at);
+      Entry next{-1, false};
+      if constexpr (PASS == 1) next = entry_of(w, w.at);
       for (int u = 0; u < count; ++u, ++j) {
         if constexpr (PASS == 1) {
-          const int now = id;
-          if (u + 1 < count) id = page_id(w, w.at + u + 1);  // read a tile ahead
+          const int now = page_id(next);
+          if (u + 1 < count) next = entry_of(w, w.at + u + 1);  // read a tile ahead
           const int valid = __popc(__ballot_sync(0xffffffffu, now >= 0));
           if constexpr (F8) {
             const int st = j & 1;
@@ -444,11 +455,8 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
           if (lane == 0) {
             const int tile = w.s.first_row_tile(w.pair) + w.at + u;
-            const int64_t item1 = w.item1 + int64_t(w.g) * w.s.row_pairs() + (tile >> 1);
-            mbar_arrive_expect_tx(ring_full + slot, kTileBytes + kTile * 4);
-            copy_rows(sm + S::ring + slot * kTileBytes, w, tile * w.s.tile_tokens, ring_full + slot);
-            bulk_copy(sm + S::lse + slot * kTile * 4, p.lse + item1 * kPair + (tile & 1) * kTile, kTile * 4,
-                      ring_full + slot);
+            mbar_arrive_expect_tx(ring_full + slot, kTileBytes);
+            copy_rows(sm + S::ring + slot * kTileBytes, w, tile << w.s.log_tokens, ring_full + slot);
           }
         }
       }
@@ -558,36 +566,47 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     const int r = (warp & 3) * 32 + lane;                 // TMEM lane: row or key of the tile
     const uint32_t columns = tmem + x * 256 + half * 64 + (uint32_t((warp & 3) * 32) << 16);
     const uint64_t qs2 = f2(a.qscale, a.qscale);
-    int j = 0, done = 0;
+    int done = 0;
     while (left > 0 && ok) {
       const int count = w.count(left);
       const bool active = x < tiles_of(w);
+      // pass 2: log-sums of the row tiles; read through L1, where the tile's
+      // are asked for while the one before it is added up
+      const float* lse = PASS == 1 ? nullptr
+                                   : p.lse + (w.item1 + int64_t(w.g) * w.s.row_pairs()) * kPair +
+                                         int64_t(w.s.first_row_tile(w.pair) + w.at) * kTile + half * 64;
       float m = kWeighNoScore, sum = 0.f;
-      // pass 1: the row's last key; pass 2: the thread's key
-      int mark;
+      // Pass 1: keys up to the row's last one, from the piece's first tile and
+      // this half on.  Pass 2: the token, from the piece's first row tile on,
+      // whose rows are the first to see the thread's key, and the first behind
+      // the sequence.
+      int seen, end = 0;
       if constexpr (PASS == 1) {
-        const int token = (2 * w.pair + x) * w.s.tile_tokens + (r >> shift);
-        mark = token < w.s.n ? w.s.context + token : INT32_MAX;
+        const int token = ((2 * w.pair + x) << w.s.log_tokens) + (r >> shift);
+        seen = (token < w.s.n ? w.s.context + token + 1 : INT32_MAX) - w.at * kTile - half * 64;
       } else {
-        mark = w.pair * kPair + x * kTile + r;
+        const int token = (w.s.first_row_tile(w.pair) + w.at) << w.s.log_tokens;
+        seen = w.pair * kPair + x * kTile + r - w.s.context - token;
+        end = w.s.n - token;
       }
-      for (int u = 0; u < count; ++u, ++j) {
-        const int slot = j % kN;
-        if constexpr (PASS == 2) {
-          if (!(ok = wait_all(ring_full + slot, (j / kN) & 1))) break;  // the tile's log-sums
-        }
+      for (int u = 0; u < count; ++u) {
         if (active) {
           const int buf = done & 1;
           // Columns [from, to) of the half count, for this thread; `full`: all, for the whole warp.
           int from = 0, to;
           if constexpr (PASS == 1) {
-            to = int(min(int64_t(64), int64_t(mark) + 1 - int64_t(w.at + u) * kTile - half * 64));
+            to = min(64, seen);
+            seen -= kTile;
           } else {
-            const int token = (w.s.first_row_tile(w.pair) + w.at + u) * w.s.tile_tokens;
-            from = int(min(int64_t(64), max(int64_t(0), (int64_t(mark) - w.s.context - token) * G - half * 64)));
-            to = int(min(int64_t(64), int64_t(w.s.n - token) * G - half * 64));
+            from = max(0, (min(kTile, max(0, seen)) << shift) - half * 64);
+            to = min(64, (min(kTile, end) << shift) - half * 64);
+            seen -= 1 << w.s.log_tokens;
+            end -= 1 << w.s.log_tokens;
           }
-          const bool full = __all_sync(0xffffffffu, from == 0 && to == 64);
+          const bool full = __all_sync(0xffffffffu, from == 0 && to >= 64);
+          const float2 ahead = PASS == 2 && u + 1 < count
+                                   ? reinterpret_cast<const float2*>(lse + kTile)[lane]
+                                   : make_float2(0.f, 0.f);
           if (!(ok = wait_all(s_full + 2 * x + buf, (done >> 1) & 1))) break;
           tc_fence_after();
           uint64_t acc[2] = {0ull, 0ull};
@@ -625,11 +644,10 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
                 acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
               }
             } else {
-              const ulonglong2* lse = reinterpret_cast<const ulonglong2*>(
-                  sm + S::lse + (slot * kTile + half * 64 + chunk * 32) * 4);
+              const ulonglong2* n = reinterpret_cast<const ulonglong2*>(lse + chunk * 32);
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
-                const ulonglong2 n4 = lse[c >> 2];
+                const ulonglong2 n4 = n[c >> 2];
                 float e[4];
                 f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, n4.x), e[0], e[1]);
                 f2_split(f2_fma(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), qs2, n4.y), e[2], e[3]);
@@ -660,11 +678,9 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           f2_split(acc[0], s0, s1);
           f2_split(acc[1], s2, s3);
           sum += (s0 + s1) + (s2 + s3);
+          asm volatile("" ::"f"(ahead.x), "f"(ahead.y));
+          if constexpr (PASS == 2) lse += kTile;
           ++done;
-        }
-        if constexpr (PASS == 2) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(ring_free + slot);
         }
       }
       if (!ok) break;
@@ -700,6 +716,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
 
 // A row pair's pieces, in CTA order -> -log2 of its rows' sums.
 __global__ void __launch_bounds__(kPair) pkv_weigh_join_kernel(const TcParams p) {
+  griddep_launch_dependents();  // pass 2 of the same call, which waits before it reads or writes pools
   griddep_wait();
   const int64_t items = p.totals[0];
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
