@@ -20,7 +20,13 @@
 //     behind the first tokens.  A kept token never moves up (src >= dst, as
 //     the list is in order), so what a round writes can only be what the same
 //     or an earlier round reads: a round's rows are all in registers, cluster
-//     wide, before any of them is written, and nothing else has to wait.
+//     wide, before any of them is written, and nothing else has to wait.  Once
+//     a round's first row comes from behind all that it writes, only earlier
+//     rounds read there, and the barrier of the round before is enough.
+//
+// Items that fill the GPU get 256 threads each, four CTAs an SM; fewer items a
+// cluster of CTAs of 1024 threads, one an SM (one sequence of 131072 tokens,
+// eight heads: 16 CTAs of 256 threads and a barrier a round took 258 us).
 //
 // What bounds it: bytes, a row read and written once (2 x 512 bytes a token
 // and head on bf16 pages); on few tokens the chain of steps 1 to 3.
@@ -34,16 +40,16 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEvThreads = 256;
-constexpr int kEvWarps = kEvThreads / 32;
-constexpr int kKeys = 8192;   // keys of a slice held in shared memory
+constexpr int kSmallThreads = 256, kBigThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 16;
 
+template <int kThreads>
 struct EvictShared {
+  static constexpr int kKeys = kThreads == kBigThreads ? 24576 : 8192;  // of a slice, held here
   uint32_t hist[2][kBins];
   uint32_t keys[kKeys];
-  uint32_t warp_sum[kEvWarps], warp_eq[kEvWarps];
+  uint32_t warp_sum[kThreads / 32], warp_eq[kThreads / 32];
   uint32_t digit, rest;         // of the last selection pass
   uint32_t count_gt, count_eq;  // of this CTA's slice
 };
@@ -55,10 +61,20 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-template <bool F8>
-__global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArgs p, int cluster, int list_stride) {
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool F8, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
+    pkv_evict_kernel(const EvictArgs p, int cluster, int list_stride) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  EvictShared& sh = *reinterpret_cast<EvictShared*>(smem_raw);
+  using Shared = EvictShared<kThreads>;
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
+  constexpr int kWarps = kThreads / 32, kKeys = Shared::kKeys;
   const cg::cluster_group cl = cg::this_cluster();
   auto sync_all = [&] {
     if (cluster > 1) cl.sync();
@@ -111,7 +127,7 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
       return order_key(__ldcg(p.scores + row_of(page, token)));
     };
     auto key_at = [&](int i) { return i < kKeys ? sh.keys[i] : read_key(i); };
-    for (int i = tid; i < min(n, kKeys); i += kEvThreads) sh.keys[i] = read_key(i);
+    for (int i = tid; i < min(n, kKeys); i += kThreads) sh.keys[i] = read_key(i);
 
     // ---- the c-th largest key, digit by digit ----
     uint32_t prefix = 0, rest = uint32_t(c);
@@ -122,25 +138,29 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       uint32_t* hist = sh.hist[pass & 1];
       // (its readers of two passes ago have been through the barrier of the last)
-      for (int i = tid; i < kBins; i += kEvThreads) hist[i] = 0;
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < n; i += kEvThreads) {
+      for (int i = tid; i < n; i += kThreads) {
         const uint32_t key = key_at(i);
         if (above == 32 || key >> above == prefix >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
       }
       sync_all();
-      // Bins from the top: thread t has bins 2047 - 8t .. 2040 - 8t, summed over the cluster.
-      uint32_t bin[8] = {};
+      // Bins from the top, kPer a thread, summed over the cluster.
+      constexpr int kPer = kBins / kThreads;
+      const int low = kBins - kPer * (tid + 1);
+      uint32_t bin[kPer] = {};  // of bins low + kPer - 1 down to low
       for (int k = 0; k < cluster; ++k) {
-        const uint32_t* h = cluster > 1 ? cl.map_shared_rank(hist, k) : hist;
-        const uint4 hi = *reinterpret_cast<const uint4*>(h + kBins - 8 - 8 * tid + 4);
-        const uint4 lo = *reinterpret_cast<const uint4*>(h + kBins - 8 - 8 * tid);
-        bin[0] += hi.w, bin[1] += hi.z, bin[2] += hi.y, bin[3] += hi.x;
-        bin[4] += lo.w, bin[5] += lo.z, bin[6] += lo.y, bin[7] += lo.x;
+        const uint32_t* h = (cluster > 1 ? cl.map_shared_rank(hist, k) : hist) + low;
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(h + i);
+          bin[kPer - 1 - i] += v.x;
+          bin[kPer - 2 - i] += v.y;
+        }
       }
       uint32_t mine = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine += bin[i];
+      for (int i = 0; i < kPer; ++i) mine += bin[i];
       uint32_t incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -153,9 +173,9 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
       for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
       if (before < rest && rest <= before + mine) {  // one thread: the digit is in its bins
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kPer; ++i) {
           if (before < rest && rest <= before + bin[i]) {
-            sh.digit = uint32_t(kBins - 1 - 8 * tid - i);
+            sh.digit = uint32_t(low + kPer - 1 - i);
             sh.rest = rest - before;
           }
           before += bin[i];
@@ -170,7 +190,7 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
     // ---- how many stay of the slices before ----
     // Warps take whole words of 32 candidates in order, a contiguous run each.
     const int words = (n + 31) / 32;
-    const int w_per = (words + kEvWarps - 1) / kEvWarps;
+    const int w_per = (words + kWarps - 1) / kWarps;
     const int w0 = min(words, warp * w_per), w1 = min(words, w0 + w_per);
     uint32_t gt = 0, eq = 0;
     for (int w = w0; w < w1; ++w) {
@@ -186,7 +206,7 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
     __syncthreads();
     if (tid == 0) {
       uint32_t a = 0, e = 0;
-      for (int w = 0; w < kEvWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         a += sh.warp_sum[w];
         e += sh.warp_eq[w];
       }
@@ -228,7 +248,7 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
   constexpr int kSub = 32 / kLanes;             // rows that a warp moves at a time
   constexpr int kDeep = 8;                      // times, all in flight
   constexpr int kWarpRows = kSub * kDeep;       // 8 or 16
-  constexpr int kRows = kWarpRows * kEvWarps;   // rows of a CTA's round
+  constexpr int kRows = kWarpRows * kWarps;   // rows of a CTA's round
   const int total = c + r;
   const int sub = lane / kLanes, in_row = lane % kLanes;
   uint4* const pool = reinterpret_cast<uint4*>(in_row < kVecs ? p.k_cache : p.v_cache);
@@ -270,7 +290,20 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
     }
     int64_t next_src, next_dst;
     places(base + round_rows + mine, next_src, next_dst);
-    sync_all();  // every row of the round is in registers
+    // Every row that these writes may hit has been read (release and acquire
+    // order reads too).
+    if (cluster == 1) {
+      __syncthreads();
+    } else {
+      const int lowest = base < c ? __ldcg(list + base) : L - r + int(base - c);  // of the round's sources
+      const bool ahead = lowest >= f + base + round_rows;
+      if (base > 0) cluster_wait();  // rounds before
+      cluster_arrive();
+      if (!ahead) {
+        cluster_wait();
+        cluster_arrive();  // (so that one is always under way)
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
       const int64_t d = __shfl_sync(0xffffffffu, dst, i * kSub + sub);
@@ -286,35 +319,72 @@ __global__ void __launch_bounds__(kEvThreads, 4) pkv_evict_kernel(const EvictArg
     src = next_src;
     dst = next_dst;
   }
-}
-
-// CTAs an item: as many as fill the GPU twice, none with less than 256 tokens
-// of the widest sequence.
-int cluster_size(const DeviceInfo& dev, const pkv_desc& d, int64_t items) {
-  int n = 1;
-  while (n < kMaxCluster && items * n * 2 <= 2 * dev.sm_count &&
-         int64_t(d.max_blocks_per_seq) * kPage >= int64_t(n) * 2 * 256)
-    n *= 2;
-  return n;
+  if (cluster > 1 && total > 0) cluster_wait();
 }
 
 int list_stride(const pkv_desc& d) { return d.max_blocks_per_seq * kPage; }
 
+using Kernel = void (*)(EvictArgs, int, int);
+
+cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], cudaStream_t stream, int64_t items, int cluster, bool big) {
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(items * cluster));
+  cfg.blockDim = dim3(unsigned(big ? kBigThreads : kSmallThreads));
+  cfg.dynamicSmemBytes = big ? sizeof(EvictShared<kBigThreads>) : sizeof(EvictShared<kSmallThreads>);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// How many clusters of 1, 2, 4, 8 and 16 CTAs of 1024 threads run at once on a
+// device, asked once (a cluster stays within a GPC).
 template <bool F8>
-int ensure_attr(int device) {
+const int* resident_clusters(int device) {
+  static int most[64][5];
   static bool done[64] = {};
-  if (device < 0 || device >= 64) return PKV_ERR_DEVICE;
+  if (device < 0 || device >= 64) return nullptr;
   if (!done[device]) {
-    if (cudaFuncSetAttribute(pkv_evict_kernel<F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(sizeof(EvictShared))) != cudaSuccess ||
-        cudaFuncSetAttribute(pkv_evict_kernel<F8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-            cudaSuccess) {
+    const Kernel big = pkv_evict_kernel<F8, kBigThreads>, small = pkv_evict_kernel<F8, kSmallThreads>;
+    if (cudaFuncSetAttribute(big, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(sizeof(EvictShared<kBigThreads>))) != cudaSuccess ||
+        cudaFuncSetAttribute(small, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(sizeof(EvictShared<kSmallThreads>))) != cudaSuccess ||
+        cudaFuncSetAttribute(big, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
       cudaGetLastError();
-      return PKV_ERR_LAUNCH;
+      return nullptr;
+    }
+    for (int i = 0; i < 5; ++i) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = config(attr, nullptr, 1, 1 << i, true);
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, big, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;  // a size that this device cannot run
+      }
+      most[device][i] = n;
     }
     done[device] = true;
   }
-  return PKV_OK;
+  return most[device];
+}
+
+// CTAs of 1024 threads an item: as many as let all items run at once, none for
+// less than 512 tokens of the widest sequence.  0: items or tables too small for
+// them, a CTA of 256 threads each.
+int cluster_size(const int* most, const pkv_desc& d, int64_t items) {
+  const int64_t tokens = int64_t(d.max_blocks_per_seq) * kPage;
+  if (items > most[0] || tokens < 4 * 512) return 0;
+  int n = 1;
+  for (int i = 1; i < 5; ++i)
+    if (items <= most[i] && tokens >= int64_t(512) << i) n = 1 << i;
+  return n;
 }
 
 }  // namespace
@@ -325,25 +395,17 @@ size_t evict_workspace_bytes(const pkv_desc& d, int32_t num_seqs) {
 
 int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
   if (a.workspace_bytes < evict_workspace_bytes(a.desc, a.num_seqs)) return PKV_ERR_WORKSPACE;
-  if (int e = fp8 ? ensure_attr<true>(ctx.dev->device) : ensure_attr<false>(ctx.dev->device)) return e;
+  const int* most = fp8 ? resident_clusters<true>(ctx.dev->device) : resident_clusters<false>(ctx.dev->device);
+  if (!most) return PKV_ERR_LAUNCH;
   const int64_t items = int64_t(a.num_seqs) * a.desc.num_kv_heads;
-  const int cluster = cluster_size(*ctx.dev, a.desc, items);
-  if (items * cluster > INT32_MAX) return PKV_ERR_RANGE;
+  if (items * kMaxCluster > INT32_MAX) return PKV_ERR_RANGE;
+  const int n = cluster_size(most, a.desc, items), cluster = n ? n : 1;
+  const Kernel kernel = n ? (fp8 ? pkv_evict_kernel<true, kBigThreads> : pkv_evict_kernel<false, kBigThreads>)
+                          : (fp8 ? pkv_evict_kernel<true, kSmallThreads> : pkv_evict_kernel<false, kSmallThreads>);
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(items * cluster));
-  cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = sizeof(EvictShared);
-  cfg.stream = ctx.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  const cudaLaunchConfig_t cfg = config(attr, ctx.stream, items, cluster, n != 0);
   TraceScope ts(ctx.stream, PKV_K_EVICT);
-  cudaLaunchKernelEx(&cfg, fp8 ? pkv_evict_kernel<true> : pkv_evict_kernel<false>, a, cluster, list_stride(a.desc));
+  cudaLaunchKernelEx(&cfg, kernel, a, cluster, list_stride(a.desc));
   return ts.done();
 }
 

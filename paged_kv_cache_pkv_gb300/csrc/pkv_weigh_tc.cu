@@ -44,17 +44,20 @@ constexpr uint32_t kHalf = kTile * 128;      // 128 rows of 64 bf16, 128-byte sw
 constexpr uint32_t kTileBytes = 2 * kHalf;
 constexpr uint32_t kColumns = 512;
 
-// Warps: 16 of the epilogue (four for the lanes of an M tile, twice for its
-// columns' halves), one each for the pairs, the stream and the MMAs, four that
-// widen E4M3 tiles.  (Eight epilogue warps: the passes of a 4095-token prompt
-// took EIGHT_WARPS.)
+// Warps: 16 of the epilogue (four for the lanes of the M tiles, four times for
+// quarters of their columns; a warp takes first one tile's 32 columns, then the
+// other's, so that in pass 2 both use the log-sums that it has read), one each
+// for the pairs, the stream, the MMAs and the log-sums, four that widen E4M3
+// tiles.
 constexpr int kEpilogueWarps = 16;
 constexpr int kPairWarp = kEpilogueWarps, kStreamWarp = kPairWarp + 1, kMmaWarp = kPairWarp + 2;
-constexpr int kWidenWarp = kPairWarp + 3, kWidenWarps = 4;
+constexpr int kLseWarp = kPairWarp + 3;  // pass 2: log-sums of the row tiles
+constexpr int kWidenWarp = kPairWarp + 4, kWidenWarps = 4;
 template <bool F8>
 constexpr int kTcThreads = 32 * (F8 ? kWidenWarp + kWidenWarps : kWidenWarp);
 template <bool F8>
 constexpr int kRing = F8 ? 2 : 3;     // tiles of the N side in flight
+constexpr int kLseRing = 3;
 
 // Shared memory, from a 1024-byte boundary.
 constexpr uint32_t kStagePage = kPage * kHeadDim;
@@ -64,7 +67,8 @@ struct Smem {
   static constexpr uint32_t pair = 0;                                 // [2][2 tiles]
   static constexpr uint32_t ring = pair + 4 * kTileBytes;
   static constexpr uint32_t stage = ring + kRing<F8> * kTileBytes;    // [2]: codes of both, then scales of both
-  static constexpr uint32_t bars = stage + (F8 ? 2 * kStageTile : 0);
+  static constexpr uint32_t lse = stage + (F8 ? 2 * kStageTile : 0);  // [kLseRing][128], pass 2
+  static constexpr uint32_t bars = lse + kLseRing * kTile * 4;
   static constexpr uint32_t total = bars + 256 + 1024;
   static_assert(total <= 232448, "above the 227 KiB of shared memory a CTA can have");
 };
@@ -80,9 +84,9 @@ struct TcParams {
   int64_t max_items1, max_items2;
   int64_t* totals;             // [2]: items of pass 1, of pass 2
   Item *items1, *items2;
-  float2* records1;            // [items1 + CTAs][2][256]: (maximum, sum) of a row, log2 domain, by column half
+  float2* records1;            // [items1 + CTAs][4][256]: (maximum, sum) of a row, log2 domain, by column quarter
   float* lse;                  // [items1][256]: -log2 of the rows' sums
-  float* records2;             // [items2 + CTAs][2][256]: weight of a key
+  float* records2;             // [items2 + CTAs][4][256]: weight of a key
 };
 
 // ---- counting units ----------------------------------------------------------
@@ -261,6 +265,37 @@ __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch,
   __syncthreads();  // scratch is free
 }
 
+// S of one tile pair: all 128 dims, eight MMAs (operands K-major: 32 bytes apart
+// in a half's rows, then the other half), and the commit to `bar`.  One block,
+// so that a lane is elected once and descriptors are a constant apart: issued
+// one by one, with descriptors made anew, they took the warp longer than the
+// tensor cores.
+__device__ __forceinline__ void umma_tile(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint64_t* bar) {
+  static_assert(kHalf / 16 == 1024, "the block below steps by it");
+  asm volatile(
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b32 l;\n\t.reg .b64 x, y;\n\t"
+      "elect.sync l|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 1024;\n\tadd.s64 y, %2, 1024;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 1026;\n\tadd.s64 y, %2, 1026;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 1028;\n\tadd.s64 y, %2, 1028;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 1030;\n\tadd.s64 y, %2, 1030;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // ---- the two passes ------------------------------------------------------------
 
 template <int PASS, bool F8>
@@ -296,8 +331,10 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
   uint64_t* s_free = s_full + 4;          // [2][2]
   uint64_t* stage_full = s_free + 4;      // [2], E4M3
   uint64_t* stage_free = stage_full + 2;  // [2]
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::bars + 240);
-  static_assert((4 + 2 * 3 + 8 + 4) * 8 <= 240, "barriers and the TMEM address share 256 bytes");
+  uint64_t* lse_full = stage_free + 2;    // [kLseRing], pass 2
+  uint64_t* lse_free = lse_full + kLseRing;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + S::bars + 248);
+  static_assert((4 + 2 * 3 + 8 + 4 + 2 * kLseRing) * 8 <= 248, "barriers and the TMEM address share 256 bytes");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -311,9 +348,13 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
       mbar_init(ring_full + i, F8 && PASS == 1 ? kWidenWarps : 1);
       mbar_init(ring_free + i, 1);
     }
+    for (int i = 0; i < kLseRing; ++i) {
+      mbar_init(lse_full + i, 1);
+      mbar_init(lse_free + i, kEpilogueWarps);
+    }
     for (int i = 0; i < 4; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, kEpilogueWarps / 2);
+      mbar_init(s_free + i, kEpilogueWarps);
     }
     fence_mbar_init();
   }
@@ -471,9 +512,32 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         ok = mbar_wait(ring_full + k % kN, (k / kN) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
     }
     if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
+  } else if (PASS == 2 && warp == kLseWarp) {
+    // ===== log-sums of the row tiles, as many tiles ahead as the ring holds =====
+    int j = 0;
+    while (left > 0 && ok) {
+      const int count = w.count(left);
+      const float* src = p.lse + (w.item1 + int64_t(w.g) * w.s.row_pairs()) * kPair +
+                         int64_t(w.s.first_row_tile(w.pair) + w.at) * kTile;
+      for (int u = 0; u < count; ++u, ++j) {
+        const int slot = j % kLseRing;
+        if (j >= kLseRing && !(ok = wait_all(lse_free + slot, (j / kLseRing - 1) & 1))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(lse_full + slot, kTile * 4);
+          bulk_copy(sm + S::lse + slot * kTile * 4, src + int64_t(u) * kTile, kTile * 4, lse_full + slot);
+        }
+      }
+      left -= count;
+      w.next(p, left);
+    }
+    for (int k = max(0, j - kLseRing); k < j; ++k)
+      ok = mbar_wait(lse_full + k % kLseRing, (k / kLseRing) & 1, ok ? kLandLimitNs : kDrainLimitNs) && ok;
+    if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
   } else if (warp == kMmaWarp) {
     // ===== MMAs: the warp runs the loop, one elected lane issues =====
     const uint32_t idesc = idesc_bf16(kTile, kTile, false);
+    const uint64_t pair_desc = smem_desc(smem_u32(sm + S::pair), 16, 1024);
+    const uint64_t ring_desc = smem_desc(smem_u32(sm + S::ring), 16, 1024);
     int i = 0, j = 0, done[2] = {0, 0}, last_tile = 0;
     for (; left > 0 && ok; ++i) {
       const int count = w.count(left), tiles = tiles_of(w), slot = i & 1;
@@ -485,14 +549,8 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           const int buf = done[x] & 1;
           if (done[x] >= 2 && !(ok = wait_all(s_free + 2 * x + buf, ((done[x] >> 1) - 1) & 1))) break;
           tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-            umma(tmem + x * 256 + buf * 128,
-                 smem_desc(smem_u32(sm + S::pair + (slot * 2 + x) * kTileBytes) + off, 16, 1024),
-                 smem_desc(smem_u32(sm + S::ring + r * kTileBytes) + off, 16, 1024), idesc, ks > 0);
-          }
-          umma_commit(s_full + 2 * x + buf);
+          umma_tile(tmem + x * 256 + buf * 128, pair_desc + ((slot * 2 + x) * kTileBytes >> 4),
+                    ring_desc + (r * kTileBytes >> 4), idesc, s_full + 2 * x + buf);
           ++done[x];
           last_tile = x;
         }
@@ -562,80 +620,95 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     }
   } else if (warp < kEpilogueWarps) {
     // ===== scores to sums or weights =====
-    const int x = (warp >> 2) & 1, half = warp >> 3;      // M tile, half of its columns
-    const int r = (warp & 3) * 32 + lane;                 // TMEM lane: row or key of the tile
-    const uint32_t columns = tmem + x * 256 + half * 64 + (uint32_t((warp & 3) * 32) << 16);
+    const int quarter = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // TMEM lane: row or key of a tile
+    const uint32_t columns = tmem + quarter * 32 + (uint32_t((warp & 3) * 32) << 16);
     const uint64_t qs2 = f2(a.qscale, a.qscale);
-    int done = 0;
+    int j = 0, done[2] = {0, 0};
     while (left > 0 && ok) {
-      const int count = w.count(left);
-      const bool active = x < tiles_of(w);
-      // pass 2: log-sums of the row tiles; read through L1, where the tile's
-      // are asked for while the one before it is added up
-      const float* lse = PASS == 1 ? nullptr
-                                   : p.lse + (w.item1 + int64_t(w.g) * w.s.row_pairs()) * kPair +
-                                         int64_t(w.s.first_row_tile(w.pair) + w.at) * kTile + half * 64;
-      float m = kWeighNoScore, sum = 0.f;
+      const int count = w.count(left), tiles = tiles_of(w);
+      float m[2] = {kWeighNoScore, kWeighNoScore}, sum[2] = {0.f, 0.f};
       // Pass 1: keys up to the row's last one, from the piece's first tile and
-      // this half on.  Pass 2: the token, from the piece's first row tile on,
+      // this quarter on.  Pass 2: the token, from the piece's first row tile on,
       // whose rows are the first to see the thread's key, and the first behind
-      // the sequence.
-      int seen, end = 0;
+      // the sequence.  (Of tile 1: the next tokens, the 128th key from there.)
+      int seen[2], end = 0;
       if constexpr (PASS == 1) {
-        const int token = ((2 * w.pair + x) << w.s.log_tokens) + (r >> shift);
-        seen = (token < w.s.n ? w.s.context + token + 1 : INT32_MAX) - w.at * kTile - half * 64;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int token = ((2 * w.pair + x) << w.s.log_tokens) + (r >> shift);
+          seen[x] = (token < w.s.n ? w.s.context + token + 1 : INT32_MAX) - w.at * kTile - quarter * 32;
+        }
       } else {
         const int token = (w.s.first_row_tile(w.pair) + w.at) << w.s.log_tokens;
-        seen = w.pair * kPair + x * kTile + r - w.s.context - token;
+        seen[0] = w.pair * kPair + r - w.s.context - token;
+        seen[1] = seen[0] + kTile;
         end = w.s.n - token;
       }
-      for (int u = 0; u < count; ++u) {
-        if (active) {
-          const int buf = done & 1;
-          // Columns [from, to) of the half count, for this thread; `full`: all, for the whole warp.
+      for (int u = 0; u < count; ++u, ++j) {
+        uint64_t lse[PASS == 2 ? 16 : 1];
+        if constexpr (PASS == 2) {
+          if (!(ok = wait_all(lse_full + j % kLseRing, (j / kLseRing) & 1))) break;
+          const ulonglong2* n = reinterpret_cast<const ulonglong2*>(
+              sm + S::lse + ((j % kLseRing) * kTile + quarter * 32) * 4);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const ulonglong2 x = n[c];
+            lse[2 * c] = x.x;
+            lse[2 * c + 1] = x.y;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(lse_free + j % kLseRing);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x >= tiles) break;
+          const int buf = done[x] & 1;
+          // Columns [from, to) of the quarter count for this thread.
           int from = 0, to;
           if constexpr (PASS == 1) {
-            to = min(64, seen);
-            seen -= kTile;
+            to = seen[x];
+            seen[x] -= kTile;
           } else {
-            from = max(0, (min(kTile, max(0, seen)) << shift) - half * 64);
-            to = min(64, (min(kTile, end) << shift) - half * 64);
-            seen -= 1 << w.s.log_tokens;
-            end -= 1 << w.s.log_tokens;
+            from = (min(kTile, max(0, seen[x])) << shift) - quarter * 32;
+            to = (min(kTile, end) << shift) - quarter * 32;
+            seen[x] -= 1 << w.s.log_tokens;
           }
-          const bool full = __all_sync(0xffffffffu, from == 0 && to >= 64);
-          const float2 ahead = PASS == 2 && u + 1 < count
-                                   ? reinterpret_cast<const float2*>(lse + kTile)[lane]
-                                   : make_float2(0.f, 0.f);
-          if (!(ok = wait_all(s_full + 2 * x + buf, (done >> 1) & 1))) break;
+          const bool full = __all_sync(0xffffffffu, from <= 0 && to >= 32);
+          const bool none = __all_sync(0xffffffffu, to <= max(0, from) || from >= 32);
+          if (!(ok = wait_all(s_full + 2 * x + buf, (done[x] >> 1) & 1))) break;
+          ++done[x];
           tc_fence_after();
-          uint64_t acc[2] = {0ull, 0ull};
-          // 32 columns; MASKED: some do not count, their weight is 0 whatever
-          // the score or (rows behind the sequence have none) the log-sum is.
-          auto add = [&](uint32_t (&v)[32], int chunk, auto masked_t) {
+          uint32_t v[32];
+          tmem_ld32(columns + x * 256 + buf * 128, v);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + 2 * x + buf);
+          // MASKED: some columns do not count, their weight is 0 whatever the
+          // score or (rows behind the sequence have none) the log-sum is.
+          auto add = [&](auto masked_t) {
             constexpr bool MASKED = decltype(masked_t)::value;
-            auto counts = [&](int c) { return chunk * 32 + c >= from && chunk * 32 + c < to; };
+            uint32_t which = ~0u;  // bit c: column c counts
+            if constexpr (MASKED)
+              which = (to <= 0 ? 0u : to >= 32 ? ~0u : (1u << to) - 1u) & (from >= 32 ? 0u : ~0u << max(0, from));
+            auto counts = [&](int c) { return (which >> c & 1u) != 0; };
+            uint64_t acc[2] = {0ull, 0ull};
             if constexpr (PASS == 1) {
               if constexpr (MASKED) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                   if (!counts(c)) v[c] = 0xFF800000u;  // -infinity
               }
-              float top[2] = {m, m};
+              float top[2] = {m[x], m[x]};
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 top[0] = max3(top[0], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
                 top[1] = max3(top[1], __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
               }
               const float mn = fmaxf(top[0], top[1]);
-              const float alpha = ex2((m - mn) * a.qscale);
-              sum *= alpha;
-              m = mn;
-              float a0, a1;  // the sums so far have the old reference
-              f2_split(acc[0], a0, a1);
-              acc[0] = f2(a0 * alpha, a1 * alpha);
-              f2_split(acc[1], a0, a1);
-              acc[1] = f2(a0 * alpha, a1 * alpha);
+              sum[x] *= ex2((m[x] - mn) * a.qscale);
+              m[x] = mn;
               const uint64_t by = f2(-mn * a.qscale, -mn * a.qscale);
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
@@ -644,50 +717,35 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
                 acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
               }
             } else {
-              const ulonglong2* n = reinterpret_cast<const ulonglong2*>(lse + chunk * 32);
 #pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                const ulonglong2 n4 = n[c >> 2];
-                float e[4];
-                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, n4.x), e[0], e[1]);
-                f2_split(f2_fma(f2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), qs2, n4.y), e[2], e[3]);
+              for (int c = 0; c < 32; c += 2) {
+                float e0, e1;
+                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, lse[c >> 1]), e0, e1);
                 if constexpr (MASKED) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    if (!counts(c + k)) e[k] = -INFINITY;
+                  if (!counts(c)) e0 = -INFINITY;
+                  if (!counts(c + 1)) e1 = -INFINITY;
                 }
-                acc[0] = f2_add(acc[0], f2(ex2(e[0]), ex2(e[1])));
-                acc[1] = f2_add(acc[1], f2(ex2(e[2]), ex2(e[3])));
+                acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2(ex2(e0), ex2(e1)));
               }
             }
+            float s0, s1, s2, s3;
+            f2_split(acc[0], s0, s1);
+            f2_split(acc[1], s2, s3);
+            sum[x] += (s0 + s1) + (s2 + s3);
           };
-#pragma unroll
-          for (int chunk = 0; chunk < 2; ++chunk) {
-            uint32_t v[32];
-            tmem_ld32(columns + buf * 128 + chunk * 32, v);
-            tmem_wait_ld();
-            if (chunk == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(s_free + 2 * x + buf);
-            }
-            if (full) add(v, chunk, std::false_type{});
-            else add(v, chunk, std::true_type{});
-          }
-          float s0, s1, s2, s3;
-          f2_split(acc[0], s0, s1);
-          f2_split(acc[1], s2, s3);
-          sum += (s0 + s1) + (s2 + s3);
-          asm volatile("" ::"f"(ahead.x), "f"(ahead.y));
-          if constexpr (PASS == 2) lse += kTile;
-          ++done;
+          if (full) add(std::false_type{});
+          else if (!none) add(std::true_type{});
         }
+        if (!ok) break;
+        if constexpr (PASS == 2) end -= 1 << w.s.log_tokens;
       }
       if (!ok) break;
-      const int64_t at = ((w.item + blockIdx.x) * 2 + half) * kPair + x * kTile + r;
-      if (active) {
-        if constexpr (PASS == 1) p.records1[at] = make_float2(m * a.qscale, sum);
-        else p.records2[at] = sum;
+      const int64_t at = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x >= tiles) break;
+        if constexpr (PASS == 1) p.records1[at + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
+        else p.records2[at + x * kTile] = sum[x];
       }
       if (tid == 0) {
         Item& item = (PASS == 1 ? p.items1 : p.items2)[w.item];
@@ -722,8 +780,8 @@ __global__ void __launch_bounds__(kPair) pkv_weigh_join_kernel(const TcParams p)
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int first = p.items1[i].first, last = p.items1[i].last;
     float m = kWeighNoScore, l = 0.f;
-    for (int c = 2 * first; c < 2 * last + 2; ++c) {
-      const float2 x = __ldcg(p.records1 + (2 * i + c) * kPair + threadIdx.x);
+    for (int c = 4 * first; c < 4 * last + 4; ++c) {
+      const float2 x = __ldcg(p.records1 + (4 * i + c) * kPair + threadIdx.x);
       const float mn = fmaxf(m, x.x);
       l = l * ex2(m - mn) + x.y * ex2(x.x - mn);
       m = mn;
@@ -749,8 +807,8 @@ __global__ void __launch_bounds__(kPair) pkv_weigh_write_kernel(const TcParams p
     if (id < 0 || id >= a.desc.num_blocks) continue;  // flagged where its keys were read
     const int64_t at = (int64_t(id) * a.desc.num_kv_heads + item.g) * kPage + key % kPage;
     float sum = 0.f;
-    for (int c = 2 * item.first; c < 2 * item.last + 2; ++c)
-      sum += __ldcg(p.records2 + (2 * i + c) * kPair + threadIdx.x);
+    for (int c = 4 * item.first; c < 4 * item.last + 4; ++c)
+      sum += __ldcg(p.records2 + (4 * i + c) * kPair + threadIdx.x);
     const float old = key < scored ? __ldcg(a.scores + at) : 0.f;
     a.scores[at] = fmaf(a.decay, old, sum);
   }
@@ -787,9 +845,9 @@ TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   w.totals = take(2 * sizeof(int64_t));
   w.items1 = take(i1 * sizeof(Item));
   w.items2 = take(i2 * sizeof(Item));
-  w.records1 = take((i1 + dev.sm_count) * 2 * kPair * sizeof(float2));
+  w.records1 = take((i1 + dev.sm_count) * 4 * kPair * sizeof(float2));
   w.lse = take(i1 * kPair * sizeof(float));
-  w.records2 = take((i2 + dev.sm_count) * 2 * kPair * sizeof(float));
+  w.records2 = take((i2 + dev.sm_count) * 4 * kPair * sizeof(float));
   w.total = off;
   return w;
 }
