@@ -127,7 +127,29 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
       return order_key(__ldcg(p.scores + row_of(page, token)));
     };
     auto key_at = [&](int i) { return i < kKeys ? sh.keys[i] : read_key(i); };
-    for (int i = tid; i < min(n, kKeys); i += kThreads) sh.keys[i] = read_key(i);
+    // (eight table reads, then eight score reads of a thread on their way at once)
+    constexpr int kBatch = 8;
+    for (int i0 = tid; i0 < min(n, kKeys); i0 += kBatch * kThreads) {
+      int page[kBatch];
+      float score[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kThreads;
+        page[k] = i < min(n, kKeys) ? __ldg(table + (f + s0 + i) / kPage) : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kThreads;
+        score[k] = -INFINITY;
+        if (page[k] < 0 || page[k] >= p.desc.num_blocks) flag_status(p.status, PKV_STATUS_BAD_BLOCK);
+        else if (i < min(n, kKeys)) score[k] = __ldcg(p.scores + row_of(page[k], f + s0 + i));
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kThreads;
+        if (i < min(n, kKeys)) sh.keys[i] = order_key(score[k]);
+      }
+    }
 
     // ---- the c-th largest key, digit by digit ----
     uint32_t prefix = 0, rest = uint32_t(c);
@@ -149,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
       constexpr int kPer = kBins / kThreads;
       const int low = kBins - kPer * (tid + 1);
       uint32_t bin[kPer] = {};  // of bins low + kPer - 1 down to low
+#pragma unroll 8
       for (int k = 0; k < cluster; ++k) {
         const uint32_t* h = (cluster > 1 ? cl.map_shared_rank(hist, k) : hist) + low;
 #pragma unroll
@@ -253,26 +276,49 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
   const int sub = lane / kLanes, in_row = lane % kLanes;
   uint4* const pool = reinterpret_cast<uint4*>(in_row < kVecs ? p.k_cache : p.v_cache);
   const int vec = in_row % kVecs;
-  // lane l < kWarpRows: source and destination of the warp's row l of a round
-  auto places = [&](int64_t q, int64_t& src, int64_t& dst) {
-    src = dst = -1;
-    if (lane >= kWarpRows || q >= total) return;
+  // Lane l < kWarpRows sees to row l of the warp's in a round: the token that it
+  // comes from is read two rounds ahead, the pages one, so that neither the row
+  // copies nor the barrier wait for a table.
+  const int64_t round_rows = int64_t(cluster) * kRows;
+  const int64_t mine = int64_t(rank) * kRows + warp * kWarpRows + lane;
+  auto token_of = [&](int64_t q) {  // -1: no row
+    return lane >= kWarpRows || q >= total ? -1 : q < c ? __ldcg(list + q) : L - r + int(q - c);
+  };
+  auto lowest_of = [&](int64_t base) {  // of a round's sources
+    return base >= total ? 0 : base < c ? __ldcg(list + base) : L - r + int(base - c);
+  };
+  struct Pages {
+    int src, dst;
+  };
+  auto pages_of = [&](int64_t q, int from) {
+    if (from < 0) return Pages{0, 0};
+    return Pages{__ldg(table + from / kPage), __ldg(table + (f + int(q)) / kPage)};
+  };
+  // Rows of the pools, -1 where nothing moves: it is in its place, or a page is
+  // not one of the pool's.
+  auto rows_of = [&](int64_t q, int from, Pages pg, int64_t& src, int64_t& dst) {
     const int to = f + int(q);
-    const int from = q < c ? __ldcg(list + q) : L - r + int(q - c);
-    if (from == to) return;  // in its place
-    const int ps = page_of(from), pd = page_of(to);
-    if (ps < 0 || pd < 0) {
+    src = dst = -1;
+    if (from < 0 || from == to) return;
+    if (pg.src < 0 || pg.src >= p.desc.num_blocks || pg.dst < 0 || pg.dst >= p.desc.num_blocks) {
       flag_status(p.status, PKV_STATUS_BAD_BLOCK);
       return;
     }
-    src = row_of(ps, from);
-    dst = row_of(pd, to);
+    src = row_of(pg.src, from);
+    dst = row_of(pg.dst, to);
   };
-  const int64_t round_rows = int64_t(cluster) * kRows;
-  int64_t src, dst;
-  const int64_t mine = int64_t(rank) * kRows + warp * kWarpRows + lane;
-  places(mine, src, dst);
+  int from = token_of(mine);
+  Pages pages = pages_of(mine, from);
+  int lowest = cluster > 1 ? lowest_of(0) : 0;
+  int next = token_of(mine + round_rows);
   for (int64_t base = 0; base < total; base += round_rows) {
+    int64_t src, dst;
+    rows_of(base + mine, from, pages, src, dst);
+    from = next;
+    pages = pages_of(base + round_rows + mine, from);
+    next = token_of(base + 2 * round_rows + mine);
+    const bool ahead = lowest >= f + base + round_rows;
+    if (cluster > 1) lowest = lowest_of(base + round_rows);
     uint4 v[kDeep];
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
@@ -288,15 +334,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
         vs = __ldcg(p.v_scale + src);
       }
     }
-    int64_t next_src, next_dst;
-    places(base + round_rows + mine, next_src, next_dst);
     // Every row that these writes may hit has been read (release and acquire
     // order reads too).
     if (cluster == 1) {
       __syncthreads();
     } else {
-      const int lowest = base < c ? __ldcg(list + base) : L - r + int(base - c);  // of the round's sources
-      const bool ahead = lowest >= f + base + round_rows;
       if (base > 0) cluster_wait();  // rounds before
       cluster_arrive();
       if (!ahead) {
@@ -316,8 +358,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
         p.v_scale[dst] = vs;
       }
     }
-    src = next_src;
-    dst = next_dst;
   }
   if (cluster > 1 && total > 0) cluster_wait();
 }
