@@ -68,231 +68,255 @@ __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <bool F8, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
-    pkv_evict_kernel(const EvictArgs p, int cluster, int list_stride) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  using Shared = EvictShared<kThreads>;
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw);
-  constexpr int kWarps = kThreads / 32, kKeys = Shared::kKeys;
+// What one kv head of one sequence keeps: its first f tokens, c of the N between,
+// the last r.
+struct Cut {
+  int b, g, L, f, r, c, N;
+  const int32_t* table;
+  int32_t* list;  // the c tokens
+};
+
+// False where nothing is cut: a short sequence, or (flagged by one thread, as new
+// lengths are written by one) numbers that do not fit.  The same in all CTAs.
+__device__ __forceinline__ bool cut_of(const EvictArgs& p, int item, int list_stride, bool speaks, Cut& x) {
+  const int Hkv = p.desc.num_kv_heads;
+  x.b = item / Hkv;
+  x.g = item - x.b * Hkv;
+  const int L = __ldg(p.seq_lens + x.b), m = __ldg(p.keep + x.b);
+  const int first = p.first ? __ldg(p.first + x.b) : 0;
+  const bool bad = L < 0 || m < 0 || first < 0 || (L > 0 && (L - 1) / kPage >= p.desc.max_blocks_per_seq);
+  if (speaks && x.g == 0 && threadIdx.x == 0) {
+    p.new_lens[x.b] = bad ? L : min(L, m);
+    if (bad) flag_status(p.status, PKV_STATUS_BAD_QUERY);
+  }
+  x.L = L;
+  x.f = min(first, m);
+  x.r = min(p.recent, m - x.f);
+  x.c = m - x.f - x.r;
+  x.N = L - x.r - x.f;  // more than c
+  x.table = p.block_tables + int64_t(x.b) * p.desc.max_blocks_per_seq;
+  x.list = reinterpret_cast<int32_t*>(p.workspace) + int64_t(item) * list_stride;
+  return !bad && L > m;
+}
+
+// A page's row of the head in the pools: [num_blocks][Hkv][16].
+__device__ __forceinline__ int64_t pool_row(const EvictArgs& p, int g, int page, int token) {
+  return (int64_t(page) * p.desc.num_kv_heads + g) * kPage + token % kPage;
+}
+
+// Steps 1 to 3 (see above): the list of c > 0 tokens, complete for the cluster
+// when it returns.
+template <int kThreads>
+__device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, int cluster, int rank,
+                                              EvictShared<kThreads>& sh) {
+  constexpr int kWarps = kThreads / 32, kKeys = EvictShared<kThreads>::kKeys;
   const cg::cluster_group cl = cg::this_cluster();
   auto sync_all = [&] {
     if (cluster > 1) cl.sync();
     else __syncthreads();
   };
-  // Everything read here may be the work of the kernel before.  No early start
-  // for the one behind: pkv_attend reads lengths before it waits, and these
-  // are new ones.
-  griddep_wait();
-  const int rank = blockIdx.x % cluster;
-  const int item = blockIdx.x / cluster;
-  const int Hkv = p.desc.num_kv_heads;
-  const int b = item / Hkv, g = item - b * Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  const int L = __ldg(p.seq_lens + b), m = __ldg(p.keep + b);
-  const int first = p.first ? __ldg(p.first + b) : 0;
-  const bool bad = L < 0 || m < 0 || first < 0 || (L > 0 && (L - 1) / kPage >= p.desc.max_blocks_per_seq);
-  if (g == 0 && rank == 0 && tid == 0) {
-    p.new_lens[b] = bad ? L : min(L, m);
-    if (bad) flag_status(p.status, PKV_STATUS_BAD_QUERY);
-  }
-  if (bad || L <= m) return;  // the whole cluster
-  const int f = min(first, m);
-  const int r = min(p.recent, m - f);
-  const int c = m - f - r;   // candidates that stay
-  const int N = L - r - f;   // candidates, more than c
-  const int32_t* table = p.block_tables + int64_t(b) * p.desc.max_blocks_per_seq;
-  // The page of a token, or -1.
-  auto page_of = [&](int token) {
-    const int id = __ldg(table + token / kPage);
-    return id >= 0 && id < p.desc.num_blocks ? id : -1;
+  // ---- this CTA's slice of the candidates, and their keys ----
+  const int per = ((x.N + cluster - 1) / cluster + 31) / 32 * 32;
+  const int s0 = min(x.N, rank * per), n = min(x.N, s0 + per) - s0;
+  const int token0 = x.f + s0;
+  // (eight table reads, then eight score reads of a thread on their way at once)
+  constexpr int kBatch = 8;
+  auto read_keys = [&](int i0, uint32_t (&key)[kBatch]) {
+    int page[kBatch];
+    float score[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kThreads;
+      page[k] = i < n ? __ldg(x.table + (token0 + i) / kPage) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kThreads;
+      score[k] = -INFINITY;
+      if (page[k] < 0 || page[k] >= p.desc.num_blocks) flag_status(p.status, PKV_STATUS_BAD_BLOCK);
+      else if (i < n) score[k] = __ldcg(p.scores + pool_row(p, x.g, page[k], token0 + i));
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) key[k] = order_key(score[k]);
   };
-  // A page's row of this head in the pools: [num_blocks][Hkv][16].
-  auto row_of = [&](int page, int token) { return (int64_t(page) * Hkv + g) * kPage + token % kPage; };
-  int32_t* list = reinterpret_cast<int32_t*>(p.workspace) + int64_t(item) * list_stride;
+  // a key beyond those that shared memory holds
+  auto read_key = [&](int i) {
+    const int page = __ldg(x.table + (token0 + i) / kPage);
+    if (page < 0 || page >= p.desc.num_blocks) return order_key(-INFINITY);
+    return order_key(__ldcg(p.scores + pool_row(p, x.g, page, token0 + i)));
+  };
+  auto key_at = [&](int i) { return i < kKeys ? sh.keys[i] : read_key(i); };
 
-  if (c > 0) {
-    // ---- this CTA's slice of the candidates, and their keys ----
-    const int per = ((N + cluster - 1) / cluster + 31) / 32 * 32;
-    const int s0 = min(N, rank * per), s1 = min(N, s0 + per);
-    const int n = s1 - s0;
-    auto read_key = [&](int i) {
-      const int token = f + s0 + i;
-      const int page = page_of(token);
-      if (page < 0) {
-        flag_status(p.status, PKV_STATUS_BAD_BLOCK);
-        return order_key(-INFINITY);
-      }
-      return order_key(__ldcg(p.scores + row_of(page, token)));
-    };
-    auto key_at = [&](int i) { return i < kKeys ? sh.keys[i] : read_key(i); };
-    // (eight table reads, then eight score reads of a thread on their way at once)
-    constexpr int kBatch = 8;
-    for (int i0 = tid; i0 < min(n, kKeys); i0 += kBatch * kThreads) {
-      int page[kBatch];
-      float score[kBatch];
+  // ---- the c-th largest key, digit by digit ----
+  // The first digit is counted while the keys come in.
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+  __syncthreads();
+  for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+    uint32_t key[kBatch];
+    read_keys(i0, key);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kThreads;
-        page[k] = i < min(n, kKeys) ? __ldg(table + (f + s0 + i) / kPage) : 0;
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kThreads;
-        score[k] = -INFINITY;
-        if (page[k] < 0 || page[k] >= p.desc.num_blocks) flag_status(p.status, PKV_STATUS_BAD_BLOCK);
-        else if (i < min(n, kKeys)) score[k] = __ldcg(p.scores + row_of(page[k], f + s0 + i));
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kThreads;
-        if (i < min(n, kKeys)) sh.keys[i] = order_key(score[k]);
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i < n) {
+        if (i < kKeys) sh.keys[i] = key[k];
+        atomicAdd(&sh.hist[0][key[k] >> 21], 1u);
       }
     }
-
-    // ---- the c-th largest key, digit by digit ----
-    uint32_t prefix = 0, rest = uint32_t(c);
+  }
+  uint32_t prefix = 0, rest = uint32_t(x.c);
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int above = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // bits from here on are known
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    uint32_t* hist = sh.hist[pass & 1];
+    if (pass > 0) {
+      const int above = pass == 1 ? 21 : 10;  // bits from here on are known
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      uint32_t* hist = sh.hist[pass & 1];
       // (its readers of two passes ago have been through the barrier of the last)
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
         const uint32_t key = key_at(i);
-        if (above == 32 || key >> above == prefix >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
+        if (key >> above == prefix >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
       }
-      sync_all();
-      // Bins from the top, kPer a thread, summed over the cluster.
-      constexpr int kPer = kBins / kThreads;
-      const int low = kBins - kPer * (tid + 1);
-      uint32_t bin[kPer] = {};  // of bins low + kPer - 1 down to low
-#pragma unroll 8
-      for (int k = 0; k < cluster; ++k) {
-        const uint32_t* h = (cluster > 1 ? cl.map_shared_rank(hist, k) : hist) + low;
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-          const uint2 v = *reinterpret_cast<const uint2*>(h + i);
-          bin[kPer - 1 - i] += v.x;
-          bin[kPer - 2 - i] += v.y;
-        }
-      }
-      uint32_t mine = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) mine += bin[i];
-      uint32_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) sh.warp_sum[warp] = incl;
-      __syncthreads();
-      uint32_t before = incl - mine;
-      for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-      if (before < rest && rest <= before + mine) {  // one thread: the digit is in its bins
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (before < rest && rest <= before + bin[i]) {
-            sh.digit = uint32_t(low + kPer - 1 - i);
-            sh.rest = rest - before;
-          }
-          before += bin[i];
-        }
-      }
-      __syncthreads();
-      prefix |= sh.digit << shift;
-      rest = sh.rest;
     }
-    const uint32_t threshold = prefix;  // rest: so many of the keys equal to it stay
-
-    // ---- how many stay of the slices before ----
-    // Warps take whole words of 32 candidates in order, a contiguous run each.
-    const int words = (n + 31) / 32;
-    const int w_per = (words + kWarps - 1) / kWarps;
-    const int w0 = min(words, warp * w_per), w1 = min(words, w0 + w_per);
-    uint32_t gt = 0, eq = 0;
-    for (int w = w0; w < w1; ++w) {
-      const int i = 32 * w + lane;
-      const uint32_t key = i < n ? key_at(i) : 0u;
-      gt += __popc(__ballot_sync(0xffffffffu, i < n && key > threshold));
-      eq += __popc(__ballot_sync(0xffffffffu, i < n && key == threshold));
+    sync_all();
+    // Bins from the top, kPer a thread, summed over the cluster.
+    constexpr int kPer = kBins / kThreads;
+    const int low = kBins - kPer * (tid + 1);
+    uint32_t bin[kPer] = {};  // of bins low + kPer - 1 down to low
+#pragma unroll 4
+    for (int k = 0; k < cluster; ++k) {
+      const uint32_t* h = (cluster > 1 ? cl.map_shared_rank(hist, k) : hist) + low;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(h + i);
+        bin[kPer - 1 - i] += v.x;
+        bin[kPer - 2 - i] += v.y;
+      }
     }
-    if (lane == 0) {
-      sh.warp_sum[warp] = gt;
-      sh.warp_eq[warp] = eq;
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) mine += bin[i];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    const uint32_t others = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane % kWarps] : 0u);
+    uint32_t before = others + incl - mine;
+    if (before < rest && rest <= before + mine) {  // one thread: the digit is in its bins
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        if (before < rest && rest <= before + bin[i]) {
+          sh.digit = uint32_t(low + kPer - 1 - i);
+          sh.rest = rest - before;
+        }
+        before += bin[i];
+      }
     }
     __syncthreads();
+    prefix |= sh.digit << shift;
+    rest = sh.rest;
+  }
+  const uint32_t threshold = prefix;  // rest: so many of the keys equal to it stay
+
+  // ---- how many stay of the slices before ----
+  // Warps take whole words of 32 candidates in order, a contiguous run each.
+  const int words = (n + 31) / 32;
+  const int w_per = (words + kWarps - 1) / kWarps;
+  const int w0 = min(words, warp * w_per), w1 = min(words, w0 + w_per);
+  uint32_t gt = 0, eq = 0;
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const int i = 32 * w + lane;
+    if (i < n) {
+      const uint32_t key = key_at(i);
+      gt += key > threshold;
+      eq += key == threshold;
+    }
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    sh.warp_sum[warp] = gt;
+    sh.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  const uint32_t gt_mine = lane < kWarps ? sh.warp_sum[lane] : 0u, eq_mine = lane < kWarps ? sh.warp_eq[lane] : 0u;
+  uint32_t gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? gt_mine : 0u);
+  uint32_t eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? eq_mine : 0u);
+  if (cluster > 1) {
+    const uint32_t a = __reduce_add_sync(0xffffffffu, gt_mine), e = __reduce_add_sync(0xffffffffu, eq_mine);
     if (tid == 0) {
-      uint32_t a = 0, e = 0;
-      for (int w = 0; w < kWarps; ++w) {
-        a += sh.warp_sum[w];
-        e += sh.warp_eq[w];
-      }
       sh.count_gt = a;
       sh.count_eq = e;
     }
-    sync_all();
-    uint32_t gt_before = 0, eq_before = 0;
-    for (int k = 0; k < rank; ++k) {
-      gt_before += *cl.map_shared_rank(&sh.count_gt, k);
-      eq_before += *cl.map_shared_rank(&sh.count_eq, k);
+    cl.sync();
+    uint32_t g_other = 0, e_other = 0;
+    if (lane < rank) {
+      g_other = *cl.map_shared_rank(&sh.count_gt, lane);
+      e_other = *cl.map_shared_rank(&sh.count_eq, lane);
     }
-    for (int w = 0; w < warp; ++w) {
-      gt_before += sh.warp_sum[w];
-      eq_before += sh.warp_eq[w];
-    }
-    // ---- the list, in order ----
-    for (int w = w0; w < w1; ++w) {
-      const int i = 32 * w + lane;
-      const uint32_t key = i < n ? key_at(i) : 0u;
-      const bool above = i < n && key > threshold, same = i < n && key == threshold;
-      const uint32_t gts = __ballot_sync(0xffffffffu, above), eqs = __ballot_sync(0xffffffffu, same);
-      const uint32_t below = (1u << lane) - 1u;
-      const uint32_t eq_rank = eq_before + __popc(eqs & below);
-      if (above || (same && eq_rank < rest))
-        list[gt_before + __popc(gts & below) + min(eq_rank, rest)] = f + s0 + i;
-      gt_before += __popc(gts);
-      eq_before += __popc(eqs);
-    }
-    sync_all();
+    gt_before += __reduce_add_sync(0xffffffffu, g_other);
+    eq_before += __reduce_add_sync(0xffffffffu, e_other);
   }
+  // ---- the list, in order ----
+#pragma unroll 4
+  for (int w = w0; w < w1; ++w) {
+    const int i = 32 * w + lane;
+    const uint32_t key = i < n ? key_at(i) : 0u;
+    const bool above = i < n && key > threshold, same = i < n && key == threshold;
+    const uint32_t gts = __ballot_sync(0xffffffffu, above), eqs = __ballot_sync(0xffffffffu, same);
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t eq_rank = eq_before + __popc(eqs & below);
+    if (above || (same && eq_rank < rest))
+      x.list[gt_before + __popc(gts & below) + min(eq_rank, rest)] = token0 + i;
+    gt_before += __popc(gts);
+    eq_before += __popc(eqs);
+  }
+  sync_all();
+}
 
-  // ---- move ----
-  // Rows q = 0 .. c + r - 1 go to token f + q: the listed ones, then the recent.
-  // bf16: a warp moves a row at a time, K in its first half and V in its
-  // second, 16 bytes a lane; E4M3 rows are half as long and a warp moves two.
-  constexpr int kVecs = F8 ? 8 : 16;            // 16-byte vectors of a row of K or of V
-  constexpr int kLanes = 2 * kVecs;             // lanes a row
-  constexpr int kSub = 32 / kLanes;             // rows that a warp moves at a time
-  constexpr int kDeep = 8;                      // times, all in flight
-  constexpr int kWarpRows = kSub * kDeep;       // 8 or 16
-  constexpr int kRows = kWarpRows * kWarps;   // rows of a CTA's round
-  const int total = c + r;
+// Step 4.  kParts 2: K and V rows of the item together, lanes of a row's first
+// half K's; 1: those of `part` (0 K, with the scores, 1 V), 16 bytes a lane.
+template <bool F8, int kThreads, int kParts>
+__device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int cluster, int rank, int part) {
+  constexpr int kVecs = F8 ? 8 : 16;                  // 16-byte vectors of a row of K or of V
+  constexpr int kLanes = kParts * kVecs;              // lanes a row
+  constexpr int kSub = 32 / kLanes;                   // rows that a warp moves at a time
+  constexpr int kDeep = 8;                            // times, all in flight
+  constexpr int kWarpRows = kSub * kDeep;             // 8 to 32
+  constexpr int kRows = kWarpRows * (kThreads / 32);  // rows of a CTA's round
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int f = x.f, c = x.c, L = x.L, r = x.r, total = c + r;
   const int sub = lane / kLanes, in_row = lane % kLanes;
-  uint4* const pool = reinterpret_cast<uint4*>(in_row < kVecs ? p.k_cache : p.v_cache);
+  const bool is_v = kParts == 2 ? in_row >= kVecs : part == 1;
+  uint4* const pool = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache);
   const int vec = in_row % kVecs;
+  const bool moves_scores = kParts == 2 || part == 0;
   // Lane l < kWarpRows sees to row l of the warp's in a round: the token that it
   // comes from is read two rounds ahead, the pages one, so that neither the row
   // copies nor the barrier wait for a table.
   const int64_t round_rows = int64_t(cluster) * kRows;
   const int64_t mine = int64_t(rank) * kRows + warp * kWarpRows + lane;
   auto token_of = [&](int64_t q) {  // -1: no row
-    return lane >= kWarpRows || q >= total ? -1 : q < c ? __ldcg(list + q) : L - r + int(q - c);
+    return lane >= kWarpRows || q >= total ? -1 : q < c ? __ldcg(x.list + q) : L - r + int(q - c);
   };
   auto lowest_of = [&](int64_t base) {  // of a round's sources
-    return base >= total ? 0 : base < c ? __ldcg(list + base) : L - r + int(base - c);
+    return base >= total ? 0 : base < c ? __ldcg(x.list + base) : L - r + int(base - c);
   };
   struct Pages {
     int src, dst;
   };
   auto pages_of = [&](int64_t q, int from) {
     if (from < 0) return Pages{0, 0};
-    return Pages{__ldg(table + from / kPage), __ldg(table + (f + int(q)) / kPage)};
+    return Pages{__ldg(x.table + from / kPage), __ldg(x.table + (f + int(q)) / kPage)};
   };
   // Rows of the pools, -1 where nothing moves: it is in its place, or a page is
   // not one of the pool's.
@@ -304,8 +328,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
       flag_status(p.status, PKV_STATUS_BAD_BLOCK);
       return;
     }
-    src = row_of(pg.src, from);
-    dst = row_of(pg.dst, to);
+    src = pool_row(p, x.g, pg.src, from);
+    dst = pool_row(p, x.g, pg.dst, to);
   };
   int from = token_of(mine);
   Pages pages = pages_of(mine, from);
@@ -328,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
     float score = 0.f;
     uint8_t ks = 0, vs = 0;
     if (src >= 0) {
-      score = __ldcg(p.scores + src);
+      if (moves_scores) score = __ldcg(p.scores + src);
       if constexpr (F8) {
-        ks = __ldcg(p.k_scale + src);
-        vs = __ldcg(p.v_scale + src);
+        if (kParts == 2 || part == 0) ks = __ldcg(p.k_scale + src);
+        if (kParts == 2 || part == 1) vs = __ldcg(p.v_scale + src);
       }
     }
     // Every row that these writes may hit has been read (release and acquire
@@ -352,78 +376,118 @@ __global__ void __launch_bounds__(kThreads, kThreads == kBigThreads ? 1 : 4)
       if (d >= 0) pool[d * kVecs + vec] = v[i];
     }
     if (dst >= 0) {
-      p.scores[dst] = score;
+      if (moves_scores) p.scores[dst] = score;
       if constexpr (F8) {
-        p.k_scale[dst] = ks;
-        p.v_scale[dst] = vs;
+        if (kParts == 2 || part == 0) p.k_scale[dst] = ks;
+        if (kParts == 2 || part == 1) p.v_scale[dst] = vs;
       }
     }
   }
   if (cluster > 1 && total > 0) cluster_wait();
 }
 
+// Everything read here may be the work of the kernel before.  No early start for
+// the one behind: pkv_attend reads lengths before it waits, and these are new.
+
+// A CTA an item, selection and move.
+template <bool F8>
+__global__ void __launch_bounds__(kSmallThreads, 4) pkv_evict_kernel(const EvictArgs p, int list_stride) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  griddep_wait();
+  Cut x;
+  if (!cut_of(p, blockIdx.x, list_stride, true, x)) return;
+  if (x.c > 0) select_tokens<kSmallThreads>(p, x, 1, 0, *reinterpret_cast<EvictShared<kSmallThreads>*>(smem_raw));
+  move_rows<F8, kSmallThreads, 2>(p, x, 1, 0, 0);
+}
+
+// A cluster an item: the selection.
+__global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_select_kernel(const EvictArgs p, int cluster,
+                                                                          int list_stride) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  griddep_launch_dependents();  // pkv_evict_move_kernel, which waits first and itself starts nothing early
+  griddep_wait();
+  const int rank = blockIdx.x % cluster;
+  Cut x;
+  if (!cut_of(p, blockIdx.x / cluster, list_stride, rank == 0, x) || x.c == 0) return;  // the whole cluster
+  select_tokens<kBigThreads>(p, x, cluster, rank, *reinterpret_cast<EvictShared<kBigThreads>*>(smem_raw));
+}
+
+// A cluster for the K rows of an item, one for its V rows: they have nothing to
+// do with each other once the list is there, and twice the SMs take part.
+template <bool F8>
+__global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_move_kernel(const EvictArgs p, int cluster,
+                                                                        int list_stride) {
+  griddep_wait();
+  const int rank = blockIdx.x % cluster, item = blockIdx.x / cluster;
+  Cut x;
+  if (!cut_of(p, item / 2, list_stride, false, x)) return;
+  move_rows<F8, kBigThreads, 1>(p, x, cluster, rank, item & 1);
+}
+
 int list_stride(const pkv_desc& d) { return d.max_blocks_per_seq * kPage; }
 
-using Kernel = void (*)(EvictArgs, int, int);
-
-cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], cudaStream_t stream, int64_t items, int cluster, bool big) {
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(cluster);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], cudaStream_t stream, int64_t ctas, int cluster, int threads,
+                          size_t smem) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(items * cluster));
-  cfg.blockDim = dim3(unsigned(big ? kBigThreads : kSmallThreads));
-  cfg.dynamicSmemBytes = big ? sizeof(EvictShared<kBigThreads>) : sizeof(EvictShared<kSmallThreads>);
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cfg;
 }
 
-// How many clusters of 1, 2, 4, 8 and 16 CTAs of 1024 threads run at once on a
-// device, asked once (a cluster stays within a GPC).
+// What a device can run, asked once.
+struct Resident {
+  int select[5], move[5];  // clusters of 1, 2, 4, 8 and 16 CTAs at once (a cluster stays within a GPC)
+};
+
 template <bool F8>
-const int* resident_clusters(int device) {
-  static int most[64][5];
+const Resident* resident(int device) {
+  static Resident most[64];
   static bool done[64] = {};
   if (device < 0 || device >= 64) return nullptr;
   if (!done[device]) {
-    const Kernel big = pkv_evict_kernel<F8, kBigThreads>, small = pkv_evict_kernel<F8, kSmallThreads>;
-    if (cudaFuncSetAttribute(big, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(sizeof(EvictShared<kBigThreads>))) != cudaSuccess ||
-        cudaFuncSetAttribute(small, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(sizeof(EvictShared<kSmallThreads>))) != cudaSuccess ||
-        cudaFuncSetAttribute(big, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    auto set = [](auto kernel, size_t smem) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess &&
+             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    };
+    if (!set(pkv_evict_kernel<F8>, sizeof(EvictShared<kSmallThreads>)) ||
+        !set(pkv_evict_select_kernel, sizeof(EvictShared<kBigThreads>)) || !set(pkv_evict_move_kernel<F8>, 0)) {
       cudaGetLastError();
       return nullptr;
     }
-    for (int i = 0; i < 5; ++i) {
+    auto ask = [](auto kernel, int cluster, size_t smem) {
       cudaLaunchAttribute attr[2];
-      cudaLaunchConfig_t cfg = config(attr, nullptr, 1, 1 << i, true);
-      cfg.numAttrs = 1;
+      const cudaLaunchConfig_t cfg = config(attr, nullptr, cluster, cluster, kBigThreads, smem);
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, big, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;  // a size that this device cannot run
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();  // a size that this device cannot run
+        n = 0;
       }
-      most[device][i] = n;
+      return n;
+    };
+    for (int i = 0; i < 5; ++i) {
+      most[device].select[i] = ask(pkv_evict_select_kernel, 1 << i, sizeof(EvictShared<kBigThreads>));
+      most[device].move[i] = ask(pkv_evict_move_kernel<F8>, 1 << i, 0);
     }
     done[device] = true;
   }
-  return most[device];
+  return &most[device];
 }
 
-// CTAs of 1024 threads an item: as many as let all items run at once, none for
-// less than 512 tokens of the widest sequence.  0: items or tables too small for
-// them, a CTA of 256 threads each.
-int cluster_size(const int* most, const pkv_desc& d, int64_t items) {
-  const int64_t tokens = int64_t(d.max_blocks_per_seq) * kPage;
-  if (items > most[0] || tokens < 4 * 512) return 0;
+// CTAs a cluster: as many as let all clusters run at once, none for less than
+// 512 tokens of the widest sequence.
+int cluster_size(const int (&most)[5], int64_t clusters, int64_t tokens) {
   int n = 1;
   for (int i = 1; i < 5; ++i)
-    if (items <= most[i] && tokens >= int64_t(512) << i) n = 1 << i;
+    if (clusters <= most[i] && tokens >= int64_t(512) << i) n = 1 << i;
   return n;
 }
 
@@ -435,17 +499,33 @@ size_t evict_workspace_bytes(const pkv_desc& d, int32_t num_seqs) {
 
 int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
   if (a.workspace_bytes < evict_workspace_bytes(a.desc, a.num_seqs)) return PKV_ERR_WORKSPACE;
-  const int* most = fp8 ? resident_clusters<true>(ctx.dev->device) : resident_clusters<false>(ctx.dev->device);
+  const Resident* most = fp8 ? resident<true>(ctx.dev->device) : resident<false>(ctx.dev->device);
   if (!most) return PKV_ERR_LAUNCH;
   const int64_t items = int64_t(a.num_seqs) * a.desc.num_kv_heads;
-  if (items * kMaxCluster > INT32_MAX) return PKV_ERR_RANGE;
-  const int n = cluster_size(most, a.desc, items), cluster = n ? n : 1;
-  const Kernel kernel = n ? (fp8 ? pkv_evict_kernel<true, kBigThreads> : pkv_evict_kernel<false, kBigThreads>)
-                          : (fp8 ? pkv_evict_kernel<true, kSmallThreads> : pkv_evict_kernel<false, kSmallThreads>);
+  const int64_t tokens = int64_t(a.desc.max_blocks_per_seq) * kPage;
+  if (items * 2 * kMaxCluster > INT32_MAX) return PKV_ERR_RANGE;
+  const int stride = list_stride(a.desc);
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = config(attr, ctx.stream, items, cluster, n != 0);
+  // Both sides of the rule: MEASURED
+  if (items * 2 > most->move[0] || tokens < 4096) {
+    const cudaLaunchConfig_t cfg =
+        config(attr, ctx.stream, items, 1, kSmallThreads, sizeof(EvictShared<kSmallThreads>));
+    TraceScope ts(ctx.stream, PKV_K_EVICT);
+    cudaLaunchKernelEx(&cfg, fp8 ? pkv_evict_kernel<true> : pkv_evict_kernel<false>, a, stride);
+    return ts.done();
+  }
+  {
+    const int cluster = cluster_size(most->select, items, tokens);
+    const cudaLaunchConfig_t cfg =
+        config(attr, ctx.stream, items * cluster, cluster, kBigThreads, sizeof(EvictShared<kBigThreads>));
+    TraceScope ts(ctx.stream, PKV_K_EVICT);
+    cudaLaunchKernelEx(&cfg, pkv_evict_select_kernel, a, cluster, stride);
+    if (int e = ts.done()) return e;
+  }
+  const int cluster = cluster_size(most->move, items * 2, tokens);
+  const cudaLaunchConfig_t cfg = config(attr, ctx.stream, items * 2 * cluster, cluster, kBigThreads, 0);
   TraceScope ts(ctx.stream, PKV_K_EVICT);
-  cudaLaunchKernelEx(&cfg, kernel, a, cluster, list_stride(a.desc));
+  cudaLaunchKernelEx(&cfg, fp8 ? pkv_evict_move_kernel<true> : pkv_evict_move_kernel<false>, a, cluster, stride);
   return ts.done();
 }
 
