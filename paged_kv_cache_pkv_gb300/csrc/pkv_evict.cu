@@ -9,8 +9,9 @@
 //     into an unsigned number), kept in shared memory (kKeys a CTA, the rest
 //     of a very long slice is read again).
 //  2. The key of the c-th largest by radix selection, 11 + 11 + 10 bits from
-//     the top: a histogram of the keys that agree so far in every CTA, read by
-//     all through distributed shared memory.  Attention weights spread over a
+//     the top: a histogram of the keys that agree so far in every CTA, its
+//     counts added up through distributed shared memory (only those that are
+//     not 0 travel; all CTAs reading all histograms took half of the selection).  Attention weights spread over a
 //     few dozen powers of two, so the first digit, exponent and two bits of
 //     the mantissa, already parts them.
 //  3. Keys above it stay; of those equal to it the lowest tokens, as many as
@@ -48,6 +49,9 @@ template <int kThreads>
 struct EvictShared {
   static constexpr int kKeys = kThreads == kBigThreads ? 24576 : 8192;  // of a slice, held here
   uint32_t hist[2][kBins];
+  // A cluster's counts, of each pass: every CTA has those of the pairs of bins
+  // that are its own, pair i the CTA i % cluster's.
+  uint32_t total[kThreads == kBigThreads ? 3 : 1][kThreads == kBigThreads ? kBins : 2];
   uint32_t keys[kKeys];
   uint32_t warp_sum[kThreads / 32], warp_eq[kThreads / 32];
   uint32_t digit, rest;         // of the last selection pass
@@ -152,6 +156,12 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
   // ---- the c-th largest key, digit by digit ----
   // The first digit is counted while the keys come in.
   for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+  if constexpr (kThreads == kBigThreads) {
+    if (cluster > 1) {
+      for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.total[0][0])[i] = 0;
+      cluster_arrive();
+    }
+  }
   __syncthreads();
   for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
     uint32_t key[kBatch];
@@ -173,7 +183,6 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
     if (pass > 0) {
       const int above = pass == 1 ? 21 : 10;  // bits from here on are known
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      // (its readers of two passes ago have been through the barrier of the last)
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
 #pragma unroll 4
@@ -182,20 +191,27 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
         if (key >> above == prefix >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
       }
     }
-    sync_all();
+    __syncthreads();
     // Bins from the top, kPer a thread, summed over the cluster.
     constexpr int kPer = kBins / kThreads;
     const int low = kBins - kPer * (tid + 1);
-    uint32_t bin[kPer] = {};  // of bins low + kPer - 1 down to low
-#pragma unroll 4
-    for (int k = 0; k < cluster; ++k) {
-      const uint32_t* h = (cluster > 1 ? cl.map_shared_rank(hist, k) : hist) + low;
-#pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(h + i);
-        bin[kPer - 1 - i] += v.x;
-        bin[kPer - 2 - i] += v.y;
+    const uint32_t* counts = hist;
+    if constexpr (kThreads == kBigThreads) {
+      if (cluster > 1) {
+        if (pass == 0) cluster_wait();  // all counts are 0
+        for (int i = tid; i < kBins; i += kThreads)
+          if (const uint32_t v = hist[i]) atomicAdd(cl.map_shared_rank(&sh.total[pass][i], (i >> 1) % cluster), v);
+        cl.sync();
+        static_assert(kBins / kBigThreads == 2, "a thread reads one pair");
+        counts = cl.map_shared_rank(sh.total[pass], (low >> 1) % cluster);
       }
+    }
+    uint32_t bin[kPer];  // of bins low + kPer - 1 down to low
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(counts + low + i);
+      bin[kPer - 1 - i] = v.x;
+      bin[kPer - 2 - i] = v.y;
     }
     uint32_t mine = 0;
 #pragma unroll
@@ -283,12 +299,12 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
   sync_all();
 }
 
-// Step 4.  kParts 2: K and V rows of the item together, lanes of a row's first
-// half K's; 1: those of `part` (0 K, with the scores, 1 V), 16 bytes a lane.
-template <bool F8, int kThreads, int kParts>
+// Step 4.  kBoth: K and V rows of the item together, the lanes of a row's first
+// half K's.  Otherwise those of `part`: 0 K's, 1 V's.  16 bytes a lane.
+template <bool F8, int kThreads, bool kBoth>
 __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int cluster, int rank, int part) {
   constexpr int kVecs = F8 ? 8 : 16;                  // 16-byte vectors of a row of K or of V
-  constexpr int kLanes = kParts * kVecs;              // lanes a row
+  constexpr int kLanes = kBoth ? 2 * kVecs : kVecs;
   constexpr int kSub = 32 / kLanes;                   // rows that a warp moves at a time
   constexpr int kDeep = 8;                            // times, all in flight
   constexpr int kWarpRows = kSub * kDeep;             // 8 to 32
@@ -296,10 +312,10 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int f = x.f, c = x.c, L = x.L, r = x.r, total = c + r;
   const int sub = lane / kLanes, in_row = lane % kLanes;
-  const bool is_v = kParts == 2 ? in_row >= kVecs : part == 1;
+  const bool is_v = kBoth ? in_row >= kVecs : part == 1;
   uint4* const pool = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache);
   const int vec = in_row % kVecs;
-  const bool moves_scores = kParts == 2 || part == 0;
+  const bool moves_k = kBoth || part == 0, moves_v = kBoth || part == 1;  // their scales, K's the scores
   // Lane l < kWarpRows sees to row l of the warp's in a round: the token that it
   // comes from is read two rounds ahead, the pages one, so that neither the row
   // copies nor the barrier wait for a table.
@@ -352,10 +368,10 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int 
     float score = 0.f;
     uint8_t ks = 0, vs = 0;
     if (src >= 0) {
-      if (moves_scores) score = __ldcg(p.scores + src);
+      if (moves_k) score = __ldcg(p.scores + src);
       if constexpr (F8) {
-        if (kParts == 2 || part == 0) ks = __ldcg(p.k_scale + src);
-        if (kParts == 2 || part == 1) vs = __ldcg(p.v_scale + src);
+        if (moves_k) ks = __ldcg(p.k_scale + src);
+        if (moves_v) vs = __ldcg(p.v_scale + src);
       }
     }
     // Every row that these writes may hit has been read (release and acquire
@@ -376,10 +392,10 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int 
       if (d >= 0) pool[d * kVecs + vec] = v[i];
     }
     if (dst >= 0) {
-      if (moves_scores) p.scores[dst] = score;
+      if (moves_k) p.scores[dst] = score;
       if constexpr (F8) {
-        if (kParts == 2 || part == 0) p.k_scale[dst] = ks;
-        if (kParts == 2 || part == 1) p.v_scale[dst] = vs;
+        if (moves_k) p.k_scale[dst] = ks;
+        if (moves_v) p.v_scale[dst] = vs;
       }
     }
   }
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(kSmallThreads, 4) pkv_evict_kernel(const Evict
   Cut x;
   if (!cut_of(p, blockIdx.x, list_stride, true, x)) return;
   if (x.c > 0) select_tokens<kSmallThreads>(p, x, 1, 0, *reinterpret_cast<EvictShared<kSmallThreads>*>(smem_raw));
-  move_rows<F8, kSmallThreads, 2>(p, x, 1, 0, 0);
+  move_rows<F8, kSmallThreads, true>(p, x, 1, 0, 0);
 }
 
 // A cluster an item: the selection.
@@ -412,16 +428,17 @@ __global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_select_kernel(const 
   select_tokens<kBigThreads>(p, x, cluster, rank, *reinterpret_cast<EvictShared<kBigThreads>*>(smem_raw));
 }
 
-// A cluster for the K rows of an item, one for its V rows: they have nothing to
-// do with each other once the list is there, and twice the SMs take part.
+// A cluster for the K rows of an item, one for its V rows: they have nothing to do
+// with each other once the list is there, and with few items twice the SMs take
+// part.  (Clusters for halves of rows took as long or longer.)
 template <bool F8>
 __global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_move_kernel(const EvictArgs p, int cluster,
                                                                         int list_stride) {
   griddep_wait();
-  const int rank = blockIdx.x % cluster, item = blockIdx.x / cluster;
+  const int rank = blockIdx.x % cluster, part = blockIdx.x / cluster;
   Cut x;
-  if (!cut_of(p, item / 2, list_stride, false, x)) return;
-  move_rows<F8, kBigThreads, 1>(p, x, cluster, rank, item & 1);
+  if (!cut_of(p, part / 2, list_stride, false, x)) return;
+  move_rows<F8, kBigThreads, false>(p, x, cluster, rank, part % 2);
 }
 
 int list_stride(const pkv_desc& d) { return d.max_blocks_per_seq * kPage; }
@@ -443,14 +460,16 @@ cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], cudaStream_t stream, i
   return cfg;
 }
 
-// What a device can run, asked once.
+// Cluster sizes in use, and how many clusters of each a device runs at once with
+// a CTA of 1024 threads an SM (a cluster stays within a GPC), asked once.
+constexpr int kSizes[] = {1, 2, 3, 4, 6, 8, 12, 16};
 struct Resident {
-  int select[5], move[5];  // clusters of 1, 2, 4, 8 and 16 CTAs at once (a cluster stays within a GPC)
+  int most[sizeof(kSizes) / sizeof(kSizes[0])];
 };
 
 template <bool F8>
 const Resident* resident(int device) {
-  static Resident most[64];
+  static Resident facts[64];
   static bool done[64] = {};
   if (device < 0 || device >= 64) return nullptr;
   if (!done[device]) {
@@ -458,36 +477,34 @@ const Resident* resident(int device) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess &&
              cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
     };
-    if (!set(pkv_evict_kernel<F8>, sizeof(EvictShared<kSmallThreads>)) ||
-        !set(pkv_evict_select_kernel, sizeof(EvictShared<kBigThreads>)) || !set(pkv_evict_move_kernel<F8>, 0)) {
+    constexpr size_t smem = sizeof(EvictShared<kBigThreads>);
+    if (!set(pkv_evict_kernel<F8>, sizeof(EvictShared<kSmallThreads>)) || !set(pkv_evict_select_kernel, smem) ||
+        !set(pkv_evict_move_kernel<F8>, 0)) {
       cudaGetLastError();
       return nullptr;
     }
-    auto ask = [](auto kernel, int cluster, size_t smem) {
+    int i = 0;
+    for (int size : kSizes) {
       cudaLaunchAttribute attr[2];
-      const cudaLaunchConfig_t cfg = config(attr, nullptr, cluster, cluster, kBigThreads, smem);
+      const cudaLaunchConfig_t cfg = config(attr, nullptr, size, size, kBigThreads, smem);
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      if (cudaOccupancyMaxActiveClusters(&n, pkv_evict_select_kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();  // a size that this device cannot run
         n = 0;
       }
-      return n;
-    };
-    for (int i = 0; i < 5; ++i) {
-      most[device].select[i] = ask(pkv_evict_select_kernel, 1 << i, sizeof(EvictShared<kBigThreads>));
-      most[device].move[i] = ask(pkv_evict_move_kernel<F8>, 1 << i, 0);
+      facts[device].most[i++] = n;
     }
     done[device] = true;
   }
-  return &most[device];
+  return &facts[device];
 }
 
 // CTAs a cluster: as many as let all clusters run at once, none for less than
 // 512 tokens of the widest sequence.
-int cluster_size(const int (&most)[5], int64_t clusters, int64_t tokens) {
-  int n = 1;
-  for (int i = 1; i < 5; ++i)
-    if (clusters <= most[i] && tokens >= int64_t(512) << i) n = 1 << i;
+int cluster_size(const Resident& r, int64_t clusters, int64_t tokens) {
+  int n = 1, i = 0;
+  for (int size : kSizes)
+    if (clusters <= r.most[i++] && tokens >= int64_t(512) * size) n = size;
   return n;
 }
 
@@ -499,15 +516,19 @@ size_t evict_workspace_bytes(const pkv_desc& d, int32_t num_seqs) {
 
 int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
   if (a.workspace_bytes < evict_workspace_bytes(a.desc, a.num_seqs)) return PKV_ERR_WORKSPACE;
-  const Resident* most = fp8 ? resident<true>(ctx.dev->device) : resident<false>(ctx.dev->device);
-  if (!most) return PKV_ERR_LAUNCH;
+  const Resident* facts = fp8 ? resident<true>(ctx.dev->device) : resident<false>(ctx.dev->device);
+  if (!facts) return PKV_ERR_LAUNCH;
   const int64_t items = int64_t(a.num_seqs) * a.desc.num_kv_heads;
   const int64_t tokens = int64_t(a.desc.max_blocks_per_seq) * kPage;
   if (items * 2 * kMaxCluster > INT32_MAX) return PKV_ERR_RANGE;
   const int stride = list_stride(a.desc);
   cudaLaunchAttribute attr[2];
-  // Both sides of the rule: MEASURED
-  if (items * 2 > most->move[0] || tokens < 4096) {
+  // Many items with little to move each are better off with a CTA each of one
+  // kernel (us, one against two, 8 heads, bf16: 240 sequences of 500 tokens 144
+  // against 196, 60 of 500 48 against 59; but 8 of 500 23 against 17, 60 of 4000
+  // 142 against 118, on E4M3 pages 85 either way, 9 of 16000 253 against 71).
+  // So is a token a thread (4 sequences of at most 255 tokens: 7.0 against 8.9).
+  if (tokens <= kSmallThreads || (items > 2 * ctx.dev->sm_count && tokens * (fp8 ? 1 : 2) <= 4096)) {
     const cudaLaunchConfig_t cfg =
         config(attr, ctx.stream, items, 1, kSmallThreads, sizeof(EvictShared<kSmallThreads>));
     TraceScope ts(ctx.stream, PKV_K_EVICT);
@@ -515,14 +536,14 @@ int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
     return ts.done();
   }
   {
-    const int cluster = cluster_size(most->select, items, tokens);
+    const int cluster = cluster_size(*facts, items, tokens);
     const cudaLaunchConfig_t cfg =
         config(attr, ctx.stream, items * cluster, cluster, kBigThreads, sizeof(EvictShared<kBigThreads>));
     TraceScope ts(ctx.stream, PKV_K_EVICT);
     cudaLaunchKernelEx(&cfg, pkv_evict_select_kernel, a, cluster, stride);
     if (int e = ts.done()) return e;
   }
-  const int cluster = cluster_size(most->move, items * 2, tokens);
+  const int cluster = cluster_size(*facts, items * 2, tokens);
   const cudaLaunchConfig_t cfg = config(attr, ctx.stream, items * 2 * cluster, cluster, kBigThreads, 0);
   TraceScope ts(ctx.stream, PKV_K_EVICT);
   cudaLaunchKernelEx(&cfg, fp8 ? pkv_evict_move_kernel<true> : pkv_evict_move_kernel<false>, a, cluster, stride);
