@@ -18,10 +18,12 @@
 //    16-byte loads, without shared memory or barriers, two pages (E4M3: four)
 //    of a warp in flight.  Each lane keeps running maxima and sums of its own
 //    keys, reduced over lanes once a piece.  Scores go to the workspace, 4
-//    bytes a (row, key): at one row of four heads a sixteenth of K's bytes,
-//    and mostly read back from L2.
+//    bytes a (row, key), a key's rounded up to 16: at one row of four heads a
+//    sixteenth of K's bytes, and mostly read back from L2.
 //  * pkv_weigh_add_kernel: joins the pieces' sums and turns scores into
-//    weights, one key a lane, with the update of the paged score.
+//    weights, one key a lane, with the update of the paged score.  Its work is
+//    little and its reads depend on one another, so all that do not are on
+//    their way before the first is used.
 //  * Units of work are pages of a kv head in the order (sequence, head, page);
 //    a warp takes an equal share of them, so that lengths of any mixture load
 //    all warps alike.  Piece p of the row has the record (items before it +
@@ -46,29 +48,32 @@ constexpr int kWsWarps = kWsThreads / 32;
 
 // The workspace of a call.
 struct WeighLayout {
-  size_t units, records, scores, many, total;
+  size_t plan, records, scores, many, total;
 };
 
 // What the kernels of few rows need beside the call's arguments.
 struct SmallParams {
   WeighArgs a;
-  int64_t* units;   // of the batch, for pkv_weigh_add_kernel
-  float2* records;  // [items + warps][rows]: (maximum, sum) of a piece
-  float* scores;    // [units][16][stride]
+  int64_t* plan;    // [2][num_seqs + 1]: units and score quads before each sequence, for pkv_weigh_add_kernel
+  float2* records;  // [items + warps][columns]: (maximum, sum) of a piece
+  float4* scores;   // of each sequence [units][16][quads]
   int64_t max_units;
   int32_t small_rows;   // rows x heads of a sequence that they take
-  int32_t stride_log2;  // of a key's scores
   int32_t share_warps;  // warps of pkv_weigh_scores_kernel
 };
+
+// Score quads of a key.
+__device__ __forceinline__ int quads_of(int rows) { return (rows + 3) >> 2; }
 
 __device__ __forceinline__ int64_t share_of(const SmallParams& p, int64_t units) {
   int64_t rest;
   return max(int64_t(1), divide(units + p.share_warps - 1, p.share_warps, rest));
 }
 
-// Units before each sequence, in shared memory: [num_seqs + 1].  Sequences of
-// other sizes, without rows or beyond the workspace have none.
-__device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before, int64_t (*warp_sums)[2]) {
+// Units and score quads before each sequence, in shared memory: [num_seqs + 1].
+// Sequences of other sizes, without rows or beyond the workspace have none.
+__device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before, int64_t* quads,
+                                           int64_t (*warp_sums)[2]) {
   const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads, G = p.a.desc.num_q_heads / Hkv;
   const int per = (B + kWsThreads - 1) / kWsThreads;
   const int b0 = min(B, int(threadIdx.x) * per), b1 = min(B, b0 + per);
@@ -77,29 +82,34 @@ __device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before
   for (int b = b0; b < b1; ++b) {
     WeighSequence s;
     bad = !weigh_sequence(p.a, b, s) || bad;
-    const int64_t units =
-        s.n > 0 && int64_t(s.n) * G <= p.small_rows ? int64_t(Hkv) * ((s.L + kPage - 1) / kPage) : 0;
-    before[b] = units;
-    sum[0] += units;
+    const bool mine = s.n > 0 && int64_t(s.n) * G <= p.small_rows;
+    before[b] = mine ? int64_t(Hkv) * ((s.L + kPage - 1) / kPage) : 0;
+    quads[b] = mine ? before[b] * kPage * quads_of(s.n * G) : 0;
+    sum[0] += before[b];
+    sum[1] += quads[b];
   }
   // The first sequence that does not fit the workspace whole ends the list.
   __shared__ unsigned long long limit;
   if (threadIdx.x == 0) limit = ~0ull;
   block_scan<kWsThreads>(sum, total, warp_sums);
-  int64_t run = sum[0];
   for (int b = b0; b < b1; ++b) {
-    const int64_t units = before[b];
-    if (units > 0 && run + units > p.max_units) {
-      atomicMin(&limit, static_cast<unsigned long long>(run));
+    const int64_t units = before[b], q = quads[b];
+    if (units > 0 && sum[0] + units > p.max_units) {
+      atomicMin(&limit, static_cast<unsigned long long>(sum[0]));
       bad = true;
     }
-    before[b] = run;
-    run += units;
+    before[b] = sum[0];
+    quads[b] = sum[1];
+    sum[0] += units;
+    sum[1] += q;
   }
   __syncthreads();
   const int64_t top = int64_t(min(limit, 0x7FFFFFFFFFFFFFFFull));
   for (int b = b0; b < b1; ++b) before[b] = min(before[b], top);
-  if (threadIdx.x == 0) before[B] = min(total[0], top);
+  if (threadIdx.x == 0) {
+    before[B] = min(total[0], top);
+    quads[B] = total[1];
+  }
   if (bad && blockIdx.x == 0) flag_status(p.a.status, PKV_STATUS_BAD_QUERY);
   __syncthreads();
 }
@@ -115,13 +125,12 @@ __device__ __forceinline__ int sequence_at(const int64_t* before, int B, int64_t
   return lo;
 }
 
-// 16 bytes that are read once: past L1, and first to leave L2, where the scores
-// written meanwhile are read back.
-__device__ __forceinline__ uint4 load_once(const void* p, uint64_t policy) {
+// 16 bytes that are read once: past L1.
+__device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy));
+               : "l"(p));
   return v;
 }
 
@@ -165,18 +174,23 @@ struct KeyPage {
 
 template <int NT, bool F8>
 __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_kernel(const SmallParams p) {
-  __shared__ int64_t before[kMaxSeqs + 1];
+  __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
   __shared__ int64_t warp_sums[kWsWarps][2];
   griddep_wait();
   griddep_launch_dependents();  // only pkv_weigh_add_kernel follows; it waits
-  plan_units(p, before, warp_sums);
+  plan_units(p, before, quads_before, warp_sums);
   const WeighArgs& a = p.a;
   const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, Hq = a.desc.num_q_heads, G = Hq / Hkv;
   const int lane = threadIdx.x & 31;
   const int row = lane >> 2, t = lane & 3;
   const int64_t units = before[B], share = share_of(p, units);
   const int64_t warp = int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.units = units;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i <= B; i += kWsThreads) {
+      p.plan[i] = before[i];
+      p.plan[B + 1 + i] = quads_before[i];
+    }
+  }
   int64_t u = min(units, warp * share);
   const int64_t end = min(units, u + share);
   if (u >= end) return;
@@ -184,8 +198,6 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
   constexpr int kDeep = F8 ? 4 : 2;      // pages in flight
   constexpr int kPieceBytes = 64;        // of a row, between a lane's pieces
   constexpr int kRowBytes = F8 ? kHeadDim : 2 * kHeadDim;
-  const int stride = 1 << p.stride_log2;
-  const uint64_t policy = l2_evict_first_policy();
   int b = sequence_at(before, B, u);
   while (u < end) {
     WeighSequence s;
@@ -195,6 +207,9 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
     const int count = int(min(end - u, int64_t(pages - first)));
     const int rows = s.n * G;  // the group's rows, j * G + h
+    const int stride = 4 * quads_of(rows);
+    float* const scores =
+        reinterpret_cast<float*>(p.scores + quads_before[b]) + ((u - before[b]) * kPage + row) * stride + 2 * t;
 
     // ---- the rows, as B fragments: lane's column row, its elements as in a key ----
     uint32_t qf[NT][8][2];
@@ -272,8 +287,8 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
       const char* at = static_cast<const char*>(a.k_cache) + r * kRowBytes + t * 16;
 #pragma unroll
       for (int c = 0; c < kPieces; ++c) {
-        k.lo[c] = load_once(at + c * kPieceBytes, policy);
-        k.hi[c] = load_once(at + 8 * kRowBytes + c * kPieceBytes, policy);
+        k.lo[c] = load_once(at + c * kPieceBytes);
+        k.hi[c] = load_once(at + 8 * kRowBytes + c * kPieceBytes);
       }
       if constexpr (F8) {
         k.sc_lo = __ldg(a.k_scale + r);
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
       }
       const int key = (first + i) * kPage + row;
       const bool edge = (first + i) * kPage + kPage - 1 > s.L - s.n;  // some row does not see all of the page
-      float* out = p.scores + ((u + i) * kPage + row) * stride + 2 * t;
+      float* out = scores + int64_t(i) * kPage * stride;
       float klo = 1.f, khi = 1.f;
       if constexpr (F8) {
         klo = __uint_as_float(k.sc_lo << 23);
@@ -369,17 +384,20 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
   }
 }
 
-// Scores -> weights -> paged scores.  STRIDE scores a key; ROWS the records' width.
-template <int STRIDE, int ROWS>
-__global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallParams p) {
-  __shared__ int64_t before[kMaxSeqs + 1];
-  __shared__ int64_t warp_sums[kWsWarps][2];
-  griddep_wait();
-  if (__ldcg(p.units) == 0) return;  // all sequences have more rows
-  plan_units(p, before, warp_sums);
+// Scores -> weights -> paged scores.  QUADS: most score quads of a key; COLUMNS:
+// the records' width.
+template <int QUADS, int COLUMNS>
+__global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_kernel(const SmallParams p) {
+  __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
   const WeighArgs& a = p.a;
   const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
   const int lane = threadIdx.x & 31;
+  griddep_wait();
+  for (int i = threadIdx.x; i <= B; i += kWsThreads) {
+    before[i] = __ldcg(p.plan + i);
+    quads_before[i] = __ldcg(p.plan + B + 1 + i);
+  }
+  __syncthreads();
   const int64_t units = before[B], share = share_of(p, units);
   const int64_t warps = int64_t(gridDim.x) * kWsWarps;
   int64_t spare;
@@ -388,24 +406,32 @@ __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallPa
   const int64_t end = min(units, u + mine);
   int b = u < end ? sequence_at(before, B, u) : 0;
   while (u < end) {
-    WeighSequence s;
-    weigh_sequence(a, b, s);
-    const int pages = (s.L + kPage - 1) / kPage;
     int64_t rest;
+    const int pages = int(divide(before[b + 1] - before[b], Hkv, rest));
     const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
     const int count = int(min(end - u, int64_t(pages - first)));
-    const int rows = s.n * G;
-    const int from = a.first ? max(0, __ldg(a.first + b)) : 0;
-    const int scored = a.decay == 0.f ? 0 : a.scored ? __ldg(a.scored + b) : s.L - s.n;
+    const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq;
+    // a lane's page of 32 keys from the piece's page i on, its entry or -1
+    auto entry_of = [&](int i) {
+      return i + (lane >> 4) < count ? __ldg(table + first + i + (lane >> 4)) : -1;
+    };
+    constexpr int kDeep = QUADS >= 4 ? 1 : 4 / QUADS;  // 32 keys each, at a time
+    int ids[kDeep];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) ids[d] = entry_of(2 * d);
+    WeighSequence s;
+    weigh_sequence(a, b, s);
+    const int from = a.first ? __ldg(a.first + b) : 0;
+    const int given = a.scored ? __ldg(a.scored + b) : 0;
 
     // ---- log-sums of the rows: a column a lane, pieces in turn ----
-    constexpr int kCols = ROWS < 32 ? ROWS : 32;
+    constexpr int kCols = COLUMNS < 32 ? COLUMNS : 32;
     const int64_t u0 = before[b] + int64_t(g) * pages;
     const int64_t w0 = divide(u0, share, rest), w1 = divide(u0 + pages - 1, share, rest);
-    const float2* rec = p.records + (int64_t(b) * Hkv + g) * ROWS + lane % kCols;
+    const float2* rec = p.records + (int64_t(b) * Hkv + g) * COLUMNS + lane % kCols;
     float m = kWeighNoScore, l = 0.f;
     for (int64_t w = w0 + lane / kCols; w <= w1; w += 32 / kCols) {
-      const float2 x = __ldcg(rec + w * ROWS);
+      const float2 x = __ldcg(rec + w * COLUMNS);
       const float mn = fmaxf(m, x.x);
       l = l * ex2((m - mn) * a.qscale) + x.y * ex2((x.x - mn) * a.qscale);
       m = mn;
@@ -418,58 +444,46 @@ __global__ void __launch_bounds__(kWsThreads) pkv_weigh_add_kernel(const SmallPa
       m = mn;
     }
     const float mine_lse = m * a.qscale + __log2f(l);
-    // Columns without a row get weight 0; whole MMA tiles of them have no scores.
-    const int columns = (rows + 7) / 8 * 8;
-    float lse[STRIDE];
+    const int rows = s.n * G, quads = quads_of(rows);
+    const int scored = a.decay == 0.f ? 0 : a.scored ? given : s.L - s.n;
+    float lse[4 * QUADS];  // a column without a row: weight 0
 #pragma unroll
-    for (int c = 0; c < STRIDE; ++c) {
+    for (int c = 0; c < 4 * QUADS; ++c) {
       lse[c] = __shfl_sync(0xffffffffu, mine_lse, c % kCols);
       if (c >= rows) lse[c] = INFINITY;
     }
 
-    // ---- a key a lane, kDeep pairs of pages at a time ----
-    const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq;
-    constexpr int kDeep = STRIDE <= 8 ? 4 : 1;
+    // ---- a key a lane ----
+    const float4* src = p.scores + quads_before[b] + ((u - before[b]) * kPage + lane) * quads;
     for (int i = 0; i < count; i += 2 * kDeep) {
       int64_t at[kDeep];
-      float old[kDeep], w[kDeep];
-      float2 x[kDeep][STRIDE / 2];
+      float old[kDeep];
+      float4 x[kDeep][QUADS];
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
-        const int page = first + i + 2 * d + (lane >> 4);
-        const int key = page * kPage + (lane & 15);
-        at[d] = -1;
-        if (i + 2 * d + (lane >> 4) < count && key >= from && key < s.L) {
-          const int id = __ldg(table + page);
-          if (id >= 0 && id < a.desc.num_blocks) at[d] = (int64_t(id) * Hkv + g) * kPage + (lane & 15);
-        }
-        if (at[d] >= 0) {
-          const float2* src = reinterpret_cast<const float2*>(
-              p.scores + ((u + i + 2 * d) * kPage + lane) * STRIDE);
-#pragma unroll
-          for (int c = 0; c < STRIDE / 2; c += 2) {
-            if (STRIDE > 8 && 2 * c >= columns) break;
-            if constexpr (STRIDE == 2) {
-              x[d][0] = __ldcg(src);
-            } else {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + c));
-              x[d][c] = make_float2(v.x, v.y);
-              x[d][c + 1] = make_float2(v.z, v.w);
-            }
-          }
+        const int key = (first + i + 2 * d) * kPage + lane;
+        const bool live = i + 2 * d + (lane >> 4) < count && key >= from && key < s.L && ids[d] >= 0 &&
+                          ids[d] < a.desc.num_blocks;  // flagged where its keys were read
+        at[d] = live ? (int64_t(ids[d]) * Hkv + g) * kPage + (lane & 15) : -1;
+        if (live) {
           old[d] = key < scored ? __ldcg(a.scores + at[d]) : 0.f;
+#pragma unroll
+          for (int c = 0; c < QUADS; ++c)
+            if (c < quads) x[d][c] = __ldcg(src + int64_t(i + 2 * d) * kPage * quads + c);
         }
+        ids[d] = entry_of(i + 2 * (kDeep + d));
       }
 #pragma unroll
       for (int d = 0; d < kDeep; ++d) {
         if (at[d] < 0) continue;
-        w[d] = 0.f;
+        float w = 0.f;
 #pragma unroll
-        for (int c = 0; c < STRIDE / 2; ++c) {
-          if (STRIDE > 8 && 2 * c >= columns) break;
-          w[d] += ex2(fmaf(x[d][c].x, a.qscale, -lse[2 * c])) + ex2(fmaf(x[d][c].y, a.qscale, -lse[2 * c + 1]));
+        for (int c = 0; c < QUADS; ++c) {
+          if (c >= quads) break;
+          w += (ex2(fmaf(x[d][c].x, a.qscale, -lse[4 * c])) + ex2(fmaf(x[d][c].y, a.qscale, -lse[4 * c + 1]))) +
+               (ex2(fmaf(x[d][c].z, a.qscale, -lse[4 * c + 2])) + ex2(fmaf(x[d][c].w, a.qscale, -lse[4 * c + 3])));
         }
-        a.scores[at[d]] = fmaf(a.decay, old[d], w[d]);
+        a.scores[at[d]] = fmaf(a.decay, old[d], w);
       }
     }
     u += count;
@@ -500,12 +514,8 @@ int launch(const LaunchCtx& ctx, void (*kernel)(Params...), dim3 grid, int threa
 // MMA columns of the few-rows kernels: rows x heads, rounded up.
 int column_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
-// Scores a key in the workspace, as a power of two.
-int stride_log2(int64_t rows) {
-  int k = 1;
-  while ((1 << k) < rows) ++k;
-  return k;
-}
+// Score quads of a key at most.
+int most_quads(int64_t rows) { return int((rows + 3) / 4); }
 
 // Rows x heads of a kv head that the few-rows kernels are launched for.
 int64_t small_rows(const pkv_desc& d, int32_t max_rows) {
@@ -527,12 +537,11 @@ ScoresKernel scores_kernel(int tiles) {
                       : pkv_weigh_scores_kernel<4, F8>;
 }
 
-ScoresKernel add_kernel(int tiles, int stride) {
-  return stride == 2    ? pkv_weigh_add_kernel<2, 8>
-         : stride == 4  ? pkv_weigh_add_kernel<4, 8>
-         : stride == 8  ? pkv_weigh_add_kernel<8, 8>
-         : stride == 16 ? pkv_weigh_add_kernel<16, 16>
-                        : pkv_weigh_add_kernel<32, 32>;
+ScoresKernel add_kernel(int tiles, int quads) {
+  return quads == 1   ? pkv_weigh_add_kernel<1, 8>
+         : quads == 2 ? pkv_weigh_add_kernel<2, 8>
+         : tiles == 2 ? pkv_weigh_add_kernel<4, 16>
+                      : pkv_weigh_add_kernel<8, 32>;
 }
 
 // Blocks of the scores kernel on an SM: what its launch bounds ask for.
@@ -545,9 +554,9 @@ int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int32_t max_rows, int6
   return int(want < 1 ? 1 : want < most ? want : most);
 }
 
-int add_grid(const DeviceInfo& dev, const pkv_desc& d, int64_t num_keys) {
+int add_grid(const DeviceInfo& dev, const pkv_desc& d, int tiles, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
-  const int64_t most = int64_t(dev.sm_count) * 8, want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
+  const int64_t most = int64_t(dev.sm_count) * (tiles == 4 ? 2 : 4), want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
   return int(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -563,9 +572,9 @@ WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   const int64_t rows = small_rows(d, max_rows);
   const size_t slots = size_t(num_seqs) * d.num_kv_heads +
                        size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
-  w.units = take(sizeof(int64_t));
+  w.plan = take(2 * (size_t(num_seqs) + 1) * sizeof(int64_t));
   w.records = take(slots * 8 * column_tiles(rows) * sizeof(float2));
-  w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * (size_t(1) << stride_log2(rows)) * sizeof(float));
+  w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * size_t(most_quads(rows)) * sizeof(float4));
   w.many = off;
   if (has_many(d, max_rows)) take(weigh_tc_workspace_bytes(dev, d, num_seqs, num_tokens, num_keys));
   w.total = off;
@@ -588,17 +597,16 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
   const int tiles = column_tiles(rows);
   const int grid = scores_grid(*ctx.dev, d, a.max_rows, a.num_keys);
   SmallParams p{a,
-                reinterpret_cast<int64_t*>(ws + w.units),
+                reinterpret_cast<int64_t*>(ws + w.plan),
                 reinterpret_cast<float2*>(ws + w.records),
-                reinterpret_cast<float*>(ws + w.scores),
+                reinterpret_cast<float4*>(ws + w.scores),
                 a.num_keys / kPage * d.num_kv_heads,
                 int32_t(rows),
-                stride_log2(rows),
                 grid * kWsWarps};
   if (int e = launch(ctx, fp8 ? scores_kernel<true>(tiles) : scores_kernel<false>(tiles), dim3(unsigned(grid)),
                      kWsThreads, p))
     return e;
-  if (int e = launch(ctx, add_kernel(tiles, 1 << p.stride_log2), dim3(unsigned(add_grid(*ctx.dev, d, a.num_keys))),
+  if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)), dim3(unsigned(add_grid(*ctx.dev, d, tiles, a.num_keys))),
                      kWsThreads, p))
     return e;
   if (!has_many(d, a.max_rows)) return PKV_OK;
