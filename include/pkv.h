@@ -478,8 +478,8 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  *                  PKV_STATUS_BAD_QUERY.
  *   num_keys       host-side upper bound on the sum of the seq_lens, each
  *                  rounded up to 16, or <= 0 if unknown (then the block tables'
- *                  width bounds them): it sizes the workspace.  Sequences
- *                  behind that many keys are skipped and flag
+ *                  width bounds them): it sizes the workspace.  Where it does
+ *                  not hold, sequences that do not fit are skipped and flag
  *                  PKV_STATUS_BAD_QUERY.
  *   workspace      at least pkv_weigh_workspace_size bytes for the same
  *                  num_seqs, num_tokens, max_query_len and num_keys, 256-byte

@@ -486,8 +486,8 @@ def weigh(q, k_cache, scores, block_tables, seq_lens, query_start_loc, scale, de
     ``decay`` (0: not read); tokens from ``scored`` on (int32 [B]; None: this
     step's own) have none yet.  The ``first`` tokens of a sequence (int32 [B])
     get none.  ``max_query_len`` and ``num_keys`` (the sum of the lengths, each
-    rounded up to 16) are host-side bounds, 0 = unknown: sequences beyond them
-    are skipped and flagged, so they must hold; they keep the workspace small."""
+    rounded up to 16) are host-side bounds, 0 = unknown.  They must hold (what
+    does not fit is skipped and flagged); they keep the workspace small."""
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).weigh(index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
                                          scale, decay, first, scored, workspace, max_query_len, num_keys)

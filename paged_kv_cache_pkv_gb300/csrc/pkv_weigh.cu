@@ -11,12 +11,12 @@
 // Few rows (up to kSmallRows query rows x heads of a kv head a sequence):
 // bound by the bytes of K, which are read once.
 //  * pkv_weigh_scores_kernel: K pages against the rows on warp-level MMAs, the
-//    page's 16 keys as M, the rows as N (8, 16 or 32).  A product of two
+//    page's 16 keys as M, the rows as N (8, 16, 24 or 32).  A product of two
 //    vectors does not go by the order of their elements, so a lane takes 16
 //    contiguous bytes of a key's row as its elements of two k-steps, and the
 //    queries' fragments are permuted alike: pages go from HBM to registers in
-//    16-byte loads, without shared memory or barriers, two pages (E4M3: four)
-//    of a warp in flight.  Each lane keeps running maxima and sums of its own
+//    16-byte loads, without shared memory or barriers, as many pages of a warp
+//    in flight as registers allow.  Each lane keeps running maxima and sums of its own
 //    keys, reduced over lanes once a piece.  Scores go to the workspace, 4
 //    bytes a (row, key), a key's rounded up to 16: at one row of four heads a
 //    sixteenth of K's bytes, and mostly read back from L2.
@@ -26,8 +26,12 @@
 //    their way before the first is used.
 //  * Units of work are pages of a kv head in the order (sequence, head, page);
 //    a warp takes an equal share of them, so that lengths of any mixture load
-//    all warps alike.  Piece p of the row has the record (items before it +
-//    warps before it), unique as one of them grows from piece to piece.
+//    all warps alike.  In a batch of many pages a head's first page counts as
+//    kHeadUnits more: what begins a piece, queries, tables and the first pages'
+//    way, takes as long as that (a long-tailed batch of 256 sequences on 8-bit
+//    pages: 344 us without, 254, 244 and 239 with 4, 8 and 16).  Piece p of the row has the
+//    record (items before it + warps before it), unique as one of them grows
+//    from piece to piece.
 //  * E4M3 pages: codes become f16 exactly; the bf16 queries become f16 under a
 //    power of two a row that takes its largest element to [2^14, 2^15).  What
 //    that loses of an element is below 2^-24 in f16's units, 2^-38 of the
@@ -43,22 +47,23 @@ namespace pkv {
 namespace {
 
 constexpr int kSmallRows = 32;
+constexpr int kHeadUnits = 16;
 constexpr int kWsThreads = 256;
 constexpr int kWsWarps = kWsThreads / 32;
 
 // The workspace of a call.
 struct WeighLayout {
-  size_t plan, records, scores, many, total;
+  size_t records, scores, many, total;
 };
 
 // What the kernels of few rows need beside the call's arguments.
 struct SmallParams {
   WeighArgs a;
-  int64_t* plan;    // [2][num_seqs + 1]: units and score quads before each sequence, for pkv_weigh_add_kernel
   float2* records;  // [items + warps][columns]: (maximum, sum) of a piece
   float4* scores;   // of each sequence [units][16][quads]
-  int64_t max_units;
+  int64_t max_quads;
   int32_t small_rows;   // rows x heads of a sequence that they take
+  int32_t head_units;   // kHeadUnits or 0
   int32_t share_warps;  // warps of pkv_weigh_scores_kernel
 };
 
@@ -83,8 +88,9 @@ __device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before
     WeighSequence s;
     bad = !weigh_sequence(p.a, b, s) || bad;
     const bool mine = s.n > 0 && int64_t(s.n) * G <= p.small_rows;
-    before[b] = mine ? int64_t(Hkv) * ((s.L + kPage - 1) / kPage) : 0;
-    quads[b] = mine ? before[b] * kPage * quads_of(s.n * G) : 0;
+    const int pages = (s.L + kPage - 1) / kPage;
+    before[b] = mine ? int64_t(Hkv) * (pages + p.head_units) : 0;
+    quads[b] = mine ? int64_t(Hkv) * pages * kPage * quads_of(s.n * G) : 0;
     sum[0] += before[b];
     sum[1] += quads[b];
   }
@@ -94,7 +100,7 @@ __device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before
   block_scan<kWsThreads>(sum, total, warp_sums);
   for (int b = b0; b < b1; ++b) {
     const int64_t units = before[b], q = quads[b];
-    if (units > 0 && sum[0] + units > p.max_units) {
+    if (units > 0 && sum[1] + q > p.max_quads) {
       atomicMin(&limit, static_cast<unsigned long long>(sum[0]));
       bad = true;
     }
@@ -172,6 +178,9 @@ struct KeyPage {
   uint32_t sc_lo, sc_hi;  // E4M3: the rows' scale bytes
 };
 
+// Width of the records of a call with NT MMA tiles of columns.
+__host__ __device__ constexpr int record_columns(int NT) { return NT == 3 ? 32 : 8 * NT; }
+
 template <int NT, bool F8>
 __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_kernel(const SmallParams p) {
   __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
@@ -185,17 +194,12 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
   const int row = lane >> 2, t = lane & 3;
   const int64_t units = before[B], share = share_of(p, units);
   const int64_t warp = int64_t(blockIdx.x) * kWsWarps + (threadIdx.x >> 5);
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i <= B; i += kWsThreads) {
-      p.plan[i] = before[i];
-      p.plan[B + 1 + i] = quads_before[i];
-    }
-  }
   int64_t u = min(units, warp * share);
   const int64_t end = min(units, u + share);
   if (u >= end) return;
   constexpr int kPieces = KeyPage<F8>::kPieces;
-  constexpr int kDeep = F8 ? 4 : 2;      // pages in flight
+  // Pages of a warp in flight: 64 to 128 KB an SM.
+  constexpr int kDeep = F8 ? (NT == 2 || NT == 3 ? 6 : 4) : NT == 2 ? 4 : NT == 3 ? 3 : 2;
   constexpr int kPieceBytes = 64;        // of a row, between a lane's pieces
   constexpr int kRowBytes = F8 ? kHeadDim : 2 * kHeadDim;
   int b = sequence_at(before, B, u);
@@ -204,12 +208,22 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     weigh_sequence(a, b, s);
     const int pages = (s.L + kPage - 1) / kPage;
     int64_t rest;
-    const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
-    const int count = int(min(end - u, int64_t(pages - first)));
+    const int g = int(divide(u - before[b], pages + p.head_units, rest));
+    const int taken = int(min(end - u, pages + p.head_units - rest));
+    const int first = max(0, int(rest) - p.head_units), count = max(0, int(rest) + taken - p.head_units) - first;
     const int rows = s.n * G;  // the group's rows, j * G + h
     const int stride = 4 * quads_of(rows);
-    float* const scores =
-        reinterpret_cast<float*>(p.scores + quads_before[b]) + ((u - before[b]) * kPage + row) * stride + 2 * t;
+    float* const scores = reinterpret_cast<float*>(p.scores + quads_before[b]) +
+                          ((int64_t(g) * pages + first) * kPage + row) * stride + 2 * t;
+    float2* const rec = p.records + (int64_t(b) * Hkv + g + warp) * record_columns(NT) + 2 * t;
+    if (count == 0) {  // the head's first units alone
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        if (row == 0)
+          *reinterpret_cast<float4*>(rec + nt * 8) = make_float4(kWeighNoScore, 0.f, kWeighNoScore, 0.f);
+      u += taken;
+      continue;
+    }
 
     // ---- the rows, as B fragments: lane's column row, its elements as in a key ----
     uint32_t qf[NT][8][2];
@@ -363,7 +377,6 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     }
 
     // ---- the piece's maxima and sums, over the lanes of a column ----
-    float2* rec = p.records + (int64_t(b) * Hkv + g + warp) * (8 * NT) + 2 * t;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -379,7 +392,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
       if (row == 0)
         *reinterpret_cast<float4*>(rec + nt * 8) = make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
     }
-    u += count;
+    u += taken;
     while (b + 1 < B && before[b + 1] <= u) ++b;  // u < end: some later sequence has it
   }
 }
@@ -389,15 +402,12 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
 template <int QUADS, int COLUMNS>
 __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_kernel(const SmallParams p) {
   __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
+  __shared__ int64_t warp_sums[kWsWarps][2];
   const WeighArgs& a = p.a;
   const int B = a.num_seqs, Hkv = a.desc.num_kv_heads, G = a.desc.num_q_heads / Hkv;
   const int lane = threadIdx.x & 31;
+  plan_units(p, before, quads_before, warp_sums);  // of arrays that the kernel before only reads
   griddep_wait();
-  for (int i = threadIdx.x; i <= B; i += kWsThreads) {
-    before[i] = __ldcg(p.plan + i);
-    quads_before[i] = __ldcg(p.plan + B + 1 + i);
-  }
-  __syncthreads();
   const int64_t units = before[B], share = share_of(p, units);
   const int64_t warps = int64_t(gridDim.x) * kWsWarps;
   int64_t spare;
@@ -407,9 +417,12 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
   int b = u < end ? sequence_at(before, B, u) : 0;
   while (u < end) {
     int64_t rest;
-    const int pages = int(divide(before[b + 1] - before[b], Hkv, rest));
-    const int g = int(divide(u - before[b], pages, rest)), first = int(rest);
-    const int count = int(min(end - u, int64_t(pages - first)));
+    const int units_a_head = int(divide(before[b + 1] - before[b], Hkv, rest)), pages = units_a_head - p.head_units;
+    const int g = int(divide(u - before[b], units_a_head, rest));
+    const int taken = int(min(end - u, units_a_head - rest));
+    const int first = max(0, int(rest) - p.head_units), count = max(0, int(rest) + taken - p.head_units) - first;
+    u += taken;
+    if (count == 0) continue;  // the head's first units alone
     const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq;
     // a lane's page of 32 keys from the piece's page i on, its entry or -1
     auto entry_of = [&](int i) {
@@ -426,10 +439,11 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
 
     // ---- log-sums of the rows: a column a lane, pieces in turn ----
     constexpr int kCols = COLUMNS < 32 ? COLUMNS : 32;
-    const int64_t u0 = before[b] + int64_t(g) * pages;
-    const int64_t w0 = divide(u0, share, rest), w1 = divide(u0 + pages - 1, share, rest);
+    const int64_t u0 = before[b] + int64_t(g) * units_a_head;
+    const int64_t w0 = divide(u0, share, rest), w1 = divide(u0 + units_a_head - 1, share, rest);
     const float2* rec = p.records + (int64_t(b) * Hkv + g) * COLUMNS + lane % kCols;
     float m = kWeighNoScore, l = 0.f;
+#pragma unroll 4
     for (int64_t w = w0 + lane / kCols; w <= w1; w += 32 / kCols) {
       const float2 x = __ldcg(rec + w * COLUMNS);
       const float mn = fmaxf(m, x.x);
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
     }
 
     // ---- a key a lane ----
-    const float4* src = p.scores + quads_before[b] + ((u - before[b]) * kPage + lane) * quads;
+    const float4* src = p.scores + quads_before[b] + ((int64_t(g) * pages + first) * kPage + lane) * quads;
     for (int i = 0; i < count; i += 2 * kDeep) {
       int64_t at[kDeep];
       float old[kDeep];
@@ -486,7 +500,6 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
         a.scores[at[d]] = fmaf(a.decay, old[d], w);
       }
     }
-    u += count;
     while (b + 1 < B && before[b + 1] <= u) ++b;
   }
   // (behind a barrier: a block's first thread to say so speaks for all of them)
@@ -512,7 +525,7 @@ int launch(const LaunchCtx& ctx, void (*kernel)(Params...), dim3 grid, int threa
 }
 
 // MMA columns of the few-rows kernels: rows x heads, rounded up.
-int column_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+int column_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 24 ? 3 : 4; }
 
 // Score quads of a key at most.
 int most_quads(int64_t rows) { return int((rows + 3) / 4); }
@@ -528,12 +541,20 @@ bool has_many(const pkv_desc& d, int32_t max_rows) {
   return int64_t(max_rows) * (d.num_q_heads / d.num_kv_heads) > kSmallRows;
 }
 
+// Whether a sequence may have no more.  Where the tokens are as many as the
+// sequences at the most rows each, all have that many; should the bound not hold
+// (a replay with fewer rows), the tensor cores take any number.
+bool has_small(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int32_t max_rows) {
+  return !has_many(d, max_rows) || int64_t(num_seqs) * max_rows != num_tokens;
+}
+
 using ScoresKernel = void (*)(SmallParams);
 
 template <bool F8>
 ScoresKernel scores_kernel(int tiles) {
   return tiles == 1   ? pkv_weigh_scores_kernel<1, F8>
          : tiles == 2 ? pkv_weigh_scores_kernel<2, F8>
+         : tiles == 3 ? pkv_weigh_scores_kernel<3, F8>
                       : pkv_weigh_scores_kernel<4, F8>;
 }
 
@@ -547,6 +568,11 @@ ScoresKernel add_kernel(int tiles, int quads) {
 // Blocks of the scores kernel on an SM: what its launch bounds ask for.
 int scores_ctas(int tiles) { return tiles == 1 ? 2 : 1; }
 
+// A batch of few pages is spread over all warps page by page.
+int head_units(const DeviceInfo& dev, const pkv_desc& d, int64_t num_keys) {
+  return num_keys / kPage * d.num_kv_heads > int64_t(dev.sm_count) * 64 ? kHeadUnits : 0;
+}
+
 int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int32_t max_rows, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
   const int64_t most = int64_t(dev.sm_count) * scores_ctas(column_tiles(small_rows(d, max_rows)));
@@ -556,7 +582,7 @@ int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int32_t max_rows, int6
 
 int add_grid(const DeviceInfo& dev, const pkv_desc& d, int tiles, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
-  const int64_t most = int64_t(dev.sm_count) * (tiles == 4 ? 2 : 4), want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
+  const int64_t most = int64_t(dev.sm_count) * (tiles > 2 ? 2 : 4), want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
   return int(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -569,11 +595,14 @@ WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
     off = align_up(off + bytes, 256);
     return at;
   };
+  if (!has_small(d, num_seqs, num_tokens, max_rows)) {
+    w.total = weigh_tc_workspace_bytes(dev, d, num_seqs, num_tokens, num_keys);
+    return w;
+  }
   const int64_t rows = small_rows(d, max_rows);
   const size_t slots = size_t(num_seqs) * d.num_kv_heads +
                        size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
-  w.plan = take(2 * (size_t(num_seqs) + 1) * sizeof(int64_t));
-  w.records = take(slots * 8 * column_tiles(rows) * sizeof(float2));
+  w.records = take(slots * record_columns(column_tiles(rows)) * sizeof(float2));
   w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * size_t(most_quads(rows)) * sizeof(float4));
   w.many = off;
   if (has_many(d, max_rows)) take(weigh_tc_workspace_bytes(dev, d, num_seqs, num_tokens, num_keys));
@@ -596,21 +625,24 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
   const int64_t rows = small_rows(d, a.max_rows);
   const int tiles = column_tiles(rows);
   const int grid = scores_grid(*ctx.dev, d, a.max_rows, a.num_keys);
-  SmallParams p{a,
-                reinterpret_cast<int64_t*>(ws + w.plan),
-                reinterpret_cast<float2*>(ws + w.records),
-                reinterpret_cast<float4*>(ws + w.scores),
-                a.num_keys / kPage * d.num_kv_heads,
-                int32_t(rows),
-                grid * kWsWarps};
-  if (int e = launch(ctx, fp8 ? scores_kernel<true>(tiles) : scores_kernel<false>(tiles), dim3(unsigned(grid)),
-                     kWsThreads, p))
-    return e;
-  if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)), dim3(unsigned(add_grid(*ctx.dev, d, tiles, a.num_keys))),
-                     kWsThreads, p))
-    return e;
+  const bool small = has_small(d, a.num_seqs, a.num_tokens, a.max_rows);
+  if (small) {
+    const SmallParams p{a,
+                        reinterpret_cast<float2*>(ws + w.records),
+                        reinterpret_cast<float4*>(ws + w.scores),
+                        a.num_keys / kPage * d.num_kv_heads * kPage * most_quads(rows),
+                        int32_t(rows),
+                        head_units(*ctx.dev, d, a.num_keys),
+                        grid * kWsWarps};
+    if (int e = launch(ctx, fp8 ? scores_kernel<true>(tiles) : scores_kernel<false>(tiles), dim3(unsigned(grid)),
+                       kWsThreads, p))
+      return e;
+    if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)),
+                       dim3(unsigned(add_grid(*ctx.dev, d, tiles, a.num_keys))), kWsThreads, p))
+      return e;
+  }
   if (!has_many(d, a.max_rows)) return PKV_OK;
-  return launch_weigh_tc(ctx, a, fp8, int32_t(rows), ws + w.many);
+  return launch_weigh_tc(ctx, a, fp8, small ? int32_t(rows) : 0, ws + w.many);
 }
 
 }  // namespace pkv

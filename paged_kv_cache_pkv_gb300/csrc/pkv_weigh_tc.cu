@@ -80,7 +80,7 @@ struct Item {
 
 struct TcParams {
   WeighArgs a;
-  int32_t small_rows;          // rows x heads that are the few-rows kernels'
+  int32_t small_rows;          // rows x heads that are the few-rows kernels'; 0: they are not launched
   int64_t max_items1, max_items2;
   int64_t* totals;             // [2]: items of pass 1, of pass 2
   Item *items1, *items2;
@@ -310,9 +310,10 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using S = Smem<F8>;
   constexpr int kN = kRing<F8>;
-  // Planned while the kernel before still runs: it is one of this call's, which
-  // has itself waited for what came before the call, and writes none of the
+  // Planned while the kernel before still runs, where that is one of this call's:
+  // it has itself waited for what came before the call, and writes none of the
   // arrays read here; no kernel before reads this pass's total any more.
+  if (PASS == 1 && p.small_rows == 0) griddep_wait();
   Walk<PASS> w;
   int64_t left = 0;
   bool idle;
