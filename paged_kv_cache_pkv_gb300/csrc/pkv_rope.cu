@@ -66,11 +66,13 @@ __device__ __forceinline__ Pair16 to_bf16(const float (&o)[16]) {
   return r;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 x = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 y = __ldg(reinterpret_cast<const float4*>(p) + 1);
+__device__ __forceinline__ void spread(const float4& x, const float4& y, float (&v)[8]) {
   v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
   v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  spread(__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1), v);
 }
 
 // Vectors of unit j of a row: the first `units` units are rotated, the rest
@@ -99,36 +101,18 @@ __device__ __forceinline__ uint2 to_e4m3(const float* o, float inv) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// Cosines and sines of unit j of a token with a position on each of several
-// axes: pair 8j + i comes from its own axis's row of the table.  A unit of a
-// block of pairs reads one row; where axes take turns it reads as many as it
-// has, from L2 and once for all heads that the thread handles (4099 tokens of
-// 32 + 8 heads, three axes in turn: 26.4 us a call, 3.9 TB/s).
-__device__ __forceinline__ void load_axes(const RopeWriteArgs& p, const int64_t (&pos)[PKV_MAX_AXES], int j,
-                                          float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int a = 0; a < PKV_MAX_AXES; ++a) {
-    const uint32_t mine = uint32_t(p.axis_pairs[a] >> (8 * j)) & 0xFFu;
-    if (mine == 0) continue;  // also every axis from num_axes on
-    const float* row = p.cos_sin + pos[a] * p.rotary_dim + 8 * j;
-    float ca[8], sa[8];
-    load8(row, ca);
-    load8(row + p.rotary_dim / 2, sa);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (mine >> i & 1u) {
-        c[i] = ca[i];
-        s[i] = sa[i];
-      }
-    }
-  }
-}
-
 // One block handles one token at a time (blockIdx.x) and the share
 // blockIdx.y of its rows: query heads (if any), K heads, V heads.  Eight
-// threads a row, one unit each.  AXES: several positions a token.
+// threads a row, one unit each.
+// AXES, several positions a token: a thread a pair reads the entries of its
+// pair's axis, and the block's rows have them from shared memory; the next
+// token's are on their way while this one's rows are turned.  (Read by every
+// thread for itself, axes in turn took three rows' vectors a unit: 4099 tokens of
+// 32 + 8 heads 21.5 us between others in a graph, 14.3 as it is.)  Its blocks are
+// bound to the registers of as many as the grid has an SM: 21.5 -> 16.8 us from
+// cold caches.
 template <bool F8, bool AXES>
-__global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const RopeWriteArgs p) {
+__global__ void __launch_bounds__(kRopeThreads, AXES ? (F8 ? 8 : 9) : 1) pkv_write_rope_kernel(const RopeWriteArgs p) {
   // What the stream did before: the projections, and calls that read the pools.
   griddep_wait();
   constexpr int kUnits = kHeadDim / 16;  // 8
@@ -141,18 +125,55 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
   const int step = gridDim.y * kRows;
   int va, vb;
   unit_vectors(j, units, p.interleaved != 0, va, vb);
-  for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    int64_t pos[AXES ? PKV_MAX_AXES : 1];
-    pos[0] = __ldg(p.positions + t);
-    bool bad_pos = pos[0] < 0 || pos[0] >= p.max_position;
-    if constexpr (AXES) {
-#pragma unroll
-      for (int a = 1; a < PKV_MAX_AXES; ++a) {
-        pos[a] = a < p.num_axes ? __ldg(p.positions + a * p.position_stride + t) : 0;
-        bad_pos = bad_pos || pos[a] < 0 || pos[a] >= p.max_position;
-      }
+  // AXES: thread i reads positions, cosine and sine for pair i, threads behind the
+  // pairs the positions of the axes once more (one may have no pair).
+  __shared__ float4 table[AXES ? 2 : 1][AXES ? 2 : 1][AXES ? kHeadDim / 8 : 1];  // [by turns][cosines, sines]
+  const int half = p.rotary_dim / 2;
+  const int64_t* axis_pos = nullptr;
+  int64_t pos_ahead = 0, slot_ahead = AXES ? __ldg(p.slots + blockIdx.x) : 0;
+  float cos_ahead = 0.f, sin_ahead = 0.f;
+  bool bad_ahead = false;
+  auto look_up = [&] {  // the table's entries at pos_ahead
+    bad_ahead = axis_pos && (pos_ahead < 0 || pos_ahead >= p.max_position);
+    if (int(threadIdx.x) < half && !bad_ahead) {
+      const float* row = p.cos_sin + pos_ahead * p.rotary_dim + threadIdx.x;
+      cos_ahead = __ldg(row);
+      sin_ahead = __ldg(row + half);
     }
-    const int64_t slot = __ldg(p.slots + t);
+  };
+  if constexpr (AXES) {
+    int axis = int(threadIdx.x) - half;
+    if (axis < 0)
+      for (axis = 0; !(p.axis_pairs[axis] >> threadIdx.x & 1); ++axis) {}
+    if (axis < p.num_axes) axis_pos = p.positions + axis * p.position_stride;
+    if (axis_pos) pos_ahead = __ldg(axis_pos + blockIdx.x);
+    look_up();
+    const int64_t next = blockIdx.x + int64_t(gridDim.x);
+    if (axis_pos && next < p.num_tokens) pos_ahead = __ldg(axis_pos + next);
+  }
+  int turn_of = 0;
+  for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x, turn_of ^= 1) {
+    int64_t pos = 0, slot;
+    bool bad_pos;
+    if constexpr (AXES) {
+      slot = slot_ahead;
+      if (int(threadIdx.x) < half) {
+        reinterpret_cast<float*>(table[turn_of][0])[threadIdx.x] = cos_ahead;
+        reinterpret_cast<float*>(table[turn_of][1])[threadIdx.x] = sin_ahead;
+      }
+      // (one barrier a token: the buffer is written again two tokens on)
+      bad_pos = __syncthreads_or(bad_ahead);
+      const int64_t next = t + int64_t(gridDim.x);
+      if (next < p.num_tokens) {
+        slot_ahead = __ldg(p.slots + next);
+        look_up();
+        if (axis_pos && next + gridDim.x < p.num_tokens) pos_ahead = __ldg(axis_pos + next + gridDim.x);
+      }
+    } else {
+      pos = __ldg(p.positions + t);
+      bad_pos = pos < 0 || pos >= p.max_position;
+      slot = __ldg(p.slots + t);
+    }
     const int64_t page = slot / kPage;
     const int r = int(slot % kPage);
     const bool store = slot >= 0 && page < p.num_blocks && !bad_pos;
@@ -165,9 +186,10 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_rope_kernel(const Rope
     float c[8], s[8];
     if (rotated) {
       if constexpr (AXES) {
-        load_axes(p, pos, j, c, s);
+        spread(table[turn_of][0][2 * j], table[turn_of][0][2 * j + 1], c);
+        spread(table[turn_of][1][2 * j], table[turn_of][1][2 * j + 1], s);
       } else {
-        const float* row = p.cos_sin + pos[0] * p.rotary_dim;
+        const float* row = p.cos_sin + pos * p.rotary_dim;
         load8(row + 8 * j, c);
         load8(row + p.rotary_dim / 2 + 8 * j, s);
       }
@@ -290,8 +312,8 @@ __global__ void __launch_bounds__(kRopeThreads) pkv_write_latent_kernel(const La
 // Blocks over tokens, and over the rows of a token while there are few
 // tokens: as many as are resident at once (nine of 128 threads an SM; 16 a SM
 // took 34.2 us for 8191 tokens of 32 + 8 heads, 9 take 33.1).
-dim3 token_grid(const DeviceInfo& dev, int64_t tokens, int rows, int rows_per_block) {
-  const int64_t want = int64_t(dev.sm_count) * 9;
+dim3 token_grid(const DeviceInfo& dev, int64_t tokens, int rows, int rows_per_block, int blocks_per_sm = 9) {
+  const int64_t want = int64_t(dev.sm_count) * blocks_per_sm;
   const int64_t gx = tokens < want ? tokens : want;
   const int most = (rows + rows_per_block - 1) / rows_per_block;
   int64_t gy = want / gx;
@@ -322,7 +344,8 @@ int launch(const LaunchCtx& ctx, void (*kernel)(Args), dim3 grid, const Args& ar
 
 int launch_write_rope(const LaunchCtx& ctx, const RopeWriteArgs& a, bool fp8) {
   const int rows = (a.q ? a.num_q_heads : 0) + 2 * a.num_kv_heads;
-  const dim3 grid = token_grid(*ctx.dev, a.num_tokens, rows, kRopeThreads / (kHeadDim / 16));
+  // (with several axes on E4M3 pages eight are)
+  const dim3 grid = token_grid(*ctx.dev, a.num_tokens, rows, kRopeThreads / (kHeadDim / 16), fp8 && a.num_axes ? 8 : 9);
   if (a.num_axes)
     return launch(ctx, fp8 ? pkv_write_rope_kernel<true, true> : pkv_write_rope_kernel<false, true>, grid, a);
   return launch(ctx, fp8 ? pkv_write_rope_kernel<true, false> : pkv_write_rope_kernel<false, false>, grid, a);
