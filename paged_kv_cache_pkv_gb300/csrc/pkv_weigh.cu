@@ -97,7 +97,7 @@ __device__ __forceinline__ void plan_units(const SmallParams& p, int64_t* before
   // The first sequence that does not fit the workspace whole ends the list.
   __shared__ unsigned long long limit;
   if (threadIdx.x == 0) limit = ~0ull;
-  block_scan<kWsThreads>(sum, total, warp_sums);
+  block_scan<kWsThreads, 2>(sum, total, warp_sums);
   for (int b = b0; b < b1; ++b) {
     const int64_t units = before[b], q = quads[b];
     if (units > 0 && sum[1] + q > p.max_quads) {

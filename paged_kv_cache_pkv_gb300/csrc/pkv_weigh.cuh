@@ -28,28 +28,30 @@ __device__ __forceinline__ bool weigh_sequence(const WeighArgs& p, int b, WeighS
   return true;
 }
 
-// Exclusive prefix sums of two counts over the block's threads, in thread
-// order; the totals come back in `total`.
-template <int kThreads>
-__device__ __forceinline__ void block_scan(int64_t (&x)[2], int64_t (&total)[2], int64_t (*warp_sums)[2]) {
+// Exclusive prefix sums of N counts over the block's threads, in thread order;
+// the totals come back in `total`.
+template <int kThreads, int N>
+__device__ __forceinline__ void block_scan(int64_t (&x)[N], int64_t (&total)[N], int64_t (*warp_sums)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl[2] = {x[0], x[1]};
+  int64_t incl[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) incl[i] = x[i];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl[i], o);
       if (lane >= o) incl[i] += v;
     }
   }
   if (lane == 31) {
-    warp_sums[warp][0] = incl[0];
-    warp_sums[warp][1] = incl[1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) warp_sums[warp][i] = incl[i];
   }
   __syncthreads();
   static_assert(kThreads <= 1024, "a lane a warp");
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < N; ++i) {
     int64_t sums = lane < kThreads / 32 ? warp_sums[lane][i] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

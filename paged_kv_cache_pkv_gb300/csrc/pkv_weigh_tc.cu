@@ -140,12 +140,15 @@ struct Shape {
   }
 };
 
-// A place in the order of units, and the walk from piece to piece.
+// A place in the order of units, and the walk from piece to piece: forward in pass
+// 1, backward in pass 2, whose first pairs then are the last keys that pass 1
+// read, of which L2 still holds a part.
 template <int PASS>
 struct Walk {
   Shape<PASS> s;
-  int b, q0, g, pair, at;  // at: first unit of the piece within the pair
-  int64_t item, item1;     // of this pass; of pass 1 at the sequence's start
+  int b, q0, g, pair;
+  int at;               // pass 1: the piece's first unit in the pair; pass 2: the one behind its last
+  int64_t item, item1;  // of this pass; of pass 1 at the sequence's start
 
   __device__ __forceinline__ bool load(const TcParams& p) {
     WeighSequence x;
@@ -155,35 +158,54 @@ struct Walk {
     q0 = x.q0;
     return true;
   }
-  // Units of this piece when `left` remain in the CTA's share.
-  __device__ __forceinline__ int count(int64_t left) const { return int(min(left, int64_t(s.units(pair) - at))); }
+  // Units of this piece when `left` remain in the CTA's share, and its first.
+  __device__ __forceinline__ int count(int64_t left) const {
+    return int(min(left, int64_t(PASS == 1 ? s.units(pair) - at : at)));
+  }
+  __device__ __forceinline__ int first(int count) const { return PASS == 1 ? at : at - count; }
   __device__ __forceinline__ void next(const TcParams& p, int64_t left) {
-    at = 0;
-    ++item;
-    if (++pair < s.items()) return;
-    pair = 0;
-    if (++g < p.a.desc.num_kv_heads) return;
-    g = 0;
-    item1 += int64_t(s.row_pairs()) * p.a.desc.num_kv_heads;
-    ++b;
-    if (left > 0)
-      while (b < p.a.num_seqs && !load(p)) ++b;
+    const int Hkv = p.a.desc.num_kv_heads;
+    if constexpr (PASS == 1) {
+      at = 0;
+      ++item;
+      if (++pair < s.items()) return;
+      pair = 0;
+      if (++g < Hkv) return;
+      g = 0;
+      item1 += int64_t(s.row_pairs()) * Hkv;
+      ++b;
+      if (left > 0)
+        while (b < p.a.num_seqs && !load(p)) ++b;
+    } else {
+      --item;
+      if (--pair < 0) {
+        if (--g < 0) {
+          g = Hkv - 1;
+          --b;
+          if (left <= 0) return;
+          while (b >= 0 && !load(p)) --b;
+          item1 -= int64_t(s.row_pairs()) * Hkv;
+        }
+        pair = s.items() - 1;
+      }
+      at = s.units(pair);
+    }
   }
 };
 
-// This CTA's share [u0, u1) and its first place, the same in every thread.
+// This CTA's share of units, and its first place, the same in every thread.
 // Sequences beyond the workspace are left out and flagged.  `scratch`: 3 x
-// (kMaxSeqs + 1) + 2 x warps + 1 int64 in shared memory.
+// (kMaxSeqs + 1) + 3 x warps + 1 int64 in shared memory.
 template <int PASS, int kThreads>
 __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch, Walk<PASS>& w, int64_t& share,
                                             bool& idle) {
-  const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads;
+  const int B = p.a.num_seqs, Hkv = p.a.desc.num_kv_heads, lane = threadIdx.x & 31;
   int64_t *units = scratch, *items1 = scratch + kMaxSeqs + 1, *items2 = items1 + kMaxSeqs + 1;
-  auto* warp_sums = reinterpret_cast<int64_t (*)[2]>(items2 + kMaxSeqs + 1);
+  auto* warp_sums = reinterpret_cast<int64_t (*)[3]>(items2 + kMaxSeqs + 1);
   auto* limit = reinterpret_cast<unsigned long long*>(warp_sums + kThreads / 32);
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(B, int(threadIdx.x) * per), b1 = min(B, b0 + per);
-  int64_t items[2] = {0, 0}, total[2];
+  int64_t sum[3] = {0, 0, 0}, total[3];  // units, items of pass 1, of pass 2
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     WeighSequence x;
@@ -194,71 +216,69 @@ __device__ __forceinline__ void plan_shares(const TcParams& p, int64_t* scratch,
     if (v.load(p)) {
       u = v.s.all() * Hkv;
       i1 = int64_t(v.s.row_pairs()) * Hkv;
-      i2 = int64_t((v.s.L + kPair - 1) / kPair) * Hkv;
+      i2 = int64_t((v.s.L - 1) / kPair + 1) * Hkv;
     }
     units[b] = u;
     items1[b] = i1;
     items2[b] = i2;
-    items[0] += i1;
-    items[1] += i2;
+    sum[0] += u;
+    sum[1] += i1;
+    sum[2] += i2;
   }
   if (threadIdx.x == 0) limit[0] = B;
-  block_scan<kThreads>(items, total, warp_sums);
-  int64_t r1 = items[0], r2 = items[1];
+  block_scan<kThreads, 3>(sum, total, warp_sums);
   for (int b = b0; b < b1; ++b) {
-    const int64_t i1 = items1[b], i2 = items2[b];
-    if (i1 > 0 && (r1 + i1 > p.max_items1 || r2 + i2 > p.max_items2)) {
+    const int64_t u = units[b], i1 = items1[b], i2 = items2[b];
+    if (i1 > 0 && (sum[1] + i1 > p.max_items1 || sum[2] + i2 > p.max_items2)) {
       atomicMin(limit, static_cast<unsigned long long>(b));
       bad = true;
     }
-    items1[b] = r1;
-    items2[b] = r2;
-    r1 += i1;
-    r2 += i2;
+    units[b] = sum[0];
+    items1[b] = sum[1];
+    items2[b] = sum[2];
+    sum[0] += u;
+    sum[1] += i1;
+    sum[2] += i2;
   }
   if (threadIdx.x == 0) {
-    items1[B] = total[0];
-    items2[B] = total[1];
+    units[B] = total[0];
+    items1[B] = total[1];
+    items2[B] = total[2];
   }
   if (PASS == 1 && bad && blockIdx.x == 0) flag_status(p.a.status, PKV_STATUS_BAD_QUERY);
   __syncthreads();
   const int end = int(limit[0]);  // sequences that count
-  int64_t mine[2] = {0, 0};
-  for (int b = b0; b < min(b1, end); ++b) mine[0] += units[b];
-  block_scan<kThreads>(mine, total, warp_sums);
-  int64_t run = mine[0];
-  for (int b = b0; b < b1; ++b) {
-    const int64_t u = b < end ? units[b] : 0;
-    units[b] = run;
-    run += u;
-  }
-  if (threadIdx.x == 0) units[B] = total[0];
   if (blockIdx.x == 0 && threadIdx.x == 0) p.totals[PASS - 1] = PASS == 1 ? items1[end] : items2[end];
-  __syncthreads();
-  const int64_t U = units[B], ctas = min(int64_t(gridDim.x), U);
+  const int64_t U = units[end], ctas = min(int64_t(gridDim.x), U);
   idle = int64_t(blockIdx.x) >= ctas;
   if (!idle) {
     int64_t rest;
     const int64_t u0 = divide(int64_t(blockIdx.x) * U, ctas, rest);
-    share = divide((int64_t(blockIdx.x) + 1) * U, ctas, rest) - u0;
-    int lo = 0, hi = B;  // last sequence with units[b] <= u0: it has units
+    const int64_t u1 = divide((int64_t(blockIdx.x) + 1) * U, ctas, rest);
+    share = u1 - u0;
+    const int64_t from = PASS == 1 ? u0 : u1 - 1;
+    int lo = 0, hi = end;  // last sequence with units[b] <= from: it has units
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (units[mid] <= u0) lo = mid;
+      if (units[mid] <= from) lo = mid;
       else hi = mid;
     }
     w.b = lo;
     w.load(p);
     int64_t rem;
-    w.g = int(divide(u0 - units[lo], w.s.all(), rem));
-    int first = 0, last = w.s.items();  // last pair with before(pair) <= rem
-    while (last - first > 1) {
-      const int mid = (first + last) >> 1;
-      if (w.s.before(mid) <= rem) first = mid;
-      else last = mid;
+    w.g = int(divide(from - units[lo], w.s.all(), rem));
+    // last pair with before(pair) <= rem, a warp's lanes trying 32 places at a time
+    int first = 0, span = w.s.items();
+    while (span > 1) {
+      const int step = (span + 31) >> 5;
+      const int mid = first + lane * step;
+      const uint32_t below = __ballot_sync(0xffffffffu, lane * step < span && w.s.before(mid) <= rem);
+      const int last = 31 - __clz(below);  // lane 0's holds always
+      first += last * step;
+      span = min(step, span - last * step);
     }
     w.pair = first;
-    w.at = int(rem - w.s.before(first));
+    w.at = int(rem - w.s.before(first)) + (PASS == 1 ? 0 : 1);
     w.item1 = items1[lo];
     w.item = (PASS == 1 ? items1[lo] : items2[lo]) + int64_t(w.g) * w.s.items() + first;
   }
@@ -472,12 +492,13 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     int j = 0;
     while (left > 0 && ok) {
       const int count = w.count(left);
+      const int at = w.first(count);
       Entry next{-1, false};
-      if constexpr (PASS == 1) next = entry_of(w, w.at);
+      if constexpr (PASS == 1) next = entry_of(w, at);
       for (int u = 0; u < count; ++u, ++j) {
         if constexpr (PASS == 1) {
           const int now = page_id(next);
-          if (u + 1 < count) next = entry_of(w, w.at + u + 1);  // read a tile ahead
+          if (u + 1 < count) next = entry_of(w, at + u + 1);  // read a tile ahead
           const int valid = __popc(__ballot_sync(0xffffffffu, now >= 0));
           if constexpr (F8) {
             const int st = j & 1;
@@ -496,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           const int slot = j % kN;
           if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
           if (lane == 0) {
-            const int tile = w.s.first_row_tile(w.pair) + w.at + u;
+            const int tile = w.s.first_row_tile(w.pair) + at + u;
             mbar_arrive_expect_tx(ring_full + slot, kTileBytes);
             copy_rows(sm + S::ring + slot * kTileBytes, w, tile << w.s.log_tokens, ring_full + slot);
           }
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     while (left > 0 && ok) {
       const int count = w.count(left);
       const float* src = p.lse + (w.item1 + int64_t(w.g) * w.s.row_pairs()) * kPair +
-                         int64_t(w.s.first_row_tile(w.pair) + w.at) * kTile;
+                         int64_t(w.s.first_row_tile(w.pair) + w.first(count)) * kTile;
       for (int u = 0; u < count; ++u, ++j) {
         const int slot = j % kLseRing;
         if (j >= kLseRing && !(ok = wait_all(lse_free + slot, (j / kLseRing - 1) & 1))) break;
@@ -602,7 +623,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           for (int u = 0; u < count; ++u, ++j) {
             const int slot = j % kN;
             if (j >= kN && !(ok = wait_all(ring_free + slot, (j / kN - 1) & 1))) break;
-            if (!(ok = widen(sm + S::ring + slot * kTileBytes, w, w.at + u))) break;
+            if (!(ok = widen(sm + S::ring + slot * kTileBytes, w, w.first(count) + u))) break;
             if (lane == 0) mbar_arrive(ring_full + slot);
           }
         } else {
@@ -627,7 +648,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     const uint64_t qs2 = f2(a.qscale, a.qscale);
     int j = 0, done[2] = {0, 0};
     while (left > 0 && ok) {
-      const int count = w.count(left), tiles = tiles_of(w);
+      const int count = w.count(left), at = w.first(count), tiles = tiles_of(w);
       float m[2] = {kWeighNoScore, kWeighNoScore}, sum[2] = {0.f, 0.f};
       // Pass 1: keys up to the row's last one, from the piece's first tile and
       // this quarter on.  Pass 2: the token, from the piece's first row tile on,
@@ -638,10 +659,10 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int token = ((2 * w.pair + x) << w.s.log_tokens) + (r >> shift);
-          seen[x] = (token < w.s.n ? w.s.context + token + 1 : INT32_MAX) - w.at * kTile - quarter * 32;
+          seen[x] = (token < w.s.n ? w.s.context + token + 1 : INT32_MAX) - at * kTile - quarter * 32;
         }
       } else {
-        const int token = (w.s.first_row_tile(w.pair) + w.at) << w.s.log_tokens;
+        const int token = (w.s.first_row_tile(w.pair) + at) << w.s.log_tokens;
         seen[0] = w.pair * kPair + r - w.s.context - token;
         seen[1] = seen[0] + kTile;
         end = w.s.n - token;
@@ -741,22 +762,22 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         if constexpr (PASS == 2) end -= 1 << w.s.log_tokens;
       }
       if (!ok) break;
-      const int64_t at = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
+      const int64_t record = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (x >= tiles) break;
-        if constexpr (PASS == 1) p.records1[at + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
-        else p.records2[at + x * kTile] = sum[x];
+        if constexpr (PASS == 1) p.records1[record + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
+        else p.records2[record + x * kTile] = sum[x];
       }
       if (tid == 0) {
         Item& item = (PASS == 1 ? p.items1 : p.items2)[w.item];
-        if (w.at == 0) {
+        if (at == 0) {
           item.b = w.b;
           item.g = w.g;
           item.pair = w.pair;
           item.first = int(blockIdx.x);
         }
-        if (w.at + count == w.s.units(w.pair)) item.last = int(blockIdx.x);
+        if (at + count == w.s.units(w.pair)) item.last = int(blockIdx.x);
       }
       left -= count;
       w.next(p, left);
