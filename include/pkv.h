@@ -170,9 +170,10 @@ PKV_API int pkv_attend_workspace_size(const pkv_desc* desc, int32_t num_seqs,
  * prefetch hints for the first pages) overlaps the write kernel through
  * programmatic dependent launch; the pools are read only after the write has
  * finished.  Those three arrays must therefore not be written by a kernel
- * right before the call that lets its dependents start early: no call of this
- * library writes them, and a kernel of the caller's that does must leave out
- * that early start (griddepcontrol.launch_dependents).
+ * right before the call that lets its dependents start early: of this
+ * library's only pkv_evict writes one of them (new lengths), and it does not,
+ * and a kernel of the caller's that does must leave out that early start
+ * (griddepcontrol.launch_dependents).
  * A call may be captured into a graph and replayed with other values in its
  * arrays, lengths among them; num_seqs, num_tokens and max_query_len stay those
  * of the capture.  It then ends with one or two small memory sets of its

@@ -464,12 +464,13 @@ int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache, const int
   return launch_attend_latent(ctx, a);
 }
 
-// Rows, units of work and keys are counted in 64 bits on the device, tokens and
-// positions in 32.
+// Units of work and keys are counted in 64 bits on the device, tokens, positions
+// and rows of the pool in 32.
 static int check_weigh(const pkv_desc* d, int32_t num_seqs, int32_t num_tokens) {
   if (int e = check_desc(d)) return e;
   if (num_seqs < 0 || num_seqs > PKV_MAX_SEQS || num_tokens < 0 || num_tokens > INT32_MAX - 1024)
     return PKV_ERR_RANGE;
+  if (int64_t(d->num_blocks) * d->num_kv_heads >= (int64_t(1) << 31) / kPage) return PKV_ERR_RANGE;
   return check_positions(d);
 }
 

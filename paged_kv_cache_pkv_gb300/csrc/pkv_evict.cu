@@ -33,6 +33,9 @@
 // and head on bf16 pages); on few tokens the chain of steps 1 to 3.
 #include <cooperative_groups.h>
 
+#include <atomic>
+#include <mutex>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 
@@ -403,7 +406,8 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int 
 }
 
 // Everything read here may be the work of the kernel before.  No early start for
-// the one behind: pkv_attend reads lengths before it waits, and these are new.
+// the one behind a kernel that writes new lengths: pkv_attend reads lengths before
+// it waits.
 
 // A CTA an item, selection and move.
 template <bool F8>
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_select_kernel(const 
   griddep_wait();
   const int rank = blockIdx.x % cluster;
   Cut x;
-  if (!cut_of(p, blockIdx.x / cluster, list_stride, rank == 0, x) || x.c == 0) return;  // the whole cluster
+  if (!cut_of(p, blockIdx.x / cluster, list_stride, false, x) || x.c == 0) return;  // the whole cluster
   select_tokens<kBigThreads>(p, x, cluster, rank, *reinterpret_cast<EvictShared<kBigThreads>*>(smem_raw));
 }
 
@@ -437,7 +441,7 @@ __global__ void __launch_bounds__(kBigThreads, 1) pkv_evict_move_kernel(const Ev
   griddep_wait();
   const int rank = blockIdx.x % cluster, part = blockIdx.x / cluster;
   Cut x;
-  if (!cut_of(p, part / 2, list_stride, false, x)) return;
+  if (!cut_of(p, part / 2, list_stride, rank == 0 && part % 2 == 0, x)) return;
   move_rows<F8, kBigThreads, false>(p, x, cluster, rank, part % 2);
 }
 
@@ -470,9 +474,11 @@ struct Resident {
 template <bool F8>
 const Resident* resident(int device) {
   static Resident facts[64];
-  static bool done[64] = {};
+  static std::atomic<bool> done[64] = {};
+  static std::mutex asking;
   if (device < 0 || device >= 64) return nullptr;
-  if (!done[device]) {
+  if (!done[device].load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(asking);
     auto set = [](auto kernel, size_t smem) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess &&
              cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
@@ -494,7 +500,7 @@ const Resident* resident(int device) {
       }
       facts[device].most[i++] = n;
     }
-    done[device] = true;
+    done[device].store(true, std::memory_order_release);
   }
   return &facts[device];
 }

@@ -28,6 +28,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "pkv_tcgen05.cuh"
@@ -876,15 +877,15 @@ TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
 
 template <int PASS, bool F8>
 int ensure_attr(int device) {
-  static bool done[64] = {};
+  static std::atomic<bool> done[64] = {};
   if (device < 0 || device >= 64) return PKV_ERR_DEVICE;
-  if (!done[device]) {
+  if (!done[device].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(pkv_weigh_tc_kernel<PASS, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(Smem<F8>::total)) != cudaSuccess) {
       cudaGetLastError();
       return PKV_ERR_LAUNCH;
     }
-    done[device] = true;
+    done[device].store(true, std::memory_order_release);
   }
   return PKV_OK;
 }

@@ -59,6 +59,7 @@ def _weigh(lib, fp8=False, desc=None, B=4, T=4, most=0, keys=0, scale=0.1, decay
     (dict(scores=FAKE + 4), ALIGN), (dict(ws=FAKE + 128), ALIGN), (dict(first=FAKE + 2), ALIGN),
     (dict(scored=FAKE + 2), ALIGN), (dict(desc=pkv.Desc(64, 16, 2, 8, 64, 16)), SHAPE),
     (dict(desc=pkv.Desc(64, 16, 2, 12, 128, 16)), SHAPE), (dict(desc=pkv.Desc(64, 16, 2, 8, 128, 1 << 27)), RANGE),
+    (dict(desc=pkv.Desc(1 << 26, 16, 2, 8, 128, 16)), RANGE),
 ])
 def test_weigh_refuses(pkvlib, fp8, bad, code):
     before = pkvlib.pkv_launch_count()
@@ -265,6 +266,49 @@ def test_weigh_bounds_that_do_not_hold_are_flagged(pkvlib):
     touched = (bound > 0) & ~second[:, None, None]
     assert (np.abs(got - want)[touched] <= bound[touched]).all()
     assert np.array_equal(got[second].view(np.uint32), x["scores"][second].view(np.uint32))
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 40])
+def test_weigh_keys_beyond_the_bound_are_flagged(pkvlib, rows):
+    """num_keys too small by far: what fits is right, the rest is left alone."""
+    pkv.get_last_error()
+    x = batch([600, 500, 700, 400], [rows] * 4, 8, 2, seed=20)
+    got = call(x, cuda(x), num_keys=608, max_query_len=rows)
+    assert pkv.get_last_error() == pkv.STATUS_BAD_QUERY
+    want, bound = E.weigh(x["q"], x["k"], x["scores"], x["tables"], x["lens"], x["qsl"], SCALE)
+    done = []
+    for b in range(4):
+        pages = x["tables"][b, :-(-x["lens"][b] // 16)]
+        same = np.array_equal(got[pages].view(np.uint32), x["scores"][pages].view(np.uint32))
+        touched = bound[pages] > 0
+        right = (np.abs(got[pages] - want[pages])[touched] <= bound[pages][touched]).all()
+        assert same or right
+        done.append(bool(right))
+    assert done[0] and not done[3]
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weigh_fewer_rows_than_a_capture_had(pkvlib, fp8):
+    """Captured where every sequence has the most rows (no kernels of few rows),
+    replayed with few rows, none, and padding behind the last sequence."""
+    x = batch([300, 64, 200], [40, 40, 40], 8, 2, seed=21, fp8=fp8)
+    d = cuda(x)
+    (pkv.weigh_fp8 if fp8 else pkv.weigh)(scale=SCALE, max_query_len=40, **cuda(x))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (pkv.weigh_fp8 if fp8 else pkv.weigh)(scale=SCALE, max_query_len=40, **d)
+    graph.replay()
+    torch.cuda.synchronize()
+    compare(x, d["scores"].cpu().numpy())
+    qsl = np.array([0, 1, 1, 38], np.int32)
+    y = dict(x, qsl=qsl, scores=d["scores"].cpu().numpy())
+    d["query_start_loc"].copy_(torch.from_numpy(qsl))
+    graph.replay()
+    torch.cuda.synchronize()
+    compare(y, d["scores"].cpu().numpy())
+    assert pkv.get_last_error() == 0
 
 
 @gpu
