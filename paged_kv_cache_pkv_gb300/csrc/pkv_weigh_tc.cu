@@ -24,7 +24,8 @@
 // scores.  A row tile is left out where causality hides the whole key pair.
 //
 // E4M3 pages: TMA lands a tile's codes and scale bytes in a staging area, four
-// warps widen them to bf16 (exact, scale included).
+// warps widen them to bf16 (exact, scale included).  What they and the epilogue
+// issue together is what bounds it.
 #include <cuda.h>
 
 #include <algorithm>
@@ -33,7 +34,6 @@
 
 #include "pkv_tcgen05.cuh"
 #include "pkv_weigh.cuh"
-#include "pkv_widen.cuh"
 
 namespace pkv {
 namespace {
@@ -315,6 +315,47 @@ __device__ __forceinline__ void umma_tile(uint32_t tmem_d, uint64_t a, uint64_t 
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n\t}" ::"r"(tmem_d),
       "l"(a), "l"(b), "r"(idesc), "r"(smem_u32(bar))
       : "memory");
+}
+
+// ---- E4M3 tiles ------------------------------------------------------------------
+
+// Two codes in the high bytes of w's halves, as bf16 times 2^120: the exponent
+// field is the code's, so codes without one are bf16 without one.
+__device__ __forceinline__ uint32_t as_bf16(uint32_t w) { return ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Half a row of a staged page, dims 64h .. 64h + 63 of row r times 2^(scale - 127),
+// as bf16 into row `out` of the half-h block of a tile (both 128-byte swizzled):
+// codes to exponent fields by shifts, one product by a power of two (exact, also
+// for codes without an exponent).  The upper half's lanes start two pieces on, so
+// that a quarter-warp's stores are on banks of their own.
+__device__ __forceinline__ void widen_half(const uint8_t* page, uint32_t scale, uint8_t* out, int r, int h) {
+  // 2^(scale - 127 + 120), in two steps where that is beyond bf16 (scales above 134)
+  const uint32_t s1 = min(scale, 134u), more = scale - s1;
+  const uint32_t m1 = ((s1 + 120u) << 7) * 0x00010001u, m2 = ((more + 127u) << 7) * 0x00010001u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = k ^ (2 * h);
+    const uint4 v = *reinterpret_cast<const uint4*>(page + r * 128 + (((4 * h + i) ^ (r & 7)) << 4));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[2 * j] = mul_bf16x2(as_bf16(__byte_perm(w[j], 0u, 0x1404u)), m1);
+      o[2 * j + 1] = mul_bf16x2(as_bf16(__byte_perm(w[j], 0u, 0x3424u)), m1);
+    }
+    if (more) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = mul_bf16x2(o[j], m2);
+    }
+    *reinterpret_cast<uint4*>(out + (((2 * i) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(out + (((2 * i + 1) ^ (r & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 
 // ---- the two passes ------------------------------------------------------------
@@ -610,8 +651,8 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
 #pragma unroll 1
         for (int k = mine; k < kTilePages; k += kWidenWarps)
           if (key_tile * kTilePages + k < pages)
-            widen_row_half(codes + k * kStagePage, scales[k * kScaleBytes + r],
-                           tile + h * kHalf + (k * kPage + r) * 128, r, h);
+            widen_half(codes + k * kStagePage, scales[k * kScaleBytes + r],
+                       tile + h * kHalf + (k * kPage + r) * 128, r, h);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(stage_free + st);
@@ -669,19 +710,23 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         end = w.s.n - token;
       }
       for (int u = 0; u < count; ++u, ++j) {
-        uint64_t lse[PASS == 2 ? 16 : 1];
+        // (E4M3 blocks have registers for one tile's scores only: read for each)
+        constexpr bool kHold = PASS == 2 && !F8;
+        uint64_t lse[kHold ? 16 : 1];
+        const ulonglong2* sums = nullptr;
         if constexpr (PASS == 2) {
           if (!(ok = wait_all(lse_full + j % kLseRing, (j / kLseRing) & 1))) break;
-          const ulonglong2* n = reinterpret_cast<const ulonglong2*>(
-              sm + S::lse + ((j % kLseRing) * kTile + quarter * 32) * 4);
+          sums = reinterpret_cast<const ulonglong2*>(sm + S::lse + ((j % kLseRing) * kTile + quarter * 32) * 4);
+          if constexpr (kHold) {
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const ulonglong2 x = n[c];
-            lse[2 * c] = x.x;
-            lse[2 * c + 1] = x.y;
+            for (int c = 0; c < 8; ++c) {
+              const ulonglong2 x = sums[c];
+              lse[2 * c] = x.x;
+              lse[2 * c + 1] = x.y;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lse_free + j % kLseRing);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(lse_free + j % kLseRing);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -742,8 +787,11 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
             } else {
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
+                uint64_t n;
+                if constexpr (kHold) n = lse[c >> 1];
+                else n = reinterpret_cast<const uint64_t*>(sums)[c >> 1];
                 float e0, e1;
-                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, lse[c >> 1]), e0, e1);
+                f2_split(f2_fma(f2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), qs2, n), e0, e1);
                 if constexpr (MASKED) {
                   if (!counts(c)) e0 = -INFINITY;
                   if (!counts(c + 1)) e1 = -INFINITY;
@@ -760,7 +808,13 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           else if (!none) add(std::true_type{});
         }
         if (!ok) break;
-        if constexpr (PASS == 2) end -= 1 << w.s.log_tokens;
+        if constexpr (PASS == 2) {
+          end -= 1 << w.s.log_tokens;
+          if constexpr (!kHold) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lse_free + j % kLseRing);
+          }
+        }
       }
       if (!ok) break;
       const int64_t record = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
