@@ -478,9 +478,12 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  *                  sequence with more rows is skipped and flags
  *                  PKV_STATUS_BAD_QUERY.
  *   num_keys       host-side upper bound on the sum of the seq_lens, each
- *                  rounded up to 16, or <= 0 if unknown (then the block tables'
- *                  width bounds them): it sizes the workspace.  Where it does
- *                  not hold, sequences that do not fit are skipped and flag
+ *                  rounded up to 16, or <= 0 if unknown: it sizes the
+ *                  workspace.  Unknown, the tokens of the pool bound them (and
+ *                  of the tables' width), which holds unless sequences share
+ *                  so many pages that together they name more than the pool
+ *                  has: such a batch passes it.  Where the bound does not hold,
+ *                  sequences that do not fit are skipped and flag
  *                  PKV_STATUS_BAD_QUERY.
  *   workspace      at least pkv_weigh_workspace_size bytes for the same
  *                  num_seqs, num_tokens, max_query_len and num_keys, 256-byte

@@ -469,7 +469,7 @@ def attend_latent(q, latent_cache, block_tables, seq_lens, query_start_loc, scal
 
 def workspace_size_weigh(desc, num_seqs, num_tokens, device=None, max_query_len=0, num_keys=0):
     """Workspace bytes weigh and weigh_fp8 need for the same max_query_len and
-    num_keys (0 = unknown: what num_tokens and the tables' width allow)."""
+    num_keys (0 = unknown: what num_tokens and the pool allow)."""
     n = _sz(0)
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         _check(lib().pkv_weigh_workspace_size(ctypes.byref(desc), int(num_seqs), int(num_tokens), int(max_query_len),
@@ -487,7 +487,9 @@ def weigh(q, k_cache, scores, block_tables, seq_lens, query_start_loc, scale, de
     step's own) have none yet.  The ``first`` tokens of a sequence (int32 [B])
     get none.  ``max_query_len`` and ``num_keys`` (the sum of the lengths, each
     rounded up to 16) are host-side bounds, 0 = unknown.  They must hold (what
-    does not fit is skipped and flagged); they keep the workspace small."""
+    does not fit is skipped and flagged); they keep the workspace small.
+    Sequences that share pages and together hold more tokens than the pool has
+    need ``num_keys``."""
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).weigh(index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
                                          scale, decay, first, scored, workspace, max_query_len, num_keys)

@@ -478,9 +478,11 @@ static int check_weigh(const pkv_desc* d, int32_t num_seqs, int32_t num_tokens) 
 static int32_t most_rows(int32_t max_query_len, int32_t num_tokens) {
   return max_query_len > 0 ? std::min(max_query_len, num_tokens) : num_tokens;
 }
+// (A pool's tokens bound the keys of sequences that share no more pages than are
+// free; others pass num_keys.)
 static int64_t most_keys(const pkv_desc* d, int32_t num_seqs, int64_t num_keys) {
   const int64_t top = int64_t(num_seqs) * d->max_blocks_per_seq * kPage;
-  return num_keys > 0 ? std::min(num_keys, top) : top;
+  return std::min(num_keys > 0 ? num_keys : int64_t(d->num_blocks) * kPage, top);
 }
 
 int pkv_weigh_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,

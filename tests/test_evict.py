@@ -169,6 +169,16 @@ def test_evict_a_batch_of_long_sequences_on_single_ctas(pkvlib):
 
 
 @gpu
+@pytest.mark.parametrize("hi", [40, 150])
+def test_evict_most_sequences(pkvlib, hi):
+    """As many sequences as a call takes."""
+    rng = np.random.default_rng(hi)
+    lens = rng.integers(0, hi, size=2048)
+    x = batch(lens, 1, seed=hi, kind="ties")
+    check(x, rng.integers(0, hi, size=2048), rng.integers(0, 9, size=2048), 4)
+
+
+@gpu
 def test_evict_keeps_a_shared_prefix_where_it_is(pkvlib):
     """Two sequences share their first two pages, 32 first tokens."""
     x = batch([100, 132], 2, seed=5)

@@ -289,6 +289,38 @@ def test_weigh_keys_beyond_the_bound_are_flagged(pkvlib, rows):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [1, 40])
+def test_weigh_sequences_on_a_shared_prefix(pkvlib, rows):
+    """Six sequences share 15 pages, their first tokens: together more tokens
+    than the pool has, which num_keys says."""
+    pkv.get_last_error()
+    x = batch([300, 290, 310, 260, 300, 281], [rows] * 6, 8, 2, seed=22)
+    own = np.unique(np.concatenate([x["tables"][0, :19]] + [x["tables"][b, 15:-(-x["lens"][b] // 16)] for b in range(6)]))
+    x["tables"][1:, :15] = x["tables"][0, :15]
+    renumber = np.full(x["k"].shape[0] + 1, len(own), np.int32)
+    renumber[own] = np.arange(len(own))
+    x["tables"] = renumber[x["tables"]]
+    x["k"], x["scores"] = x["k"][own], x["scores"][own]
+    keys = int((-(-x["lens"] // 16)).sum()) * 16
+    assert keys > x["k"].shape[0] * 16
+    check(x, first=[240] * 6, num_keys=keys, max_query_len=rows)
+    d = cuda(x)
+    call(x, d, first=torch.full((6,), 240, dtype=torch.int32, device="cuda"), max_query_len=rows)
+    assert pkv.get_last_error() in (0, pkv.STATUS_BAD_QUERY)  # the pool's tokens do not bound them
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weigh_most_sequences(pkvlib, fp8):
+    """As many sequences as a call takes, a few with a window of rows."""
+    rng = np.random.default_rng(23)
+    lens = rng.integers(1, 40, size=2048)
+    rows = np.where(rng.random(2048) < 0.02, np.minimum(lens, 30), np.minimum(lens, rng.integers(0, 3, size=2048)))
+    x = batch(lens, rows, 4, 1, seed=23, fp8=fp8)
+    check(x, decay=0.5)
+
+
+@gpu
 @pytest.mark.parametrize("fp8", [False, True])
 def test_weigh_fewer_rows_than_a_capture_had(pkvlib, fp8):
     """Captured where every sequence has the most rows (no kernels of few rows),
