@@ -22,7 +22,10 @@
 //    in flight as registers allow.  Each lane keeps running maxima and sums of its own
 //    keys, reduced over lanes once a piece.  Scores go to the workspace, 4
 //    bytes a (row, key), a key's rounded up to 16: at one row of four heads a
-//    sixteenth of K's bytes, and mostly read back from L2.
+//    sixteenth of K's bytes, and mostly read back from L2.  Four rows' scores of
+//    a page's 16 keys lie together, so that both kernels touch whole sectors (a
+//    key's scores together: 8 rows of 4 heads 134 us, now 117; 2 to 5 rows 87,
+//    now 84, and 81 since the second kernel has a form for 24 rows).
 //  * pkv_weigh_add_kernel: joins the pieces' sums and turns scores into
 //    weights, one key a lane, with the update of the paged score.  Its work is
 //    little and its reads depend on one another, so all that do not are on
@@ -44,6 +47,8 @@
 // Sequences of more rows go to the tensor cores (pkv_weigh_tc.cu).
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "pkv_weigh.cuh"
 
 namespace pkv {
@@ -63,7 +68,7 @@ struct WeighLayout {
 struct SmallParams {
   WeighArgs a;
   float2* records;  // [items + warps][columns]: (maximum, sum) of a piece
-  float4* scores;   // of each sequence [units][16][quads]
+  float4* scores;   // of each sequence [pages of its kv heads][quads][16 keys]
   int64_t max_quads;
   int32_t small_rows;   // rows x heads of a sequence that they take
   int32_t head_units;   // kHeadUnits or 0
@@ -184,8 +189,24 @@ struct KeyPage {
 // Width of the records of a call with NT MMA tiles of columns.
 __host__ __device__ constexpr int record_columns(int NT) { return NT == 3 ? 32 : 8 * NT; }
 
+// E4M3 pages against two or three tiles of rows: the rows' fragments wait in
+// shared memory, 2 KB a tile and warp, so that 16 warps an SM widen codes instead
+// of eight (32 sequences of 256 to 8192 tokens, 12 rows a kv head 57 -> 53 us, 8
+// to 20 rows 73 -> 63).  Four tiles (104 -> 103 us) and bf16 pages (three tiles,
+// 82 -> 80), bound by their bytes, would gain too little for another path.
+__host__ __device__ constexpr bool fragments_shared(int NT, bool F8) { return F8 && (NT == 2 || NT == 3); }
+__host__ __device__ constexpr size_t fragment_bytes(int NT, bool F8) {
+  return fragments_shared(NT, F8) ? size_t(NT) * kWsWarps * 2048 : 0;
+}
+// Blocks of the scores kernel on an SM; kScoresCtas at most.
+constexpr int kScoresCtas = 2;
+__host__ __device__ constexpr int scores_ctas(int NT, bool F8) { return NT == 1 || fragments_shared(NT, F8) ? 2 : 1; }
+
 template <int NT, bool F8>
-__global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_kernel(const SmallParams p) {
+__global__ void __launch_bounds__(kWsThreads, scores_ctas(NT, F8)) pkv_weigh_scores_kernel(const SmallParams p) {
+  constexpr bool kShared = fragments_shared(NT, F8);
+  extern __shared__ uint4 fragments[];  // [warp][tile][4][lane]: of two k-steps
+  uint4* const frag = fragments + (threadIdx.x >> 5) * NT * 128 + (threadIdx.x & 31);
   __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
   __shared__ int64_t warp_sums[kWsWarps][2];
   griddep_wait();
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
   if (u >= end) return;
   constexpr int kPieces = KeyPage<F8>::kPieces;
   // Pages of a warp in flight: 64 to 128 KB an SM.
-  constexpr int kDeep = F8 ? (NT == 2 || NT == 3 ? 6 : 4) : NT == 2 ? 4 : NT == 3 ? 3 : 2;
+  constexpr int kDeep = F8 ? (kShared ? 2 : 4) : NT == 2 ? 4 : NT == 3 ? 3 : 2;
   constexpr int kPieceBytes = 64;        // of a row, between a lane's pieces
   constexpr int kRowBytes = F8 ? kHeadDim : 2 * kHeadDim;
   int b = sequence_at(before, B, u);
@@ -215,9 +236,11 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     const int taken = int(min(end - u, pages + p.head_units - rest));
     const int first = max(0, int(rest) - p.head_units), count = max(0, int(rest) + taken - p.head_units) - first;
     const int rows = s.n * G;  // the group's rows, j * G + h
-    const int stride = 4 * quads_of(rows);
-    float* const scores = reinterpret_cast<float*>(p.scores + quads_before[b]) +
-                          ((int64_t(g) * pages + first) * kPage + row) * stride + 2 * t;
+    const int quads = quads_of(rows);
+    // the lane's two columns of its first key: half of quad t / 2
+    float* const scores = reinterpret_cast<float*>(p.scores + quads_before[b] +
+                                                   ((int64_t(g) * pages + first) * quads + (t >> 1)) * kPage + row) +
+                          2 * (t & 1);
     float2* const rec = p.records + (int64_t(b) * Hkv + g + warp) * record_columns(NT) + 2 * t;
     if (count == 0) {  // the head's first units alone
 #pragma unroll
@@ -229,7 +252,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     }
 
     // ---- the rows, as B fragments: lane's column row, its elements as in a key ----
-    uint32_t qf[NT][8][2];
+    uint32_t qf[kShared ? 1 : NT][8][2];
     float unscale[NT][2];  // E4M3: of the lane's two score columns
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -270,11 +293,16 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
           for (int i = 0; i < 8; ++i) {  // words of two elements
             const uint32_t w = word(v[c][i >> 2], i & 3);
             const __half2 h = __floats2half2_rn(bf_lo(w) * up, bf_hi(w) * up);
-            qf[nt][c * 4 + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+            qf[kShared ? 0 : nt][c * 4 + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
         unscale[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
         unscale[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      }
+      if constexpr (kShared) {  // each lane reads what it wrote
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          frag[(nt * 4 + c) * 32] = make_uint4(qf[0][2 * c][0], qf[0][2 * c][1], qf[0][2 * c + 1][0], qf[0][2 * c + 1][1]);
       }
     }
     float m[NT][2], l[NT][2];
@@ -314,6 +342,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
     };
     auto weigh_page = [&](const KeyPage<F8>& k, int i) {
       float d[NT][4];
+      uint4 pair[NT];  // fragments of two k-steps
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
 #pragma unroll
@@ -328,12 +357,19 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
           a1 = word(k.hi[ks >> 1], w), a3 = word(k.hi[ks >> 1], w + 1);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          if (NT == 1 || nt * 8 < rows) mma16816<F8>(d[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          if (NT > 1 && nt * 8 >= rows) continue;
+          if constexpr (kShared) {
+            if ((ks & 1) == 0) pair[nt] = frag[(nt * 4 + (ks >> 1)) * 32];
+            mma16816<F8>(d[nt], a0, a1, a2, a3, word(pair[nt], 2 * (ks & 1)), word(pair[nt], 2 * (ks & 1) + 1));
+          } else {
+            mma16816<F8>(d[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        }
       }
       const int key = (first + i) * kPage + row;
       const bool edge = (first + i) * kPage + kPage - 1 > s.L - s.n;  // some row does not see all of the page
-      float* out = scores + int64_t(i) * kPage * stride;
+      float* out = scores + int64_t(i) * quads * (4 * kPage);
       float klo = 1.f, khi = 1.f;
       if constexpr (F8) {
         klo = __uint_as_float(k.sc_lo << 23);
@@ -360,9 +396,9 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
           d[nt][j] = x;
           d[nt][2 + j] = y;
         }
-        if (nt * 8 + 2 * t < stride) {
-          *reinterpret_cast<float2*>(out + nt * 8) = make_float2(d[nt][0], d[nt][1]);
-          *reinterpret_cast<float2*>(out + 8 * stride + nt * 8) = make_float2(d[nt][2], d[nt][3]);
+        if (nt * 2 + (t >> 1) < quads) {
+          *reinterpret_cast<float2*>(out + nt * (8 * kPage)) = make_float2(d[nt][0], d[nt][1]);
+          *reinterpret_cast<float2*>(out + nt * (8 * kPage) + 8 * 4) = make_float2(d[nt][2], d[nt][3]);
         }
       }
     };
@@ -403,7 +439,7 @@ __global__ void __launch_bounds__(kWsThreads, NT == 1 ? 2 : 1) pkv_weigh_scores_
 // Scores -> weights -> paged scores.  QUADS: most score quads of a key; COLUMNS:
 // the records' width.
 template <int QUADS, int COLUMNS>
-__global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_kernel(const SmallParams p) {
+__global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : QUADS == 6 ? 3 : 4) pkv_weigh_add_kernel(const SmallParams p) {
   __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
   __shared__ int64_t warp_sums[kWsWarps][2];
   const WeighArgs& a = p.a;
@@ -471,7 +507,8 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
     }
 
     // ---- a key a lane ----
-    const float4* src = p.scores + quads_before[b] + ((int64_t(g) * pages + first) * kPage + lane) * quads;
+    const float4* src = p.scores + quads_before[b] +
+                        (int64_t(g) * pages + first + (lane >> 4)) * quads * kPage + (lane & 15);
     for (int i = 0; i < count; i += 2 * kDeep) {
       int64_t at[kDeep];
       float old[kDeep];
@@ -486,7 +523,7 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
           old[d] = key < scored ? __ldcg(a.scores + at[d]) : 0.f;
 #pragma unroll
           for (int c = 0; c < QUADS; ++c)
-            if (c < quads) x[d][c] = __ldcg(src + int64_t(i + 2 * d) * kPage * quads + c);
+            if (c < quads) x[d][c] = __ldcg(src + (int64_t(i + 2 * d) * quads + c) * kPage);
         }
         ids[d] = entry_of(i + 2 * (kDeep + d));
       }
@@ -512,13 +549,14 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : 4) pkv_weigh_add_
 
 // Launched while the kernel before may still run, if that lets it.
 template <class... Params, class... Args>
-int launch(const LaunchCtx& ctx, void (*kernel)(Params...), dim3 grid, int threads, const Args&... args) {
+int launch(const LaunchCtx& ctx, void (*kernel)(Params...), int grid, size_t smem, const Args&... args) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kWsThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = ctx.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -551,42 +589,60 @@ bool has_small(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int32_t 
   return !has_many(d, max_rows) || int64_t(num_seqs) * max_rows != num_tokens;
 }
 
-using ScoresKernel = void (*)(SmallParams);
+using AddKernel = void (*)(SmallParams);
 
-template <bool F8>
-ScoresKernel scores_kernel(int tiles) {
-  return tiles == 1   ? pkv_weigh_scores_kernel<1, F8>
-         : tiles == 2 ? pkv_weigh_scores_kernel<2, F8>
-         : tiles == 3 ? pkv_weigh_scores_kernel<3, F8>
-                      : pkv_weigh_scores_kernel<4, F8>;
-}
-
-ScoresKernel add_kernel(int tiles, int quads) {
+AddKernel add_kernel(int tiles, int quads) {
   return quads == 1   ? pkv_weigh_add_kernel<1, 8>
          : quads == 2 ? pkv_weigh_add_kernel<2, 8>
+         : tiles == 3 ? pkv_weigh_add_kernel<6, 32>
          : tiles == 2 ? pkv_weigh_add_kernel<4, 16>
                       : pkv_weigh_add_kernel<8, 32>;
 }
-
-// Blocks of the scores kernel on an SM: what its launch bounds ask for.
-int scores_ctas(int tiles) { return tiles == 1 ? 2 : 1; }
 
 // A batch of few pages is spread over all warps page by page.
 int head_units(const DeviceInfo& dev, const pkv_desc& d, int64_t num_keys) {
   return num_keys / kPage * d.num_kv_heads > int64_t(dev.sm_count) * 64 ? kHeadUnits : 0;
 }
 
-int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int32_t max_rows, int64_t num_keys) {
+int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int ctas, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
-  const int64_t most = int64_t(dev.sm_count) * scores_ctas(column_tiles(small_rows(d, max_rows)));
+  const int64_t most = int64_t(dev.sm_count) * ctas;
   const int64_t want = (units + kWsWarps - 1) / kWsWarps;
   return int(want < 1 ? 1 : want < most ? want : most);
 }
 
 int add_grid(const DeviceInfo& dev, const pkv_desc& d, int tiles, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
-  const int64_t most = int64_t(dev.sm_count) * (tiles > 2 ? 2 : 4), want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
+  const int64_t most = int64_t(dev.sm_count) * (tiles == 4 ? 2 : tiles == 3 ? 3 : 4);
+  const int64_t want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
   return int(want < 1 ? 1 : want < most ? want : most);
+}
+
+template <int NT, bool F8>
+int launch_scores(const LaunchCtx& ctx, int grid, const SmallParams& p) {
+  constexpr size_t smem = fragment_bytes(NT, F8);
+  if constexpr (smem > 0) {  // beside the static arrays more than a kernel has unasked
+    static std::atomic<bool> done[64] = {};
+    const int device = ctx.dev->device;
+    if (device < 0 || device >= 64) return PKV_ERR_DEVICE;
+    if (!done[device].load(std::memory_order_acquire)) {
+      if (cudaFuncSetAttribute(pkv_weigh_scores_kernel<NT, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               int(smem)) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_LAUNCH;
+      }
+      done[device].store(true, std::memory_order_release);
+    }
+  }
+  return launch(ctx, pkv_weigh_scores_kernel<NT, F8>, grid, smem, p);
+}
+
+template <bool F8>
+int launch_scores(const LaunchCtx& ctx, int tiles, int grid, const SmallParams& p) {
+  return tiles == 1   ? launch_scores<1, F8>(ctx, grid, p)
+         : tiles == 2 ? launch_scores<2, F8>(ctx, grid, p)
+         : tiles == 3 ? launch_scores<3, F8>(ctx, grid, p)
+                      : launch_scores<4, F8>(ctx, grid, p);
 }
 
 WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int32_t max_rows,
@@ -604,7 +660,7 @@ WeighLayout layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   }
   const int64_t rows = small_rows(d, max_rows);
   const size_t slots = size_t(num_seqs) * d.num_kv_heads +
-                       size_t(scores_grid(dev, d, max_rows, num_keys)) * kWsWarps;
+                       size_t(scores_grid(dev, d, kScoresCtas, num_keys)) * kWsWarps;
   w.records = take(slots * record_columns(column_tiles(rows)) * sizeof(float2));
   w.scores = take(size_t(num_keys / kPage) * d.num_kv_heads * kPage * size_t(most_quads(rows)) * sizeof(float4));
   w.many = off;
@@ -627,7 +683,7 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int64_t rows = small_rows(d, a.max_rows);
   const int tiles = column_tiles(rows);
-  const int grid = scores_grid(*ctx.dev, d, a.max_rows, a.num_keys);
+  const int grid = scores_grid(*ctx.dev, d, scores_ctas(tiles, fp8), a.num_keys);
   const bool small = has_small(d, a.num_seqs, a.num_tokens, a.max_rows);
   if (small) {
     const SmallParams p{a,
@@ -637,11 +693,8 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
                         int32_t(rows),
                         head_units(*ctx.dev, d, a.num_keys),
                         grid * kWsWarps};
-    if (int e = launch(ctx, fp8 ? scores_kernel<true>(tiles) : scores_kernel<false>(tiles), dim3(unsigned(grid)),
-                       kWsThreads, p))
-      return e;
-    if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)),
-                       dim3(unsigned(add_grid(*ctx.dev, d, tiles, a.num_keys))), kWsThreads, p))
+    if (int e = fp8 ? launch_scores<true>(ctx, tiles, grid, p) : launch_scores<false>(ctx, tiles, grid, p)) return e;
+    if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)), add_grid(*ctx.dev, d, tiles, a.num_keys), 0, p))
       return e;
   }
   if (!has_many(d, a.max_rows)) return PKV_OK;
