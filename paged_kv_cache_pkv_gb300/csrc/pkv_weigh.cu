@@ -10,9 +10,9 @@
 //
 // Few rows (up to kSmallRows query rows x heads of a kv head a sequence):
 // bound by the bytes of K, which are read once.  Between others in a graph: 64
-// sequences of 512 to 4096 tokens, 32 + 8 heads, 60 to 62 us (K alone 44 at the
-// copy rate; 5.8 TB/s while K streams); a long-tailed batch of 256 sequences on
-// E4M3 pages 242 us (1.17 GB; 200 us of them K at 5.6 TB/s).
+// sequences of 512 to 4096 tokens, 32 + 8 heads, 60 us (K alone 47 at the copy
+// rate; 6.0 TB/s while K streams); a long-tailed batch of 256 sequences on E4M3
+// pages 240 us (K 1.10 GB, 200 us of them at 5.5 TB/s).
 //  * pkv_weigh_scores_kernel: K pages against the rows on warp-level MMAs, the
 //    page's 16 keys as M, the rows as N (8, 16, 24 or 32).  A product of two
 //    vectors does not go by the order of their elements, so a lane takes 16
