@@ -21,7 +21,8 @@ __all__ = [
     "PkvError", "PkvUnavailable", "lib", "open_library", "library_path", "Desc", "write", "attend",
     "workspace_size", "get_last_error", "launch_count", "Trace", "PagePool", "KERNELS",
     "export_pages", "import_pages", "write_fp8", "attend_fp8", "workspace_size_fp8",
-    "write_rope", "write_rope_fp8", "write_rope_axes", "write_rope_axes_fp8", "rope_axes", "write_latent", "attend_latent", "workspace_size_latent",
+    "write_rope", "write_rope_fp8", "write_rope_axes", "write_rope_axes_fp8", "rope_axes",
+    "write_latent", "attend_latent", "workspace_size_latent",
     "weigh", "weigh_fp8", "workspace_size_weigh", "evict", "evict_fp8", "workspace_size_evict",
     "make_desc", "make_latent_desc", "Rope", "RopeAxes",
     "STATUS_BAD_SLOT", "STATUS_BAD_BLOCK", "STATUS_BAD_QUERY", "STATUS_TIMEOUT", "STATUS_BAD_POSITION",
