@@ -191,6 +191,15 @@ def test_weigh_row_counts(pkvlib, n):
 
 
 @gpu
+@pytest.mark.parametrize("n", [2, 3, 4, 5, 6, 7, 8, 9])
+def test_weigh_row_counts_fp8(pkvlib, n):
+    """Every number of MMA tiles of rows on E4M3 pages, fewer rows beside the most."""
+    x = batch([n + 700, n, 350, 17], [n, n, 1, 2], 8, 2, seed=50 + n, fp8=True)
+    check(x, max_query_len=n)
+    check(x, decay=0.5)
+
+
+@gpu
 @pytest.mark.parametrize("fp8", [False, True])
 def test_weigh_scores_kept_and_new(pkvlib, fp8):
     """first: no score is written; scored: what is held from there on is not
