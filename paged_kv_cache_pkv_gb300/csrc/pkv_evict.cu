@@ -32,7 +32,7 @@
 // and head on bf16 pages); on few tokens the chain of steps 1 to 3.  From cold
 // caches: one sequence of 131072 tokens cut to 32768, eight heads, bf16 pages, 74
 // us (selection 24, moves 50 at 5.3 TB/s); 64 sequences of 512 to 4096 tokens cut
-// to 1023, E4M3 pages, 69 us (moves at 4.8 TB/s).  With one kernel and a barrier
+// to 1023, E4M3 pages, 68 us (moves at 4.8 TB/s).  With one kernel and a barrier
 // a round the first took 213 us.
 #include <cooperative_groups.h>
 
@@ -365,11 +365,15 @@ __device__ __forceinline__ void move_rows(const EvictArgs& p, const Cut& x, int 
     next = token_of(base + 2 * round_rows + mine);
     const bool ahead = lowest >= f + base + round_rows;
     if (cluster > 1) lowest = lowest_of(base + round_rows);
-    uint4 v[kDeep];
+    // 0 and not undefined, so that the loads are predicated and not branched
+    // around, and in one kernel with the selection past L1: 240 sequences of 500
+    // tokens 144 -> 130 -> 124 us.  (Loads that stream, in kernels of their own:
+    // 30 sequences of 4000 tokens 64 us, 66 past L1.)
+    uint4 v[kDeep] = {};
 #pragma unroll
     for (int i = 0; i < kDeep; ++i) {
       const int64_t s = __shfl_sync(0xffffffffu, src, i * kSub + sub);
-      if (s >= 0) v[i] = __ldcs(pool + s * kVecs + vec);
+      if (s >= 0) v[i] = kBoth ? __ldcg(pool + s * kVecs + vec) : __ldcs(pool + s * kVecs + vec);
     }
     float score = 0.f;
     uint8_t ks = 0, vs = 0;
@@ -533,9 +537,10 @@ int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
   const int stride = list_stride(a.desc);
   cudaLaunchAttribute attr[2];
   // Many items with little to move each are better off with a CTA each of one
-  // kernel (us, one against two, 8 heads, bf16: 240 sequences of 500 tokens 144
-  // against 196, 60 of 500 48 against 59; but 8 of 500 23 against 17, 60 of 4000
-  // 142 against 118, on E4M3 pages 85 either way, 9 of 16000 253 against 71).
+  // kernel (us, one against two, 8 heads, bf16: 240 sequences of 500 tokens 122
+  // against 197, 60 of 500 42 against 58, 64 of 2000 115 against 119; but 8 of 500
+  // 19 against 17, 60 of 4000 121 against 117, on E4M3 pages 81 against 87, 9 of
+  // 16000 179 against 70).
   // So is a token a thread (4 sequences of at most 255 tokens: 7.0 against 8.9).
   if (tokens <= kSmallThreads || (items > 2 * ctx.dev->sm_count && tokens * (fp8 ? 1 : 2) <= 4096)) {
     const cudaLaunchConfig_t cfg =
