@@ -53,14 +53,16 @@ constexpr int kMaxCluster = 16;
 
 template <int kThreads>
 struct EvictShared {
-  static constexpr int kKeys = kThreads == kBigThreads ? 24576 : 8192;  // of a slice, held here
-  uint32_t hist[2][kBins];
+  // Keys of a slice that are held here: all that the kernel of 256 threads is
+  // launched for, four CTAs of it an SM.
+  static constexpr int kKeys = kThreads == kBigThreads ? 24576 : 4096;
+  uint32_t hist[3][kBins];  // of each pass
   // A cluster's counts, of each pass: every CTA has those of the pairs of bins
   // that are its own, pair i the CTA i % cluster's.
   uint32_t total[kThreads == kBigThreads ? 3 : 1][kThreads == kBigThreads ? kBins : 2];
   uint32_t keys[kKeys];
   uint32_t warp_sum[kThreads / 32], warp_eq[kThreads / 32];
-  uint32_t digit, rest;         // of the last selection pass
+  uint32_t digit, rest, whole;  // of the last selection pass
   uint32_t count_gt, count_eq;  // of this CTA's slice
 };
 
@@ -121,10 +123,6 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
                                               EvictShared<kThreads>& sh) {
   constexpr int kWarps = kThreads / 32, kKeys = EvictShared<kThreads>::kKeys;
   const cg::cluster_group cl = cg::this_cluster();
-  auto sync_all = [&] {
-    if (cluster > 1) cl.sync();
-    else __syncthreads();
-  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   // ---- this CTA's slice of the candidates, and their keys ----
@@ -133,14 +131,14 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
   const int token0 = x.f + s0;
   // (eight table reads, then eight score reads of a thread on their way at once)
   constexpr int kBatch = 8;
-  auto read_keys = [&](int i0, uint32_t (&key)[kBatch]) {
-    int page[kBatch];
-    float score[kBatch];
+  auto read_pages = [&](int i0, int (&page)[kBatch]) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * kThreads;
       page[k] = i < n ? __ldg(x.table + (token0 + i) / kPage) : 0;
     }
+  };
+  auto read_scores = [&](int i0, const int (&page)[kBatch], float (&score)[kBatch]) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * kThreads;
@@ -148,8 +146,6 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
       if (page[k] < 0 || page[k] >= p.desc.num_blocks) flag_status(p.status, PKV_STATUS_BAD_BLOCK);
       else if (i < n) score[k] = __ldcg(p.scores + pool_row(p, x.g, page[k], token0 + i));
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) key[k] = order_key(score[k]);
   };
   // a key beyond those that shared memory holds
   auto read_key = [&](int i) {
@@ -159,9 +155,12 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
   };
   auto key_at = [&](int i) { return i < kKeys ? sh.keys[i] : read_key(i); };
 
+  int page[kBatch];
+  read_pages(tid, page);
+
   // ---- the c-th largest key, digit by digit ----
   // The first digit is counted while the keys come in.
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
   if constexpr (kThreads == kBigThreads) {
     if (cluster > 1) {
       for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.total[0][0])[i] = 0;
@@ -170,31 +169,32 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
   }
   __syncthreads();
   for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
-    uint32_t key[kBatch];
-    read_keys(i0, key);
+    float score[kBatch];
+    read_scores(i0, page, score);
+    read_pages(i0 + kBatch * kThreads, page);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * kThreads;
       if (i < n) {
-        if (i < kKeys) sh.keys[i] = key[k];
-        atomicAdd(&sh.hist[0][key[k] >> 21], 1u);
+        const uint32_t key = order_key(score[k]);
+        if (i < kKeys) sh.keys[i] = key;
+        atomicAdd(&sh.hist[0][key >> 21], 1u);
       }
     }
   }
-  uint32_t prefix = 0, rest = uint32_t(x.c);
+  // threshold, rest: keys above it stay, and so many of those equal to it.
+  uint32_t threshold = 0, rest = uint32_t(x.c);
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    uint32_t* hist = sh.hist[pass & 1];
+    uint32_t* hist = sh.hist[pass];
     if (pass > 0) {
       const int above = pass == 1 ? 21 : 10;  // bits from here on are known
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
-      __syncthreads();
 #pragma unroll 4
       for (int i = tid; i < n; i += kThreads) {
         const uint32_t key = key_at(i);
-        if (key >> above == prefix >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
+        if (key >> above == threshold >> above) atomicAdd(&hist[(key >> shift) & mask], 1u);
       }
     }
     __syncthreads();
@@ -238,15 +238,22 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
         if (before < rest && rest <= before + bin[i]) {
           sh.digit = uint32_t(low + kPer - 1 - i);
           sh.rest = rest - before;
+          sh.whole = rest - before == bin[i];
         }
         before += bin[i];
       }
     }
     __syncthreads();
-    prefix |= sh.digit << shift;
+    threshold |= sh.digit << shift;
     rest = sh.rest;
+    // All keys of the bin stay: no more digits.  (Of a few thousand scores 22 bits
+    // part the last that stays from the next.  No key is 0.)
+    if (sh.whole) {
+      --threshold;
+      rest = 0;
+      break;
+    }
   }
-  const uint32_t threshold = prefix;  // rest: so many of the keys equal to it stay
 
   // ---- how many stay of the slices before ----
   // Warps take whole words of 32 candidates in order, a contiguous run each.
@@ -287,6 +294,7 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
     }
     gt_before += __reduce_add_sync(0xffffffffu, g_other);
     eq_before += __reduce_add_sync(0xffffffffu, e_other);
+    cluster_arrive();  // nothing of the other CTAs is read any more
   }
   // ---- the list, in order ----
 #pragma unroll 4
@@ -302,7 +310,8 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, 
     gt_before += __popc(gts);
     eq_before += __popc(eqs);
   }
-  sync_all();
+  if (cluster > 1) cluster_wait();
+  else __syncthreads();
 }
 
 // Step 4.  kBoth: K and V rows of the item together, the lanes of a row's first
@@ -536,13 +545,13 @@ int launch_evict(const LaunchCtx& ctx, const EvictArgs& a, bool fp8) {
   if (items * 2 * kMaxCluster > INT32_MAX) return PKV_ERR_RANGE;
   const int stride = list_stride(a.desc);
   cudaLaunchAttribute attr[2];
-  // Many items with little to move each are better off with a CTA each of one
-  // kernel (us, one against two, 8 heads, bf16: 240 sequences of 500 tokens 122
-  // against 197, 60 of 500 42 against 58, 64 of 2000 115 against 119; but 8 of 500
-  // 19 against 17, 60 of 4000 121 against 117, on E4M3 pages 81 against 87, 9 of
-  // 16000 179 against 70).
-  // So is a token a thread (4 sequences of at most 255 tokens: 7.0 against 8.9).
-  if (tokens <= kSmallThreads || (items > 2 * ctx.dev->sm_count && tokens * (fp8 ? 1 : 2) <= 4096)) {
+  // Items of few tokens are better off with a CTA each of one kernel where they
+  // fill the GPU (us, one kernel against two, 8 heads, bf16: 240 sequences of 500
+  // tokens 105 against 187, 64 of 2000 100 against 116, 60 of 4000 102 against 113,
+  // on E4M3 pages 63 against 82, 20 of 4000 48 against 50; but 16 of 4000 44
+  // against 38, 8 of 4000 38 against 29, 60 of 8000 210 against 197).  So are two
+  // tokens a thread (16 sequences of 500 13 against 18, 1 of 500 15 against 14).
+  if (tokens <= EvictShared<kSmallThreads>::kKeys && (items > ctx.dev->sm_count || tokens <= 2 * kSmallThreads)) {
     const cudaLaunchConfig_t cfg =
         config(attr, ctx.stream, items, 1, kSmallThreads, sizeof(EvictShared<kSmallThreads>));
     TraceScope ts(ctx.stream, PKV_K_EVICT);
