@@ -14,9 +14,10 @@
 //  2. The key of the c-th largest by radix selection, 11 + 11 + 10 bits from
 //     the top: a histogram of the keys that agree so far in every CTA, its
 //     counts added up through distributed shared memory (only those that are
-//     not 0 travel; all CTAs reading all histograms took half of the selection).  Attention weights spread over a
-//     few dozen powers of two, so the first digit, exponent and two bits of
-//     the mantissa, already parts them.
+//     not 0 travel; all CTAs reading all histograms took half of the selection).
+//     Attention weights spread over a few dozen powers of two, so the first
+//     digit, exponent and two bits of the mantissa, already parts them; where
+//     all of a bin stay, the digits behind it are not looked at.
 //  3. Keys above it stay; of those equal to it the lowest tokens, as many as
 //     are missing, counted over the slices in order.  The tokens that stay are
 //     listed in the workspace (4 bytes each beside 512 or 258 bytes that move).
@@ -30,9 +31,9 @@
 //
 // What bounds it: bytes, a row read and written once (2 x 512 bytes a token
 // and head on bf16 pages); on few tokens the chain of steps 1 to 3.  From cold
-// caches: one sequence of 131072 tokens cut to 32768, eight heads, bf16 pages, 74
-// us (selection 24, moves 50 at 5.3 TB/s); 64 sequences of 512 to 4096 tokens cut
-// to 1023, E4M3 pages, 68 us (moves at 4.8 TB/s).  With one kernel and a barrier
+// caches: one sequence of 131072 tokens cut to 32768, eight heads, bf16 pages, 73
+// us (selection 23, moves 50 at 5.3 TB/s); 64 sequences of 512 to 4096 tokens cut
+// to 1023, E4M3 pages, 55 us (moves at 5.8 TB/s).  With one kernel and a barrier
 // a round the first took 213 us.
 #include <cooperative_groups.h>
 
@@ -54,7 +55,9 @@ constexpr int kMaxCluster = 16;
 template <int kThreads>
 struct EvictShared {
   // Keys of a slice that are held here: all that the kernel of 256 threads is
-  // launched for, four CTAs of it an SM.
+  // launched for, four CTAs of it an SM (6144, which halve what they leave L1 for
+  // rows on their way: the E4M3 case above 66 us; two or three CTAs an SM of
+  // more registers: 60 sequences of 4000 tokens 74 us, 64 as it is).
   static constexpr int kKeys = kThreads == kBigThreads ? 24576 : 4096;
   uint32_t hist[3][kBins];  // of each pass
   // A cluster's counts, of each pass: every CTA has those of the pairs of bins
