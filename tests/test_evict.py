@@ -169,6 +169,29 @@ def test_evict_a_batch_of_long_sequences_on_single_ctas(pkvlib):
 
 
 @gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,hkv", [([4096, 4095, 2500, 300] + [40] * 36, 4), ([4096, 4095, 2500, 300], 2),
+                                      ([500, 512, 400, 33], 2), ([9000, 4097], 1)])
+@pytest.mark.parametrize("bits", [0, 6, 13, 24])
+def test_evict_scores_that_differ_late(pkvlib, lens, hkv, fp8, bits):
+    """Scores that agree but for their lowest bits (bits: how many), so that the
+    last that stays is told from the next by the third digit, the second or at
+    once, with all or a part of what shares a digit staying; on one kernel and two,
+    and at the longest tables of one."""
+    rng = np.random.default_rng(bits)
+    x = batch(lens, hkv, seed=bits + hkv, fp8=fp8)
+    low = rng.integers(0, 1 << bits, size=x["scores"].shape, dtype=np.uint32)
+    x["scores"] = (np.uint32(0x3E000000) + low).view(np.float32)
+    keep = [n // 3 for n in lens]
+    check(x, keep, [5] * len(lens), 11)
+    half = x["scores"].copy()  # exactly as many larger ones as stay, in the second half
+    for b, n in enumerate(lens):
+        j = np.arange(n - 11 - (n // 3 - 16), n - 11) if n // 3 > 16 else np.arange(0)
+        half[x["tables"][b, j // 16], :, j % 16] += np.float32(1.0)
+    check(dict(x, scores=half), keep, [5] * len(lens), 11)
+
+
+@gpu
 @pytest.mark.parametrize("hi", [40, 150])
 def test_evict_most_sequences(pkvlib, hi):
     """As many sequences as a call takes."""
