@@ -10,7 +10,7 @@
 //
 // Few rows (up to kSmallRows query rows x heads of a kv head a sequence):
 // bound by the bytes of K, which are read once.  Between others in a graph: 64
-// sequences of 512 to 4096 tokens, 32 + 8 heads, 60 us (K alone 47 at the copy
+// sequences of 512 to 4096 tokens, 32 + 8 heads, 58.5 us (K alone 47 at the copy
 // rate; 6.0 TB/s while K streams); a long-tailed batch of 256 sequences on E4M3
 // pages 240 us (K 1.10 GB, 200 us of them at 5.5 TB/s).
 //  * pkv_weigh_scores_kernel: K pages against the rows on warp-level MMAs, the
@@ -436,10 +436,16 @@ __global__ void __launch_bounds__(kWsThreads, scores_ctas(NT, F8)) pkv_weigh_sco
   }
 }
 
+// Blocks of the kernel below on an SM.  One or two quads a key: three, whose
+// registers let a lane have six or three keys on their way (decode 60.7 -> 59.3 us
+// against four blocks and four keys, drafts of two rows 63.7 -> 61.9; five or six
+// blocks spill: 63 and 72).
+__host__ __device__ constexpr int add_ctas(int quads) { return quads == 8 ? 2 : quads == 4 ? 4 : 3; }
+
 // Scores -> weights -> paged scores.  QUADS: most score quads of a key; COLUMNS:
 // the records' width.
 template <int QUADS, int COLUMNS>
-__global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : QUADS == 6 ? 3 : 4) pkv_weigh_add_kernel(const SmallParams p) {
+__global__ void __launch_bounds__(kWsThreads, add_ctas(QUADS)) pkv_weigh_add_kernel(const SmallParams p) {
   __shared__ int64_t before[kMaxSeqs + 1], quads_before[kMaxSeqs + 1];
   __shared__ int64_t warp_sums[kWsWarps][2];
   const WeighArgs& a = p.a;
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : QUADS == 6 ? 3 : 
     auto entry_of = [&](int i) {
       return i + (lane >> 4) < count ? __ldg(table + first + i + (lane >> 4)) : -1;
     };
-    constexpr int kDeep = QUADS >= 4 ? 1 : 4 / QUADS;  // 32 keys each, at a time
+    constexpr int kDeep = QUADS == 1 ? 6 : QUADS == 2 ? 3 : 1;  // 32 keys each, at a time
     int ids[kDeep];
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) ids[d] = entry_of(2 * d);
@@ -519,11 +525,12 @@ __global__ void __launch_bounds__(kWsThreads, QUADS == 8 ? 2 : QUADS == 6 ? 3 : 
         const bool live = i + 2 * d + (lane >> 4) < count && key >= from && key < s.L && ids[d] >= 0 &&
                           ids[d] < a.desc.num_blocks;  // flagged where its keys were read
         at[d] = live ? (int64_t(ids[d]) * Hkv + g) * kPage + (lane & 15) : -1;
-        if (live) {
-          old[d] = key < scored ? __ldcg(a.scores + at[d]) : 0.f;
+        old[d] = 0.f;
+        if (live && key < scored) old[d] = __ldcg(a.scores + at[d]);
 #pragma unroll
-          for (int c = 0; c < QUADS; ++c)
-            if (c < quads) x[d][c] = __ldcg(src + (int64_t(i + 2 * d) * quads + c) * kPage);
+        for (int c = 0; c < QUADS; ++c) {
+          x[d][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (live && c < quads) x[d][c] = __ldcg(src + (int64_t(i + 2 * d) * quads + c) * kPage);
         }
         ids[d] = entry_of(i + 2 * (kDeep + d));
       }
@@ -591,11 +598,14 @@ bool has_small(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int32_t 
 
 using AddKernel = void (*)(SmallParams);
 
-AddKernel add_kernel(int tiles, int quads) {
-  return quads == 1   ? pkv_weigh_add_kernel<1, 8>
+// QUADS of pkv_weigh_add_kernel for so many at most.
+int add_quads(int quads) { return quads <= 2 ? quads : quads <= 4 ? 4 : quads <= 6 ? 6 : 8; }
+
+AddKernel add_kernel(int quads) {
+  return quads <= 1   ? pkv_weigh_add_kernel<1, 8>
          : quads == 2 ? pkv_weigh_add_kernel<2, 8>
-         : tiles == 3 ? pkv_weigh_add_kernel<6, 32>
-         : tiles == 2 ? pkv_weigh_add_kernel<4, 16>
+         : quads == 4 ? pkv_weigh_add_kernel<4, 16>
+         : quads == 6 ? pkv_weigh_add_kernel<6, 32>
                       : pkv_weigh_add_kernel<8, 32>;
 }
 
@@ -611,9 +621,9 @@ int scores_grid(const DeviceInfo& dev, const pkv_desc& d, int ctas, int64_t num_
   return int(want < 1 ? 1 : want < most ? want : most);
 }
 
-int add_grid(const DeviceInfo& dev, const pkv_desc& d, int tiles, int64_t num_keys) {
+int add_grid(const DeviceInfo& dev, const pkv_desc& d, int quads, int64_t num_keys) {
   const int64_t units = num_keys / kPage * d.num_kv_heads;
-  const int64_t most = int64_t(dev.sm_count) * (tiles == 4 ? 2 : tiles == 3 ? 3 : 4);
+  const int64_t most = int64_t(dev.sm_count) * add_ctas(quads);
   const int64_t want = (units + 2 * kWsWarps - 1) / (2 * kWsWarps);
   return int(want < 1 ? 1 : want < most ? want : most);
 }
@@ -694,7 +704,8 @@ int launch_weigh(const LaunchCtx& ctx, const WeighArgs& a, bool fp8) {
                         head_units(*ctx.dev, d, a.num_keys),
                         grid * kWsWarps};
     if (int e = fp8 ? launch_scores<true>(ctx, tiles, grid, p) : launch_scores<false>(ctx, tiles, grid, p)) return e;
-    if (int e = launch(ctx, add_kernel(tiles, most_quads(rows)), add_grid(*ctx.dev, d, tiles, a.num_keys), 0, p))
+    const int quads = add_quads(most_quads(rows));
+    if (int e = launch(ctx, add_kernel(quads), add_grid(*ctx.dev, d, quads, a.num_keys), 0, p))
       return e;
   }
   if (!has_many(d, a.max_rows)) return PKV_OK;
