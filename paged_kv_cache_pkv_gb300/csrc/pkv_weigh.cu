@@ -19,8 +19,8 @@
 //    contiguous bytes of a key's row as its elements of two k-steps, and the
 //    queries' fragments are permuted alike: pages go from HBM to registers in
 //    16-byte loads, without shared memory or barriers, as many pages of a warp
-//    in flight as registers allow.  Each lane keeps running maxima and sums of its own
-//    keys, reduced over lanes once a piece.  Scores go to the workspace, 4
+//    in flight as registers allow.  Each lane keeps running maxima and sums of its
+//    own keys, reduced over lanes once a piece.  Scores go to the workspace, 4
 //    bytes a (row, key), a key's rounded up to 16: at one row of four heads a
 //    sixteenth of K's bytes, and mostly read back from L2.  Four rows' scores of
 //    a page's 16 keys lie together, so that both kernels touch whole sectors (a
@@ -35,7 +35,7 @@
 //    all warps alike.  In a batch of many pages a head's first page counts as
 //    kHeadUnits more: what begins a piece, queries, tables and the first pages'
 //    way, takes as long as that (a long-tailed batch of 256 sequences on 8-bit
-//    pages: 344 us without, 254, 244 and 239 with 4, 8 and 16).  Piece p of the row has the
+//    pages: 344 us without, 275, 246 and 242 with 4, 8 and 16).  A piece has the
 //    record (items before it + warps before it), unique as one of them grows
 //    from piece to piece.
 //  * E4M3 pages: codes become f16 exactly; the bf16 queries become f16 under a
@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kWsThreads, scores_ctas(NT, F8)) pkv_weigh_sco
       if constexpr (kShared) {  // each lane reads what it wrote
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          frag[(nt * 4 + c) * 32] = make_uint4(qf[0][2 * c][0], qf[0][2 * c][1], qf[0][2 * c + 1][0], qf[0][2 * c + 1][1]);
+          frag[(nt * 4 + c) * 32] =
+              make_uint4(qf[0][2 * c][0], qf[0][2 * c][1], qf[0][2 * c + 1][0], qf[0][2 * c + 1][1]);
       }
     }
     float m[NT][2], l[NT][2];

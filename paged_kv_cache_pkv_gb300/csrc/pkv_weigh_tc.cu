@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
   const int shift = 31 - __clz(G);
   // Tiles of the M side that the pair has.
   auto tiles_of = [&](const Walk<PASS>& x) {
-    return PASS == 1 ? ((x.s.n - 1) >> x.s.log_tokens > 2 * x.pair ? 2 : 1) : ((x.s.L - 1) / kTile > 2 * x.pair ? 2 : 1);
+    return (PASS == 1 ? (x.s.n - 1) >> x.s.log_tokens : (x.s.L - 1) / kTile) > 2 * x.pair ? 2 : 1;
   };
   // The table entry of this lane's page (lane < 8) of a key tile, -1 behind the
   // sequence; nothing here waits for it.
