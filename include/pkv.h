@@ -492,7 +492,8 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  * Sums and scores are fp32, in an order that goes by the call's shapes and
  * lengths alone: the same inputs give the same bits.  K rows and scores of
  * rows past a sequence's end are never used, whatever they hold; the rows of
- * its cached tokens and its queries must be finite. */
+ * its cached tokens and its queries must be finite.  Where a bounded wait runs
+ * out (PKV_STATUS_TIMEOUT), scores of the sequences it was for become NaN. */
 PKV_API int pkv_weigh_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens,
                                      int32_t max_query_len, int64_t num_keys, size_t* bytes);
 PKV_API int pkv_weigh(const pkv_bf16* q, const pkv_bf16* k_cache, float* scores,

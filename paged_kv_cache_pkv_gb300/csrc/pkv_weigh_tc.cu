@@ -505,14 +505,14 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
           const int valid = __popc(__ballot_sync(0xffffffffu, ids[u] >= 0));
           if (lane == 0) mbar_arrive_expect_tx(stage_full + st, uint32_t(valid) * (kStagePage + kScaleBytes));
           __syncwarp();
-          stage_page(st, ids[u], w.g);
+          if (!(kDropFirstCopy && staged == 0)) stage_page(st, ids[u], w.g);
         }
       } else {
         if (i >= 2 && !(ok = wait_all(pair_free + slot, ((i >> 1) - 1) & 1))) break;
         if constexpr (PASS == 1) {
           if (lane == 0) {
             mbar_arrive_expect_tx(pair_full + slot, uint32_t(tiles) * kTileBytes);
-            for (int u = 0; u < tiles; ++u)
+            for (int u = 0; u < (kDropFirstCopy && i == 0 ? 0 : tiles); ++u)
               copy_rows(dst + u * kTileBytes, w, (2 * w.pair + u) << w.s.log_tokens, pair_full + slot);
           }
         } else {
@@ -520,8 +520,10 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
                             __popc(__ballot_sync(0xffffffffu, ids[1] >= 0));
           if (lane == 0) mbar_arrive_expect_tx(pair_full + slot, uint32_t(valid) * 4096);
           __syncwarp();
-          copy_page(dst, ids[0], w.g, pair_full + slot);
-          copy_page(dst + kTileBytes, ids[1], w.g, pair_full + slot);
+          if (!(kDropFirstCopy && i == 0)) {
+            copy_page(dst, ids[0], w.g, pair_full + slot);
+            copy_page(dst + kTileBytes, ids[1], w.g, pair_full + slot);
+          }
         }
       }
       left -= count;
@@ -637,9 +639,13 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     if (ok) {
       ok = mbar_wait(pair_free + ((i - 1) & 1), ((i - 1) >> 1) & 1, kLandLimitNs) &&
            mbar_wait(ring_free + (j - 1) % kN, ((j - 1) / kN) & 1, kLandLimitNs);
-    } else if (done[last_tile] > 0) {
-      const int k = done[last_tile] - 1;
-      mbar_wait(s_full + 2 * last_tile + (k & 1), (k >> 1) & 1, kDrainLimitNs);
+    } else {
+      if (done[last_tile] > 0) {
+        const int k = done[last_tile] - 1;
+        mbar_wait(s_full + 2 * last_tile + (k & 1), (k >> 1) & 1, kDrainLimitNs);
+      }
+      if (j > 0) mbar_wait(ring_free + (j - 1) % kN, ((j - 1) / kN) & 1, kDrainLimitNs);
+      if (i > 0) mbar_wait(pair_free + ((i - 1) & 1), ((i - 1) >> 1) & 1, kDrainLimitNs);
     }
     if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
     __syncwarp();
@@ -695,6 +701,28 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     const int r = (warp & 3) * 32 + lane;  // TMEM lane: row or key of a tile
     const uint32_t columns = tmem + quarter * 32 + (uint32_t((warp & 3) * 32) << 16);
     const uint64_t qs2 = f2(a.qscale, a.qscale);
+    // A piece's sums and, of its first and its last piece, the item's place.
+    auto leave = [&](int count, int at, int tiles, const float (&m)[2], const float (&sum)[2]) {
+      const int64_t record = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x >= tiles) break;
+        if constexpr (PASS == 1) p.records1[record + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
+        else p.records2[record + x * kTile] = sum[x];
+      }
+      if (tid == 0) {
+        Item& item = (PASS == 1 ? p.items1 : p.items2)[w.item];
+        if (at == 0) {
+          item.b = w.b;
+          item.g = w.g;
+          item.pair = w.pair;
+          item.first = int(blockIdx.x);
+        }
+        if (at + count == w.s.units(w.pair)) item.last = int(blockIdx.x);
+      }
+      left -= count;
+      w.next(p, left);
+    };
     int j = 0, done[2] = {0, 0};
     while (left > 0 && ok) {
       const int count = w.count(left), at = w.first(count), tiles = tiles_of(w);
@@ -824,25 +852,16 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
         }
       }
       if (!ok) break;
-      const int64_t record = ((w.item + blockIdx.x) * 4 + quarter) * kPair + r;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (x >= tiles) break;
-        if constexpr (PASS == 1) p.records1[record + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
-        else p.records2[record + x * kTile] = sum[x];
-      }
-      if (tid == 0) {
-        Item& item = (PASS == 1 ? p.items1 : p.items2)[w.item];
-        if (at == 0) {
-          item.b = w.b;
-          item.g = w.g;
-          item.pair = w.pair;
-          item.first = int(blockIdx.x);
-        }
-        if (at + count == w.s.units(w.pair)) item.last = int(blockIdx.x);
-      }
-      left -= count;
-      w.next(p, left);
+      leave(count, at, tiles, m, sum);
+    }
+    // Once a wait has run out the sums of its piece and of those behind it are not
+    // numbers; their records and items are written all the same: the joining
+    // kernels go by what stands there, in a workspace that nobody initialised.
+    const float lost[2] = {__uint_as_float(0x7FC00000u), __uint_as_float(0x7FC00000u)}, none[2] = {0.f, 0.f};
+#pragma unroll 1
+    while (left > 0) {
+      const int count = w.count(left);
+      leave(count, w.first(count), tiles_of(w), none, lost);
     }
     if (!ok && lane == 0) flag_status(a.status, PKV_STATUS_TIMEOUT);
   }
