@@ -496,31 +496,32 @@ const Resident* resident(int device) {
   static std::atomic<bool> done[64] = {};
   static std::mutex asking;
   if (device < 0 || device >= 64) return nullptr;
-  if (!done[device].load(std::memory_order_acquire)) {
-    std::lock_guard<std::mutex> lock(asking);
-    auto set = [](auto kernel, size_t smem) {
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess &&
-             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-    };
-    constexpr size_t smem = sizeof(EvictShared<kBigThreads>);
-    if (!set(pkv_evict_kernel<F8>, sizeof(EvictShared<kSmallThreads>)) || !set(pkv_evict_select_kernel, smem) ||
-        !set(pkv_evict_move_kernel<F8>, 0)) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    int i = 0;
-    for (int size : kSizes) {
-      cudaLaunchAttribute attr[2];
-      const cudaLaunchConfig_t cfg = config(attr, nullptr, size, size, kBigThreads, smem);
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, pkv_evict_select_kernel, &cfg) != cudaSuccess) {
-        cudaGetLastError();  // a size that this device cannot run
-        n = 0;
-      }
-      facts[device].most[i++] = n;
-    }
-    done[device].store(true, std::memory_order_release);
+  if (done[device].load(std::memory_order_acquire)) return &facts[device];
+  std::lock_guard<std::mutex> lock(asking);
+  // (another thread may have been through meanwhile: what others read is written once)
+  if (done[device].load(std::memory_order_relaxed)) return &facts[device];
+  auto set = [](auto kernel, size_t smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  };
+  constexpr size_t smem = sizeof(EvictShared<kBigThreads>);
+  if (!set(pkv_evict_kernel<F8>, sizeof(EvictShared<kSmallThreads>)) || !set(pkv_evict_select_kernel, smem) ||
+      !set(pkv_evict_move_kernel<F8>, 0)) {
+    cudaGetLastError();
+    return nullptr;
   }
+  int i = 0;
+  for (int size : kSizes) {
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config(attr, nullptr, size, size, kBigThreads, smem);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, pkv_evict_select_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();  // a size that this device cannot run
+      n = 0;
+    }
+    facts[device].most[i++] = n;
+  }
+  done[device].store(true, std::memory_order_release);
   return &facts[device];
 }
 
