@@ -466,7 +466,9 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  *   score[k] = (k < scored[b] ? decay * score[k] : 0) + w[k]  for first[b] <= k < L
  *   q, k_cache, block_tables, seq_lens, query_start_loc and scale are as in
  *   pkv_attend (scale finite and not negative).  Sequences without query rows
- *   are left alone, scores of rows past a sequence's end too.
+ *   are left alone, scores of rows past a sequence's end too.  So are sequences
+ *   whose table names a page outside the pool (PKV_STATUS_BAD_BLOCK): their
+ *   softmax is not known.
  *   scored         NULL, or [num_seqs] int32: tokens from scored[b] on have no
  *                  score yet and what their pages hold is not read.  NULL:
  *                  L - n, i.e. this step's own tokens are new, the others have

@@ -490,7 +490,8 @@ def weigh(q, k_cache, scores, block_tables, seq_lens, query_start_loc, scale, de
     rounded up to 16) are host-side bounds, 0 = unknown.  They must hold (what
     does not fit is skipped and flagged); they keep the workspace small.
     Sequences that share pages and together hold more tokens than the pool has
-    need ``num_keys``."""
+    need ``num_keys``.  A sequence with a page id outside the pool is left
+    alone and flagged."""
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).weigh(index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
                                          scale, decay, first, scored, workspace, max_query_len, num_keys)

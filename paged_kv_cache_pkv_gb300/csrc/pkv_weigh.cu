@@ -315,15 +315,21 @@ __global__ void __launch_bounds__(kWsThreads, scores_ctas(NT, F8)) pkv_weigh_sco
 
     // ---- pages ----
     // Page ids 32 at a time, one a lane; an id outside the pool is flagged and
-    // page 0 read in its place.
+    // page 0 read in its place, and the piece's maxima say so: the sequence's scores
+    // are left alone.
     const int32_t* table = a.block_tables + int64_t(b) * a.desc.max_blocks_per_seq + first;
     int ids = 0;
     auto page_id = [&](int i) {
       if ((i & 31) == 0) {
         ids = i + lane < count ? __ldg(table + i + lane) : 0;
-        if (ids < 0 || ids >= a.desc.num_blocks) {
+        const bool bad = ids < 0 || ids >= a.desc.num_blocks;
+        if (bad) {
           flag_status(a.status, PKV_STATUS_BAD_BLOCK);
           ids = 0;
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = INFINITY;
         }
       }
       return __shfl_sync(0xffffffffu, ids, i & 31);
@@ -503,6 +509,7 @@ __global__ void __launch_bounds__(kWsThreads, add_ctas(QUADS)) pkv_weigh_add_ker
       l = l * ex2((m - mn) * a.qscale) + lo * ex2((mo - mn) * a.qscale);
       m = mn;
     }
+    const bool damaged = __any_sync(0xffffffffu, m == INFINITY);  // a page of the sequence is not the pool's
     const float mine_lse = m * a.qscale + __log2f(l);
     const int rows = s.n * G, quads = quads_of(rows);
     const int scored = a.decay == 0.f ? 0 : a.scored ? given : s.L - s.n;
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kWsThreads, add_ctas(QUADS)) pkv_weigh_add_ker
     // ---- a key a lane ----
     const float4* src = p.scores + quads_before[b] +
                         (int64_t(g) * pages + first + (lane >> 4)) * quads * kPage + (lane & 15);
-    for (int i = 0; i < count; i += 2 * kDeep) {
+    for (int i = damaged ? count : 0; i < count; i += 2 * kDeep) {
       int64_t at[kDeep];
       float old[kDeep];
       float4 x[kDeep][QUADS];

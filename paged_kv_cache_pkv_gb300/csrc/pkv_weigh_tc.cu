@@ -95,6 +95,7 @@ struct TcParams {
   float2* records1;            // [items1 + CTAs][4][256]: (maximum, sum) of a row, log2 domain, by column quarter
   float* lse;                  // [items1][256]: -log2 of the rows' sums
   float* records2;             // [items2 + CTAs][4][256]: weight of a key
+  int32_t* damaged;            // [num_seqs]: 1 where a page of the sequence is not the pool's
 };
 
 // ---- counting units ----------------------------------------------------------
@@ -458,10 +459,12 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
     const bool live = lane < kTilePages && page < (x.s.L + kPage - 1) / kPage;
     return Entry{live ? __ldg(a.block_tables + int64_t(x.b) * a.desc.max_blocks_per_seq + page) : -1, live};
   };
-  // Its page id; one outside the pool is flagged and page 0 read in its place.
-  auto page_id = [&](const Entry& e) {
+  // Its page id; one outside the pool is flagged and page 0 read in its place, and
+  // pass 2, which meets every page, marks the sequence: its scores are left alone.
+  auto page_id = [&](const Walk<PASS>& x, const Entry& e) {
     if (!e.live || (e.id >= 0 && e.id < a.desc.num_blocks)) return e.id;
     flag_status(a.status, PKV_STATUS_BAD_BLOCK);
+    if (PASS == 2) p.damaged[x.b] = 1;
     return 0;
   };
   // A lane's page of a key tile into the tile's buffer, bytes announced before.
@@ -495,8 +498,8 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
       int ids[2];
       if constexpr (PASS == 2) {
         const Entry e0 = entry_of(w, 2 * w.pair), e1 = entry_of(w, 2 * w.pair + 1);
-        ids[0] = page_id(e0);
-        ids[1] = page_id(e1);
+        ids[0] = page_id(w, e0);
+        ids[1] = page_id(w, e1);
       }
       if constexpr (PASS == 2 && F8) {
         for (int u = 0; u < tiles && ok; ++u, ++staged) {
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
       if constexpr (PASS == 1) next = entry_of(w, at);
       for (int u = 0; u < count; ++u, ++j) {
         if constexpr (PASS == 1) {
-          const int now = page_id(next);
+          const int now = page_id(w, next);
           if (u + 1 < count) next = entry_of(w, at + u + 1);  // read a tile ahead
           const int valid = __popc(__ballot_sync(0xffffffffu, now >= 0));
           if constexpr (F8) {
@@ -879,6 +882,8 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
 __global__ void __launch_bounds__(kPair) pkv_weigh_join_kernel(const TcParams p) {
   griddep_launch_dependents();  // pass 2 of the same call, which waits before it reads or writes pools
   griddep_wait();
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < p.a.num_seqs; b += kPair) p.damaged[b] = 0;
   const int64_t items = p.totals[0];
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const int first = p.items1[i].first, last = p.items1[i].last;
@@ -900,11 +905,12 @@ __global__ void __launch_bounds__(kPair) pkv_weigh_write_kernel(const TcParams p
   const int64_t items = p.totals[1];
   for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
     const Item item = p.items2[i];
+    const int damaged = p.damaged[item.b];
     WeighSequence s;
     weigh_sequence(a, item.b, s);
     const int64_t key = int64_t(item.pair) * kPair + threadIdx.x;
     const int from = a.first ? __ldg(a.first + item.b) : 0;
-    if (key >= s.L || key < from) continue;
+    if (key >= s.L || key < from || damaged) continue;
     const int scored = a.decay == 0.f ? 0 : a.scored ? __ldg(a.scored + item.b) : s.L - s.n;
     const int id = __ldg(a.block_tables + int64_t(item.b) * a.desc.max_blocks_per_seq + key / kPage);
     if (id < 0 || id >= a.desc.num_blocks) continue;  // flagged where its keys were read
@@ -932,7 +938,7 @@ int64_t most_items2(const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int
 }
 
 struct TcLayout {
-  size_t totals, items1, items2, records1, lse, records2, total;
+  size_t totals, items1, items2, records1, lse, records2, damaged, total;
 };
 
 TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, int32_t num_tokens, int64_t num_keys) {
@@ -951,6 +957,7 @@ TcLayout tc_layout(const DeviceInfo& dev, const pkv_desc& d, int32_t num_seqs, i
   w.records1 = take((i1 + dev.sm_count) * 4 * kPair * sizeof(float2));
   w.lse = take(i1 * kPair * sizeof(float));
   w.records2 = take((i2 + dev.sm_count) * 4 * kPair * sizeof(float));
+  w.damaged = take(size_t(num_seqs) * sizeof(int32_t));
   w.total = off;
   return w;
 }
@@ -1033,7 +1040,8 @@ int launch_weigh_tc(const LaunchCtx& ctx, const WeighArgs& a, bool fp8, int32_t 
                    reinterpret_cast<Item*>(workspace + w.items2),
                    reinterpret_cast<float2*>(workspace + w.records1),
                    reinterpret_cast<float*>(workspace + w.lse),
-                   reinterpret_cast<float*>(workspace + w.records2)};
+                   reinterpret_cast<float*>(workspace + w.records2),
+                   reinterpret_cast<int32_t*>(workspace + w.damaged)};
   return fp8 ? run<true>(ctx, q, k, p) : run<false>(ctx, q, k, p);
 }
 
