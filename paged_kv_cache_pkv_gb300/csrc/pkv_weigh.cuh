@@ -7,9 +7,10 @@
 
 namespace pkv {
 
-// Running maxima start here instead of at -infinity, whose difference with
-// itself is not a number; a masked score, -infinity, adds exp2(-inf) = 0.
-constexpr float kWeighNoScore = -1e30f;
+// Running maxima start here, below any score, instead of at -infinity, whose
+// difference with itself is not a number; a masked score, -infinity, adds
+// exp2(-inf) = 0.
+constexpr float kWeighNoScore = -3.402823466e38f;
 
 struct WeighSequence {
   int q0, n, L;

@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (x >= tiles) break;
-        if constexpr (PASS == 1) p.records1[record + x * kTile] = make_float2(m[x] * a.qscale, sum[x]);
+        if constexpr (PASS == 1) p.records1[record + x * kTile] = make_float2(m[x], sum[x]);
         else p.records2[record + x * kTile] = sum[x];
       }
       if (tid == 0) {
@@ -806,16 +806,18 @@ __global__ void __launch_bounds__(kTcThreads<F8>, 1)
                 for (int c = 0; c < 32; ++c)
                   if (!counts(c)) v[c] = 0xFF800000u;  // -infinity
               }
-              float top[2] = {m[x], m[x]};
+              // (the maximum times the scale: kept before the product, one that no key
+              // has raised would leave fp32's range where scales are large)
+              float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 top[0] = max3(top[0], __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
                 top[1] = max3(top[1], __uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
               }
-              const float mn = fmaxf(top[0], top[1]);
-              sum[x] *= ex2((m[x] - mn) * a.qscale);
+              const float mn = fmaxf(m[x], fmaxf(top[0], top[1]) * a.qscale);
+              sum[x] *= ex2(m[x] - mn);
               m[x] = mn;
-              const uint64_t by = f2(-mn * a.qscale, -mn * a.qscale);
+              const uint64_t by = f2(-mn, -mn);
 #pragma unroll
               for (int c = 0; c < 32; c += 2) {
                 float e0, e1;
