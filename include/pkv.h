@@ -465,7 +465,7 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  *          key k (softmax of scale * q[j, h] . K over the keys that row j sees)
  *   score[k] = (k < scored[b] ? decay * score[k] : 0) + w[k]  for first[b] <= k < L
  *   q, k_cache, block_tables, seq_lens, query_start_loc and scale are as in
- *   pkv_attend (scale finite and not negative).  Sequences without query rows
+ *   pkv_attend (scale not negative, below 2^127).  Sequences without query rows
  *   are left alone, scores of rows past a sequence's end too.  So are sequences
  *   whose table names a page outside the pool (PKV_STATUS_BAD_BLOCK): their
  *   softmax is not known.

@@ -503,8 +503,9 @@ static int weigh(const pkv_bf16* q, const void* k_cache, const uint8_t* k_scale,
                  int32_t max_query_len, int64_t num_keys, float scale, float decay, void* workspace,
                  size_t workspace_bytes, const pkv_desc* desc, pkv_stream_t stream, bool fp8) {
   if (int e = check_weigh(desc, num_seqs, num_tokens)) return e;
-  // (not >=: a NaN is refused too)
-  if (!(scale >= 0.f) || !std::isfinite(scale) || !(decay >= 0.f) || !std::isfinite(decay)) return PKV_ERR_RANGE;
+  // (not >=: a NaN is refused too; the kernels have the scale times log2(e))
+  const float qscale = scale * 1.4426950408889634f;
+  if (!(scale >= 0.f) || !std::isfinite(qscale) || !(decay >= 0.f) || !std::isfinite(decay)) return PKV_ERR_RANGE;
   if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
   if (!q || !k_cache || (fp8 && !k_scale) || !scores || !block_tables || !seq_lens || !query_start_loc || !workspace)
     return PKV_ERR_NULL;
@@ -522,7 +523,7 @@ static int weigh(const pkv_bf16* q, const void* k_cache, const uint8_t* k_scale,
   a.max_rows = most_rows(max_query_len, num_tokens);
   a.num_keys = most_keys(desc, num_seqs, num_keys);
   // (a masked score is -infinity: scale 0, all keys alike, is a scale too small to part them)
-  a.qscale = std::max(scale * 1.4426950408889634f, std::numeric_limits<float>::min());
+  a.qscale = std::max(qscale, std::numeric_limits<float>::min());
   a.decay = decay;
   a.workspace = workspace, a.workspace_bytes = workspace_bytes;
   a.desc = *desc;

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import eviction as E
-from test_weigh import SCALE, batch, check
+from test_weigh import RANGE, SCALE, _weigh, batch, check
 
 gpu = pytest.mark.gpu
 
@@ -20,6 +20,12 @@ def scaled(x, by_q, by_k=1.0):
     else:
         x["k"] = bf(x["k"], by_k).astype(np.uint16)
     return x
+
+
+@pytest.mark.parametrize("scale,code", [(2.0 ** 126, 0), (2.0 ** 127, 0), (2.36e38, RANGE), (3.4e38, RANGE)])
+def test_scales_beyond_range_are_refused(pkvlib, scale, code):
+    """Where scale times log2(e) is no fp32 number.  (B = 0: nothing is launched.)"""
+    assert _weigh(pkvlib, B=0, scale=scale) == code
 
 
 @gpu
