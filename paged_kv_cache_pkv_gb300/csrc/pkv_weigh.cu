@@ -509,9 +509,11 @@ __global__ void __launch_bounds__(kWsThreads, add_ctas(QUADS)) pkv_weigh_add_ker
       l = l * ex2((m - mn) * a.qscale) + lo * ex2((mo - mn) * a.qscale);
       m = mn;
     }
-    const bool damaged = __any_sync(0xffffffffu, m == INFINITY);  // a page of the sequence is not the pool's
     const float mine_lse = m * a.qscale + __log2f(l);
     const int rows = s.n * G, quads = quads_of(rows);
+    // A page of the sequence is not the pool's.  (Columns behind the rows' may never
+    // have been written.)
+    const bool damaged = __any_sync(0xffffffffu, lane % kCols < rows && m == INFINITY);
     const int scored = a.decay == 0.f ? 0 : a.scored ? given : s.L - s.n;
     float lse[4 * QUADS];  // a column without a row: weight 0
 #pragma unroll
