@@ -494,8 +494,14 @@ PKV_API int pkv_attend_latent(const pkv_bf16* q, const pkv_bf16* latent_cache,
  * Sums and scores are fp32, in an order that goes by the call's shapes and
  * lengths alone: the same inputs give the same bits.  K rows and scores of
  * rows past a sequence's end are never used, whatever they hold; the rows of
- * its cached tokens and its queries must be finite.  Where a bounded wait runs
- * out (PKV_STATUS_TIMEOUT), scores of the sequences it was for become NaN. */
+ * its cached tokens and its queries must be finite, and so must the products of
+ * both.  A weight is off by its exponent's rounding, about 2^-23 of the row's
+ * largest |scale * q . K|: rows of scores beyond 2^16 lose their weights' third
+ * digit.  Where a bounded wait runs out (PKV_STATUS_TIMEOUT), scores of the
+ * sequences it was for become NaN.
+ * The kernels for few rows are sized by the batch's most rows: decode rows and
+ * query chunks are better off with a call each (scores of different sequences
+ * have nothing to do with each other). */
 PKV_API int pkv_weigh_workspace_size(const pkv_desc* desc, int32_t num_seqs, int32_t num_tokens,
                                      int32_t max_query_len, int64_t num_keys, size_t* bytes);
 PKV_API int pkv_weigh(const pkv_bf16* q, const pkv_bf16* k_cache, float* scores,
@@ -504,7 +510,8 @@ PKV_API int pkv_weigh(const pkv_bf16* q, const pkv_bf16* k_cache, float* scores,
                       int32_t num_seqs, int32_t num_tokens, int32_t max_query_len, int64_t num_keys,
                       float scale, float decay, void* workspace, size_t workspace_bytes,
                       const pkv_desc* desc, pkv_stream_t stream);
-/* pkv_weigh_fp8 -- the same over FP8 pages (k_scale as in pkv_attend_fp8). */
+/* pkv_weigh_fp8 -- the same over FP8 pages (k_scale as in pkv_attend_fp8, scale
+ * bytes of cached tokens in [1, 254]). */
 PKV_API int pkv_weigh_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const uint8_t* k_scale,
                           float* scores, const int32_t* block_tables, const int32_t* seq_lens,
                           const int32_t* query_start_loc, const int32_t* first,
@@ -528,7 +535,11 @@ PKV_API int pkv_weigh_fp8(const pkv_bf16* q, const pkv_fp8* k_cache, const uint8
  *   recent         >= 0.
  *   workspace      at least pkv_evict_workspace_size bytes, 256-byte aligned,
  *                  no initialisation needed; calls that may overlap on the
- *                  GPU need workspaces of their own.
+ *                  GPU need workspaces of their own.  4 bytes a kv head and
+ *                  token of the tables' width, for each sequence.
+ * Kernels and workspace go by the tables' width (max_blocks_per_seq), not by
+ * the lengths: a batch of short sequences is better off with tables no wider
+ * than its longest.
  * desc: num_q_heads is not used (any valid value).  Pages of a sequence from
  * its first[b]-th token on must belong to it alone.  A sequence whose numbers
  * do not fit (length negative or beyond its table, negative keep or first) is

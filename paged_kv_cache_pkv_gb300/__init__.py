@@ -491,7 +491,8 @@ def weigh(q, k_cache, scores, block_tables, seq_lens, query_start_loc, scale, de
     does not fit is skipped and flagged); they keep the workspace small.
     Sequences that share pages and together hold more tokens than the pool has
     need ``num_keys``.  A sequence with a page id outside the pool is left
-    alone and flagged."""
+    alone and flagged.  Decode rows and query chunks are better off with a call
+    each."""
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).weigh(index, stream, q, k_cache, scores, block_tables, seq_lens, query_start_loc,
                                          scale, decay, first, scored, workspace, max_query_len, num_keys)
@@ -507,7 +508,8 @@ def weigh_fp8(q, k_cache, k_scale, scores, block_tables, seq_lens, query_start_l
 
 
 def workspace_size_evict(desc, num_seqs, device=None):
-    """Workspace bytes evict and evict_fp8 need."""
+    """Workspace bytes evict and evict_fp8 need: 4 a kv head and token of the
+    block tables' width, for each sequence."""
     n = _sz(0)
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         _check(lib().pkv_evict_workspace_size(ctypes.byref(desc), int(num_seqs), ctypes.byref(n)),
@@ -523,7 +525,8 @@ def evict(k_cache, v_cache, scores, block_tables, seq_lens, keep, first=None, re
     the largest ``scores`` (fp32 [NB, Hkv, 16]) between; they move, in their
     order, to the front of the sequence's pages, their scores too.  Returns
     the new lengths (``new_lens``, int32 [B], not seq_lens itself): pages
-    behind them may be let go of."""
+    behind them may be let go of.  Kernels and workspace go by the width of
+    ``block_tables``: short sequences are better off with narrow ones."""
     index = _index(k_cache, "k_cache")
     return (_binding or _native()).evict(index, stream, k_cache, v_cache, scores, block_tables, seq_lens, keep, first,
                                          recent, new_lens, workspace)

@@ -119,8 +119,11 @@ __device__ __forceinline__ int64_t pool_row(const EvictArgs& p, int g, int page,
   return (int64_t(page) * p.desc.num_kv_heads + g) * kPage + token % kPage;
 }
 
-// Steps 1 to 3 (see above): the list of c > 0 tokens, complete for the cluster
-// when it returns.
+// Steps 1 to 3 (see above): the list of c > 0 tokens.  When it returns, a single
+// CTA has its list whole; of a cluster each CTA has written its own part, and
+// the others' parts are there only for the kernel behind (the last cluster
+// barrier is arrived at before the list is written: it lets the CTAs' shared
+// memory go).
 template <int kThreads>
 __device__ __forceinline__ void select_tokens(const EvictArgs& p, const Cut& x, int cluster, int rank,
                                               EvictShared<kThreads>& sh) {

@@ -24,15 +24,17 @@
 // scores.  A row tile is left out where causality hides the whole key pair.
 //
 // What bounds it: of a unit of two 128 x 128 x 128 products, 1024 cycles of the
-// tensor pipe, operand reads and copies take shared memory about 1300 and the
-// epilogue's chain (score tile to registers, maxima, 32 exponentials a thread) as
-// long as the measured 1700 (pass 1) to 2000.  All rows of a 4095-token prompt, 32
+// tensor pipe, operand reads and copies take shared memory about 1300; measured are
+// 1700 (pass 1) to 2000, no unit is full, and what the epilogue's chain (score tile
+// to registers, maxima, 32 exponentials a thread) takes of the rest has not been
+// measured alone.  All rows of a 4095-token prompt, 32
 // + 8 heads: 138 us between others in a graph, passes of 65 and 76 under ncu; the
 // last 32 rows of eight prompts of 4096 to 8192 tokens 59, K twice from HBM.
 //
 // E4M3 pages: TMA lands a tile's codes and scale bytes in a staging area, four
-// warps widen them to bf16 (exact, scale included).  What they and the epilogue
-// issue together is what bounds it.
+// warps widen them to bf16, scale included: exact but for codes without an exponent
+// under scale bytes 1 and 2, whose last bits fall below bf16's smallest number
+// (2^-133).  What they and the epilogue issue together is what bounds it.
 #include <cuda.h>
 
 #include <algorithm>
@@ -339,9 +341,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 // Half a row of a staged page, dims 64h .. 64h + 63 of row r times 2^(scale - 127),
 // as bf16 into row `out` of the half-h block of a tile (both 128-byte swizzled):
-// codes to exponent fields by shifts, one product by a power of two (exact, also
-// for codes without an exponent).  The upper half's lanes start two pieces on, so
-// that a quarter-warp's stores are on banks of their own.
+// codes to exponent fields by shifts, one product by a power of two (exact above
+// bf16's smallest number, also for codes without an exponent).  The upper half's
+// lanes start two pieces on, so that a quarter-warp's stores are on banks of their
+// own.
 __device__ __forceinline__ void widen_half(const uint8_t* page, uint32_t scale, uint8_t* out, int r, int h) {
   // 2^(scale - 127 + 120), in two steps where that is beyond bf16 (scales above 134)
   const uint32_t s1 = min(scale, 134u), more = scale - s1;
