@@ -28,7 +28,7 @@
 // 1700 (pass 1) to 2000, no unit is full, and what the epilogue's chain (score tile
 // to registers, maxima, 32 exponentials a thread) takes of the rest has not been
 // measured alone.  All rows of a 4095-token prompt, 32
-// + 8 heads: 139 us between others in a graph, passes of 65 and 76 under ncu; the
+// + 8 heads: 139 us between others in a graph, passes of 67 and 80 under ncu; the
 // last 32 rows of eight prompts of 4096 to 8192 tokens 59, K twice from HBM.
 //
 // E4M3 pages: TMA lands a tile's codes and scale bytes in a staging area, four
